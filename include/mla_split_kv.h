@@ -552,6 +552,101 @@ mla_status_t mla_decode_unembed(const void* q_absorbed, const void* q_pe, const 
                                 float* out_lse, const mla_decode_desc_t* desc);
 
 /*
+ * Block-scaled 8-bit caches ("q8"). The caches hold E4M3 bytes (MLA_E4M3's
+ * format), and every `scale_block` = g consecutive tokens of a page share one
+ * fp32 scale: the value of byte x of page row r is
+ *     e4m3(x) * scales[page, r / g],
+ * latent and rope columns alike. g is a power of two that divides the page
+ * (1: a scale for every token). A scale is NaN, which every value of its block
+ * then is, or lies in [2^-60, 2^60].
+ *
+ * mla_cache_append_q8 -- mla_cache_append into such a cache: each request's
+ * newest tokens (positions, pages and out-of-range pages as there) quantized
+ * as they are written. A block's scale is the least power of two s in [2^-60,
+ * 2^60] with max|x| / s <= 448 over the new tokens that fall into it; if
+ * tokens before the request's first new one lie in the block too, the larger
+ * of that and the scale they have, and where the scale grows their bytes are
+ * moved to it (e4m3(byte) * old / new, rounded once; exact but for values that
+ * become subnormal). A value is stored as the E4M3 byte nearest to x / s, ties
+ * to even, saturating at +-448. Whatever the block held behind its first new
+ * token counts for nothing, so positions may be written again after a
+ * rejected draft. A block that gets a NaN, an infinity or a value above
+ * 448 * 2^60 has its scale set to NaN and those new bytes to 0.
+ *
+ * ckv_new  : device [B, q_len, 512] of new_dtype (MLA_F16 / MLA_BF16), 16-byte
+ *            aligned
+ * kpe_new  : device [B, q_len, 64] of new_dtype, 16-byte aligned
+ * q_len    : new tokens per request, at least 1 (B * q_len < 2^31; a whole
+ *            prefill chunk may be one call)
+ * ckv_cache: device [num_blocks, bs, 512] bytes, 16-byte aligned (written)
+ * kpe_cache: device [num_blocks, bs, 64] bytes, 16-byte aligned (written)
+ * scales   : device [num_blocks, bs / g] fp32 (written)
+ * No two requests of a call may write to one block. A programmatic dependent
+ * launch, as mla_cache_append. The scalar MLA_E4M3 caches have no counterpart.
+ */
+mla_status_t mla_cache_append_q8(const void* ckv_new, const void* kpe_new, int32_t new_dtype,
+                                 const int32_t* block_table, const int32_t* context_lens, int32_t B, int32_t q_len,
+                                 int32_t block_size, int32_t scale_block, int32_t num_blocks,
+                                 int32_t max_blocks_per_req, void* ckv_cache, void* kpe_cache, float* scales,
+                                 void* stream);
+
+/* Shapes and options of mla_decode_q8. */
+typedef struct {
+  int32_t num_requests;       /* B, at most 65535                             */
+  int32_t num_heads;          /* H in {16, 64, 128}                           */
+  int32_t q_len;              /* query rows per request, 1..32                */
+  int32_t block_size;         /* tokens per page: 16, 32 or 64                */
+  int32_t num_blocks;         /* pages in the cache pool                      */
+  int32_t max_blocks_per_req; /* row stride of block_table, in entries        */
+  int32_t dtype;              /* of the queries: MLA_F16 or MLA_BF16          */
+  int32_t causal;             /* as mla_decode_desc_t.causal                  */
+  int32_t scale_block;        /* g: tokens that share a scale                 */
+  int32_t window;             /* W >= 1: the row at position pos sees tokens
+                                 t > pos - W, and the first `sinks` ones; pos is
+                                 L - q_len + i for row i when causal, else
+                                 L - 1. 0: no window                           */
+  int32_t sinks;              /* >= 0 (0 without a window)                    */
+  int32_t out_dtype;          /* MLA_F16, MLA_BF16 or MLA_F32                 */
+  void* workspace;            /* DEVICE, >= mla_decode_q8_workspace_bytes(...)
+                                 bytes, 16-byte aligned; need not be cleared.
+                                 Calls sharing it must not overlap in time.    */
+  uint64_t workspace_bytes;
+  void* stream;               /* cudaStream_t                                 */
+} mla_q8_desc_t;
+
+/*
+ * mla_decode_q8 -- one whole decode layer call over a block-scaled 8-bit
+ * cache. With z_t the scale of token t and c_t, k_t its bytes' E4M3 values:
+ *   s_t     = scale * z_t * (q_absorbed[b,i,h,:] . c_t + q_pe[b,i,h,:] . k_t)
+ *   out[b,i,h,:]   = sum_t softmax(s)_t * z_t * c_t   (rounded once)
+ *   out_lse[b,i,h] = log2 sum_t exp(s_t)
+ * over the tokens that the row sees (all of its request's, those up to its own
+ * position when causal, of these the window's and the sinks); a row that sees
+ * none gives 0 and -inf. What lies in the cache behind a request's last token,
+ * and tokens that no row sees, do not matter, NaN among it or not.
+ *
+ * The batch's tokens are shared out over the GPU on the device itself, from
+ * context_lens as they are when the call runs: no plan, and a captured call
+ * may be replayed as the contexts grow. The same bits on every call with the
+ * same lengths. Pages: as for mla_decode_partial (one outside the pool or the
+ * table row reads zeros and raises MLA_ERR_DEVICE_CHECK).
+ *
+ * out     : device [B, q_len, H, 512] of desc->out_dtype, 16-byte aligned
+ * out_lse : device [B, q_len, H] fp32, or NULL
+ * Other arguments: as for mla_decode_partial and mla_cache_append_q8. With
+ * out in MLA_F32, out and out_lse are a partial per request for
+ * mla_merge_states or mla_merge_unembed (o_indptr[b] = b).
+ */
+mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                           const float* scales, const int32_t* block_table, const int32_t* context_lens, float scale,
+                           void* out, float* out_lse, const mla_q8_desc_t* desc);
+
+/* Workspace bytes of mla_decode_q8 on `dev` (its num_sms): two open ends per
+ * group of CTAs, each [rows, 512] fp32 with rows' maxima and sums. 0 for bad
+ * arguments. */
+uint64_t mla_decode_q8_workspace_bytes(const mla_device_info_t* dev, int32_t q_len, int32_t num_heads);
+
+/*
  * mla_check_device_errors -- synchronize `stream`, read and clear the device
  * error word the kernels set (bit 0: a bounded wait timed out; bit 1: a page
  * id outside the pool; bit 2: a kernel found its launch unusable -- the
@@ -598,8 +693,9 @@ mla_status_t mla_selfcheck(float* max_abs_err);
 #define MLA_CTR_REJECTED 3
 #define MLA_CTR_CTAS 4 /* CTAs launched by partial kernels */
 #define MLA_CTR_DECODE_FUSED 5 /* mla_decode calls that ran as one launch */
-#define MLA_CTR_WRAP 6 /* mla_cache_append, mla_merge_unembed and mla_decode_unembed unembed launches */
-#define MLA_NUM_COUNTERS 7
+#define MLA_CTR_WRAP 6 /* mla_cache_append(_q8), mla_merge_unembed and mla_decode_unembed unembed launches */
+#define MLA_CTR_DECODE_Q8 7 /* mla_decode_q8 calls */
+#define MLA_NUM_COUNTERS 8
 /* mla_get_counters -- copy min(n, MLA_NUM_COUNTERS) counters to out (host). */
 void mla_get_counters(uint64_t* out, int32_t n);
 void mla_reset_counters(void);

@@ -31,8 +31,8 @@ MLA_MERGE_ENTRIES, MLA_MERGE_PARTIALS = 0, 1
 MLA_DECODE_MERGE_ENTRIES, MLA_DECODE_MERGE_TICKETS = 0, 1
 MLA_SCORE_EXCHANGE_EXACT, MLA_SCORE_EXCHANGE_F16, MLA_SCORE_EXCHANGE_NONE, MLA_SCORE_EXCHANGE_F32 = 0, 1, 2, 3
 
-CTR_PARTIAL_SIMT, CTR_PARTIAL_TC, CTR_MERGE, CTR_REJECTED, CTR_CTAS, CTR_DECODE_FUSED, CTR_WRAP = range(7)
-NUM_COUNTERS = 7
+CTR_PARTIAL_SIMT, CTR_PARTIAL_TC, CTR_MERGE, CTR_REJECTED, CTR_CTAS, CTR_DECODE_FUSED, CTR_WRAP, CTR_DECODE_Q8 = range(8)
+NUM_COUNTERS = 8
 
 DTYPE_CODES = {"f16": MLA_F16, "bf16": MLA_BF16, "f32": MLA_F32, "e4m3": MLA_E4M3}
 
@@ -94,6 +94,26 @@ class mla_decode_desc_t(ctypes.Structure):
     ]
 
 
+class mla_q8_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("num_requests", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("q_len", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("max_blocks_per_req", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("scale_block", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("sinks", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_uint64),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -124,6 +144,12 @@ def load() -> ctypes.CDLL:
     lib.mla_decode_workspace_bytes.restype = u64
     lib.mla_cache_append.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
     lib.mla_cache_append.restype = i32
+    lib.mla_cache_append_q8.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+    lib.mla_cache_append_q8.restype = i32
+    lib.mla_decode_q8.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, vp, vp, ctypes.POINTER(mla_q8_desc_t)]
+    lib.mla_decode_q8.restype = i32
+    lib.mla_decode_q8_workspace_bytes.argtypes = [ctypes.POINTER(mla_device_info_t), i32, i32]
+    lib.mla_decode_q8_workspace_bytes.restype = u64
     lib.mla_merge_unembed.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp]
     lib.mla_merge_unembed.restype = i32
     lib.mla_decode_unembed.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, vp, vp, vp, vp, i32, i32, vp, i32,
@@ -275,6 +301,24 @@ def mla_cache_append(ckv_new: int, kpe_new: int, block_table: int, context_lens:
                      stream: Optional[int]) -> None:
     _check(load().mla_cache_append(ckv_new, kpe_new, block_table, context_lens, B, q_len, block_size, num_blocks,
                                    max_blocks_per_req, ckv_cache, kpe_cache, stream or None), "mla_cache_append")
+
+
+def mla_cache_append_q8(ckv_new: int, kpe_new: int, new_dtype: int, block_table: int, context_lens: int, B: int,
+                        q_len: int, block_size: int, scale_block: int, num_blocks: int, max_blocks_per_req: int,
+                        ckv_cache: int, kpe_cache: int, scales: int, stream: Optional[int]) -> None:
+    _check(load().mla_cache_append_q8(ckv_new, kpe_new, new_dtype, block_table, context_lens, B, q_len, block_size,
+                                      scale_block, num_blocks, max_blocks_per_req, ckv_cache, kpe_cache, scales,
+                                      stream or None), "mla_cache_append_q8")
+
+
+def mla_decode_q8(q_absorbed: int, q_pe: int, ckv_cache: int, kpe_cache: int, scales: int, block_table: int,
+                  context_lens: int, scale: float, out: int, out_lse: Optional[int], desc: mla_q8_desc_t) -> None:
+    _check(load().mla_decode_q8(q_absorbed, q_pe, ckv_cache, kpe_cache, scales, block_table, context_lens,
+                                scale, out, out_lse or None, desc), "mla_decode_q8")
+
+
+def mla_decode_q8_workspace_bytes(dev: mla_device_info_t, q_len: int, num_heads: int) -> int:
+    return int(load().mla_decode_q8_workspace_bytes(ctypes.byref(dev), q_len, num_heads))
 
 
 def mla_merge_unembed(partials: int, lse: int, o_indptr: int, B: int, q_len: int, num_heads: int, w_uv_t: int,

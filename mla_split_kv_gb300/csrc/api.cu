@@ -784,14 +784,145 @@ mla_status_t mla_merge_unembed(const float* partials, const float* lse, const in
   return MLA_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+bool valid_page(int32_t bs) { return bs == 16 || bs == 32 || bs == 64; }
+// tokens that share a scale: a power of two that divides the page
+bool valid_scale_block(int32_t g, int32_t bs) { return g >= 1 && g <= bs && (g & (g - 1)) == 0; }
+
+uint64_t q8_workspace_bytes(int32_t sms, int32_t q_len, int32_t num_heads) {
+  const int rows = q_len * num_heads, nr = mla::q8_rows_per_cta(rows);
+  const uint64_t row_pad = static_cast<uint64_t>((rows + nr - 1) / nr) * nr;
+  return static_cast<uint64_t>(mla::q8_gangs(rows, sms)) * 2 * row_pad * (mla::kRank + 2) * 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status_t mla_cache_append_q8(const void* ckv_new, const void* kpe_new, int32_t new_dtype,
+                                 const int32_t* block_table, const int32_t* context_lens, int32_t B, int32_t q_len,
+                                 int32_t block_size, int32_t scale_block, int32_t num_blocks,
+                                 int32_t max_blocks_per_req, void* ckv_cache, void* kpe_cache, float* scales,
+                                 void* stream) {
+  if (ckv_new == nullptr || kpe_new == nullptr || block_table == nullptr || context_lens == nullptr ||
+      ckv_cache == nullptr || kpe_cache == nullptr || scales == nullptr)
+    return reject(MLA_ERR_INVALID_ARG);
+  if (B < 1 || B > (1 << 24) || num_blocks < 1 || max_blocks_per_req < 1 || q_len < 1) return reject(MLA_ERR_INVALID_ARG);
+  if (new_dtype != MLA_F16 && new_dtype != MLA_BF16) return reject(MLA_ERR_UNSUPPORTED);
+  if (!valid_page(block_size)) return reject(MLA_ERR_UNSUPPORTED);
+  if (!valid_scale_block(scale_block, block_size)) return reject(MLA_ERR_INVALID_ARG);
+  if (static_cast<int64_t>(B) * q_len > 0x7fffffffll) return reject(MLA_ERR_UNSUPPORTED);
+  if (!aligned(ckv_new, 16) || !aligned(kpe_new, 16) || !aligned(ckv_cache, 16) || !aligned(kpe_cache, 16) ||
+      !aligned(scales, 4) || !aligned(block_table, 4) || !aligned(context_lens, 4))
+    return reject(MLA_ERR_INVALID_ARG);
+  mla::AppendQ8Params p;
+  p.ckv_new = static_cast<const uint16_t*>(ckv_new);
+  p.kpe_new = static_cast<const uint16_t*>(kpe_new);
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.ckv = static_cast<uint8_t*>(ckv_cache);
+  p.kpe = static_cast<uint8_t*>(kpe_cache);
+  p.scales = scales;
+  p.B = B;
+  p.q_len = q_len;
+  p.bs = block_size;
+  p.max_blocks = max_blocks_per_req;
+  p.num_blocks = num_blocks;
+  p.g = scale_block;
+  if (mla::launch_append_q8(p, new_dtype == MLA_BF16, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  g_counters[MLA_CTR_WRAP].fetch_add(1, std::memory_order_relaxed);
+  return MLA_OK;
+}
+
+uint64_t mla_decode_q8_workspace_bytes(const mla_device_info_t* dev, int32_t q_len, int32_t num_heads) {
+  if (dev == nullptr || dev->num_sms < 1 || !valid_heads(num_heads) || q_len < 1 || q_len > MLA_MAX_Q_LEN) return 0;
+  return q8_workspace_bytes(dev->num_sms, q_len, num_heads);
+}
+
+mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                           const float* scales, const int32_t* block_table, const int32_t* context_lens, float scale,
+                           void* out, float* out_lse, const mla_q8_desc_t* d) {
+  if (d == nullptr || q_absorbed == nullptr || q_pe == nullptr || ckv_cache == nullptr || kpe_cache == nullptr ||
+      scales == nullptr || block_table == nullptr || context_lens == nullptr || out == nullptr)
+    return reject(MLA_ERR_INVALID_ARG);
+  if (d->num_requests < 1 || d->num_blocks < 1 || d->max_blocks_per_req < 1) return reject(MLA_ERR_INVALID_ARG);
+  if (d->num_requests > 65535) return reject(MLA_ERR_UNSUPPORTED);
+  if (!valid_heads(d->num_heads) || d->q_len < 1 || d->q_len > MLA_MAX_Q_LEN) return reject(MLA_ERR_UNSUPPORTED);
+  if (!valid_page(d->block_size)) return reject(MLA_ERR_UNSUPPORTED);
+  if (d->dtype != MLA_F16 && d->dtype != MLA_BF16) return reject(MLA_ERR_UNSUPPORTED);
+  if (d->out_dtype != MLA_F16 && d->out_dtype != MLA_BF16 && d->out_dtype != MLA_F32) return reject(MLA_ERR_UNSUPPORTED);
+  if (d->causal != 0 && d->causal != 1) return reject(MLA_ERR_INVALID_ARG);
+  if (!valid_scale_block(d->scale_block, d->block_size)) return reject(MLA_ERR_INVALID_ARG);
+  if (d->window < 0 || d->sinks < 0 || (d->window == 0 && d->sinks != 0)) return reject(MLA_ERR_INVALID_ARG);
+  if (!std::isfinite(scale)) return reject(MLA_ERR_INVALID_ARG);
+  if (!aligned(q_absorbed, 16) || !aligned(q_pe, 16) || !aligned(ckv_cache, 16) || !aligned(kpe_cache, 16) ||
+      !aligned(scales, 4) || !aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(out, 16) ||
+      (out_lse != nullptr && !aligned(out_lse, 4)))
+    return reject(MLA_ERR_INVALID_ARG);
+  if (static_cast<uint64_t>(d->num_blocks) * static_cast<uint64_t>(d->block_size) > 0x7fffffffull)
+    return reject(MLA_ERR_UNSUPPORTED);
+  if (d->workspace == nullptr || !aligned(d->workspace, 16)) return reject(MLA_ERR_INVALID_ARG);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  if (d->workspace_bytes < q8_workspace_bytes(sms, d->q_len, d->num_heads)) return reject(MLA_ERR_INVALID_ARG);
+
+  const int rows = d->q_len * d->num_heads, nr = mla::q8_rows_per_cta(rows);
+  mla::DecodeQ8Params p;
+  p.q_abs = static_cast<const uint16_t*>(q_absorbed);
+  p.q_pe = static_cast<const uint16_t*>(q_pe);
+  p.ckv = static_cast<const uint8_t*>(ckv_cache);
+  p.kpe = static_cast<const uint8_t*>(kpe_cache);
+  p.scales = scales;
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.out = out;
+  p.out_lse = out_lse;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.B = d->num_requests;
+  p.H = d->num_heads;
+  p.q_len = d->q_len;
+  p.bs = d->block_size;
+  p.max_blocks = d->max_blocks_per_req;
+  p.num_blocks = d->num_blocks;
+  p.g_shift = 0;
+  while ((1 << p.g_shift) < d->scale_block) ++p.g_shift;
+  p.causal = d->causal;
+  p.window = d->window;
+  p.sinks = d->sinks;
+  p.out_dtype = d->out_dtype;
+  p.gangs = mla::q8_gangs(rows, sms);
+  p.groups = (rows + nr - 1) / nr;
+  p.row_pad = p.groups * nr;
+  p.ws_o = static_cast<float*>(d->workspace);
+  p.ws_ml = p.ws_o + static_cast<uint64_t>(p.gangs) * 2 * p.row_pad * mla::kRank;
+  p.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  if (mla::launch_decode_q8(p, d->dtype == MLA_BF16, static_cast<cudaStream_t>(d->stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  g_counters[MLA_CTR_DECODE_Q8].fetch_add(1, std::memory_order_relaxed);
+  return MLA_OK;
+}
+
 mla_status_t mla_check_device_errors(void* stream, uint32_t* code_out) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
-  uint32_t a = 0, b = 0, c = 0, e = 0, f = 0, g = 0;
+  uint32_t a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, h = 0, k = 0;
   if (mla::simt_read_clear_error(&a) != cudaSuccess || mla::tc_read_clear_error(&b) != cudaSuccess ||
       mla::tc128_read_clear_error(&c) != cudaSuccess || mla::mh_read_clear_error(&e) != cudaSuccess ||
-      mla::wrap_read_clear_error(&f) != cudaSuccess || mla::mh_nx_read_clear_error(&g) != cudaSuccess)
+      mla::wrap_read_clear_error(&f) != cudaSuccess || mla::mh_nx_read_clear_error(&g) != cudaSuccess ||
+      mla::append_q8_read_clear_error(&h) != cudaSuccess || mla::decode_q8_read_clear_error(&k) != cudaSuccess)
     return MLA_ERR_CUDA;
-  const uint32_t code = a | b | c | e | f | g;
+  const uint32_t code = a | b | c | e | f | g | h | k;
   if (code_out != nullptr) *code_out = code;
   if (code != 0 && !clear_static_workspace()) return MLA_ERR_CUDA;
   if (code & mla::MLA_DEVERR_TIMEOUT) return MLA_ERR_TIMEOUT;

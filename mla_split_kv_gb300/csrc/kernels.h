@@ -114,6 +114,74 @@ struct UnembedParams {
   int32_t tables_ready;        // o_indptr complete before the preceding kernel started: read before the wait
 };
 
+// What the rows of a request see of its L tokens through a sliding window beside its first `sinks`
+// tokens: the pages of the sinks, then, `skip` tokens further on, the pages from the first token that
+// the earliest row's window reaches. The n tokens of both, one after the other, are the request's
+// visible run; position u of the run is token u below `sa` and token u + skip from there on, both
+// page-aligned. window = 0: the whole request. Whether row i sees position u is, in the run's own
+// positions, the rule on tokens: with n for L, u <= n - q_len + i (causal) and (u > pos - window or
+// u < sinks), pos the row's own position: `skip` shifts a token and its row alike, and where skip > 0
+// every position below sa is below every row's window.
+struct WindowView {
+  int32_t n, sa, skip;
+};
+#ifdef __CUDACC__
+#define MLA_HOST_DEVICE __host__ __device__
+#else
+#define MLA_HOST_DEVICE
+#endif
+MLA_HOST_DEVICE inline WindowView window_view(int32_t L, int32_t q_len, int32_t bs, int32_t causal, int32_t window,
+                                              int32_t sinks) {
+  WindowView v{L > 0 ? L : 0, 0, 0};
+  if (window <= 0 || L <= 0) return v;
+  const int64_t first = static_cast<int64_t>(L) - (causal ? q_len : 1);  // the earliest row's position
+  const int64_t low = first - window + 1;                                // the first token its window reaches
+  if (low <= 0) return v;
+  const int64_t low_page = low / bs * bs, sink_end = (static_cast<int64_t>(sinks) + bs - 1) / bs * bs;
+  v.sa = static_cast<int32_t>(sink_end < low_page ? sink_end : low_page);
+  v.skip = static_cast<int32_t>(low_page - v.sa);
+  v.n = L - v.skip;
+  return v;
+}
+
+// Block-scaled 8-bit caches: the value of a cached byte x of token row r is e4m3(x) * scales[r >> g_shift].
+struct AppendQ8Params {
+  const uint16_t* ckv_new;     // [B, q_len, 512]
+  const uint16_t* kpe_new;     // [B, q_len, 64]
+  const int32_t* block_table;  // [B, max_blocks]
+  const int32_t* context_lens; // [B]
+  uint8_t* ckv;                // [num_blocks, bs, 512]
+  uint8_t* kpe;                // [num_blocks, bs, 64]
+  float* scales;               // [num_blocks, bs / g]
+  int32_t B, q_len, bs, max_blocks, num_blocks, g;
+};
+cudaError_t launch_append_q8(const AppendQ8Params& p, bool bf16, cudaStream_t stream);
+cudaError_t append_q8_read_clear_error(uint32_t* out);
+
+struct DecodeQ8Params {
+  const uint16_t* q_abs;       // [B, q_len, H, 512]
+  const uint16_t* q_pe;        // [B, q_len, H, 64]
+  const uint8_t* ckv;          // [num_blocks, bs, 512]
+  const uint8_t* kpe;          // [num_blocks, bs, 64]
+  const float* scales;         // [num_blocks, bs >> g_shift]
+  const int32_t* block_table;  // [B, max_blocks]
+  const int32_t* context_lens; // [B]
+  void* out;                   // [B, q_len, H, 512] of out_dtype
+  float* out_lse;              // [B, q_len, H] or null
+  float* ws_o;                 // [gangs, 2, row_pad, 512] unnormalized O of a gang's two open ends
+  float* ws_ml;                // [gangs, 2, row_pad, 2] their row maxima and sums
+  float scale_log2;            // softmax scale * log2(e)
+  int32_t B, H, q_len, bs, max_blocks, num_blocks, g_shift, causal, window, sinks, out_dtype;
+  int32_t gangs;               // CTAs that share the tiles of the batch, one per row group each
+  int32_t groups, row_pad;     // row groups; rows padded to whole groups
+  uint64_t timeout_ns;
+};
+// Rows per CTA, and gangs, of the launch for q_len * H rows on a device of `sms` SMs.
+int q8_rows_per_cta(int total_rows);
+int q8_gangs(int total_rows, int sms);
+cudaError_t launch_decode_q8(const DecodeQ8Params& p, bool bf16, cudaStream_t stream);
+cudaError_t decode_q8_read_clear_error(uint32_t* out);
+
 // Launchers return cudaSuccess or the launch error. grid.x = cluster of
 // `cluster` CTAs, grid.y = chunks, grid.z = row groups.
 cudaError_t launch_partial_simt(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kpe, const PartialParams& p,

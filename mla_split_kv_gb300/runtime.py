@@ -216,3 +216,107 @@ def plan_segments(seg, dev: nb.mla_device_info_t, max_partitions: int = 0, devic
         tables.append(chunks_to_device(rows, device))
     return SegmentPlan(chunk_tables=tables, plans=plans,
                        o_indptr=torch.tensor(indptr, dtype=torch.int32, device=device), num_slots=indptr[-1])
+
+
+# ---------------------------------------------------------------------------
+# block-scaled 8-bit caches
+# ---------------------------------------------------------------------------
+
+CODE_OF = {torch.float16: nb.MLA_F16, torch.bfloat16: nb.MLA_BF16, torch.float32: nb.MLA_F32}
+
+
+@dataclasses.dataclass
+class Q8Cache:
+    """A paged latent cache in E4M3 bytes with an fp32 scale for every `scale_block` tokens of a page."""
+    ckv: torch.Tensor     # uint8 [num_blocks, bs, 512]
+    kpe: torch.Tensor     # uint8 [num_blocks, bs, 64]
+    scales: torch.Tensor  # float32 [num_blocks, bs / scale_block]
+
+    def __post_init__(self):
+        nblk, bs = int(self.ckv.shape[0]), int(self.ckv.shape[1])
+        _expect(self.ckv, (nblk, bs, 512), torch.uint8, "ckv")
+        _expect(self.kpe, (nblk, bs, 64), torch.uint8, "kpe")
+        if self.scales.dim() != 2 or self.scales.shape[1] < 1 or bs % int(self.scales.shape[1]):
+            raise ValueError(f"scales: {tuple(self.scales.shape)} does not divide pages of {bs} tokens")
+        _expect(self.scales, (nblk, int(self.scales.shape[1])), torch.float32, "scales")
+
+    @property
+    def scale_block(self) -> int:
+        return int(self.ckv.shape[1]) // int(self.scales.shape[1])
+
+
+def _expect(t: torch.Tensor, shape, dtype, what: str) -> None:
+    """The C ABI takes raw pointers to dense row-major buffers: anything else is refused here."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}{'' if t.is_contiguous() else ' with strides ' + str(t.stride())}")
+
+
+def _expect_batch(B: int, block_table: torch.Tensor, context_lens: torch.Tensor) -> None:
+    _expect(context_lens, (B,), torch.int32, "context_lens")
+    _expect(block_table, (B, int(block_table.shape[-1])), torch.int32, "block_table")
+
+
+def alloc_q8_cache(num_blocks: int, block_size: int, scale_block: int, device="cuda") -> Q8Cache:
+    """An empty pool (every byte 0, every scale 1)."""
+    return Q8Cache(torch.zeros((num_blocks, block_size, 512), dtype=torch.uint8, device=device),
+                   torch.zeros((num_blocks, block_size, 64), dtype=torch.uint8, device=device),
+                   torch.ones((num_blocks, block_size // scale_block), dtype=torch.float32, device=device))
+
+
+def cache_append_q8(cache: Q8Cache, ckv_new: torch.Tensor, kpe_new: torch.Tensor, block_table: torch.Tensor,
+                    context_lens: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantize each request's newest tokens [B, q_len, 512 / 64] into the cache (mla_cache_append_q8)."""
+    B, q_len = int(ckv_new.shape[0]), int(ckv_new.shape[1])
+    _expect(ckv_new, (B, q_len, 512), ckv_new.dtype, "ckv_new")
+    _expect(kpe_new, (B, q_len, 64), ckv_new.dtype, "kpe_new")
+    _expect_batch(B, block_table, context_lens)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    nb.mla_cache_append_q8(ckv_new.data_ptr(), kpe_new.data_ptr(), CODE_OF[ckv_new.dtype], block_table.data_ptr(),
+                           context_lens.data_ptr(), B, q_len, int(cache.ckv.shape[1]), cache.scale_block,
+                           int(cache.ckv.shape[0]), int(block_table.shape[1]), cache.ckv.data_ptr(),
+                           cache.kpe.data_ptr(), cache.scales.data_ptr(), s.cuda_stream)
+
+
+@dataclasses.dataclass
+class Q8Plan:
+    """What calls of one shape keep between them: the descriptor's options and the workspace. Calls that may
+    overlap in time (other streams) need a plan each."""
+    num_requests: int
+    num_heads: int
+    q_len: int
+    causal: bool
+    window: int
+    sinks: int
+    workspace: torch.Tensor
+
+
+def plan_q8(num_requests: int, num_heads: int, q_len: int = 1, causal: bool = False, window: int = 0, sinks: int = 0,
+            device="cuda") -> Q8Plan:
+    index = torch.device(device).index
+    n = nb.mla_decode_q8_workspace_bytes(nb.mla_device_query(-1 if index is None else index), q_len, num_heads)
+    if n == 0:
+        raise nb.MlaError(nb.MLA_ERR_UNSUPPORTED, "mla_decode_q8_workspace_bytes")
+    return Q8Plan(num_requests, num_heads, q_len, causal, window, sinks,
+                  torch.empty(n, dtype=torch.uint8, device=device))
+
+
+def decode_q8(plan: Q8Plan, q_abs: torch.Tensor, q_pe: torch.Tensor, cache: Q8Cache, block_table: torch.Tensor,
+              context_lens: torch.Tensor, scale: float, out: torch.Tensor, out_lse: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One decode layer call over a block-scaled 8-bit cache (mla_decode_q8), into out [B, q_len, H, 512]."""
+    B, q_len, H = plan.num_requests, plan.q_len, plan.num_heads
+    _expect(q_abs, (B, q_len, H, 512), q_abs.dtype, "q_abs")
+    _expect(q_pe, (B, q_len, H, 64), q_abs.dtype, "q_pe")
+    _expect(out, (B, q_len, H, 512), out.dtype, "out")
+    if out_lse is not None:
+        _expect(out_lse, (B, q_len, H), torch.float32, "out_lse")
+    _expect_batch(B, block_table, context_lens)
+    d = nb.mla_q8_desc_t(B, H, q_len, int(cache.ckv.shape[1]), int(cache.ckv.shape[0]), int(block_table.shape[1]),
+                         CODE_OF[q_abs.dtype], 1 if plan.causal else 0, cache.scale_block, plan.window, plan.sinks,
+                         CODE_OF[out.dtype], plan.workspace.data_ptr(), plan.workspace.numel(),
+                         (stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+    nb.mla_decode_q8(q_abs.data_ptr(), q_pe.data_ptr(), cache.ckv.data_ptr(), cache.kpe.data_ptr(),
+                     cache.scales.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), scale,
+                     out.data_ptr(), out_lse.data_ptr() if out_lse is not None else None, d)
+    return out

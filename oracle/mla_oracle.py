@@ -383,6 +383,92 @@ def merge_unembed(part, lse2, o_indptr, W_UV_T):
 
 
 # ---------------------------------------------------------------------------
+# sliding windows with sinks; block-scaled 8-bit caches
+# ---------------------------------------------------------------------------
+
+
+def visible_window(n_tokens: int, q_len: int, i: int, causal: bool, window: int, sinks: int) -> np.ndarray:
+    """Tokens row ``i`` sees through a window: those it sees without one (``visible``) that are among the last
+    ``window`` up to its own position (the request's last token without the causal rule), or among the first
+    ``sinks`` of the request. ``window`` 0: no window."""
+    t = np.arange(n_tokens)
+    ok = visible(n_tokens, q_len, i, causal)
+    if window == 0:
+        return ok
+    pos = n_tokens - q_len + i if causal else n_tokens - 1
+    return ok & ((t > pos - window) | (t < sinks))
+
+
+def attend_rows(q_abs, q_pe, ckv_rows, kpe_rows, scale: float, causal: bool, window: int = 0, sinks: int = 0):
+    """Attention of one request's rows ``q_abs [q_len, H, r]`` over its tokens (f64 values in logical order):
+    ``out [q_len, H, r]`` and the log2 LSE ``[q_len, H]``."""
+    q_len, H, r = q_abs.shape
+    out, lse = np.zeros((q_len, H, r)), np.full((q_len, H), -math.inf)
+    for i in range(q_len):
+        vis = visible_window(len(ckv_rows), q_len, i, causal, window, sinks)
+        for h in range(H):
+            s = scores(q_abs[i, h], q_pe[i, h], ckv_rows[vis], kpe_rows[vis], scale)
+            out[i, h], lse[i, h] = attend(s, ckv_rows[vis])
+    return out, lse
+
+
+def request_values_q8(ckv, kpe, scales, table_row, n_tokens: int):
+    """f64 latent and rope rows of a request in a block-scaled cache: ``e4m3(byte) * scale of its block``,
+    blocks of ``page / scales.shape[1]`` tokens."""
+    bs = ckv.shape[1]
+    rows = physical_rows(table_row, n_tokens, bs)
+    z = np.repeat(np.asarray(scales, dtype=np.float64), bs // scales.shape[1], axis=1).reshape(-1)[rows, None]
+    return decode_e4m3(ckv.reshape(-1, ckv.shape[-1])[rows]) * z, decode_e4m3(kpe.reshape(-1, kpe.shape[-1])[rows]) * z
+
+
+def encode_e4m3(x: np.ndarray) -> np.ndarray:
+    """E4M3 pattern nearest to each value (ties to the even mantissa, +-448 beyond), by search among all of them."""
+    values = decode_e4m3(np.arange(127, dtype=np.uint8))  # 0 .. 448, ascending
+    a = np.minimum(np.abs(np.asarray(x, dtype=np.float64)), 448.0)
+    hi = np.clip(np.searchsorted(values, a), 1, 126)
+    below, above = a - values[hi - 1], values[hi] - a
+    pick = np.where((below < above) | ((below == above) & ((hi - 1) % 2 == 0)), hi - 1, hi)
+    return (pick | np.where(np.signbit(x), 0x80, 0)).astype(np.uint8)
+
+
+def block_scale(amax: float) -> float:
+    """The least power of two in [2^-60, 2^60] that takes ``amax`` to 448 or less; NaN if there is none."""
+    for k in range(-60, 61):
+        if amax / 2.0 ** k <= 448.0:
+            return 2.0 ** k
+    return math.nan
+
+
+def cache_append_q8(ckv, kpe, scales, block_table, context_lens, ckv_new, kpe_new):
+    """A block-scaled cache after writing each request's newest tokens (f64 values ``[B, q_len, .]``, positions
+    as in ``cache_append``). Per block with new tokens: the scale of their largest magnitude, or the block's own
+    where earlier tokens stay in it and it is larger; earlier bytes move to a scale that grew. A non-finite
+    value (or one beyond every scale) leaves NaN for the scale and zeros for the block's new bytes."""
+    ckv, kpe, scales = (np.array(a, copy=True) for a in (ckv, kpe, scales))
+    bs, g = ckv.shape[1], ckv.shape[1] // scales.shape[1]
+    for b in range(len(context_lens)):
+        L, q_len = int(context_lens[b]), ckv_new.shape[1]
+        start = max(0, L - q_len)
+        for blk in range(start // g, -(-L // g)):
+            page, at = int(block_table[b][blk * g // bs]), blk * g % bs
+            new = range(max(start, blk * g), min(L, blk * g + g))
+            x = [np.concatenate([ckv_new[b, t - (L - q_len)], kpe_new[b, t - (L - q_len)]]) for t in new]
+            s = block_scale(max(np.abs(v).max() for v in x))
+            old = float(scales[page, at // g])
+            kept = new[0] - blk * g
+            if kept:
+                s = math.nan if math.isnan(s) or math.isnan(old) else max(s, old)
+                if s > old:
+                    for c in (ckv, kpe):
+                        c[page, at:at + kept] = encode_e4m3(decode_e4m3(c[page, at:at + kept]) * (old / s))
+            scales[page, at // g] = s
+            for t, v in zip(new, x):
+                bits = encode_e4m3(v / s) if not math.isnan(s) else np.zeros(v.shape, np.uint8)
+                ckv[page, t % bs], kpe[page, t % bs] = bits[:ckv.shape[-1]], bits[ckv.shape[-1]:]
+    return ckv, kpe, scales
+
+
+# ---------------------------------------------------------------------------
 # KV-memory accounting (mlxcel PR #995, performance-validation commit)
 # ---------------------------------------------------------------------------
 
