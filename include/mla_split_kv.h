@@ -463,6 +463,43 @@ mla_status_t mla_decode(const void* q_absorbed, const void* q_pe, const void* ck
                         float* partials, float* lse, const int32_t* o_indptr, void* out, int32_t out_dtype,
                         float* out_lse, const mla_decode_desc_t* desc);
 
+/*
+ * mla_decode_window -- mla_decode through a sliding window: the row at
+ * position pos (L - q_len + i for row i when causal, L - 1 otherwise) sees, of
+ * the tokens it sees there, those with t > pos - window and the request's
+ * first `sinks` (window >= 1, sinks >= 0; a row may see none: 0 and -inf).
+ * Tokens hidden from a row do not reach it, NaN among them or not.
+ *
+ * Only the pages that some row sees are read. Of each request they form, one
+ * after the other, a visible run: the sinks' pages, then the pages from the
+ * first token that the earliest row's window reaches (mla_window_lens gives
+ * the runs' lengths; a request too short to leave pages out is its own run).
+ * Partitions are of the run: desc->chunks holds positions of it, as mla_plan
+ * makes them from the runs' lengths in place of the contexts', and with
+ * desc->chunks == NULL the run is split into num_partitions. A chunk past the
+ * end of a run is empty, so a plan for the longest run a request can have
+ * (a run's length repeats from page to page of its context) serves every
+ * step, and a captured call may be replayed as the contexts grow.
+ *
+ * The CTA-pair kernels only: MLA_ERR_UNSUPPORTED for MLA_KERNEL_SIMT,
+ * cluster_ctas 1, and clusters other than 2 (or 0 = auto) with more than 16
+ * rows. Caches of any dtype that mla_decode takes. desc->prefix_ready speaks
+ * of the same positions as there. Otherwise mla_decode's arguments and
+ * results. The pages have no counterpart.
+ */
+mla_status_t mla_decode_window(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                               const int32_t* block_table, const int32_t* context_lens, float scale,
+                               int32_t num_partitions, float* partials, float* lse, const int32_t* o_indptr, void* out,
+                               int32_t out_dtype, float* out_lse, int32_t window, int32_t sinks,
+                               const mla_decode_desc_t* desc);
+
+/* The lengths of the requests' visible runs (see mla_decode_window) into
+ * visible_lens_host [B]. Host code; touches no GPU. MLA_ERR_INVALID_ARG /
+ * MLA_ERR_UNSUPPORTED for arguments that mla_plan or mla_decode_window would
+ * refuse. */
+mla_status_t mla_window_lens(const int32_t* context_lens_host, int32_t B, int32_t q_len, int32_t block_size,
+                             int32_t causal, int32_t window, int32_t sinks, int32_t* visible_lens_host);
+
 /* Workspace bytes of mla_decode on the paired kernel, one layout for both of
  * its ways: B * 16 uint32 request tickets and num_chunks * q_len * H fp32 LSE
  * copies (the TICKETS way's; each block 256-byte aligned), then two uint32

@@ -140,6 +140,11 @@ def load() -> ctypes.CDLL:
     lib.mla_decode.argtypes = [vp, vp, vp, vp, vp, vp, f32, i32, vp, vp, vp, vp, i32, vp,
                                ctypes.POINTER(mla_decode_desc_t)]
     lib.mla_decode.restype = i32
+    lib.mla_decode_window.argtypes = [vp, vp, vp, vp, vp, vp, f32, i32, vp, vp, vp, vp, i32, vp, i32, i32,
+                                      ctypes.POINTER(mla_decode_desc_t)]
+    lib.mla_decode_window.restype = i32
+    lib.mla_window_lens.argtypes = [ctypes.POINTER(i32), i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
+    lib.mla_window_lens.restype = i32
     lib.mla_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.mla_decode_workspace_bytes.restype = u64
     lib.mla_cache_append.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
@@ -272,6 +277,25 @@ def mla_decode(q_absorbed: int, q_pe: int, ckv_cache: int, kpe_cache: int, block
     _check(load().mla_decode(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, ctypes.c_float(scale),
                              num_partitions, partials, lse, o_indptr, out, out_dtype, out_lse or None,
                              ctypes.byref(desc)), "mla_decode")
+
+
+def mla_decode_window(q_absorbed: int, q_pe: int, ckv_cache: int, kpe_cache: int, block_table: int, context_lens: int,
+                      scale: float, num_partitions: int, partials: int, lse: int, o_indptr: int, out: int,
+                      out_dtype: int, out_lse: Optional[int], window: int, sinks: int,
+                      desc: mla_decode_desc_t) -> None:
+    _check(load().mla_decode_window(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, scale,
+                                    num_partitions, partials, lse, o_indptr, out, out_dtype, out_lse or None, window,
+                                    sinks, desc), "mla_decode_window")
+
+
+def mla_window_lens(context_lens: Sequence[int], q_len: int, block_size: int, causal: bool, window: int,
+                    sinks: int) -> list:
+    B = len(context_lens)
+    lens = (ctypes.c_int32 * B)(*[int(x) for x in context_lens])
+    out = (ctypes.c_int32 * B)()
+    _check(load().mla_window_lens(lens, B, q_len, block_size, 1 if causal else 0, window, sinks, out),
+           "mla_window_lens")
+    return list(out)
 
 
 def mla_decode_unembed(q_absorbed: int, q_pe: int, ckv_cache: int, kpe_cache: int, block_table: int,

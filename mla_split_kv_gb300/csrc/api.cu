@@ -269,8 +269,13 @@ struct FusedMerge {
   float* lse_copy = nullptr;
 };
 
+// The window of mla_decode_window (0: none).
+struct Window {
+  int32_t window = 0, sinks = 0;
+};
+
 // Cluster size the launch will use (the descriptor's, or the library's choice).
-int launch_cluster(const mla_decode_desc_t* d, int64_t N) {
+int launch_cluster(const mla_decode_desc_t* d, int64_t N, Window win = Window{}) {
   const bool use_simt = (d->kernel == MLA_KERNEL_SIMT);
   const int rows_total = d->num_heads * d->q_len;
   const bool mh = !use_simt && mla::mh_supports(rows_total, d->cluster_ctas ? d->cluster_ctas : 2);
@@ -278,7 +283,7 @@ int launch_cluster(const mla_decode_desc_t* d, int64_t N) {
                           : (mh ? 128 : mla::tc_rows_per_cta(rows_total, d->dtype == MLA_BF16));
   const int64_t groups = (rows_total + nr - 1) / nr;
   const int C = d->cluster_ctas ? d->cluster_ctas : (mh ? 2 : default_cluster(N * groups));
-  return (d->dtype == MLA_E4M3 && C < 2) ? 2 : C;  // E4M3 runs on CTA pairs
+  return ((d->dtype == MLA_E4M3 || win.window > 0) && C < 2) ? 2 : C;  // E4M3 and windows run on CTA pairs
 }
 
 // One launch of the partial kernel the descriptor selects (arguments already checked; N chunks;
@@ -286,7 +291,8 @@ int launch_cluster(const mla_decode_desc_t* d, int64_t N) {
 mla_status_t launch_decode(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
                            const int32_t* block_table, const int32_t* context_lens, float scale,
                            int32_t num_partitions, float* partials, float* lse, const mla_decode_desc_t* d,
-                           int64_t N, void* spread_ws, const FusedMerge& fm, bool entries_only = false) {
+                           int64_t N, void* spread_ws, const FusedMerge& fm, bool entries_only = false,
+                           Window win = Window{}) {
   const int32_t C0 = d->cluster_ctas;
   const uint64_t rows = static_cast<uint64_t>(d->num_blocks) * static_cast<uint64_t>(d->block_size);
   const bool use_simt = (d->kernel == MLA_KERNEL_SIMT);
@@ -298,7 +304,7 @@ mla_status_t launch_decode(const void* q_absorbed, const void* q_pe, const void*
   const int nr = use_simt ? mla::simt_rows_per_cta() : (mh ? 128 : mla::tc_rows_per_cta(rows_total, bf16));
   const int64_t groups = (rows_total + nr - 1) / nr;
   const int32_t subs = (d->clusters_per_chunk > 1) ? d->clusters_per_chunk : 1;
-  const int C = launch_cluster(d, N);
+  const int C = launch_cluster(d, N, win);
 
   CUtensorMap tm_ckv, tm_kpe, tm_pages, tm_kpe_half;
   const bool fp8 = (d->dtype == MLA_E4M3);
@@ -342,6 +348,8 @@ mla_status_t launch_decode(const void* q_absorbed, const void* q_pe, const void*
   p.causal = d->causal;
   p.tables_ready = d->tables_ready;
   p.prefix_ready = d->prefix_ready;
+  p.window = win.window;
+  p.sinks = win.sinks;
   // the 128-row kernel's pair: 0 fp32 partial scores cross, 1 fp16 ones, 2 none (each CTA computes the full
   // scores). The exact default: none on 16-bit caches with a full group of 128 rows; with fewer rows (a
   // 64-row group: half of each score product is padding) the fp32 exchange of the real rows' scores
@@ -440,9 +448,9 @@ struct PairEntries {
 mla_status_t launch_pair_entries(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
                                  const int32_t* block_table, const int32_t* context_lens, float scale,
                                  int32_t num_partitions, float* partials, float* lse, const mla_decode_desc_t* d,
-                                 int64_t N, PairEntries* out) {
+                                 int64_t N, PairEntries* out, Window win = Window{}) {
   const int rows_total = d->num_heads * d->q_len;
-  const int32_t C = launch_cluster(d, N);
+  const int32_t C = launch_cluster(d, N, win);
   const uint64_t head = round256(static_cast<uint64_t>(d->num_requests) * mla::kSliceTickets * 4) +
                         round256(static_cast<uint64_t>(N) * rows_total * 4);  // the TICKETS way's blocks
   const uint64_t need = head + entries_ws_bytes(N, d->clusters_per_chunk, C, d->q_len, d->num_heads);
@@ -451,7 +459,7 @@ mla_status_t launch_pair_entries(const void* q_absorbed, const void* q_pe, const
   uint8_t* ws = static_cast<uint8_t*>(d->workspace) + head;
   const int32_t k = d->clusters_per_chunk > 1 ? d->clusters_per_chunk : 1;
   mla_status_t st = launch_decode(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, scale,
-                                  num_partitions, partials, lse, d, N, ws, FusedMerge{}, true);
+                                  num_partitions, partials, lse, d, N, ws, FusedMerge{}, true, win);
   if (st != MLA_OK) return st;
   const uint64_t entries = static_cast<uint64_t>(N) * k * (C / 2);
   out->o = reinterpret_cast<const float*>(ws + round256(static_cast<uint64_t>(N) * 2 * 4));
@@ -462,12 +470,13 @@ mla_status_t launch_pair_entries(const void* q_absorbed, const void* q_pe, const
 
 }  // namespace
 
-extern "C" {
+namespace {
 
-mla_status_t mla_decode(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
-                        const int32_t* block_table, const int32_t* context_lens, float scale, int32_t num_partitions,
-                        float* partials, float* lse, const int32_t* o_indptr, void* out, int32_t out_dtype,
-                        float* out_lse, const mla_decode_desc_t* d) {
+// mla_decode, and mla_decode_window with its window
+mla_status_t decode_call(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                         const int32_t* block_table, const int32_t* context_lens, float scale, int32_t num_partitions,
+                         float* partials, float* lse, const int32_t* o_indptr, void* out, int32_t out_dtype,
+                         float* out_lse, const mla_decode_desc_t* d, Window win) {
   int64_t N = 0;
   const mla_status_t chk = check_decode(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, scale,
                                         num_partitions, partials, lse, d, false, &N);
@@ -478,7 +487,7 @@ mla_status_t mla_decode(const void* q_absorbed, const void* q_pe, const void* ck
   if (out_dtype != MLA_F16 && out_dtype != MLA_BF16 && out_dtype != MLA_F32) return reject(MLA_ERR_UNSUPPORTED);
   const int rows_total = d->num_heads * d->q_len;
   const bool paired = d->kernel != MLA_KERNEL_SIMT &&
-                      mla::tc128_supports(rows_total, d->dtype == MLA_BF16, launch_cluster(d, N));
+                      mla::tc128_supports(rows_total, d->dtype == MLA_BF16, launch_cluster(d, N, win));
   const bool fused = paired && d->decode_merge == MLA_DECODE_MERGE_TICKETS;
   if (paired && !fused) {
     // the paired kernel writes every CTA pair's part to the workspace and exits; the entries merge
@@ -486,7 +495,7 @@ mla_status_t mla_decode(const void* q_absorbed, const void* q_pe, const void* ck
     // straight into the output
     PairEntries pe;
     mla_status_t st = launch_pair_entries(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, scale,
-                                          num_partitions, partials, lse, d, N, &pe);
+                                          num_partitions, partials, lse, d, N, &pe, win);
     if (st != MLA_OK) return st;
     mla::EntryMergeParams mp;
     mp.ws_partials = pe.o;
@@ -515,7 +524,7 @@ mla_status_t mla_decode(const void* q_absorbed, const void* q_pe, const void* ck
         return reject(MLA_ERR_INVALID_ARG);
     }
     mla_status_t st = launch_decode(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, scale,
-                                    num_partitions, partials, lse, d, N, d->workspace, FusedMerge{});
+                                    num_partitions, partials, lse, d, N, d->workspace, FusedMerge{}, false, win);
     if (st != MLA_OK) return st;
     return mla_merge_states(partials, lse, o_indptr, d->num_requests, d->q_len, d->num_heads, out, out_dtype, out_lse,
                             d->stream);
@@ -535,7 +544,33 @@ mla_status_t mla_decode(const void* q_absorbed, const void* q_pe, const void* ck
   fm.lse_copy = reinterpret_cast<float*>(ws + tickets);
   void* spread_ws = ws + tickets + round256(static_cast<uint64_t>(N) * rows_total * 4);
   return launch_decode(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, scale, num_partitions,
-                       partials, lse, d, N, spread_ws, fm);
+                       partials, lse, d, N, spread_ws, fm, false, win);
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status_t mla_decode(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                        const int32_t* block_table, const int32_t* context_lens, float scale, int32_t num_partitions,
+                        float* partials, float* lse, const int32_t* o_indptr, void* out, int32_t out_dtype,
+                        float* out_lse, const mla_decode_desc_t* d) {
+  return decode_call(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, scale, num_partitions, partials,
+                     lse, o_indptr, out, out_dtype, out_lse, d, Window{});
+}
+
+mla_status_t mla_decode_window(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                               const int32_t* block_table, const int32_t* context_lens, float scale,
+                               int32_t num_partitions, float* partials, float* lse, const int32_t* o_indptr, void* out,
+                               int32_t out_dtype, float* out_lse, int32_t window, int32_t sinks,
+                               const mla_decode_desc_t* d) {
+  if (d == nullptr || window < 1 || sinks < 0) return reject(MLA_ERR_INVALID_ARG);
+  // the CTA-pair kernels only (16 rows: clusters of 2 or more; more rows: the 128-row kernels' pairs)
+  if (d->kernel == MLA_KERNEL_SIMT || d->cluster_ctas == 1) return reject(MLA_ERR_UNSUPPORTED);
+  if (static_cast<int64_t>(d->num_heads) * d->q_len > 16 && d->cluster_ctas != 0 && d->cluster_ctas != 2)
+    return reject(MLA_ERR_UNSUPPORTED);
+  return decode_call(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, scale, num_partitions, partials,
+                     lse, o_indptr, out, out_dtype, out_lse, d, Window{window, sinks});
 }
 
 mla_status_t mla_decode_unembed(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,

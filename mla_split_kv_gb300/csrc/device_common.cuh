@@ -508,7 +508,8 @@ __device__ __forceinline__ void ticket_reset(uint32_t* t) {
 // ---------------------------------------------------------------------------
 struct CtaWork {
   int32_t b, t0, t1, slot;  // chunk
-  int32_t L;                // context length of request b
+  int32_t L;                // context length of request b (with a window: of its visible run)
+  int32_t gap_page, gap;    // pages of the run from gap_page on lie `gap` pages further on in the table
   int32_t sub0, sub1;       // this CTA's tokens [sub0, sub1)
   int32_t row0, nrows;      // query rows [row0, row0 + nrows) of this CTA
 };
@@ -549,6 +550,13 @@ __device__ __forceinline__ CtaWork cta_work(const PartialParams& p, int32_t rows
   w.L = 0;
   if (w.b >= 0 && w.b < p.B) w.L = p.context_lens[w.b];
   if (w.L < 0) w.L = 0;
+  w.gap_page = w.gap = 0;
+  if (p.window > 0) {
+    const WindowView v = window_view(w.L, p.q_len, p.bs, p.causal, p.window, p.sinks);
+    w.L = v.n;
+    w.gap_page = v.sa / p.bs;
+    w.gap = v.skip / p.bs;
+  }
   if (p.chunks == nullptr) uniform_chunk(w.L, p.num_parts, n % p.num_parts, p.bs, &w.t0, &w.t1);
   if (w.t1 > w.L) w.t1 = w.L;
   if (w.t0 < 0) w.t0 = 0;
@@ -575,6 +583,19 @@ __device__ __forceinline__ CtaWork cta_work(const PartialParams& p, int32_t rows
   if (w.sub1 > tend) w.sub1 = tend;
   if (w.sub0 > w.sub1) w.sub0 = w.sub1;
   return w;
+}
+
+// The table's column of page `pg` of a request's visible run.
+__device__ __forceinline__ int32_t table_page(const CtaWork& w, int32_t pg) {
+  return pg + (pg >= w.gap_page ? w.gap : 0);
+}
+// The last position of the visible run that the window of the row at position `pos` leaves out (-1: none).
+__device__ __forceinline__ int32_t window_low(const PartialParams& p, int32_t pos) {
+  return p.window > 0 ? max(-1, pos - p.window) : -1;
+}
+// Whether a window hides position u from the row at position `pos`, both in the visible run.
+__device__ __forceinline__ bool window_hides(const PartialParams& p, int32_t u, int32_t pos) {
+  return u <= window_low(p, pos) && u >= p.sinks;
 }
 
 // Page id of logical page `pg` of request b, with a range check: an entry
@@ -820,6 +841,39 @@ __device__ __forceinline__ void widen_ckv_steps(uint32_t slot, uint32_t stage_sr
     const uint32_t row = slot + (t >> 3) * 4096 + cbl * 1024 + r * 128;
     widen16(v, row + (((2 * kk) ^ r) << 4), row + (((2 * kk + 1) ^ r) << 4));
   }
+}
+
+// Infinities and NaN to zero in tokens [t0, t1) of a CTA's half of a tile's 16-bit ckv (row groups of four
+// swizzled [8 x 64] atoms, 4 KB apart): tokens that some row of a windowed call does not see. Their
+// probability there is 0, and 0 times a non-finite value would not be; for a row that does see one, its
+// score has already made the probability non-finite.
+template <bool BF16>
+__device__ __forceinline__ void clear_non_finite(uint8_t* ckv, int t0, int t1, int tid, int nthreads) {
+  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+  for (int x = tid; x < (t1 - t0) * 32; x += nthreads) {
+    const int t = t0 + (x >> 5), c = (x >> 3) & 3;
+    uint32_t* const at = reinterpret_cast<uint32_t*>(ckv + (t >> 3) * 4096 + c * 1024 + (t & 7) * 128 + (x & 7) * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t v = at[j];
+      if ((v & kExp) == kExp) v &= 0xffff0000u;
+      if ((v & (kExp << 16)) == (kExp << 16)) v &= 0xffffu;
+      at[j] = v;
+    }
+  }
+}
+// The same for the tokens of the tile [tok0, tok0 + nvalid) that a windowed call hides from some row: below
+// the last row's window, and behind the first row when causal. Call with all softmax threads once the
+// tile's score product is done, before its PV product is released.
+template <bool BF16>
+__device__ __forceinline__ void clear_hidden(const PartialParams& p, const CtaWork& w, uint8_t* ckv, int tok0,
+                                             int nvalid, int tid, int nthreads) {
+  const int first = p.causal ? max(w.L - p.q_len + 1, 0) : w.L;  // positions behind the first row
+  const int a0 = max(tok0, min(p.sinks, tok0 + nvalid)), a1 = min(tok0 + nvalid, window_low(p, w.L - 1) + 1);
+  const int b0 = max(tok0, first), b1 = tok0 + nvalid;
+  if (a0 < a1) clear_non_finite<BF16>(ckv, a0 - tok0, a1 - tok0, tid, nthreads);
+  if (b0 < b1) clear_non_finite<BF16>(ckv, b0 - tok0, b1 - tok0, tid, nthreads);
+  fence_proxy_async_smem();
 }
 
 // Request b's chunk slots [lo, hi): from the offsets, or the uniform split.

@@ -62,6 +62,9 @@ struct PartialParams {
   // the paired kernel writes every CTA pair's part (unnormalized O^T, row maxima and sums) as an
   // entry of ws_partials / ws_lse and nothing else; the entries merge kernel combines them
   int32_t entries_only;
+  // a sliding window beside the first `sinks` tokens (0: none); chunks, lengths and positions are then those
+  // of the requests' visible runs (WindowView)
+  int32_t window, sinks;
 };
 constexpr int kSliceTickets = 16;  // per request: one per column slice (cluster rank) or column half
 

@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (base != win_base) {
         win_base = base;
         const int q = base + lane;
-        win_pid = (q < npages_req && q < p.max_blocks) ? checked_page(p, w.b, q) : -1;
+        const int tq = table_page(w, q);
+        win_pid = (q < npages_req && tq < p.max_blocks) ? checked_page(p, w.b, tq) : -1;
       }
       return __shfl_sync(0xffffffffu, win_pid, pg & 31);
     };
@@ -671,15 +672,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_remote_arrive_relaxed(peer_xempty);
         }
         const int nvis = min(kT, tlim - tok0) - kHalfT * hf;  // tokens of this half the row can see
-        if (__builtin_expect(nvis < kHalfT, 0)) {
+        if (__builtin_expect(nvis < kHalfT || tok0 <= window_low(p, w.L - 1), 0)) {
+          const int low = window_low(p, p.causal ? w.L - p.q_len + row_q : w.L - 1) - tok0 - kHalfT * hf;
+          const int sink = p.sinks - tok0 - kHalfT * hf;
 #pragma unroll
-          for (int t = 0; t < kHalfT; ++t) x[t] = (t < nvis) ? x[t] * scale_log2 : -INFINITY;
+          for (int t = 0; t < kHalfT; ++t)
+            x[t] = (t < nvis && (t > low || t < sink)) ? x[t] * scale_log2 : -INFINITY;
         } else {
 #pragma unroll
           for (int t = 0; t < kHalfT; ++t) x[t] *= scale_log2;
         }
 #pragma unroll
         for (int t = 0; t < kHalfT; ++t) mx = fmaxf(mx, x[t]);
+        if (p.window > 0 && (tok0 <= window_low(p, w.L - 1) || p.causal))
+          clear_hidden<BF16>(p, w, smem + kOffTile + (i % kSlots) * kTileSlot, tok0, min(kT, w.sub1 - tok0), tid, kSoftmaxThreads);
       }
       sm->half_val[hf][r] = mx;
       if (named_bar_sync_or(1, kSoftmaxThreads, !ok || *abort_flag != 0)) {

@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (base != win_base) {
         win_base = base;
         const int q = base + lane;
-        win_pid = (q < npages_req && q < p.max_blocks) ? checked_page(p, w.b, q) : -1;
+        const int tq = table_page(w, q);
+        win_pid = (q < npages_req && tq < p.max_blocks) ? checked_page(p, w.b, tq) : -1;
       }
       return __shfl_sync(0xffffffffu, win_pid, pg & 31);
     };
@@ -431,15 +432,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(sa + 16, x + 16);
         tmem_wait_ld();
         const int nvis = min(kT, tlim - (w.sub0 + i * kT)) - kHalfT * hf;  // tokens of this half the row sees
-        if (__builtin_expect(nvis < kHalfT, 0)) {
+        if (__builtin_expect(nvis < kHalfT || (w.sub0 + i * kT) <= window_low(p, w.L - 1), 0)) {
+          const int low = window_low(p, p.causal ? w.L - p.q_len + row_q : w.L - 1) - (w.sub0 + i * kT) - kHalfT * hf;
+          const int sink = p.sinks - (w.sub0 + i * kT) - kHalfT * hf;
 #pragma unroll
-          for (int t = 0; t < kHalfT; ++t) x[t] = (t < nvis) ? x[t] * scale_log2 : -INFINITY;
+          for (int t = 0; t < kHalfT; ++t)
+            x[t] = (t < nvis && (t > low || t < sink)) ? x[t] * scale_log2 : -INFINITY;
         } else {
 #pragma unroll
           for (int t = 0; t < kHalfT; ++t) x[t] *= scale_log2;
         }
 #pragma unroll
         for (int t = 0; t < kHalfT; ++t) mx = fmaxf(mx, x[t]);
+        if (p.window > 0 && ((w.sub0 + i * kT) <= window_low(p, w.L - 1) || p.causal))
+          clear_hidden<BF16>(p, w, smem + kOffTile + (i % kSlots) * kTileSlot + half * kCkvBytes, (w.sub0 + i * kT), min(kT, w.sub1 - (w.sub0 + i * kT)), tid, kSoftmaxThreads);
       }
       sm->half_val[hf][r] = mx;
       if (named_bar_sync_or(1, kSoftmaxThreads, !ok || *abort_flag != 0)) {

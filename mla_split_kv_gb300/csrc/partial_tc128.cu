@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     win_base = pg & ~31;
     const int q = win_base + lane;
     const int npages_req = (w.L + p.bs - 1) / p.bs;
-    win_pid = (q < npages_req && q < p.max_blocks) ? checked_page(p, w.b, q) : -1;
+    const int tq = table_page(w, q);
+    win_pid = (q < npages_req && tq < p.max_blocks) ? checked_page(p, w.b, tq) : -1;
   };
   // producers: warp kMmaWarp + 1 + k0 loads pages k0, k0 + kPageWarps, ... of each tile
   const int k0 = warp - kMmaWarp - 1;
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* region = smem + kOffTile + s * kTileSlot + kCkvBytes;  // the peer's partial S, then P^T
       const int tok0 = w.sub0 + i * kT;
       const int nvalid = min(kT, w.sub1 - tok0);
-      const bool masked_tile = (nvalid < kT) || (tok0 + kT - 1 > causal_floor) || (w.nrows < kNR);
+      const bool masked_tile = (nvalid < kT) || (tok0 + kT - 1 > causal_floor) || (w.nrows < kNR) || (tok0 <= window_low(p, w.L - 1));
       int ok = sent ? mbar_wait_cluster(&sm->xfull[s], (i / kSlots) & 1, tmo) : 0;
       ok = __all_sync(0xffffffffu, ok);
       bool need_local = false;
@@ -696,8 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = kRH * h + k;
             bool vis = (tl < nvalid) && (r < w.nrows);
             if (p.causal) vis = vis && (t <= w.L - p.q_len + (w.row0 + r) / p.H);
+            vis = vis && !window_hides(p, t, p.causal ? w.L - p.q_len + (w.row0 + r) / p.H : w.L - 1);
             x[k] = vis ? x[k] * scale_log2 : -INFINITY;
           }
+          if (p.window > 0) clear_hidden<kBf16>(p, w, smem + kOffTile + s * kTileSlot, tok0, nvalid, tid, kSoftmaxThreads);
         } else {
 #pragma unroll
           for (int k = 0; k < kRH; ++k) x[k] *= scale_log2;

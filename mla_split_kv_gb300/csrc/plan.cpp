@@ -74,6 +74,19 @@ double paired_cost_us(int64_t L, int64_t P, int64_t k, int C, int32_t merge_path
 
 }  // namespace
 
+extern "C" mla_status_t mla_window_lens(const int32_t* context_lens_host, int32_t B, int32_t q_len, int32_t block_size,
+                                        int32_t causal, int32_t window, int32_t sinks, int32_t* visible_lens_host) {
+  if (context_lens_host == nullptr || visible_lens_host == nullptr || B < 1) return MLA_ERR_INVALID_ARG;
+  if (q_len < 1 || q_len > MLA_MAX_Q_LEN) return MLA_ERR_UNSUPPORTED;
+  if (block_size != 16 && block_size != 32 && block_size != 64) return MLA_ERR_UNSUPPORTED;
+  if ((causal != 0 && causal != 1) || window < 1 || sinks < 0) return MLA_ERR_INVALID_ARG;
+  for (int32_t b = 0; b < B; ++b)
+    if (context_lens_host[b] < 0) return MLA_ERR_INVALID_ARG;
+  for (int32_t b = 0; b < B; ++b)
+    visible_lens_host[b] = mla::window_view(context_lens_host[b], q_len, block_size, causal, window, sinks).n;
+  return MLA_OK;
+}
+
 extern "C" mla_status_t mla_plan(const int32_t* context_lens_host, int32_t B, int32_t num_heads, int32_t q_len,
                                  int32_t block_size, const mla_device_info_t* dev, mla_plan_t* plan) {
   if (context_lens_host == nullptr || dev == nullptr || plan == nullptr) return MLA_ERR_INVALID_ARG;

@@ -219,6 +219,76 @@ def plan_segments(seg, dev: nb.mla_device_info_t, max_partitions: int = 0, devic
 
 
 # ---------------------------------------------------------------------------
+# sliding windows
+# ---------------------------------------------------------------------------
+
+
+@dataclasses.dataclass
+class WindowPlan:
+    """A plan of mla_decode_window for one batch shape, with the buffers its calls use. It serves the lengths it
+    was made for and every request with a visible run no longer than planned. Calls that may overlap in time
+    (other streams) need a plan each."""
+    num_requests: int
+    num_heads: int
+    q_len: int
+    block_size: int
+    dtype: str
+    causal: bool
+    window: int
+    sinks: int
+    plan: nb.Plan
+    chunks: torch.Tensor
+    o_indptr: torch.Tensor
+    partials: torch.Tensor
+    lse: torch.Tensor
+    workspace: torch.Tensor
+
+
+def plan_window(context_lens: Sequence[int], num_heads: int, q_len: int, block_size: int, window: int, sinks: int = 0,
+                dtype: str = "f16", causal: bool = False, dev: Optional[nb.mla_device_info_t] = None,
+                max_partitions: int = 0, device="cuda") -> WindowPlan:
+    runs = nb.mla_window_lens(context_lens, q_len, block_size, causal, window, sinks)
+    index = torch.device(device).index
+    dev = dev if dev is not None else nb.mla_device_query(-1 if index is None else index)
+    plan = nb.mla_plan(runs, num_heads, q_len, block_size, dev, max_partitions=max_partitions, dtype=dtype)
+    part, lse = alloc_partials(plan.num_chunks, q_len, num_heads, device)
+    return WindowPlan(len(runs), num_heads, q_len, block_size, dtype, causal, window, sinks, plan,
+                      chunks_to_device(plan.chunks, device),
+                      torch.tensor(plan.o_indptr, dtype=torch.int32, device=device), part, lse,
+                      alloc_decode_workspace(len(runs), plan.num_chunks, plan.clusters_per_chunk, plan.cluster_ctas,
+                                             q_len, num_heads, device))
+
+
+def decode_window(plan: WindowPlan, q_abs: torch.Tensor, q_pe: torch.Tensor, ckv: torch.Tensor, kpe: torch.Tensor,
+                  block_table: torch.Tensor, context_lens: torch.Tensor, scale: float, out: torch.Tensor,
+                  out_lse: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                  cache_scale: float = 1.0) -> torch.Tensor:
+    """One decode layer call through a sliding window (mla_decode_window), into out [B, q_len, H, 512]."""
+    B, q_len, H, bs = plan.num_requests, plan.q_len, plan.num_heads, plan.block_size
+    cache_dtype = torch.uint8 if plan.dtype == "e4m3" else TORCH_DTYPE[plan.dtype]
+    q_dtype = TORCH_DTYPE[query_dtype(plan.dtype)]
+    _expect(q_abs, (B, q_len, H, 512), q_dtype, "q_abs")
+    _expect(q_pe, (B, q_len, H, 64), q_dtype, "q_pe")
+    _expect(ckv, (int(ckv.shape[0]), bs, 512), cache_dtype, "ckv")
+    _expect(kpe, (int(ckv.shape[0]), bs, 64), cache_dtype, "kpe")
+    _expect(out, (B, q_len, H, 512), out.dtype, "out")
+    if out_lse is not None:
+        _expect(out_lse, (B, q_len, H), torch.float32, "out_lse")
+    _expect_batch(B, block_table, context_lens)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    p = plan.plan
+    d = nb.mla_decode_desc_t(B, H, q_len, bs, int(ckv.shape[0]), int(block_table.shape[1]), nb.DTYPE_CODES[plan.dtype],
+                             1 if plan.causal else 0, plan.chunks.data_ptr(), p.num_chunks, p.cluster_ctas,
+                             nb.MLA_KERNEL_TC, s.cuda_stream, p.clusters_per_chunk, plan.workspace.data_ptr(),
+                             plan.workspace.numel(), 0, 0, 0, cache_scale, 0)
+    nb.mla_decode_window(q_abs.data_ptr(), q_pe.data_ptr(), ckv.data_ptr(), kpe.data_ptr(), block_table.data_ptr(),
+                         context_lens.data_ptr(), scale, 0, plan.partials.data_ptr(), plan.lse.data_ptr(),
+                         plan.o_indptr.data_ptr(), out.data_ptr(), CODE_OF[out.dtype],
+                         out_lse.data_ptr() if out_lse is not None else None, plan.window, plan.sinks, d)
+    return out
+
+
+# ---------------------------------------------------------------------------
 # block-scaled 8-bit caches
 # ---------------------------------------------------------------------------
 
