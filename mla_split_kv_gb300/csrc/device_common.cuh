@@ -529,7 +529,9 @@ __device__ __forceinline__ void uniform_chunk(int32_t L, int32_t P, int32_t p, i
 // `unit`-token tiles split evenly over the cluster, or over `nparts` groups,
 // this CTA in group `part`) and its query rows (row group blockIdx.z, or
 // `row_group`). Tokens are trimmed to the last one any row
-// of this CTA can see under the causal rule.
+// of this CTA can see under the causal rule. kWin: a windowed call
+// (mla_decode_window; instances of their own, so that other calls pay nothing for it).
+template <bool kWin = false>
 __device__ __forceinline__ CtaWork cta_work(const PartialParams& p, int32_t rows_per_cta,
                                             int32_t unit = kTileTokens, int32_t part = -1, int32_t nparts = 0,
                                             int32_t chunk = -1, int32_t row_group = -1) {
@@ -551,7 +553,7 @@ __device__ __forceinline__ CtaWork cta_work(const PartialParams& p, int32_t rows
   if (w.b >= 0 && w.b < p.B) w.L = p.context_lens[w.b];
   if (w.L < 0) w.L = 0;
   w.gap_page = w.gap = 0;
-  if (p.window > 0) {
+  if constexpr (kWin) {
     const WindowView v = window_view(w.L, p.q_len, p.bs, p.causal, p.window, p.sinks);
     w.L = v.n;
     w.gap_page = v.sa / p.bs;
@@ -586,16 +588,19 @@ __device__ __forceinline__ CtaWork cta_work(const PartialParams& p, int32_t rows
 }
 
 // The table's column of page `pg` of a request's visible run.
+template <bool kWin>
 __device__ __forceinline__ int32_t table_page(const CtaWork& w, int32_t pg) {
-  return pg + (pg >= w.gap_page ? w.gap : 0);
+  return pg + (kWin && pg >= w.gap_page ? w.gap : 0);
 }
 // The last position of the visible run that the window of the row at position `pos` leaves out (-1: none).
+template <bool kWin>
 __device__ __forceinline__ int32_t window_low(const PartialParams& p, int32_t pos) {
-  return p.window > 0 ? max(-1, pos - p.window) : -1;
+  return kWin ? max(-1, pos - p.window) : -1;
 }
 // Whether a window hides position u from the row at position `pos`, both in the visible run.
+template <bool kWin>
 __device__ __forceinline__ bool window_hides(const PartialParams& p, int32_t u, int32_t pos) {
-  return u <= window_low(p, pos) && u >= p.sinks;
+  return kWin && u <= window_low<kWin>(p, pos) && u >= p.sinks;
 }
 
 // Page id of logical page `pg` of request b, with a range check: an entry
@@ -869,7 +874,7 @@ template <bool BF16>
 __device__ __forceinline__ void clear_hidden(const PartialParams& p, const CtaWork& w, uint8_t* ckv, int tok0,
                                              int nvalid, int tid, int nthreads) {
   const int first = p.causal ? max(w.L - p.q_len + 1, 0) : w.L;  // positions behind the first row
-  const int a0 = max(tok0, min(p.sinks, tok0 + nvalid)), a1 = min(tok0 + nvalid, window_low(p, w.L - 1) + 1);
+  const int a0 = max(tok0, min(p.sinks, tok0 + nvalid)), a1 = min(tok0 + nvalid, window_low<true>(p, w.L - 1) + 1);
   const int b0 = max(tok0, first), b1 = tok0 + nvalid;
   if (a0 < a1) clear_non_finite<BF16>(ckv, a0 - tok0, a1 - tok0, tid, nthreads);
   if (b0 < b1) clear_non_finite<BF16>(ckv, b0 - tok0, b1 - tok0, tid, nthreads);

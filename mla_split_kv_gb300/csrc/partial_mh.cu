@@ -115,7 +115,7 @@ __device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { retur
 
 // X16: the pair's partial scores cross as fp16 (an instance each, no run-time branch in the loop);
 // FP8: E4M3 caches beside fp16 queries (BF16 false), widened in the tile slots, scaled on the output
-template <bool BF16, bool X16, bool FP8>
+template <bool BF16, bool X16, bool FP8, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_partial_mh_kernel(const __grid_constant__ CUtensorMap tm_pages, const __grid_constant__ CUtensorMap tm_kpe_half,
                           const PartialParams p) {
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // both CTAs of the pair take the whole chunk; pair g = blockIdx.x / 2 takes query rows [128 g, 128 g + 128)
   // (the row groups of a chunk are adjacent clusters, so they stream the same tiles at about the same time
   // and the later reads are served by L2)
-  const CtaWork w = cta_work(p, kRows, kT, 0, 1, -1, static_cast<int32_t>(blockIdx.x >> 1));
+  const CtaWork w = cta_work<kWin>(p, kRows, kT, 0, 1, -1, static_cast<int32_t>(blockIdx.x >> 1));
   const int ntiles = (w.sub1 - w.sub0 + kT - 1) / kT;
   // only the group's real rows exchange their partial scores (a group of 64 rows, H=64, sends half),
   // 4 bytes a score, or 2 with the fp16 exchange; the peer's bytes of tile 0 may land before this
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (base != win_base) {
         win_base = base;
         const int q = base + lane;
-        const int tq = table_page(w, q);
+        const int tq = table_page<kWin>(w, q);
         win_pid = (q < npages_req && tq < p.max_blocks) ? checked_page(p, w.b, tq) : -1;
       }
       return __shfl_sync(0xffffffffu, win_pid, pg & 31);
@@ -672,19 +672,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_remote_arrive_relaxed(peer_xempty);
         }
         const int nvis = min(kT, tlim - tok0) - kHalfT * hf;  // tokens of this half the row can see
-        if (__builtin_expect(nvis < kHalfT || tok0 <= window_low(p, w.L - 1), 0)) {
-          const int low = window_low(p, p.causal ? w.L - p.q_len + row_q : w.L - 1) - tok0 - kHalfT * hf;
+        if (__builtin_expect(nvis < kHalfT || tok0 <= window_low<kWin>(p, w.L - 1), 0)) {
+          const int low = window_low<kWin>(p, p.causal ? w.L - p.q_len + row_q : w.L - 1) - tok0 - kHalfT * hf;
           const int sink = p.sinks - tok0 - kHalfT * hf;
 #pragma unroll
           for (int t = 0; t < kHalfT; ++t)
-            x[t] = (t < nvis && (t > low || t < sink)) ? x[t] * scale_log2 : -INFINITY;
+            x[t] = (t < nvis && (!kWin || t > low || t < sink)) ? x[t] * scale_log2 : -INFINITY;
         } else {
 #pragma unroll
           for (int t = 0; t < kHalfT; ++t) x[t] *= scale_log2;
         }
 #pragma unroll
         for (int t = 0; t < kHalfT; ++t) mx = fmaxf(mx, x[t]);
-        if (p.window > 0 && (tok0 <= window_low(p, w.L - 1) || p.causal))
+        if (kWin && (tok0 <= window_low<kWin>(p, w.L - 1) || p.causal))
           clear_hidden<BF16>(p, w, smem + kOffTile + (i % kSlots) * kTileSlot, tok0, min(kT, w.sub1 - tok0), tid, kSoftmaxThreads);
       }
       sm->half_val[hf][r] = mx;
@@ -781,14 +781,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool BF16, bool X16, bool FP8>
-cudaError_t prepare_mh() {
+template <bool BF16, bool X16, bool FP8, bool kWin>
+cudaError_t launch_mh(const cudaLaunchConfig_t& cfg, const CUtensorMap& tm_pages, const CUtensorMap& tm_kpe_half,
+                      const PartialParams& p) {
   static bool done = false;
-  if (done) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_partial_mh_kernel<BF16, X16, FP8>),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e == cudaSuccess) done = true;
-  return e;
+  if (!done) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_partial_mh_kernel<BF16, X16, FP8, kWin>),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    done = true;
+  }
+  return cudaLaunchKernelEx(&cfg, mla_partial_mh_kernel<BF16, X16, FP8, kWin>, tm_pages, tm_kpe_half, p);
+}
+template <bool X16, bool kWin>
+cudaError_t launch_mh_dtype(const cudaLaunchConfig_t& cfg, const CUtensorMap& tm_pages, const CUtensorMap& tm_kpe_half,
+                            const PartialParams& p, bool bf16) {
+  if (p.fp8) return launch_mh<false, X16, true, kWin>(cfg, tm_pages, tm_kpe_half, p);
+  return bf16 ? launch_mh<true, X16, false, kWin>(cfg, tm_pages, tm_kpe_half, p)
+              : launch_mh<false, X16, false, kWin>(cfg, tm_pages, tm_kpe_half, p);
 }
 
 }  // namespace
@@ -801,10 +812,6 @@ cudaError_t launch_partial_mh(const CUtensorMap& tm_pages, const CUtensorMap& tm
                               int num_chunks, bool bf16, cudaStream_t stream) {
   const bool x16 = p.xchg16 != 0;
   if (p.fp8 && bf16) return cudaErrorInvalidValue;  // E4M3 caches go with fp16 queries
-  cudaError_t e = p.fp8 ? (x16 ? prepare_mh<false, true, true>() : prepare_mh<false, false, true>())
-                  : bf16 ? (x16 ? prepare_mh<true, true, false>() : prepare_mh<true, false, false>())
-                         : (x16 ? prepare_mh<false, true, false>() : prepare_mh<false, false, false>());
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * ((p.q_len * p.H + kRows - 1) / kRows), num_chunks, 1);  // one CTA pair per 128-row group
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -819,14 +826,11 @@ cudaError_t launch_partial_mh(const CUtensorMap& tm_pages, const CUtensorMap& tm
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.fp8)
-    return x16 ? cudaLaunchKernelEx(&cfg, mla_partial_mh_kernel<false, true, true>, tm_pages, tm_kpe_half, p)
-               : cudaLaunchKernelEx(&cfg, mla_partial_mh_kernel<false, false, true>, tm_pages, tm_kpe_half, p);
-  if (bf16)
-    return x16 ? cudaLaunchKernelEx(&cfg, mla_partial_mh_kernel<true, true, false>, tm_pages, tm_kpe_half, p)
-               : cudaLaunchKernelEx(&cfg, mla_partial_mh_kernel<true, false, false>, tm_pages, tm_kpe_half, p);
-  return x16 ? cudaLaunchKernelEx(&cfg, mla_partial_mh_kernel<false, true, false>, tm_pages, tm_kpe_half, p)
-             : cudaLaunchKernelEx(&cfg, mla_partial_mh_kernel<false, false, false>, tm_pages, tm_kpe_half, p);
+  if (p.window > 0)
+    return x16 ? launch_mh_dtype<true, true>(cfg, tm_pages, tm_kpe_half, p, bf16)
+               : launch_mh_dtype<false, true>(cfg, tm_pages, tm_kpe_half, p, bf16);
+  return x16 ? launch_mh_dtype<true, false>(cfg, tm_pages, tm_kpe_half, p, bf16)
+             : launch_mh_dtype<false, false>(cfg, tm_pages, tm_kpe_half, p, bf16);
 }
 
 cudaError_t mh_read_clear_error(uint32_t* out) {

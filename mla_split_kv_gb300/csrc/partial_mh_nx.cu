@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 __device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
-template <bool BF16>
+template <bool BF16, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_partial_mh_nx_kernel(const __grid_constant__ CUtensorMap tm_pages,
                              const __grid_constant__ CUtensorMap tm_kpe_half, const PartialParams p) {
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
   // both CTAs of the pair take the whole chunk; pair g = blockIdx.x / 2 takes query rows [128 g, 128 g + 128)
-  const CtaWork w = cta_work(p, kRows, kT, 0, 1, -1, static_cast<int32_t>(blockIdx.x >> 1));
+  const CtaWork w = cta_work<kWin>(p, kRows, kT, 0, 1, -1, static_cast<int32_t>(blockIdx.x >> 1));
   const int ntiles = (w.sub1 - w.sub0 + kT - 1) / kT;
 
   if (warp > kMmaWarp) {
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (base != win_base) {
         win_base = base;
         const int q = base + lane;
-        const int tq = table_page(w, q);
+        const int tq = table_page<kWin>(w, q);
         win_pid = (q < npages_req && tq < p.max_blocks) ? checked_page(p, w.b, tq) : -1;
       }
       return __shfl_sync(0xffffffffu, win_pid, pg & 31);
@@ -432,19 +432,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(sa + 16, x + 16);
         tmem_wait_ld();
         const int nvis = min(kT, tlim - (w.sub0 + i * kT)) - kHalfT * hf;  // tokens of this half the row sees
-        if (__builtin_expect(nvis < kHalfT || (w.sub0 + i * kT) <= window_low(p, w.L - 1), 0)) {
-          const int low = window_low(p, p.causal ? w.L - p.q_len + row_q : w.L - 1) - (w.sub0 + i * kT) - kHalfT * hf;
+        if (__builtin_expect(nvis < kHalfT || (w.sub0 + i * kT) <= window_low<kWin>(p, w.L - 1), 0)) {
+          const int low = window_low<kWin>(p, p.causal ? w.L - p.q_len + row_q : w.L - 1) - (w.sub0 + i * kT) - kHalfT * hf;
           const int sink = p.sinks - (w.sub0 + i * kT) - kHalfT * hf;
 #pragma unroll
           for (int t = 0; t < kHalfT; ++t)
-            x[t] = (t < nvis && (t > low || t < sink)) ? x[t] * scale_log2 : -INFINITY;
+            x[t] = (t < nvis && (!kWin || t > low || t < sink)) ? x[t] * scale_log2 : -INFINITY;
         } else {
 #pragma unroll
           for (int t = 0; t < kHalfT; ++t) x[t] *= scale_log2;
         }
 #pragma unroll
         for (int t = 0; t < kHalfT; ++t) mx = fmaxf(mx, x[t]);
-        if (p.window > 0 && ((w.sub0 + i * kT) <= window_low(p, w.L - 1) || p.causal))
+        if (kWin && ((w.sub0 + i * kT) <= window_low<kWin>(p, w.L - 1) || p.causal))
           clear_hidden<BF16>(p, w, smem + kOffTile + (i % kSlots) * kTileSlot + half * kCkvBytes, (w.sub0 + i * kT), min(kT, w.sub1 - (w.sub0 + i * kT)), tid, kSoftmaxThreads);
       }
       sm->half_val[hf][r] = mx;
@@ -549,14 +549,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool BF16>
-cudaError_t prepare_nx() {
+template <bool BF16, bool kWin>
+cudaError_t launch_nx(const cudaLaunchConfig_t& cfg, const CUtensorMap& tm_pages, const CUtensorMap& tm_kpe_half,
+                      const PartialParams& p) {
   static bool done = false;
-  if (done) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_partial_mh_nx_kernel<BF16>),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e == cudaSuccess) done = true;
-  return e;
+  if (!done) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_partial_mh_nx_kernel<BF16, kWin>),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    done = true;
+  }
+  return cudaLaunchKernelEx(&cfg, mla_partial_mh_nx_kernel<BF16, kWin>, tm_pages, tm_kpe_half, p);
 }
 
 }  // namespace
@@ -564,8 +567,6 @@ cudaError_t prepare_nx() {
 cudaError_t launch_partial_mh_nx(const CUtensorMap& tm_pages, const CUtensorMap& tm_kpe_half, const PartialParams& p,
                                  int num_chunks, bool bf16, cudaStream_t stream) {
   if (p.fp8) return cudaErrorInvalidValue;  // 16-bit caches only
-  const cudaError_t e = bf16 ? prepare_nx<true>() : prepare_nx<false>();
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * ((p.q_len * p.H + kRows - 1) / kRows), num_chunks, 1);  // one CTA pair per 128-row group
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -578,8 +579,9 @@ cudaError_t launch_partial_mh_nx(const CUtensorMap& tm_pages, const CUtensorMap&
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return bf16 ? cudaLaunchKernelEx(&cfg, mla_partial_mh_nx_kernel<true>, tm_pages, tm_kpe_half, p)
-              : cudaLaunchKernelEx(&cfg, mla_partial_mh_nx_kernel<false>, tm_pages, tm_kpe_half, p);
+  if (p.window > 0)
+    return bf16 ? launch_nx<true, true>(cfg, tm_pages, tm_kpe_half, p) : launch_nx<false, true>(cfg, tm_pages, tm_kpe_half, p);
+  return bf16 ? launch_nx<true, false>(cfg, tm_pages, tm_kpe_half, p) : launch_nx<false, false>(cfg, tm_pages, tm_kpe_half, p);
 }
 
 cudaError_t mh_nx_read_clear_error(uint32_t* out) {

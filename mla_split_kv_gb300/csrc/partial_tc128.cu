@@ -125,8 +125,9 @@ static_assert(sizeof(Small) <= kSmallBytes, "small smem region");
 __device__ __forceinline__ uint32_t tmem_lane_base(int warp) { return static_cast<uint32_t>(32 * (warp & 3)) << 16; }
 
 // kFp8: E4M3 caches (byte loads, widened in the slot, cache scale on the output); kBf16: bf16 queries and
-// caches (the probabilities carried as two bf16 terms, two PV products a step); one instance each
-template <bool kFp8, bool kBf16>
+// caches (the probabilities carried as two bf16 terms, two PV products a step); kWin: windowed calls; one
+// instance each
+template <bool kFp8, bool kBf16, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_partial_tc128_kernel(const __grid_constant__ CUtensorMap tm_pages, const __grid_constant__ CUtensorMap tm_kpe_half,
                              const PartialParams p) {
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     win_base = pg & ~31;
     const int q = win_base + lane;
     const int npages_req = (w.L + p.bs - 1) / p.bs;
-    const int tq = table_page(w, q);
+    const int tq = table_page<kWin>(w, q);
     win_pid = (q < npages_req && tq < p.max_blocks) ? checked_page(p, w.b, tq) : -1;
   };
   // producers: warp kMmaWarp + 1 + k0 loads pages k0, k0 + kPageWarps, ... of each tile
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   int issued = -1;  // producers: the last tile whose loads this warp issued
   if (p.tables_ready) {
-    w = cta_work(p, kNR, kT, pair_index, subs * cluster_pairs, chunk);
+    w = cta_work<kWin>(p, kNR, kT, pair_index, subs * cluster_pairs, chunk);
     if (warp > kMmaWarp && w.sub1 > w.sub0) load_window(w.sub0 / p.bs);
   }
   // the tensor-map descriptors are kernel parameters, not data of the preceding kernel: fetch them
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();  // the merge of these partials may be scheduled now; it waits for this grid
-  if (!p.tables_ready) w = cta_work(p, kNR, kT, pair_index, subs * cluster_pairs, chunk);
+  if (!p.tables_ready) w = cta_work<kWin>(p, kNR, kT, pair_index, subs * cluster_pairs, chunk);
   const int ntiles = (w.sub1 - w.sub0 + kT - 1) / kT;
   // single-launch decode: request b's chunk slots, whose partials this launch also merges
   const bool fused = p.out != nullptr;  // the TICKETS way of mla_decode
@@ -675,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* region = smem + kOffTile + s * kTileSlot + kCkvBytes;  // the peer's partial S, then P^T
       const int tok0 = w.sub0 + i * kT;
       const int nvalid = min(kT, w.sub1 - tok0);
-      const bool masked_tile = (nvalid < kT) || (tok0 + kT - 1 > causal_floor) || (w.nrows < kNR) || (tok0 <= window_low(p, w.L - 1));
+      const bool masked_tile = (nvalid < kT) || (tok0 + kT - 1 > causal_floor) || (w.nrows < kNR) || (tok0 <= window_low<kWin>(p, w.L - 1));
       int ok = sent ? mbar_wait_cluster(&sm->xfull[s], (i / kSlots) & 1, tmo) : 0;
       ok = __all_sync(0xffffffffu, ok);
       bool need_local = false;
@@ -697,10 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = kRH * h + k;
             bool vis = (tl < nvalid) && (r < w.nrows);
             if (p.causal) vis = vis && (t <= w.L - p.q_len + (w.row0 + r) / p.H);
-            vis = vis && !window_hides(p, t, p.causal ? w.L - p.q_len + (w.row0 + r) / p.H : w.L - 1);
+            vis = vis && !window_hides<kWin>(p, t, p.causal ? w.L - p.q_len + (w.row0 + r) / p.H : w.L - 1);
             x[k] = vis ? x[k] * scale_log2 : -INFINITY;
           }
-          if (p.window > 0) clear_hidden<kBf16>(p, w, smem + kOffTile + s * kTileSlot, tok0, nvalid, tid, kSoftmaxThreads);
+          if constexpr (kWin)
+            clear_hidden<kBf16>(p, w, smem + kOffTile + s * kTileSlot, tok0, nvalid, tid, kSoftmaxThreads);
         } else {
 #pragma unroll
           for (int k = 0; k < kRH; ++k) x[k] *= scale_log2;
@@ -1101,10 +1103,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kFp8, bool kBf16>
+template <bool kFp8, bool kBf16, bool kWin>
 cudaError_t prepare(int cluster) {
   static bool smem_set = false, np_set = false;
-  const void* fn = reinterpret_cast<const void*>(&mla_partial_tc128_kernel<kFp8, kBf16>);
+  const void* fn = reinterpret_cast<const void*>(&mla_partial_tc128_kernel<kFp8, kBf16, kWin>);
   cudaError_t e = cudaSuccess;
   if (!smem_set) {
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -1119,6 +1121,17 @@ cudaError_t prepare(int cluster) {
   return e;
 }
 
+template <bool kWin>
+cudaError_t launch_tc128(cudaLaunchConfig_t cfg, const CUtensorMap& tm_pages, const CUtensorMap& tm_kpe_half,
+                         const PartialParams& p, int cluster, bool bf16) {
+  const cudaError_t e = p.fp8 ? prepare<true, false, kWin>(cluster)
+                        : bf16 ? prepare<false, true, kWin>(cluster) : prepare<false, false, kWin>(cluster);
+  if (e != cudaSuccess) return e;
+  if (p.fp8) return cudaLaunchKernelEx(&cfg, mla_partial_tc128_kernel<true, false, kWin>, tm_pages, tm_kpe_half, p);
+  return bf16 ? cudaLaunchKernelEx(&cfg, mla_partial_tc128_kernel<false, true, kWin>, tm_pages, tm_kpe_half, p)
+              : cudaLaunchKernelEx(&cfg, mla_partial_tc128_kernel<false, false, kWin>, tm_pages, tm_kpe_half, p);
+}
+
 }  // namespace
 
 bool tc128_supports(int total_rows, bool, int cluster) {
@@ -1128,9 +1141,6 @@ bool tc128_supports(int total_rows, bool, int cluster) {
 cudaError_t launch_partial_tc128(const CUtensorMap& tm_pages, const CUtensorMap& tm_kpe_half, const PartialParams& p,
                                  int num_chunks, int cluster, bool bf16, cudaStream_t stream) {
   if (p.fp8 && bf16) return cudaErrorInvalidValue;  // E4M3 caches go with fp16 queries
-  cudaError_t e = p.fp8 ? prepare<true, false>(cluster)
-                  : bf16 ? prepare<false, true>(cluster) : prepare<false, false>(cluster);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster, num_chunks * (p.subs > 1 ? p.subs : 1), 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -1145,14 +1155,13 @@ cudaError_t launch_partial_tc128(const CUtensorMap& tm_pages, const CUtensorMap&
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (p.fp8) return cudaLaunchKernelEx(&cfg, mla_partial_tc128_kernel<true, false>, tm_pages, tm_kpe_half, p);
-  return bf16 ? cudaLaunchKernelEx(&cfg, mla_partial_tc128_kernel<false, true>, tm_pages, tm_kpe_half, p)
-              : cudaLaunchKernelEx(&cfg, mla_partial_tc128_kernel<false, false>, tm_pages, tm_kpe_half, p);
+  return p.window > 0 ? launch_tc128<true>(cfg, tm_pages, tm_kpe_half, p, cluster, bf16)
+                      : launch_tc128<false>(cfg, tm_pages, tm_kpe_half, p, cluster, bf16);
 }
 
 int tc128_max_active_clusters(int cluster) {
   // every instance takes the same threads, shared memory and (at most) registers
-  if (prepare<false, false>(cluster) != cudaSuccess) {
+  if (prepare<false, false, false>(cluster) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -1168,7 +1177,7 @@ int tc128_max_active_clusters(int cluster) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(&mla_partial_tc128_kernel<false, false>), &cfg) !=
+  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(&mla_partial_tc128_kernel<false, false, false>), &cfg) !=
       cudaSuccess) {
     cudaGetLastError();
     return 0;
