@@ -45,7 +45,8 @@ struct MapKey {
   int dtype;
   int device;
   int kind;  // 0: the 2D map; 1: the page map of the ckv cache (see page_map); 2: the kpe half map;
-             // 3 / 4: the ckv / kpe half maps of an E4M3 cache (bytes, no swizzle)
+             // 3 / 4: the ckv / kpe half maps of an E4M3 cache (bytes, no swizzle);
+             // 5 / 6: the ckv / kpe page maps of a block-scaled E4M3 cache (bytes, swizzled)
 };
 struct MapEntry {
   MapKey key;
@@ -88,6 +89,14 @@ bool fp8_half_map(CUtensorMap* out, const void* base, uint64_t rows, uint64_t co
   return encode_map(out, MapKey{base, rows, cols, box_rows, MLA_E4M3, dev, kind});
 }
 
+// Block-scaled caches: a page of the [rows, 512] byte cache as (128 columns, 8 rows, 4 column blocks, row
+// groups) -- page_map's layout in bytes -- and of the [rows, 64] one.
+bool q8_map(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, int kind) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  return encode_map(out, MapKey{base, rows, cols, box_rows, MLA_E4M3, dev, kind});
+}
+
 bool kpe_half_map(CUtensorMap* out, const void* base, uint64_t rows, uint32_t box_rows, int dtype) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
@@ -117,6 +126,22 @@ bool encode_map(CUtensorMap* out, const MapKey& key) {
     cuuint32_t estr[2] = {1, 1};
     r = enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(key.base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else if (key.kind == 5) {
+    cuuint64_t dims[4] = {128, 8, key.cols / 128, key.rows / 8};
+    cuuint64_t strides[3] = {key.cols, 128, key.cols * 8};
+    cuuint32_t box[4] = {128, 8, static_cast<cuuint32_t>(key.cols / 128), key.box_rows / 8};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    r = enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(key.base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else if (key.kind == 6) {
+    cuuint64_t dims[2] = {key.cols, key.rows};
+    cuuint64_t strides[1] = {key.cols};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(key.cols), key.box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    r = enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(key.base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   } else if (key.kind == 0) {
     cuuint64_t dims[2] = {key.cols, key.rows};
@@ -941,7 +966,12 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
   p.ws_o = static_cast<float*>(d->workspace);
   p.ws_ml = p.ws_o + static_cast<uint64_t>(p.gangs) * 2 * p.row_pad * mla::kRank;
   p.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
-  if (mla::launch_decode_q8(p, d->dtype == MLA_BF16, static_cast<cudaStream_t>(d->stream)) != cudaSuccess) {
+  CUtensorMap tm_ckv, tm_kpe;
+  const uint64_t cache_rows = static_cast<uint64_t>(d->num_blocks) * static_cast<uint64_t>(d->block_size);
+  if (!q8_map(&tm_ckv, ckv_cache, cache_rows, mla::kRank, d->block_size, 5) ||
+      !q8_map(&tm_kpe, kpe_cache, cache_rows, mla::kRope, d->block_size, 6))
+    return reject(MLA_ERR_CUDA);
+  if (mla::launch_decode_q8(tm_ckv, tm_kpe, p, d->dtype == MLA_BF16, static_cast<cudaStream_t>(d->stream)) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;
   }

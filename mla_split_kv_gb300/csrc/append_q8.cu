@@ -32,23 +32,6 @@ __device__ __forceinline__ float block_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
-// two values to two E4M3 bytes (a in the low one), round to nearest even, +-448 beyond
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
-}
-
-// the larger of two magnitudes, NaN if either is
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4 v, float* x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -4,43 +4,195 @@
 //   s_t = scale * z_t * (q_abs . c_t + q_pe . k_t)
 //   out = sum_t softmax(s)_t * z_t * c_t,   lse = log2 sum_t exp(s_t)
 // with c_t, k_t the E4M3 values of the token's bytes and z_t its block's scale.
+//
+// The tensor core takes the bytes as they are (kind::f8f6f4, E4M3 x E4M3 with
+// fp32 sums): nothing is widened, and a 128-token tile of the whole latent is
+// 72 KB, so one CTA holds it for both products and no CTA waits on another.
+// What is not 8-bit is split into E4M3 terms, each the rounding of what the
+// terms before it leave: x = t1 + 2^-5 t2 + 2^-10 t3. A term keeps 4
+// significant bits and leaves at most 2^-4 of its value, so three terms hold
+// an fp16 query exactly (11 bits) and two a bf16 one (8 bits), as long as its
+// magnitude is above 2^-14 of the row's largest (the row is first scaled by a
+// power of two to [128, 256)), and below that to 2^-23 of the largest; the
+// weights of the value product, three terms, to 2^-12 of themselves or 2^-25
+// of the largest. The terms are further columns of the MMA's N side:
+//   S^T[tok, (term, row)]  = [c | k][tok, :] . Qterms^T    M=128 tokens, K=576
+//   O^T[d, (term, row)]   += c^T[d, tok] . Wterms^T        M=128 columns x 4, K=128
+// At 16 rows an MMA's time is that of reading the 4 KB A operand from shared
+// memory, which the terms share.
+//
+// A token's scale goes with its weight: with y_t = s_t log2 e + log2 z_t the
+// weights are w_t = 2^(y_t - m), m a running maximum of y, so they stay in
+// range whatever the scales; out = sum w_t c_t / sum (w_t / z_t), and the LSE
+// is m + log2 of that same sum.
+//
+// NR rows a CTA: 16, or 32 for calls with more (a group of CTAs, a gang, then
+// shares each tile through L2). O^T is 4 x 3 NR columns of tensor memory, all
+// of it but the scores' at 32. Two tile slots of 72 KB: the MMAs of a tile take
+// a third of the time that HBM takes to bring one, and pages further ahead are
+// on their way to L2.
+//
+// Warp roles (384 threads): warps 0-7 softmax, rescale and output (thread =
+// token; the two warps of a TMEM lane quadrant take half of the rows each),
+// warp 8 MMA issue, warp 9 page loads, warps 10-11 split the queries of the
+// next request while this one's tiles run.
 #include "q8_schedule.cuh"
 
 namespace mla {
 
 namespace {
 
-constexpr int kNR = 16;       // query rows per CTA
-constexpr int kThreads = 256;
-constexpr int kStep = 16;     // tokens taken at a time
-constexpr int kPad = kQkDim + 1;
+constexpr int kT = kQ8Tile;                       // tokens per tile
+constexpr int kGroupBytes = 8 * kRank;            // 4 KB: 8 tokens, four swizzled [8 x 128] atoms
+constexpr int kCkvBytes = kT * kRank;             // 64 KB
+constexpr int kTileSlot = kCkvBytes + kT * kRope; // 72 KB
+constexpr int kSlots = 2;
+constexpr int kTerms = 3;                         // of a weight
+constexpr int kPre = 2;                           // tiles ahead that are prefetched to L2
+constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = kSoftmaxWarps * 32;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kQueryWarp = 10, kQueryWarps = 2;
+constexpr int kThreads = (kQueryWarp + kQueryWarps) * 32;  // 384
+constexpr float kTermStep = 32.0f, kTermInv = 1.0f / 32.0f;
+// The reference maximum moves when a score passes it by more than this, so weights are at most 2^kTau; times
+// 2^kWeightExp they fit E4M3's 448, and its subnormals reach down to 2^-25 of the reference in the third term.
+constexpr float kTau = 2.0f;
+constexpr int kWeightExp = 6;
+constexpr int kQueryRows = 4;                     // rows a query warp has in flight
+constexpr int kSums = 4;                          // row factors kept: queries split ahead of their softmax
 
-struct Smem {
-  float q[kNR][kPad];
-  float kv[kStep][kPad];
-  float prob[kNR][kStep];
-  float alpha[kNR], m[kNR], l[kNR];
+template <int NR, bool BF16>
+struct Cfg {
+  static constexpr int kQTerms = BF16 ? 2 : 3;
+  static constexpr int kNS = NR * kQTerms, kNP = NR * kTerms;      // N of the two products
+  static constexpr int kSBufs = (4 * kNP + 2 * kNS <= 512) ? 2 : 1;  // score buffers in tensor memory
+  static constexpr int kQBufs = NR == 16 ? 2 : 1;
+  static constexpr uint32_t kQChunk = kNS * 128;                   // [kNS x 128 columns], swizzled
+  static constexpr uint32_t kQBytes = kNS * kQkDim;                // four chunks, then [kNS x 64] (64-byte swizzle)
+  static constexpr uint32_t kPBytes = kNP * kT;                    // [kNP x 128 tokens], swizzled
+  static constexpr uint32_t kOffQ = kSlots * kTileSlot;
+  static constexpr uint32_t kOffP = kOffQ + kQBufs * kQBytes;
+  static constexpr uint32_t kOffSmall = kOffP + 2 * kPBytes;
+  static constexpr uint32_t kSmem = kOffSmall + 3072;
+  static constexpr uint32_t kTmemO = 0, kTmemS = 4 * kNP;
+  static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kQChunk % 1024 == 0, "swizzle atoms stay aligned");
+  static_assert(kTmemS + kSBufs * kNS <= 512, "tensor memory");
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+
+struct Small {
+  uint64_t full[kSlots], empty[kSlots];  // tile slots
+  uint64_t sfull[2], sfree[2];           // score buffers
+  uint64_t pfull[2], pvdone[2];          // weight buffers
+  uint64_t qfull[2], qfree[2];           // query buffers
+  uint64_t ofree, drain;
   int64_t scratch[33];
   int64_t off0;
   int b0;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+  float factor[kSums][32];               // per row: score scale over the query's power of two, log2 units
+  float red[4][32], mref[32], alpha[32];
 };
+static_assert(sizeof(Small) <= 3072, "small smem region");
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 1) mla_decode_q8_kernel(const DecodeQ8Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-  const int tid = threadIdx.x;
-  const int group = blockIdx.x, gang = blockIdx.y;
+// x = t1 + t2 / 32 + t3 / 1024 for the two values of a pair, each term two E4M3 bytes
+template <int N>
+__device__ __forceinline__ void split_terms(float a, float b, uint32_t* t) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    t[i] = e4m3x2(a, b);
+    if (i + 1 < N) {
+      const float2 v = e4m3x2_values(t[i]);
+      a = (a - v.x) * kTermStep;
+      b = (b - v.y) * kTermStep;
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t a, float* v) {
+  static_assert(N == 8 || N == 16, "");
+  if constexpr (N == 8)
+    tmem_ld8(a, v);
+  else
+    tmem_ld16(a, v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t a, const float* v) {
+  if constexpr (N == 8)
+    tmem_st8(a, v);
+  else
+    tmem_st16(a, v);
+}
+
+// NaN bytes of tokens [t0, t1) of a tile to zero: tokens that some row does not see. Its weight for them is 0,
+// and every other byte is finite; for a row that does see one, the score has already made the weight NaN.
+__device__ __forceinline__ void clear_nan_bytes(uint8_t* ckv, int t0, int t1, int tid) {
+  for (int x = tid; x < (t1 - t0) * 32; x += kSoftmaxThreads) {
+    const int t = t0 + (x >> 5);
+    uint4* const at = reinterpret_cast<uint4*>(ckv + (t >> 3) * kGroupBytes + ((x >> 3) & 3) * 1024 + (t & 7) * 128 + (x & 7) * 16);
+    uint4 v = *at;
+    uint32_t* const w = &v.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t nan = (((w[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in each NaN byte
+      w[j] &= ~(nan * 255u);
+    }
+    *at = v;
+  }
+}
+
+template <int NR, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_ckv, const __grid_constant__ CUtensorMap tm_kpe,
+                         const DecodeQ8Params p) {
+  using C = Cfg<NR, BF16>;
+  constexpr int RH = NR / 2;  // rows per softmax thread
+  extern __shared__ uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need it; the size leaves no slack to align it
+    if (threadIdx.x == 0) flag_error(MLA_DEVERR_CONFIG);
+    return;
+  }
+  Small* sm = reinterpret_cast<Small*>(smem + C::kOffSmall);
+  volatile int32_t* abort_flag = &sm->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gang = blockIdx.y;
   const int rows_total = p.q_len * p.H;
-  const int row0 = group * kNR, nrows = min(kNR, rows_total - row0);
+  const int row0 = blockIdx.x * NR, nrows = min(NR, rows_total - row0);
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm->full[s], 1);
+      mbar_init(&sm->empty[s], 1);
+      mbar_init(&sm->sfull[s], 1);
+      mbar_init(&sm->sfree[s], kSoftmaxWarps);
+      mbar_init(&sm->pfull[s], kSoftmaxWarps);
+      mbar_init(&sm->pvdone[s], 1);
+      mbar_init(&sm->qfull[s], kQueryWarps);
+      mbar_init(&sm->qfree[s], 1);
+    }
+    mbar_init(&sm->ofree, kSoftmaxWarps);
+    mbar_init(&sm->drain, 1);
+    sm->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sm->tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&tm_ckv);
+    tma_prefetch_desc(&tm_kpe);
+  }
   pdl_wait();
   pdl_launch_dependents();
+
   // this gang's place on the line of tiles
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
   int64_t mine = 0, T = 0;
   for (int b = b_lo; b < b_hi; ++b) mine += q8_tiles(p, b);
-  const int64_t prefix = block_prefix<kThreads>(mine, sm.scratch, &T);
+  const int64_t prefix = block_prefix<kThreads>(mine, sm->scratch, &T);
   const int64_t J = q8_live_gangs(T, p.gangs);
   const bool work = gang < J;
   const int64_t lo = work ? q8_gang_begin(gang, T, J) : 0, hi = work ? q8_gang_begin(gang + 1, T, J) : 0;
@@ -53,133 +205,525 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_q8_kernel(const Decode
       at += n;
       ++b;
     }
-    sm.b0 = b;
-    sm.off0 = lo - at;
+    sm->b0 = b;
+    sm->off0 = lo - at;
   }
   // requests with nothing to see
   for (int b = gang; b < p.B; b += p.gangs) {
     if (q8_tiles(p, b) != 0) continue;
-    for (int r = 0; r < nrows; ++r) {
-      const long long at = static_cast<long long>(b) * rows_total + row0 + r;
-      if (tid < kRank / 4) store_out4(p.out, p.out_dtype, at * kRank + 4 * tid, make_float4(0.f, 0.f, 0.f, 0.f));
-      if (tid == 0 && p.out_lse != nullptr) p.out_lse[at] = -INFINITY;
+    for (int x = tid; x < nrows * (kRank / 4); x += kThreads) {
+      const long long at = static_cast<long long>(b) * rows_total + row0 + x / (kRank / 4);
+      store_out4(p.out, p.out_dtype, at * kRank + 4 * (x % (kRank / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
+      if (x % (kRank / 4) == 0 && p.out_lse != nullptr) p.out_lse[at] = -INFINITY;
     }
   }
+  tc_fence_before();
   __syncthreads();
-  if (!work) return;
-  int b = sm.b0;
-  int64_t ta = sm.off0;
-  for (int64_t left = hi - lo; left > 0; ++b, ta = 0) {
-    const int64_t n_tiles = q8_tiles(p, b);
-    const int64_t tb = min(n_tiles, ta + left);
-    if (tb <= ta) continue;
-    left -= tb - ta;
-    const WindowView v = window_view(__ldcg(p.context_lens + b), p.q_len, p.bs, p.causal, p.window, p.sinks);
-    const int u0 = static_cast<int>(ta * kQ8Tile);
-    const int u1 = tb == n_tiles ? v.n : static_cast<int>(tb * kQ8Tile);
-    for (int x = tid; x < kNR * kQkDim; x += kThreads) {
-      const int r = x / kQkDim, c = x % kQkDim;
-      const long long at = static_cast<long long>(b) * rows_total + row0 + r;
-      sm.q[r][c] = r >= nrows ? 0.f
-                              : h2f<BF16>(c < kRank ? p.q_abs[at * kRank + c] : p.q_pe[at * kRope + c - kRank]);
-    }
-    if (tid < kNR) {
-      sm.m[tid] = -INFINITY;
-      sm.l[tid] = 0.f;
-    }
-    float acc[kNR][2] = {};
-    const int r = tid / kStep, tl = tid % kStep;
-    const long long row_pos = p.causal ? static_cast<long long>(v.n) - p.q_len + (row0 + r) / p.H : v.n - 1LL;
-    for (int u = u0; u < u1; u += kStep) {
-      __syncthreads();
-      for (int x = tid; x < kStep * (kQkDim / 4); x += kThreads) {
-        const int t = x / (kQkDim / 4), c = (x % (kQkDim / 4)) * 4;
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
-        if (u + t < u1) {
-          const int tok = u + t + (u + t >= v.sa ? v.skip : 0);
-          const int pg = tok / p.bs;
-          const int pid = pg < p.max_blocks ? p.block_table[static_cast<long long>(b) * p.max_blocks + pg] : -1;
-          if (pid < 0 || pid >= p.num_blocks) {
-            flag_error(MLA_DEVERR_BAD_PAGE);
-          } else {
-            const long long row = static_cast<long long>(pid) * p.bs + tok % p.bs;
-            const uint32_t w = c < kRank ? *reinterpret_cast<const uint32_t*>(p.ckv + row * kRank + c)
-                                         : *reinterpret_cast<const uint32_t*>(p.kpe + row * kRope + c - kRank);
-            const float z = p.scales[row >> p.g_shift];
-            uint32_t a, d;
-            e4m3x4_to_f16x4(w, a, d);
-            const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
-            const float2 fd = __half22float2(*reinterpret_cast<const __half2*>(&d));
-            f[0] = fa.x * z;
-            f[1] = fa.y * z;
-            f[2] = fd.x * z;
-            f[3] = fd.y * z;
-          }
-        }
-        for (int j = 0; j < 4; ++j) sm.kv[t][c + j] = f[j];
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem_base;
+  const int N = static_cast<int>(hi - lo);  // this gang's tiles
+  Q8Walk w = q8_walk(work ? sm->b0 : 0, work ? sm->off0 : 0, N);
+  uint64_t tmo = p.timeout_ns;
+  asm volatile("" : "+l"(tmo));
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------------ page loads
+    const uint64_t pol = l2_policy_evict_first();
+    // the page that this lane loads of a tile (one lane a page): -1 for one outside the pool or the table row
+    // (it reads zeros), -2 for none
+    auto page_of = [&](const Q8Walk& w, int tile) -> int {
+      const int pages = (min(kT, w.v.n - tile * kT) + p.bs - 1) / p.bs;
+      if (lane >= pages) return -2;
+      int pg = tile * (kT / p.bs) + lane;
+      if (pg >= w.v.sa / p.bs) pg += w.v.skip / p.bs;
+      const int pid = pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
+      return (pid >= 0 && pid < p.num_blocks) ? pid : -1;
+    };
+    // a walk that runs ahead: its page numbers wait in registers until their tile's prefetch and load
+    Q8Walk a = w;
+    bool a_live = q8_next(p, a, true);
+    int a_tile = a.ta;
+    auto ahead = [&]() -> int {
+      if (!a_live) return -2;
+      const int pid = page_of(a, a_tile);
+      if (++a_tile == a.tb) {
+        a_live = q8_next(p, a, false);
+        a_tile = a.ta;
       }
-      __syncthreads();
-      float s = 0.f;
-      for (int c = 0; c < kQkDim; ++c) s = fmaf(sm.q[r][c], sm.kv[tl][c], s);
-      const int ut = u + tl;
-      bool vis = ut < u1 && r < nrows && ut <= row_pos;
-      if (p.window > 0) vis = vis && (ut > row_pos - p.window || ut < p.sinks);
-      s = vis ? s * p.scale_log2 : -INFINITY;
-      float mx = s;
-      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float m_old = sm.m[r], m_new = fmaxf(m_old, mx);
-      const float ref = m_new == -INFINITY ? 0.f : m_new;
-      const float pr = vis ? exp2f(s - ref) : 0.f;
-      float sum = pr;
-      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      return pid;
+    };
+    int ring[kPre + 2];
+#pragma unroll
+    for (int j = 0; j < kPre + 2; ++j) ring[j] = ahead();
+    int issued = -1;
+    for (int i = 0; i < N; ++i) {
+      const int s = i & 1;
+      if (i >= kSlots) {
+        int ok = 1;
+        if (lane == 0) {
+          ok = mbar_wait(&sm->empty[s], ((i >> 1) - 1) & 1, tmo) && !*abort_flag;
+          if (!ok) *abort_flag = 1;
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      }
+      const int pid = ring[0];
+      if (pid == -1) flag_error(MLA_DEVERR_BAD_PAGE);
+      const int pages = __popc(__ballot_sync(0xffffffffu, pid != -2));
+      if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>(pages * p.bs * kQkDim));
       __syncwarp();
-      if (tl == 0) {
-        const float al = m_old == -INFINITY ? 0.f : exp2f(m_old - m_new);
-        sm.alpha[r] = al;
-        sm.m[r] = m_new;
-        sm.l[r] = sm.l[r] * al + sum;
+      if (pid != -2) {
+        uint8_t* slot = smem + s * kTileSlot;
+        tma_load_4d(slot + lane * p.bs * kRank, &tm_ckv, 0, 0, 0, pid * (p.bs / 8), &sm->full[s], pol);
+        tma_load_2d(slot + kCkvBytes + lane * p.bs * kRope, &tm_kpe, 0, pid * p.bs, &sm->full[s], pol);
       }
-      sm.prob[r][tl] = pr;
-      __syncthreads();
-      for (int rr = 0; rr < kNR; ++rr) {
-        const float al = sm.alpha[rr];
-        float a0 = acc[rr][0] * al, a1 = acc[rr][1] * al;
-        for (int t = 0; t < kStep; ++t) {
-          const float w = sm.prob[rr][t];
-          if (w != 0.f) {  // (a hidden token's row may hold anything)
-            a0 = fmaf(w, sm.kv[t][tid], a0);
-            a1 = fmaf(w, sm.kv[t][tid + kThreads], a1);
+      issued = i;
+      if (ring[kPre] >= 0) {
+        const long long row = static_cast<long long>(ring[kPre]) * p.bs;
+        bulk_prefetch_l2(p.ckv + row * kRank, static_cast<uint32_t>(p.bs * kRank));
+        bulk_prefetch_l2(p.kpe + row * kRope, static_cast<uint32_t>(p.bs * kRope));
+      }
+#pragma unroll
+      for (int j = 0; j <= kPre; ++j) ring[j] = ring[j + 1];
+      ring[kPre + 1] = ahead();
+    }
+    // after an abort, loads in flight land before shared memory is released
+    if (lane == 0 && *abort_flag)
+      for (int t = max(0, issued - (kSlots - 1)); t <= issued; ++t) mbar_wait(&sm->full[t & 1], (t >> 1) & 1, kDrainTimeoutNs);
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ MMA issue
+    constexpr uint32_t idesc_s = idesc_e4m3_f32(128, C::kNS, false, false);
+    constexpr uint32_t idesc_o = idesc_e4m3_f32(128, C::kNP, true, false);
+    const uint32_t base = smem_u32(smem);
+    auto score = [&](int i, int qbuf, bool last) {
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t slot = base + (i & 1) * kTileSlot, q = base + C::kOffQ + qbuf * C::kQBytes;
+        const Desc2 ad = desc2(smem_desc_sw128(slot, 16, kGroupBytes)), ak = desc2(smem_desc_sw64(slot + kCkvBytes, 512));
+        const Desc2 bd = desc2(smem_desc_sw128(q, 16, 1024)), bk = desc2(smem_desc_sw64(q + 4 * C::kQChunk, 512));
+        const uint32_t d = tmem + C::kTmemS + (i % C::kSBufs) * C::kNS;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma8_ss(d, ad, (c * 1024 + kk * 32) >> 4, bd, (c * C::kQChunk + kk * 32) >> 4, idesc_s, (c | kk) != 0 ? 1u : 0u);
+        umma8_ss(d, ak, 0, bk, 0, idesc_s, 1u);
+        umma8_ss(d, ak, 32 >> 4, bk, 32 >> 4, idesc_s, 1u);
+        umma_commit(&sm->sfull[i % C::kSBufs]);
+        if (last) umma_commit(&sm->qfree[qbuf]);
+      }
+      __syncwarp();
+    };
+    auto pv = [&](int i, int ksteps, bool first) {
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t slot = base + (i & 1) * kTileSlot;
+        const Desc2 pb = desc2(smem_desc_sw128(base + C::kOffP + (i & 1) * C::kPBytes, 16, 1024));
+        const Desc2 a0 = desc2(smem_desc_sw128(slot, 1024, kGroupBytes));
+#pragma unroll
+        for (int ks = 0; ks < kT / 32; ++ks) {
+          if (ks < ksteps) {
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk)
+              umma8_ss(tmem + C::kTmemO + blk * C::kNP, a0, (blk * 1024 + ks * 4 * kGroupBytes) >> 4, pb, (ks * 32) >> 4,
+                       idesc_o, (first && ks == 0) ? 0u : 1u);
           }
         }
-        acc[rr][0] = a0;
-        acc[rr][1] = a1;
+        umma_commit(&sm->empty[i & 1]);
+        umma_commit(&sm->pvdone[i & 1]);
+      }
+      __syncwarp();
+    };
+    // Issue as the inputs get ready, each product in tile order: the value product of tile np once its weights
+    // are written (it frees a slot), else the scores of tile ns. Nothing ready for longer than the wait limit
+    // (or an abort elsewhere) ends it.
+    Q8Walk a = w, b = w;  // of the scores, of the value products
+    int ns = 0, np = 0, a_seg = 0, b_seg = 0, a_tile = 0, b_tile = 0;
+    if (N > 0) {
+      q8_next(p, a, true);
+      q8_next(p, b, true);
+      a_tile = a.ta;
+      b_tile = b.ta;
+    }
+    bool idle = false;
+    uint64_t idle_t0 = 0;
+    while (np < N) {
+      int act = 0;
+      if (lane == 0) {
+        if (np < ns && mbar_test(&sm->pfull[np & 1], (np >> 1) & 1) &&
+            (b_tile != b.ta || b_seg == 0 || mbar_test(&sm->ofree, (b_seg - 1) & 1))) {
+          act = 2;
+        } else if (ns < N && mbar_test(&sm->full[ns & 1], (ns >> 1) & 1) &&
+                   (ns < C::kSBufs || mbar_test(&sm->sfree[ns % C::kSBufs], (ns / C::kSBufs - 1) & 1)) &&
+                   (a_tile != a.ta || mbar_test(&sm->qfull[a_seg % C::kQBufs], (a_seg / C::kQBufs) & 1))) {
+          act = 1;
+        } else if (*abort_flag) {
+          act = -1;
+        } else {
+          const uint64_t now = globaltimer_ns();
+          if (!idle) {
+            idle = true;
+            idle_t0 = now;
+          } else if (now - idle_t0 > tmo) {
+            act = -1;
+            *abort_flag = 1;
+            flag_error(MLA_DEVERR_TIMEOUT);
+          }
+        }
+        if (act > 0) idle = false;
+      }
+      act = __shfl_sync(0xffffffffu, act, 0);
+      if (act == 2) {
+        pv(np, (min(kT, b.v.n - b_tile * kT) + 31) >> 5, b_tile == b.ta);
+        ++np;
+        if (++b_tile == b.tb && np < N) {
+          q8_next(p, b, false);
+          b_tile = b.ta;
+          ++b_seg;
+        }
+      } else if (act == 1) {
+        score(ns, a_seg % C::kQBufs, a_tile + 1 == a.tb);
+        ++ns;
+        if (++a_tile == a.tb && ns < N) {
+          q8_next(p, a, false);
+          a_tile = a.ta;
+          ++a_seg;
+        }
+      } else if (act < 0) {
+        break;
       }
     }
-    __syncthreads();
-    const bool whole = ta == 0 && tb == n_tiles;
-    const long long entry = static_cast<long long>(gang) * 2 + (ta == 0 ? 1 : 0);
-    for (int rr = 0; rr < nrows; ++rr) {
-      const float m = sm.m[rr], l = sm.l[rr];
-      if (whole) {
-        const long long at = static_cast<long long>(b) * rows_total + row0 + rr;
-        for (int j = 0; j < 2; ++j) {
-          const float o = l == 0.f ? 0.f : acc[rr][j] / l;
-          const long long off = at * kRank + tid + j * kThreads;
-          if (p.out_dtype == 2)
-            static_cast<float*>(p.out)[off] = o;
-          else
-            static_cast<uint16_t*>(p.out)[off] = p.out_dtype == 1 ? f2h<true>(o) : f2h<false>(o);
+    if (lane == 0) {  // every MMA issued so far has completed before TMEM is freed
+      umma_commit(&sm->drain);
+      mbar_wait(&sm->drain, 0, kDrainTimeoutNs);
+    }
+    __syncwarp();
+  } else if (warp >= kQueryWarp) {
+    // ------------------------------------------------------------------ queries to terms
+    const int qw = warp - kQueryWarp;
+    bool first = true;
+    for (int seg = 0; q8_next(p, w, first); ++seg, first = false) {
+      const int buf = seg % C::kQBufs;
+      // this warp's rows qw, qw + 2, ..., kQueryRows at a time: 16 latent columns a lane (8 lane .., 256 + 8
+      // lane ..) and, in lanes 0-7, 8 rope ones
+      uint4 v[kQueryRows][3];
+      auto load = [&](int g) {
+#pragma unroll
+        for (int j = 0; j < kQueryRows; ++j) {
+          const int r = qw + kQueryWarps * (kQueryRows * g + j);
+          const long long at = static_cast<long long>(w.b) * rows_total + row0 + r;
+#pragma unroll
+          for (int x = 0; x < 3; ++x) v[j][x] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < nrows) {
+            v[j][0] = __ldcg(reinterpret_cast<const uint4*>(p.q_abs + at * kRank) + lane);
+            v[j][1] = __ldcg(reinterpret_cast<const uint4*>(p.q_abs + at * kRank) + 32 + lane);
+            if (lane < kRope / 8) v[j][2] = __ldcg(reinterpret_cast<const uint4*>(p.q_pe + at * kRope) + lane);
+          }
         }
-        if (tid == 0 && p.out_lse != nullptr) p.out_lse[at] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(l);
-      } else {
-        const long long at = entry * p.row_pad + row0 + rr;
-        for (int j = 0; j < 2; ++j) p.ws_o[at * kRank + tid + j * kThreads] = acc[rr][j];
-        if (tid == 0) {
-          p.ws_ml[at * 2] = m;
-          p.ws_ml[at * 2 + 1] = l;
+      };
+      load(0);
+      if (seg >= C::kQBufs) {
+        int ok = 1;
+        if (lane == 0) {
+          ok = mbar_wait(&sm->qfree[buf], (seg / C::kQBufs - 1) & 1, tmo) && !*abort_flag;
+          if (!ok) *abort_flag = 1;
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      }
+      uint8_t* const q = smem + C::kOffQ + buf * C::kQBytes;
+#pragma unroll 1
+      for (int g = 0; g < NR / (kQueryWarps * kQueryRows); ++g) {
+       if (g > 0) load(g);
+#pragma unroll
+       for (int j = 0; j < kQueryRows; ++j) {
+        const int r = qw + kQueryWarps * (kQueryRows * g + j);
+        float f[24];
+        float amax = 0.f;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          const uint32_t u[4] = {v[j][x].x, v[j][x].y, v[j][x].z, v[j][x].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            f[8 * x + 2 * y] = h2f<BF16>(static_cast<uint16_t>(u[y] & 0xffffu));
+            f[8 * x + 2 * y + 1] = h2f<BF16>(static_cast<uint16_t>(u[y] >> 16));
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 24; ++x) amax = max_nan(amax, fabsf(f[x]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // 2^e takes the row's largest magnitude to [128, 256); a row below 2^-119 stays under it
+        const int e = min(126, 134 - static_cast<int>(__float_as_uint(amax) >> 23));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if (lane == 0)
+          sm->factor[seg % kSums][r] = (amax < INFINITY) ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
+                                                         : __uint_as_float(0x7fc00000u);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          if (x == 2 && lane >= kRope / 8) break;
+          uint32_t t[4][C::kQTerms];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) split_terms<C::kQTerms>(f[8 * x + 2 * y] * up, f[8 * x + 2 * y + 1] * up, t[y]);
+#pragma unroll
+          for (int n = 0; n < C::kQTerms; ++n) {
+            const int row = n * NR + r;
+            const uint2 bytes = make_uint2(t[0][n] | (t[1][n] << 16), t[2][n] | (t[3][n] << 16));
+            // columns 8 lane .. + 7 of latent half x (or of the rope part)
+            uint8_t* const at =
+                x < 2 ? q + (2 * x + (lane >> 4)) * C::kQChunk + row * 128 + (((lane >> 1) ^ row) & 7) * 16 + (lane & 1) * 8
+                      : q + 4 * C::kQChunk + row * 64 + (((lane >> 1) ^ (row >> 1)) & 3) * 16 + (lane & 1) * 8;
+            *reinterpret_cast<uint2*>(at) = bytes;
+          }
+        }
+       }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->qfull[buf]);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax (warps 0-7)
+    const int q4 = warp & 3, h = warp >> 2;
+    const int tl = 32 * q4 + lane;  // this thread's token of each tile, and latent column of each block of O
+    const uint32_t lane_base = static_cast<uint32_t>(32 * q4) << 16;
+    const float w_up = static_cast<float>(1 << kWeightExp), w_down = 1.0f / w_up;
+    // the scale of position u of a request, NaN where it is neither NaN nor in range; 1 for none
+    auto page_at = [&](const Q8Walk& w, int tile) -> int {
+      if (tl >= w.v.n - tile * kT) return -1;
+      const int u = tile * kT + tl;
+      const int pg = u / p.bs + (u >= w.v.sa ? w.v.skip / p.bs : 0);
+      const int pid = pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
+      return (pid < 0 || pid >= p.num_blocks) ? -1 : pid;
+    };
+    auto scale_at = [&](int pid) -> float {
+      if (pid < 0) return 1.f;
+      const long long row = static_cast<long long>(pid) * p.bs + (tl & (p.bs - 1));
+      const float z = __ldg(p.scales + (row >> p.g_shift));
+      return (z >= 0x1p-60f && z <= 0x1p60f) ? z : __uint_as_float(0x7fc00000u);
+    };
+    int i = 0;  // tile count
+    bool first = true;
+    for (int seg = 0; q8_next(p, w, first); ++seg, first = false) {
+      float z = scale_at(page_at(w, w.ta));
+      int pid_next = w.ta + 1 < w.tb ? page_at(w, w.ta + 1) : -1;
+      float lsum[RH], mr[RH], factor[RH];
+#pragma unroll
+      for (int k = 0; k < RH; ++k) {
+        lsum[k] = 0.f;
+        mr[k] = -INFINITY;
+      }
+      if (tid < NR) sm->mref[tid] = -INFINITY;
+      // rows' positions: the first and last row of this CTA, and what their windows leave out
+      const int pos_first = p.causal ? w.v.n - p.q_len + row0 / p.H : w.v.n - 1;
+      const int pos_last = p.causal ? w.v.n - p.q_len + (row0 + nrows - 1) / p.H : w.v.n - 1;
+      const int low_last = p.window > 0 ? max(-1, pos_last - p.window) : -1;
+      bool stop = false;
+      for (int tile = w.ta; tile < w.tb; ++tile, ++i) {
+        const float z_next = tile + 1 < w.tb ? scale_at(pid_next) : 1.f;
+        pid_next = tile + 2 < w.tb ? page_at(w, tile + 2) : -1;
+        const int sb = i % C::kSBufs;
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(&sm->sfull[sb], (i / C::kSBufs) & 1, tmo);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (tile == w.ta) {
+#pragma unroll
+          for (int k = 0; k < RH; ++k) factor[k] = sm->factor[seg % kSums][RH * h + k];
+        }
+        float x[RH];
+        bool need_local = false;
+        const int u0 = tile * kT, nvalid = min(kT, w.v.n - u0);
+        const bool masked = nvalid < kT || u0 + kT - 1 > pos_first || u0 <= low_last || nrows < NR;
+        if (ok) {
+          tc_fence_after();
+          float t2[RH], t3[RH];
+          const uint32_t sa = tmem + lane_base + C::kTmemS + sb * C::kNS + RH * h;
+          tmem_ld<RH>(sa, x);
+          tmem_ld<RH>(sa + NR, t2);
+          if constexpr (C::kQTerms == 3) tmem_ld<RH>(sa + 2 * NR, t3);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->sfree[sb]);
+          const float lz = log2f(z);
+#pragma unroll
+          for (int k = 0; k < RH; ++k) {
+            if constexpr (C::kQTerms == 3) t2[k] = fmaf(t3[k], kTermInv, t2[k]);
+            x[k] = fmaf(fmaf(t2[k], kTermInv, x[k]) * factor[k], z, lz);
+          }
+          if (__builtin_expect(masked, 0)) {
+#pragma unroll
+            for (int k = 0; k < RH; ++k) {
+              const int r = row0 + RH * h + k, u = u0 + tl;
+              const int pos = p.causal ? w.v.n - p.q_len + r / p.H : w.v.n - 1;
+              bool vis = tl < nvalid && RH * h + k < nrows && u <= pos;
+              if (p.window > 0) vis = vis && (u > pos - p.window || u < p.sinks);
+              if (!vis) x[k] = -INFINITY;
+            }
+            // tokens that some row does not see: below the last row's window, behind the first row, and the
+            // rest of the tail's last step
+            uint8_t* const slot = smem + (i & 1) * kTileSlot;
+            const int a0 = min(kT, max(0, p.sinks - u0)), a1 = min(kT, low_last + 1 - u0);
+            const int b0 = max(0, min(kT, min(w.v.n, pos_first + 1) - u0)), b1 = (nvalid + 31) & ~31;
+            if (a0 < a1) clear_nan_bytes(slot, a0, a1, tid);
+            if (b0 < b1) clear_nan_bytes(slot, b0, b1, tid);
+          }
+#pragma unroll
+          for (int k = 0; k < RH; ++k) need_local |= x[k] > mr[k] + kTau;
+        } else {
+#pragma unroll
+          for (int k = 0; k < RH; ++k) x[k] = -INFINITY;
+          *abort_flag = 1;
+        }
+        if (named_bar_sync_or(1, kSoftmaxThreads, need_local || *abort_flag != 0)) {
+          if (named_bar_sync_or(1, kSoftmaxThreads, *abort_flag != 0)) {
+            stop = true;
+            break;
+          }
+          // the reference maxima move, and with them O and the sums
+#pragma unroll
+          for (int k = 0; k < RH; ++k) {
+            float v = x[k];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            if (lane == 0) sm->red[q4][RH * h + k] = v;
+          }
+          named_bar_sync(1, kSoftmaxThreads);
+          if (tid < NR) {
+            const float mprev = sm->mref[tid];
+            const float mnew = fmaxf(mprev, fmaxf(fmaxf(sm->red[0][tid], sm->red[1][tid]), fmaxf(sm->red[2][tid], sm->red[3][tid])));
+            sm->alpha[tid] = (mprev == -INFINITY) ? 1.f : exp2f(mprev - mnew);  // (nothing summed yet, or only NaN)
+            sm->mref[tid] = mnew;
+          }
+          named_bar_sync(1, kSoftmaxThreads);
+          float al[RH];
+#pragma unroll
+          for (int k = 0; k < RH; ++k) {
+            mr[k] = sm->mref[RH * h + k];
+            al[k] = sm->alpha[RH * h + k];
+            lsum[k] *= al[k];
+          }
+          if (tile > w.ta) {  // the value product of the tile before must be complete
+            int ok2 = 1;
+            if (lane == 0) ok2 = mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo);
+            if (__shfl_sync(0xffffffffu, ok2, 0)) {
+              tc_fence_after();
+#pragma unroll
+              for (int blk = 0; blk < 4 * kTerms; ++blk) {
+                float v[RH];
+                const uint32_t a = tmem + lane_base + C::kTmemO + blk * NR + RH * h;
+                tmem_ld<RH>(a, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < RH; ++k) v[k] *= al[k];
+                tmem_st<RH>(a, v);
+              }
+              tmem_wait_st();
+            } else if (lane == 0) {
+              *abort_flag = 1;
+            }
+          }
+        }
+        // the weight buffer was last read by the value product of tile i - 2
+        if (i >= 2) {
+          int ok3 = 1;
+          if (lane == 0) ok3 = mbar_wait(&sm->pvdone[i & 1], ((i >> 1) - 1) & 1, tmo);
+          if (!__shfl_sync(0xffffffffu, ok3, 0) && lane == 0) *abort_flag = 1;
+        }
+        {
+          const float iz = 1.f / z;
+          uint8_t* const pb = smem + C::kOffP + (i & 1) * C::kPBytes + (tl & 15);
+#pragma unroll
+          for (int k = 0; k < RH; k += 2) {
+            float wt[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              wt[j] = fast_exp2(x[k + j] - ((mr[k + j] == -INFINITY) ? 0.f : mr[k + j]));  // hidden tokens (-inf) give 0
+              lsum[k + j] += (wt[j] == 0.f) ? 0.f : wt[j] * iz;  // (a hidden token's scale may be NaN)
+            }
+            uint32_t t[kTerms];
+            split_terms<kTerms>(wt[0] * w_up, wt[1] * w_up, t);
+#pragma unroll
+            for (int n = 0; n < kTerms; ++n)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int row = n * NR + RH * h + k + j;
+                pb[row * 128 + ((((tl >> 4) ^ row) & 7) << 4)] = static_cast<uint8_t>(t[n] >> (8 * j));
+              }
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->pfull[i & 1]);
+        z = z_next;
+      }
+      // the segment's end: its sums, and O once its last value product is complete
+      if (!stop) {
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) *abort_flag = 1;
+      }
+      if (stop || named_bar_sync_or(1, kSoftmaxThreads, *abort_flag != 0)) break;
+#pragma unroll
+      for (int k = 0; k < RH; ++k) {
+        float v = lsum[k];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) sm->red[q4][RH * h + k] = v;
+      }
+      named_bar_sync(1, kSoftmaxThreads);
+      const bool whole = w.ta == 0 && w.tb == w.n_tiles;
+      const long long orow = whole ? static_cast<long long>(w.b) * rows_total + row0 + RH * h
+                                   : (static_cast<long long>(gang) * 2 + (w.ta == 0 ? 1 : 0)) * p.row_pad + row0 + RH * h;
+      float inv[RH];
+#pragma unroll
+      for (int k = 0; k < RH; ++k) {
+        const int r = RH * h + k;
+        const float l = (sm->red[0][r] + sm->red[1][r]) + (sm->red[2][r] + sm->red[3][r]);
+        inv[k] = !whole ? w_down : (l == 0.f ? 0.f : w_down / l);  // (no visible token: every weight was 0)
+        if (r < nrows && q4 == 0 && lane == 0) {
+          if (!whole) {
+            p.ws_ml[(orow + k) * 2] = mr[k];
+            p.ws_ml[(orow + k) * 2 + 1] = l;
+          } else if (p.out_lse != nullptr) {
+            p.out_lse[orow + k] = l == 0.f ? -INFINITY : ((mr[k] == -INFINITY) ? 0.f : mr[k]) + log2f(l);
+          }
+        }
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int blk = 0; blk < 4; ++blk) {
+        float o1[RH], o2[RH], o3[RH];
+        const uint32_t a = tmem + lane_base + C::kTmemO + blk * C::kNP + RH * h;
+        tmem_ld<RH>(a, o1);
+        tmem_ld<RH>(a + NR, o2);
+        tmem_ld<RH>(a + 2 * NR, o3);
+        tmem_wait_ld();
+        if (blk == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->ofree);
+        }
+#pragma unroll
+        for (int k = 0; k < RH; ++k) {
+          if (RH * h + k < nrows) {
+            const float o = fmaf(fmaf(o3[k], kTermInv, o2[k]), kTermInv, o1[k]) * inv[k];
+            const long long off = (orow + k) * kRank + blk * 128 + tl;
+            if (!whole)
+              p.ws_o[off] = o;
+            else if (p.out_dtype == 2)
+              static_cast<float*>(p.out)[off] = o;
+            else
+              static_cast<uint16_t*>(p.out)[off] = p.out_dtype == 1 ? f2h<true>(o) : f2h<false>(o);
+          }
         }
       }
     }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -314,34 +858,39 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_q8_kernel(const Decod
   }
 }
 
+template <int NR, bool BF16>
+cudaError_t launch(cudaLaunchConfig_t cfg, const CUtensorMap& tm_ckv, const CUtensorMap& tm_kpe, const DecodeQ8Params& p) {
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_decode_q8_kernel<NR, BF16>),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR, BF16>::kSmem);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.groups), static_cast<unsigned>(p.gangs), 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg<NR, BF16>::kSmem;
+  return cudaLaunchKernelEx(&cfg, mla_decode_q8_kernel<NR, BF16>, tm_ckv, tm_kpe, p);
+}
+
 }  // namespace
 
-int q8_rows_per_cta(int total_rows) {
-  (void)total_rows;
-  return kNR;
-}
+int q8_rows_per_cta(int total_rows) { return total_rows <= 16 ? 16 : 32; }
 int q8_gangs(int total_rows, int sms) {
-  const int groups = (total_rows + kNR - 1) / kNR;
+  const int nr = q8_rows_per_cta(total_rows), groups = (total_rows + nr - 1) / nr;
   return sms > groups ? sms / groups : 1;
 }
 
-cudaError_t launch_decode_q8(const DecodeQ8Params& p, bool bf16, cudaStream_t stream) {
-  const void* fn = bf16 ? reinterpret_cast<const void*>(&mla_decode_q8_kernel<true>)
-                        : reinterpret_cast<const void*>(&mla_decode_q8_kernel<false>);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
-  if (e != cudaSuccess) return e;
+cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kpe, const DecodeQ8Params& p, bool bf16,
+                             cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.groups), static_cast<unsigned>(p.gangs), 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(Smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = bf16 ? cudaLaunchKernelEx(&cfg, mla_decode_q8_kernel<true>, p)
-           : cudaLaunchKernelEx(&cfg, mla_decode_q8_kernel<false>, p);
+  cudaError_t e;
+  if (q8_rows_per_cta(p.q_len * p.H) == 16)
+    e = bf16 ? launch<16, true>(cfg, tm_ckv, tm_kpe, p) : launch<16, false>(cfg, tm_ckv, tm_kpe, p);
+  else
+    e = bf16 ? launch<32, true>(cfg, tm_ckv, tm_kpe, p) : launch<32, false>(cfg, tm_ckv, tm_kpe, p);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(2 * 152, 1, 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);

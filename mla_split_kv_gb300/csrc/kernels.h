@@ -182,7 +182,10 @@ struct DecodeQ8Params {
 // Rows per CTA, and gangs, of the launch for q_len * H rows on a device of `sms` SMs.
 int q8_rows_per_cta(int total_rows);
 int q8_gangs(int total_rows, int sms);
-cudaError_t launch_decode_q8(const DecodeQ8Params& p, bool bf16, cudaStream_t stream);
+// tm_ckv: boxes of one page of the byte cache, [8 rows x 128 columns] swizzled atoms, four column blocks to a
+// row group; tm_kpe: boxes of one page's 64 rope columns with the 64-byte swizzle.
+cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kpe, const DecodeQ8Params& p, bool bf16,
+                             cudaStream_t stream);
 cudaError_t decode_q8_read_clear_error(uint32_t* out);
 
 // Launchers return cudaSuccess or the launch error. grid.x = cluster of

@@ -52,4 +52,36 @@ __device__ __forceinline__ int64_t block_prefix(int64_t mine, int64_t* scratch, 
   return before + x - mine;
 }
 
+// A gang's tiles, request after request.
+struct Q8Walk {
+  int b;            // request of the current segment
+  int ta, tb;       // its tiles [ta, tb) are this gang's ...
+  int n_tiles;      // ... of so many
+  int64_t left;     // tiles behind the segment
+  WindowView v;
+};
+__device__ __forceinline__ Q8Walk q8_walk(int b0, int64_t off0, int64_t tiles) {
+  Q8Walk w;
+  w.b = b0 - 1;
+  w.ta = 0;
+  w.tb = static_cast<int>(off0);  // (where the first segment starts)
+  w.n_tiles = 0;
+  w.left = tiles;
+  return w;
+}
+// The next segment; false at the end.
+__device__ __forceinline__ bool q8_next(const DecodeQ8Params& p, Q8Walk& w, bool first) {
+  if (w.left <= 0) return false;
+  const int start = first ? w.tb : 0;
+  do {
+    ++w.b;
+    w.v = window_view(__ldcg(p.context_lens + w.b), p.q_len, p.bs, p.causal, p.window, p.sinks);
+    w.n_tiles = static_cast<int>((static_cast<int64_t>(w.v.n) + kQ8Tile - 1) / kQ8Tile);
+  } while (w.n_tiles == 0);
+  w.ta = start;
+  w.tb = static_cast<int>(w.n_tiles < start + w.left ? w.n_tiles : start + w.left);
+  w.left -= w.tb - w.ta;
+  return true;
+}
+
 }  // namespace mla
