@@ -57,8 +57,10 @@ constexpr float kTermStep = 32.0f, kTermInv = 1.0f / 32.0f;
 // 2^kWeightExp they fit E4M3's 448, and its subnormals reach down to 2^-25 of the reference in the third term.
 constexpr float kTau = 2.0f;
 constexpr int kWeightExp = 6;
-constexpr int kQueryRows = 4;                     // rows a query warp has in flight
+constexpr int kFirstWarps = kSoftmaxWarps + kQueryWarps;  // that split the first request's queries
 constexpr int kSums = 4;                          // row factors kept: queries split ahead of their softmax
+
+constexpr uint32_t kSmallBytes = 5120;
 
 template <int NR, bool BF16>
 struct Cfg {
@@ -72,7 +74,7 @@ struct Cfg {
   static constexpr uint32_t kOffQ = kSlots * kTileSlot;
   static constexpr uint32_t kOffP = kOffQ + kQBufs * kQBytes;
   static constexpr uint32_t kOffSmall = kOffP + 2 * kPBytes;
-  static constexpr uint32_t kSmem = kOffSmall + 3072;
+  static constexpr uint32_t kSmem = kOffSmall + kSmallBytes;
   static constexpr uint32_t kTmemO = 0, kTmemS = 4 * kNP;
   static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kQChunk % 1024 == 0, "swizzle atoms stay aligned");
   static_assert(kTmemS + kSBufs * kNS <= 512, "tensor memory");
@@ -83,30 +85,41 @@ struct Small {
   uint64_t full[kSlots], empty[kSlots];  // tile slots
   uint64_t sfull[2], sfree[2];           // score buffers
   uint64_t pfull[2], pvdone[2];          // weight buffers
-  uint64_t qfull[2], qfree[2];           // query buffers
+  uint64_t qfull[2], qfree[2], qfirst;   // query buffers
   uint64_t ofree, drain;
   int64_t scratch[33];
   int64_t off0;
   int b0;
   uint32_t tmem_base;
   int32_t abort_flag;
-  float factor[kSums][32];               // per row: score scale over the query's power of two, log2 units
-  float red[4][32], mref[32], alpha[32];
+  alignas(16) float factor[kSums][32];   // per row: score scale over the query's power of two, log2 units
+  alignas(16) float red[2][4][32];       // per tile parity and token quadrant, rows' maxima (then their sums)
+  int32_t lens[kQ8Lens];
 };
-static_assert(sizeof(Small) <= 3072, "small smem region");
+static_assert(sizeof(Small) <= kSmallBytes, "small smem region");
 
-// x = t1 + t2 / 32 + t3 / 1024 for the two values of a pair, each term two E4M3 bytes
+// (x - v) * 32 for the two fp16 values of a pair
+__device__ __forceinline__ uint32_t next_term(uint32_t x, uint32_t v) {
+  const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&v)),
+                            __float2half2_rn(kTermStep));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+// x = t1 + t2 / 32 + ... for a pair of fp16 values of at most 256, each term two E4M3 bytes: x has 11 bits, so
+// what a term leaves, and that times 32, are fp16 values themselves, and the third term leaves nothing
 template <int N>
-__device__ __forceinline__ void split_terms(float a, float b, uint32_t* t) {
+__device__ __forceinline__ void split_f16(uint32_t x, uint32_t* t) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    t[i] = e4m3x2(a, b);
-    if (i + 1 < N) {
-      const float2 v = e4m3x2_values(t[i]);
-      a = (a - v.x) * kTermStep;
-      b = (b - v.y) * kTermStep;
-    }
+    t[i] = f16x2_to_e4m3x2(x);
+    if (i + 1 < N) x = next_term(x, e4m3x2_to_f16x2(t[i]));
   }
+}
+// The same for fp32 values: the first term and what it leaves in fp32, the rest of that (11 bits of it) in fp16.
+__device__ __forceinline__ void split_f32(float a, float b, uint32_t* t) {
+  t[0] = e4m3x2(a, b);
+  const float2 v = e4m3x2_values(t[0]);
+  const __half2 rest = __hmul2(__floats2half2_rn(a - v.x, b - v.y), __float2half2_rn(kTermStep));
+  split_f16<kTerms - 1>(*reinterpret_cast<const uint32_t*>(&rest), t + 1);
 }
 
 template <int N>
@@ -148,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const DecodeQ8Params p) {
   using C = Cfg<NR, BF16>;
   constexpr int RH = NR / 2;  // rows per softmax thread
+  constexpr int kPieces = NR == 16 ? 4 : 2;
   extern __shared__ uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need it; the size leaves no slack to align it
     if (threadIdx.x == 0) flag_error(MLA_DEVERR_CONFIG);
@@ -171,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm->qfull[s], kQueryWarps);
       mbar_init(&sm->qfree[s], 1);
     }
+    mbar_init(&sm->qfirst, kFirstWarps);
     mbar_init(&sm->ofree, kSoftmaxWarps);
     mbar_init(&sm->drain, 1);
     sm->abort_flag = 0;
@@ -188,10 +203,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   // this gang's place on the line of tiles
+  const Q8Lens lens{p.context_lens, sm->lens};
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
   int64_t mine = 0, T = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += q8_tiles(p, b);
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int L = __ldcg(p.context_lens + b);
+    if (b < kQ8Lens) sm->lens[b] = L;
+    mine += q8_tiles(q8_view(p, L));
+  }
   const int64_t prefix = block_prefix<kThreads>(mine, sm->scratch, &T);
   const int64_t J = q8_live_gangs(T, p.gangs);
   const bool work = gang < J;
@@ -200,22 +220,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t at = prefix;
     int b = b_lo;
     while (true) {
-      const int64_t n = q8_tiles(p, b);
+      const int n = q8_tiles(q8_view(p, lens(b)));
       if (at + n > lo) break;
       at += n;
       ++b;
     }
     sm->b0 = b;
     sm->off0 = lo - at;
-  }
-  // requests with nothing to see
-  for (int b = gang; b < p.B; b += p.gangs) {
-    if (q8_tiles(p, b) != 0) continue;
-    for (int x = tid; x < nrows * (kRank / 4); x += kThreads) {
-      const long long at = static_cast<long long>(b) * rows_total + row0 + x / (kRank / 4);
-      store_out4(p.out, p.out_dtype, at * kRank + 4 * (x % (kRank / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
-      if (x % (kRank / 4) == 0 && p.out_lse != nullptr) p.out_lse[at] = -INFINITY;
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -225,6 +236,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   Q8Walk w = q8_walk(work ? sm->b0 : 0, work ? sm->off0 : 0, N);
   uint64_t tmo = p.timeout_ns;
   asm volatile("" : "+l"(tmo));
+
+  // One row of request b's queries to its terms, by one warp: a lane takes latent columns 8 lane .. and 256 + 8
+  // lane .., and in lanes 0-7 8 rope columns. In two steps, so that rows' loads overlap.
+  struct QueryRow {
+    uint4 v[3];
+  };
+  auto load_query = [&](int b, int r) -> QueryRow {
+    QueryRow q;
+#pragma unroll
+    for (int x = 0; x < 3; ++x) q.v[x] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < nrows) {
+      const long long at = static_cast<long long>(b) * rows_total + row0 + r;
+      q.v[0] = __ldcg(reinterpret_cast<const uint4*>(p.q_abs + at * kRank) + lane);
+      q.v[1] = __ldcg(reinterpret_cast<const uint4*>(p.q_abs + at * kRank) + 32 + lane);
+      if (lane < kRope / 8) q.v[2] = __ldcg(reinterpret_cast<const uint4*>(p.q_pe + at * kRope) + lane);
+    }
+    return q;
+  };
+  auto split_query = [&](const QueryRow& qr, int seg, int r) {
+    uint8_t* const q = smem + C::kOffQ + (seg % C::kQBufs) * C::kQBytes;
+    const uint32_t* const u = reinterpret_cast<const uint32_t*>(qr.v);
+    // the row's largest magnitude (its bits: 15 of them order both types, NaN and infinity on top)
+    uint32_t top = 0;
+#pragma unroll
+    for (int x = 0; x < 12; ++x) top = __vmaxu2(top, u[x] & 0x7fff7fffu);
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    const float amax = h2f<BF16>(static_cast<uint16_t>(top));
+    // 2^e takes it to [128, 256); a row below 2^-119 stays under it
+    const int e = min(126, 134 - static_cast<int>(__float_as_uint(amax) >> 23));
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if (lane == 0)
+      sm->factor[seg % kSums][r] = (amax < INFINITY) ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
+                                                     : __uint_as_float(0x7fc00000u);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      if (x == 2 && lane >= kRope / 8) break;
+      uint32_t t[4][C::kQTerms];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t w = u[4 * x + y];
+        const __half2 f = __floats2half2_rn(h2f<BF16>(static_cast<uint16_t>(w & 0xffffu)) * up,
+                                            h2f<BF16>(static_cast<uint16_t>(w >> 16)) * up);
+        split_f16<C::kQTerms>(*reinterpret_cast<const uint32_t*>(&f), t[y]);
+      }
+#pragma unroll
+      for (int n = 0; n < C::kQTerms; ++n) {
+        const int row = n * NR + r;
+        // columns 8 lane .. + 7 of latent half x (or of the rope part)
+        uint8_t* const at = x < 2 ? q + (2 * x + (lane >> 4)) * C::kQChunk + row * 128 + (((lane >> 1) ^ row) & 7) * 16 + (lane & 1) * 8
+                                  : q + 4 * C::kQChunk + row * 64 + (((lane >> 1) ^ (row >> 1)) & 3) * 16 + (lane & 1) * 8;
+        *reinterpret_cast<uint2*>(at) = make_uint2(t[0][n] | (t[1][n] << 16), t[2][n] | (t[3][n] << 16));
+      }
+    }
+  };
+  // rows r0, r0 + step, ... of request b, two at a time
+  auto split_rows = [&](int b, int seg, int r0, int step) {
+#pragma unroll 1
+    for (int r = r0; r < NR; r += 2 * step) {
+      const bool two = r + step < NR;
+      const QueryRow q0 = load_query(b, r);
+      QueryRow q1 = q0;
+      if (two) q1 = load_query(b, r + step);
+      split_query(q0, seg, r);
+      if (two) split_query(q1, seg, r + step);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+  // the first request's queries: all warps that would wait for its scores
+  if (work && warp != kLoadWarp && warp != kMmaWarp) {
+    split_rows(sm->b0, 0, warp < kSoftmaxWarps ? warp : warp - kQueryWarp + kSoftmaxWarps, kFirstWarps);
+    if (lane == 0) mbar_arrive(&sm->qfirst);
+  }
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ page loads
@@ -241,13 +325,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // a walk that runs ahead: its page numbers wait in registers until their tile's prefetch and load
     Q8Walk a = w;
-    bool a_live = q8_next(p, a, true);
+    bool a_live = q8_next(p, lens, a, true);
     int a_tile = a.ta;
     auto ahead = [&]() -> int {
       if (!a_live) return -2;
       const int pid = page_of(a, a_tile);
       if (++a_tile == a.tb) {
-        a_live = q8_next(p, a, false);
+        a_live = q8_next(p, lens, a, false);
         a_tile = a.ta;
       }
       return pid;
@@ -339,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Q8Walk a = w, b = w;  // of the scores, of the value products
     int ns = 0, np = 0, a_seg = 0, b_seg = 0, a_tile = 0, b_tile = 0;
     if (N > 0) {
-      q8_next(p, a, true);
-      q8_next(p, b, true);
+      q8_next(p, lens, a, true);
+      q8_next(p, lens, b, true);
       a_tile = a.ta;
       b_tile = b.ta;
     }
@@ -354,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           act = 2;
         } else if (ns < N && mbar_test(&sm->full[ns & 1], (ns >> 1) & 1) &&
                    (ns < C::kSBufs || mbar_test(&sm->sfree[ns % C::kSBufs], (ns / C::kSBufs - 1) & 1)) &&
-                   (a_tile != a.ta || mbar_test(&sm->qfull[a_seg % C::kQBufs], (a_seg / C::kQBufs) & 1))) {
+                   (a_tile != a.ta || (a_seg == 0 ? mbar_test(&sm->qfirst, 0) : mbar_test(&sm->qfull[a_seg & 1], ((a_seg - 1) >> 1) & 1)))) {
           act = 1;
         } else if (*abort_flag) {
           act = -1;
@@ -376,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         pv(np, (min(kT, b.v.n - b_tile * kT) + 31) >> 5, b_tile == b.ta);
         ++np;
         if (++b_tile == b.tb && np < N) {
-          q8_next(p, b, false);
+          q8_next(p, lens, b, false);
           b_tile = b.ta;
           ++b_seg;
         }
@@ -384,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         score(ns, a_seg % C::kQBufs, a_tile + 1 == a.tb);
         ++ns;
         if (++a_tile == a.tb && ns < N) {
-          q8_next(p, a, false);
+          q8_next(p, lens, a, false);
           a_tile = a.ta;
           ++a_seg;
         }
@@ -398,158 +482,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= kQueryWarp) {
-    // ------------------------------------------------------------------ queries to terms
-    const int qw = warp - kQueryWarp;
-    bool first = true;
-    for (int seg = 0; q8_next(p, w, first); ++seg, first = false) {
-      const int buf = seg % C::kQBufs;
-      // this warp's rows qw, qw + 2, ..., kQueryRows at a time: 16 latent columns a lane (8 lane .., 256 + 8
-      // lane ..) and, in lanes 0-7, 8 rope ones
-      uint4 v[kQueryRows][3];
-      auto load = [&](int g) {
-#pragma unroll
-        for (int j = 0; j < kQueryRows; ++j) {
-          const int r = qw + kQueryWarps * (kQueryRows * g + j);
-          const long long at = static_cast<long long>(w.b) * rows_total + row0 + r;
-#pragma unroll
-          for (int x = 0; x < 3; ++x) v[j][x] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < nrows) {
-            v[j][0] = __ldcg(reinterpret_cast<const uint4*>(p.q_abs + at * kRank) + lane);
-            v[j][1] = __ldcg(reinterpret_cast<const uint4*>(p.q_abs + at * kRank) + 32 + lane);
-            if (lane < kRope / 8) v[j][2] = __ldcg(reinterpret_cast<const uint4*>(p.q_pe + at * kRope) + lane);
-          }
-        }
-      };
-      load(0);
-      if (seg >= C::kQBufs) {
+    // ------------------------------------------------------------------ the next requests' queries to terms
+    bool more = q8_next(p, lens, w, true);
+    for (int seg = 1; more && (more = q8_next(p, lens, w, false)); ++seg) {
+      if (seg >= C::kQBufs) {  // the request whose place they take has its scores
         int ok = 1;
         if (lane == 0) {
-          ok = mbar_wait(&sm->qfree[buf], (seg / C::kQBufs - 1) & 1, tmo) && !*abort_flag;
+          ok = mbar_wait(&sm->qfree[seg % C::kQBufs], (seg / C::kQBufs - 1) & 1, tmo) && !*abort_flag;
           if (!ok) *abort_flag = 1;
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       }
-      uint8_t* const q = smem + C::kOffQ + buf * C::kQBytes;
-#pragma unroll 1
-      for (int g = 0; g < NR / (kQueryWarps * kQueryRows); ++g) {
-       if (g > 0) load(g);
-#pragma unroll
-       for (int j = 0; j < kQueryRows; ++j) {
-        const int r = qw + kQueryWarps * (kQueryRows * g + j);
-        float f[24];
-        float amax = 0.f;
-#pragma unroll
-        for (int x = 0; x < 3; ++x) {
-          const uint32_t u[4] = {v[j][x].x, v[j][x].y, v[j][x].z, v[j][x].w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            f[8 * x + 2 * y] = h2f<BF16>(static_cast<uint16_t>(u[y] & 0xffffu));
-            f[8 * x + 2 * y + 1] = h2f<BF16>(static_cast<uint16_t>(u[y] >> 16));
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < 24; ++x) amax = max_nan(amax, fabsf(f[x]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // 2^e takes the row's largest magnitude to [128, 256); a row below 2^-119 stays under it
-        const int e = min(126, 134 - static_cast<int>(__float_as_uint(amax) >> 23));
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        if (lane == 0)
-          sm->factor[seg % kSums][r] = (amax < INFINITY) ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
-                                                         : __uint_as_float(0x7fc00000u);
-#pragma unroll
-        for (int x = 0; x < 3; ++x) {
-          if (x == 2 && lane >= kRope / 8) break;
-          uint32_t t[4][C::kQTerms];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) split_terms<C::kQTerms>(f[8 * x + 2 * y] * up, f[8 * x + 2 * y + 1] * up, t[y]);
-#pragma unroll
-          for (int n = 0; n < C::kQTerms; ++n) {
-            const int row = n * NR + r;
-            const uint2 bytes = make_uint2(t[0][n] | (t[1][n] << 16), t[2][n] | (t[3][n] << 16));
-            // columns 8 lane .. + 7 of latent half x (or of the rope part)
-            uint8_t* const at =
-                x < 2 ? q + (2 * x + (lane >> 4)) * C::kQChunk + row * 128 + (((lane >> 1) ^ row) & 7) * 16 + (lane & 1) * 8
-                      : q + 4 * C::kQChunk + row * 64 + (((lane >> 1) ^ (row >> 1)) & 3) * 16 + (lane & 1) * 8;
-            *reinterpret_cast<uint2*>(at) = bytes;
-          }
-        }
-       }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->qfull[buf]);
+      split_rows(w.b, seg, warp - kQueryWarp, kQueryWarps);
+      if (lane == 0) mbar_arrive(&sm->qfull[seg & 1]);
     }
   } else {
     // ------------------------------------------------------------------ softmax (warps 0-7)
     const int q4 = warp & 3, h = warp >> 2;
     const int tl = 32 * q4 + lane;  // this thread's token of each tile, and latent column of each block of O
     const uint32_t lane_base = static_cast<uint32_t>(32 * q4) << 16;
+    const uint32_t bar = 1 + h, kHalf = kSoftmaxThreads / 2;  // the four warps of a row half meet by themselves
     const float w_up = static_cast<float>(1 << kWeightExp), w_down = 1.0f / w_up;
-    // the scale of position u of a request, NaN where it is neither NaN nor in range; 1 for none
+    // this thread's page of a tile, and its token's scale there: loads a tile ahead of their use each, so
+    // neither looks at what it loaded
     auto page_at = [&](const Q8Walk& w, int tile) -> int {
       if (tl >= w.v.n - tile * kT) return -1;
       const int u = tile * kT + tl;
       const int pg = u / p.bs + (u >= w.v.sa ? w.v.skip / p.bs : 0);
-      const int pid = pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
-      return (pid < 0 || pid >= p.num_blocks) ? -1 : pid;
+      return pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
     };
-    auto scale_at = [&](int pid) -> float {
-      if (pid < 0) return 1.f;
+    auto scale_at = [&](int pid) -> float {  // 1 where there is no page
+      if (pid < 0 || pid >= p.num_blocks) return 1.f;
       const long long row = static_cast<long long>(pid) * p.bs + (tl & (p.bs - 1));
-      const float z = __ldg(p.scales + (row >> p.g_shift));
-      return (z >= 0x1p-60f && z <= 0x1p60f) ? z : __uint_as_float(0x7fc00000u);
+      return __ldg(p.scales + (row >> p.g_shift));
     };
     int i = 0;  // tile count
     bool first = true;
-    for (int seg = 0; q8_next(p, w, first); ++seg, first = false) {
-      float z = scale_at(page_at(w, w.ta));
-      int pid_next = w.ta + 1 < w.tb ? page_at(w, w.ta + 1) : -1;
-      float lsum[RH], mr[RH], factor[RH];
+    for (int seg = 0; q8_next(p, lens, w, first); ++seg, first = false) {
+      float z_raw = scale_at(page_at(w, w.ta));
+      int pid = w.ta + 1 < w.tb ? page_at(w, w.ta + 1) : -1;
+      float lsum[RH], mr[RH];
 #pragma unroll
       for (int k = 0; k < RH; ++k) {
         lsum[k] = 0.f;
         mr[k] = -INFINITY;
       }
-      if (tid < NR) sm->mref[tid] = -INFINITY;
       // rows' positions: the first and last row of this CTA, and what their windows leave out
       const int pos_first = p.causal ? w.v.n - p.q_len + row0 / p.H : w.v.n - 1;
       const int pos_last = p.causal ? w.v.n - p.q_len + (row0 + nrows - 1) / p.H : w.v.n - 1;
       const int low_last = p.window > 0 ? max(-1, pos_last - p.window) : -1;
       bool stop = false;
       for (int tile = w.ta; tile < w.tb; ++tile, ++i) {
-        const float z_next = tile + 1 < w.tb ? scale_at(pid_next) : 1.f;
-        pid_next = tile + 2 < w.tb ? page_at(w, tile + 2) : -1;
+        // NaN for a scale that is neither NaN nor in range
+        const float z = (z_raw >= 0x1p-60f && z_raw <= 0x1p60f) ? z_raw : __uint_as_float(0x7fc00000u);
+        const float lz = log2f(z), iz = 1.f / z;
+        z_raw = tile + 1 < w.tb ? scale_at(pid) : 1.f;
+        pid = tile + 2 < w.tb ? page_at(w, tile + 2) : -1;
         const int sb = i % C::kSBufs;
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait(&sm->sfull[sb], (i / C::kSBufs) & 1, tmo);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (tile == w.ta) {
-#pragma unroll
-          for (int k = 0; k < RH; ++k) factor[k] = sm->factor[seg % kSums][RH * h + k];
-        }
+        bool ok = mbar_wait(&sm->sfull[sb], (i / C::kSBufs) & 1, tmo);
         float x[RH];
-        bool need_local = false;
         const int u0 = tile * kT, nvalid = min(kT, w.v.n - u0);
-        const bool masked = nvalid < kT || u0 + kT - 1 > pos_first || u0 <= low_last || nrows < NR;
-        if (ok) {
+        if (__all_sync(0xffffffffu, ok)) {
           tc_fence_after();
           float t2[RH], t3[RH];
           const uint32_t sa = tmem + lane_base + C::kTmemS + sb * C::kNS + RH * h;
           tmem_ld<RH>(sa, x);
           tmem_ld<RH>(sa + NR, t2);
           if constexpr (C::kQTerms == 3) tmem_ld<RH>(sa + 2 * NR, t3);
+          float factor[RH];
+#pragma unroll
+          for (int k = 0; k < RH; k += 4)
+            *reinterpret_cast<float4*>(factor + k) = *reinterpret_cast<const float4*>(&sm->factor[seg % kSums][RH * h + k]);
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm->sfree[sb]);
-          const float lz = log2f(z);
 #pragma unroll
           for (int k = 0; k < RH; ++k) {
             if constexpr (C::kQTerms == 3) t2[k] = fmaf(t3[k], kTermInv, t2[k]);
             x[k] = fmaf(fmaf(t2[k], kTermInv, x[k]) * factor[k], z, lz);
           }
-          if (__builtin_expect(masked, 0)) {
+          if (__builtin_expect(nvalid < kT || u0 + kT - 1 > pos_first || u0 <= low_last || nrows < NR, 0)) {
 #pragma unroll
             for (int k = 0; k < RH; ++k) {
               const int r = row0 + RH * h + k, u = u0 + tl;
@@ -566,70 +579,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a0 < a1) clear_nan_bytes(slot, a0, a1, tid);
             if (b0 < b1) clear_nan_bytes(slot, b0, b1, tid);
           }
-#pragma unroll
-          for (int k = 0; k < RH; ++k) need_local |= x[k] > mr[k] + kTau;
         } else {
+          ok = false;
+          *abort_flag = 1;
 #pragma unroll
           for (int k = 0; k < RH; ++k) x[k] = -INFINITY;
-          *abort_flag = 1;
         }
-        if (named_bar_sync_or(1, kSoftmaxThreads, need_local || *abort_flag != 0)) {
-          if (named_bar_sync_or(1, kSoftmaxThreads, *abort_flag != 0)) {
-            stop = true;
-            break;
-          }
-          // the reference maxima move, and with them O and the sums
+        // rows' maxima over the tile: over the warp's tokens, then, behind one barrier, over the four warps'
+        {
+          float v[RH];
 #pragma unroll
-          for (int k = 0; k < RH; ++k) {
-            float v = x[k];
+          for (int k = 0; k < RH; ++k) v[k] = warp_max(x[k]);
+          if (lane == 0) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            if (lane == 0) sm->red[q4][RH * h + k] = v;
+            for (int k = 0; k < RH; k += 4)
+              *reinterpret_cast<float4*>(&sm->red[i & 1][q4][RH * h + k]) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
-          named_bar_sync(1, kSoftmaxThreads);
-          if (tid < NR) {
-            const float mprev = sm->mref[tid];
-            const float mnew = fmaxf(mprev, fmaxf(fmaxf(sm->red[0][tid], sm->red[1][tid]), fmaxf(sm->red[2][tid], sm->red[3][tid])));
-            sm->alpha[tid] = (mprev == -INFINITY) ? 1.f : exp2f(mprev - mnew);  // (nothing summed yet, or only NaN)
-            sm->mref[tid] = mnew;
-          }
-          named_bar_sync(1, kSoftmaxThreads);
+        }
+        if (named_bar_sync_or(bar, kHalf, !ok || *abort_flag != 0)) {
+          stop = true;
+          break;
+        }
+        float mx[RH];
+        bool need = false;  // the same in all threads of the half
+#pragma unroll
+        for (int k = 0; k < RH; k += 4) {
+          float4 m4[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) m4[q] = *reinterpret_cast<const float4*>(&sm->red[i & 1][q][RH * h + k]);
+          mx[k] = fmaxf(fmaxf(m4[0].x, m4[1].x), fmaxf(m4[2].x, m4[3].x));
+          mx[k + 1] = fmaxf(fmaxf(m4[0].y, m4[1].y), fmaxf(m4[2].y, m4[3].y));
+          mx[k + 2] = fmaxf(fmaxf(m4[0].z, m4[1].z), fmaxf(m4[2].z, m4[3].z));
+          mx[k + 3] = fmaxf(fmaxf(m4[0].w, m4[1].w), fmaxf(m4[2].w, m4[3].w));
+        }
+#pragma unroll
+        for (int k = 0; k < RH; ++k) need |= mx[k] > mr[k] + kTau;
+        if (need) {  // the reference maxima move, and with them the sums and O
           float al[RH];
 #pragma unroll
           for (int k = 0; k < RH; ++k) {
-            mr[k] = sm->mref[RH * h + k];
-            al[k] = sm->alpha[RH * h + k];
+            const float m = fmaxf(mr[k], mx[k]);
+            al[k] = (mr[k] == -INFINITY) ? 1.f : fast_exp2(mr[k] - m);  // (nothing summed yet, or only NaN)
+            mr[k] = m;
             lsum[k] *= al[k];
           }
           if (tile > w.ta) {  // the value product of the tile before must be complete
-            int ok2 = 1;
-            if (lane == 0) ok2 = mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo);
-            if (__shfl_sync(0xffffffffu, ok2, 0)) {
+            if (__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo))) {
               tc_fence_after();
 #pragma unroll
-              for (int blk = 0; blk < 4 * kTerms; ++blk) {
-                float v[RH];
-                const uint32_t a = tmem + lane_base + C::kTmemO + blk * NR + RH * h;
-                tmem_ld<RH>(a, v);
+              for (int part = 0; part < 4 * kTerms; part += kPieces) {  // kPieces runs of columns in flight at once
+                float v[kPieces][RH];
+                const uint32_t a = tmem + lane_base + C::kTmemO + part * NR + RH * h;
+#pragma unroll
+                for (int blk = 0; blk < kPieces; ++blk) tmem_ld<RH>(a + blk * NR, v[blk]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < RH; ++k) v[k] *= al[k];
-                tmem_st<RH>(a, v);
+                for (int blk = 0; blk < kPieces; ++blk) {
+#pragma unroll
+                  for (int k = 0; k < RH; ++k) v[blk][k] *= al[k];
+                  tmem_st<RH>(a + blk * NR, v[blk]);
+                }
               }
               tmem_wait_st();
-            } else if (lane == 0) {
+            } else {
               *abort_flag = 1;
             }
           }
         }
-        // the weight buffer was last read by the value product of tile i - 2
-        if (i >= 2) {
-          int ok3 = 1;
-          if (lane == 0) ok3 = mbar_wait(&sm->pvdone[i & 1], ((i >> 1) - 1) & 1, tmo);
-          if (!__shfl_sync(0xffffffffu, ok3, 0) && lane == 0) *abort_flag = 1;
-        }
+        // The weight buffer is free: the value product of tile i - 2 read it, and that product had freed the slot
+        // that tile i was then loaded into.
         {
-          const float iz = 1.f / z;
           uint8_t* const pb = smem + C::kOffP + (i & 1) * C::kPBytes + (tl & 15);
 #pragma unroll
           for (int k = 0; k < RH; k += 2) {
@@ -640,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               lsum[k + j] += (wt[j] == 0.f) ? 0.f : wt[j] * iz;  // (a hidden token's scale may be NaN)
             }
             uint32_t t[kTerms];
-            split_terms<kTerms>(wt[0] * w_up, wt[1] * w_up, t);
+            split_f32(wt[0] * w_up, wt[1] * w_up, t);
 #pragma unroll
             for (int n = 0; n < kTerms; ++n)
 #pragma unroll
@@ -654,23 +673,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->pfull[i & 1]);
-        z = z_next;
       }
       // the segment's end: its sums, and O once its last value product is complete
-      if (!stop) {
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) *abort_flag = 1;
-      }
-      if (stop || named_bar_sync_or(1, kSoftmaxThreads, *abort_flag != 0)) break;
+      if (stop) break;
+      const bool ended = mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo);
+      if (!ended) *abort_flag = 1;
 #pragma unroll
       for (int k = 0; k < RH; ++k) {
         float v = lsum[k];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) sm->red[q4][RH * h + k] = v;
+        if (lane == 0) sm->red[(i - 1) & 1][q4][RH * h + k] = v;
       }
-      named_bar_sync(1, kSoftmaxThreads);
+      if (named_bar_sync_or(bar, kHalf, !ended || *abort_flag != 0)) break;
       const bool whole = w.ta == 0 && w.tb == w.n_tiles;
       const long long orow = whole ? static_cast<long long>(w.b) * rows_total + row0 + RH * h
                                    : (static_cast<long long>(gang) * 2 + (w.ta == 0 ? 1 : 0)) * p.row_pad + row0 + RH * h;
@@ -678,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < RH; ++k) {
         const int r = RH * h + k;
-        const float l = (sm->red[0][r] + sm->red[1][r]) + (sm->red[2][r] + sm->red[3][r]);
+        const auto& sum = sm->red[(i - 1) & 1];
+        const float l = (sum[0][r] + sum[1][r]) + (sum[2][r] + sum[3][r]);
         inv[k] = !whole ? w_down : (l == 0.f ? 0.f : w_down / l);  // (no visible token: every weight was 0)
         if (r < nrows && q4 == 0 && lane == 0) {
           if (!whole) {
@@ -719,6 +735,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  // requests with nothing to see
+  for (int b = gang; b < p.B; b += p.gangs) {
+    if (q8_view(p, lens(b)).n != 0) continue;
+    for (int x = tid; x < nrows * (kRank / 4); x += kThreads) {
+      const long long at = static_cast<long long>(b) * rows_total + row0 + x / (kRank / 4);
+      store_out4(p.out, p.out_dtype, at * kRank + 4 * (x % (kRank / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
+      if (x % (kRank / 4) == 0 && p.out_lse != nullptr) p.out_lse[at] = -INFINITY;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -750,7 +775,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_q8_kernel(const Decod
   const int per = (p.B + kMergeThreads - 1) / kMergeThreads;
   const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
   int64_t mine = 0, T = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += q8_tiles(p, b);
+  for (int b = b_lo; b < b_hi; ++b) mine += q8_tiles(q8_view(p, __ldcg(p.context_lens + b)));
   int64_t at = block_prefix<kMergeThreads>(mine, sm.scratch, &T);
   const int64_t J = q8_live_gangs(T, p.gangs);
   pdl_wait();
@@ -762,7 +787,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_q8_kernel(const Decod
     __syncthreads();
     int j0 = 0, j1 = 0;
     if (b_lo + k < b_hi) {
-      const int64_t n = q8_tiles(p, b_lo + k);
+      const int64_t n = q8_tiles(q8_view(p, __ldcg(p.context_lens + b_lo + k)));
       if (n > 0) {
         j0 = q8_gang_of(at, T, J);
         j1 = q8_gang_of(at + n - 1, T, J);

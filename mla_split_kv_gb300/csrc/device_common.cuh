@@ -826,11 +826,27 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
 }
-// the values of two E4M3 bytes (exact)
-__device__ __forceinline__ float2 e4m3x2_values(uint32_t w) {
+// between fp16 and E4M3 (two values in a word)
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+  return h;
+}
+// the values of two E4M3 bytes (exact)
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t w) {
+  const uint32_t h = e4m3x2_to_f16x2(w);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// the maximum over the warp (NaN passed over)
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 // the larger of two, NaN if either is
 __device__ __forceinline__ float max_nan(float a, float b) {

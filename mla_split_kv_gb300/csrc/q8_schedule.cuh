@@ -17,10 +17,19 @@ namespace mla {
 
 constexpr int kQ8Tile = 128;
 
-__device__ __forceinline__ int64_t q8_tiles(const DecodeQ8Params& p, int b) {
-  const WindowView v = window_view(__ldcg(p.context_lens + b), p.q_len, p.bs, p.causal, p.window, p.sinks);
-  return (static_cast<int64_t>(v.n) + kQ8Tile - 1) / kQ8Tile;
+__device__ __forceinline__ WindowView q8_view(const DecodeQ8Params& p, int L) {
+  return window_view(L, p.q_len, p.bs, p.causal, p.window, p.sinks);
 }
+__device__ __forceinline__ int q8_tiles(const WindowView& v) {
+  return static_cast<int>((static_cast<int64_t>(v.n) + kQ8Tile - 1) / kQ8Tile);
+}
+// Context lengths, the first of them kept in shared memory: the walks below read them one after the other.
+constexpr int kQ8Lens = 640;
+struct Q8Lens {
+  const int32_t* global;
+  const int32_t* cached;  // shared memory, kQ8Lens
+  __device__ __forceinline__ int operator()(int b) const { return b < kQ8Lens ? cached[b] : __ldcg(global + b); }
+};
 
 // Gangs that get tiles (all of them unless there are fewer tiles), gang j's first tile, and the gang of tile x.
 __device__ __forceinline__ int64_t q8_live_gangs(int64_t T, int gangs) { return T < gangs ? T : gangs; }
@@ -70,13 +79,13 @@ __device__ __forceinline__ Q8Walk q8_walk(int b0, int64_t off0, int64_t tiles) {
   return w;
 }
 // The next segment; false at the end.
-__device__ __forceinline__ bool q8_next(const DecodeQ8Params& p, Q8Walk& w, bool first) {
+__device__ __forceinline__ bool q8_next(const DecodeQ8Params& p, const Q8Lens& lens, Q8Walk& w, bool first) {
   if (w.left <= 0) return false;
   const int start = first ? w.tb : 0;
   do {
     ++w.b;
-    w.v = window_view(__ldcg(p.context_lens + w.b), p.q_len, p.bs, p.causal, p.window, p.sinks);
-    w.n_tiles = static_cast<int>((static_cast<int64_t>(w.v.n) + kQ8Tile - 1) / kQ8Tile);
+    w.v = q8_view(p, lens(w.b));
+    w.n_tiles = q8_tiles(w.v);
   } while (w.n_tiles == 0);
   w.ta = start;
   w.tb = static_cast<int>(w.n_tiles < start + w.left ? w.n_tiles : start + w.left);
