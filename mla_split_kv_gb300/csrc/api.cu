@@ -963,13 +963,15 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
   p.gangs = mla::q8_gangs(rows, sms);
   p.groups = (rows + nr - 1) / nr;
   p.row_pad = p.groups * nr;
+  p.tile = mla::q8_tile_tokens(rows, d->dtype == MLA_BF16);
   p.ws_o = static_cast<float*>(d->workspace);
   p.ws_ml = p.ws_o + static_cast<uint64_t>(p.gangs) * 2 * p.row_pad * mla::kRank;
   p.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
   CUtensorMap tm_ckv, tm_kpe;
   const uint64_t cache_rows = static_cast<uint64_t>(d->num_blocks) * static_cast<uint64_t>(d->block_size);
-  if (!q8_map(&tm_ckv, ckv_cache, cache_rows, mla::kRank, d->block_size, 5) ||
-      !q8_map(&tm_kpe, kpe_cache, cache_rows, mla::kRope, d->block_size, 6))
+  const uint32_t unit = d->block_size < 32 ? d->block_size : 32;  // rows of a load: a page, or half of one of 64
+  if (!q8_map(&tm_ckv, ckv_cache, cache_rows, mla::kRank, unit, 5) ||
+      !q8_map(&tm_kpe, kpe_cache, cache_rows, mla::kRope, unit, 6))
     return reject(MLA_ERR_CUDA);
   if (mla::launch_decode_q8(tm_ckv, tm_kpe, p, d->dtype == MLA_BF16, static_cast<cudaStream_t>(d->stream)) != cudaSuccess) {
     cudaGetLastError();

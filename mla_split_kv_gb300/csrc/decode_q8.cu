@@ -34,23 +34,20 @@
 //
 // Warp roles (384 threads): warps 0-7 softmax, rescale and output (thread =
 // token; the two warps of a TMEM lane quadrant take half of the rows each),
-// warp 8 MMA issue, warp 9 page loads, warps 10-11 split the queries of the
-// next request while this one's tiles run.
+// warps 8 and 9 issue the score and the value products, warp 10 loads pages,
+// warp 11 splits the queries of the next request while this one's tiles run.
 #include "q8_schedule.cuh"
 
 namespace mla {
 
 namespace {
 
-constexpr int kT = kQ8Tile;                       // tokens per tile
 constexpr int kGroupBytes = 8 * kRank;            // 4 KB: 8 tokens, four swizzled [8 x 128] atoms
-constexpr int kCkvBytes = kT * kRank;             // 64 KB
-constexpr int kTileSlot = kCkvBytes + kT * kRope; // 72 KB
-constexpr int kSlots = 2;
+constexpr int kStep = 32;                         // tokens of an MMA step of the value product
+constexpr int kMaxSlots = 3, kMaxSteps = 4;
 constexpr int kTerms = 3;                         // of a weight
-constexpr int kPre = 2;                           // tiles ahead that are prefetched to L2
 constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kQueryWarp = 10, kQueryWarps = 2;
+constexpr int kScoreWarp = 8, kValueWarp = 9, kLoadWarp = 10, kQueryWarp = 11, kQueryWarps = 1;
 constexpr int kThreads = (kQueryWarp + kQueryWarps) * 32;  // 384
 constexpr float kTermStep = 32.0f, kTermInv = 1.0f / 32.0f;
 // The reference maximum moves when a score passes it by more than this, so weights are at most 2^kTau; times
@@ -68,25 +65,33 @@ struct Cfg {
   static constexpr int kNS = NR * kQTerms, kNP = NR * kTerms;      // N of the two products
   static constexpr int kSBufs = (4 * kNP + 2 * kNS <= 512) ? 2 : 1;  // score buffers in tensor memory
   static constexpr int kQBufs = NR == 16 ? 2 : 1;
+  static constexpr int kT = (NR == 32 && !BF16) ? 128 : 96;  // tokens per tile
+  static constexpr int kSlots = kT == 96 ? 3 : 2, kSteps = kT / kStep;
+  static constexpr uint32_t kCkvBytes = kT * kRank, kTileSlot = kT * kQkDim;
+  // the weights of 16 rows take the place of the tile's rope columns, which only the scores read
+  static constexpr bool kPInSlot = NR == 16;
+  static constexpr int kPre = kSlots;                              // tiles ahead that are prefetched to L2
   static constexpr uint32_t kQChunk = kNS * 128;                   // [kNS x 128 columns], swizzled
   static constexpr uint32_t kQBytes = kNS * kQkDim;                // four chunks, then [kNS x 64] (64-byte swizzle)
-  static constexpr uint32_t kPBytes = kNP * kT;                    // [kNP x 128 tokens], swizzled
+  static constexpr uint32_t kPBytes = kNP * 128;                   // [kNP x 128 tokens], swizzled
   static constexpr uint32_t kOffQ = kSlots * kTileSlot;
   static constexpr uint32_t kOffP = kOffQ + kQBufs * kQBytes;
-  static constexpr uint32_t kOffSmall = kOffP + 2 * kPBytes;
+  static constexpr uint32_t kOffSmall = kOffP + (kPInSlot ? 0 : 2 * kPBytes);
   static constexpr uint32_t kSmem = kOffSmall + kSmallBytes;
   static constexpr uint32_t kTmemO = 0, kTmemS = 4 * kNP;
   static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kQChunk % 1024 == 0, "swizzle atoms stay aligned");
+  static_assert(kTileSlot % 1024 == 0 && kCkvBytes % 1024 == 0 && (!kPInSlot || kPBytes <= kT * kRope), "tile slots");
+  static_assert(kSlots <= kMaxSlots && kSteps <= kMaxSteps, "barriers");
   static_assert(kTmemS + kSBufs * kNS <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
 struct Small {
-  uint64_t full[kSlots], empty[kSlots];  // tile slots
+  uint64_t full[kMaxSlots], empty[kMaxSlots][kMaxSteps];  // tile slots, freed step by step
   uint64_t sfull[2], sfree[2];           // score buffers
-  uint64_t pfull[2], pvdone[2];          // weight buffers
+  uint64_t pfull[kMaxSlots], pvdone[2];  // weights per slot; value products per tile parity
   uint64_t qfull[2], qfree[2], qfirst;   // query buffers
-  uint64_t ofree, drain;
+  uint64_t ofree, drain[2];
   int64_t scratch[33];
   int64_t off0;
   int b0;
@@ -140,8 +145,8 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float* v) {
 
 // NaN bytes of tokens [t0, t1) of a tile to zero: tokens that some row does not see. Its weight for them is 0,
 // and every other byte is finite; for a row that does see one, the score has already made the weight NaN.
-__device__ __forceinline__ void clear_nan_bytes(uint8_t* ckv, int t0, int t1, int tid) {
-  for (int x = tid; x < (t1 - t0) * 32; x += kSoftmaxThreads) {
+__device__ __forceinline__ void clear_nan_bytes(uint8_t* ckv, int t0, int t1, int tid, int nthreads) {
+  for (int x = tid; x < (t1 - t0) * 32; x += nthreads) {
     const int t = t0 + (x >> 5);
     uint4* const at = reinterpret_cast<uint4*>(ckv + (t >> 3) * kGroupBytes + ((x >> 3) & 3) * 1024 + (t & 7) * 128 + (x & 7) * 16);
     uint4 v = *at;
@@ -161,7 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const DecodeQ8Params p) {
   using C = Cfg<NR, BF16>;
   constexpr int RH = NR / 2;  // rows per softmax thread
-  constexpr int kPieces = NR == 16 ? 4 : 2;
+  constexpr int kPieces = 4;
+  constexpr int kT = C::kT, kSlots = C::kSlots, kSteps = C::kSteps, kPre = C::kPre;
+  constexpr uint32_t kCkvBytes = C::kCkvBytes, kTileSlot = C::kTileSlot;
   extern __shared__ uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need it; the size leaves no slack to align it
     if (threadIdx.x == 0) flag_error(MLA_DEVERR_CONFIG);
@@ -175,23 +182,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int row0 = blockIdx.x * NR, nrows = min(NR, rows_total - row0);
 
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kMaxSlots; ++s) {
       mbar_init(&sm->full[s], 1);
-      mbar_init(&sm->empty[s], 1);
+      for (int k = 0; k < kMaxSteps; ++k) mbar_init(&sm->empty[s][k], 1);
+      mbar_init(&sm->pfull[s], kSoftmaxWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&sm->sfull[s], 1);
       mbar_init(&sm->sfree[s], kSoftmaxWarps);
-      mbar_init(&sm->pfull[s], kSoftmaxWarps);
       mbar_init(&sm->pvdone[s], 1);
       mbar_init(&sm->qfull[s], kQueryWarps);
       mbar_init(&sm->qfree[s], 1);
     }
     mbar_init(&sm->qfirst, kFirstWarps);
     mbar_init(&sm->ofree, kSoftmaxWarps);
-    mbar_init(&sm->drain, 1);
+    mbar_init(&sm->drain[0], 1);
+    mbar_init(&sm->drain[1], 1);
     sm->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tmem_alloc(&sm->tmem_base, 512);
     tmem_relinquish();
   }
@@ -210,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int b = b_lo; b < b_hi; ++b) {
     const int L = __ldcg(p.context_lens + b);
     if (b < kQ8Lens) sm->lens[b] = L;
-    mine += q8_tiles(q8_view(p, L));
+    mine += q8_tiles(q8_view(p, L), kT);
   }
   const int64_t prefix = block_prefix<kThreads>(mine, sm->scratch, &T);
   const int64_t J = q8_live_gangs(T, p.gangs);
@@ -220,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t at = prefix;
     int b = b_lo;
     while (true) {
-      const int n = q8_tiles(q8_view(p, lens(b)));
+      const int n = q8_tiles(q8_view(p, lens(b)), kT);
       if (at + n > lo) break;
       at += n;
       ++b;
@@ -305,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   };
   // the first request's queries: all warps that would wait for its scores
-  if (work && warp != kLoadWarp && warp != kMmaWarp) {
+  if (work && (warp < kSoftmaxWarps || warp >= kQueryWarp)) {
     split_rows(sm->b0, 0, warp < kSoftmaxWarps ? warp : warp - kQueryWarp + kSoftmaxWarps, kFirstWarps);
     if (lane == 0) mbar_arrive(&sm->qfirst);
   }
@@ -313,58 +323,68 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ page loads
     const uint64_t pol = l2_policy_evict_first();
-    // the page that this lane loads of a tile (one lane a page): -1 for one outside the pool or the table row
-    // (it reads zeros), -2 for none
-    auto page_of = [&](const Q8Walk& w, int tile) -> int {
-      const int pages = (min(kT, w.v.n - tile * kT) + p.bs - 1) / p.bs;
-      if (lane >= pages) return -2;
-      int pg = tile * (kT / p.bs) + lane;
-      if (pg >= w.v.sa / p.bs) pg += w.v.skip / p.bs;
-      const int pid = pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
-      return (pid >= 0 && pid < p.num_blocks) ? pid : -1;
+    // One lane a unit of a tile: a page, or half of one of 64 tokens, so that a unit lies within a step.
+    const int unit = min(p.bs, kStep), per_step = kStep / unit, units = kT / unit;
+    // the table's entry for this lane's unit (looked at when it is used: its load has a tile's time)
+    auto entry_of = [&](const Q8Walk& w, int tile) -> int {
+      const int u = tile * kT + lane * unit;
+      if (lane >= units || u >= w.v.n) return -1;
+      const int pg = u / p.bs + (u >= w.v.sa ? w.v.skip / p.bs : 0);
+      return pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
     };
-    // a walk that runs ahead: its page numbers wait in registers until their tile's prefetch and load
+    // a walk that runs ahead: its entries wait in registers until their tile's prefetch and load
     Q8Walk a = w;
-    bool a_live = q8_next(p, lens, a, true);
+    bool a_live = q8_next<kT>(p, lens, a, true);
     int a_tile = a.ta;
-    auto ahead = [&]() -> int {
-      if (!a_live) return -2;
-      const int pid = page_of(a, a_tile);
+    struct Ahead {
+      int entry, sub, count;  // this lane's entry and first row in its page; units of the tile
+    };
+    auto ahead = [&]() -> Ahead {
+      if (!a_live) return Ahead{-1, 0, 0};
+      const Ahead r{entry_of(a, a_tile), (a_tile * kT + lane * unit) & (p.bs - 1), (min(kT, a.v.n - a_tile * kT) + unit - 1) / unit};
       if (++a_tile == a.tb) {
-        a_live = q8_next(p, lens, a, false);
+        a_live = q8_next<kT>(p, lens, a, false);
         a_tile = a.ta;
       }
-      return pid;
+      return r;
     };
-    int ring[kPre + 2];
+    Ahead ring[kPre + 2];
 #pragma unroll
     for (int j = 0; j < kPre + 2; ++j) ring[j] = ahead();
     int issued = -1;
-    for (int i = 0; i < N; ++i) {
-      const int s = i & 1;
-      if (i >= kSlots) {
-        int ok = 1;
-        if (lane == 0) {
-          ok = mbar_wait(&sm->empty[s], ((i >> 1) - 1) & 1, tmo) && !*abort_flag;
-          if (!ok) *abort_flag = 1;
-        }
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    bool stop = false;
+    for (int i = 0; i < N && !stop; ++i) {
+      const int s = i % kSlots;
+      // an entry outside the pool or the table row reads zeros
+      int pid = ring[0].entry;
+      if (lane < ring[0].count && (pid < 0 || pid >= p.num_blocks)) {
+        flag_error(MLA_DEVERR_BAD_PAGE);
+        pid = -1;
       }
-      const int pid = ring[0];
-      if (pid == -1) flag_error(MLA_DEVERR_BAD_PAGE);
-      const int pages = __popc(__ballot_sync(0xffffffffu, pid != -2));
-      if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>(pages * p.bs * kQkDim));
-      __syncwarp();
-      if (pid != -2) {
-        uint8_t* slot = smem + s * kTileSlot;
-        tma_load_4d(slot + lane * p.bs * kRank, &tm_ckv, 0, 0, 0, pid * (p.bs / 8), &sm->full[s], pol);
-        tma_load_2d(slot + kCkvBytes + lane * p.bs * kRope, &tm_kpe, 0, pid * p.bs, &sm->full[s], pol);
+      uint8_t* const slot = smem + s * kTileSlot;
+#pragma unroll 1
+      for (int k = 0; k < kSteps; ++k) {
+        // the value product of tile i - kSlots has read this step. (Given up, the tile's other loads are issued all the
+        // same, so that its barrier completes.)
+        if (i >= kSlots && !stop) {
+          stop = !__all_sync(0xffffffffu, mbar_wait(&sm->empty[s][k], (i / kSlots - 1) & 1, tmo) && !*abort_flag);
+          if (stop) *abort_flag = 1;
+        }
+        if (k == 0) {
+          if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>(ring[0].count * unit * kQkDim));
+          __syncwarp();
+        }
+        const int row = pid * p.bs + (pid < 0 ? 0 : ring[0].sub);
+        if (lane < ring[0].count && lane / per_step == k)
+          tma_load_4d(slot + lane * unit * kRank, &tm_ckv, 0, 0, 0, row / 8, &sm->full[s], pol);
+        if (lane < ring[0].count && (C::kPInSlot ? k == kSteps - 1 : lane / per_step == k))
+          tma_load_2d(slot + kCkvBytes + lane * unit * kRope, &tm_kpe, 0, row, &sm->full[s], pol);
       }
       issued = i;
-      if (ring[kPre] >= 0) {
-        const long long row = static_cast<long long>(ring[kPre]) * p.bs;
-        bulk_prefetch_l2(p.ckv + row * kRank, static_cast<uint32_t>(p.bs * kRank));
-        bulk_prefetch_l2(p.kpe + row * kRope, static_cast<uint32_t>(p.bs * kRope));
+      if (lane < ring[kPre].count && ring[kPre].entry >= 0 && ring[kPre].entry < p.num_blocks) {
+        const long long row = static_cast<long long>(ring[kPre].entry) * p.bs + ring[kPre].sub;
+        bulk_prefetch_l2(p.ckv + row * kRank, static_cast<uint32_t>(unit * kRank));
+        bulk_prefetch_l2(p.kpe + row * kRope, static_cast<uint32_t>(unit * kRope));
       }
 #pragma unroll
       for (int j = 0; j <= kPre; ++j) ring[j] = ring[j + 1];
@@ -372,119 +392,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // after an abort, loads in flight land before shared memory is released
     if (lane == 0 && *abort_flag)
-      for (int t = max(0, issued - (kSlots - 1)); t <= issued; ++t) mbar_wait(&sm->full[t & 1], (t >> 1) & 1, kDrainTimeoutNs);
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMA issue
-    constexpr uint32_t idesc_s = idesc_e4m3_f32(128, C::kNS, false, false);
-    constexpr uint32_t idesc_o = idesc_e4m3_f32(128, C::kNP, true, false);
+      for (int t = max(0, issued - (kSlots - 1)); t <= issued; ++t) mbar_wait(&sm->full[t % kSlots], (t / kSlots) & 1, kDrainTimeoutNs);
+  } else if (warp == kScoreWarp) {
+    // ------------------------------------------------------------------ score products
+    // One thread issues them in tile order as tiles land, another one the value products: each waits for its
+    // own inputs only, and its issue (some 60 cycles an MMA) overlaps the other's waits.
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, C::kNS, false, false);
     const uint32_t base = smem_u32(smem);
-    auto score = [&](int i, int qbuf, bool last) {
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t slot = base + (i & 1) * kTileSlot, q = base + C::kOffQ + qbuf * C::kQBytes;
-        const Desc2 ad = desc2(smem_desc_sw128(slot, 16, kGroupBytes)), ak = desc2(smem_desc_sw64(slot + kCkvBytes, 512));
+    if (lane == 0) {
+      int i = 0;
+      bool first = true, ok = true;
+      for (int seg = 0; ok && q8_next<kT>(p, lens, w, first); ++seg, first = false) {
+        const uint32_t q = base + C::kOffQ + (seg % C::kQBufs) * C::kQBytes;
         const Desc2 bd = desc2(smem_desc_sw128(q, 16, 1024)), bk = desc2(smem_desc_sw64(q + 4 * C::kQChunk, 512));
-        const uint32_t d = tmem + C::kTmemS + (i % C::kSBufs) * C::kNS;
+        ok = seg == 0 ? mbar_wait(&sm->qfirst, 0, tmo) : mbar_wait(&sm->qfull[seg & 1], ((seg - 1) >> 1) & 1, tmo);
+        for (int tile = w.ta; ok && tile < w.tb; ++tile, ++i) {
+          ok = mbar_wait(&sm->full[i % kSlots], (i / kSlots) & 1, tmo) &&
+               (i < C::kSBufs || mbar_wait(&sm->sfree[i % C::kSBufs], (i / C::kSBufs - 1) & 1, tmo)) && !*abort_flag;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t slot = base + (i % kSlots) * kTileSlot;
+          const Desc2 ad = desc2(smem_desc_sw128(slot, 16, kGroupBytes)), ak = desc2(smem_desc_sw64(slot + kCkvBytes, 512));
+          const uint32_t d = tmem + C::kTmemS + (i % C::kSBufs) * C::kNS;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma8_ss(d, ad, (c * 1024 + kk * 32) >> 4, bd, (c * C::kQChunk + kk * 32) >> 4, idesc_s, (c | kk) != 0 ? 1u : 0u);
-        umma8_ss(d, ak, 0, bk, 0, idesc_s, 1u);
-        umma8_ss(d, ak, 32 >> 4, bk, 32 >> 4, idesc_s, 1u);
-        umma_commit(&sm->sfull[i % C::kSBufs]);
-        if (last) umma_commit(&sm->qfree[qbuf]);
-      }
-      __syncwarp();
-    };
-    auto pv = [&](int i, int ksteps, bool first) {
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t slot = base + (i & 1) * kTileSlot;
-        const Desc2 pb = desc2(smem_desc_sw128(base + C::kOffP + (i & 1) * C::kPBytes, 16, 1024));
-        const Desc2 a0 = desc2(smem_desc_sw128(slot, 1024, kGroupBytes));
-#pragma unroll
-        for (int ks = 0; ks < kT / 32; ++ks) {
-          if (ks < ksteps) {
-#pragma unroll
-            for (int blk = 0; blk < 4; ++blk)
-              umma8_ss(tmem + C::kTmemO + blk * C::kNP, a0, (blk * 1024 + ks * 4 * kGroupBytes) >> 4, pb, (ks * 32) >> 4,
-                       idesc_o, (first && ks == 0) ? 0u : 1u);
-          }
+            for (int kk = 0; kk < 4; ++kk)
+              umma8_ss(d, ad, (c * 1024 + kk * 32) >> 4, bd, (c * C::kQChunk + kk * 32) >> 4, idesc, (c | kk) != 0 ? 1u : 0u);
+          umma8_ss(d, ak, 0, bk, 0, idesc, 1u);
+          umma8_ss(d, ak, 32 >> 4, bk, 32 >> 4, idesc, 1u);
+          umma_commit(&sm->sfull[i % C::kSBufs]);
+          if (tile + 1 == w.tb) umma_commit(&sm->qfree[seg % C::kQBufs]);
         }
-        umma_commit(&sm->empty[i & 1]);
-        umma_commit(&sm->pvdone[i & 1]);
       }
-      __syncwarp();
-    };
-    // Issue as the inputs get ready, each product in tile order: the value product of tile np once its weights
-    // are written (it frees a slot), else the scores of tile ns. Nothing ready for longer than the wait limit
-    // (or an abort elsewhere) ends it.
-    Q8Walk a = w, b = w;  // of the scores, of the value products
-    int ns = 0, np = 0, a_seg = 0, b_seg = 0, a_tile = 0, b_tile = 0;
-    if (N > 0) {
-      q8_next(p, lens, a, true);
-      q8_next(p, lens, b, true);
-      a_tile = a.ta;
-      b_tile = b.ta;
+      if (!ok) *abort_flag = 1;
+      umma_commit(&sm->drain[0]);  // every MMA issued has completed before TMEM is freed
+      mbar_wait(&sm->drain[0], 0, kDrainTimeoutNs);
     }
-    bool idle = false;
-    uint64_t idle_t0 = 0;
-    while (np < N) {
-      int act = 0;
-      if (lane == 0) {
-        if (np < ns && mbar_test(&sm->pfull[np & 1], (np >> 1) & 1) &&
-            (b_tile != b.ta || b_seg == 0 || mbar_test(&sm->ofree, (b_seg - 1) & 1))) {
-          act = 2;
-        } else if (ns < N && mbar_test(&sm->full[ns & 1], (ns >> 1) & 1) &&
-                   (ns < C::kSBufs || mbar_test(&sm->sfree[ns % C::kSBufs], (ns / C::kSBufs - 1) & 1)) &&
-                   (a_tile != a.ta || (a_seg == 0 ? mbar_test(&sm->qfirst, 0) : mbar_test(&sm->qfull[a_seg & 1], ((a_seg - 1) >> 1) & 1)))) {
-          act = 1;
-        } else if (*abort_flag) {
-          act = -1;
-        } else {
-          const uint64_t now = globaltimer_ns();
-          if (!idle) {
-            idle = true;
-            idle_t0 = now;
-          } else if (now - idle_t0 > tmo) {
-            act = -1;
-            *abort_flag = 1;
-            flag_error(MLA_DEVERR_TIMEOUT);
+    __syncwarp();
+  } else if (warp == kValueWarp) {
+    // ------------------------------------------------------------------ value products
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, C::kNP, true, false);
+    const uint32_t base = smem_u32(smem);
+    if (lane == 0) {
+      int i = 0;
+      bool first = true, ok = true;
+      for (int seg = 0; ok && q8_next<kT>(p, lens, w, first); ++seg, first = false) {
+        if (seg > 0) ok = mbar_wait(&sm->ofree, (seg - 1) & 1, tmo);  // the last segment's O has been read
+        for (int tile = w.ta; ok && tile < w.tb; ++tile, ++i) {
+          ok = mbar_wait(&sm->pfull[i % kSlots], (i / kSlots) & 1, tmo) && !*abort_flag;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t slot = base + (i % kSlots) * kTileSlot;
+          const Desc2 pb = desc2(smem_desc_sw128(C::kPInSlot ? slot + kCkvBytes : base + C::kOffP + (i & 1) * C::kPBytes, 16, 1024));
+          const Desc2 a0 = desc2(smem_desc_sw128(slot, 1024, kGroupBytes));
+          const int ksteps = (min(kT, w.v.n - tile * kT) + kStep - 1) / kStep;
+#pragma unroll
+          for (int ks = 0; ks < kSteps; ++ks) {
+            if (ks < ksteps) {
+#pragma unroll
+              for (int blk = 0; blk < 4; ++blk)
+                umma8_ss(tmem + C::kTmemO + blk * C::kNP, a0, (blk * 1024 + ks * 4 * kGroupBytes) >> 4, pb, (ks * 32) >> 4, idesc,
+                         (tile == w.ta && ks == 0) ? 0u : 1u);
+            }
+            umma_commit(&sm->empty[i % kSlots][ks]);
           }
+          umma_commit(&sm->pvdone[i & 1]);
         }
-        if (act > 0) idle = false;
       }
-      act = __shfl_sync(0xffffffffu, act, 0);
-      if (act == 2) {
-        pv(np, (min(kT, b.v.n - b_tile * kT) + 31) >> 5, b_tile == b.ta);
-        ++np;
-        if (++b_tile == b.tb && np < N) {
-          q8_next(p, lens, b, false);
-          b_tile = b.ta;
-          ++b_seg;
-        }
-      } else if (act == 1) {
-        score(ns, a_seg % C::kQBufs, a_tile + 1 == a.tb);
-        ++ns;
-        if (++a_tile == a.tb && ns < N) {
-          q8_next(p, lens, a, false);
-          a_tile = a.ta;
-          ++a_seg;
-        }
-      } else if (act < 0) {
-        break;
-      }
-    }
-    if (lane == 0) {  // every MMA issued so far has completed before TMEM is freed
-      umma_commit(&sm->drain);
-      mbar_wait(&sm->drain, 0, kDrainTimeoutNs);
+      if (!ok) *abort_flag = 1;
+      umma_commit(&sm->drain[1]);
+      mbar_wait(&sm->drain[1], 0, kDrainTimeoutNs);
     }
     __syncwarp();
   } else if (warp >= kQueryWarp) {
     // ------------------------------------------------------------------ the next requests' queries to terms
-    bool more = q8_next(p, lens, w, true);
-    for (int seg = 1; more && (more = q8_next(p, lens, w, false)); ++seg) {
+    bool more = q8_next<kT>(p, lens, w, true);
+    for (int seg = 1; more && (more = q8_next<kT>(p, lens, w, false)); ++seg) {
       if (seg >= C::kQBufs) {  // the request whose place they take has its scores
         int ok = 1;
         if (lane == 0) {
@@ -501,25 +485,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q4 = warp & 3, h = warp >> 2;
     const int tl = 32 * q4 + lane;  // this thread's token of each tile, and latent column of each block of O
     const uint32_t lane_base = static_cast<uint32_t>(32 * q4) << 16;
+    const bool has_tokens = 32 * q4 < kT;  // (a 96-token tile leaves the last quadrant's warps without)
     const uint32_t bar = 1 + h, kHalf = kSoftmaxThreads / 2;  // the four warps of a row half meet by themselves
     const float w_up = static_cast<float>(1 << kWeightExp), w_down = 1.0f / w_up;
     // this thread's page of a tile, and its token's scale there: loads a tile ahead of their use each, so
     // neither looks at what it loaded
     auto page_at = [&](const Q8Walk& w, int tile) -> int {
-      if (tl >= w.v.n - tile * kT) return -1;
+      if (tl >= min(kT, w.v.n - tile * kT)) return -1;
       const int u = tile * kT + tl;
       const int pg = u / p.bs + (u >= w.v.sa ? w.v.skip / p.bs : 0);
       return pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
     };
-    auto scale_at = [&](int pid) -> float {  // 1 where there is no page
+    auto scale_at = [&](int pid, int tile) -> float {  // 1 where there is no page
       if (pid < 0 || pid >= p.num_blocks) return 1.f;
-      const long long row = static_cast<long long>(pid) * p.bs + (tl & (p.bs - 1));
+      const long long row = static_cast<long long>(pid) * p.bs + ((tile * kT + tl) & (p.bs - 1));
       return __ldg(p.scales + (row >> p.g_shift));
     };
     int i = 0;  // tile count
     bool first = true;
-    for (int seg = 0; q8_next(p, lens, w, first); ++seg, first = false) {
-      float z_raw = scale_at(page_at(w, w.ta));
+    for (int seg = 0; q8_next<kT>(p, lens, w, first); ++seg, first = false) {
+      float z_raw = scale_at(page_at(w, w.ta), w.ta);
       int pid = w.ta + 1 < w.tb ? page_at(w, w.ta + 1) : -1;
       float lsum[RH], mr[RH];
 #pragma unroll
@@ -536,13 +521,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // NaN for a scale that is neither NaN nor in range
         const float z = (z_raw >= 0x1p-60f && z_raw <= 0x1p60f) ? z_raw : __uint_as_float(0x7fc00000u);
         const float lz = log2f(z), iz = 1.f / z;
-        z_raw = tile + 1 < w.tb ? scale_at(pid) : 1.f;
+        z_raw = tile + 1 < w.tb ? scale_at(pid, tile + 1) : 1.f;
         pid = tile + 2 < w.tb ? page_at(w, tile + 2) : -1;
         const int sb = i % C::kSBufs;
         bool ok = mbar_wait(&sm->sfull[sb], (i / C::kSBufs) & 1, tmo);
         float x[RH];
         const int u0 = tile * kT, nvalid = min(kT, w.v.n - u0);
-        if (__all_sync(0xffffffffu, ok)) {
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && has_tokens) {
           tc_fence_after();
           float t2[RH], t3[RH];
           const uint32_t sa = tmem + lane_base + C::kTmemS + sb * C::kNS + RH * h;
@@ -573,15 +559,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // tokens that some row does not see: below the last row's window, behind the first row, and the
             // rest of the tail's last step
-            uint8_t* const slot = smem + (i & 1) * kTileSlot;
+            uint8_t* const slot = smem + (i % kSlots) * kTileSlot;
             const int a0 = min(kT, max(0, p.sinks - u0)), a1 = min(kT, low_last + 1 - u0);
             const int b0 = max(0, min(kT, min(w.v.n, pos_first + 1) - u0)), b1 = (nvalid + 31) & ~31;
-            if (a0 < a1) clear_nan_bytes(slot, a0, a1, tid);
-            if (b0 < b1) clear_nan_bytes(slot, b0, b1, tid);
+            if (a0 < a1) clear_nan_bytes(slot, a0, a1, h * kT + tl, 2 * kT);
+            if (b0 < b1) clear_nan_bytes(slot, b0, b1, h * kT + tl, 2 * kT);
           }
         } else {
-          ok = false;
-          *abort_flag = 1;
+          if (!ok) *abort_flag = 1;
+          if (lane == 0) mbar_arrive(&sm->sfree[sb]);
 #pragma unroll
           for (int k = 0; k < RH; ++k) x[k] = -INFINITY;
         }
@@ -614,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < RH; ++k) need |= mx[k] > mr[k] + kTau;
+        float al[RH];
         if (need) {  // the reference maxima move, and with them the sums and O
-          float al[RH];
 #pragma unroll
           for (int k = 0; k < RH; ++k) {
             const float m = fmaxf(mr[k], mx[k]);
@@ -623,33 +609,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mr[k] = m;
             lsum[k] *= al[k];
           }
-          if (tile > w.ta) {  // the value product of the tile before must be complete
-            if (__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo))) {
-              tc_fence_after();
-#pragma unroll
-              for (int part = 0; part < 4 * kTerms; part += kPieces) {  // kPieces runs of columns in flight at once
-                float v[kPieces][RH];
-                const uint32_t a = tmem + lane_base + C::kTmemO + part * NR + RH * h;
-#pragma unroll
-                for (int blk = 0; blk < kPieces; ++blk) tmem_ld<RH>(a + blk * NR, v[blk]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int blk = 0; blk < kPieces; ++blk) {
-#pragma unroll
-                  for (int k = 0; k < RH; ++k) v[blk][k] *= al[k];
-                  tmem_st<RH>(a + blk * NR, v[blk]);
-                }
-              }
-              tmem_wait_st();
-            } else {
-              *abort_flag = 1;
-            }
-          }
         }
-        // The weight buffer is free: the value product of tile i - 2 read it, and that product had freed the slot
-        // that tile i was then loaded into.
-        {
-          uint8_t* const pb = smem + C::kOffP + (i & 1) * C::kPBytes + (tl & 15);
+        // Weights in the slot: its rope columns have been read. In a buffer of their own: the value product of
+        // tile i - 2 has to have read it, which with two slots the load of tile i waited for.
+        if (!C::kPInSlot && kSlots > 2 && i >= 2 &&
+            !__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[i & 1], ((i >> 1) - 1) & 1, tmo)))
+          *abort_flag = 1;
+        if (has_tokens) {
+          uint8_t* const pb = smem + (C::kPInSlot ? (i % kSlots) * kTileSlot + kCkvBytes : C::kOffP + (i & 1) * C::kPBytes) + (tl & 15);
 #pragma unroll
           for (int k = 0; k < RH; k += 2) {
             float wt[2];
@@ -670,9 +637,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
         }
+        if (need && tile > w.ta) {  // O: the value product of the tile before must be complete
+          if (__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo))) {
+            tc_fence_after();
+#pragma unroll
+            for (int part = 0; part < 4 * kTerms; part += kPieces) {  // kPieces runs of columns in flight at once
+              float v[kPieces][RH];
+              const uint32_t a = tmem + lane_base + C::kTmemO + part * NR + RH * h;
+#pragma unroll
+              for (int blk = 0; blk < kPieces; ++blk) tmem_ld<RH>(a + blk * NR, v[blk]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int blk = 0; blk < kPieces; ++blk) {
+#pragma unroll
+                for (int k = 0; k < RH; ++k) v[blk][k] *= al[k];
+                tmem_st<RH>(a + blk * NR, v[blk]);
+              }
+            }
+            tmem_wait_st();
+          } else {
+            *abort_flag = 1;
+          }
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->pfull[i & 1]);
+        if (lane == 0) mbar_arrive(&sm->pfull[i % kSlots]);
       }
       // the segment's end: its sums, and O once its last value product is complete
       if (stop) break;
@@ -746,28 +735,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-// The requests cut by gang borders: per (request, row, 64 columns) the parts of its gangs,
+// The requests cut by gang borders: per (request, row) the parts of its gangs,
 //   M = max m_j, w_j = 2^(m_j - M), out = sum w_j O_j / sum w_j l_j, lse = M + log2 sum w_j l_j.
-// 16 column quads x 8 part lanes a block; lane e adds parts e, e + 8, ... in order, then the lanes'
-// sums are added in lane order: the same bits on every call.
-constexpr int kMergeThreads = 128, kMergeLanes = 8, kMergeCols = 64;
-constexpr int kMergeLoads = 10;  // parts a lane has in flight: 80 gangs in a round
+// A warp takes 128 columns of a row with one lane a column quad where a request has at most kFewParts parts
+// (a batch: two or three), and 16 columns with eight part lanes where it has more (one long request: as many
+// as there are gangs): every lane's loads of a round in flight at once either way. Lane sums are added in a
+// fixed tree: the same bits on every call.
+constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32;
+constexpr int kFewParts = 8, kPartLanes = 8;
+constexpr int kMergeLoads = 10;     // parts a lane has in flight with part lanes: 80 gangs in a round
+constexpr int kMergeBlocks = 4;     // per SM: one wave, each block takes items in strides
+
+// a part's weight: one without a visible token has l = 0; one whose every score is NaN has no maximum, and l NaN
+__device__ __forceinline__ float part_weight(float2 ml, float ref) {
+  return ml.y == 0.f ? 0.f : (ml.x == -INFINITY ? 1.f : exp2f(ml.x - ref));
+}
+__device__ __forceinline__ void fma4(float4& acc, float w, const float4 v) {
+  acc.x = fmaf(w, v.x, acc.x);
+  acc.y = fmaf(w, v.y, acc.y);
+  acc.z = fmaf(w, v.z, acc.z);
+  acc.w = fmaf(w, v.w, acc.w);
+}
 
 struct MergeSmem {
   int64_t scratch[33];
-  int cut[kMergeThreads / 32];
+  int cut[kMergeWarps];
   int b[kMergeThreads], j0[kMergeThreads], n[kMergeThreads];
-  float4 acc[kMergeLanes][kMergeCols / 4];
-  float den[kMergeLanes], max[kMergeLanes];
+  int64_t first[kMergeThreads + 1];  // items before each
 };
 
-__global__ void __launch_bounds__(kMergeThreads) mla_merge_q8_kernel(const DecodeQ8Params p) {
+__global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_kernel(const DecodeQ8Params p) {
   __shared__ MergeSmem sm;
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -775,19 +778,20 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_q8_kernel(const Decod
   const int per = (p.B + kMergeThreads - 1) / kMergeThreads;
   const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
   int64_t mine = 0, T = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += q8_tiles(q8_view(p, __ldcg(p.context_lens + b)));
+  for (int b = b_lo; b < b_hi; ++b) mine += q8_tiles(q8_view(p, __ldcg(p.context_lens + b)), p.tile);
   int64_t at = block_prefix<kMergeThreads>(mine, sm.scratch, &T);
   const int64_t J = q8_live_gangs(T, p.gangs);
-  pdl_wait();
-  if (J < 2) return;
+  if (J < 2) {
+    pdl_wait();
+    return;
+  }
   const int rows_total = p.q_len * p.H;
-  const int q = tid % (kMergeCols / 4), e = tid / (kMergeCols / 4);
+  bool waited = false;
   // requests are taken in rounds of those that the threads' next ones are
   for (int k = 0; k < per; ++k) {
-    __syncthreads();
     int j0 = 0, j1 = 0;
     if (b_lo + k < b_hi) {
-      const int64_t n = q8_tiles(q8_view(p, __ldcg(p.context_lens + b_lo + k)));
+      const int n = q8_tiles(q8_view(p, __ldcg(p.context_lens + b_lo + k)), p.tile);
       if (n > 0) {
         j0 = q8_gang_of(at, T, J);
         j1 = q8_gang_of(at + n - 1, T, J);
@@ -797,10 +801,12 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_q8_kernel(const Decod
     // the cut ones among them, in thread order: the same list in every block
     const uint32_t cut = __ballot_sync(0xffffffffu, j1 > j0);
     if (lane == 0) sm.cut[warp] = __popc(cut);
-    __syncthreads();
+    const int64_t items_mine = j1 > j0 ? static_cast<int64_t>(rows_total) * (kRank / (j1 - j0 < kFewParts ? 128 : 16)) : 0;
+    int64_t items = 0;
+    const int64_t before = block_prefix<kMergeThreads>(items_mine, sm.scratch, &items);  // (two barriers)
     int count = 0, mine_at = __popc(cut & ((1u << lane) - 1u));
 #pragma unroll
-    for (int w = 0; w < kMergeThreads / 32; ++w) {
+    for (int w = 0; w < kMergeWarps; ++w) {
       if (w < warp) mine_at += sm.cut[w];
       count += sm.cut[w];
     }
@@ -808,78 +814,102 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_q8_kernel(const Decod
       sm.b[mine_at] = b_lo + k;
       sm.j0[mine_at] = j0;
       sm.n[mine_at] = j1 - j0 + 1;
+      sm.first[mine_at] = before;
     }
     __syncthreads();
-    const long long items = static_cast<long long>(count) * rows_total * (kRank / kMergeCols);
-    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-      const int c = static_cast<int>(item % (kRank / kMergeCols)) * kMergeCols + 4 * q;
-      const long long rest = item / (kRank / kMergeCols);
-      const int row = static_cast<int>(rest % rows_total), i = static_cast<int>(rest / rows_total);
-      const int b = sm.b[i], j0 = sm.j0[i], n = sm.n[i];
-      // part x of the request: gang j0 + x, entry 1 of the first gang, entry 0 of the others
-      auto slot = [&](int x) { return (static_cast<long long>(j0 + x) * 2 + (x == 0 ? 1 : 0)) * p.row_pad + row; };
+    if (!waited) pdl_wait();
+    waited = true;
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp; item < items;
+         item += static_cast<int64_t>(gridDim.x) * kMergeWarps) {
+      int i = 0;  // the last of the list that starts at or before the item
+      for (int step = kMergeThreads / 2; step > 0; step >>= 1)
+        if (i + step < count && sm.first[i + step] <= item) i += step;
+      const int b = sm.b[i], g0 = sm.j0[i], n = sm.n[i];
+      const int rest = static_cast<int>(item - sm.first[i]);
+      // part x of the request: gang g0 + x, entry 1 of the first gang, entry 0 of the others
+      auto slot = [&](int x, int row) { return (static_cast<long long>(g0 + x) * 2 + (x == 0 ? 1 : 0)) * p.row_pad + row; };
       float M = -INFINITY, den = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x0 = 0; x0 < n; x0 += kMergeLanes * kMergeLoads) {
-        float2 ml[kMergeLoads];
-        float4 v[kMergeLoads];
+      int row, c;
+      bool writes = true;
+      if (n <= kFewParts) {
+        row = rest >> 2;
+        c = (rest & 3) * 128 + 4 * lane;
+        float2 ml[kFewParts];
+        float4 v[kFewParts];
 #pragma unroll
-        for (int y = 0; y < kMergeLoads; ++y) {
-          const int x = x0 + e + kMergeLanes * y;
-          const bool in = x < n;
-          ml[y] = in ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml + slot(x) * 2)) : make_float2(-INFINITY, 0.f);
-          v[y] = in ? __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(x) * kRank + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < kFewParts; ++x) {
+          ml[x] = make_float2(-INFINITY, 0.f);
+          if (x < n) {
+            ml[x] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + slot(x, row) * 2));
+            v[x] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(x, row) * kRank + c));
+          }
         }
-        float m = M;
 #pragma unroll
-        for (int y = 0; y < kMergeLoads; ++y) m = fmaxf(m, ml[y].x);
-        const float ref = m == -INFINITY ? 0.f : m;
-        const float al = exp2f(M - ref);  // 0 before the first round
-        den *= al;
-        acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
-        M = m;
+        for (int x = 0; x < kFewParts; ++x) M = fmaxf(M, ml[x].x);
+        const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
-        for (int y = 0; y < kMergeLoads; ++y) {
-          // a part without a visible token has l = 0; one whose every score is NaN has no maximum, and l NaN
-          const float w = ml[y].y == 0.f ? 0.f : (ml[y].x == -INFINITY ? 1.f : exp2f(ml[y].x - ref));
-          den = fmaf(w, ml[y].y, den);
-          acc.x = fmaf(w, v[y].x, acc.x);
-          acc.y = fmaf(w, v[y].y, acc.y);
-          acc.z = fmaf(w, v[y].z, acc.z);
-          acc.w = fmaf(w, v[y].w, acc.w);
+        for (int x = 0; x < kFewParts; ++x) {
+          if (x < n) {
+            const float w = part_weight(ml[x], ref);
+            den = fmaf(w, ml[x].y, den);
+            fma4(acc, w, v[x]);
+          }
         }
+      } else {
+        row = rest >> 5;
+        const int e = lane >> 2;
+        c = (rest & 31) * 16 + 4 * (lane & 3);
+        for (int x0 = 0; x0 < n; x0 += kPartLanes * kMergeLoads) {
+          float2 ml[kMergeLoads];
+          float4 v[kMergeLoads];
+#pragma unroll
+          for (int y = 0; y < kMergeLoads; ++y) {
+            const int x = x0 + e + kPartLanes * y;
+            ml[y] = make_float2(-INFINITY, 0.f);
+            v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < n) {
+              ml[y] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + slot(x, row) * 2));
+              v[y] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(x, row) * kRank + c));
+            }
+          }
+          float m = M;
+#pragma unroll
+          for (int y = 0; y < kMergeLoads; ++y) m = fmaxf(m, ml[y].x);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          const float ref = m == -INFINITY ? 0.f : m;
+          const float al = M == -INFINITY ? 1.f : exp2f(M - ref);  // (nothing summed before the first, or only NaN)
+          den *= al;
+          acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
+          M = m;
+#pragma unroll
+          for (int y = 0; y < kMergeLoads; ++y) {
+            const float w = part_weight(ml[y], ref);
+            den = fmaf(w, ml[y].y, den);
+            fma4(acc, w, v[y]);
+          }
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          den += __shfl_xor_sync(0xffffffffu, den, o);
+          acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+          acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+          acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+          acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+        }
+        writes = e == 0;
       }
-      __syncthreads();
-      sm.acc[e][q] = acc;
-      if (q == 0) {
-        sm.den[e] = den;
-        sm.max[e] = M;
-      }
-      __syncthreads();
-      if (e == 0) {
-        float Mt = -INFINITY;
-#pragma unroll
-        for (int y = 0; y < kMergeLanes; ++y) Mt = fmaxf(Mt, sm.max[y]);
-        const float ref = Mt == -INFINITY ? 0.f : Mt;
-        float dt = 0.f;
-        float4 at4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int y = 0; y < kMergeLanes; ++y) {
-          const float w = sm.den[y] == 0.f ? 0.f : (sm.max[y] == -INFINITY ? 1.f : exp2f(sm.max[y] - ref));
-          const float4 v = sm.acc[y][q];
-          dt = fmaf(w, sm.den[y], dt);
-          at4.x = fmaf(w, v.x, at4.x);
-          at4.y = fmaf(w, v.y, at4.y);
-          at4.z = fmaf(w, v.z, at4.z);
-          at4.w = fmaf(w, v.w, at4.w);
-        }
+      if (writes) {
         const long long br = static_cast<long long>(b) * rows_total + row;
-        const bool none = dt == 0.f;
-        store_out4(p.out, p.out_dtype, br * kRank + c,
-                   none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(at4.x / dt, at4.y / dt, at4.z / dt, at4.w / dt));
-        if (p.out_lse != nullptr && c == 0 && q == 0) p.out_lse[br] = none ? -INFINITY : ref + log2f(dt);
+        const bool none = den == 0.f;
+        const float inv = none ? 0.f : 1.f / den;
+        store_out4(p.out, p.out_dtype, br * kRank + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        if (p.out_lse != nullptr && c == 0) p.out_lse[br] = none ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(den);
       }
     }
+    __syncthreads();
   }
 }
 
@@ -897,6 +927,10 @@ cudaError_t launch(cudaLaunchConfig_t cfg, const CUtensorMap& tm_ckv, const CUte
 }  // namespace
 
 int q8_rows_per_cta(int total_rows) { return total_rows <= 16 ? 16 : 32; }
+int q8_tile_tokens(int total_rows, bool bf16) {
+  if (q8_rows_per_cta(total_rows) == 16) return bf16 ? Cfg<16, true>::kT : Cfg<16, false>::kT;
+  return bf16 ? Cfg<32, true>::kT : Cfg<32, false>::kT;
+}
 int q8_gangs(int total_rows, int sms) {
   const int nr = q8_rows_per_cta(total_rows), groups = (total_rows + nr - 1) / nr;
   return sms > groups ? sms / groups : 1;
@@ -917,7 +951,12 @@ cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kp
   else
     e = bf16 ? launch<32, true>(cfg, tm_ckv, tm_kpe, p) : launch<32, false>(cfg, tm_ckv, tm_kpe, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(2 * 152, 1, 1);
+  // one warp an item, for as many requests as gang borders can cut
+  const int64_t cuts = p.B < p.gangs ? p.B : p.gangs;
+  const int64_t items = cuts * p.q_len * p.H * (p.gangs > kFewParts && p.B < p.gangs ? kRank / 16 : kRank / 128);
+  const int64_t blocks = (items + kMergeWarps - 1) / kMergeWarps;
+  const int64_t wave = static_cast<int64_t>(kMergeBlocks) * p.gangs * p.groups;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < wave ? blocks : wave), 1, 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, mla_merge_q8_kernel, p);

@@ -1,7 +1,7 @@
 // How the tiles of a batch are shared out by the block-scaled 8-bit decode and
 // found again by its merge.
 //
-// The batch's visible runs, cut into tiles of 128 tokens request after request,
+// The batch's visible runs, cut into tiles of p.tile tokens request after request,
 // are one line of T tiles. Gang j of J takes tiles [jT/J, (j+1)T/J) of it (one
 // CTA of a gang per row group), so every gang works on the same number of tiles
 // whatever the lengths, and lengths are read where they lie: no host plan, and
@@ -15,13 +15,11 @@
 
 namespace mla {
 
-constexpr int kQ8Tile = 128;
-
 __device__ __forceinline__ WindowView q8_view(const DecodeQ8Params& p, int L) {
   return window_view(L, p.q_len, p.bs, p.causal, p.window, p.sinks);
 }
-__device__ __forceinline__ int q8_tiles(const WindowView& v) {
-  return static_cast<int>((static_cast<int64_t>(v.n) + kQ8Tile - 1) / kQ8Tile);
+__device__ __forceinline__ int q8_tiles(const WindowView& v, int tile) {
+  return v.n / tile + (v.n % tile != 0 ? 1 : 0);
 }
 // Context lengths, the first of them kept in shared memory: the walks below read them one after the other.
 constexpr int kQ8Lens = 640;
@@ -79,13 +77,14 @@ __device__ __forceinline__ Q8Walk q8_walk(int b0, int64_t off0, int64_t tiles) {
   return w;
 }
 // The next segment; false at the end.
+template <int kT>
 __device__ __forceinline__ bool q8_next(const DecodeQ8Params& p, const Q8Lens& lens, Q8Walk& w, bool first) {
   if (w.left <= 0) return false;
   const int start = first ? w.tb : 0;
   do {
     ++w.b;
     w.v = q8_view(p, lens(w.b));
-    w.n_tiles = q8_tiles(w.v);
+    w.n_tiles = q8_tiles(w.v, kT);
   } while (w.n_tiles == 0);
   w.ta = start;
   w.tb = static_cast<int>(w.n_tiles < start + w.left ? w.n_tiles : start + w.left);
