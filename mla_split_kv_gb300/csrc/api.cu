@@ -952,6 +952,7 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
   p.H = d->num_heads;
   p.q_len = d->q_len;
   p.bs = d->block_size;
+  p.bs_shift = d->block_size == 16 ? 4 : (d->block_size == 32 ? 5 : 6);
   p.max_blocks = d->max_blocks_per_req;
   p.num_blocks = d->num_blocks;
   p.g_shift = 0;

@@ -45,43 +45,46 @@ namespace {
 constexpr int kGroupBytes = 8 * kRank;            // 4 KB: 8 tokens, four swizzled [8 x 128] atoms
 constexpr int kStep = 32;                         // tokens of an MMA step of the value product
 constexpr int kMaxSlots = 3, kMaxSteps = 4;
-constexpr int kTerms = 3;                         // of a weight
-constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kScoreWarp = 8, kValueWarp = 9, kLoadWarp = 10, kQueryWarp = 11, kQueryWarps = 1;
-constexpr int kThreads = (kQueryWarp + kQueryWarps) * 32;  // 384
+constexpr int RH = 8;                             // rows per softmax thread
 constexpr float kTermStep = 32.0f, kTermInv = 1.0f / 32.0f;
-// The reference maximum moves when a score passes it by more than this, so weights are at most 2^kTau; times
-// 2^kWeightExp they fit E4M3's 448, and its subnormals reach down to 2^-25 of the reference in the third term.
-constexpr float kTau = 2.0f;
-constexpr int kWeightExp = 6;
-constexpr int kFirstWarps = kSoftmaxWarps + kQueryWarps;  // that split the first request's queries
 constexpr int kSums = 4;                          // row factors kept: queries split ahead of their softmax
 
 constexpr uint32_t kSmallBytes = 5120;
 
 template <int NR, bool BF16>
 struct Cfg {
-  static constexpr int kQTerms = BF16 ? 2 : 3;
+  // terms of a query, of a weight. Four for the weights of 16 rows: 64 columns take the MMA no longer than 48.
+  static constexpr int kQTerms = BF16 ? 2 : 3, kTerms = NR == 16 ? 4 : 3;
+  // The reference maximum moves when a score passes it by more than kTau, so weights are at most 2^kTau; times
+  // 2^kWeightExp they fit E4M3's 448, and its subnormals reach down to 2^-25 of the reference in the last term.
+  static constexpr float kTau = NR == 16 ? 7.0f : 2.0f;
+  static constexpr int kWeightExp = NR == 16 ? 1 : 6;
   static constexpr int kNS = NR * kQTerms, kNP = NR * kTerms;      // N of the two products
   static constexpr int kSBufs = (4 * kNP + 2 * kNS <= 512) ? 2 : 1;  // score buffers in tensor memory
   static constexpr int kQBufs = NR == 16 ? 2 : 1;
-  static constexpr int kT = (NR == 32 && !BF16) ? 128 : 96;  // tokens per tile
+  static constexpr int kT = (NR == 32 && !BF16) ? 128 : 96;        // tokens per tile
   static constexpr int kSlots = kT == 96 ? 3 : 2, kSteps = kT / kStep;
   static constexpr uint32_t kCkvBytes = kT * kRank, kTileSlot = kT * kQkDim;
-  // the weights of 16 rows take the place of the tile's rope columns, which only the scores read
-  static constexpr bool kPInSlot = NR == 16;
   static constexpr int kPre = kSlots;                              // tiles ahead that are prefetched to L2
   static constexpr uint32_t kQChunk = kNS * 128;                   // [kNS x 128 columns], swizzled
   static constexpr uint32_t kQBytes = kNS * kQkDim;                // four chunks, then [kNS x 64] (64-byte swizzle)
-  static constexpr uint32_t kPBytes = kNP * 128;                   // [kNP x 128 tokens], swizzled
+  // Weights: [kT tokens x kNP] bytes, rows of 64 or 128 with the swizzle of that width (the value product reads
+  // them N-major, so a thread stores its token's rows as words). Those of 16 rows take the place of the tile's
+  // rope columns, which only the scores read; those of 32 have kPBufs buffers of their own.
+  static constexpr bool kPInSlot = NR == 16;
+  static constexpr uint32_t kPRow = kNP <= 64 ? 64 : 128, kPBytes = kT * kPRow;
+  static constexpr int kPBufs = kPInSlot ? 0 : (BF16 ? 2 : 1);
   static constexpr uint32_t kOffQ = kSlots * kTileSlot;
   static constexpr uint32_t kOffP = kOffQ + kQBufs * kQBytes;
-  static constexpr uint32_t kOffSmall = kOffP + (kPInSlot ? 0 : 2 * kPBytes);
+  static constexpr uint32_t kOffSmall = kOffP + kPBufs * kPBytes;
   static constexpr uint32_t kSmem = kOffSmall + kSmallBytes;
   static constexpr uint32_t kTmemO = 0, kTmemS = 4 * kNP;
+  // warps
+  static constexpr int kSoftmaxWarps = NR / RH * 4, kScoreWarp = kSoftmaxWarps, kValueWarp = kScoreWarp + 1;
+  static constexpr int kLoadWarp = kValueWarp + 1, kQueryWarp = kLoadWarp + 1, kThreads = (kQueryWarp + 1) * 32;
   static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kQChunk % 1024 == 0, "swizzle atoms stay aligned");
   static_assert(kTileSlot % 1024 == 0 && kCkvBytes % 1024 == 0 && (!kPInSlot || kPBytes <= kT * kRope), "tile slots");
-  static_assert(kSlots <= kMaxSlots && kSteps <= kMaxSteps, "barriers");
+  static_assert(kSlots <= kMaxSlots && kSteps <= kMaxSteps && kNP <= static_cast<int>(kPRow), "layouts");
   static_assert(kTmemS + kSBufs * kNS <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
@@ -120,27 +123,12 @@ __device__ __forceinline__ void split_f16(uint32_t x, uint32_t* t) {
   }
 }
 // The same for fp32 values: the first term and what it leaves in fp32, the rest of that (11 bits of it) in fp16.
+template <int N>
 __device__ __forceinline__ void split_f32(float a, float b, uint32_t* t) {
   t[0] = e4m3x2(a, b);
   const float2 v = e4m3x2_values(t[0]);
   const __half2 rest = __hmul2(__floats2half2_rn(a - v.x, b - v.y), __float2half2_rn(kTermStep));
-  split_f16<kTerms - 1>(*reinterpret_cast<const uint32_t*>(&rest), t + 1);
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t a, float* v) {
-  static_assert(N == 8 || N == 16, "");
-  if constexpr (N == 8)
-    tmem_ld8(a, v);
-  else
-    tmem_ld16(a, v);
-}
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t a, const float* v) {
-  if constexpr (N == 8)
-    tmem_st8(a, v);
-  else
-    tmem_st16(a, v);
+  split_f16<N - 1>(*reinterpret_cast<const uint32_t*>(&rest), t + 1);
 }
 
 // NaN bytes of tokens [t0, t1) of a tile to zero: tokens that some row does not see. Its weight for them is 0,
@@ -161,12 +149,11 @@ __device__ __forceinline__ void clear_nan_bytes(uint8_t* ckv, int t0, int t1, in
 }
 
 template <int NR, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     mla_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_ckv, const __grid_constant__ CUtensorMap tm_kpe,
                          const DecodeQ8Params p) {
   using C = Cfg<NR, BF16>;
-  constexpr int RH = NR / 2;  // rows per softmax thread
-  constexpr int kPieces = 4;
+  constexpr int kTerms = C::kTerms, kThreads = C::kThreads, kSoftmaxWarps = C::kSoftmaxWarps;
   constexpr int kT = C::kT, kSlots = C::kSlots, kSteps = C::kSteps, kPre = C::kPre;
   constexpr uint32_t kCkvBytes = C::kCkvBytes, kTileSlot = C::kTileSlot;
   extern __shared__ uint8_t smem[];
@@ -191,21 +178,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm->sfull[s], 1);
       mbar_init(&sm->sfree[s], kSoftmaxWarps);
       mbar_init(&sm->pvdone[s], 1);
-      mbar_init(&sm->qfull[s], kQueryWarps);
+      mbar_init(&sm->qfull[s], 1);
       mbar_init(&sm->qfree[s], 1);
     }
-    mbar_init(&sm->qfirst, kFirstWarps);
+    mbar_init(&sm->qfirst, kSoftmaxWarps + 1);
     mbar_init(&sm->ofree, kSoftmaxWarps);
     mbar_init(&sm->drain[0], 1);
     mbar_init(&sm->drain[1], 1);
     sm->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kScoreWarp) {
+  if (warp == C::kScoreWarp) {
     tmem_alloc(&sm->tmem_base, 512);
     tmem_relinquish();
   }
-  if (warp == kLoadWarp && lane == 0) {
+  if (warp == C::kLoadWarp && lane == 0) {
     tma_prefetch_desc(&tm_ckv);
     tma_prefetch_desc(&tm_kpe);
   }
@@ -315,21 +302,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   };
   // the first request's queries: all warps that would wait for its scores
-  if (work && (warp < kSoftmaxWarps || warp >= kQueryWarp)) {
-    split_rows(sm->b0, 0, warp < kSoftmaxWarps ? warp : warp - kQueryWarp + kSoftmaxWarps, kFirstWarps);
+  if (work && (warp < kSoftmaxWarps || warp >= C::kQueryWarp)) {
+    split_rows(sm->b0, 0, warp < kSoftmaxWarps ? warp : kSoftmaxWarps, kSoftmaxWarps + 1);
     if (lane == 0) mbar_arrive(&sm->qfirst);
   }
 
-  if (warp == kLoadWarp) {
+  if (warp == C::kLoadWarp) {
     // ------------------------------------------------------------------ page loads
     const uint64_t pol = l2_policy_evict_first();
     // One lane a unit of a tile: a page, or half of one of 64 tokens, so that a unit lies within a step.
-    const int unit = min(p.bs, kStep), per_step = kStep / unit, units = kT / unit;
+    const int unit_shift = min(p.bs_shift, 5), unit = 1 << unit_shift;
+    const int my_step = lane >> (5 - unit_shift);  // 32-token step of this lane's unit
+    const int tok = lane << unit_shift;            // its first token in the tile
     // the table's entry for this lane's unit (looked at when it is used: its load has a tile's time)
     auto entry_of = [&](const Q8Walk& w, int tile) -> int {
-      const int u = tile * kT + lane * unit;
-      if (lane >= units || u >= w.v.n) return -1;
-      const int pg = u / p.bs + (u >= w.v.sa ? w.v.skip / p.bs : 0);
+      const int u = tile * kT + tok;
+      if (tok >= kT || u >= w.v.n) return -1;
+      const int pg = (u >> p.bs_shift) + (u >= w.v.sa ? w.v.skip >> p.bs_shift : 0);
       return pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
     };
     // a walk that runs ahead: its entries wait in registers until their tile's prefetch and load
@@ -341,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto ahead = [&]() -> Ahead {
       if (!a_live) return Ahead{-1, 0, 0};
-      const Ahead r{entry_of(a, a_tile), (a_tile * kT + lane * unit) & (p.bs - 1), (min(kT, a.v.n - a_tile * kT) + unit - 1) / unit};
+      const Ahead r{entry_of(a, a_tile), (a_tile * kT + tok) & (p.bs - 1), (min(kT, a.v.n - a_tile * kT) + unit - 1) >> unit_shift};
       if (++a_tile == a.tb) {
         a_live = q8_next<kT>(p, lens, a, false);
         a_tile = a.ta;
@@ -362,27 +351,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         pid = -1;
       }
       uint8_t* const slot = smem + s * kTileSlot;
+      const int row = (pid << p.bs_shift) + (pid < 0 ? 0 : ring[0].sub);
+      const bool mine = lane < ring[0].count;
+      auto load_ckv = [&]() { tma_load_4d(slot + tok * kRank, &tm_ckv, 0, 0, 0, row >> 3, &sm->full[s], pol); };
+      auto load_kpe = [&]() { tma_load_2d(slot + kCkvBytes + tok * kRope, &tm_kpe, 0, row, &sm->full[s], pol); };
+      auto expect = [&]() {
+        if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>((ring[0].count << unit_shift) * kQkDim));
+        __syncwarp();
+      };
+      const uint32_t parity = (i / kSlots - 1) & 1;
+      if (i < kSlots || __all_sync(0xffffffffu, mbar_test(&sm->empty[s][kSteps - 1], parity))) {  // the whole slot is free
+        expect();
+        if (mine) {
+          load_ckv();
+          load_kpe();
+        }
+      } else {
+        // As the value product of tile i - kSlots has read its steps; the rope columns, where the weights are now,
+        // behind the last one. (Given up, the loads are issued all the same, so that the barrier completes.)
 #pragma unroll 1
-      for (int k = 0; k < kSteps; ++k) {
-        // the value product of tile i - kSlots has read this step. (Given up, the tile's other loads are issued all the
-        // same, so that its barrier completes.)
-        if (i >= kSlots && !stop) {
-          stop = !__all_sync(0xffffffffu, mbar_wait(&sm->empty[s][k], (i / kSlots - 1) & 1, tmo) && !*abort_flag);
-          if (stop) *abort_flag = 1;
+        for (int k = 0; k < kSteps; ++k) {
+          if (!stop) stop = !__all_sync(0xffffffffu, mbar_wait(&sm->empty[s][k], parity, tmo) && !*abort_flag);
+          if (k == 0) expect();
+          if (mine && my_step == k) load_ckv();
         }
-        if (k == 0) {
-          if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>(ring[0].count * unit * kQkDim));
-          __syncwarp();
-        }
-        const int row = pid * p.bs + (pid < 0 ? 0 : ring[0].sub);
-        if (lane < ring[0].count && lane / per_step == k)
-          tma_load_4d(slot + lane * unit * kRank, &tm_ckv, 0, 0, 0, row / 8, &sm->full[s], pol);
-        if (lane < ring[0].count && (C::kPInSlot ? k == kSteps - 1 : lane / per_step == k))
-          tma_load_2d(slot + kCkvBytes + lane * unit * kRope, &tm_kpe, 0, row, &sm->full[s], pol);
+        if (mine) load_kpe();
+        if (stop) *abort_flag = 1;
       }
       issued = i;
       if (lane < ring[kPre].count && ring[kPre].entry >= 0 && ring[kPre].entry < p.num_blocks) {
-        const long long row = static_cast<long long>(ring[kPre].entry) * p.bs + ring[kPre].sub;
+        const long long row = (static_cast<long long>(ring[kPre].entry) << p.bs_shift) + ring[kPre].sub;
         bulk_prefetch_l2(p.ckv + row * kRank, static_cast<uint32_t>(unit * kRank));
         bulk_prefetch_l2(p.kpe + row * kRope, static_cast<uint32_t>(unit * kRope));
       }
@@ -393,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after an abort, loads in flight land before shared memory is released
     if (lane == 0 && *abort_flag)
       for (int t = max(0, issued - (kSlots - 1)); t <= issued; ++t) mbar_wait(&sm->full[t % kSlots], (t / kSlots) & 1, kDrainTimeoutNs);
-  } else if (warp == kScoreWarp) {
+  } else if (warp == C::kScoreWarp) {
     // ------------------------------------------------------------------ score products
     // One thread issues them in tile order as tiles land, another one the value products: each waits for its
     // own inputs only, and its issue (some 60 cycles an MMA) overlaps the other's waits.
@@ -430,9 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&sm->drain[0], 0, kDrainTimeoutNs);
     }
     __syncwarp();
-  } else if (warp == kValueWarp) {
+  } else if (warp == C::kValueWarp) {
     // ------------------------------------------------------------------ value products
-    constexpr uint32_t idesc = idesc_e4m3_f32(128, C::kNP, true, false);
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, C::kNP, true, true);
     const uint32_t base = smem_u32(smem);
     if (lane == 0) {
       int i = 0;
@@ -444,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t slot = base + (i % kSlots) * kTileSlot;
-          const Desc2 pb = desc2(smem_desc_sw128(C::kPInSlot ? slot + kCkvBytes : base + C::kOffP + (i & 1) * C::kPBytes, 16, 1024));
+          const uint32_t wts = C::kPInSlot ? slot + kCkvBytes : base + C::kOffP + (i % (C::kPBufs > 0 ? C::kPBufs : 1)) * C::kPBytes;
+          const Desc2 pb = desc2(C::kPRow == 64 ? smem_desc_sw64(wts, 512) : smem_desc_sw128(wts, 16, 1024));
           const Desc2 a0 = desc2(smem_desc_sw128(slot, 1024, kGroupBytes));
           const int ksteps = (min(kT, w.v.n - tile * kT) + kStep - 1) / kStep;
 #pragma unroll
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ks < ksteps) {
 #pragma unroll
               for (int blk = 0; blk < 4; ++blk)
-                umma8_ss(tmem + C::kTmemO + blk * C::kNP, a0, (blk * 1024 + ks * 4 * kGroupBytes) >> 4, pb, (ks * 32) >> 4, idesc,
+                umma8_ss(tmem + C::kTmemO + blk * C::kNP, a0, (blk * 1024 + ks * 4 * kGroupBytes) >> 4, pb, (ks * kStep * C::kPRow) >> 4, idesc,
                          (tile == w.ta && ks == 0) ? 0u : 1u);
             }
             umma_commit(&sm->empty[i % kSlots][ks]);
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&sm->drain[1], 0, kDrainTimeoutNs);
     }
     __syncwarp();
-  } else if (warp >= kQueryWarp) {
+  } else if (warp >= C::kQueryWarp) {
     // ------------------------------------------------------------------ the next requests' queries to terms
     bool more = q8_next<kT>(p, lens, w, true);
     for (int seg = 1; more && (more = q8_next<kT>(p, lens, w, false)); ++seg) {
@@ -477,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       }
-      split_rows(w.b, seg, warp - kQueryWarp, kQueryWarps);
+      split_rows(w.b, seg, 0, 1);
       if (lane == 0) mbar_arrive(&sm->qfull[seg & 1]);
     }
   } else {
@@ -486,19 +485,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tl = 32 * q4 + lane;  // this thread's token of each tile, and latent column of each block of O
     const uint32_t lane_base = static_cast<uint32_t>(32 * q4) << 16;
     const bool has_tokens = 32 * q4 < kT;  // (a 96-token tile leaves the last quadrant's warps without)
-    const uint32_t bar = 1 + h, kHalf = kSoftmaxThreads / 2;  // the four warps of a row half meet by themselves
-    const float w_up = static_cast<float>(1 << kWeightExp), w_down = 1.0f / w_up;
+    const uint32_t bar = 1 + h;  // the four warps of a run of rows meet by themselves
+    constexpr uint32_t kMeet = 128;
+    constexpr float w_up = static_cast<float>(1 << C::kWeightExp), w_down = 1.0f / w_up;
     // this thread's page of a tile, and its token's scale there: loads a tile ahead of their use each, so
     // neither looks at what it loaded
     auto page_at = [&](const Q8Walk& w, int tile) -> int {
       if (tl >= min(kT, w.v.n - tile * kT)) return -1;
       const int u = tile * kT + tl;
-      const int pg = u / p.bs + (u >= w.v.sa ? w.v.skip / p.bs : 0);
+      const int pg = (u >> p.bs_shift) + (u >= w.v.sa ? w.v.skip >> p.bs_shift : 0);
       return pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
     };
     auto scale_at = [&](int pid, int tile) -> float {  // 1 where there is no page
       if (pid < 0 || pid >= p.num_blocks) return 1.f;
-      const long long row = static_cast<long long>(pid) * p.bs + ((tile * kT + tl) & (p.bs - 1));
+      const long long row = (static_cast<long long>(pid) << p.bs_shift) + ((tile * kT + tl) & (p.bs - 1));
       return __ldg(p.scales + (row >> p.g_shift));
     };
     int i = 0;  // tile count
@@ -532,9 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           float t2[RH], t3[RH];
           const uint32_t sa = tmem + lane_base + C::kTmemS + sb * C::kNS + RH * h;
-          tmem_ld<RH>(sa, x);
-          tmem_ld<RH>(sa + NR, t2);
-          if constexpr (C::kQTerms == 3) tmem_ld<RH>(sa + 2 * NR, t3);
+          tmem_ld8(sa, x);
+          tmem_ld8(sa + NR, t2);
+          if constexpr (C::kQTerms == 3) tmem_ld8(sa + 2 * NR, t3);
           float factor[RH];
 #pragma unroll
           for (int k = 0; k < RH; k += 4)
@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* const slot = smem + (i % kSlots) * kTileSlot;
             const int a0 = min(kT, max(0, p.sinks - u0)), a1 = min(kT, low_last + 1 - u0);
             const int b0 = max(0, min(kT, min(w.v.n, pos_first + 1) - u0)), b1 = (nvalid + 31) & ~31;
-            if (a0 < a1) clear_nan_bytes(slot, a0, a1, h * kT + tl, 2 * kT);
-            if (b0 < b1) clear_nan_bytes(slot, b0, b1, h * kT + tl, 2 * kT);
+            if (a0 < a1) clear_nan_bytes(slot, a0, a1, h * kT + tl, NR / RH * kT);
+            if (b0 < b1) clear_nan_bytes(slot, b0, b1, h * kT + tl, NR / RH * kT);
           }
         } else {
           if (!ok) *abort_flag = 1;
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<float4*>(&sm->red[i & 1][q4][RH * h + k]) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
         }
-        if (named_bar_sync_or(bar, kHalf, !ok || *abort_flag != 0)) {
+        if (named_bar_sync_or(bar, kMeet, !ok || *abort_flag != 0)) {
           stop = true;
           break;
         }
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx[k + 3] = fmaxf(fmaxf(m4[0].w, m4[1].w), fmaxf(m4[2].w, m4[3].w));
         }
 #pragma unroll
-        for (int k = 0; k < RH; ++k) need |= mx[k] > mr[k] + kTau;
+        for (int k = 0; k < RH; ++k) need |= mx[k] > mr[k] + C::kTau;
         float al[RH];
         if (need) {  // the reference maxima move, and with them the sums and O
 #pragma unroll
@@ -610,13 +610,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             lsum[k] *= al[k];
           }
         }
-        // Weights in the slot: its rope columns have been read. In a buffer of their own: the value product of
-        // tile i - 2 has to have read it, which with two slots the load of tile i waited for.
-        if (!C::kPInSlot && kSlots > 2 && i >= 2 &&
-            !__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[i & 1], ((i >> 1) - 1) & 1, tmo)))
-          *abort_flag = 1;
+        // Weights in the slot: its rope columns have been read. In a buffer of their own: the value product that
+        // read it last has to be done.
+        if (!C::kPInSlot && i >= C::kPBufs) {
+          const int j = i - C::kPBufs;
+          if (!__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[j & 1], (j >> 1) & 1, tmo))) *abort_flag = 1;
+        }
         if (has_tokens) {
-          uint8_t* const pb = smem + (C::kPInSlot ? (i % kSlots) * kTileSlot + kCkvBytes : C::kOffP + (i & 1) * C::kPBytes) + (tl & 15);
+          uint32_t word[kTerms][RH / 4];
 #pragma unroll
           for (int k = 0; k < RH; k += 2) {
             float wt[2];
@@ -626,32 +627,36 @@ __global__ void __launch_bounds__(kThreads, 1)
               lsum[k + j] += (wt[j] == 0.f) ? 0.f : wt[j] * iz;  // (a hidden token's scale may be NaN)
             }
             uint32_t t[kTerms];
-            split_f32(wt[0] * w_up, wt[1] * w_up, t);
+            split_f32<kTerms>(wt[0] * w_up, wt[1] * w_up, t);
 #pragma unroll
-            for (int n = 0; n < kTerms; ++n)
+            for (int n = 0; n < kTerms; ++n) word[n][k / 4] = (k & 2) ? word[n][k / 4] | (t[n] << 16) : t[n];
+          }
+          uint8_t* const pb = smem + (C::kPInSlot ? (i % kSlots) * kTileSlot + kCkvBytes
+                                                  : C::kOffP + (i % (C::kPBufs > 0 ? C::kPBufs : 1)) * C::kPBytes);
+          // columns n * NR + 8 h .. + 7 of this token's row: half of one 16-byte piece
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int row = n * NR + RH * h + k + j;
-                pb[row * 128 + ((((tl >> 4) ^ row) & 7) << 4)] = static_cast<uint8_t>(t[n] >> (8 * j));
-              }
+          for (int n = 0; n < kTerms; ++n) {
+            const int piece = (n * NR + RH * h) >> 4;
+            const int at = C::kPRow == 64 ? tl * 64 + ((piece ^ (tl >> 1)) & 3) * 16 : tl * 128 + ((piece ^ tl) & 7) * 16;
+            *reinterpret_cast<uint2*>(pb + at + (h & 1) * 8) = make_uint2(word[n][0], word[n][1]);
           }
           fence_proxy_async_smem();
         }
         if (need && tile > w.ta) {  // O: the value product of the tile before must be complete
           if (__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo))) {
             tc_fence_after();
+#pragma unroll 1
+            for (int blk = 0; blk < 4; ++blk) {
+              float v[kTerms][RH];
+              const uint32_t a = tmem + lane_base + C::kTmemO + blk * C::kNP + RH * h;
 #pragma unroll
-            for (int part = 0; part < 4 * kTerms; part += kPieces) {  // kPieces runs of columns in flight at once
-              float v[kPieces][RH];
-              const uint32_t a = tmem + lane_base + C::kTmemO + part * NR + RH * h;
-#pragma unroll
-              for (int blk = 0; blk < kPieces; ++blk) tmem_ld<RH>(a + blk * NR, v[blk]);
+              for (int n = 0; n < kTerms; ++n) tmem_ld8(a + n * NR, v[n]);
               tmem_wait_ld();
 #pragma unroll
-              for (int blk = 0; blk < kPieces; ++blk) {
+              for (int n = 0; n < kTerms; ++n) {
 #pragma unroll
-                for (int k = 0; k < RH; ++k) v[blk][k] *= al[k];
-                tmem_st<RH>(a + blk * NR, v[blk]);
+                for (int k = 0; k < RH; ++k) v[n][k] *= al[k];
+                tmem_st8(a + n * NR, v[n]);
               }
             }
             tmem_wait_st();
@@ -674,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane == 0) sm->red[(i - 1) & 1][q4][RH * h + k] = v;
       }
-      if (named_bar_sync_or(bar, kHalf, !ended || *abort_flag != 0)) break;
+      if (named_bar_sync_or(bar, kMeet, !ended || *abort_flag != 0)) break;
       const bool whole = w.ta == 0 && w.tb == w.n_tiles;
       const long long orow = whole ? static_cast<long long>(w.b) * rows_total + row0 + RH * h
                                    : (static_cast<long long>(gang) * 2 + (w.ta == 0 ? 1 : 0)) * p.row_pad + row0 + RH * h;
@@ -695,13 +700,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int blk = 0; blk < 4; ++blk) {
-        float o1[RH], o2[RH], o3[RH];
+        float o[kTerms][RH];
         const uint32_t a = tmem + lane_base + C::kTmemO + blk * C::kNP + RH * h;
-        tmem_ld<RH>(a, o1);
-        tmem_ld<RH>(a + NR, o2);
-        tmem_ld<RH>(a + 2 * NR, o3);
+#pragma unroll
+        for (int n = 0; n < kTerms; ++n) tmem_ld8(a + n * NR, o[n]);
         tmem_wait_ld();
         if (blk == 3) {
           tc_fence_before();
@@ -711,14 +715,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < RH; ++k) {
           if (RH * h + k < nrows) {
-            const float o = fmaf(fmaf(o3[k], kTermInv, o2[k]), kTermInv, o1[k]) * inv[k];
+            float v = o[kTerms - 1][k];
+#pragma unroll
+            for (int n = kTerms - 2; n >= 0; --n) v = fmaf(v, kTermInv, o[n][k]);
+            v *= inv[k];
             const long long off = (orow + k) * kRank + blk * 128 + tl;
             if (!whole)
-              p.ws_o[off] = o;
+              p.ws_o[off] = v;
             else if (p.out_dtype == 2)
-              static_cast<float*>(p.out)[off] = o;
+              static_cast<float*>(p.out)[off] = v;
             else
-              static_cast<uint16_t*>(p.out)[off] = p.out_dtype == 1 ? f2h<true>(o) : f2h<false>(o);
+              static_cast<uint16_t*>(p.out)[off] = p.out_dtype == 1 ? f2h<true>(v) : f2h<false>(v);
           }
         }
       }
@@ -735,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kScoreWarp) {
+  if (warp == C::kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -749,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // fixed tree: the same bits on every call.
 constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32;
 constexpr int kFewParts = 8, kPartLanes = 8;
-constexpr int kMergeLoads = 10;     // parts a lane has in flight with part lanes: 80 gangs in a round
+constexpr int kMergeLoads = 8;      // parts a lane has in flight with part lanes: 64 gangs in a round
 constexpr int kMergeBlocks = 4;     // per SM: one wave, each block takes items in strides
 
 // a part's weight: one without a visible token has l = 0; one whose every score is NaN has no maximum, and l NaN
@@ -919,7 +926,7 @@ cudaError_t launch(cudaLaunchConfig_t cfg, const CUtensorMap& tm_ckv, const CUte
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR, BF16>::kSmem);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(p.groups), static_cast<unsigned>(p.gangs), 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(Cfg<NR, BF16>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg<NR, BF16>::kSmem;
   return cudaLaunchKernelEx(&cfg, mla_decode_q8_kernel<NR, BF16>, tm_ckv, tm_kpe, p);
 }
