@@ -210,9 +210,9 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     mine += q8_tiles(q8_view(p, L), kT);
   }
   const int64_t prefix = block_prefix<kThreads>(mine, sm->scratch, &T);
-  const int64_t J = q8_live_gangs(T, p.gangs);
-  const bool work = gang < J;
-  const int64_t lo = work ? q8_gang_begin(gang, T, J) : 0, hi = work ? q8_gang_begin(gang + 1, T, J) : 0;
+  const Q8Line line = q8_line(T, p.gangs);
+  const bool work = gang < line.gangs;
+  const int64_t lo = work ? line.begin(gang) : 0, hi = work ? line.begin(gang + 1) : 0;
   if (work && lo >= prefix && lo < prefix + mine) {
     int64_t at = prefix;
     int b = b_lo;
@@ -287,24 +287,32 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       }
     }
   };
-  // rows r0, r0 + step, ... of request b, two at a time
-  auto split_rows = [&](int b, int seg, int r0, int step) {
+  // The queries: the first request's by all warps that would wait for its scores, each further one's by the query
+  // warp while its predecessor's tiles run.
+  if (work && (warp < kSoftmaxWarps || warp == C::kQueryWarp)) {
+    Q8Walk a = w;
+    q8_next<kT>(p, lens, a, true);
+    for (int seg = 0;; ++seg) {
+      if (seg >= C::kQBufs) {  // the request whose place they take has its scores
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm->qfree[seg % C::kQBufs], (seg / C::kQBufs - 1) & 1, tmo) && !*abort_flag)) {
+          *abort_flag = 1;
+          break;
+        }
+      }
+      const int step = seg == 0 ? kSoftmaxWarps + 1 : 1;
+      int r = seg == 0 ? (warp < kSoftmaxWarps ? warp : kSoftmaxWarps) : 0;
+      QueryRow next = load_query(a.b, r);
 #pragma unroll 1
-    for (int r = r0; r < NR; r += 2 * step) {
-      const bool two = r + step < NR;
-      const QueryRow q0 = load_query(b, r);
-      QueryRow q1 = q0;
-      if (two) q1 = load_query(b, r + step);
-      split_query(q0, seg, r);
-      if (two) split_query(q1, seg, r + step);
+      for (; r < NR; r += step) {
+        const QueryRow row = next;
+        next = load_query(a.b, r + step);  // (past the last: zeros)
+        split_query(row, seg, r);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(seg == 0 ? &sm->qfirst : &sm->qfull[seg & 1]);
+      if (warp < kSoftmaxWarps || !q8_next<kT>(p, lens, a, false)) break;
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-  };
-  // the first request's queries: all warps that would wait for its scores
-  if (work && (warp < kSoftmaxWarps || warp >= C::kQueryWarp)) {
-    split_rows(sm->b0, 0, warp < kSoftmaxWarps ? warp : kSoftmaxWarps, kSoftmaxWarps + 1);
-    if (lane == 0) mbar_arrive(&sm->qfirst);
   }
 
   if (warp == C::kLoadWarp) {
@@ -321,42 +329,51 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       const int pg = (u >> p.bs_shift) + (u >= w.v.sa ? w.v.skip >> p.bs_shift : 0);
       return pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
     };
-    // a walk that runs ahead: its entries wait in registers until their tile's prefetch and load
-    Q8Walk a = w;
-    bool a_live = q8_next<kT>(p, lens, a, true);
-    int a_tile = a.ta;
-    struct Ahead {
+    struct Unit {
       int entry, sub, count;  // this lane's entry and first row in its page; units of the tile
     };
-    auto ahead = [&]() -> Ahead {
-      if (!a_live) return Ahead{-1, 0, 0};
-      const Ahead r{entry_of(a, a_tile), (a_tile * kT + tok) & (p.bs - 1), (min(kT, a.v.n - a_tile * kT) + unit - 1) >> unit_shift};
-      if (++a_tile == a.tb) {
-        a_live = q8_next<kT>(p, lens, a, false);
-        a_tile = a.ta;
+    // the next tile of a walk
+    struct Tiles {
+      Q8Walk w;
+      int tile;
+      bool live;
+    };
+    auto start = [&](Tiles& t) {
+      t.w = w;
+      t.live = q8_next<kT>(p, lens, t.w, true);
+      t.tile = t.w.ta;
+    };
+    auto next_unit = [&](Tiles& t) -> Unit {
+      if (!t.live) return Unit{-1, 0, 0};
+      const Unit r{entry_of(t.w, t.tile), (t.tile * kT + tok) & (p.bs - 1), (min(kT, t.w.v.n - t.tile * kT) + unit - 1) >> unit_shift};
+      if (++t.tile == t.w.tb) {
+        t.live = q8_next<kT>(p, lens, t.w, false);
+        t.tile = t.w.ta;
       }
       return r;
     };
-    Ahead ring[kPre + 2];
-#pragma unroll
-    for (int j = 0; j < kPre + 2; ++j) ring[j] = ahead();
+    // one walk for the loads, an entry ahead of them, and one kPre tiles further on for prefetches to L2
+    Tiles loads, pres;
+    start(loads);
+    Unit cur = next_unit(loads), pre{-1, 0, 0};
     int issued = -1;
     bool stop = false;
     for (int i = 0; i < N && !stop; ++i) {
       const int s = i % kSlots;
       // an entry outside the pool or the table row reads zeros
-      int pid = ring[0].entry;
-      if (lane < ring[0].count && (pid < 0 || pid >= p.num_blocks)) {
+      const Unit nxt = next_unit(loads);
+      int pid = cur.entry;
+      if (lane < cur.count && (pid < 0 || pid >= p.num_blocks)) {
         flag_error(MLA_DEVERR_BAD_PAGE);
         pid = -1;
       }
       uint8_t* const slot = smem + s * kTileSlot;
-      const int row = (pid << p.bs_shift) + (pid < 0 ? 0 : ring[0].sub);
-      const bool mine = lane < ring[0].count;
+      const int row = (pid << p.bs_shift) + (pid < 0 ? 0 : cur.sub);
+      const bool mine = lane < cur.count;
       auto load_ckv = [&]() { tma_load_4d(slot + tok * kRank, &tm_ckv, 0, 0, 0, row >> 3, &sm->full[s], pol); };
       auto load_kpe = [&]() { tma_load_2d(slot + kCkvBytes + tok * kRope, &tm_kpe, 0, row, &sm->full[s], pol); };
       auto expect = [&]() {
-        if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>((ring[0].count << unit_shift) * kQkDim));
+        if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>((cur.count << unit_shift) * kQkDim));
         __syncwarp();
       };
       const uint32_t parity = (i / kSlots - 1) & 1;
@@ -379,14 +396,20 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         if (stop) *abort_flag = 1;
       }
       issued = i;
-      if (lane < ring[kPre].count && ring[kPre].entry >= 0 && ring[kPre].entry < p.num_blocks) {
-        const long long row = (static_cast<long long>(ring[kPre].entry) << p.bs_shift) + ring[kPre].sub;
-        bulk_prefetch_l2(p.ckv + row * kRank, static_cast<uint32_t>(unit * kRank));
-        bulk_prefetch_l2(p.kpe + row * kRope, static_cast<uint32_t>(unit * kRope));
+      cur = nxt;
+      if (i + 1 >= kSlots) {  // (the first loads go out before anything else)
+        if (i + 1 == kSlots) start(pres);
+        // tiles up to i + kPre; the first time all of them, one an iteration from then on
+#pragma unroll 1
+        for (int j = i + 1 == kSlots ? -kSlots - 1 : kPre - 1; j < kPre; ++j) {
+          if (j >= 0 && lane < pre.count && pre.entry >= 0 && pre.entry < p.num_blocks) {
+            const long long at = (static_cast<long long>(pre.entry) << p.bs_shift) + pre.sub;
+            bulk_prefetch_l2(p.ckv + at * kRank, static_cast<uint32_t>(unit * kRank));
+            bulk_prefetch_l2(p.kpe + at * kRope, static_cast<uint32_t>(unit * kRope));
+          }
+          pre = next_unit(pres);
+        }
       }
-#pragma unroll
-      for (int j = 0; j <= kPre; ++j) ring[j] = ring[j + 1];
-      ring[kPre + 1] = ahead();
     }
     // after an abort, loads in flight land before shared memory is released
     if (lane == 0 && *abort_flag)
@@ -446,7 +469,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           const Desc2 pb = desc2(C::kPRow == 64 ? smem_desc_sw64(wts, 512) : smem_desc_sw128(wts, 16, 1024));
           const Desc2 a0 = desc2(smem_desc_sw128(slot, 1024, kGroupBytes));
           const int ksteps = (min(kT, w.v.n - tile * kT) + kStep - 1) / kStep;
-#pragma unroll
+#pragma unroll 1
           for (int ks = 0; ks < kSteps; ++ks) {
             if (ks < ksteps) {
 #pragma unroll
@@ -464,23 +487,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       mbar_wait(&sm->drain[1], 0, kDrainTimeoutNs);
     }
     __syncwarp();
-  } else if (warp >= C::kQueryWarp) {
-    // ------------------------------------------------------------------ the next requests' queries to terms
-    bool more = q8_next<kT>(p, lens, w, true);
-    for (int seg = 1; more && (more = q8_next<kT>(p, lens, w, false)); ++seg) {
-      if (seg >= C::kQBufs) {  // the request whose place they take has its scores
-        int ok = 1;
-        if (lane == 0) {
-          ok = mbar_wait(&sm->qfree[seg % C::kQBufs], (seg / C::kQBufs - 1) & 1, tmo) && !*abort_flag;
-          if (!ok) *abort_flag = 1;
-        }
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      }
-      split_rows(w.b, seg, 0, 1);
-      if (lane == 0) mbar_arrive(&sm->qfull[seg & 1]);
-    }
-  } else {
-    // ------------------------------------------------------------------ softmax (warps 0-7)
+  } else if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------------ softmax
     const int q4 = warp & 3, h = warp >> 2;
     const int tl = 32 * q4 + lane;  // this thread's token of each tile, and latent column of each block of O
     const uint32_t lane_base = static_cast<uint32_t>(32 * q4) << 16;
@@ -520,7 +528,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       for (int tile = w.ta; tile < w.tb; ++tile, ++i) {
         // NaN for a scale that is neither NaN nor in range
         const float z = (z_raw >= 0x1p-60f && z_raw <= 0x1p60f) ? z_raw : __uint_as_float(0x7fc00000u);
-        const float lz = log2f(z), iz = 1.f / z;
+        // (approximate: their errors, 2^-22, make a token's weight and its share of the sum wrong alike)
+        const float lz = __log2f(z), iz = __frcp_rn(z);
         z_raw = tile + 1 < w.tb ? scale_at(pid, tile + 1) : 1.f;
         pid = tile + 2 < w.tb ? page_at(w, tile + 2) : -1;
         const int sb = i % C::kSBufs;
@@ -645,7 +654,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         if (need && tile > w.ta) {  // O: the value product of the tile before must be complete
           if (__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo))) {
             tc_fence_after();
-#pragma unroll 1
+#pragma unroll 2
             for (int blk = 0; blk < 4; ++blk) {
               float v[kTerms][RH];
               const uint32_t a = tmem + lane_base + C::kTmemO + blk * C::kNP + RH * h;
@@ -787,8 +796,8 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_kern
   int64_t mine = 0, T = 0;
   for (int b = b_lo; b < b_hi; ++b) mine += q8_tiles(q8_view(p, __ldcg(p.context_lens + b)), p.tile);
   int64_t at = block_prefix<kMergeThreads>(mine, sm.scratch, &T);
-  const int64_t J = q8_live_gangs(T, p.gangs);
-  if (J < 2) {
+  const Q8Line line = q8_line(T, p.gangs);
+  if (line.gangs < 2) {
     pdl_wait();
     return;
   }
@@ -800,8 +809,8 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_kern
     if (b_lo + k < b_hi) {
       const int n = q8_tiles(q8_view(p, __ldcg(p.context_lens + b_lo + k)), p.tile);
       if (n > 0) {
-        j0 = q8_gang_of(at, T, J);
-        j1 = q8_gang_of(at + n - 1, T, J);
+        j0 = line.gang_of(at);
+        j1 = line.gang_of(at + n - 1);
       }
       at += n;
     }

@@ -140,7 +140,8 @@ MLA_HOST_DEVICE inline WindowView window_view(int32_t L, int32_t q_len, int32_t 
   const int64_t first = static_cast<int64_t>(L) - (causal ? q_len : 1);  // the earliest row's position
   const int64_t low = first - window + 1;                                // the first token its window reaches
   if (low <= 0) return v;
-  const int64_t low_page = low / bs * bs, sink_end = (static_cast<int64_t>(sinks) + bs - 1) / bs * bs;
+  const int64_t page = ~static_cast<int64_t>(bs - 1);  // (bs is a power of two)
+  const int64_t low_page = low & page, sink_end = (static_cast<int64_t>(sinks) + bs - 1) & page;
   v.sa = static_cast<int32_t>(sink_end < low_page ? sink_end : low_page);
   v.skip = static_cast<int32_t>(low_page - v.sa);
   v.n = L - v.skip;

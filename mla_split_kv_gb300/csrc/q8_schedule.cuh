@@ -2,8 +2,8 @@
 // found again by its merge.
 //
 // The batch's visible runs, cut into tiles of p.tile tokens request after request,
-// are one line of T tiles. Gang j of J takes tiles [jT/J, (j+1)T/J) of it (one
-// CTA of a gang per row group), so every gang works on the same number of tiles
+// are one line of T tiles. Gang j of J takes T / J of it, the first T % J gangs
+// one more (one CTA of a gang per row group), so every gang works on the same number of tiles
 // whatever the lengths, and lengths are read where they lie: no host plan, and
 // a captured call follows contexts as they grow. A request that lies within
 // one gang is finished there; one cut by gang borders has a part per gang: its
@@ -29,11 +29,27 @@ struct Q8Lens {
   __device__ __forceinline__ int operator()(int b) const { return b < kQ8Lens ? cached[b] : __ldcg(global + b); }
 };
 
-// Gangs that get tiles (all of them unless there are fewer tiles), gang j's first tile, and the gang of tile x.
-__device__ __forceinline__ int64_t q8_live_gangs(int64_t T, int gangs) { return T < gangs ? T : gangs; }
-__device__ __forceinline__ int64_t q8_gang_begin(int64_t j, int64_t T, int64_t J) { return j * T / J; }
-__device__ __forceinline__ int q8_gang_of(int64_t x, int64_t T, int64_t J) {
-  return static_cast<int>(((x + 1) * J - 1) / T);
+// The line of T tiles among the gangs that get any (all of them unless there are fewer tiles).
+struct Q8Line {
+  int64_t base;      // tiles of a gang
+  int32_t gangs, more;  // the first `more` gangs have one more
+  __device__ __forceinline__ int64_t begin(int j) const { return base * j + min(j, more); }
+  // the gang of tile x
+  __device__ __forceinline__ int gang_of(int64_t x) const {
+    const int64_t head = (base + 1) * more;
+    return x < head ? static_cast<int>(div(x, base + 1)) : more + static_cast<int>(div(x - head, base));
+  }
+  // (32-bit division where it does)
+  static __device__ __forceinline__ int64_t div(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+  }
+};
+__device__ __forceinline__ Q8Line q8_line(int64_t T, int gangs) {
+  Q8Line l;
+  l.gangs = T < gangs ? static_cast<int32_t>(T) : gangs;
+  l.base = l.gangs > 0 ? Q8Line::div(T, l.gangs) : 0;
+  l.more = static_cast<int32_t>(T - l.base * l.gangs);
+  return l;
 }
 
 // Exclusive prefix over the block's threads of each thread's `mine`, and the total. `scratch`: 33 values.
