@@ -855,7 +855,8 @@ bool valid_scale_block(int32_t g, int32_t bs) { return g >= 1 && g <= bs && (g &
 uint64_t q8_workspace_bytes(int32_t sms, int32_t q_len, int32_t num_heads) {
   const int rows = q_len * num_heads, nr = mla::q8_rows_per_cta(rows);
   const uint64_t row_pad = static_cast<uint64_t>((rows + nr - 1) / nr) * nr;
-  return static_cast<uint64_t>(mla::q8_gangs(rows, sms)) * 2 * row_pad * (mla::kRank + 2) * 4;
+  const uint64_t gangs = static_cast<uint64_t>(mla::q8_gangs(rows, sms));
+  return gangs * 2 * row_pad * (mla::kRank + 2) * 4 + round256(gangs * 8);
 }
 
 }  // namespace
@@ -950,6 +951,7 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
   p.scale_log2 = scale * 1.4426950408889634f;
   p.B = d->num_requests;
   p.H = d->num_heads;
+  p.h_shift = d->num_heads == 16 ? 4 : (d->num_heads == 64 ? 6 : 7);
   p.q_len = d->q_len;
   p.bs = d->block_size;
   p.bs_shift = d->block_size == 16 ? 4 : (d->block_size == 32 ? 5 : 6);
@@ -967,6 +969,7 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
   p.tile = mla::q8_tile_tokens(rows, d->dtype == MLA_BF16);
   p.ws_o = static_cast<float*>(d->workspace);
   p.ws_ml = p.ws_o + static_cast<uint64_t>(p.gangs) * 2 * p.row_pad * mla::kRank;
+  p.ws_cut = reinterpret_cast<int2*>(p.ws_ml + static_cast<uint64_t>(p.gangs) * 2 * p.row_pad * 2);
   p.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
   CUtensorMap tm_ckv, tm_kpe;
   const uint64_t cache_rows = static_cast<uint64_t>(d->num_blocks) * static_cast<uint64_t>(d->block_size);

@@ -34,8 +34,7 @@
 //
 // Warp roles (384 threads): warps 0-7 softmax, rescale and output (thread =
 // token; the two warps of a TMEM lane quadrant take half of the rows each),
-// warps 8 and 9 issue the score and the value products, warp 10 loads pages,
-// warp 11 splits the queries of the next request while this one's tiles run.
+// two more that issue the score and the value products, one that loads pages.
 #include "q8_schedule.cuh"
 
 namespace mla {
@@ -47,7 +46,6 @@ constexpr int kStep = 32;                         // tokens of an MMA step of th
 constexpr int kMaxSlots = 3, kMaxSteps = 4;
 constexpr int RH = 8;                             // rows per softmax thread
 constexpr float kTermStep = 32.0f, kTermInv = 1.0f / 32.0f;
-constexpr int kSums = 4;                          // row factors kept: queries split ahead of their softmax
 
 constexpr uint32_t kSmallBytes = 5120;
 
@@ -61,7 +59,6 @@ struct Cfg {
   static constexpr int kWeightExp = NR == 16 ? 1 : 6;
   static constexpr int kNS = NR * kQTerms, kNP = NR * kTerms;      // N of the two products
   static constexpr int kSBufs = (4 * kNP + 2 * kNS <= 512) ? 2 : 1;  // score buffers in tensor memory
-  static constexpr int kQBufs = NR == 16 ? 2 : 1;
   static constexpr int kT = (NR == 32 && !BF16) ? 128 : 96;        // tokens per tile
   static constexpr int kSlots = kT == 96 ? 3 : 2, kSteps = kT / kStep;
   static constexpr uint32_t kCkvBytes = kT * kRank, kTileSlot = kT * kQkDim;
@@ -75,13 +72,13 @@ struct Cfg {
   static constexpr uint32_t kPRow = kNP <= 64 ? 64 : 128, kPBytes = kT * kPRow;
   static constexpr int kPBufs = kPInSlot ? 0 : (BF16 ? 2 : 1);
   static constexpr uint32_t kOffQ = kSlots * kTileSlot;
-  static constexpr uint32_t kOffP = kOffQ + kQBufs * kQBytes;
+  static constexpr uint32_t kOffP = kOffQ + kQBytes;
   static constexpr uint32_t kOffSmall = kOffP + kPBufs * kPBytes;
   static constexpr uint32_t kSmem = kOffSmall + kSmallBytes;
   static constexpr uint32_t kTmemO = 0, kTmemS = 4 * kNP;
   // warps
   static constexpr int kSoftmaxWarps = NR / RH * 4, kScoreWarp = kSoftmaxWarps, kValueWarp = kScoreWarp + 1;
-  static constexpr int kLoadWarp = kValueWarp + 1, kQueryWarp = kLoadWarp + 1, kThreads = (kQueryWarp + 1) * 32;
+  static constexpr int kLoadWarp = kValueWarp + 1, kThreads = (kLoadWarp + 1) * 32;
   static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kQChunk % 1024 == 0, "swizzle atoms stay aligned");
   static_assert(kTileSlot % 1024 == 0 && kCkvBytes % 1024 == 0 && (!kPInSlot || kPBytes <= kT * kRope), "tile slots");
   static_assert(kSlots <= kMaxSlots && kSteps <= kMaxSteps && kNP <= static_cast<int>(kPRow), "layouts");
@@ -93,14 +90,13 @@ struct Small {
   uint64_t full[kMaxSlots], empty[kMaxSlots][kMaxSteps];  // tile slots, freed step by step
   uint64_t sfull[2], sfree[2];           // score buffers
   uint64_t pfull[kMaxSlots], pvdone[2];  // weights per slot; value products per tile parity
-  uint64_t qfull[2], qfree[2], qfirst;   // query buffers
-  uint64_t ofree, drain[2];
+  uint64_t qfull, ofree, drain[2];
   int64_t scratch[33];
   int64_t off0;
   int b0;
   uint32_t tmem_base;
   int32_t abort_flag;
-  alignas(16) float factor[kSums][32];   // per row: score scale over the query's power of two, log2 units
+  alignas(16) float factor[2][32];       // per row: score scale over the query's power of two, log2 units
   alignas(16) float red[2][4][32];       // per tile parity and token quadrant, rows' maxima (then their sums)
   int32_t lens[kQ8Lens];
 };
@@ -178,10 +174,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       mbar_init(&sm->sfull[s], 1);
       mbar_init(&sm->sfree[s], kSoftmaxWarps);
       mbar_init(&sm->pvdone[s], 1);
-      mbar_init(&sm->qfull[s], 1);
-      mbar_init(&sm->qfree[s], 1);
     }
-    mbar_init(&sm->qfirst, kSoftmaxWarps + 1);
+    mbar_init(&sm->qfull, kSoftmaxWarps);
     mbar_init(&sm->ofree, kSoftmaxWarps);
     mbar_init(&sm->drain[0], 1);
     mbar_init(&sm->drain[1], 1);
@@ -252,7 +246,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     return q;
   };
   auto split_query = [&](const QueryRow& qr, int seg, int r) {
-    uint8_t* const q = smem + C::kOffQ + (seg % C::kQBufs) * C::kQBytes;
+    uint8_t* const q = smem + C::kOffQ;
     const uint32_t* const u = reinterpret_cast<const uint32_t*>(qr.v);
     // the row's largest magnitude (its bits: 15 of them order both types, NaN and infinity on top)
     uint32_t top = 0;
@@ -264,7 +258,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     const int e = min(126, 134 - static_cast<int>(__float_as_uint(amax) >> 23));
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     if (lane == 0)
-      sm->factor[seg % kSums][r] = (amax < INFINITY) ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
+      sm->factor[seg & 1][r] = (amax < INFINITY) ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
                                                      : __uint_as_float(0x7fc00000u);
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
@@ -287,34 +281,6 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       }
     }
   };
-  // The queries: the first request's by all warps that would wait for its scores, each further one's by the query
-  // warp while its predecessor's tiles run.
-  if (work && (warp < kSoftmaxWarps || warp == C::kQueryWarp)) {
-    Q8Walk a = w;
-    q8_next<kT>(p, lens, a, true);
-    for (int seg = 0;; ++seg) {
-      if (seg >= C::kQBufs) {  // the request whose place they take has its scores
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm->qfree[seg % C::kQBufs], (seg / C::kQBufs - 1) & 1, tmo) && !*abort_flag)) {
-          *abort_flag = 1;
-          break;
-        }
-      }
-      const int step = seg == 0 ? kSoftmaxWarps + 1 : 1;
-      int r = seg == 0 ? (warp < kSoftmaxWarps ? warp : kSoftmaxWarps) : 0;
-      QueryRow next = load_query(a.b, r);
-#pragma unroll 1
-      for (; r < NR; r += step) {
-        const QueryRow row = next;
-        next = load_query(a.b, r + step);  // (past the last: zeros)
-        split_query(row, seg, r);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(seg == 0 ? &sm->qfirst : &sm->qfull[seg & 1]);
-      if (warp < kSoftmaxWarps || !q8_next<kT>(p, lens, a, false)) break;
-    }
-  }
-
   if (warp == C::kLoadWarp) {
     // ------------------------------------------------------------------ page loads
     const uint64_t pol = l2_policy_evict_first();
@@ -424,9 +390,9 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       int i = 0;
       bool first = true, ok = true;
       for (int seg = 0; ok && q8_next<kT>(p, lens, w, first); ++seg, first = false) {
-        const uint32_t q = base + C::kOffQ + (seg % C::kQBufs) * C::kQBytes;
+        const uint32_t q = base + C::kOffQ;
         const Desc2 bd = desc2(smem_desc_sw128(q, 16, 1024)), bk = desc2(smem_desc_sw64(q + 4 * C::kQChunk, 512));
-        ok = seg == 0 ? mbar_wait(&sm->qfirst, 0, tmo) : mbar_wait(&sm->qfull[seg & 1], ((seg - 1) >> 1) & 1, tmo);
+        ok = mbar_wait(&sm->qfull, seg & 1, tmo);
         for (int tile = w.ta; ok && tile < w.tb; ++tile, ++i) {
           ok = mbar_wait(&sm->full[i % kSlots], (i / kSlots) & 1, tmo) &&
                (i < C::kSBufs || mbar_wait(&sm->sfree[i % C::kSBufs], (i / C::kSBufs - 1) & 1, tmo)) && !*abort_flag;
@@ -443,10 +409,14 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           umma8_ss(d, ak, 0, bk, 0, idesc, 1u);
           umma8_ss(d, ak, 32 >> 4, bk, 32 >> 4, idesc, 1u);
           umma_commit(&sm->sfull[i % C::kSBufs]);
-          if (tile + 1 == w.tb) umma_commit(&sm->qfree[seg % C::kQBufs]);
         }
       }
       if (!ok) *abort_flag = 1;
+      // (after the last segment) a request that starts here and goes on: its parts, for the merge
+      if (blockIdx.x == 0) {
+        const bool cut = N > 0 && w.ta == 0 && w.tb < w.n_tiles;
+        p.ws_cut[gang] = make_int2(w.b, cut ? line.gang_of(hi + (w.n_tiles - w.tb) - 1) - gang + 1 : 0);
+      }
       umma_commit(&sm->drain[0]);  // every MMA issued has completed before TMEM is freed
       mbar_wait(&sm->drain[0], 0, kDrainTimeoutNs);
     }
@@ -510,21 +480,25 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       return __ldg(p.scales + (row >> p.g_shift));
     };
     int i = 0;  // tile count
-    bool first = true;
-    for (int seg = 0; q8_next<kT>(p, lens, w, first); ++seg, first = false) {
+    // Each round: a request's tiles, the split of the next one's queries (while the last value product runs), then
+    // the request's output. The first round only splits.
+    Q8Walk next = w;
+    bool more = q8_next<kT>(p, lens, next, true);
+    for (int seg = -1;; ++seg) {
+     bool stop = false;
+     float lsum[RH], mr[RH];
+     if (seg >= 0) {
       float z_raw = scale_at(page_at(w, w.ta), w.ta);
       int pid = w.ta + 1 < w.tb ? page_at(w, w.ta + 1) : -1;
-      float lsum[RH], mr[RH];
 #pragma unroll
       for (int k = 0; k < RH; ++k) {
         lsum[k] = 0.f;
         mr[k] = -INFINITY;
       }
       // rows' positions: the first and last row of this CTA, and what their windows leave out
-      const int pos_first = p.causal ? w.v.n - p.q_len + row0 / p.H : w.v.n - 1;
-      const int pos_last = p.causal ? w.v.n - p.q_len + (row0 + nrows - 1) / p.H : w.v.n - 1;
+      const int pos_first = p.causal ? w.v.n - p.q_len + (row0 >> p.h_shift) : w.v.n - 1;
+      const int pos_last = p.causal ? w.v.n - p.q_len + ((row0 + nrows - 1) >> p.h_shift) : w.v.n - 1;
       const int low_last = p.window > 0 ? max(-1, pos_last - p.window) : -1;
-      bool stop = false;
       for (int tile = w.ta; tile < w.tb; ++tile, ++i) {
         // NaN for a scale that is neither NaN nor in range
         const float z = (z_raw >= 0x1p-60f && z_raw <= 0x1p60f) ? z_raw : __uint_as_float(0x7fc00000u);
@@ -547,7 +521,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           float factor[RH];
 #pragma unroll
           for (int k = 0; k < RH; k += 4)
-            *reinterpret_cast<float4*>(factor + k) = *reinterpret_cast<const float4*>(&sm->factor[seg % kSums][RH * h + k]);
+            *reinterpret_cast<float4*>(factor + k) = *reinterpret_cast<const float4*>(&sm->factor[seg & 1][RH * h + k]);
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
@@ -561,7 +535,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 #pragma unroll
             for (int k = 0; k < RH; ++k) {
               const int r = row0 + RH * h + k, u = u0 + tl;
-              const int pos = p.causal ? w.v.n - p.q_len + r / p.H : w.v.n - 1;
+              const int pos = p.causal ? w.v.n - p.q_len + (r >> p.h_shift) : w.v.n - 1;
               bool vis = tl < nvalid && RH * h + k < nrows && u <= pos;
               if (p.window > 0) vis = vis && (u > pos - p.window || u < p.sinks);
               if (!vis) x[k] = -INFINITY;
@@ -677,8 +651,23 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->pfull[i % kSlots]);
       }
+     }
+     if (stop) break;
+     if (more) {
+      // (their scores done, nothing reads the last request's queries any more)
+      QueryRow row = load_query(next.b, warp);
+#pragma unroll 1
+      for (int r = warp; r < NR; r += kSoftmaxWarps) {
+        const QueryRow ahead = load_query(next.b, r + kSoftmaxWarps);  // (past the last: zeros)
+        split_query(row, seg + 1, r);
+        row = ahead;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->qfull);
+     }
+     if (seg >= 0) {
       // the segment's end: its sums, and O once its last value product is complete
-      if (stop) break;
       const bool ended = mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo);
       if (!ended) *abort_flag = 1;
 #pragma unroll
@@ -738,6 +727,10 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           }
         }
       }
+     }
+     if (!more) break;
+     w = next;
+     more = q8_next<kT>(p, lens, next, false);
     }
   }
   // requests with nothing to see
@@ -759,14 +752,15 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 
 // The requests cut by gang borders: per (request, row) the parts of its gangs,
 //   M = max m_j, w_j = 2^(m_j - M), out = sum w_j O_j / sum w_j l_j, lse = M + log2 sum w_j l_j.
-// A warp takes 128 columns of a row with one lane a column quad where a request has at most kFewParts parts
-// (a batch: two or three), and 16 columns with eight part lanes where it has more (one long request: as many
-// as there are gangs): every lane's loads of a round in flight at once either way. Lane sums are added in a
-// fixed tree: the same bits on every call.
-constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32;
-constexpr int kFewParts = 8, kPartLanes = 8;
-constexpr int kMergeLoads = 8;      // parts a lane has in flight with part lanes: 64 gangs in a round
-constexpr int kMergeBlocks = 4;     // per SM: one wave, each block takes items in strides
+// A block takes a whole row, a warp 128 columns of it, where a request has at most kFewParts parts (a batch: two or
+// three); where it has more (one long request: as many as there are gangs) 32 columns of a row, the parts shared by 16
+// lanes each. Every thread's loads are in flight at once either way; lanes' sums are added in lane order: the same
+// bits on every call.
+constexpr int kMergeThreads = 128;
+constexpr int kMergeBlocks = 4;  // per SM: one wave, each block takes units in strides
+constexpr int kFewParts = 8, kPartLanes = 16, kColLanes = kMergeThreads / kPartLanes;
+constexpr int kMergeLoads = 10;  // parts a lane has in flight: 160 gangs in a round
+constexpr int kMaxCuts = 512;    // gangs looked at
 
 // a part's weight: one without a visible token has l = 0; one whose every score is NaN has no maximum, and l NaN
 __device__ __forceinline__ float part_weight(float2 ml, float ref) {
@@ -780,152 +774,117 @@ __device__ __forceinline__ void fma4(float4& acc, float w, const float4 v) {
 }
 
 struct MergeSmem {
-  int64_t scratch[33];
-  int cut[kMergeWarps];
-  int b[kMergeThreads], j0[kMergeThreads], n[kMergeThreads];
-  int64_t first[kMergeThreads + 1];  // items before each
+  int count;
+  int b[kMaxCuts], j0[kMaxCuts], n[kMaxCuts], first[kMaxCuts + 1];  // the cut requests; units before each
+  float4 acc[kPartLanes][kColLanes];
+  float2 ml[kPartLanes];
 };
 
 __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_kernel(const DecodeQ8Params p) {
   __shared__ MergeSmem sm;
+  pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the lengths are no output of the decode kernel, whose start waited for the kernel before it
-  const int per = (p.B + kMergeThreads - 1) / kMergeThreads;
-  const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
-  int64_t mine = 0, T = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += q8_tiles(q8_view(p, __ldcg(p.context_lens + b)), p.tile);
-  int64_t at = block_prefix<kMergeThreads>(mine, sm.scratch, &T);
-  const Q8Line line = q8_line(T, p.gangs);
-  if (line.gangs < 2) {
-    pdl_wait();
-    return;
-  }
+  const int tid = threadIdx.x, lane = tid & 31;
   const int rows_total = p.q_len * p.H;
-  bool waited = false;
-  // requests are taken in rounds of those that the threads' next ones are
-  for (int k = 0; k < per; ++k) {
-    int j0 = 0, j1 = 0;
-    if (b_lo + k < b_hi) {
-      const int n = q8_tiles(q8_view(p, __ldcg(p.context_lens + b_lo + k)), p.tile);
-      if (n > 0) {
-        j0 = line.gang_of(at);
-        j1 = line.gang_of(at + n - 1);
+  if (tid < 32) {  // the list, in gang order: the same in every block
+    int count = 0, units = 0;
+    for (int g0 = 0; g0 < p.gangs; g0 += 32) {
+      const int2 c = g0 + lane < p.gangs ? __ldcg(p.ws_cut + g0 + lane) : make_int2(0, 0);
+      const uint32_t cut = __ballot_sync(0xffffffffu, c.y > 1);
+      int mine = c.y > 1 ? rows_total * (c.y <= kFewParts ? 1 : kRank / (4 * kColLanes)) : 0, upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
       }
-      at += n;
-    }
-    // the cut ones among them, in thread order: the same list in every block
-    const uint32_t cut = __ballot_sync(0xffffffffu, j1 > j0);
-    if (lane == 0) sm.cut[warp] = __popc(cut);
-    const int64_t items_mine = j1 > j0 ? static_cast<int64_t>(rows_total) * (kRank / (j1 - j0 < kFewParts ? 128 : 16)) : 0;
-    int64_t items = 0;
-    const int64_t before = block_prefix<kMergeThreads>(items_mine, sm.scratch, &items);  // (two barriers)
-    int count = 0, mine_at = __popc(cut & ((1u << lane) - 1u));
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-      if (w < warp) mine_at += sm.cut[w];
-      count += sm.cut[w];
-    }
-    if (j1 > j0) {
-      sm.b[mine_at] = b_lo + k;
-      sm.j0[mine_at] = j0;
-      sm.n[mine_at] = j1 - j0 + 1;
-      sm.first[mine_at] = before;
-    }
-    __syncthreads();
-    if (!waited) pdl_wait();
-    waited = true;
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp; item < items;
-         item += static_cast<int64_t>(gridDim.x) * kMergeWarps) {
-      int i = 0;  // the last of the list that starts at or before the item
-      for (int step = kMergeThreads / 2; step > 0; step >>= 1)
-        if (i + step < count && sm.first[i + step] <= item) i += step;
-      const int b = sm.b[i], g0 = sm.j0[i], n = sm.n[i];
-      const int rest = static_cast<int>(item - sm.first[i]);
-      // part x of the request: gang g0 + x, entry 1 of the first gang, entry 0 of the others
-      auto slot = [&](int x, int row) { return (static_cast<long long>(g0 + x) * 2 + (x == 0 ? 1 : 0)) * p.row_pad + row; };
-      float M = -INFINITY, den = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      int row, c;
-      bool writes = true;
-      if (n <= kFewParts) {
-        row = rest >> 2;
-        c = (rest & 3) * 128 + 4 * lane;
-        float2 ml[kFewParts];
-        float4 v[kFewParts];
-#pragma unroll
-        for (int x = 0; x < kFewParts; ++x) {
-          ml[x] = make_float2(-INFINITY, 0.f);
-          if (x < n) {
-            ml[x] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + slot(x, row) * 2));
-            v[x] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(x, row) * kRank + c));
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < kFewParts; ++x) M = fmaxf(M, ml[x].x);
-        const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-        for (int x = 0; x < kFewParts; ++x) {
-          if (x < n) {
-            const float w = part_weight(ml[x], ref);
-            den = fmaf(w, ml[x].y, den);
-            fma4(acc, w, v[x]);
-          }
-        }
-      } else {
-        row = rest >> 5;
-        const int e = lane >> 2;
-        c = (rest & 31) * 16 + 4 * (lane & 3);
-        for (int x0 = 0; x0 < n; x0 += kPartLanes * kMergeLoads) {
-          float2 ml[kMergeLoads];
-          float4 v[kMergeLoads];
-#pragma unroll
-          for (int y = 0; y < kMergeLoads; ++y) {
-            const int x = x0 + e + kPartLanes * y;
-            ml[y] = make_float2(-INFINITY, 0.f);
-            v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x < n) {
-              ml[y] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + slot(x, row) * 2));
-              v[y] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(x, row) * kRank + c));
-            }
-          }
-          float m = M;
-#pragma unroll
-          for (int y = 0; y < kMergeLoads; ++y) m = fmaxf(m, ml[y].x);
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          const float ref = m == -INFINITY ? 0.f : m;
-          const float al = M == -INFINITY ? 1.f : exp2f(M - ref);  // (nothing summed before the first, or only NaN)
-          den *= al;
-          acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
-          M = m;
-#pragma unroll
-          for (int y = 0; y < kMergeLoads; ++y) {
-            const float w = part_weight(ml[y], ref);
-            den = fmaf(w, ml[y].y, den);
-            fma4(acc, w, v[y]);
-          }
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          den += __shfl_xor_sync(0xffffffffu, den, o);
-          acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
-          acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
-          acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
-          acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
-        }
-        writes = e == 0;
+      if (c.y > 1) {
+        const int at = count + __popc(cut & ((1u << lane) - 1u));
+        sm.b[at] = c.x;
+        sm.j0[at] = g0 + lane;
+        sm.n[at] = c.y;
+        sm.first[at] = units + upto - mine;
       }
-      if (writes) {
-        const long long br = static_cast<long long>(b) * rows_total + row;
-        const bool none = den == 0.f;
-        const float inv = none ? 0.f : 1.f / den;
-        store_out4(p.out, p.out_dtype, br * kRank + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        if (p.out_lse != nullptr && c == 0) p.out_lse[br] = none ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(den);
+      count += __popc(cut);
+      units += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) {
+      sm.count = count;
+      sm.first[count] = units;
+    }
+  }
+  __syncthreads();
+  const int count = sm.count, units = sm.first[count];
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    int i = 0;  // the last of the list that starts at or before the unit
+    for (int step = kMaxCuts / 2; step > 0; step >>= 1)
+      if (i + step < count && sm.first[i + step] <= unit) i += step;
+    const int n = sm.n[i], rest = unit - sm.first[i];
+    const bool few = n <= kFewParts;
+    const int row = few ? rest : rest / (kRank / (4 * kColLanes));
+    // part x of the request: gang j0 + x, entry 1 of the first gang, entry 0 of the others
+    const long long slot0 = static_cast<long long>(sm.j0[i]) * 2 * p.row_pad + row;
+    auto slot = [&](int x) { return slot0 + static_cast<long long>(x == 0 ? 1 : 2 * x) * p.row_pad; };
+    const int e = few ? 0 : tid / kColLanes, lanes = few ? 1 : kPartLanes;
+    const int c = few ? 4 * tid : (rest % (kRank / (4 * kColLanes))) * 4 * kColLanes + 4 * (tid % kColLanes);
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int x0 = e; x0 < n; x0 += lanes * kMergeLoads) {
+      float2 ml[kMergeLoads];
+      float4 v[kMergeLoads];
+#pragma unroll
+      for (int y = 0; y < kMergeLoads; ++y) {
+        const int x = x0 + lanes * y;
+        ml[y] = make_float2(-INFINITY, 0.f);
+        v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < n) {
+          ml[y] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + slot(x) * 2));
+          v[y] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(x) * kRank + c));
+        }
+      }
+      float m = M;
+#pragma unroll
+      for (int y = 0; y < kMergeLoads; ++y) m = fmaxf(m, ml[y].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float al = M == -INFINITY ? 1.f : exp2f(M - ref);  // (nothing summed before the first, or only NaN)
+      den *= al;
+      acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
+      M = m;
+#pragma unroll
+      for (int y = 0; y < kMergeLoads; ++y) {
+        const float w = part_weight(ml[y], ref);
+        den = fmaf(w, ml[y].y, den);
+        fma4(acc, w, v[y]);
       }
     }
-    __syncthreads();
+    if (!few) {  // lanes' sums, each a part of its own
+      sm.acc[e][tid % kColLanes] = acc;
+      if (tid % kColLanes == 0) sm.ml[e] = make_float2(M, den);
+      __syncthreads();
+      M = -INFINITY;
+#pragma unroll
+      for (int y = 0; y < kPartLanes; ++y) M = fmaxf(M, sm.ml[y].x);
+      const float ref = M == -INFINITY ? 0.f : M;
+      den = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e == 0) {
+#pragma unroll
+        for (int y = 0; y < kPartLanes; ++y) {
+          const float2 ml = sm.ml[y];
+          const float w = part_weight(ml, ref);
+          den += w * ml.y;
+          fma4(acc, w, sm.acc[y][tid]);
+        }
+      }
+      __syncthreads();
+    }
+    if (e == 0) {
+      const long long br = static_cast<long long>(sm.b[i]) * rows_total + row;
+      const bool none = den == 0.f;
+      const float inv = none ? 0.f : 1.f / den;
+      store_out4(p.out, p.out_dtype, br * kRank + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      if (p.out_lse != nullptr && c == 0) p.out_lse[br] = none ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(den);
+    }
   }
 }
 
@@ -949,7 +908,8 @@ int q8_tile_tokens(int total_rows, bool bf16) {
 }
 int q8_gangs(int total_rows, int sms) {
   const int nr = q8_rows_per_cta(total_rows), groups = (total_rows + nr - 1) / nr;
-  return sms > groups ? sms / groups : 1;
+  const int gangs = sms > groups ? sms / groups : 1;
+  return gangs < kMaxCuts ? gangs : kMaxCuts;
 }
 
 cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kpe, const DecodeQ8Params& p, bool bf16,
@@ -967,12 +927,11 @@ cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kp
   else
     e = bf16 ? launch<32, true>(cfg, tm_ckv, tm_kpe, p) : launch<32, false>(cfg, tm_ckv, tm_kpe, p);
   if (e != cudaSuccess) return e;
-  // one warp an item, for as many requests as gang borders can cut
-  const int64_t cuts = p.B < p.gangs ? p.B : p.gangs;
-  const int64_t items = cuts * p.q_len * p.H * (p.gangs > kFewParts && p.B < p.gangs ? kRank / 16 : kRank / 128);
-  const int64_t blocks = (items + kMergeWarps - 1) / kMergeWarps;
+  // a block a unit, for as many requests as gang borders can cut
+  const int64_t cuts = p.B < p.gangs ? p.B : p.gangs - 1;
+  const int64_t units = (cuts > 0 ? cuts : 1) * p.q_len * p.H * (p.gangs > kFewParts && p.B < p.gangs ? kRank / (4 * kColLanes) : 1);
   const int64_t wave = static_cast<int64_t>(kMergeBlocks) * p.gangs * p.groups;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks < wave ? blocks : wave), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(units < wave ? units : wave), 1, 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, mla_merge_q8_kernel, p);

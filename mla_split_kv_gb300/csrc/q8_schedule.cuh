@@ -8,7 +8,7 @@
 // a captured call follows contexts as they grow. A request that lies within
 // one gang is finished there; one cut by gang borders has a part per gang: its
 // first gang keeps it in entry 1 (that gang's open end), the others in entry
-// 0, and the merge finds the gangs from the request's place on the line.
+// 0, and says in its first gang's entry of ws_cut how many there are.
 #pragma once
 
 #include "device_common.cuh"
