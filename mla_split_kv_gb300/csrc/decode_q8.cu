@@ -554,8 +554,14 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 #pragma unroll
           for (int k = 0; k < RH; ++k) x[k] = -INFINITY;
         }
-        // rows' maxima over the tile: over the warp's tokens, then, behind one barrier, over the four warps'
-        {
+        // Does a score pass its row's reference by more than kTau? One barrier of the four warps that share the rows;
+        // only then are the rows' maxima taken, and the references move to them, with the sums and O.
+        bool need = false;
+#pragma unroll
+        for (int k = 0; k < RH; ++k) need |= x[k] > mr[k] + C::kTau;
+        need = named_bar_sync_or(bar, kMeet, need || !ok || *abort_flag != 0);
+        float al[RH];
+        if (need) {
           float v[RH];
 #pragma unroll
           for (int k = 0; k < RH; ++k) v[k] = warp_max(x[k]);
@@ -564,30 +570,23 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
             for (int k = 0; k < RH; k += 4)
               *reinterpret_cast<float4*>(&sm->red[i & 1][q4][RH * h + k]) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
-        }
-        if (named_bar_sync_or(bar, kMeet, !ok || *abort_flag != 0)) {
-          stop = true;
-          break;
-        }
-        float mx[RH];
-        bool need = false;  // the same in all threads of the half
+          if (named_bar_sync_or(bar, kMeet, !ok || *abort_flag != 0)) {
+            stop = true;
+            break;
+          }
 #pragma unroll
-        for (int k = 0; k < RH; k += 4) {
-          float4 m4[4];
+          for (int k = 0; k < RH; k += 4) {
+            float4 m4[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) m4[q] = *reinterpret_cast<const float4*>(&sm->red[i & 1][q][RH * h + k]);
-          mx[k] = fmaxf(fmaxf(m4[0].x, m4[1].x), fmaxf(m4[2].x, m4[3].x));
-          mx[k + 1] = fmaxf(fmaxf(m4[0].y, m4[1].y), fmaxf(m4[2].y, m4[3].y));
-          mx[k + 2] = fmaxf(fmaxf(m4[0].z, m4[1].z), fmaxf(m4[2].z, m4[3].z));
-          mx[k + 3] = fmaxf(fmaxf(m4[0].w, m4[1].w), fmaxf(m4[2].w, m4[3].w));
-        }
-#pragma unroll
-        for (int k = 0; k < RH; ++k) need |= mx[k] > mr[k] + C::kTau;
-        float al[RH];
-        if (need) {  // the reference maxima move, and with them the sums and O
+            for (int q = 0; q < 4; ++q) m4[q] = *reinterpret_cast<const float4*>(&sm->red[i & 1][q][RH * h + k]);
+            v[k] = fmaxf(fmaxf(m4[0].x, m4[1].x), fmaxf(m4[2].x, m4[3].x));
+            v[k + 1] = fmaxf(fmaxf(m4[0].y, m4[1].y), fmaxf(m4[2].y, m4[3].y));
+            v[k + 2] = fmaxf(fmaxf(m4[0].z, m4[1].z), fmaxf(m4[2].z, m4[3].z));
+            v[k + 3] = fmaxf(fmaxf(m4[0].w, m4[1].w), fmaxf(m4[2].w, m4[3].w));
+          }
 #pragma unroll
           for (int k = 0; k < RH; ++k) {
-            const float m = fmaxf(mr[k], mx[k]);
+            const float m = fmaxf(mr[k], v[k]);
             al[k] = (mr[k] == -INFINITY) ? 1.f : fast_exp2(mr[k] - m);  // (nothing summed yet, or only NaN)
             mr[k] = m;
             lsum[k] *= al[k];
@@ -670,17 +669,27 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       // the segment's end: its sums, and O once its last value product is complete
       const bool ended = mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo);
       if (!ended) *abort_flag = 1;
+      // rows' sums over the warp's tokens: at each of three steps a lane hands half of its rows to its partner
 #pragma unroll
-      for (int k = 0; k < RH; ++k) {
-        float v = lsum[k];
+      for (int o = 16, n = RH / 2; n > 0; o >>= 1, n >>= 1) {
+        const bool up = (lane & o) != 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) sm->red[(i - 1) & 1][q4][RH * h + k] = v;
+        for (int k = 0; k < n; ++k) {
+          const float mine = up ? lsum[k + n] : lsum[k], his = up ? lsum[k] : lsum[k + n];
+          lsum[k] = mine + __shfl_xor_sync(0xffffffffu, his, o);
+        }
       }
+      lsum[0] += __shfl_xor_sync(0xffffffffu, lsum[0], 2);
+      lsum[0] += __shfl_xor_sync(0xffffffffu, lsum[0], 1);
+      if ((lane & 3) == 0) sm->red[(i - 1) & 1][q4][RH * h + (lane >> 2)] = lsum[0];
       if (named_bar_sync_or(bar, kMeet, !ended || *abort_flag != 0)) break;
       const bool whole = w.ta == 0 && w.tb == w.n_tiles;
       const long long orow = whole ? static_cast<long long>(w.b) * rows_total + row0 + RH * h
                                    : (static_cast<long long>(gang) * 2 + (w.ta == 0 ? 1 : 0)) * p.row_pad + row0 + RH * h;
+      const int my_rows = nrows - RH * h;
+      const bool f32 = !whole || p.out_dtype == 2;
+      void* const dst = whole ? p.out : p.ws_o;
+      const long long first_off = orow * kRank + tl;
       float inv[RH];
 #pragma unroll
       for (int k = 0; k < RH; ++k) {
@@ -712,19 +721,22 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         }
 #pragma unroll
         for (int k = 0; k < RH; ++k) {
-          if (RH * h + k < nrows) {
-            float v = o[kTerms - 1][k];
+          float v = o[kTerms - 1][k];
 #pragma unroll
-            for (int n = kTerms - 2; n >= 0; --n) v = fmaf(v, kTermInv, o[n][k]);
-            v *= inv[k];
-            const long long off = (orow + k) * kRank + blk * 128 + tl;
-            if (!whole)
-              p.ws_o[off] = v;
-            else if (p.out_dtype == 2)
-              static_cast<float*>(p.out)[off] = v;
-            else
-              static_cast<uint16_t*>(p.out)[off] = p.out_dtype == 1 ? f2h<true>(v) : f2h<false>(v);
-          }
+          for (int n = kTerms - 2; n >= 0; --n) v = fmaf(v, kTermInv, o[n][k]);
+          o[0][k] = v * inv[k];
+        }
+        // (rows and blocks of columns at fixed distances: one address a thread)
+        if (f32) {
+          float* const at = static_cast<float*>(dst) + first_off + blk * 128;
+#pragma unroll
+          for (int k = 0; k < RH; ++k)
+            if (k < my_rows) at[k * kRank] = o[0][k];
+        } else {
+          uint16_t* const at = static_cast<uint16_t*>(dst) + first_off + blk * 128;
+#pragma unroll
+          for (int k = 0; k < RH; ++k)
+            if (k < my_rows) at[k * kRank] = p.out_dtype == 1 ? f2h<true>(o[0][k]) : f2h<false>(o[0][k]);
         }
       }
      }
@@ -752,14 +764,14 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 
 // The requests cut by gang borders: per (request, row) the parts of its gangs,
 //   M = max m_j, w_j = 2^(m_j - M), out = sum w_j O_j / sum w_j l_j, lse = M + log2 sum w_j l_j.
-// A block takes a whole row, a warp 128 columns of it, where a request has at most kFewParts parts (a batch: two or
-// three); where it has more (one long request: as many as there are gangs) 32 columns of a row, the parts shared by 16
-// lanes each. Every thread's loads are in flight at once either way; lanes' sums are added in lane order: the same
-// bits on every call.
+// A block takes a whole row, a warp 128 columns of it; where that gives less than a block an SM and a request has
+// more than kFewParts parts (one long request: as many as there are gangs), 16 columns of a row, the parts shared by
+// 32 lanes each. A thread's loads of a round are in flight at once either way; lanes' sums are added in lane order:
+// the same bits on every call.
 constexpr int kMergeThreads = 128;
-constexpr int kMergeBlocks = 4;  // per SM: one wave, each block takes units in strides
-constexpr int kFewParts = 8, kPartLanes = 16, kColLanes = kMergeThreads / kPartLanes;
-constexpr int kMergeLoads = 10;  // parts a lane has in flight: 160 gangs in a round
+constexpr int kMergeBlocks = 6;  // per SM: one wave, each block takes units in strides
+constexpr int kFewParts = 8, kPartLanes = 32, kColLanes = kMergeThreads / kPartLanes;
+constexpr int kMergeLoads = 5;   // parts a lane has in flight: 160 gangs in a round of part lanes
 constexpr int kMaxCuts = 512;    // gangs looked at
 
 // a part's weight: one without a visible token has l = 0; one whose every score is NaN has no maximum, and l NaN
@@ -775,6 +787,7 @@ __device__ __forceinline__ void fma4(float4& acc, float w, const float4 v) {
 
 struct MergeSmem {
   int count;
+  int2 cut[kMaxCuts];
   int b[kMaxCuts], j0[kMaxCuts], n[kMaxCuts], first[kMaxCuts + 1];  // the cut requests; units before each
   float4 acc[kPartLanes][kColLanes];
   float2 ml[kPartLanes];
@@ -786,12 +799,19 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_kern
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
   const int rows_total = p.q_len * p.H;
+  int all = 0;
+  for (int g0 = 0; g0 < p.gangs; g0 += kMergeThreads) {
+    const int2 c = g0 + tid < p.gangs ? __ldcg(p.ws_cut + g0 + tid) : make_int2(0, 0);
+    if (g0 + tid < p.gangs) sm.cut[g0 + tid] = c;
+    all += __syncthreads_count(c.y > 1);
+  }
+  const int few_parts = all * rows_total < p.gangs * p.groups ? kFewParts : 0x7fffffff;
   if (tid < 32) {  // the list, in gang order: the same in every block
     int count = 0, units = 0;
     for (int g0 = 0; g0 < p.gangs; g0 += 32) {
-      const int2 c = g0 + lane < p.gangs ? __ldcg(p.ws_cut + g0 + lane) : make_int2(0, 0);
+      const int2 c = g0 + lane < p.gangs ? sm.cut[g0 + lane] : make_int2(0, 0);
       const uint32_t cut = __ballot_sync(0xffffffffu, c.y > 1);
-      int mine = c.y > 1 ? rows_total * (c.y <= kFewParts ? 1 : kRank / (4 * kColLanes)) : 0, upto = mine;
+      int mine = c.y > 1 ? rows_total * (c.y <= few_parts ? 1 : kRank / (4 * kColLanes)) : 0, upto = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, upto, o);
@@ -819,7 +839,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_kern
     for (int step = kMaxCuts / 2; step > 0; step >>= 1)
       if (i + step < count && sm.first[i + step] <= unit) i += step;
     const int n = sm.n[i], rest = unit - sm.first[i];
-    const bool few = n <= kFewParts;
+    const bool few = n <= few_parts;
     const int row = few ? rest : rest / (kRank / (4 * kColLanes));
     // part x of the request: gang j0 + x, entry 1 of the first gang, entry 0 of the others
     const long long slot0 = static_cast<long long>(sm.j0[i]) * 2 * p.row_pad + row;
@@ -929,7 +949,7 @@ cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kp
   if (e != cudaSuccess) return e;
   // a block a unit, for as many requests as gang borders can cut
   const int64_t cuts = p.B < p.gangs ? p.B : p.gangs - 1;
-  const int64_t units = (cuts > 0 ? cuts : 1) * p.q_len * p.H * (p.gangs > kFewParts && p.B < p.gangs ? kRank / (4 * kColLanes) : 1);
+  const int64_t units = (cuts > 0 ? cuts : 1) * p.q_len * p.H * (cuts * p.q_len * p.H < p.gangs * p.groups ? kRank / (4 * kColLanes) : 1);
   const int64_t wave = static_cast<int64_t>(kMergeBlocks) * p.gangs * p.groups;
   cfg.gridDim = dim3(static_cast<unsigned>(units < wave ? units : wave), 1, 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);
