@@ -6,6 +6,7 @@ all computation happens in the CUDA library.
 from __future__ import annotations
 
 import dataclasses
+import heapq
 from typing import Optional, Sequence
 
 import numpy as np
@@ -244,13 +245,45 @@ class WindowPlan:
     workspace: torch.Tensor
 
 
+def _window_partitions(runs: Sequence[int], num_heads: int, q_len: int, block_size: int, dtype: str,
+                       dev: nb.mla_device_info_t) -> nb.Plan:
+    """A plan of visible runs. mla_plan's own thresholds leave runs below 4096 tokens whole, as long as most windows
+    are: the longest partition then sets the time (16 runs of 2048 tokens, 64 rows: 100 us whole, 35 us over all CTA
+    pairs). So plans with more and smaller partitions are laid out beside its own, none below the 128 tokens that a
+    CTA pair needs, and the one whose busiest pair has the least to read is taken."""
+    groups = -(-num_heads * q_len // 128)
+
+    def busiest_pair(plan: nb.Plan) -> int:
+        pairs = plan.clusters_per_chunk * (plan.cluster_ctas // 2)
+        servers = max(1, dev.max_clusters[plan.cluster_ctas.bit_length() - 1] // (groups * plan.clusters_per_chunk))
+        ends = [0] * min(servers, plan.num_chunks)
+        for _, t0, t1, _ in plan.chunks:  # in launch order, each to the pairs that are free first
+            heapq.heapreplace(ends, ends[0] + -(-(t1 - t0) // pairs))
+        parts = max(plan.o_indptr[b + 1] - plan.o_indptr[b] for b in range(len(runs)))
+        return max(ends) + 2 * parts  # the merge reads a part in about the time of two tokens
+
+    best = nb.mla_plan(runs, num_heads, q_len, block_size, dev, dtype=dtype)
+    cost = busiest_pair(best)
+    for most, split_min in [(n, 128 * n) for n in (2, 4, 8, 16, 32, 64)] + [(8, 256), (64, 256)]:
+        plan = nb.mla_plan(runs, num_heads, q_len, block_size, dev, max_partitions=most, min_partitions=1,
+                           split_min_tokens=split_min, dtype=dtype)
+        if plan.cluster_ctas > 1 and busiest_pair(plan) < cost:
+            best, cost = plan, busiest_pair(plan)
+    return best
+
+
 def plan_window(context_lens: Sequence[int], num_heads: int, q_len: int, block_size: int, window: int, sinks: int = 0,
                 dtype: str = "f16", causal: bool = False, dev: Optional[nb.mla_device_info_t] = None,
                 max_partitions: int = 0, device="cuda") -> WindowPlan:
+    """Partitions of the requests' visible runs: at most max_partitions each by mla_plan's thresholds, or (0) as many
+    as fill the device."""
     runs = nb.mla_window_lens(context_lens, q_len, block_size, causal, window, sinks)
     index = torch.device(device).index
     dev = dev if dev is not None else nb.mla_device_query(-1 if index is None else index)
-    plan = nb.mla_plan(runs, num_heads, q_len, block_size, dev, max_partitions=max_partitions, dtype=dtype)
+    if max_partitions:
+        plan = nb.mla_plan(runs, num_heads, q_len, block_size, dev, max_partitions=max_partitions, dtype=dtype)
+    else:
+        plan = _window_partitions(runs, num_heads, q_len, block_size, dtype, dev)
     part, lse = alloc_partials(plan.num_chunks, q_len, num_heads, device)
     return WindowPlan(len(runs), num_heads, q_len, block_size, dtype, causal, window, sinks, plan,
                       chunks_to_device(plan.chunks, device),
@@ -267,23 +300,27 @@ def decode_window(plan: WindowPlan, q_abs: torch.Tensor, q_pe: torch.Tensor, ckv
     B, q_len, H, bs = plan.num_requests, plan.q_len, plan.num_heads, plan.block_size
     cache_dtype = torch.uint8 if plan.dtype == "e4m3" else TORCH_DTYPE[plan.dtype]
     q_dtype = TORCH_DTYPE[query_dtype(plan.dtype)]
-    _expect(q_abs, (B, q_len, H, 512), q_dtype, "q_abs")
-    _expect(q_pe, (B, q_len, H, 64), q_dtype, "q_pe")
-    _expect(ckv, (int(ckv.shape[0]), bs, 512), cache_dtype, "ckv")
-    _expect(kpe, (int(ckv.shape[0]), bs, 64), cache_dtype, "kpe")
-    _expect(out, (B, q_len, H, 512), out.dtype, "out")
+    dev = _device_of(plan.workspace)
+    nblk, width = ckv.shape[0], block_table.shape[-1]
+    _expect(q_abs, (B, q_len, H, 512), q_dtype, "q_abs", dev)
+    _expect(q_pe, (B, q_len, H, 64), q_dtype, "q_pe", dev)
+    _expect(ckv, (nblk, bs, 512), cache_dtype, "ckv", dev)
+    _expect(kpe, (nblk, bs, 64), cache_dtype, "kpe", dev)
+    _expect(out, (B, q_len, H, 512), out.dtype, "out", dev)
     if out_lse is not None:
-        _expect(out_lse, (B, q_len, H), torch.float32, "out_lse")
-    _expect_batch(B, block_table, context_lens)
-    s = stream if stream is not None else torch.cuda.current_stream()
+        _expect(out_lse, (B, q_len, H), torch.float32, "out_lse", dev)
+    _expect(context_lens, (B,), torch.int32, "context_lens", dev)
+    _expect(block_table, (B, width), torch.int32, "block_table", dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
     p = plan.plan
-    d = nb.mla_decode_desc_t(B, H, q_len, bs, int(ckv.shape[0]), int(block_table.shape[1]), nb.DTYPE_CODES[plan.dtype],
+    d = nb.mla_decode_desc_t(B, H, q_len, bs, nblk, width, nb.DTYPE_CODES[plan.dtype],
                              1 if plan.causal else 0, plan.chunks.data_ptr(), p.num_chunks, p.cluster_ctas,
-                             nb.MLA_KERNEL_TC, s.cuda_stream, p.clusters_per_chunk, plan.workspace.data_ptr(),
+                             nb.MLA_KERNEL_TC, stream.cuda_stream, p.clusters_per_chunk, plan.workspace.data_ptr(),
                              plan.workspace.numel(), 0, 0, 0, cache_scale, 0)
     nb.mla_decode_window(q_abs.data_ptr(), q_pe.data_ptr(), ckv.data_ptr(), kpe.data_ptr(), block_table.data_ptr(),
                          context_lens.data_ptr(), scale, 0, plan.partials.data_ptr(), plan.lse.data_ptr(),
-                         plan.o_indptr.data_ptr(), out.data_ptr(), CODE_OF[out.dtype],
+                         plan.o_indptr.data_ptr(), out.data_ptr(), _code_of(out, "out"),
                          out_lse.data_ptr() if out_lse is not None else None, plan.window, plan.sinks, d)
     return out
 
@@ -304,27 +341,36 @@ class Q8Cache:
 
     def __post_init__(self):
         nblk, bs = int(self.ckv.shape[0]), int(self.ckv.shape[1])
-        _expect(self.ckv, (nblk, bs, 512), torch.uint8, "ckv")
-        _expect(self.kpe, (nblk, bs, 64), torch.uint8, "kpe")
+        dev = self.ckv.get_device()
+        _expect(self.ckv, (nblk, bs, 512), torch.uint8, "ckv", dev)
+        _expect(self.kpe, (nblk, bs, 64), torch.uint8, "kpe", dev)
         if self.scales.dim() != 2 or self.scales.shape[1] < 1 or bs % int(self.scales.shape[1]):
             raise ValueError(f"scales: {tuple(self.scales.shape)} does not divide pages of {bs} tokens")
-        _expect(self.scales, (nblk, int(self.scales.shape[1])), torch.float32, "scales")
-
-    @property
-    def scale_block(self) -> int:
-        return int(self.ckv.shape[1]) // int(self.scales.shape[1])
+        _expect(self.scales, (nblk, int(self.scales.shape[1])), torch.float32, "scales", dev)
+        self.num_blocks, self.block_size = nblk, bs
+        self.scale_block = bs // int(self.scales.shape[1])
 
 
-def _expect(t: torch.Tensor, shape, dtype, what: str) -> None:
-    """The C ABI takes raw pointers to dense row-major buffers: anything else is refused here."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)}{'' if t.is_contiguous() else ' with strides ' + str(t.stride())}")
+def _device_of(t: torch.Tensor) -> int:
+    """The library launches on the current device: a buffer that is elsewhere is refused here."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"a buffer on {t.device}: the call runs on the current CUDA device")
+    return dev
 
 
-def _expect_batch(B: int, block_table: torch.Tensor, context_lens: torch.Tensor) -> None:
-    _expect(context_lens, (B,), torch.int32, "context_lens")
-    _expect(block_table, (B, int(block_table.shape[-1])), torch.int32, "block_table")
+def _expect(t: torch.Tensor, shape, dtype, what: str, dev: int) -> None:
+    """The C ABI takes raw pointers to dense row-major buffers of one device: anything else is refused here."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {shape} beside the call's other "
+                         f"buffers, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _code_of(t: torch.Tensor, what: str) -> int:
+    code = CODE_OF.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what}: {t.dtype} is none of {', '.join(str(k) for k in CODE_OF)}")
+    return code
 
 
 def alloc_q8_cache(num_blocks: int, block_size: int, scale_block: int, device="cuda") -> Q8Cache:
@@ -337,15 +383,19 @@ def alloc_q8_cache(num_blocks: int, block_size: int, scale_block: int, device="c
 def cache_append_q8(cache: Q8Cache, ckv_new: torch.Tensor, kpe_new: torch.Tensor, block_table: torch.Tensor,
                     context_lens: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Quantize each request's newest tokens [B, q_len, 512 / 64] into the cache (mla_cache_append_q8)."""
-    B, q_len = int(ckv_new.shape[0]), int(ckv_new.shape[1])
-    _expect(ckv_new, (B, q_len, 512), ckv_new.dtype, "ckv_new")
-    _expect(kpe_new, (B, q_len, 64), ckv_new.dtype, "kpe_new")
-    _expect_batch(B, block_table, context_lens)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    nb.mla_cache_append_q8(ckv_new.data_ptr(), kpe_new.data_ptr(), CODE_OF[ckv_new.dtype], block_table.data_ptr(),
-                           context_lens.data_ptr(), B, q_len, int(cache.ckv.shape[1]), cache.scale_block,
-                           int(cache.ckv.shape[0]), int(block_table.shape[1]), cache.ckv.data_ptr(),
-                           cache.kpe.data_ptr(), cache.scales.data_ptr(), s.cuda_stream)
+    dev = _device_of(cache.ckv)
+    B, q_len = ckv_new.shape[0], ckv_new.shape[1]
+    width = block_table.shape[-1]
+    _expect(ckv_new, (B, q_len, 512), ckv_new.dtype, "ckv_new", dev)
+    _expect(kpe_new, (B, q_len, 64), ckv_new.dtype, "kpe_new", dev)
+    _expect(context_lens, (B,), torch.int32, "context_lens", dev)
+    _expect(block_table, (B, width), torch.int32, "block_table", dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    nb.mla_cache_append_q8(ckv_new.data_ptr(), kpe_new.data_ptr(), _code_of(ckv_new, "ckv_new"),
+                           block_table.data_ptr(), context_lens.data_ptr(), B, q_len, cache.block_size,
+                           cache.scale_block, cache.num_blocks, width, cache.ckv.data_ptr(), cache.kpe.data_ptr(),
+                           cache.scales.data_ptr(), stream.cuda_stream)
 
 
 @dataclasses.dataclass
@@ -376,16 +426,22 @@ def decode_q8(plan: Q8Plan, q_abs: torch.Tensor, q_pe: torch.Tensor, cache: Q8Ca
               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """One decode layer call over a block-scaled 8-bit cache (mla_decode_q8), into out [B, q_len, H, 512]."""
     B, q_len, H = plan.num_requests, plan.q_len, plan.num_heads
-    _expect(q_abs, (B, q_len, H, 512), q_abs.dtype, "q_abs")
-    _expect(q_pe, (B, q_len, H, 64), q_abs.dtype, "q_pe")
-    _expect(out, (B, q_len, H, 512), out.dtype, "out")
+    dev = _device_of(plan.workspace)
+    width = block_table.shape[-1]
+    _expect(q_abs, (B, q_len, H, 512), q_abs.dtype, "q_abs", dev)
+    _expect(q_pe, (B, q_len, H, 64), q_abs.dtype, "q_pe", dev)
+    _expect(out, (B, q_len, H, 512), out.dtype, "out", dev)
     if out_lse is not None:
-        _expect(out_lse, (B, q_len, H), torch.float32, "out_lse")
-    _expect_batch(B, block_table, context_lens)
-    d = nb.mla_q8_desc_t(B, H, q_len, int(cache.ckv.shape[1]), int(cache.ckv.shape[0]), int(block_table.shape[1]),
-                         CODE_OF[q_abs.dtype], 1 if plan.causal else 0, cache.scale_block, plan.window, plan.sinks,
-                         CODE_OF[out.dtype], plan.workspace.data_ptr(), plan.workspace.numel(),
-                         (stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+        _expect(out_lse, (B, q_len, H), torch.float32, "out_lse", dev)
+    _expect(context_lens, (B,), torch.int32, "context_lens", dev)
+    _expect(block_table, (B, width), torch.int32, "block_table", dev)
+    if cache.ckv.get_device() != dev:
+        raise ValueError(f"cache: on {cache.ckv.device}, the plan's workspace on {plan.workspace.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    d = nb.mla_q8_desc_t(B, H, q_len, cache.block_size, cache.num_blocks, width, _code_of(q_abs, "q_abs"),
+                         1 if plan.causal else 0, cache.scale_block, plan.window, plan.sinks, _code_of(out, "out"),
+                         plan.workspace.data_ptr(), plan.workspace.numel(), stream.cuda_stream)
     nb.mla_decode_q8(q_abs.data_ptr(), q_pe.data_ptr(), cache.ckv.data_ptr(), cache.kpe.data_ptr(),
                      cache.scales.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), scale,
                      out.data_ptr(), out_lse.data_ptr() if out_lse is not None else None, d)
