@@ -965,6 +965,7 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
   p.out_dtype = d->out_dtype;
   p.gangs = mla::q8_gangs(rows, sms);
   p.groups = (rows + nr - 1) / nr;
+  p.cuts_by_request = static_cast<int64_t>(p.B) * rows < static_cast<int64_t>(p.gangs) * p.groups ? 1 : 0;
   p.row_pad = p.groups * nr;
   p.tile = mla::q8_tile_tokens(rows, d->dtype == MLA_BF16);
   p.ws_o = static_cast<float*>(d->workspace);

@@ -55,8 +55,8 @@ struct Cfg {
   static constexpr int kQTerms = BF16 ? 2 : 3, kTerms = NR == 16 ? 4 : 3;
   // The reference maximum moves when a score passes it by more than kTau, so weights are at most 2^kTau; times
   // 2^kWeightExp they fit E4M3's 448, and its subnormals reach down to 2^-25 of the reference in the last term.
-  static constexpr float kTau = NR == 16 ? 7.0f : 2.0f;
-  static constexpr int kWeightExp = NR == 16 ? 1 : 6;
+  static constexpr float kTau = NR == 16 ? 7.0f : (BF16 ? 6.0f : 4.0f);
+  static constexpr int kWeightExp = NR == 16 ? 1 : (BF16 ? 2 : 4);
   static constexpr int kNS = NR * kQTerms, kNP = NR * kTerms;      // N of the two products
   static constexpr int kSBufs = (4 * kNP + 2 * kNS <= 512) ? 2 : 1;  // score buffers in tensor memory
   static constexpr int kT = (NR == 32 && !BF16) ? 128 : 96;        // tokens per tile
@@ -271,14 +271,12 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
                                             h2f<BF16>(static_cast<uint16_t>(w >> 16)) * up);
         split_f16<C::kQTerms>(*reinterpret_cast<const uint32_t*>(&f), t[y]);
       }
+      // columns 8 lane .. + 7 of latent half x (or of the rope part)
+      uint8_t* at = x < 2 ? q + (2 * x + (lane >> 4)) * C::kQChunk + r * 128 + (((lane >> 1) ^ r) & 7) * 16 + (lane & 1) * 8
+                          : q + 4 * C::kQChunk + r * 64 + (((lane >> 1) ^ (r >> 1)) & 3) * 16 + (lane & 1) * 8;
 #pragma unroll
-      for (int n = 0; n < C::kQTerms; ++n) {
-        const int row = n * NR + r;
-        // columns 8 lane .. + 7 of latent half x (or of the rope part)
-        uint8_t* const at = x < 2 ? q + (2 * x + (lane >> 4)) * C::kQChunk + row * 128 + (((lane >> 1) ^ row) & 7) * 16 + (lane & 1) * 8
-                                  : q + 4 * C::kQChunk + row * 64 + (((lane >> 1) ^ (row >> 1)) & 3) * 16 + (lane & 1) * 8;
-        *reinterpret_cast<uint2*>(at) = make_uint2(t[0][n] | (t[1][n] << 16), t[2][n] | (t[3][n] << 16));
-      }
+      for (int n = 0; n < C::kQTerms; ++n)  // (NR rows on: the same swizzle)
+        *reinterpret_cast<uint2*>(at + n * NR * (x < 2 ? 128 : 64)) = make_uint2(t[0][n] | (t[1][n] << 16), t[2][n] | (t[3][n] << 16));
     }
   };
   if (warp == C::kLoadWarp) {
@@ -389,9 +387,15 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     if (lane == 0) {
       int i = 0;
       bool first = true, ok = true;
+      // gangs that a request which starts in this one is cut into
+      auto parts_of = [&](const Q8Walk& w) -> int {
+        return w.tb < w.n_tiles ? line.gang_of(hi + (w.n_tiles - w.tb) - 1) - gang + 1 : 1;
+      };
       for (int seg = 0; ok && q8_next<kT>(p, lens, w, first); ++seg, first = false) {
         const uint32_t q = base + C::kOffQ;
         const Desc2 bd = desc2(smem_desc_sw128(q, 16, 1024)), bk = desc2(smem_desc_sw64(q + 4 * C::kQChunk, 512));
+        if (p.cuts_by_request && w.ta == 0 && blockIdx.x == 0)  // a request that starts here: its gangs, for the merge
+          p.ws_cut[w.b] = make_int2(gang, parts_of(w));
         ok = mbar_wait(&sm->qfull, seg & 1, tmo);
         for (int tile = w.ta; ok && tile < w.tb; ++tile, ++i) {
           ok = mbar_wait(&sm->full[i % kSlots], (i / kSlots) & 1, tmo) &&
@@ -412,11 +416,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         }
       }
       if (!ok) *abort_flag = 1;
-      // (after the last segment) a request that starts here and goes on: its parts, for the merge
-      if (blockIdx.x == 0) {
-        const bool cut = N > 0 && w.ta == 0 && w.tb < w.n_tiles;
-        p.ws_cut[gang] = make_int2(w.b, cut ? line.gang_of(hi + (w.n_tiles - w.tb) - 1) - gang + 1 : 0);
-      }
+      // ... and (after the last segment) the request at this gang's open end
+      if (!p.cuts_by_request && blockIdx.x == 0) p.ws_cut[gang] = make_int2(w.b, N > 0 && w.ta == 0 ? parts_of(w) : 0);
       umma_commit(&sm->drain[0]);  // every MMA issued has completed before TMEM is freed
       mbar_wait(&sm->drain[0], 0, kDrainTimeoutNs);
     }
@@ -484,12 +485,12 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     // the request's output. The first round only splits.
     Q8Walk next = w;
     bool more = q8_next<kT>(p, lens, next, true);
+    float z_raw = 1.f;  // the scale of this thread's token in the next tile, and its page in the one after that
+    int pid = -1;
     for (int seg = -1;; ++seg) {
      bool stop = false;
      float lsum[RH], mr[RH];
      if (seg >= 0) {
-      float z_raw = scale_at(page_at(w, w.ta), w.ta);
-      int pid = w.ta + 1 < w.tb ? page_at(w, w.ta + 1) : -1;
 #pragma unroll
       for (int k = 0; k < RH; ++k) {
         lsum[k] = 0.f;
@@ -654,6 +655,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
      if (stop) break;
      if (more) {
       // (their scores done, nothing reads the last request's queries any more)
+      pid = page_at(next, next.ta);
       QueryRow row = load_query(next.b, warp);
 #pragma unroll 1
       for (int r = warp; r < NR; r += kSoftmaxWarps) {
@@ -664,6 +666,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->qfull);
+      z_raw = scale_at(pid, next.ta);
+      pid = next.ta + 1 < next.tb ? page_at(next, next.ta + 1) : -1;
      }
      if (seg >= 0) {
       // the segment's end: its sums, and O once its last value product is complete
@@ -690,22 +694,25 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       const bool f32 = !whole || p.out_dtype == 2;
       void* const dst = whole ? p.out : p.ws_o;
       const long long first_off = orow * kRank + tl;
-      float inv[RH];
+      // lane k (mod 8) works out row k's factor
+      float m = mr[0];
 #pragma unroll
-      for (int k = 0; k < RH; ++k) {
-        const int r = RH * h + k;
-        const auto& sum = sm->red[(i - 1) & 1];
-        const float l = (sum[0][r] + sum[1][r]) + (sum[2][r] + sum[3][r]);
-        inv[k] = !whole ? w_down : (l == 0.f ? 0.f : w_down / l);  // (no visible token: every weight was 0)
-        if (r < nrows && q4 == 0 && lane == 0) {
-          if (!whole) {
-            p.ws_ml[(orow + k) * 2] = mr[k];
-            p.ws_ml[(orow + k) * 2 + 1] = l;
-          } else if (p.out_lse != nullptr) {
-            p.out_lse[orow + k] = l == 0.f ? -INFINITY : ((mr[k] == -INFINITY) ? 0.f : mr[k]) + log2f(l);
-          }
+      for (int k = 1; k < RH; ++k)
+        if ((lane & (RH - 1)) == k) m = mr[k];
+      const int r = RH * h + (lane & (RH - 1));
+      const auto& sum = sm->red[(i - 1) & 1];
+      const float l = (sum[0][r] + sum[1][r]) + (sum[2][r] + sum[3][r]);
+      const float my_inv = !whole ? w_down : (l == 0.f ? 0.f : w_down / l);  // (no visible token: every weight was 0)
+      if (q4 == 0 && lane < my_rows && lane < RH) {
+        if (!whole) {
+          *reinterpret_cast<float2*>(p.ws_ml + (orow + lane) * 2) = make_float2(m, l);
+        } else if (p.out_lse != nullptr) {
+          p.out_lse[orow + lane] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(l);
         }
       }
+      float inv[RH];
+#pragma unroll
+      for (int k = 0; k < RH; ++k) inv[k] = __shfl_sync(0xffffffffu, my_inv, k);
       tc_fence_after();
 #pragma unroll 1
       for (int blk = 0; blk < 4; ++blk) {
@@ -748,6 +755,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
   // requests with nothing to see
   for (int b = gang; b < p.B; b += p.gangs) {
     if (q8_view(p, lens(b)).n != 0) continue;
+    if (p.cuts_by_request && blockIdx.x == 0 && tid == 0) p.ws_cut[b] = make_int2(gang, 0);
     for (int x = tid; x < nrows * (kRank / 4); x += kThreads) {
       const long long at = static_cast<long long>(b) * rows_total + row0 + x / (kRank / 4);
       store_out4(p.out, p.out_dtype, at * kRank + 4 * (x % (kRank / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
@@ -764,19 +772,16 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 
 // The requests cut by gang borders: per (request, row) the parts of its gangs,
 //   M = max m_j, w_j = 2^(m_j - M), out = sum w_j O_j / sum w_j l_j, lse = M + log2 sum w_j l_j.
-// A block takes a whole row, a warp 128 columns of it; where that gives less than a block an SM and a request has
-// more than kFewParts parts (one long request: as many as there are gangs), 16 columns of a row, the parts shared by
-// 32 lanes each. A thread's loads of a round are in flight at once either way; lanes' sums are added in lane order:
-// the same bits on every call.
-constexpr int kMergeThreads = 128;
-constexpr int kMergeBlocks = 6;  // per SM: one wave, each block takes units in strides
-constexpr int kFewParts = 8, kPartLanes = 32, kColLanes = kMergeThreads / kPartLanes;
-constexpr int kMergeLoads = 5;   // parts a lane has in flight: 160 gangs in a round of part lanes
-constexpr int kMaxCuts = 512;    // gangs looked at
+// Two kernels, by what there is to share out; in both, sums are added in a fixed order: the same bits on every call.
+// Their time is one chain of loads (an entry of ws_cut, then a row's parts) and the fetch and issue of their code, so
+// both keep it short, and a warp asks for its own entry of ws_cut only (a list of all entries made by every block:
+// the same lines asked for by a thousand blocks, 1 to 3 us).
+constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeBlocks = 7;  // per SM: one wave
 
 // a part's weight: one without a visible token has l = 0; one whose every score is NaN has no maximum, and l NaN
-__device__ __forceinline__ float part_weight(float2 ml, float ref) {
-  return ml.y == 0.f ? 0.f : (ml.x == -INFINITY ? 1.f : exp2f(ml.x - ref));
+__device__ __forceinline__ float part_weight(float m, float l, float ref) {
+  return l == 0.f ? 0.f : (m == -INFINITY ? 1.f : exp2f(m - ref));
 }
 __device__ __forceinline__ void fma4(float4& acc, float w, const float4 v) {
   acc.x = fmaf(w, v.x, acc.x);
@@ -785,84 +790,110 @@ __device__ __forceinline__ void fma4(float4& acc, float w, const float4 v) {
   acc.w = fmaf(w, v.w, acc.w);
 }
 
-struct MergeSmem {
-  int count;
-  int2 cut[kMaxCuts];
-  int b[kMaxCuts], j0[kMaxCuts], n[kMaxCuts], first[kMaxCuts + 1];  // the cut requests; units before each
-  float4 acc[kPartLanes][kColLanes];
-  float2 ml[kPartLanes];
+// the parts of row `row` of a request whose first gang is j0: gang j0's in entry 1, the others' in entry 0
+struct MergeParts {
+  const float2* ml;
+  const float* o;
+  long long slot0, pitch;
+  __device__ __forceinline__ MergeParts(const DecodeQ8Params& p, int j0, int row)
+      : ml(reinterpret_cast<const float2*>(p.ws_ml)), o(p.ws_o),
+        slot0(static_cast<long long>(j0) * 2 * p.row_pad + row), pitch(p.row_pad) {}
+  __device__ __forceinline__ long long slot(int x) const { return slot0 + (x == 0 ? 1 : 2 * x) * pitch; }
+  __device__ __forceinline__ float2 max_sum(int x) const { return __ldcg(ml + slot(x)); }
+  __device__ __forceinline__ float4 values(int x, int col) const {
+    return __ldcg(reinterpret_cast<const float4*>(o + slot(x) * kRank + col));
+  }
 };
+// (a call that gave up has left entries as they were: they lead nowhere outside the buffers)
+__device__ __forceinline__ bool merge_entry_ok(const DecodeQ8Params& p, int b, int j0, int n) {
+  return n > 1 && n <= p.gangs && j0 >= 0 && j0 <= p.gangs - n && b >= 0 && b < p.B;
+}
+__device__ __forceinline__ void merge_out(const DecodeQ8Params& p, long long br, int col, float4 acc, float inv) {
+  store_out4(p.out, p.out_dtype, br * kRank + col, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+}
 
-__global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_kernel(const DecodeQ8Params p) {
-  __shared__ MergeSmem sm;
+// Batches whose rows fill the device: a warp a (gang, row), which ends at once where no request with that gang as
+// its first is cut. Lane x weighs part x, then each part's 512 columns go by 16 a lane (with a block a row, 4
+// columns a lane, the weights' code run by every warp was most of the time: 8 us for 3000 rows of 2 to 3 parts).
+__global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_rows_kernel(const DecodeQ8Params p) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t rows_total = p.q_len * p.H, units = p.gangs * rows_total;
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int rows_total = p.q_len * p.H;
-  int all = 0;
-  for (int g0 = 0; g0 < p.gangs; g0 += kMergeThreads) {
-    const int2 c = g0 + tid < p.gangs ? __ldcg(p.ws_cut + g0 + tid) : make_int2(0, 0);
-    if (g0 + tid < p.gangs) sm.cut[g0 + tid] = c;
-    all += __syncthreads_count(c.y > 1);
-  }
-  const int few_parts = all * rows_total < p.gangs * p.groups ? kFewParts : 0x7fffffff;
-  if (tid < 32) {  // the list, in gang order: the same in every block
-    int count = 0, units = 0;
-    for (int g0 = 0; g0 < p.gangs; g0 += 32) {
-      const int2 c = g0 + lane < p.gangs ? sm.cut[g0 + lane] : make_int2(0, 0);
-      const uint32_t cut = __ballot_sync(0xffffffffu, c.y > 1);
-      int mine = c.y > 1 ? rows_total * (c.y <= few_parts ? 1 : kRank / (4 * kColLanes)) : 0, upto = mine;
+  for (uint32_t unit = blockIdx.x * kMergeWarps + (threadIdx.x >> 5); unit < units; unit += gridDim.x * kMergeWarps) {
+    const int j0 = unit / rows_total, row = unit % rows_total;
+    const int2 cut = __ldcg(p.ws_cut + j0);
+    const int n = cut.y;
+    if (!merge_entry_ok(p, cut.x, j0, n)) continue;
+    const MergeParts parts(p, j0, row);
+    float M = -INFINITY, den = 0.f;
+    float4 acc[4];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int x0 = 0; x0 < n; x0 += 32) {
+      const float2 ml = x0 + lane < n ? parts.max_sum(x0 + lane) : make_float2(-INFINITY, 0.f);
+      const float m = fmaxf(M, warp_max(ml.x)), ref = m == -INFINITY ? 0.f : m;
+      const float al = M == -INFINITY ? 1.f : exp2f(M - ref);  // (nothing summed before the first, or only NaN)
+      const float w = part_weight(ml.x, ml.y, ref);
+      float sum = w * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      den = fmaf(den, al, sum);
+      M = m;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] = make_float4(acc[k].x * al, acc[k].y * al, acc[k].z * al, acc[k].w * al);
+      const int here = min(32, n - x0);
+#pragma unroll 2
+      for (int x = 0; x < here; ++x) {
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = parts.values(x0 + x, 4 * lane + 128 * k);
+        const float wx = __shfl_sync(0xffffffffu, w, x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) fma4(acc[k], wx, v[k]);
       }
-      if (c.y > 1) {
-        const int at = count + __popc(cut & ((1u << lane) - 1u));
-        sm.b[at] = c.x;
-        sm.j0[at] = g0 + lane;
-        sm.n[at] = c.y;
-        sm.first[at] = units + upto - mine;
-      }
-      count += __popc(cut);
-      units += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (lane == 0) {
-      sm.count = count;
-      sm.first[count] = units;
-    }
+    const long long br = static_cast<long long>(cut.x) * rows_total + row;
+    const bool none = den == 0.f;
+    const float inv = none ? 0.f : 1.f / den;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) merge_out(p, br, 4 * lane + 128 * k, acc[k], inv);
+    if (p.out_lse != nullptr && lane == 0) p.out_lse[br] = none ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(den);
   }
-  __syncthreads();
-  const int count = sm.count, units = sm.first[count];
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    int i = 0;  // the last of the list that starts at or before the unit
-    for (int step = kMaxCuts / 2; step > 0; step >>= 1)
-      if (i + step < count && sm.first[i + step] <= unit) i += step;
-    const int n = sm.n[i], rest = unit - sm.first[i];
-    const bool few = n <= few_parts;
-    const int row = few ? rest : rest / (kRank / (4 * kColLanes));
-    // part x of the request: gang j0 + x, entry 1 of the first gang, entry 0 of the others
-    const long long slot0 = static_cast<long long>(sm.j0[i]) * 2 * p.row_pad + row;
-    auto slot = [&](int x) { return slot0 + static_cast<long long>(x == 0 ? 1 : 2 * x) * p.row_pad; };
-    const int e = few ? 0 : tid / kColLanes, lanes = few ? 1 : kPartLanes;
-    const int c = few ? 4 * tid : (rest % (kRank / (4 * kColLanes))) * 4 * kColLanes + 4 * (tid % kColLanes);
+}
+
+// Few rows (one long request: each in as many parts as there are gangs): a block 16 columns of a row, the parts
+// shared by 32 lanes, a lane's loads of a round in flight at once.
+constexpr int kPartLanes = 32, kColLanes = kMergeThreads / kPartLanes, kColUnits = kRank / (4 * kColLanes);
+constexpr int kMergeLoads = 5;   // 160 gangs in a round
+__global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_parts_kernel(const DecodeQ8Params p) {
+  __shared__ float4 sm_acc[kMergeWarps][kColLanes];
+  __shared__ float sm_m[kMergeWarps], sm_den[kMergeWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int e = tid / kColLanes, rows_total = p.q_len * p.H;
+  const uint32_t per_request = rows_total * kColUnits, units = per_request * p.B;
+  pdl_wait();
+  pdl_launch_dependents();
+  for (uint32_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int b = unit / per_request, rest = unit % per_request, row = rest / kColUnits;
+    const int2 cut = __ldcg(p.ws_cut + b);
+    const int n = cut.y, col = rest % kColUnits * 4 * kColLanes + 4 * (tid % kColLanes);
+    if (!merge_entry_ok(p, b, cut.x, n)) continue;
+    const MergeParts parts(p, cut.x, row);
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int x0 = e; x0 < n; x0 += lanes * kMergeLoads) {
+    for (int x0 = e; x0 < n; x0 += kPartLanes * kMergeLoads) {
       float2 ml[kMergeLoads];
       float4 v[kMergeLoads];
+      float m = M;
 #pragma unroll
       for (int y = 0; y < kMergeLoads; ++y) {
-        const int x = x0 + lanes * y;
-        ml[y] = make_float2(-INFINITY, 0.f);
-        v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x < n) {
-          ml[y] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + slot(x) * 2));
-          v[y] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(x) * kRank + c));
-        }
+        const int x = x0 + kPartLanes * y;
+        ml[y] = x < n ? parts.max_sum(x) : make_float2(-INFINITY, 0.f);
+        v[y] = x < n ? parts.values(x, col) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      float m = M;
 #pragma unroll
       for (int y = 0; y < kMergeLoads; ++y) m = fmaxf(m, ml[y].x);
       const float ref = m == -INFINITY ? 0.f : m;
@@ -872,39 +903,38 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_kern
       M = m;
 #pragma unroll
       for (int y = 0; y < kMergeLoads; ++y) {
-        const float w = part_weight(ml[y], ref);
+        const float w = part_weight(ml[y].x, ml[y].y, ref);
         den = fmaf(w, ml[y].y, den);
         fma4(acc, w, v[y]);
       }
     }
-    if (!few) {  // lanes' sums, each a part of its own
-      sm.acc[e][tid % kColLanes] = acc;
-      if (tid % kColLanes == 0) sm.ml[e] = make_float2(M, den);
-      __syncthreads();
-      M = -INFINITY;
+    // lanes' sums, each a part of its own: over the warp's 8 part lanes, then over the warps
+    float m = M;
 #pragma unroll
-      for (int y = 0; y < kPartLanes; ++y) M = fmaxf(M, sm.ml[y].x);
-      const float ref = M == -INFINITY ? 0.f : M;
-      den = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (e == 0) {
+    for (int o = kColLanes; o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) sm_m[warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+    const float w = part_weight(M, den, m == -INFINITY ? 0.f : m);
+    float s[5] = {den * w, acc.x * w, acc.y * w, acc.z * w, acc.w * w};
 #pragma unroll
-        for (int y = 0; y < kPartLanes; ++y) {
-          const float2 ml = sm.ml[y];
-          const float w = part_weight(ml, ref);
-          den += w * ml.y;
-          fma4(acc, w, sm.acc[y][tid]);
-        }
-      }
-      __syncthreads();
-    }
+    for (int o = kColLanes; o < 32; o *= 2)
+#pragma unroll
+      for (int k = 0; k < 5; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    if (lane < kColLanes) sm_acc[warp][lane] = make_float4(s[1], s[2], s[3], s[4]);
+    if (lane == 0) sm_den[warp] = s[0];
+    __syncthreads();
     if (e == 0) {
-      const long long br = static_cast<long long>(sm.b[i]) * rows_total + row;
+      den = (sm_den[0] + sm_den[1]) + (sm_den[2] + sm_den[3]);
+      acc = sm_acc[0][lane];
+#pragma unroll
+      for (int k = 1; k < kMergeWarps; ++k) fma4(acc, 1.f, sm_acc[k][lane]);
+      const long long br = static_cast<long long>(b) * rows_total + row;
       const bool none = den == 0.f;
-      const float inv = none ? 0.f : 1.f / den;
-      store_out4(p.out, p.out_dtype, br * kRank + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-      if (p.out_lse != nullptr && c == 0) p.out_lse[br] = none ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(den);
+      merge_out(p, br, col, acc, none ? 0.f : 1.f / den);
+      if (p.out_lse != nullptr && col == 0) p.out_lse[br] = none ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(den);
     }
+    __syncthreads();
   }
 }
 
@@ -929,7 +959,7 @@ int q8_tile_tokens(int total_rows, bool bf16) {
 int q8_gangs(int total_rows, int sms) {
   const int nr = q8_rows_per_cta(total_rows), groups = (total_rows + nr - 1) / nr;
   const int gangs = sms > groups ? sms / groups : 1;
-  return gangs < kMaxCuts ? gangs : kMaxCuts;
+  return gangs;
 }
 
 cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kpe, const DecodeQ8Params& p, bool bf16,
@@ -947,14 +977,14 @@ cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kp
   else
     e = bf16 ? launch<32, true>(cfg, tm_ckv, tm_kpe, p) : launch<32, false>(cfg, tm_ckv, tm_kpe, p);
   if (e != cudaSuccess) return e;
-  // a block a unit, for as many requests as gang borders can cut
-  const int64_t cuts = p.B < p.gangs ? p.B : p.gangs - 1;
-  const int64_t units = (cuts > 0 ? cuts : 1) * p.q_len * p.H * (cuts * p.q_len * p.H < p.gangs * p.groups ? kRank / (4 * kColLanes) : 1);
+  if (p.gangs == 1) return cudaSuccess;  // nothing is cut
+  const int64_t rows = static_cast<int64_t>(p.q_len) * p.H;
+  const int64_t blocks = p.cuts_by_request ? rows * p.B * kColUnits : (rows * p.gangs + kMergeWarps - 1) / kMergeWarps;
   const int64_t wave = static_cast<int64_t>(kMergeBlocks) * p.gangs * p.groups;
-  cfg.gridDim = dim3(static_cast<unsigned>(units < wave ? units : wave), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < wave ? blocks : wave), 1, 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, mla_merge_q8_kernel, p);
+  return cudaLaunchKernelEx(&cfg, p.cuts_by_request ? mla_merge_q8_parts_kernel : mla_merge_q8_rows_kernel, p);
 }
 
 cudaError_t decode_q8_read_clear_error(uint32_t* out) {

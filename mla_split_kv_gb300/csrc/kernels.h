@@ -174,12 +174,14 @@ struct DecodeQ8Params {
   float* out_lse;              // [B, q_len, H] or null
   float* ws_o;                 // [gangs, 2, row_pad, 512] unnormalized O of a gang's two open ends
   float* ws_ml;                // [gangs, 2, row_pad, 2] their row maxima and sums
-  int2* ws_cut;                // [gangs] the request that starts in a gang and goes on in others, and its parts (0: none)
+  int2* ws_cut;                // by gang, the request that starts there and goes on in others, and its parts (0: none); with
+                               // cuts_by_request by request, its first gang and its parts
   float scale_log2;            // softmax scale * log2(e)
   int32_t B, H, h_shift, q_len, bs, bs_shift, max_blocks, num_blocks, g_shift, causal, window, sinks, out_dtype;
   int32_t gangs;               // CTAs that share the tiles of the batch, one per row group each
   int32_t groups, row_pad;     // row groups; rows padded to whole groups
   int32_t tile;                // tokens per tile
+  int32_t cuts_by_request;     // the batch has fewer rows than the grid has CTAs
   uint64_t timeout_ns;
 };
 // Rows per CTA, tokens per tile and gangs of the launch for q_len * H rows on a device of `sms` SMs.

@@ -92,19 +92,28 @@ __device__ __forceinline__ Q8Walk q8_walk(int b0, int64_t off0, int64_t tiles) {
   w.left = tiles;
   return w;
 }
-// The next segment; false at the end.
+// The next segment; false at the end. (Its search is one function for all roles: code that is met once costs what
+// it takes to fetch, some ten cycles an instruction, and so it has been fetched after the first role's call.)
+template <int kT>
+__device__ __noinline__ Q8Walk q8_search(const int32_t* lens_global, const int32_t* lens_cached, int q_len, int bs,
+                                         int causal, int window, int sinks, int b, int start, int64_t left) {
+  const Q8Lens lens{lens_global, lens_cached};
+  Q8Walk w;
+  do {
+    ++b;
+    w.v = window_view(lens(b), q_len, bs, causal, window, sinks);
+    w.n_tiles = q8_tiles(w.v, kT);
+  } while (w.n_tiles == 0);
+  w.b = b;
+  w.ta = start;
+  w.tb = static_cast<int>(w.n_tiles < start + left ? w.n_tiles : start + left);
+  w.left = left - (w.tb - start);
+  return w;
+}
 template <int kT>
 __device__ __forceinline__ bool q8_next(const DecodeQ8Params& p, const Q8Lens& lens, Q8Walk& w, bool first) {
   if (w.left <= 0) return false;
-  const int start = first ? w.tb : 0;
-  do {
-    ++w.b;
-    w.v = q8_view(p, lens(w.b));
-    w.n_tiles = q8_tiles(w.v, kT);
-  } while (w.n_tiles == 0);
-  w.ta = start;
-  w.tb = static_cast<int>(w.n_tiles < start + w.left ? w.n_tiles : start + w.left);
-  w.left -= w.tb - w.ta;
+  w = q8_search<kT>(lens.global, lens.cached, p.q_len, p.bs, p.causal, p.window, p.sinks, w.b, first ? w.tb : 0, w.left);
   return true;
 }
 
