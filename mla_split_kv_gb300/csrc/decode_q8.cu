@@ -55,8 +55,8 @@ struct Cfg {
   static constexpr int kQTerms = BF16 ? 2 : 3, kTerms = NR == 16 ? 4 : 3;
   // The reference maximum moves when a score passes it by more than kTau, so weights are at most 2^kTau; times
   // 2^kWeightExp they fit E4M3's 448, and its subnormals reach down to 2^-25 of the reference in the last term.
-  static constexpr float kTau = NR == 16 ? 7.0f : (BF16 ? 6.0f : 4.0f);
-  static constexpr int kWeightExp = NR == 16 ? 1 : (BF16 ? 2 : 4);
+  static constexpr float kTau = NR == 16 ? 7.0f : 2.0f;
+  static constexpr int kWeightExp = NR == 16 ? 1 : 6;
   static constexpr int kNS = NR * kQTerms, kNP = NR * kTerms;      // N of the two products
   static constexpr int kSBufs = (4 * kNP + 2 * kNS <= 512) ? 2 : 1;  // score buffers in tensor memory
   static constexpr int kT = (NR == 32 && !BF16) ? 128 : 96;        // tokens per tile

@@ -416,3 +416,90 @@ def test_decode_q8_refuses_a_short_workspace_and_wrong_shapes():
         args = dict(q_abs=case.qa, q_pe=case.qp, cache=case.cache, block_table=case.tab, context_lens=case.ctx, scale=SCALE, out=out)
         with pytest.raises(ValueError):
             rt.decode_q8(plan, **{**args, **bad})
+
+
+@pytest.mark.parametrize("H,dtype", [(16, "f16"), (16, "bf16"), (64, "f16"), (64, "bf16")])
+def test_decode_q8_lengths_around_tiles_and_steps(H, dtype):
+    lens = [31, 32, 33, 63, 64, 65, 95, 96, 97, 127, 128, 129, 191, 192, 193, 255, 256, 257, 287, 288, 289, 383, 384, 385]
+    case = Q8Case(30, lens, H=H, bs=32, g=8, dtype=dtype).upload()
+    out, lse = case.decode("f32")
+    case.check(out, lse, heads=[1, H - 1])
+
+
+@pytest.mark.parametrize("lens,H", [([60000] + [1] * 12, 16),        # rows merged by warps, in more parts than a warp has lanes
+                                    ([0, 9000, 0, 30, 0], 16),       # by part lanes, beside requests without a tile
+                                    ([200, 0, 40000, 3, 7, 0], 64)])
+def test_decode_q8_merges_requests_in_many_parts(lens, H):
+    case = Q8Case(31, lens, H=H, bs=64, g=64).upload()
+    out, lse = case.decode("f32")
+    case.check(out, lse, heads=[0, H - 1])
+
+
+@pytest.mark.parametrize("H,dtype", [(16, "f16"), (64, "f16"), (64, "bf16")])
+def test_decode_q8_one_token_far_above_a_long_even_tail(H, dtype):
+    """One token's weight is 2^13 times each of 30000 equal ones, which make most of the sum: their weights are
+    rounded alike, so their errors add up. Each is off by 2^-12 of itself or 2^-26 of the greatest one."""
+    case = Q8Case(32, [30001], H=H, bs=32, g=1, dtype=dtype, pow2=True)
+    q = np.zeros((1, 1, H, 512))
+    q[..., 0] = 13.0 * math.log(2.0) / SCALE / 8
+    case.q_abs, case.q_pe = gen.to_bits(q, dtype), gen.to_bits(np.zeros((1, 1, H, 64)), dtype)
+    case.scales[:] = 1.0
+    rows = orc.physical_rows(case.table[0], 30001, 32)
+    flat = case.ckv.reshape(-1, 512)
+    flat[rows] = flat[rows[1]]            # the tail: one value row
+    flat[rows, 0] = orc.encode_e4m3(np.zeros(1))[0]
+    flat[rows[777], 0] = orc.encode_e4m3(np.full(1, 8.0))[0]
+    case.upload()
+    out, lse = case.decode("f32")
+    case.check(out, lse, heads=[0, H - 1])
+
+
+@pytest.mark.parametrize("lens,H,dtype", [([131072], 16, "f16"), ([40000, 9000], 128, "bf16"), ([40000, 9000], 64, "f16")])
+def test_decode_q8_bounded_waits_run_out_then_the_plan_is_usable(lens, H, dtype):
+    """A limit of a few microseconds, far less than the call takes: every role gives up at its next wait, the call
+    comes back with the error, and the next one on the same workspace is right."""
+    case = Q8Case(33, lens, H=H, bs=64, g=64, dtype=dtype).upload()
+    plan = case.plan()
+    plan.workspace.fill_(0xFF)
+    try:
+        nb.mla_set_wait_timeout_ns(2_000)
+        case.decode("f32", plan=plan)
+        st, code = nb.mla_check_device_errors(None)
+    finally:
+        nb.mla_set_wait_timeout_ns(2_000_000_000)
+    assert st == nb.MLA_ERR_TIMEOUT and code & 1, (st, code)
+    out, lse = case.decode("f32", plan=plan)
+    st, code = nb.mla_check_device_errors(None)
+    assert st == nb.MLA_OK, code
+    case.check(out, lse, heads=[0, H - 1])
+
+
+def test_q8_calls_refuse_buffers_elsewhere():
+    case = Q8Case(34, [50], bs=32, g=32).upload()
+    plan = case.plan()
+    out = torch.empty(1, 1, 16, 512, device="cuda")
+    args = dict(q_abs=case.qa, q_pe=case.qp, cache=case.cache, block_table=case.tab, context_lens=case.ctx, scale=SCALE, out=out)
+    cpu_cache = rt.Q8Cache(case.cache.ckv.cpu(), case.cache.kpe.cpu(), case.cache.scales.cpu())
+    for name in ("q_abs", "q_pe", "block_table", "context_lens", "out", "cache"):
+        with pytest.raises(ValueError):
+            rt.decode_q8(plan, **{**args, name: cpu_cache if name == "cache" else args[name].cpu()})
+    with pytest.raises(ValueError):
+        rt.decode_q8(plan, **{**args, "out": out.double()})
+    c, k = (torch.zeros(1, 1, n, dtype=torch.float16, device="cuda") for n in (512, 64))
+    for bad in ((cpu_cache, c, k, case.tab, case.ctx), (case.cache, c.cpu(), k, case.tab, case.ctx),
+                (case.cache, c, k, case.tab, case.ctx.cpu()), (case.cache, c.double(), k.double(), case.tab, case.ctx)):
+        with pytest.raises(ValueError):
+            rt.cache_append_q8(*bad)
+
+
+@pytest.mark.parametrize("g,scale", [(8, 3.0), (8, 0.3), (16, 2.0 ** 100), (2, 1e-30)])
+def test_append_q8_beside_tokens_under_a_foreign_scale(g, scale):
+    """The block's scale comes from elsewhere, a power of two or not, in range or not: it stays unless the new
+    token needs a larger one."""
+    case = Q8Case(35, [20, 46], q_len=1, bs=16, g=g, dtype="f16", pow2=True)  # (the last token is not its block's first)
+    case.scales[:] = np.float32(scale)
+    case.upload()
+    c, k = new_tokens(36, 2, 1, "f16", spread=1.0)
+    want = orc.cache_append_q8(case.ckv, case.kpe, case.scales, case.table, case.lens, orc.decode16(c, "f16"), orc.decode16(k, "f16"))
+    append(case, c, k)
+    same_cache(case, want)

@@ -174,3 +174,15 @@ def test_q8_cache_refuses_tensors_of_another_form():
                 (ckv, kpe, torch.ones(2, 4).T), (ckv, kpe, torch.ones(8))):
         with pytest.raises(ValueError):
             rt.Q8Cache(*bad)
+
+
+def test_q8_calls_refuse_host_tensors():
+    cache = rt.Q8Cache(torch.zeros(4, 32, 512, dtype=torch.uint8), torch.zeros(4, 32, 64, dtype=torch.uint8), torch.ones(4, 2))
+    tab, ctx = torch.zeros(1, 4, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    new = [torch.zeros(1, 1, n, dtype=torch.float16) for n in (512, 64)]
+    with pytest.raises(ValueError):
+        rt.cache_append_q8(cache, *new, tab, ctx)
+    q = [torch.zeros(1, 1, 16, n, dtype=torch.float16) for n in (512, 64)]
+    plan = rt.Q8Plan(1, 16, 1, False, 0, 0, torch.zeros(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        rt.decode_q8(plan, *q, cache, tab, ctx, 0.1, torch.zeros(1, 1, 16, 512))

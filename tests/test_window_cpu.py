@@ -6,6 +6,7 @@ import pytest
 
 from mla_split_kv_gb300 import binding as nb
 from mla_split_kv_gb300 import build as nbuild
+from mla_split_kv_gb300 import runtime as rt
 from oracle import mla_oracle as orc
 from tests.test_abi_cpu import desc, fake_gb300
 
@@ -92,3 +93,23 @@ def test_a_plan_of_the_runs_covers_them():
     for b, n in enumerate(runs):
         chunks = plan.chunks[plan.o_indptr[b]:plan.o_indptr[b + 1]]
         assert chunks[0][1] == 0 and chunks[-1][2] == n
+
+
+@pytest.mark.parametrize("H,q_len", [(16, 1), (16, 4), (64, 1), (128, 1), (128, 32)])
+@pytest.mark.parametrize("lens", [[1], [40], [300], [4200], [131072], [0, 0], [0, 1, 129, 257, 700], [2048] * 16, [4224] * 32,
+                                  [100] * 200, [9000] + [1] * 90])
+def test_window_partitions_cover_the_runs_in_order(lens, H, q_len):
+    """Whatever plan is taken: a request's partitions follow one another from its first token to its last, none of a
+    split run is empty, slots are numbered in order, and the pair kernels can run it."""
+    bs, dev = 32, fake_gb300()
+    plan = rt._window_partitions(lens, H, q_len, bs, "f16", dev)
+    assert plan.cluster_ctas >= 2 and (H * q_len <= 16 or plan.cluster_ctas == 2)
+    assert plan.o_indptr[0] == 0 and plan.o_indptr[-1] == plan.num_chunks == len(plan.chunks)
+    for b, n in enumerate(lens):
+        at = 0
+        parts = plan.chunks[plan.o_indptr[b]:plan.o_indptr[b + 1]]
+        for k, (rb, t0, t1, slot) in enumerate(parts):
+            assert rb == b and t0 == at and slot == plan.o_indptr[b] + k
+            assert t1 > t0 or (len(parts) == 1 and n == 0)
+            at = t1
+        assert parts and at == n
