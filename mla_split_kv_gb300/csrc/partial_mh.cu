@@ -530,6 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t peer_xrow = peer_x + static_cast<uint32_t>(r * kT * 4);
     const uint32_t xsw8 = static_cast<uint32_t>(r & 7);
     float m_r = -INFINITY, l_r = 0.f;
+    // In fp16 the sum that normalizes O is that of the rounded probabilities, as O's own are (off by up to 2^-11 of a
+    // row that one token dominates); windowed calls keep the exact sum beside it for the LSE.
+    constexpr bool kExactLse = kWin && !BF16;
+    float l_x = 0.f;
     float own[kHalfT];  // this CTA's partial scores of the current tile, kept for B
     // C(j): probabilities of tile j (its scaled scores wait in its P buffer) -> the same buffer (hi, and lo
     // for bf16), 32 tokens at a time; then PV(j) may run
@@ -559,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l_r += (h0 + h2f<BF16>(static_cast<uint16_t>(l & 0xffffu))) + (h1 + h2f<BF16>(static_cast<uint16_t>(l >> 16)));
           } else {
             l_r += h0 + h1;
+            if (kExactLse) l_x += p0 + p1;
           }
         }
         tmem_st16(pa, hw);
@@ -719,6 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l_r *= alpha;
+        if (kExactLse) l_x *= alpha;
         m_r = m_new;
       }
       // tile i's P buffer was last read by PV(i-2)
@@ -743,6 +749,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm->half_val[hf][r] = l_r;
     const bool read_o = (ntiles > 0) && !named_bar_sync_or(1, kSoftmaxThreads, *abort_flag != 0);  // uniform
     const float l_row = sm->half_val[0][r] + sm->half_val[1][r];  // the row's sum, the same in both halves
+    float l_lse = l_row;
+    if (kExactLse) {
+      named_bar_sync(1, kSoftmaxThreads);
+      sm->half_val[hf][r] = l_x;
+      named_bar_sync(1, kSoftmaxThreads);
+      l_lse = sm->half_val[0][r] + sm->half_val[1][r];
+    }
     // epilogue: the normalized partial of this row over this thread's half of the CTA's 256 columns,
     // and the LSE (rank 0)
     const bool has_mass = read_o && (r < w.nrows) && (m_r != -INFINITY) && (l_row > 0.f);
@@ -765,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
-    if (rank == 0 && hf == 0 && r < w.nrows) p.lse[orow] = has_mass ? m_r + log2f(l_row) : -INFINITY;
+    if (rank == 0 && hf == 0 && r < w.nrows) p.lse[orow] = has_mass ? m_r + log2f(l_lse) : -INFINITY;
   }
   tc_fence_before();
   __syncthreads();

@@ -418,6 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_q = (w.row0 + r) / p.H;
     const int tlim = min(w.sub1, p.causal ? (w.L - p.q_len + row_q + 1) : w.L);
     float m_r = -INFINITY, l_r = 0.f;
+    // In fp16 the sum that normalizes O is that of the rounded probabilities, as O's own are (off by up to 2^-11 of a
+    // row that one token dominates); windowed calls keep the exact sum beside it for the LSE.
+    constexpr bool kExactLse = kWin && !BF16;
+    float l_x = 0.f;
     for (int i = 0; i < ntiles; ++i) {
       const int buf = i & 1;
       int ok = 1;
@@ -480,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l_r *= alpha;
+        if (kExactLse) l_x *= alpha;
         m_r = m_new;
       }
       // probabilities of tile i over this thread's 32 tokens -> the same 32 columns (hi, then lo)
@@ -500,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           lw[u] = 0.f;
           l_r += h0 + h1;
+          if (kExactLse) l_x += p0 + p1;
         }
       }
       tmem_st16(sa, hw);
@@ -518,6 +524,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm->half_val[hf][r] = l_r;
     const bool read_o = (ntiles > 0) && !named_bar_sync_or(1, kSoftmaxThreads, *abort_flag != 0);  // uniform
     const float l_row = sm->half_val[0][r] + sm->half_val[1][r];  // the row's sum, the same in both halves
+    float l_lse = l_row;
+    if (kExactLse) {
+      named_bar_sync(1, kSoftmaxThreads);
+      sm->half_val[hf][r] = l_x;
+      named_bar_sync(1, kSoftmaxThreads);
+      l_lse = sm->half_val[0][r] + sm->half_val[1][r];
+    }
     // epilogue: the normalized partial of this row over this thread's half of the CTA's 256 columns,
     // and the LSE (rank 0)
     const bool has_mass = read_o && real && (m_r != -INFINITY) && (l_row > 0.f);
@@ -539,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
-    if (half == 0 && hf == 0 && real) p.lse[orow] = has_mass ? m_r + log2f(l_row) : -INFINITY;
+    if (half == 0 && hf == 0 && real) p.lse[orow] = has_mass ? m_r + log2f(l_lse) : -INFINITY;
   }
   tc_fence_before();
   __syncthreads();
