@@ -6,20 +6,21 @@
 // with c_t, k_t the E4M3 values of the token's bytes and z_t its block's scale.
 //
 // The tensor core takes the bytes as they are (kind::f8f6f4, E4M3 x E4M3 with
-// fp32 sums): nothing is widened, and a 128-token tile of the whole latent is
-// 72 KB, so one CTA holds it for both products and no CTA waits on another.
+// fp32 sums): nothing is widened, and a 96-token tile of the whole latent is
+// 54 KB, so one CTA holds it for both products and no CTA waits on another.
 // What is not 8-bit is split into E4M3 terms, each the rounding of what the
-// terms before it leave: x = t1 + 2^-5 t2 + 2^-10 t3. A term keeps 4
+// terms before it leave: x = t1 + 2^-5 t2 + 2^-10 t3 + ... A term keeps 4
 // significant bits and leaves at most 2^-4 of its value, so three terms hold
 // an fp16 query exactly (11 bits) and two a bf16 one (8 bits), as long as its
 // magnitude is above 2^-14 of the row's largest (the row is first scaled by a
 // power of two to [128, 256)), and below that to 2^-23 of the largest; the
-// weights of the value product, three terms, to 2^-12 of themselves or 2^-25
-// of the largest. The terms are further columns of the MMA's N side:
+// weights of the value product, three terms (four for 16 rows), to 2^-12
+// (2^-16) of themselves or 2^-26 of the largest. The terms are further columns
+// of the MMA's N side:
 //   S^T[tok, (term, row)]  = [c | k][tok, :] . Qterms^T    M=128 tokens, K=576
-//   O^T[d, (term, row)]   += c^T[d, tok] . Wterms^T        M=128 columns x 4, K=128
-// At 16 rows an MMA's time is that of reading the 4 KB A operand from shared
-// memory, which the terms share.
+//   O^T[d, (term, row)]   += c^T[d, tok] . Wterms^T        M=128 columns x 4, K=tokens
+// An MMA's time is that of reading its operands from shared memory, 4 KB of A
+// (47 cycles up to N = 48, 57 at 96), which the terms share.
 //
 // A token's scale goes with its weight: with y_t = s_t log2 e + log2 z_t the
 // weights are w_t = 2^(y_t - m), m a running maximum of y, so they stay in
@@ -27,14 +28,42 @@
 // is m + log2 of that same sum.
 //
 // NR rows a CTA: 16, or 32 for calls with more (a group of CTAs, a gang, then
-// shares each tile through L2). O^T is 4 x 3 NR columns of tensor memory, all
-// of it but the scores' at 32. Two tile slots of 72 KB: the MMAs of a tile take
-// a third of the time that HBM takes to bring one, and pages further ahead are
-// on their way to L2.
+// shares each tile through L2). O^T is 4 x kTerms NR columns of tensor memory,
+// 384 of the 512 at 32 rows. The tiles of the batch are one line, shared out
+// evenly over the gangs (q8_schedule.cuh), and a second kernel merges the
+// requests that gang borders cut.
 //
-// Warp roles (384 threads): warps 0-7 softmax, rescale and output (thread =
-// token; the two warps of a TMEM lane quadrant take half of the rows each),
-// two more that issue the score and the value products, one that loads pages.
+// The pipeline. Three tile slots of 54 KB (two of 72 for 32 fp16 rows, whose
+// queries take 54 KB); a slot is refilled in the 32-token steps in which the
+// value product leaves it, and pages further ahead are on their way to L2. One
+// thread issues the score products, another the value products (one for both
+// spent the MMAs' time on asking whose inputs were there). The softmax warps
+// write weights as 8-byte words of their token's row (the value product reads
+// them N-major); byte stores of the K-major layout took longer than the MMAs.
+// Four warps share 8 rows and meet once a tile; only when a score passes its
+// row's reference by 2^kTau do they take maxima and rescale O. After a
+// request's last tile they split the next one's queries first, while its last
+// value product runs, then write its output.
+//
+// What bounds it, in cycles of an SM (2070 MHz) for a 96-token tile: HBM's share
+// 2570; the MMAs 1550 with nothing else on shared memory, 2300 as they run. At
+// 16 rows a tile takes 2600: HBM. At 32 rows it takes 3000 to 4000: MMAs, the
+// weights, and the tiles in which a reference moves (1800 more). A call has
+// some 10 us around that: the lengths and the schedule 1.5 to 2 us, the first
+// tiles from HBM 3 us, the last output and the merge 5 us; a good part of it
+// is the fetch of code that is met once (ten cycles an instruction), so what
+// runs once per call or request is kept short.
+//
+// Measured (us a call, captured back to back; scaling by HBM alone in brackets):
+// 131,072 tokens, 16 fp16 heads 26.2 (11.1); 32 requests up to 16K, 16 bf16 heads
+// 49.7 (25.8); 8 requests up to 64K, 128 bf16 heads 177 (26.2; the formula's
+// products at the card's 16-bit matrix rate 44); 9 causal fp16 rows over 16 heads,
+// 4 requests up to 82K, 177 (19.9 and 38); 48 requests through a window of 4096,
+// 64 bf16 heads, 81 (17.3); 37 tokens 10.1.
+//
+// Warp roles: softmax, rescale and output (thread = token; 8 rows a thread: 8
+// warps for 16 rows, 16 for 32), one warp each that issues the score and the
+// value products, one that loads pages.
 #include "q8_schedule.cuh"
 
 namespace mla {
@@ -92,7 +121,7 @@ struct Small {
   uint64_t pfull[kMaxSlots], pvdone[2];  // weights per slot; value products per tile parity
   uint64_t qfull, ofree, drain[2];
   int64_t scratch[33];
-  int64_t off0;
+  int64_t off0, first_tile, last_tile;
   int b0;
   uint32_t tmem_base;
   int32_t abort_flag;
@@ -201,29 +230,38 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
   for (int b = b_lo; b < b_hi; ++b) {
     const int L = __ldcg(p.context_lens + b);
     if (b < kQ8Lens) sm->lens[b] = L;
-    mine += q8_tiles(q8_view(p, L), kT);
+    const int n = q8_tiles(q8_view(p, L), kT);
+    mine += n + (n > 0 ? int64_t{1} << kQ8CountShift : 0);
   }
   const int64_t prefix = block_prefix<kThreads>(mine, sm->scratch, &T);
-  const Q8Line line = q8_line(T, p.gangs);
+  const Q8Line line = q8_line(T & kQ8Tiles, static_cast<int32_t>(T >> kQ8CountShift), p.gangs);
   const bool work = gang < line.gangs;
   const int64_t lo = work ? line.begin(gang) : 0, hi = work ? line.begin(gang + 1) : 0;
-  if (work && lo >= prefix && lo < prefix + mine) {
-    int64_t at = prefix;
-    int b = b_lo;
-    while (true) {
-      const int n = q8_tiles(q8_view(p, lens(b)), kT);
-      if (at + n > lo) break;
-      at += n;
-      ++b;
+  {  // the thread whose requests the gang starts (ends) in finds the place: its request and tile, tiles before it
+    int64_t tiles = prefix & kQ8Tiles, at = tiles + line.gap * (prefix >> kQ8CountShift);
+    const int64_t end = at + (mine & kQ8Tiles) + line.gap * (mine >> kQ8CountShift);
+    if (work && ((lo >= at && lo < end) || (hi >= at && hi < end))) {
+      for (int b = b_lo; b < b_hi; ++b) {
+        const int n = q8_tiles(q8_view(p, lens(b)), kT);
+        const int64_t next = at + n + (n > 0 ? line.gap : 0);
+        if (lo >= at && lo < next) {
+          const bool in_gap = lo - at >= n;
+          sm->b0 = in_gap ? b + 1 : b;
+          sm->off0 = in_gap ? 0 : lo - at;
+          sm->first_tile = tiles + min(lo - at, static_cast<int64_t>(n));
+        }
+        if (hi >= at && hi < next) sm->last_tile = tiles + min(hi - at, static_cast<int64_t>(n));
+        at = next;
+        tiles += n;
+      }
     }
-    sm->b0 = b;
-    sm->off0 = lo - at;
+    if (tid == 0 && hi == line.length) sm->last_tile = T & kQ8Tiles;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  const int N = static_cast<int>(hi - lo);  // this gang's tiles
+  const int N = work ? static_cast<int>(sm->last_tile - sm->first_tile) : 0;  // this gang's tiles
   Q8Walk w = q8_walk(work ? sm->b0 : 0, work ? sm->off0 : 0, N);
   uint64_t tmo = p.timeout_ns;
   asm volatile("" : "+l"(tmo));

@@ -2,13 +2,17 @@
 // found again by its merge.
 //
 // The batch's visible runs, cut into tiles of p.tile tokens request after request,
-// are one line of T tiles. Gang j of J takes T / J of it, the first T % J gangs
-// one more (one CTA of a gang per row group), so every gang works on the same number of tiles
-// whatever the lengths, and lengths are read where they lie: no host plan, and
-// a captured call follows contexts as they grow. A request that lies within
-// one gang is finished there; one cut by gang borders has a part per gang: its
-// first gang keeps it in entry 1 (that gang's open end), the others in entry
-// 0, and says in its first gang's entry of ws_cut how many there are.
+// are one line, with a gap of a few cells between requests: what a gang spends on
+// going from one request to the next (its output, the next one's queries, the
+// first tiles' rescales: 10 us at 32 rows, 5 at 16, about four tiles) counts as
+// tiles. Gang j of J takes L / J cells of the line's L, the first L % J gangs one
+// more (one CTA of a gang per row group), so every gang works as long as the
+// others whatever the lengths (without the gaps, gangs with one request ended
+// after 55 us, those with two after 65 to 76; calls 4 to 7% slower). Lengths are
+// read where they lie: no host plan, and a captured call follows contexts as they
+// grow. A request that lies within one gang is finished there; one cut by gang
+// borders has a part per gang: its first gang keeps it in entry 1 (that gang's
+// open end), the others in entry 0, and ws_cut says how many there are.
 #pragma once
 
 #include "device_common.cuh"
@@ -29,12 +33,17 @@ struct Q8Lens {
   __device__ __forceinline__ int operator()(int b) const { return b < kQ8Lens ? cached[b] : __ldcg(global + b); }
 };
 
-// The line of T tiles among the gangs that get any (all of them unless there are fewer tiles).
+// A pair of counts in one sum: tiles (at most 65535 * 2^25 < 2^44) and the requests that have any.
+constexpr int kQ8CountShift = 44;
+constexpr int64_t kQ8Tiles = (int64_t{1} << kQ8CountShift) - 1;
+constexpr int kQ8Gap = 4;
+
+// The line among the gangs that get any of it (all of them unless there are fewer tiles).
 struct Q8Line {
-  int64_t base;      // tiles of a gang
-  int32_t gangs, more;  // the first `more` gangs have one more
+  int64_t length, base;      // cells, and those of a gang
+  int32_t gangs, more, gap;  // the first `more` gangs have one more
   __device__ __forceinline__ int64_t begin(int j) const { return base * j + min(j, more); }
-  // the gang of tile x
+  // the gang of cell x
   __device__ __forceinline__ int gang_of(int64_t x) const {
     const int64_t head = (base + 1) * more;
     return x < head ? static_cast<int>(div(x, base + 1)) : more + static_cast<int>(div(x - head, base));
@@ -44,11 +53,15 @@ struct Q8Line {
     return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
   }
 };
-__device__ __forceinline__ Q8Line q8_line(int64_t T, int gangs) {
+__device__ __forceinline__ Q8Line q8_line(int64_t tiles, int32_t requests, int gangs) {
   Q8Line l;
-  l.gangs = T < gangs ? static_cast<int32_t>(T) : gangs;
-  l.base = l.gangs > 0 ? Q8Line::div(T, l.gangs) : 0;
-  l.more = static_cast<int32_t>(T - l.base * l.gangs);
+  // a gap is at most a fifth of a gang's tiles, so every gang has some
+  const int64_t share = Q8Line::div(tiles, gangs);
+  l.gap = share >= 5 * kQ8Gap ? kQ8Gap : static_cast<int32_t>(share) / 5;
+  l.length = tiles + (requests > 1 ? static_cast<int64_t>(l.gap) * (requests - 1) : 0);
+  l.gangs = l.length < gangs ? static_cast<int32_t>(l.length) : gangs;
+  l.base = l.gangs > 0 ? Q8Line::div(l.length, l.gangs) : 0;
+  l.more = static_cast<int32_t>(l.length - l.base * l.gangs);
   return l;
 }
 
