@@ -64,6 +64,8 @@
 // Warp roles: softmax, rescale and output (thread = token; 8 rows a thread: 8
 // warps for 16 rows, 16 for 32), one warp each that issues the score and the
 // value products, one that loads pages.
+#include <atomic>
+
 #include "q8_schedule.cuh"
 
 namespace mla {
@@ -850,24 +852,24 @@ __device__ __forceinline__ void merge_out(const DecodeQ8Params& p, long long br,
   store_out4(p.out, p.out_dtype, br * kRank + col, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
 }
 
-// Batches whose rows fill the device: a warp a (gang, row), which ends at once where no request with that gang as
-// its first is cut. Lane x weighs part x, then each part's 512 columns go by 16 a lane (with a block a row, 4
-// columns a lane, the weights' code run by every warp was most of the time: 8 us for 3000 rows of 2 to 3 parts).
+// Batches whose rows fill the device: kRowWarps warps a (gang, row), which end at once where no request with that
+// gang as its first is cut. Lane x weighs part x, then the parts' columns go by, 8 float4 a lane in flight.
+constexpr int kRowWarps = 2, kRowLoads = 4 / kRowWarps;
 __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_rows_kernel(const DecodeQ8Params p) {
   const int lane = threadIdx.x & 31;
-  const uint32_t rows_total = p.q_len * p.H, units = p.gangs * rows_total;
+  const uint32_t rows_total = p.q_len * p.H, per_gang = rows_total * kRowWarps, units = p.gangs * per_gang;
   pdl_wait();
   pdl_launch_dependents();
   for (uint32_t unit = blockIdx.x * kMergeWarps + (threadIdx.x >> 5); unit < units; unit += gridDim.x * kMergeWarps) {
-    const int j0 = unit / rows_total, row = unit % rows_total;
+    const int j0 = unit / per_gang, row = unit % per_gang / kRowWarps, col = unit % kRowWarps * (kRank / kRowWarps) + 4 * lane;
     const int2 cut = __ldcg(p.ws_cut + j0);
     const int n = cut.y;
     if (!merge_entry_ok(p, cut.x, j0, n)) continue;
     const MergeParts parts(p, j0, row);
     float M = -INFINITY, den = 0.f;
-    float4 acc[4];
+    float4 acc[kRowLoads];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < kRowLoads; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int x0 = 0; x0 < n; x0 += 32) {
       const float2 ml = x0 + lane < n ? parts.max_sum(x0 + lane) : make_float2(-INFINITY, 0.f);
@@ -880,24 +882,24 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_rows
       den = fmaf(den, al, sum);
       M = m;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[k] = make_float4(acc[k].x * al, acc[k].y * al, acc[k].z * al, acc[k].w * al);
+      for (int k = 0; k < kRowLoads; ++k) acc[k] = make_float4(acc[k].x * al, acc[k].y * al, acc[k].z * al, acc[k].w * al);
       const int here = min(32, n - x0);
-#pragma unroll 2
+#pragma unroll (8 / kRowLoads)
       for (int x = 0; x < here; ++x) {
-        float4 v[4];
+        float4 v[kRowLoads];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = parts.values(x0 + x, 4 * lane + 128 * k);
+        for (int k = 0; k < kRowLoads; ++k) v[k] = parts.values(x0 + x, col + 128 * k);
         const float wx = __shfl_sync(0xffffffffu, w, x);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) fma4(acc[k], wx, v[k]);
+        for (int k = 0; k < kRowLoads; ++k) fma4(acc[k], wx, v[k]);
       }
     }
     const long long br = static_cast<long long>(cut.x) * rows_total + row;
     const bool none = den == 0.f;
     const float inv = none ? 0.f : 1.f / den;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) merge_out(p, br, 4 * lane + 128 * k, acc[k], inv);
-    if (p.out_lse != nullptr && lane == 0) p.out_lse[br] = none ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(den);
+    for (int k = 0; k < kRowLoads; ++k) merge_out(p, br, col + 128 * k, acc[k], inv);
+    if (p.out_lse != nullptr && col == 0) p.out_lse[br] = none ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(den);
   }
 }
 
@@ -978,9 +980,17 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_part
 
 template <int NR, bool BF16>
 cudaError_t launch(cudaLaunchConfig_t cfg, const CUtensorMap& tm_ckv, const CUtensorMap& tm_kpe, const DecodeQ8Params& p) {
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_decode_q8_kernel<NR, BF16>),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR, BF16>::kSmem);
+  static std::atomic<uint64_t> ready{0};  // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (dev > 63 || (ready.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_decode_q8_kernel<NR, BF16>),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR, BF16>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev <= 63) ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cfg.gridDim = dim3(static_cast<unsigned>(p.groups), static_cast<unsigned>(p.gangs), 1);
   cfg.blockDim = dim3(Cfg<NR, BF16>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg<NR, BF16>::kSmem;
@@ -1017,7 +1027,7 @@ cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kp
   if (e != cudaSuccess) return e;
   if (p.gangs == 1) return cudaSuccess;  // nothing is cut
   const int64_t rows = static_cast<int64_t>(p.q_len) * p.H;
-  const int64_t blocks = p.cuts_by_request ? rows * p.B * kColUnits : (rows * p.gangs + kMergeWarps - 1) / kMergeWarps;
+  const int64_t blocks = p.cuts_by_request ? rows * p.B * kColUnits : (rows * p.gangs * kRowWarps + kMergeWarps - 1) / kMergeWarps;
   const int64_t wave = static_cast<int64_t>(kMergeBlocks) * p.gangs * p.groups;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks < wave ? blocks : wave), 1, 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);

@@ -311,12 +311,11 @@ def decode_window(plan: WindowPlan, q_abs: torch.Tensor, q_pe: torch.Tensor, ckv
         _expect(out_lse, (B, q_len, H), torch.float32, "out_lse", dev)
     _expect(context_lens, (B,), torch.int32, "context_lens", dev)
     _expect(block_table, (B, width), torch.int32, "block_table", dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
     p = plan.plan
     d = nb.mla_decode_desc_t(B, H, q_len, bs, nblk, width, nb.DTYPE_CODES[plan.dtype],
                              1 if plan.causal else 0, plan.chunks.data_ptr(), p.num_chunks, p.cluster_ctas,
-                             nb.MLA_KERNEL_TC, stream.cuda_stream, p.clusters_per_chunk, plan.workspace.data_ptr(),
+                             nb.MLA_KERNEL_TC, raw_stream, p.clusters_per_chunk, plan.workspace.data_ptr(),
                              plan.workspace.numel(), 0, 0, 0, cache_scale, 0)
     nb.mla_decode_window(q_abs.data_ptr(), q_pe.data_ptr(), ckv.data_ptr(), kpe.data_ptr(), block_table.data_ptr(),
                          context_lens.data_ptr(), scale, 0, plan.partials.data_ptr(), plan.lse.data_ptr(),
@@ -359,6 +358,11 @@ def _device_of(t: torch.Tensor) -> int:
     return dev
 
 
+# the current stream's handle without a Stream object around it (1 us of a call that takes 4 on the GPU)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _expect(t: torch.Tensor, shape, dtype, what: str, dev: int) -> None:
     """The C ABI takes raw pointers to dense row-major buffers of one device: anything else is refused here."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
@@ -390,12 +394,11 @@ def cache_append_q8(cache: Q8Cache, ckv_new: torch.Tensor, kpe_new: torch.Tensor
     _expect(kpe_new, (B, q_len, 64), ckv_new.dtype, "kpe_new", dev)
     _expect(context_lens, (B,), torch.int32, "context_lens", dev)
     _expect(block_table, (B, width), torch.int32, "block_table", dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
     nb.mla_cache_append_q8(ckv_new.data_ptr(), kpe_new.data_ptr(), _code_of(ckv_new, "ckv_new"),
                            block_table.data_ptr(), context_lens.data_ptr(), B, q_len, cache.block_size,
                            cache.scale_block, cache.num_blocks, width, cache.ckv.data_ptr(), cache.kpe.data_ptr(),
-                           cache.scales.data_ptr(), stream.cuda_stream)
+                           cache.scales.data_ptr(), raw_stream)
 
 
 @dataclasses.dataclass
@@ -437,11 +440,10 @@ def decode_q8(plan: Q8Plan, q_abs: torch.Tensor, q_pe: torch.Tensor, cache: Q8Ca
     _expect(block_table, (B, width), torch.int32, "block_table", dev)
     if cache.ckv.get_device() != dev:
         raise ValueError(f"cache: on {cache.ckv.device}, the plan's workspace on {plan.workspace.device}")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
     d = nb.mla_q8_desc_t(B, H, q_len, cache.block_size, cache.num_blocks, width, _code_of(q_abs, "q_abs"),
                          1 if plan.causal else 0, cache.scale_block, plan.window, plan.sinks, _code_of(out, "out"),
-                         plan.workspace.data_ptr(), plan.workspace.numel(), stream.cuda_stream)
+                         plan.workspace.data_ptr(), plan.workspace.numel(), raw_stream)
     nb.mla_decode_q8(q_abs.data_ptr(), q_pe.data_ptr(), cache.ckv.data_ptr(), cache.kpe.data_ptr(),
                      cache.scales.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), scale,
                      out.data_ptr(), out_lse.data_ptr() if out_lse is not None else None, d)
