@@ -267,9 +267,10 @@ typedef struct {
                                  the two CTAs of a pair send each other of
                                  their scores. MLA_SCORE_EXCHANGE_EXACT (0,
                                  default): exact; on 16-bit caches with at
-                                 least 128 rows nothing crosses (as NONE),
-                                 otherwise (64 rows, E4M3 caches) fp32
-                                 partial scores of the real rows (as F32).
+                                 least 128 rows, or through a window, nothing
+                                 crosses (as NONE), otherwise (64 rows, E4M3
+                                 caches) fp32 partial scores of the real rows
+                                 (as F32).
                                  MLA_SCORE_EXCHANGE_F16 (1): each CTA's partial
                                  dot product of a tile is rounded once to fp16
                                  (both CTAs add the same rounded values, so
