@@ -969,7 +969,6 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
   p.groups = (rows + nr - 1) / nr;
   p.cuts_by_request = static_cast<int64_t>(p.B) * rows < static_cast<int64_t>(p.gangs) * p.groups ? 1 : 0;
   p.row_pad = p.groups * nr;
-  p.tile = mla::q8_tile_tokens(rows, d->dtype == MLA_BF16);
   p.ws_o = static_cast<float*>(d->workspace);
   p.ws_ml = p.ws_o + static_cast<uint64_t>(p.gangs) * 2 * p.row_pad * mla::kRank;
   p.ws_cut = reinterpret_cast<int2*>(p.ws_ml + static_cast<uint64_t>(p.gangs) * 2 * p.row_pad * 2);

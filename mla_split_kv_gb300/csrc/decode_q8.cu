@@ -73,12 +73,27 @@ namespace mla {
 namespace {
 
 constexpr int kGroupBytes = 8 * kRank;            // 4 KB: 8 tokens, four swizzled [8 x 128] atoms
-constexpr int kStep = 32;                         // tokens of an MMA step of the value product
-constexpr int kMaxSlots = 3, kMaxSteps = 4;
+constexpr int kT = 96;                            // tokens per tile
+constexpr int kStep = 32, kSteps = kT / kStep;    // tokens of an MMA step of the value product
+constexpr int kSlots = 3;
 constexpr int RH = 8;                             // rows per softmax thread
 constexpr float kTermStep = 32.0f, kTermInv = 1.0f / 32.0f;
 
-constexpr uint32_t kSmallBytes = 5120;
+template <int kLens>
+struct Small {
+  uint64_t full[kSlots], empty[kSlots][kSteps];  // tile slots, freed step by step
+  uint64_t sfull[2], sfree[2];           // score buffers
+  uint64_t pfull[kSlots], pvdone[2];  // weights per slot; value products per tile parity
+  uint64_t qfull, ofree, drain[2];
+  int64_t scratch[33];
+  int64_t off0, first_tile, last_tile;
+  int b0;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+  alignas(16) float factor[2][32];       // per row: score scale over the query's power of two, log2 units
+  alignas(16) float red[2][4][32];       // per tile parity and token quadrant, rows' maxima (then their sums)
+  int32_t lens[kLens];
+};
 
 template <int NR, bool BF16>
 struct Cfg {
@@ -90,48 +105,29 @@ struct Cfg {
   static constexpr int kWeightExp = NR == 16 ? 1 : 6;
   static constexpr int kNS = NR * kQTerms, kNP = NR * kTerms;      // N of the two products
   static constexpr int kSBufs = (4 * kNP + 2 * kNS <= 512) ? 2 : 1;  // score buffers in tensor memory
-  static constexpr int kT = (NR == 32 && !BF16) ? 128 : 96;        // tokens per tile
-  static constexpr int kSlots = kT == 96 ? 3 : 2, kSteps = kT / kStep;
-  static constexpr uint32_t kCkvBytes = kT * kRank, kTileSlot = kT * kQkDim;
+  // Weights: [kT tokens x kNP] bytes, N-major, a thread storing its token's row as words, in the place of the tile's
+  // rope columns, which only the scores read: for 16 rows in rows of 64 bytes with the swizzle of that width, for 32
+  // a run of 32-byte rows per term, 3 KB of a slot more than its rope columns.
+  static constexpr uint32_t kPRow = NR == 16 ? 64 : 32, kPBytes = kT * kNP;
+  static constexpr uint32_t kCkvBytes = kT * kRank;
+  static constexpr uint32_t kTileSlot = kCkvBytes + (kPBytes > kT * kRope ? kPBytes : kT * kRope);
   static constexpr int kPre = kSlots;                              // tiles ahead that are prefetched to L2
   static constexpr uint32_t kQChunk = kNS * 128;                   // [kNS x 128 columns], swizzled
   static constexpr uint32_t kQBytes = kNS * kQkDim;                // four chunks, then [kNS x 64] (64-byte swizzle)
-  // Weights: [kT tokens x kNP] bytes, rows of 64 or 128 with the swizzle of that width (the value product reads
-  // them N-major, so a thread stores its token's rows as words). Those of 16 rows take the place of the tile's
-  // rope columns, which only the scores read; those of 32 have kPBufs buffers of their own.
-  static constexpr bool kPInSlot = NR == 16;
-  static constexpr uint32_t kPRow = kNP <= 64 ? 64 : 128, kPBytes = kT * kPRow;
-  static constexpr int kPBufs = kPInSlot ? 0 : (BF16 ? 2 : 1);
+  static constexpr int kLens = NR == 32 && !BF16 ? 64 : 640;       // context lengths kept in shared memory
   static constexpr uint32_t kOffQ = kSlots * kTileSlot;
-  static constexpr uint32_t kOffP = kOffQ + kQBytes;
-  static constexpr uint32_t kOffSmall = kOffP + kPBufs * kPBytes;
-  static constexpr uint32_t kSmem = kOffSmall + kSmallBytes;
+  static constexpr uint32_t kOffSmall = kOffQ + kQBytes;
+  static constexpr uint32_t kSmem = kOffSmall + sizeof(Small<kLens>);
   static constexpr uint32_t kTmemO = 0, kTmemS = 4 * kNP;
   // warps
   static constexpr int kSoftmaxWarps = NR / RH * 4, kScoreWarp = kSoftmaxWarps, kValueWarp = kScoreWarp + 1;
   static constexpr int kLoadWarp = kValueWarp + 1, kThreads = (kLoadWarp + 1) * 32;
-  static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kQChunk % 1024 == 0, "swizzle atoms stay aligned");
-  static_assert(kTileSlot % 1024 == 0 && kCkvBytes % 1024 == 0 && (!kPInSlot || kPBytes <= kT * kRope), "tile slots");
-  static_assert(kSlots <= kMaxSlots && kSteps <= kMaxSteps && kNP <= static_cast<int>(kPRow), "layouts");
+  static_assert(kQBytes % 1024 == 0 && kQChunk % 1024 == 0 && kOffSmall % 16 == 0, "swizzle atoms stay aligned");
+  static_assert(kTileSlot % 1024 == 0 && kCkvBytes % 1024 == 0, "tile slots");
+  static_assert(kPRow == 32 ? NR == 32 : kNP == static_cast<int>(kPRow), "layouts");
   static_assert(kTmemS + kSBufs * kNS <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
-
-struct Small {
-  uint64_t full[kMaxSlots], empty[kMaxSlots][kMaxSteps];  // tile slots, freed step by step
-  uint64_t sfull[2], sfree[2];           // score buffers
-  uint64_t pfull[kMaxSlots], pvdone[2];  // weights per slot; value products per tile parity
-  uint64_t qfull, ofree, drain[2];
-  int64_t scratch[33];
-  int64_t off0, first_tile, last_tile;
-  int b0;
-  uint32_t tmem_base;
-  int32_t abort_flag;
-  alignas(16) float factor[2][32];       // per row: score scale over the query's power of two, log2 units
-  alignas(16) float red[2][4][32];       // per tile parity and token quadrant, rows' maxima (then their sums)
-  int32_t lens[kQ8Lens];
-};
-static_assert(sizeof(Small) <= kSmallBytes, "small smem region");
 
 // (x - v) * 32 for the two fp16 values of a pair
 __device__ __forceinline__ uint32_t next_term(uint32_t x, uint32_t v) {
@@ -181,14 +177,14 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
                          const DecodeQ8Params p) {
   using C = Cfg<NR, BF16>;
   constexpr int kTerms = C::kTerms, kThreads = C::kThreads, kSoftmaxWarps = C::kSoftmaxWarps;
-  constexpr int kT = C::kT, kSlots = C::kSlots, kSteps = C::kSteps, kPre = C::kPre;
+  constexpr int kPre = C::kPre;
   constexpr uint32_t kCkvBytes = C::kCkvBytes, kTileSlot = C::kTileSlot;
   extern __shared__ uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need it; the size leaves no slack to align it
     if (threadIdx.x == 0) flag_error(MLA_DEVERR_CONFIG);
     return;
   }
-  Small* sm = reinterpret_cast<Small*>(smem + C::kOffSmall);
+  auto* const sm = reinterpret_cast<Small<C::kLens>*>(smem + C::kOffSmall);
   volatile int32_t* abort_flag = &sm->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gang = blockIdx.y;
@@ -196,9 +192,9 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
   const int row0 = blockIdx.x * NR, nrows = min(NR, rows_total - row0);
 
   if (tid == 0) {
-    for (int s = 0; s < kMaxSlots; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sm->full[s], 1);
-      for (int k = 0; k < kMaxSteps; ++k) mbar_init(&sm->empty[s][k], 1);
+      for (int k = 0; k < kSteps; ++k) mbar_init(&sm->empty[s][k], 1);
       mbar_init(&sm->pfull[s], kSoftmaxWarps);
     }
     for (int s = 0; s < 2; ++s) {
@@ -225,13 +221,13 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
   pdl_launch_dependents();
 
   // this gang's place on the line of tiles
-  const Q8Lens lens{p.context_lens, sm->lens};
+  const Q8Lens<C::kLens> lens{p.context_lens, sm->lens};
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
   int64_t mine = 0, T = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const int L = __ldcg(p.context_lens + b);
-    if (b < kQ8Lens) sm->lens[b] = L;
+    if (b < C::kLens) sm->lens[b] = L;
     const int n = q8_tiles(q8_view(p, L), kT);
     mine += n + (n > 0 ? int64_t{1} << kQ8CountShift : 0);
   }
@@ -476,8 +472,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t slot = base + (i % kSlots) * kTileSlot;
-          const uint32_t wts = C::kPInSlot ? slot + kCkvBytes : base + C::kOffP + (i % (C::kPBufs > 0 ? C::kPBufs : 1)) * C::kPBytes;
-          const Desc2 pb = desc2(C::kPRow == 64 ? smem_desc_sw64(wts, 512) : smem_desc_sw128(wts, 16, 1024));
+          const uint32_t wts = slot + kCkvBytes;
+          const Desc2 pb = desc2(C::kPRow == 32 ? smem_desc_sw32(wts, kT * 32, 256) : smem_desc_sw64(wts, 512));
           const Desc2 a0 = desc2(smem_desc_sw128(slot, 1024, kGroupBytes));
           const int ksteps = (min(kT, w.v.n - tile * kT) + kStep - 1) / kStep;
 #pragma unroll 1
@@ -633,12 +629,6 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
             lsum[k] *= al[k];
           }
         }
-        // Weights in the slot: its rope columns have been read. In a buffer of their own: the value product that
-        // read it last has to be done.
-        if (!C::kPInSlot && i >= C::kPBufs) {
-          const int j = i - C::kPBufs;
-          if (!__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[j & 1], (j >> 1) & 1, tmo))) *abort_flag = 1;
-        }
         if (has_tokens) {
           uint32_t word[kTerms][RH / 4];
 #pragma unroll
@@ -654,13 +644,13 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 #pragma unroll
             for (int n = 0; n < kTerms; ++n) word[n][k / 4] = (k & 2) ? word[n][k / 4] | (t[n] << 16) : t[n];
           }
-          uint8_t* const pb = smem + (C::kPInSlot ? (i % kSlots) * kTileSlot + kCkvBytes
-                                                  : C::kOffP + (i % (C::kPBufs > 0 ? C::kPBufs : 1)) * C::kPBytes);
+          uint8_t* const pb = smem + (i % kSlots) * kTileSlot + kCkvBytes;  // (the scores are done with what lay there)
           // columns n * NR + 8 h .. + 7 of this token's row: half of one 16-byte piece
 #pragma unroll
           for (int n = 0; n < kTerms; ++n) {
             const int piece = (n * NR + RH * h) >> 4;
-            const int at = C::kPRow == 64 ? tl * 64 + ((piece ^ (tl >> 1)) & 3) * 16 : tl * 128 + ((piece ^ tl) & 7) * 16;
+            const int at = C::kPRow == 32 ? (piece >> 1) * kT * 32 + tl * 32 + ((piece ^ (tl >> 2)) & 1) * 16
+                                          : tl * 64 + ((piece ^ (tl >> 1)) & 3) * 16;
             *reinterpret_cast<uint2*>(pb + at + (h & 1) * 8) = make_uint2(word[n][0], word[n][1]);
           }
           fence_proxy_async_smem();
@@ -1000,10 +990,6 @@ cudaError_t launch(cudaLaunchConfig_t cfg, const CUtensorMap& tm_ckv, const CUte
 }  // namespace
 
 int q8_rows_per_cta(int total_rows) { return total_rows <= 16 ? 16 : 32; }
-int q8_tile_tokens(int total_rows, bool bf16) {
-  if (q8_rows_per_cta(total_rows) == 16) return bf16 ? Cfg<16, true>::kT : Cfg<16, false>::kT;
-  return bf16 ? Cfg<32, true>::kT : Cfg<32, false>::kT;
-}
 int q8_gangs(int total_rows, int sms) {
   const int nr = q8_rows_per_cta(total_rows), groups = (total_rows + nr - 1) / nr;
   const int gangs = sms > groups ? sms / groups : 1;

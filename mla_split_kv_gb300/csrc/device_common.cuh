@@ -443,6 +443,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t start, uint32_t sbo)
   return d;
 }
 
+// The same for the 32-byte swizzle, MN-major: rows of 32 bytes, 8 of them a group, groups sbo bytes apart along K
+// and runs of 32 bytes lbo apart along the other dimension.
+__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t start, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((start >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(6) << 61;  // SWIZZLE_32B
+  return d;
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16 with an fp32 accumulator.
 // a_mn / b_mn: operand stored MN-major (1) or K-major (0).
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool bf16, bool a_mn, bool b_mn) {

@@ -180,13 +180,11 @@ struct DecodeQ8Params {
   int32_t B, H, h_shift, q_len, bs, bs_shift, max_blocks, num_blocks, g_shift, causal, window, sinks, out_dtype;
   int32_t gangs;               // CTAs that share the tiles of the batch, one per row group each
   int32_t groups, row_pad;     // row groups; rows padded to whole groups
-  int32_t tile;                // tokens per tile
   int32_t cuts_by_request;     // the batch has fewer rows than the grid has CTAs
   uint64_t timeout_ns;
 };
-// Rows per CTA, tokens per tile and gangs of the launch for q_len * H rows on a device of `sms` SMs.
+// Rows per CTA and gangs of the launch for q_len * H rows on a device of `sms` SMs.
 int q8_rows_per_cta(int total_rows);
-int q8_tile_tokens(int total_rows, bool bf16);
 int q8_gangs(int total_rows, int sms);
 // tm_ckv: boxes of one page of the byte cache, [8 rows x 128 columns] swizzled atoms, four column blocks to a
 // row group; tm_kpe: boxes of one page's 64 rope columns with the 64-byte swizzle.

@@ -1,7 +1,7 @@
 // How the tiles of a batch are shared out by the block-scaled 8-bit decode and
 // found again by its merge.
 //
-// The batch's visible runs, cut into tiles of p.tile tokens request after request,
+// The batch's visible runs, cut into tiles request after request,
 // are one line, with a gap of a few cells between requests: what a gang spends on
 // going from one request to the next (its output, the next one's queries, the
 // first tiles' rescales: 10 us at 32 rows, 5 at 16, about four tiles) counts as
@@ -26,11 +26,11 @@ __device__ __forceinline__ int q8_tiles(const WindowView& v, int tile) {
   return v.n / tile + (v.n % tile != 0 ? 1 : 0);
 }
 // Context lengths, the first of them kept in shared memory: the walks below read them one after the other.
-constexpr int kQ8Lens = 640;
+template <int kCached>
 struct Q8Lens {
   const int32_t* global;
-  const int32_t* cached;  // shared memory, kQ8Lens
-  __device__ __forceinline__ int operator()(int b) const { return b < kQ8Lens ? cached[b] : __ldcg(global + b); }
+  const int32_t* cached;  // shared memory, kCached
+  __device__ __forceinline__ int operator()(int b) const { return b < kCached ? cached[b] : __ldcg(global + b); }
 };
 
 // A pair of counts in one sum: tiles (at most 65535 * 2^25 < 2^44) and the requests that have any.
@@ -107,10 +107,10 @@ __device__ __forceinline__ Q8Walk q8_walk(int b0, int64_t off0, int64_t tiles) {
 }
 // The next segment; false at the end. (Its search is one function for all roles: code that is met once costs what
 // it takes to fetch, some ten cycles an instruction, and so it has been fetched after the first role's call.)
-template <int kT>
+template <int kT, int kCached>
 __device__ __noinline__ Q8Walk q8_search(const int32_t* lens_global, const int32_t* lens_cached, int q_len, int bs,
                                          int causal, int window, int sinks, int b, int start, int64_t left) {
-  const Q8Lens lens{lens_global, lens_cached};
+  const Q8Lens<kCached> lens{lens_global, lens_cached};
   Q8Walk w;
   do {
     ++b;
@@ -123,10 +123,10 @@ __device__ __noinline__ Q8Walk q8_search(const int32_t* lens_global, const int32
   w.left = left - (w.tb - start);
   return w;
 }
-template <int kT>
-__device__ __forceinline__ bool q8_next(const DecodeQ8Params& p, const Q8Lens& lens, Q8Walk& w, bool first) {
+template <int kT, int kCached>
+__device__ __forceinline__ bool q8_next(const DecodeQ8Params& p, const Q8Lens<kCached>& lens, Q8Walk& w, bool first) {
   if (w.left <= 0) return false;
-  w = q8_search<kT>(lens.global, lens.cached, p.q_len, p.bs, p.causal, p.window, p.sinks, w.b, first ? w.tb : 0, w.left);
+  w = q8_search<kT, kCached>(lens.global, lens.cached, p.q_len, p.bs, p.causal, p.window, p.sinks, w.b, first ? w.tb : 0, w.left);
   return true;
 }
 
