@@ -99,10 +99,10 @@ template <int NR, bool BF16>
 struct Cfg {
   // terms of a query, of a weight. Four for the weights of 16 rows: 64 columns take the MMA no longer than 48.
   static constexpr int kQTerms = BF16 ? 2 : 3, kTerms = NR == 16 ? 4 : 3;
-  // The reference maximum moves when a score passes it by more than kTau, so weights are at most 2^kTau; times
-  // 2^kWeightExp they fit E4M3's 448, and its subnormals reach down to 2^-25 of the reference in the last term.
-  static constexpr float kTau = NR == 16 ? 7.0f : 2.0f;
-  static constexpr int kWeightExp = NR == 16 ? 1 : 6;
+  // A row's reference lies 2^kWeightExp below the maximum it was taken from and moves when a score passes that by
+  // more than kTau, so weights are at most 2^(kTau + kWeightExp), within E4M3's 448, and its subnormals reach down to
+  // 2^-25 of the maximum in the last term.
+  static constexpr float kTau = NR == 16 ? 7.0f : 2.0f, kWeightExp = NR == 16 ? 1.0f : 6.0f;
   static constexpr int kNS = NR * kQTerms, kNP = NR * kTerms;      // N of the two products
   static constexpr int kSBufs = (4 * kNP + 2 * kNS <= 512) ? 2 : 1;  // score buffers in tensor memory
   // Weights: [kT tokens x kNP] bytes, N-major, a thread storing its token's row as words, in the place of the tile's
@@ -145,13 +145,19 @@ __device__ __forceinline__ void split_f16(uint32_t x, uint32_t* t) {
     if (i + 1 < N) x = next_term(x, e4m3x2_to_f16x2(t[i]));
   }
 }
-// The same for fp32 values: the first term and what it leaves in fp32, the rest of that (11 bits of it) in fp16.
+// The same for two weights. Three terms hold what a rounding to fp16 leaves (2^-12 of the value, or half of 2^-24 of
+// the least one); of four, the first and what it leaves are taken in fp32, the rest of that (11 bits of it) in fp16.
 template <int N>
-__device__ __forceinline__ void split_f32(float a, float b, uint32_t* t) {
-  t[0] = e4m3x2(a, b);
-  const float2 v = e4m3x2_values(t[0]);
-  const __half2 rest = __hmul2(__floats2half2_rn(a - v.x, b - v.y), __float2half2_rn(kTermStep));
-  split_f16<N - 1>(*reinterpret_cast<const uint32_t*>(&rest), t + 1);
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t* t) {
+  if constexpr (N == 3) {
+    const __half2 h = __floats2half2_rn(a, b);
+    split_f16<3>(*reinterpret_cast<const uint32_t*>(&h), t);
+  } else {
+    t[0] = e4m3x2(a, b);
+    const float2 v = e4m3x2_values(t[0]);
+    const __half2 rest = __hmul2(__floats2half2_rn(a - v.x, b - v.y), __float2half2_rn(kTermStep));
+    split_f16<N - 1>(*reinterpret_cast<const uint32_t*>(&rest), t + 1);
+  }
 }
 
 // NaN bytes of tokens [t0, t1) of a tile to zero: tokens that some row does not see. Its weight for them is 0,
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     const bool has_tokens = 32 * q4 < kT;  // (a 96-token tile leaves the last quadrant's warps without)
     const uint32_t bar = 1 + h;  // the four warps of a run of rows meet by themselves
     constexpr uint32_t kMeet = 128;
-    constexpr float w_up = static_cast<float>(1 << C::kWeightExp), w_down = 1.0f / w_up;
+    constexpr float kNone = -3.402823466e38f;  // the reference of a row that has seen no token: finite, below any score
     // this thread's page of a tile, and its token's scale there: loads a tile ahead of their use each, so
     // neither looks at what it loaded
     auto page_at = [&](const Q8Walk& w, int tile) -> int {
@@ -530,7 +536,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 #pragma unroll
       for (int k = 0; k < RH; ++k) {
         lsum[k] = 0.f;
-        mr[k] = -INFINITY;
+        mr[k] = kNone;
       }
       // rows' positions: the first and last row of this CTA, and what their windows leave out
       const int pos_first = p.causal ? w.v.n - p.q_len + (row0 >> p.h_shift) : w.v.n - 1;
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         // NaN for a scale that is neither NaN nor in range
         const float z = (z_raw >= 0x1p-60f && z_raw <= 0x1p60f) ? z_raw : __uint_as_float(0x7fc00000u);
         // (approximate: their errors, 2^-22, make a token's weight and its share of the sum wrong alike)
-        const float lz = __log2f(z), iz = __frcp_rn(z);
+        const float lz = __log2f(z), iz = z == z ? __frcp_rn(z) : 0.f;  // (NaN: who sees the token has a NaN weight)
         z_raw = tile + 1 < w.tb ? scale_at(pid, tile + 1) : 1.f;
         pid = tile + 2 < w.tb ? page_at(w, tile + 2) : -1;
         const int sb = i % C::kSBufs;
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         // only then are the rows' maxima taken, and the references move to them, with the sums and O.
         bool need = false;
 #pragma unroll
-        for (int k = 0; k < RH; ++k) need |= x[k] > mr[k] + C::kTau;
+        for (int k = 0; k < RH; ++k) need |= x[k] - mr[k] > C::kTau + C::kWeightExp;
         need = named_bar_sync_or(bar, kMeet, need || !ok || *abort_flag != 0);
         float al[RH];
         if (need) {
@@ -623,8 +629,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           }
 #pragma unroll
           for (int k = 0; k < RH; ++k) {
-            const float m = fmaxf(mr[k], v[k]);
-            al[k] = (mr[k] == -INFINITY) ? 1.f : fast_exp2(mr[k] - m);  // (nothing summed yet, or only NaN)
+            const float m = fmaxf(mr[k], v[k] - C::kWeightExp);
+            al[k] = fast_exp2(mr[k] - m);
             mr[k] = m;
             lsum[k] *= al[k];
           }
@@ -636,11 +642,11 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
             float wt[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              wt[j] = fast_exp2(x[k + j] - ((mr[k + j] == -INFINITY) ? 0.f : mr[k + j]));  // hidden tokens (-inf) give 0
-              lsum[k + j] += (wt[j] == 0.f) ? 0.f : wt[j] * iz;  // (a hidden token's scale may be NaN)
+              wt[j] = fast_exp2(x[k + j] - mr[k + j]);  // hidden tokens (-inf) give 0
+              lsum[k + j] = fmaf(wt[j], iz, lsum[k + j]);
             }
             uint32_t t[kTerms];
-            split_f32<kTerms>(wt[0] * w_up, wt[1] * w_up, t);
+            split_weights<kTerms>(wt[0], wt[1], t);
 #pragma unroll
             for (int n = 0; n < kTerms; ++n) word[n][k / 4] = (k & 2) ? word[n][k / 4] | (t[n] << 16) : t[n];
           }
@@ -732,12 +738,12 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       const int r = RH * h + (lane & (RH - 1));
       const auto& sum = sm->red[(i - 1) & 1];
       const float l = (sum[0][r] + sum[1][r]) + (sum[2][r] + sum[3][r]);
-      const float my_inv = !whole ? w_down : (l == 0.f ? 0.f : w_down / l);  // (no visible token: every weight was 0)
+      const float my_inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);  // (no visible token: every weight was 0)
       if (q4 == 0 && lane < my_rows && lane < RH) {
         if (!whole) {
-          *reinterpret_cast<float2*>(p.ws_ml + (orow + lane) * 2) = make_float2(m, l);
+          *reinterpret_cast<float2*>(p.ws_ml + (orow + lane) * 2) = make_float2(m == kNone ? -INFINITY : m, l);
         } else if (p.out_lse != nullptr) {
-          p.out_lse[orow + lane] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(l);
+          p.out_lse[orow + lane] = l == 0.f ? -INFINITY : (m == kNone ? 0.f : m) + log2f(l);
         }
       }
       float inv[RH];
