@@ -546,7 +546,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         // NaN for a scale that is neither NaN nor in range
         const float z = (z_raw >= 0x1p-60f && z_raw <= 0x1p60f) ? z_raw : __uint_as_float(0x7fc00000u);
         // (approximate: their errors, 2^-22, make a token's weight and its share of the sum wrong alike)
-        const float lz = __log2f(z), iz = z == z ? __frcp_rn(z) : 0.f;  // (NaN: who sees the token has a NaN weight)
+        const float lz = __log2f(z), iz = z == z ? fast_rcp(z) : 0.f;  // (NaN: who sees the token has a NaN weight)
         z_raw = tile + 1 < w.tb ? scale_at(pid, tile + 1) : 1.f;
         pid = tile + 2 < w.tb ? page_at(w, tile + 2) : -1;
         const int sb = i % C::kSBufs;
@@ -570,9 +570,14 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm->sfree[sb]);
 #pragma unroll
-          for (int k = 0; k < RH; ++k) {
-            if constexpr (C::kQTerms == 3) t2[k] = fmaf(t3[k], kTermInv, t2[k]);
-            x[k] = fmaf(fmaf(t2[k], kTermInv, x[k]) * factor[k], z, lz);
+          for (int k = 0; k < RH; k += 2) {
+            const float2 inv = make_float2(kTermInv, kTermInv);
+            float2 t = make_float2(t2[k], t2[k + 1]);
+            if constexpr (C::kQTerms == 3) t = fma2(make_float2(t3[k], t3[k + 1]), inv, t);
+            t = mul2(fma2(t, inv, make_float2(x[k], x[k + 1])), make_float2(factor[k], factor[k + 1]));
+            t = fma2(t, make_float2(z, z), make_float2(lz, lz));
+            x[k] = t.x;
+            x[k + 1] = t.y;
           }
           if (__builtin_expect(nvalid < kT || u0 + kT - 1 > pos_first || u0 <= low_last || nrows < NR, 0)) {
 #pragma unroll
@@ -601,7 +606,10 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         // only then are the rows' maxima taken, and the references move to them, with the sums and O.
         bool need = false;
 #pragma unroll
-        for (int k = 0; k < RH; ++k) need |= x[k] - mr[k] > C::kTau + C::kWeightExp;
+        for (int k = 0; k < RH; k += 2) {
+          const float2 d = fma2(make_float2(mr[k], mr[k + 1]), make_float2(-1.f, -1.f), make_float2(x[k], x[k + 1]));
+          need |= d.x > C::kTau + C::kWeightExp || d.y > C::kTau + C::kWeightExp;
+        }
         need = named_bar_sync_or(bar, kMeet, need || !ok || *abort_flag != 0);
         float al[RH];
         if (need) {
@@ -639,14 +647,13 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           uint32_t word[kTerms][RH / 4];
 #pragma unroll
           for (int k = 0; k < RH; k += 2) {
-            float wt[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              wt[j] = fast_exp2(x[k + j] - mr[k + j]);  // hidden tokens (-inf) give 0
-              lsum[k + j] = fmaf(wt[j], iz, lsum[k + j]);
-            }
+            const float2 d = fma2(make_float2(mr[k], mr[k + 1]), make_float2(-1.f, -1.f), make_float2(x[k], x[k + 1]));
+            const float2 wt = make_float2(fast_exp2(d.x), fast_exp2(d.y));  // hidden tokens (-inf) give 0
+            const float2 l = fma2(wt, make_float2(iz, iz), make_float2(lsum[k], lsum[k + 1]));
+            lsum[k] = l.x;
+            lsum[k + 1] = l.y;
             uint32_t t[kTerms];
-            split_weights<kTerms>(wt[0], wt[1], t);
+            split_weights<kTerms>(wt.x, wt.y, t);
 #pragma unroll
             for (int n = 0; n < kTerms; ++n) word[n][k / 4] = (k & 2) ? word[n][k / 4] | (t[n] << 16) : t[n];
           }
@@ -664,7 +671,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         if (need && tile > w.ta) {  // O: the value product of the tile before must be complete
           if (__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo))) {
             tc_fence_after();
-#pragma unroll 2
+#pragma unroll (BF16 ? 2 : 1)  // (registers)
             for (int blk = 0; blk < 4; ++blk) {
               float v[kTerms][RH];
               const uint32_t a = tmem + lane_base + C::kTmemO + blk * C::kNP + RH * h;
