@@ -138,7 +138,7 @@ __device__ __forceinline__ uint32_t next_term(uint32_t x, uint32_t v) {
 // x = t1 + t2 / 32 + ... for a pair of fp16 values of at most 256, each term two E4M3 bytes: x has 11 bits, so
 // what a term leaves, and that times 32, are fp16 values themselves, and the third term leaves nothing
 template <int N>
-__device__ __forceinline__ void split_f16(uint32_t x, uint32_t* t) {
+__device__ __forceinline__ void split_f16(uint32_t x, uint16_t* t) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     t[i] = f16x2_to_e4m3x2(x);
@@ -148,7 +148,7 @@ __device__ __forceinline__ void split_f16(uint32_t x, uint32_t* t) {
 // The same for two weights. Three terms hold what a rounding to fp16 leaves (2^-12 of the value, or half of 2^-24 of
 // the least one); of four, the first and what it leaves are taken in fp32, the rest of that (11 bits of it) in fp16.
 template <int N>
-__device__ __forceinline__ void split_weights(float a, float b, uint32_t* t) {
+__device__ __forceinline__ void split_weights(float a, float b, uint16_t* t) {
   if constexpr (N == 3) {
     const __half2 h = __floats2half2_rn(a, b);
     split_f16<3>(*reinterpret_cast<const uint32_t*>(&h), t);
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
       if (x == 2 && lane >= kRope / 8) break;
-      uint32_t t[4][C::kQTerms];
+      uint16_t t[4][C::kQTerms];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const uint32_t w = u[4 * x + y];
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
                           : q + 4 * C::kQChunk + r * 64 + (((lane >> 1) ^ (r >> 1)) & 3) * 16 + (lane & 1) * 8;
 #pragma unroll
       for (int n = 0; n < C::kQTerms; ++n)  // (NR rows on: the same swizzle)
-        *reinterpret_cast<uint2*>(at + n * NR * (x < 2 ? 128 : 64)) = make_uint2(t[0][n] | (t[1][n] << 16), t[2][n] | (t[3][n] << 16));
+        *reinterpret_cast<uint2*>(at + n * NR * (x < 2 ? 128 : 64)) = make_uint2(pack16(t[0][n], t[1][n]), pack16(t[2][n], t[3][n]));
     }
   };
   if (warp == C::kLoadWarp) {
@@ -512,14 +512,15 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     // this thread's page of a tile, and its token's scale there: loads a tile ahead of their use each, so
     // neither looks at what it loaded
     auto page_at = [&](const Q8Walk& w, int tile) -> int {
-      if (tl >= min(kT, w.v.n - tile * kT)) return -1;
-      const int u = tile * kT + tl;
+      const uint32_t at = tile * kT + tl;  // (past 2^31 at the end of the longest context)
+      if (!has_tokens || at >= static_cast<uint32_t>(w.v.n)) return -1;
+      const int u = static_cast<int>(at);
       const int pg = (u >> p.bs_shift) + (u >= w.v.sa ? w.v.skip >> p.bs_shift : 0);
-      return pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
+      return pg < p.max_blocks ? __ldg(p.block_table + (static_cast<long long>(w.b) * p.max_blocks + pg)) : -1;
     };
     auto scale_at = [&](int pid, int tile) -> float {  // 1 where there is no page
       if (pid < 0 || pid >= p.num_blocks) return 1.f;
-      const long long row = (static_cast<long long>(pid) << p.bs_shift) + ((tile * kT + tl) & (p.bs - 1));
+      const int row = (pid << p.bs_shift) + ((tile * kT + tl) & (p.bs - 1));  // (a pool has fewer than 2^31 tokens)
       return __ldg(p.scales + (row >> p.g_shift));
     };
     int i = 0;  // tile count
@@ -542,6 +543,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       const int pos_first = p.causal ? w.v.n - p.q_len + (row0 >> p.h_shift) : w.v.n - 1;
       const int pos_last = p.causal ? w.v.n - p.q_len + ((row0 + nrows - 1) >> p.h_shift) : w.v.n - 1;
       const int low_last = p.window > 0 ? max(-1, pos_last - p.window) : -1;
+      // tiles of which every row sees every token
+      const int plain_lo = (low_last + kT) / kT, plain_hi = nrows < NR ? 0 : max(0, pos_first + 1) / kT;
       for (int tile = w.ta; tile < w.tb; ++tile, ++i) {
         // NaN for a scale that is neither NaN nor in range
         const float z = (z_raw >= 0x1p-60f && z_raw <= 0x1p60f) ? z_raw : __uint_as_float(0x7fc00000u);
@@ -552,7 +555,6 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         const int sb = i % C::kSBufs;
         bool ok = mbar_wait(&sm->sfull[sb], (i / C::kSBufs) & 1, tmo);
         float x[RH];
-        const int u0 = tile * kT, nvalid = min(kT, w.v.n - u0);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && has_tokens) {
           tc_fence_after();
@@ -579,7 +581,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
             x[k] = t.x;
             x[k + 1] = t.y;
           }
-          if (__builtin_expect(nvalid < kT || u0 + kT - 1 > pos_first || u0 <= low_last || nrows < NR, 0)) {
+          if (__builtin_expect(tile < plain_lo || tile >= plain_hi, 0)) {
+            const int u0 = tile * kT, nvalid = min(kT, w.v.n - u0);
 #pragma unroll
             for (int k = 0; k < RH; ++k) {
               const int r = row0 + RH * h + k, u = u0 + tl;
@@ -644,7 +647,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           }
         }
         if (has_tokens) {
-          uint32_t word[kTerms][RH / 4];
+          uint16_t term[RH / 2][kTerms];
 #pragma unroll
           for (int k = 0; k < RH; k += 2) {
             const float2 d = fma2(make_float2(mr[k], mr[k + 1]), make_float2(-1.f, -1.f), make_float2(x[k], x[k + 1]));
@@ -652,10 +655,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
             const float2 l = fma2(wt, make_float2(iz, iz), make_float2(lsum[k], lsum[k + 1]));
             lsum[k] = l.x;
             lsum[k + 1] = l.y;
-            uint32_t t[kTerms];
-            split_weights<kTerms>(wt.x, wt.y, t);
-#pragma unroll
-            for (int n = 0; n < kTerms; ++n) word[n][k / 4] = (k & 2) ? word[n][k / 4] | (t[n] << 16) : t[n];
+            split_weights<kTerms>(wt.x, wt.y, term[k / 2]);
           }
           uint8_t* const pb = smem + (i % kSlots) * kTileSlot + kCkvBytes;  // (the scores are done with what lay there)
           // columns n * NR + 8 h .. + 7 of this token's row: half of one 16-byte piece
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
             const int piece = (n * NR + RH * h) >> 4;
             const int at = C::kPRow == 32 ? (piece >> 1) * kT * 32 + tl * 32 + ((piece ^ (tl >> 2)) & 1) * 16
                                           : tl * 64 + ((piece ^ (tl >> 1)) & 3) * 16;
-            *reinterpret_cast<uint2*>(pb + at + (h & 1) * 8) = make_uint2(word[n][0], word[n][1]);
+            *reinterpret_cast<uint2*>(pb + at + (h & 1) * 8) = make_uint2(pack16(term[0][n], term[1][n]), pack16(term[2][n], term[3][n]));
           }
           fence_proxy_async_smem();
         }

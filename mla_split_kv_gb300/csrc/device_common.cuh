@@ -830,27 +830,33 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
 }
 
 // two values to two E4M3 bytes (a in the low one), round to nearest even, +-448 beyond
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+__device__ __forceinline__ uint16_t e4m3x2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
+// two halves of a word (as registers of 16 bits: one instruction, no extension of either)
+__device__ __forceinline__ uint32_t pack16(uint16_t lo, uint16_t hi) {
+  uint32_t w;
+  asm("mov.b32 %0, {%1, %2};" : "=r"(w) : "h"(lo), "h"(hi));
+  return w;
+}
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+  return pack16(e4m3x2(a, b), e4m3x2(c, d));
 }
 // between fp16 and E4M3 (two values in a word)
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t h) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t w) {
   uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(w));
   return h;
 }
 // the values of two E4M3 bytes (exact)
-__device__ __forceinline__ float2 e4m3x2_values(uint32_t w) {
+__device__ __forceinline__ float2 e4m3x2_values(uint16_t w) {
   const uint32_t h = e4m3x2_to_f16x2(w);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
