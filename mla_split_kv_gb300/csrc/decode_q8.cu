@@ -671,7 +671,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
         if (need && tile > w.ta) {  // O: the value product of the tile before must be complete
           if (__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo))) {
             tc_fence_after();
-#pragma unroll (BF16 ? 2 : 1)  // (registers)
+#pragma unroll 1
             for (int blk = 0; blk < 4; ++blk) {
               float v[kTerms][RH];
               const uint32_t a = tmem + lane_base + C::kTmemO + blk * C::kNP + RH * h;
@@ -681,7 +681,11 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 #pragma unroll
               for (int n = 0; n < kTerms; ++n) {
 #pragma unroll
-                for (int k = 0; k < RH; ++k) v[n][k] *= al[k];
+                for (int k = 0; k < RH; k += 2) {
+                  const float2 y = mul2(make_float2(v[n][k], v[n][k + 1]), make_float2(al[k], al[k + 1]));
+                  v[n][k] = y.x;
+                  v[n][k + 1] = y.y;
+                }
                 tmem_st8(a + n * NR, v[n]);
               }
             }
@@ -770,11 +774,13 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           if (lane == 0) mbar_arrive(&sm->ofree);
         }
 #pragma unroll
-        for (int k = 0; k < RH; ++k) {
-          float v = o[kTerms - 1][k];
+        for (int k = 0; k < RH; k += 2) {
+          float2 v = make_float2(o[kTerms - 1][k], o[kTerms - 1][k + 1]);
 #pragma unroll
-          for (int n = kTerms - 2; n >= 0; --n) v = fmaf(v, kTermInv, o[n][k]);
-          o[0][k] = v * inv[k];
+          for (int n = kTerms - 2; n >= 0; --n) v = fma2(v, make_float2(kTermInv, kTermInv), make_float2(o[n][k], o[n][k + 1]));
+          v = mul2(v, make_float2(inv[k], inv[k + 1]));
+          o[0][k] = v.x;
+          o[0][k + 1] = v.y;
         }
         // (rows and blocks of columns at fixed distances: one address a thread)
         if (f32) {
