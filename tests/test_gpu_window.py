@@ -204,3 +204,30 @@ def test_decode_window_refuses_wrong_tensors():
                 dict(block_table=dc.block_table.long()), dict(context_lens=dc.context_lens.repeat(2))):
         with pytest.raises(ValueError):
             rt.decode_window(plan, **{**args, **bad})
+
+
+@pytest.mark.parametrize("n", [1, 2, 33, 40])
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_merges_of_many_rows_have_the_bits_of_few(n, out_dtype):
+    """2048 rows and more are merged by a warp a row, fewer by four: request by request the same bits. Some parts
+    have no mass, one request none at all."""
+    B, H = 20, 128
+    gen_t = torch.Generator(device="cuda").manual_seed(5)
+    part = torch.randn(B * n, 1, H, 512, device="cuda", generator=gen_t)
+    lse = 4 * torch.randn(B * n, 1, H, device="cuda", generator=gen_t)
+    lse[::3, :, ::5] = -float("inf")
+    lse[n:2 * n] = -float("inf")
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[out_dtype]
+
+    def merge(lo, hi):
+        out, out_lse = torch.empty(hi - lo, 1, H, 512, dtype=dt, device="cuda"), torch.empty(hi - lo, 1, H, device="cuda")
+        nb.mla_merge_states(part[lo * n:].data_ptr(), lse[lo * n:].data_ptr(), rt.uniform_indptr(hi - lo, n).data_ptr(),
+                            hi - lo, 1, H, out.data_ptr(), rt.CODE_OF[dt], out_lse.data_ptr(), None)
+        torch.cuda.synchronize()
+        return out, out_lse
+
+    out, out_lse = merge(0, B)
+    for b in range(B):
+        one, one_lse = merge(b, b + 1)
+        assert torch.equal(out[b], one[0]) and torch.equal(out_lse[b], one_lse[0])
+    assert not out[1].any() and torch.isneginf(out_lse[1]).all()
