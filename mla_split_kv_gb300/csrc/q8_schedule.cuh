@@ -109,14 +109,15 @@ __device__ __forceinline__ Q8Walk q8_walk(int b0, int64_t off0, int64_t tiles) {
 // it takes to fetch, some ten cycles an instruction, and so it has been fetched after the first role's call.)
 template <int kT, int kCached>
 __device__ __noinline__ Q8Walk q8_search(const int32_t* lens_global, const int32_t* lens_cached, int q_len, int bs,
-                                         int causal, int window, int sinks, int b, int start, int64_t left) {
+                                         int causal, int window, int sinks, int B, int b, int start, int64_t left) {
   const Q8Lens<kCached> lens{lens_global, lens_cached};
   Q8Walk w;
   do {
     ++b;
-    w.v = window_view(lens(b), q_len, bs, causal, window, sinks);
+    w.v = window_view(b < B ? lens(b) : 0, q_len, bs, causal, window, sinks);
     w.n_tiles = q8_tiles(w.v, kT);
-  } while (w.n_tiles == 0);
+  } while (w.n_tiles == 0 && b < B);
+  if (b >= B) left = 0;  // (only when the lengths changed under the call: the walk ends, the waits run out)
   w.b = b;
   w.ta = start;
   w.tb = static_cast<int>(w.n_tiles < start + left ? w.n_tiles : start + left);
@@ -126,7 +127,7 @@ __device__ __noinline__ Q8Walk q8_search(const int32_t* lens_global, const int32
 template <int kT, int kCached>
 __device__ __forceinline__ bool q8_next(const DecodeQ8Params& p, const Q8Lens<kCached>& lens, Q8Walk& w, bool first) {
   if (w.left <= 0) return false;
-  w = q8_search<kT, kCached>(lens.global, lens.cached, p.q_len, p.bs, p.causal, p.window, p.sinks, w.b, first ? w.tb : 0, w.left);
+  w = q8_search<kT, kCached>(lens.global, lens.cached, p.q_len, p.bs, p.causal, p.window, p.sinks, p.B, w.b, first ? w.tb : 0, w.left);
   return true;
 }
 

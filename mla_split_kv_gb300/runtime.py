@@ -274,10 +274,16 @@ def _window_partitions(runs: Sequence[int], num_heads: int, q_len: int, block_si
 
 def plan_window(context_lens: Sequence[int], num_heads: int, q_len: int, block_size: int, window: int, sinks: int = 0,
                 dtype: str = "f16", causal: bool = False, dev: Optional[nb.mla_device_info_t] = None,
-                max_partitions: int = 0, device="cuda") -> WindowPlan:
+                max_partitions: int = 0, device="cuda", grow: int = 0) -> WindowPlan:
     """Partitions of the requests' visible runs: at most max_partitions each by mla_plan's thresholds, or (0) as many
-    as fill the device."""
+    as fill the device. `grow`: tokens by which each context may grow while the plan is used (a run's length goes up
+    and down by a page with its context's place in the page, so a plan made for one length may miss the next)."""
+    if grow < 0:
+        raise ValueError(f"grow: {grow}")
     runs = nb.mla_window_lens(context_lens, q_len, block_size, causal, window, sinks)
+    for back in range(min(grow, block_size)):  # the longest run on the way is within a page of its end
+        lens = [min(int(n) + grow - back, 2 ** 31 - 1) for n in context_lens]
+        runs = [max(a, b) for a, b in zip(runs, nb.mla_window_lens(lens, q_len, block_size, causal, window, sinks))]
     index = torch.device(device).index
     dev = dev if dev is not None else nb.mla_device_query(-1 if index is None else index)
     if max_partitions:

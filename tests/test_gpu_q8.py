@@ -503,3 +503,34 @@ def test_append_q8_beside_tokens_under_a_foreign_scale(g, scale):
     want = orc.cache_append_q8(case.ckv, case.kpe, case.scales, case.table, case.lens, orc.decode16(c, "f16"), orc.decode16(k, "f16"))
     append(case, c, k)
     same_cache(case, want)
+
+
+@pytest.mark.parametrize("H,q_len,dtype", [(128, 32, "f16"), (64, 32, "bf16"), (128, 5, "bf16")])
+def test_decode_q8_many_rows(H, q_len, dtype):
+    """More row groups than there are SMs, or nearly: one gang, two, or nine."""
+    case = Q8Case(40, [300, 0, 31, 900], H=H, q_len=q_len, bs=32, g=16, dtype=dtype, causal=True).upload()
+    out, lse = case.decode("f32")
+    case.check(out, lse, heads=[0, H - 1])
+
+
+def test_q8_calls_reach_past_four_gigabytes():
+    """Pages whose bytes lie more than 2^32 into the pool, written and read."""
+    nblk, bs = 140_000, 64  # 4.6 GB of latent bytes
+    case = Q8Case(41, [200, 70], bs=bs, g=8, dtype="bf16", pow2=True)
+    small, n = case.table.copy(), case.nb
+    case.table = np.where(small >= 0, small + (nblk - n), small).astype(np.int32)
+    pool = rt.Q8Cache(torch.empty(nblk, bs, 512, dtype=torch.uint8, device="cuda"),
+                      torch.empty(nblk, bs, 64, dtype=torch.uint8, device="cuda"), torch.empty(nblk, bs // 8, device="cuda"))
+    for whole, part in zip((pool.ckv, pool.kpe, pool.scales), (case.ckv, case.kpe, case.scales)):
+        whole[nblk - n:] = torch.from_numpy(part).cuda()
+    case.upload()
+    case.cache = pool
+    c, k = new_tokens(42, 2, 1, "bf16", spread=1.0)
+    append(case, c, k)
+    out, lse = case.decode("f32")
+    case.table = small
+    case.ckv, case.kpe, case.scales = orc.cache_append_q8(case.ckv, case.kpe, case.scales, small, case.lens,
+                                                          orc.decode16(c, "bf16"), orc.decode16(k, "bf16"))
+    for whole, part in zip((pool.ckv, pool.kpe, pool.scales), (case.ckv, case.kpe, case.scales)):
+        assert np.array_equal(whole[nblk - n:].cpu().numpy(), part)
+    case.check(out, lse)

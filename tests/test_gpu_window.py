@@ -75,9 +75,9 @@ LENS = [0, 1, 40, 333, 2500, 5003]
     (16, 1, 32, "f16", False),    # the paired 16-row kernel
     (16, 1, 16, "bf16", False),
     (16, 1, 64, "e4m3", False),
-    (16, 4, 32, "f16", True),     # 64 rows: the 128-row kernel, fp32 exchange
+    (16, 4, 32, "f16", True),     # 64 rows: the 128-row kernel, half of it padding
     (64, 1, 16, "bf16", False),
-    (128, 1, 64, "bf16", False),  # a full group: no exchange
+    (128, 1, 64, "bf16", False),  # a full group
     (16, 9, 32, "bf16", True),    # 144 rows: a second, ragged group
     (16, 32, 64, "f16", True),
     (64, 2, 32, "e4m3", True),

@@ -113,3 +113,26 @@ def test_window_partitions_cover_the_runs_in_order(lens, H, q_len):
             assert t1 > t0 or (len(parts) == 1 and n == 0)
             at = t1
         assert parts and at == n
+
+
+@pytest.mark.parametrize("q_len,causal", [(1, False), (5, True)])
+def test_a_window_plan_covers_growing_contexts(monkeypatch, q_len, causal):
+    """With `grow`, every run up to that many tokens later is covered, whatever the page phase; without, the very
+    next one may not be."""
+    monkeypatch.setattr(rt, "alloc_partials", lambda *a, **k: (None, None))
+    monkeypatch.setattr(rt, "alloc_decode_workspace", lambda *a, **k: None)
+    bs, W, S, dev = 32, 300, 5, fake_gb300()
+    lens = [0, 1, 290, 310, 1000, 1023, 5000]
+    covered = lambda plan: [plan.plan.chunks[plan.plan.o_indptr[b + 1] - 1][2] for b in range(len(lens))]  # noqa: E731
+    missed = False
+    for grow in (0, 1, 20, 33, 400):
+        got = covered(rt.plan_window(lens, 16, q_len, bs, W, S, causal=causal, dev=dev, device="cpu", grow=grow))
+        for more in range(grow + 1):
+            runs = nb.mla_window_lens([n + more for n in lens], q_len, bs, causal, W, S)
+            assert all(n <= c for n, c in zip(runs, got)), (grow, more)
+        if grow == 0:
+            runs = nb.mla_window_lens([n + 1 for n in lens], q_len, bs, causal, W, S)
+            missed = any(n > c for n, c in zip(runs, got))
+    assert missed
+    with pytest.raises(ValueError):
+        rt.plan_window(lens, 16, q_len, bs, W, S, dev=dev, device="cpu", grow=-1)
