@@ -16,7 +16,7 @@
 // read twice, and 4.6 KB per warp are in flight), the warps of a block meet
 // once, and the maximum is taken over the 16-bit patterns themselves: without
 // its sign a pattern orders like its value, NaN above infinity. 65,536 tokens
-// in blocks of one: 25.1 us, 4.5 TB/s (one token at a time per warp, read
+// in blocks of one: 24.6 us, 4.6 TB/s (one token at a time per warp, read
 // twice: 87 us); a single token: 3.8 us.
 #include "device_common.cuh"
 
@@ -24,7 +24,7 @@ namespace mla {
 
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 16, kFewWarps = 8;  // of a CTA; where a block needs no more, 8: shorter tails (24.6 us, 26.2 with 16)
 constexpr int kHold = 4;  // tokens per warp: 16 warps hold a block of the longest page, 64 tokens
 constexpr int kMinExp = -60, kMaxExp = 60;
 
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mla_append_q8_kernel(const App
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp & (subs - 1);
-  const uint32_t unit = blockIdx.x * (kWarps / subs) + warp / subs;  // (at most 1.25 B q_len + 2 B: below 2^32)
+  const uint32_t unit = blockIdx.x * ((blockDim.x >> 5) / subs) + warp / subs;  // (at most 1.25 B q_len + 2 B: below 2^32)
   if (unit >= per_request * p.B) return;
   const uint32_t b = unit / per_request;
   const int run = subs * kHold;
@@ -198,10 +198,11 @@ cudaError_t launch_append_q8(const AppendQ8Params& p, bool bf16, cudaStream_t st
   // aligned runs that q_len consecutive tokens can touch
   const uint32_t per_request = static_cast<uint32_t>((static_cast<int64_t>(p.q_len) + run - 2) / run + 1);
   const int64_t units = static_cast<int64_t>(p.B) * per_request;
-  const int64_t blocks = (units + kWarps / subs - 1) / (kWarps / subs);
+  const int warps = subs > kFewWarps ? kWarps : kFewWarps;
+  const int64_t blocks = (units + warps / subs - 1) / (warps / subs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.blockDim = dim3(warps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
