@@ -83,7 +83,7 @@ template <int kLens>
 struct Small {
   uint64_t full[kSlots], empty[kSlots][kSteps];  // tile slots, freed step by step
   uint64_t sfull[2], sfree[2];           // score buffers
-  uint64_t pfull[kSlots], pvdone[2];  // weights per slot; value products per tile parity
+  uint64_t pfull[kSlots];                // weights per slot
   uint64_t qfull, ofree, drain[2];
   int64_t scratch[33];
   int64_t off0, first_tile, last_tile;
@@ -206,7 +206,6 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm->sfull[s], 1);
       mbar_init(&sm->sfree[s], kSoftmaxWarps);
-      mbar_init(&sm->pvdone[s], 1);
     }
     mbar_init(&sm->qfull, kSoftmaxWarps);
     mbar_init(&sm->ofree, kSoftmaxWarps);
@@ -492,7 +491,6 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
             }
             umma_commit(&sm->empty[i % kSlots][ks]);
           }
-          umma_commit(&sm->pvdone[i & 1]);
         }
       }
       if (!ok) *abort_flag = 1;
@@ -523,6 +521,9 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       const int row = (pid << p.bs_shift) + ((tile * kT + tl) & (p.bs - 1));  // (a pool has fewer than 2^31 tokens)
       return __ldg(p.scales + (row >> p.g_shift));
     };
+    // The value product of tile t: its last step has left the slot. (The phase before on that barrier, tile t - kSlots,
+    // was complete before tile t was loaded, so its parity cannot be taken for this one's.)
+    auto product_done = [&](int t) -> bool { return mbar_wait(&sm->empty[t % kSlots][kSteps - 1], (t / kSlots) & 1, tmo); };
     int i = 0;  // tile count
     // Each round: a request's tiles, the split of the next one's queries (while the last value product runs), then
     // the request's output. The first round only splits.
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           fence_proxy_async_smem();
         }
         if (need && tile > w.ta) {  // O: the value product of the tile before must be complete
-          if (__all_sync(0xffffffffu, mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo))) {
+          if (__all_sync(0xffffffffu, product_done(i - 1))) {
             tc_fence_after();
 #pragma unroll 1
             for (int blk = 0; blk < 4; ++blk) {
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
      }
      if (seg >= 0) {
       // the segment's end: its sums, and O once its last value product is complete
-      const bool ended = mbar_wait(&sm->pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, tmo);
+      const bool ended = product_done(i - 1);
       if (!ended) *abort_flag = 1;
       // rows' sums over the warp's tokens: at each of three steps a lane hands half of its rows to its partner
 #pragma unroll

@@ -534,3 +534,29 @@ def test_q8_calls_reach_past_four_gigabytes():
     for whole, part in zip((pool.ckv, pool.kpe, pool.scales), (case.ckv, case.kpe, case.scales)):
         assert np.array_equal(whole[nblk - n:].cpu().numpy(), part)
     case.check(out, lse)
+
+
+COLD = """
+import sys
+import numpy as np
+import tests.test_gpu_q8 as t
+from mla_split_kv_gb300 import binding as nb
+nb.load()
+for H, dtype in ((16, "f16"), (16, "bf16"), (64, "f16"), (64, "bf16")):
+    case = t.Q8Case(50, [30001, 0, 4000], H=H, bs=32, g=1, dtype=dtype).upload()
+    first, first_lse = case.decode("f32")
+    for _ in range(3):
+        out, lse = case.decode("f32")
+    assert t.torch.equal(first, out) and t.torch.equal(first_lse, lse), (H, dtype)
+    case.check(first, first_lse, heads=[3, H - 1], requests=[2])
+print("same bits")
+"""
+
+
+def test_decode_q8_first_calls_of_a_process():
+    """Cold caches spread the warps of a CTA apart as nothing later does: the first call's bits are the later ones'."""
+    import subprocess
+    import sys
+
+    r = subprocess.run([sys.executable, "-c", COLD], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same bits" in r.stdout, r.stdout + r.stderr
