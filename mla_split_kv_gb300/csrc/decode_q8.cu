@@ -544,8 +544,9 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       const int pos_first = p.causal ? w.v.n - p.q_len + (row0 >> p.h_shift) : w.v.n - 1;
       const int pos_last = p.causal ? w.v.n - p.q_len + ((row0 + nrows - 1) >> p.h_shift) : w.v.n - 1;
       const int low_last = p.window > 0 ? max(-1, pos_last - p.window) : -1;
-      // tiles of which every row sees every token
-      const int plain_lo = (low_last + kT) / kT, plain_hi = nrows < NR ? 0 : max(0, pos_first + 1) / kT;
+      // tiles of which every row sees every token (rows past the last, zeros, may see what they like: nothing of
+      // theirs is written)
+      const int plain_lo = (low_last + kT) / kT, plain_hi = max(0, pos_first + 1) / kT;
       for (int tile = w.ta; tile < w.tb; ++tile, ++i) {
         // NaN for a scale that is neither NaN nor in range
         const float z = (z_raw >= 0x1p-60f && z_raw <= 0x1p60f) ? z_raw : __uint_as_float(0x7fc00000u);
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
             for (int k = 0; k < RH; ++k) {
               const int r = row0 + RH * h + k, u = u0 + tl;
               const int pos = p.causal ? w.v.n - p.q_len + (r >> p.h_shift) : w.v.n - 1;
-              bool vis = tl < nvalid && RH * h + k < nrows && u <= pos;
+              bool vis = tl < nvalid && u <= pos;
               if (p.window > 0) vis = vis && (u > pos - p.window || u < p.sinks);
               if (!vis) x[k] = -INFINITY;
             }
