@@ -828,7 +828,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
 // both keep it short, and a warp asks for its own entry of ws_cut only (a list of all entries made by every block:
 // the same lines asked for by a thousand blocks, 1 to 3 us).
 constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeBlocks = 7;  // per SM: one wave
+constexpr int kMergeBlocks = 8;  // per SM: one wave
 
 // a part's weight: one without a visible token has l = 0; one whose every score is NaN has no maximum, and l NaN
 __device__ __forceinline__ float part_weight(float m, float l, float ref) {
@@ -865,7 +865,7 @@ __device__ __forceinline__ void merge_out(const DecodeQ8Params& p, long long br,
 
 // Batches whose rows fill the device: kRowWarps warps a (gang, row), which end at once where no request with that
 // gang as its first is cut. Lane x weighs part x, then the parts' columns go by, 8 float4 a lane in flight.
-constexpr int kRowWarps = 2, kRowLoads = 4 / kRowWarps;
+constexpr int kRowWarps = 2, kRowLoads = 4 / kRowWarps, kRowParts = 8 / kRowLoads;
 __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_rows_kernel(const DecodeQ8Params p) {
   const int lane = threadIdx.x & 31;
   const uint32_t rows_total = p.q_len * p.H, per_gang = rows_total * kRowWarps, units = p.gangs * per_gang;
@@ -877,33 +877,41 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_rows
     const int n = cut.y;
     if (!merge_entry_ok(p, cut.x, j0, n)) continue;
     const MergeParts parts(p, j0, row);
-    float M = -INFINITY, den = 0.f;
+    float4 v[kRowParts][kRowLoads];
+    auto load = [&](int x0) {
+#pragma unroll
+      for (int y = 0; y < kRowParts; ++y)
+#pragma unroll
+        for (int k = 0; k < kRowLoads; ++k)
+          v[y][k] = x0 + y < n ? parts.values(x0 + y, col + 128 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);  // (they do not depend on the weights)
+    float M = -INFINITY, den = 0.f, w = 0.f;
     float4 acc[kRowLoads];
 #pragma unroll
     for (int k = 0; k < kRowLoads; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int x0 = 0; x0 < n; x0 += 32) {
-      const float2 ml = x0 + lane < n ? parts.max_sum(x0 + lane) : make_float2(-INFINITY, 0.f);
-      const float m = fmaxf(M, warp_max(ml.x)), ref = m == -INFINITY ? 0.f : m;
-      const float al = M == -INFINITY ? 1.f : exp2f(M - ref);  // (nothing summed before the first, or only NaN)
-      const float w = part_weight(ml.x, ml.y, ref);
-      float sum = w * ml.y;
+    for (int x0 = 0; x0 < n; x0 += kRowParts) {
+      if (x0 % 32 == 0) {  // lane x weighs part x0 + x
+        const float2 ml = x0 + lane < n ? parts.max_sum(x0 + lane) : make_float2(-INFINITY, 0.f);
+        const float m = fmaxf(M, warp_max(ml.x)), ref = m == -INFINITY ? 0.f : m;
+        const float al = M == -INFINITY ? 1.f : exp2f(M - ref);  // (nothing summed before the first, or only NaN)
+        w = part_weight(ml.x, ml.y, ref);
+        float sum = w * ml.y;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      den = fmaf(den, al, sum);
-      M = m;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        den = fmaf(den, al, sum);
+        M = m;
 #pragma unroll
-      for (int k = 0; k < kRowLoads; ++k) acc[k] = make_float4(acc[k].x * al, acc[k].y * al, acc[k].z * al, acc[k].w * al);
-      const int here = min(32, n - x0);
-#pragma unroll (8 / kRowLoads)
-      for (int x = 0; x < here; ++x) {
-        float4 v[kRowLoads];
-#pragma unroll
-        for (int k = 0; k < kRowLoads; ++k) v[k] = parts.values(x0 + x, col + 128 * k);
-        const float wx = __shfl_sync(0xffffffffu, w, x);
-#pragma unroll
-        for (int k = 0; k < kRowLoads; ++k) fma4(acc[k], wx, v[k]);
+        for (int k = 0; k < kRowLoads; ++k) acc[k] = make_float4(acc[k].x * al, acc[k].y * al, acc[k].z * al, acc[k].w * al);
       }
+#pragma unroll
+      for (int y = 0; y < kRowParts; ++y) {
+        const float wx = __shfl_sync(0xffffffffu, w, (x0 + y) & 31);  // (0 past the last part)
+#pragma unroll
+        for (int k = 0; k < kRowLoads; ++k) fma4(acc[k], wx, v[y][k]);
+      }
+      if (x0 + kRowParts < n) load(x0 + kRowParts);
     }
     const long long br = static_cast<long long>(cut.x) * rows_total + row;
     const bool none = den == 0.f;
