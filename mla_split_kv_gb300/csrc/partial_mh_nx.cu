@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mla_partial_mh_nx_kernel(const __grid_constant__ CUtensorMap tm_pages,
                              const __grid_constant__ CUtensorMap tm_kpe_half, const PartialParams p) {
   extern __shared__ uint8_t smem_raw[];
-  pdl_launch_dependents();  // the merge of these partials may be scheduled now; it waits for this grid
+  if (!kWin) pdl_launch_dependents();  // the merge of these partials may be scheduled now; it waits for this grid
   uint8_t* smem = align1024(smem_raw);
   uint8_t* qs = smem + kOffQ;
   Small* sm = reinterpret_cast<Small*>(smem + kOffSmall);
@@ -137,6 +137,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
+  if (kWin) {  // a windowed call's launch is a dependent one
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   // both CTAs of the pair take the whole chunk; pair g = blockIdx.x / 2 takes query rows [128 g, 128 g + 128)
   const CtaWork w = cta_work<kWin>(p, kRows, kT, 0, 1, -1, static_cast<int32_t>(blockIdx.x >> 1));
   const int ntiles = (w.sub1 - w.sub0 + kT - 1) / kT;
@@ -585,13 +589,15 @@ cudaError_t launch_partial_mh_nx(const CUtensorMap& tm_pages, const CUtensorMap&
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.window > 0 ? 2 : 1;
   if (p.window > 0)
     return bf16 ? launch_nx<true, true>(cfg, tm_pages, tm_kpe_half, p) : launch_nx<false, true>(cfg, tm_pages, tm_kpe_half, p);
   return bf16 ? launch_nx<true, false>(cfg, tm_pages, tm_kpe_half, p) : launch_nx<false, false>(cfg, tm_pages, tm_kpe_half, p);
