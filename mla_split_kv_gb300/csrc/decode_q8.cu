@@ -33,33 +33,34 @@
 // evenly over the gangs (q8_schedule.cuh), and a second kernel merges the
 // requests that gang borders cut.
 //
-// The pipeline. Three tile slots of 54 KB (two of 72 for 32 fp16 rows, whose
-// queries take 54 KB); a slot is refilled in the 32-token steps in which the
-// value product leaves it, and pages further ahead are on their way to L2. One
-// thread issues the score products, another the value products (one for both
-// spent the MMAs' time on asking whose inputs were there). The softmax warps
-// write weights as 8-byte words of their token's row (the value product reads
-// them N-major); byte stores of the K-major layout took longer than the MMAs.
-// Four warps share 8 rows and meet once a tile; only when a score passes its
-// row's reference by 2^kTau do they take maxima and rescale O. After a
-// request's last tile they split the next one's queries first, while its last
-// value product runs, then write its output.
+// The pipeline. Three tile slots of 54 to 57 KB, refilled in the 32-token steps
+// in which the value product leaves them; pages further ahead are on their way
+// to L2. A tile's weights take the place of its rope columns, which the scores
+// have read by then. One thread issues the score products, another the value
+// products (one for both spent the MMAs' time on asking whose inputs were
+// there). The softmax warps write weights as 8-byte words of their token's row
+// (the value product reads them N-major); byte stores of the K-major layout
+// took longer than the MMAs. Four warps share 8 rows and meet once a tile; only
+// when a score passes its row's reference by 2^kTau do they take maxima and
+// rescale O. After a request's last tile they split the next one's queries
+// first, while its last value product runs, then write its output.
 //
 // What bounds it, in cycles of an SM (2070 MHz) for a 96-token tile: HBM's share
 // 2570; the MMAs 1550 with nothing else on shared memory, 2300 as they run. At
-// 16 rows a tile takes 2600: HBM. At 32 rows it takes 3000 to 4000: MMAs, the
-// weights, and the tiles in which a reference moves (1800 more). A call has
+// 16 rows a tile takes 2600: HBM. At 32 rows it takes 2600, with the references
+// that move early in a request (1700 more each time) 3100 on average: a slot's
+// round of load, scores, weights and value product, three at a time. A call has
 // some 10 us around that: the lengths and the schedule 1.5 to 2 us, the first
 // tiles from HBM 3 us, the last output and the merge 5 us; a good part of it
 // is the fetch of code that is met once (ten cycles an instruction), so what
 // runs once per call or request is kept short.
 //
 // Measured (us a call, captured back to back; scaling by HBM alone in brackets):
-// 131,072 tokens, 16 fp16 heads 26.2 (11.1); 32 requests up to 16K, 16 bf16 heads
-// 49.7 (25.8); 8 requests up to 64K, 128 bf16 heads 177 (26.2; the formula's
+// 131,072 tokens, 16 fp16 heads 25.7 (11.1); 32 requests up to 16K, 16 bf16 heads
+// 45.5 (25.8); 8 requests up to 64K, 128 bf16 heads 147 (26.2; the formula's
 // products at the card's 16-bit matrix rate 44); 9 causal fp16 rows over 16 heads,
-// 4 requests up to 82K, 177 (19.9 and 38); 48 requests through a window of 4096,
-// 64 bf16 heads, 81 (17.3); 37 tokens 10.1.
+// 4 requests up to 82K, 146 (19.9 and 38); 48 requests through a window of 4096,
+// 64 bf16 heads, 68.7 (17.3); 37 tokens 10.3.
 //
 // Warp roles: softmax, rescale and output (thread = token; 8 rows a thread: 8
 // warps for 16 rows, 16 for 32), one warp each that issues the score and the
