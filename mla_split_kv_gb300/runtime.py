@@ -245,29 +245,50 @@ class WindowPlan:
     workspace: torch.Tensor
 
 
+# What a partition costs a CTA pair beside its tokens, in tokens: 5 to 8 us of start and end, at the 64-token tile's
+# 2.6 us of more than 16 rows and the 128-token tile's 1.75 of 16.
+_PART_TOKENS = 250
+
+
 def _window_partitions(runs: Sequence[int], num_heads: int, q_len: int, block_size: int, dtype: str,
                        dev: nb.mla_device_info_t) -> nb.Plan:
     """A plan of visible runs. mla_plan's own thresholds leave runs below 4096 tokens whole, as long as most windows
     are: the longest partition then sets the time (16 runs of 2048 tokens, 64 rows: 100 us whole, 35 us over all CTA
-    pairs). So plans with more and smaller partitions are laid out beside its own, none below the 128 tokens that a
-    CTA pair needs, and the one whose busiest pair has the least to read is taken."""
-    groups = -(-num_heads * q_len // 128)
+    pairs). And it fills the device with CTAs rather than with requests: batches of short runs go through large
+    clusters in several waves. So plans with more and smaller partitions, none below the 128 tokens that a CTA pair
+    needs, and with one cluster size at a time are laid out beside its own, and the one whose busiest pair is done
+    first is taken."""
+    rows = num_heads * q_len
+    groups = -(-rows // 128)
 
     def busiest_pair(plan: nb.Plan) -> int:
         pairs = plan.clusters_per_chunk * (plan.cluster_ctas // 2)
         servers = max(1, dev.max_clusters[plan.cluster_ctas.bit_length() - 1] // (groups * plan.clusters_per_chunk))
         ends = [0] * min(servers, plan.num_chunks)
         for _, t0, t1, _ in plan.chunks:  # in launch order, each to the pairs that are free first
-            heapq.heapreplace(ends, ends[0] + -(-(t1 - t0) // pairs))
+            heapq.heapreplace(ends, ends[0] + _PART_TOKENS + -(-(t1 - t0) // pairs))
         parts = max(plan.o_indptr[b + 1] - plan.o_indptr[b] for b in range(len(runs)))
         return max(ends) + 2 * parts  # the merge reads a part in about the time of two tokens
 
+    def only(size: int, clusters: int) -> nb.mla_device_info_t:
+        d = nb.mla_device_info_t()
+        d.num_sms = dev.num_sms
+        d.max_clusters[size] = min(dev.max_clusters[size], clusters)
+        return d
+
     best = nb.mla_plan(runs, num_heads, q_len, block_size, dev, dtype=dtype)
-    cost = busiest_pair(best)
-    for most, split_min in [(n, 128 * n) for n in (2, 4, 8, 16, 32, 64)] + [(8, 256), (64, 256)]:
-        plan = nb.mla_plan(runs, num_heads, q_len, block_size, dev, max_partitions=most, min_partitions=1,
+    cost = busiest_pair(best) if best.cluster_ctas > 1 else None
+    tries = [(dev, n, 128 * n) for n in (2, 4, 8, 16, 32, 64)] + [(dev, 8, 256), (dev, 64, 256)]
+    # partitions of about so many tokens, whatever their request's length
+    tries += [(only(1, max(len(runs), sum(runs) // tokens) * groups), 64, 256) for tokens in (160, 256, 384)]
+    if rows <= 16:
+        tries += [(only(size, 1 << 30), 1, 0) for size in (1, 2, 3, 4)]
+    for where, most, split_min in tries:
+        if not any(where.max_clusters):
+            continue
+        plan = nb.mla_plan(runs, num_heads, q_len, block_size, where, max_partitions=most, min_partitions=1,
                            split_min_tokens=split_min, dtype=dtype)
-        if plan.cluster_ctas > 1 and busiest_pair(plan) < cost:
+        if plan.cluster_ctas > 1 and (cost is None or busiest_pair(plan) < cost):
             best, cost = plan, busiest_pair(plan)
     return best
 
