@@ -533,6 +533,7 @@ mla_status_t decode_call(const void* q_absorbed, const void* q_pe, const void* c
     mp.B = d->num_requests;
     mp.rows = rows_total;
     mp.epc = pe.epc;
+    mp.entries = N * pe.epc;
     mp.out_dtype = out_dtype;
     mp.tables_ready = d->tables_ready;
     if (mla::launch_merge_entries(mp, static_cast<cudaStream_t>(d->stream)) != cudaSuccess) {

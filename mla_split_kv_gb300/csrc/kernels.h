@@ -78,6 +78,7 @@ struct EntryMergeParams {
   float* out_lse;              // [B, rows] or null
   int32_t B, rows, epc, out_dtype;
   int32_t tables_ready;        // o_indptr complete before the partial kernel started: read before the wait
+  int64_t entries;             // of all requests
 };
 cudaError_t launch_merge_entries(const EntryMergeParams& p, cudaStream_t stream);
 

@@ -231,3 +231,30 @@ def test_merges_of_many_rows_have_the_bits_of_few(n, out_dtype):
         one, one_lse = merge(b, b + 1)
         assert torch.equal(out[b], one[0]) and torch.equal(out_lse[b], one_lse[0])
     assert not out[1].any() and torch.isneginf(out_lse[1]).all()
+
+
+@pytest.mark.parametrize("lens,P", [([700] * 20, 3), ([90, 0, 2500, 1] * 5, 1), ([4000] * 9, 2)])
+def test_batches_of_16_rows_have_the_bits_of_their_requests(lens, P):
+    """Eight requests and more with few entries each are merged by two warps a row, fewer requests by 32: the same
+    bits. Uniform partitions, so a request's parts do not depend on its batch."""
+    case = gen.make_decode_case(81, lens, num_heads=16, block_size=32, dtype="f16")
+    dc = rt.upload(case)
+
+    def run(lo, hi):
+        B = hi - lo
+        part, lse_p = rt.alloc_partials(B * P, 1, 16)
+        ws = rt.alloc_decode_workspace(B, B * P, 1, 4, 1, 16)
+        out, lse = torch.full((B, 1, 16, 512), float("nan"), device="cuda"), torch.full((B, 1, 16), float("nan"), device="cuda")
+        d = rt.make_desc(dc, None, nb.MLA_KERNEL_TC, 4, workspace=ws)
+        d.num_requests = B
+        nb.mla_decode(dc.q_abs[lo:].data_ptr(), dc.q_pe[lo:].data_ptr(), dc.ckv.data_ptr(), dc.kpe.data_ptr(),
+                      dc.block_table[lo:].data_ptr(), dc.context_lens[lo:].data_ptr(), case.scale, P, part.data_ptr(),
+                      lse_p.data_ptr(), rt.uniform_indptr(B, P).data_ptr(), out.data_ptr(), nb.MLA_F32, lse.data_ptr(), d)
+        torch.cuda.synchronize()
+        return out, lse
+
+    out, lse = run(0, len(lens))
+    assert not torch.isnan(out).any()
+    for b in range(0, len(lens), 3):
+        one, one_lse = run(b, b + 1)
+        assert torch.equal(out[b], one[0]) and torch.equal(lse[b], one_lse[0])
