@@ -179,6 +179,18 @@ __global__ void __launch_bounds__(kRowWarps * 32) mla_merge_rows_kernel(const Me
   if (p.out_lse != nullptr && lane == 0) p.out_lse[br] = (M == -INFINITY) ? -INFINITY : M + log2f(den);
 }
 
+// sum_e w_e l_e of a row from its entries' second copies, over the warp
+__device__ __forceinline__ float second_sum(const float* ml1, long long mlstride, int e0, int e1, float M, int lane) {
+  float s = 0.f;
+  for (int e = e0 + lane; e < e1; e += 32) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(ml1 + e * mlstride));
+    s = fmaf((ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M), ml.y, s);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
 // The merge of the paired kernel's pair entries into the output (mla_decode's default on that
 // kernel). Entry e holds one CTA pair's unnormalized O (its tokens, all 512 columns: each CTA of
 // the pair wrote its 256), its row maximum m_e and its row sum l_e relative to m_e. Per (request,
@@ -282,11 +294,13 @@ __global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_kernel(
     acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
     acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
   }
+  float den_lse = den;
+  if (p.exact_lse && cb == 0 && M != -INFINITY) den_lse = second_sum(mlbase + 2 * p.rows, mlstride, e0, e1, M, lane);
   if (g != 0) return;
   float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
   if (M != -INFINITY) out = make_float4(acc.x / den, acc.y / den, acc.z / den, acc.w / den);
   store_out4(p.out, p.out_dtype, br * kRank + col, out);
-  if (p.out_lse != nullptr && cb == 0 && q == 0) p.out_lse[br] = merged_lse(M, den);
+  if (p.out_lse != nullptr && cb == 0 && q == 0) p.out_lse[br] = merged_lse(M, den_lse);
 }
 
 // The same for batches, whose requests have few entries each: two warps a (request, row), 8 columns a lane, the same
@@ -371,7 +385,10 @@ __global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_rows_ke
     if (M != -INFINITY) out = make_float4(tree(ax) / den, tree(ay) / den, tree(az) / den, tree(aw) / den);
     store_out4(p.out, p.out_dtype, br * kRank + col + 128 * k, out);
   }
-  if (p.out_lse != nullptr && col == 0) p.out_lse[br] = merged_lse(M, den);
+  if (p.out_lse != nullptr && gw % kEntryRowWarps == 0) {
+    if (p.exact_lse && M != -INFINITY) den = second_sum(mlbase + 2 * p.rows, mlstride, e0, e1, M, lane);
+    if (lane == 0) p.out_lse[br] = merged_lse(M, den);
+  }
 }
 
 }  // namespace

@@ -617,6 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tl = 32 * q4 + lane;
     const uint32_t lane_base = tmem_lane_base(q4);
     float lsum[kRH], mr[kRH];  // running row sums over this thread's tokens; reference max per row
+    // In fp16 the sum that normalizes O is that of the rounded probabilities, as O's own are (off by up to 2^-11 of a
+    // row that one token dominates). Of a windowed call's entries the second copy, which nothing else reads, keeps the
+    // exact one, for the LSE.
+    const bool exact_sum = kWin && !kBf16 && half == 1 && p.entries_only;
 #pragma unroll
     for (int k = 0; k < kRH; ++k) {
       lsum[k] = 0.f;
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             lsum[k] += hf + h2f<true>(lv);
             *reinterpret_cast<uint16_t*>(pb + kPBytes + off) = lv;
           } else {
-            lsum[k] += h2f<false>(hv);
+            lsum[k] += exact_sum ? pr : h2f<false>(hv);
           }
         }
         fence_proxy_async_smem();
