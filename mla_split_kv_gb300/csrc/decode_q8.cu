@@ -34,8 +34,7 @@
 // requests that gang borders cut.
 //
 // The pipeline. Three tile slots of 54 to 57 KB, refilled in the 32-token steps
-// in which the value product leaves them; pages further ahead are on their way
-// to L2. A tile's weights take the place of its rope columns, which the scores
+// in which the value product leaves them. A tile's weights take the place of its rope columns, which the scores
 // have read by then. One thread issues the score products, another the value
 // products (one for both spent the MMAs' time on asking whose inputs were
 // there). The softmax warps write weights as 8-byte words of their token's row
@@ -112,7 +111,6 @@ struct Cfg {
   static constexpr uint32_t kPRow = NR == 16 ? 64 : 32, kPBytes = kT * kNP;
   static constexpr uint32_t kCkvBytes = kT * kRank;
   static constexpr uint32_t kTileSlot = kCkvBytes + (kPBytes > kT * kRope ? kPBytes : kT * kRope);
-  static constexpr int kPre = kSlots;                              // tiles ahead that are prefetched to L2
   static constexpr uint32_t kQChunk = kNS * 128;                   // [kNS x 128 columns], swizzled
   static constexpr uint32_t kQBytes = kNS * kQkDim;                // four chunks, then [kNS x 64] (64-byte swizzle)
   static constexpr int kLens = NR == 32 && !BF16 ? 64 : 640;       // context lengths kept in shared memory
@@ -184,7 +182,6 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
                          const DecodeQ8Params p) {
   using C = Cfg<NR, BF16>;
   constexpr int kTerms = C::kTerms, kThreads = C::kThreads, kSoftmaxWarps = C::kSoftmaxWarps;
-  constexpr int kPre = C::kPre;
   constexpr uint32_t kCkvBytes = C::kCkvBytes, kTileSlot = C::kTileSlot;
   extern __shared__ uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need it; the size leaves no slack to align it
@@ -338,36 +335,26 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     struct Unit {
       int entry, sub, count;  // this lane's entry and first row in its page; units of the tile
     };
-    // the next tile of a walk
-    struct Tiles {
-      Q8Walk w;
-      int tile;
-      bool live;
-    };
-    auto start = [&](Tiles& t) {
-      t.w = w;
-      t.live = q8_next<kT>(p, lens, t.w, true);
-      t.tile = t.w.ta;
-    };
-    auto next_unit = [&](Tiles& t) -> Unit {
-      if (!t.live) return Unit{-1, 0, 0};
-      const Unit r{entry_of(t.w, t.tile), (t.tile * kT + tok) & (p.bs - 1), (min(kT, t.w.v.n - t.tile * kT) + unit - 1) >> unit_shift};
-      if (++t.tile == t.w.tb) {
-        t.live = q8_next<kT>(p, lens, t.w, false);
-        t.tile = t.w.ta;
+    // the walk's tiles, one after the other
+    bool live = q8_next<kT>(p, lens, w, true);
+    int tile = w.ta;
+    auto next_unit = [&]() -> Unit {
+      if (!live) return Unit{-1, 0, 0};
+      const Unit r{entry_of(w, tile), (tile * kT + tok) & (p.bs - 1), (min(kT, w.v.n - tile * kT) + unit - 1) >> unit_shift};
+      if (++tile == w.tb) {
+        live = q8_next<kT>(p, lens, w, false);
+        tile = w.ta;
       }
       return r;
     };
-    // one walk for the loads, an entry ahead of them, and one kPre tiles further on for prefetches to L2
-    Tiles loads, pres;
-    start(loads);
-    Unit cur = next_unit(loads), pre{-1, 0, 0};
+    // (an entry ahead of the loads; asking L2 for pages further on made calls 1 to 5% slower)
+    Unit cur = next_unit();
     int issued = -1;
     bool stop = false;
     for (int i = 0; i < N && !stop; ++i) {
       const int s = i % kSlots;
       // an entry outside the pool or the table row reads zeros
-      const Unit nxt = next_unit(loads);
+      const Unit nxt = next_unit();
       int pid = cur.entry;
       if (lane < cur.count && (pid < 0 || pid >= p.num_blocks)) {
         flag_error(MLA_DEVERR_BAD_PAGE);
@@ -403,19 +390,6 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       }
       issued = i;
       cur = nxt;
-      if (i + 1 >= kSlots) {  // (the first loads go out before anything else)
-        if (i + 1 == kSlots) start(pres);
-        // tiles up to i + kPre; the first time all of them, one an iteration from then on
-#pragma unroll 1
-        for (int j = i + 1 == kSlots ? -kSlots - 1 : kPre - 1; j < kPre; ++j) {
-          if (j >= 0 && lane < pre.count && pre.entry >= 0 && pre.entry < p.num_blocks) {
-            const long long at = (static_cast<long long>(pre.entry) << p.bs_shift) + pre.sub;
-            bulk_prefetch_l2(p.ckv + at * kRank, static_cast<uint32_t>(unit * kRank));
-            bulk_prefetch_l2(p.kpe + at * kRope, static_cast<uint32_t>(unit * kRope));
-          }
-          pre = next_unit(pres);
-        }
-      }
     }
     // after an abort, loads in flight land before shared memory is released
     if (lane == 0 && *abort_flag)
