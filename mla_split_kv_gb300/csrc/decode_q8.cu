@@ -33,8 +33,7 @@
 // evenly over the gangs (q8_schedule.cuh), and a second kernel merges the
 // requests that gang borders cut.
 //
-// The pipeline. Three tile slots of 54 to 57 KB, refilled in the 32-token steps
-// in which the value product leaves them. A tile's weights take the place of its rope columns, which the scores
+// The pipeline. Three tile slots of 54 to 57 KB. A tile's weights take the place of its rope columns, which the scores
 // have read by then. One thread issues the score products, another the value
 // products (one for both spent the MMAs' time on asking whose inputs were
 // there). The softmax warps write weights as 8-byte words of their token's row
@@ -81,7 +80,7 @@ constexpr float kTermStep = 32.0f, kTermInv = 1.0f / 32.0f;
 
 template <int kLens>
 struct Small {
-  uint64_t full[kSlots], empty[kSlots][kSteps];  // tile slots, freed step by step
+  uint64_t full[kSlots], empty[kSlots];  // tile slots
   uint64_t sfull[2], sfree[2];           // score buffers
   uint64_t pfull[kSlots];                // weights per slot
   uint64_t qfull, ofree, drain[2];
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sm->full[s], 1);
-      for (int k = 0; k < kSteps; ++k) mbar_init(&sm->empty[s][k], 1);
+      mbar_init(&sm->empty[s], 1);
       mbar_init(&sm->pfull[s], kSoftmaxWarps);
     }
     for (int s = 0; s < 2; ++s) {
@@ -321,9 +320,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
   if (warp == C::kLoadWarp) {
     // ------------------------------------------------------------------ page loads
     const uint64_t pol = l2_policy_evict_first();
-    // One lane a unit of a tile: a page, or half of one of 64 tokens, so that a unit lies within a step.
+    // One lane a unit of a tile: a page, or half of one of 64 tokens, so that units fill a tile.
     const int unit_shift = min(p.bs_shift, 5), unit = 1 << unit_shift;
-    const int my_step = lane >> (5 - unit_shift);  // 32-token step of this lane's unit
     const int tok = lane << unit_shift;            // its first token in the tile
     // the table's entry for this lane's unit (looked at when it is used: its load has a tile's time)
     auto entry_of = [&](const Q8Walk& w, int tile) -> int {
@@ -363,30 +361,17 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       uint8_t* const slot = smem + s * kTileSlot;
       const int row = (pid << p.bs_shift) + (pid < 0 ? 0 : cur.sub);
       const bool mine = lane < cur.count;
-      auto load_ckv = [&]() { tma_load_4d(slot + tok * kRank, &tm_ckv, 0, 0, 0, row >> 3, &sm->full[s], pol); };
-      auto load_kpe = [&]() { tma_load_2d(slot + kCkvBytes + tok * kRope, &tm_kpe, 0, row, &sm->full[s], pol); };
-      auto expect = [&]() {
-        if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>((cur.count << unit_shift) * kQkDim));
-        __syncwarp();
-      };
-      const uint32_t parity = (i / kSlots - 1) & 1;
-      if (i < kSlots || __all_sync(0xffffffffu, mbar_test(&sm->empty[s][kSteps - 1], parity))) {  // the whole slot is free
-        expect();
-        if (mine) {
-          load_ckv();
-          load_kpe();
-        }
-      } else {
-        // As the value product of tile i - kSlots has read its steps; the rope columns, where the weights are now,
-        // behind the last one. (Given up, the loads are issued all the same, so that the barrier completes.)
-#pragma unroll 1
-        for (int k = 0; k < kSteps; ++k) {
-          if (!stop) stop = !__all_sync(0xffffffffu, mbar_wait(&sm->empty[s][k], parity, tmo) && !*abort_flag);
-          if (k == 0) expect();
-          if (mine && my_step == k) load_ckv();
-        }
-        if (mine) load_kpe();
-        if (stop) *abort_flag = 1;
+      // Once the value product of tile i - kSlots has left the slot. (Given up, the loads are issued all the same, so
+      // that the barrier completes.)
+      if (i >= kSlots && !__all_sync(0xffffffffu, mbar_wait(&sm->empty[s], (i / kSlots - 1) & 1, tmo) && !*abort_flag)) {
+        stop = true;
+        *abort_flag = 1;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>((cur.count << unit_shift) * kQkDim));
+      __syncwarp();
+      if (mine) {
+        tma_load_4d(slot + tok * kRank, &tm_ckv, 0, 0, 0, row >> 3, &sm->full[s], pol);
+        tma_load_2d(slot + kCkvBytes + tok * kRope, &tm_kpe, 0, row, &sm->full[s], pol);
       }
       issued = i;
       cur = nxt;
@@ -464,8 +449,8 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
                 umma8_ss(tmem + C::kTmemO + blk * C::kNP, a0, (blk * 1024 + ks * 4 * kGroupBytes) >> 4, pb, (ks * kStep * C::kPRow) >> 4, idesc,
                          (tile == w.ta && ks == 0) ? 0u : 1u);
             }
-            umma_commit(&sm->empty[i % kSlots][ks]);
           }
+          umma_commit(&sm->empty[i % kSlots]);
         }
       }
       if (!ok) *abort_flag = 1;
@@ -496,9 +481,9 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       const int row = (pid << p.bs_shift) + ((tile * kT + tl) & (p.bs - 1));  // (a pool has fewer than 2^31 tokens)
       return __ldg(p.scales + (row >> p.g_shift));
     };
-    // The value product of tile t: its last step has left the slot. (The phase before on that barrier, tile t - kSlots,
+    // The value product of tile t: it has left the slot. (The phase before on that barrier, tile t - kSlots,
     // was complete before tile t was loaded, so its parity cannot be taken for this one's.)
-    auto product_done = [&](int t) -> bool { return mbar_wait(&sm->empty[t % kSlots][kSteps - 1], (t / kSlots) & 1, tmo); };
+    auto product_done = [&](int t) -> bool { return mbar_wait(&sm->empty[t % kSlots], (t / kSlots) & 1, tmo); };
     int i = 0;  // tile count
     // Each round: a request's tiles, the split of the next one's queries (while the last value product runs), then
     // the request's output. The first round only splits.
