@@ -73,7 +73,7 @@ namespace {
 
 constexpr int kGroupBytes = 8 * kRank;            // 4 KB: 8 tokens, four swizzled [8 x 128] atoms
 constexpr int kT = 96;                            // tokens per tile
-constexpr int kStep = 32, kSteps = kT / kStep;    // tokens of an MMA step of the value product
+constexpr int kStep = 32;                         // tokens of an MMA step of the value product
 constexpr int kSlots = 3;
 constexpr int RH = 8;                             // rows per softmax thread
 constexpr float kTermStep = 32.0f, kTermInv = 1.0f / 32.0f;
@@ -442,13 +442,11 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
           const Desc2 a0 = desc2(smem_desc_sw128(slot, 1024, kGroupBytes));
           const int ksteps = (min(kT, w.v.n - tile * kT) + kStep - 1) / kStep;
 #pragma unroll 1
-          for (int ks = 0; ks < kSteps; ++ks) {
-            if (ks < ksteps) {
+          for (int ks = 0; ks < ksteps; ++ks) {
 #pragma unroll
-              for (int blk = 0; blk < 4; ++blk)
-                umma8_ss(tmem + C::kTmemO + blk * C::kNP, a0, (blk * 1024 + ks * 4 * kGroupBytes) >> 4, pb, (ks * kStep * C::kPRow) >> 4, idesc,
-                         (tile == w.ta && ks == 0) ? 0u : 1u);
-            }
+            for (int blk = 0; blk < 4; ++blk)
+              umma8_ss(tmem + C::kTmemO + blk * C::kNP, a0, (blk * 1024 + ks * 4 * kGroupBytes) >> 4, pb, (ks * kStep * C::kPRow) >> 4, idesc,
+                       (tile == w.ta && ks == 0) ? 0u : 1u);
           }
           umma_commit(&sm->empty[i % kSlots]);
         }

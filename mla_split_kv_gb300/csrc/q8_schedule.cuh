@@ -4,7 +4,7 @@
 // The batch's visible runs, cut into tiles request after request,
 // are one line, with a gap of a few cells between requests: what a gang spends on
 // going from one request to the next (its output, the next one's queries, the
-// first tiles' rescales: 8 us at 32 rows, 5 at 16, four to five tiles) counts as
+// first tiles' rescales: 8 us at 32 rows, 5 at 16, five to seven tiles) counts as
 // tiles. Gang j of J takes L / J cells of the line's L, the first L % J gangs one
 // more (one CTA of a gang per row group), so every gang works as long as the
 // others whatever the lengths (without the gaps, gangs with one request ended
@@ -36,7 +36,7 @@ struct Q8Lens {
 // A pair of counts in one sum: tiles (at most 65535 * 2^25 < 2^44) and the requests that have any.
 constexpr int kQ8CountShift = 44;
 constexpr int64_t kQ8Tiles = (int64_t{1} << kQ8CountShift) - 1;
-constexpr int kQ8Gap = 5;
+constexpr int kQ8Gap = 6;
 
 // The line among the gangs that get any of it (all of them unless there are fewer tiles).
 struct Q8Line {
