@@ -46,7 +46,7 @@
 // What bounds it, in cycles of an SM (2070 MHz) for a 96-token tile: HBM's share
 // 2570; the MMAs 1550 with nothing else on shared memory, 2300 as they run. At
 // 16 rows a tile takes 2600: HBM. At 32 rows it takes 2600, with the references
-// that move early in a request (1700 more each time) 3100 on average: a slot's
+// that move early in a request (1700 more each time) 2900 on average: a slot's
 // round of load, scores, weights and value product, three at a time. A call has
 // some 10 us around that: the lengths and the schedule 1.5 to 2 us, the first
 // tiles from HBM 3 us, the last output and the merge 5 us; a good part of it
@@ -54,11 +54,11 @@
 // runs once per call or request is kept short.
 //
 // Measured (us a call, captured back to back; scaling by HBM alone in brackets):
-// 131,072 tokens, 16 fp16 heads 25.7 (11.1); 32 requests up to 16K, 16 bf16 heads
-// 45.5 (25.8); 8 requests up to 64K, 128 bf16 heads 147 (26.2; the formula's
+// 131,072 tokens, 16 fp16 heads 25.5 (11.1); 32 requests up to 16K, 16 bf16 heads
+// 42.5 (25.8); 8 requests up to 64K, 128 bf16 heads 139 (26.2; the formula's
 // products at the card's 16-bit matrix rate 44); 9 causal fp16 rows over 16 heads,
-// 4 requests up to 82K, 146 (19.9 and 38); 48 requests through a window of 4096,
-// 64 bf16 heads, 68.7 (17.3); 37 tokens 10.3.
+// 4 requests up to 82K, 141 (19.9 and 38); 48 requests through a window of 4096,
+// 64 bf16 heads, 66.3 (17.3); 37 tokens 10.3.
 //
 // Warp roles: softmax, rescale and output (thread = token; 8 rows a thread: 8
 // warps for 16 rows, 16 for 32), one warp each that issues the score and the
