@@ -325,8 +325,9 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     const int tok = lane << unit_shift;            // its first token in the tile
     // the table's entry for this lane's unit (looked at when it is used: its load has a tile's time)
     auto entry_of = [&](const Q8Walk& w, int tile) -> int {
-      const int u = tile * kT + tok;
-      if (tok >= kT || u >= w.v.n) return -1;
+      const uint32_t at = tile * kT + tok;  // (past 2^31 at the end of the longest context)
+      if (tok >= kT || at >= static_cast<uint32_t>(w.v.n)) return -1;
+      const int u = static_cast<int>(at);
       const int pg = (u >> p.bs_shift) + (u >= w.v.sa ? w.v.skip >> p.bs_shift : 0);
       return pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
     };
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       const int low_last = p.window > 0 ? max(-1, pos_last - p.window) : -1;
       // tiles of which every row sees every token (rows past the last, zeros, may see what they like: nothing of
       // theirs is written)
-      const int plain_lo = (low_last + kT) / kT, plain_hi = max(0, pos_first + 1) / kT;
+      const int plain_lo = low_last < 0 ? 0 : low_last / kT + 1, plain_hi = max(0, pos_first + 1) / kT;
       for (int tile = w.ta; tile < w.tb; ++tile, ++i) {
         // NaN for a scale that is neither NaN nor in range
         const float z = (z_raw >= 0x1p-60f && z_raw <= 0x1p60f) ? z_raw : __uint_as_float(0x7fc00000u);

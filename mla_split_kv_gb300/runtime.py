@@ -443,6 +443,9 @@ class Q8Plan:
 
 def plan_q8(num_requests: int, num_heads: int, q_len: int = 1, causal: bool = False, window: int = 0, sinks: int = 0,
             device="cuda") -> Q8Plan:
+    """The options and the workspace of decode_q8 calls of one shape: the first `num_requests` lengths and table rows
+    count, each request's q_len rows see its tokens up to their own (causal) or all of them, and with window >= 1 only
+    the last `window` of those and the request's first `sinks`. Lengths are not part of it."""
     index = torch.device(device).index
     n = nb.mla_decode_q8_workspace_bytes(nb.mla_device_query(-1 if index is None else index), q_len, num_heads)
     if n == 0:
