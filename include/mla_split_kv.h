@@ -669,6 +669,12 @@ typedef struct {
  * same lengths. Pages: as for mla_decode_partial (one outside the pool or the
  * table row reads zeros and raises MLA_ERR_DEVICE_CHECK).
  *
+ * Precision: scores, maxima, sums and out_lse are fp32. The softmax weights
+ * of the value product are kept to 2^-16 of themselves with at most 16 rows
+ * (q_len * H), to 2^-14 + 2^-16 with more, and in both to 2^-26 of the row's
+ * greatest weight so far; the sum that normalizes takes them unrounded. An
+ * fp32 `out` shows these roundings, a 16-bit one its own beside them.
+ *
  * out     : device [B, q_len, H, 512] of desc->out_dtype, 16-byte aligned
  * out_lse : device [B, q_len, H] fp32, or NULL
  * Other arguments: as for mla_decode_partial and mla_cache_append_q8. With
