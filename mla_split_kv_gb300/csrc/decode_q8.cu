@@ -219,7 +219,9 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // this gang's place on the line of tiles
+  // Data of the call: what the kernel before may have written until the wait above returned (scales by the cache's
+  // write, tables and lengths on the device) is read past L1, whose lines may be older than that.
+  // This gang's place on the line of tiles
   const Q8Lens<C::kLens> lens{p.context_lens, sm->lens};
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       if (tok >= kT || at >= static_cast<uint32_t>(w.v.n)) return -1;
       const int u = static_cast<int>(at);
       const int pg = (u >> p.bs_shift) + (u >= w.v.sa ? w.v.skip >> p.bs_shift : 0);
-      return pg < p.max_blocks ? __ldg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
+      return pg < p.max_blocks ? __ldcg(p.block_table + static_cast<long long>(w.b) * p.max_blocks + pg) : -1;
     };
     struct Unit {
       int entry, sub, count;  // this lane's entry and first row in its page; units of the tile
@@ -470,12 +472,12 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       if (!has_tokens || at >= static_cast<uint32_t>(w.v.n)) return -1;
       const int u = static_cast<int>(at);
       const int pg = (u >> p.bs_shift) + (u >= w.v.sa ? w.v.skip >> p.bs_shift : 0);
-      return pg < p.max_blocks ? __ldg(p.block_table + (static_cast<long long>(w.b) * p.max_blocks + pg)) : -1;
+      return pg < p.max_blocks ? __ldcg(p.block_table + (static_cast<long long>(w.b) * p.max_blocks + pg)) : -1;
     };
     auto scale_at = [&](int pid, int tile) -> float {  // 1 where there is no page
       if (pid < 0 || pid >= p.num_blocks) return 1.f;
       const int row = (pid << p.bs_shift) + ((tile * kT + tl) & (p.bs - 1));  // (a pool has fewer than 2^31 tokens)
-      return __ldg(p.scales + (row >> p.g_shift));
+      return __ldcg(p.scales + (row >> p.g_shift));
     };
     // The value product of tile t: it has left the slot. (The phase before on that barrier, tile t - kSlots,
     // was complete before tile t was loaded, so its parity cannot be taken for this one's.)
