@@ -534,6 +534,7 @@ mla_status_t decode_call(const void* q_absorbed, const void* q_pe, const void* c
     mp.rows = rows_total;
     mp.epc = pe.epc;
     mp.entries = N * pe.epc;
+    mp.uniform = d->chunks == nullptr ? 1 : 0;  // (with a table the counts are in o_indptr, on the device)
     mp.exact_lse = win.window > 0 && d->dtype != MLA_BF16 ? 1 : 0;
     mp.out_dtype = out_dtype;
     mp.tables_ready = d->tables_ready;

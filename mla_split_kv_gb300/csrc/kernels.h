@@ -79,6 +79,7 @@ struct EntryMergeParams {
   int32_t B, rows, epc, out_dtype;
   int32_t tables_ready;        // o_indptr complete before the partial kernel started: read before the wait
   int64_t entries;             // of all requests
+  int32_t uniform;             // as many in each
   int32_t exact_lse;           // the entries' second copies hold sums of their own, for the LSE
 };
 cudaError_t launch_merge_entries(const EntryMergeParams& p, cudaStream_t stream);

@@ -211,27 +211,9 @@ constexpr int kEntryGroups = 8;                  // entry groups per warp
 constexpr int kEntriesPerLane = 12;              // per round of loads
 constexpr int kEntryRound = kEntryGroups * kEntriesPerLane;
 
-__global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_kernel(const EntryMergeParams p) {
-  pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long gw = static_cast<long long>(blockIdx.x) * kEntryWarps + warp;
-  const bool active = gw < static_cast<long long>(p.B) * p.rows * 32;
-  const int cb = static_cast<int>(gw & 31);  // columns [16 cb, 16 cb + 16)
-  const long long br = gw >> 5;              // b * rows + row
-  const int b = static_cast<int>(br / p.rows), row = static_cast<int>(br % p.rows);
-  // the offsets are an input of the call, not data of the partial kernel: with tables_ready (complete
-  // before that kernel started) they are read before the wait, so the entries' loads follow it at once
-  int e0 = 0, e1 = 0;
-  if (active && p.tables_ready) {
-    e0 = __ldg(p.o_indptr + b) * p.epc;
-    e1 = __ldg(p.o_indptr + b + 1) * p.epc;
-  }
-  pdl_wait();  // the entries are complete once the partial kernel has
-  if (!active) return;
-  if (!p.tables_ready) {
-    e0 = p.o_indptr[b] * p.epc;
-    e1 = p.o_indptr[b + 1] * p.epc;
-  }
+// One warp's 16 columns of a (request, row): the request's entries [e0, e1).
+__device__ __forceinline__ void merge_entry_columns(const EntryMergeParams& p, long long br, int row, int cb, int e0, int e1,
+                                                    int lane) {
   const int g = lane >> 2, q = lane & 3;
   const int col = 16 * cb + 4 * q;
   const long long ostride = static_cast<long long>(p.rows) * kRank;  // one entry's O
@@ -303,20 +285,79 @@ __global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_kernel(
   if (p.out_lse != nullptr && cb == 0 && q == 0) p.out_lse[br] = merged_lse(M, den_lse);
 }
 
+__global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_kernel(const EntryMergeParams p) {
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long gw = static_cast<long long>(blockIdx.x) * kEntryWarps + warp;
+  const bool active = gw < static_cast<long long>(p.B) * p.rows * 32;
+  const int cb = static_cast<int>(gw & 31);  // columns [16 cb, 16 cb + 16)
+  const long long br = gw >> 5;              // b * rows + row
+  const int b = static_cast<int>(br / p.rows), row = static_cast<int>(br % p.rows);
+  // the offsets are an input of the call, not data of the partial kernel: with tables_ready (complete
+  // before that kernel started) they are read before the wait, so the entries' loads follow it at once
+  int e0 = 0, e1 = 0;
+  if (active && p.tables_ready) {
+    e0 = __ldg(p.o_indptr + b) * p.epc;
+    e1 = __ldg(p.o_indptr + b + 1) * p.epc;
+  }
+  pdl_wait();  // the entries are complete once the partial kernel has
+  if (!active) return;
+  if (!p.tables_ready) {
+    e0 = p.o_indptr[b] * p.epc;
+    e1 = p.o_indptr[b + 1] * p.epc;
+  }
+  merge_entry_columns(p, br, row, cb, e0, e1, lane);
+}
+
 // The same for batches, whose requests have few entries each: two warps a (request, row), 8 columns a lane, the same
-// operations in the same order (entry groups g, g + 8, ... summed in entry order, then added in the shuffles' order).
+// operations in the same order (entry groups g, g + 8 summed in entry order, then added in the shuffles' order).
 // A warp of the kernel above looks after 12 entries a lane whether they are there or not; 32 of them a row, a thousand
 // rows are 13 waves of blocks.
 constexpr int kEntryRowWarps = 2, kEntryRowLoads = 4 / kEntryRowWarps;
 // Measured as whole calls of 16 rows, against the kernel above: 4 requests with 8 / 18 entries each 11.5 / 17.3 us
 // against 12.0 / 14.5, 8 with 4 / 9 entries 11.8 / 16.2 against 14.2 / 17.1, 32 with 2 entries 12.9 against 26.0,
-// 64 with one 13.2 against 41.5.
-constexpr long long kMinEntryRows = 128, kMaxRowEntries = 12;
+// 64 with one 13.2 against 41.5. So a request of more than 12 entries is merged as above, request by request (the host
+// knows no request's count, only their sum): the grid's last blocks look such requests up in the offsets and share
+// their (row, 16 columns) out (one of 131,072 tokens, 40 entries, beside seven of 2000: 62.6 us, 67.1 by rows; eight
+// requests with 9 entries each, where the last blocks find nothing, 14.4 against 14.1 without them).
+constexpr long long kMinEntryRows = 128;
+constexpr int kMaxRowEntries = 12, kLongBlocks = 256;
 
-__global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_rows_kernel(const EntryMergeParams p) {
+__global__ void __launch_bounds__(kEntryWarps * 32, 4)
+    mla_merge_entries_rows_kernel(const EntryMergeParams p, uint32_t row_blocks) {
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long gw = static_cast<long long>(blockIdx.x) * kEntryWarps + (threadIdx.x >> 5);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x >= row_blocks) {  // long requests
+    __shared__ int found[kEntryWarps * 32];
+    __shared__ uint32_t masks[kEntryWarps];
+    pdl_wait();
+    for (int base = 0; base < p.B; base += kEntryWarps * 32) {
+      const int b = base + tid;
+      const bool is_long = b < p.B && (__ldcg(p.o_indptr + b + 1) - __ldcg(p.o_indptr + b)) * p.epc > kMaxRowEntries;
+      const uint32_t mask = __ballot_sync(0xffffffffu, is_long);
+      if (lane == 0) masks[warp] = mask;
+      __syncthreads();
+      int at = __popc(mask & ((1u << lane) - 1)), count = 0;  // in request order: the same list in every block
+#pragma unroll
+      for (int w = 0; w < kEntryWarps; ++w) {
+        const int n = __popc(masks[w]);
+        at += w < warp ? n : 0;
+        count += n;
+      }
+      if (is_long) found[at] = b;
+      __syncthreads();
+      const long long units = static_cast<long long>(count) * p.rows * 32;
+      const long long step = static_cast<long long>(gridDim.x - row_blocks) * kEntryWarps;
+      for (long long u = static_cast<long long>(blockIdx.x - row_blocks) * kEntryWarps + warp; u < units; u += step) {
+        const int which = found[u / (p.rows * 32)], row = static_cast<int>(u / 32 % p.rows);
+        merge_entry_columns(p, static_cast<long long>(which) * p.rows + row, row, static_cast<int>(u % 32),
+                            __ldcg(p.o_indptr + which) * p.epc, __ldcg(p.o_indptr + which + 1) * p.epc, lane);
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  const long long gw = static_cast<long long>(blockIdx.x) * kEntryWarps + warp;
   const long long br = gw / kEntryRowWarps;  // b * rows + row
   const bool active = br < static_cast<long long>(p.B) * p.rows;
   const int b = static_cast<int>(br / p.rows), row = static_cast<int>(br % p.rows);
@@ -331,14 +372,12 @@ __global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_rows_ke
     e0 = p.o_indptr[b] * p.epc;
     e1 = p.o_indptr[b + 1] * p.epc;
   }
+  if (e1 - e0 > kMaxRowEntries) return;  // a long request
   const int col = static_cast<int>(gw % kEntryRowWarps) * (kRank / kEntryRowWarps) + 4 * lane;
   const long long ostride = static_cast<long long>(p.rows) * kRank;  // one entry's O
   const float* const obase = p.ws_partials + static_cast<long long>(row) * kRank + col;
   const float* const mlbase = p.ws_lse + static_cast<long long>(row) * 2;  // copy 0 of the entry's m, l
   const long long mlstride = 4LL * p.rows;                                  // one entry's two copies
-  auto max_sum = [&](int e) -> float2 {
-    return e < e1 ? __ldcg(reinterpret_cast<const float2*>(mlbase + e * mlstride)) : make_float2(-INFINITY, 0.f);
-  };
   // the first entries' values (they do not depend on the weights)
   float4 v[kEntryGroups];
   auto load = [&](int base, int k) {
@@ -348,10 +387,12 @@ __global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_rows_ke
                            : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   load(e0, 0);
-  float M = -INFINITY;
-  for (int base = e0; base < e1; base += 32) M = fmaxf(M, max_sum(base + lane).x);
+  // lane x weighs entry e0 + x
+  const float2 ml = e0 + lane < e1 ? __ldcg(reinterpret_cast<const float2*>(mlbase + (e0 + lane) * mlstride)) : make_float2(-INFINITY, 0.f);
+  float M = ml.x;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float w = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
   auto tree = [](const float* a) -> float { return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7])); };
   float den = 0.f;
 #pragma unroll 1
@@ -360,18 +401,12 @@ __global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_rows_ke
 #pragma unroll
     for (int g = 0; g < kEntryGroups; ++g) d[g] = ax[g] = ay[g] = az[g] = aw[g] = 0.f;
     if (M != -INFINITY) {
-      float w = 0.f, l = 0.f;
 #pragma unroll 1
       for (int base = e0; base < e1; base += kEntryGroups) {
-        if ((base - e0) % 32 == 0) {  // lane x weighs entry base + x
-          const float2 ml = max_sum(base + lane);
-          w = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
-          l = ml.y;
-        }
         if (base != e0 || k != 0) load(base, k);
 #pragma unroll
         for (int g = 0; g < kEntryGroups; ++g) {
-          const float we = __shfl_sync(0xffffffffu, w, (base - e0 + g) & 31), le = __shfl_sync(0xffffffffu, l, (base - e0 + g) & 31);
+          const float we = __shfl_sync(0xffffffffu, w, base - e0 + g), le = __shfl_sync(0xffffffffu, ml.y, base - e0 + g);
           d[g] = fmaf(we, le, d[g]);
           ax[g] = fmaf(we, v[g].x, ax[g]);
           ay[g] = fmaf(we, v[g].y, ay[g]);
@@ -395,10 +430,16 @@ __global__ void __launch_bounds__(kEntryWarps * 32, 4) mla_merge_entries_rows_ke
 
 cudaError_t launch_merge_entries(const EntryMergeParams& p, cudaStream_t stream) {
   const long long rows = static_cast<long long>(p.B) * p.rows;
-  const bool by_row = rows >= kMinEntryRows && p.entries <= kMaxRowEntries * p.B;
+  // by rows where most requests are short (all of them, or all but a few: the sum of the counts is at most 12 a request)
+  const bool by_row = rows >= kMinEntryRows && p.entries <= static_cast<long long>(kMaxRowEntries) * p.B;
   const long long warps = rows * (by_row ? kEntryRowWarps : 32);
-  const long long blocks = (warps + kEntryWarps - 1) / kEntryWarps;
+  long long blocks = (warps + kEntryWarps - 1) / kEntryWarps;
   if (blocks <= 0) return cudaSuccess;
+  const uint32_t row_blocks = static_cast<uint32_t>(blocks);
+  if (by_row && !p.uniform) {  // as many blocks as the long requests that there may be can use
+    const long long most = p.entries / (kMaxRowEntries + 1) * p.rows * (32 / kEntryWarps);
+    blocks += most < kLongBlocks ? most : kLongBlocks;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(kEntryWarps * 32, 1, 1);
@@ -409,7 +450,8 @@ cudaError_t launch_merge_entries(const EntryMergeParams& p, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, by_row ? mla_merge_entries_rows_kernel : mla_merge_entries_kernel, p);
+  return by_row ? cudaLaunchKernelEx(&cfg, mla_merge_entries_rows_kernel, p, row_blocks)
+                : cudaLaunchKernelEx(&cfg, mla_merge_entries_kernel, p);
 }
 
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
