@@ -106,48 +106,62 @@ __global__ void __launch_bounds__(kWarps * 32) mla_merge_kernel(const MergeParam
     p.out_lse[br] = (M == -INFINITY) ? -INFINITY : M + log2f(den);
 }
 
-// The same merge, the same operations in the same order, with one warp per (request, row): a lane owns 4 columns of
-// each quarter, so the weights' code runs once a row instead of four times. For batches with rows to fill the device
-// with warps either way; with fewer, a row's four warps are four chains of loads side by side. Measured with 2 / 9
-// partials a row, a row's warp against four: 512 rows 2.4 / 3.6 us against 2.4 / 3.2, 1024 rows 2.6 / 4.0 against
-// 3.9 / 5.3 alone but 1 us more behind a partial kernel (fewer of its larger blocks are resident early), 2048 rows
-// 3.6 / 5.9 against 6.3 / 8.3, 4096 rows 4.7 / 9.5 against 10.9 / 15.8.
-constexpr int kRowWarps = 4, kRowAhead = 2;
-constexpr long long kMinRows = 2048;
+// The same merge, the same operations in the same order, for batches with rows to fill the device with fewer warps a
+// (request, row): one, or two, a lane owning 4 columns of each of its warp's quarters, so the weights' code runs once
+// (twice) a row instead of four times. A request of many partials goes through rounds of loads one behind the other
+// whatever its batch, so from 2048 rows on, where one such request sets the time, two warps with eight partials in
+// flight take a row, from 4096 on one warp with two. Measured, one warp / two / four: 2048 rows with 2 partials a row
+// 3.6 / 4.1 / 6.3 us, with 9 6.1 / 5.7 / 8.3, with 40 29 / 27.5 / 31, with 60 (76) in one request of 16 and 1 (2) in the
+// others 11.3 (14.1) / 6.8 (8.2) / 7.4 (8.3); 4096 rows with 60 in one request of 32 11.4 / 7.8 / 12.0, with 16 a row
+// 25.8 / 21.9 / 24.8, with 2 behind a partial kernel 1 us less with one than with two. Below 2048 rows four warps are
+// four chains of loads side by side: 1024 rows with 2 / 9 partials 2.6 / 4.0 us with one against 3.9 / 5.3, but 1 us
+// more behind a partial kernel (fewer of its larger blocks are resident early); 512 rows 2.4 / 3.6 against 2.4 / 3.2.
+constexpr long long kMinRows = 2048, kMinRowsOneWarp = 4096;
+template <int kRowWarps>  // warps a row
+struct RowMerge {
+  static constexpr int kQuarters = 4 / kRowWarps, kAhead = kRowWarps == 1 ? 2 : 8;
+  static constexpr int kBlockRows = kRowWarps == 1 ? 4 : 1, kThreads = kBlockRows * kRowWarps * 32;
+  static constexpr int kMinBlocks = kRowWarps == 1 ? 6 : 10;  // registers for six blocks of 128 threads, ten of 64: no spills
+};
 
-__global__ void __launch_bounds__(kRowWarps * 32) mla_merge_rows_kernel(const MergeParams p) {
+template <int kRowWarps>
+__global__ void __launch_bounds__((RowMerge<kRowWarps>::kThreads), (RowMerge<kRowWarps>::kMinBlocks))
+    mla_merge_rows_kernel(const MergeParams p) {
+  using C = RowMerge<kRowWarps>;
+  constexpr int kQuarters = C::kQuarters, kAhead = C::kAhead;
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long br = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);  // b * rows + row
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long br = static_cast<long long>(blockIdx.x) * C::kBlockRows + warp / kRowWarps;  // b * rows + row
   if (br >= static_cast<long long>(p.B) * p.rows) return;
   const int b = static_cast<int>(br / p.rows), row = static_cast<int>(br % p.rows);
   const int lo = p.o_indptr[b], n = p.o_indptr[b + 1] - lo;
-  const float* const col = p.partials + static_cast<long long>(row) * kRank + lane * 4;
+  const int first_col = warp % kRowWarps * (kQuarters * 128) + lane * 4;
+  const float* const col = p.partials + static_cast<long long>(row) * kRank + first_col;
   const long long stride = static_cast<long long>(p.rows) * kRank;  // one partial slot
-  auto load = [&](float4 (&v)[kRowAhead][4], int j0, int cnt) {
+  auto load = [&](float4 (&v)[kAhead][kQuarters], int j0, int cnt) {
 #pragma unroll
-    for (int jj = 0; jj < kRowAhead; ++jj)
+    for (int jj = 0; jj < kAhead; ++jj)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < kQuarters; ++q)
         v[jj][q] = (j0 + jj < cnt) ? *reinterpret_cast<const float4*>(col + (lo + j0 + jj) * stride + q * 128)
                                    : make_float4(0.f, 0.f, 0.f, 0.f);
   };
-  float4 v[kRowAhead][4];
+  float4 v[kAhead][kQuarters];
   load(v, 0, n);  // (they do not depend on the weights)
   const float l0 = (lane < n) ? p.lse[static_cast<long long>(lo + lane) * p.rows + row] : -INFINITY;
   float M = l0;
   for (int s = lane + 32; s < n; s += 32) M = fmaxf(M, p.lse[static_cast<long long>(lo + s) * p.rows + row]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float4 acc[4];
+  float4 acc[kQuarters];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = 0; q < kQuarters; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
   if (M != -INFINITY) {
     float wl = 0.f;
 #pragma unroll 1
-    for (int j0 = 0; j0 < n; j0 += kRowAhead) {
+    for (int j0 = 0; j0 < n; j0 += kAhead) {
       if (j0 % 32 == 0) {  // lane s holds the weight of partial j0 + s
         wl = 0.f;
         if (j0 + lane < n) {
@@ -156,12 +170,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) mla_merge_rows_kernel(const Me
         }
       }
 #pragma unroll
-      for (int jj = 0; jj < kRowAhead; ++jj) {
+      for (int jj = 0; jj < kAhead; ++jj) {
+        if (jj > 0 && jj % 2 == 0 && j0 + jj >= n) break;
         const float wj = __shfl_sync(0xffffffffu, wl, (j0 + jj) & 31);
         if (j0 + jj < n) {
           den += wj;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < kQuarters; ++q) {
             acc[q].x = fmaf(wj, v[jj][q].x, acc[q].x);
             acc[q].y = fmaf(wj, v[jj][q].y, acc[q].y);
             acc[q].z = fmaf(wj, v[jj][q].z, acc[q].z);
@@ -169,14 +184,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) mla_merge_rows_kernel(const Me
           }
         }
       }
-      if (j0 + kRowAhead < n) load(v, j0 + kRowAhead, n);
+      if (j0 + kAhead < n) load(v, j0 + kAhead, n);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[q] = make_float4(acc[q].x / den, acc[q].y / den, acc[q].z / den, acc[q].w / den);
+    for (int q = 0; q < kQuarters; ++q) acc[q] = make_float4(acc[q].x / den, acc[q].y / den, acc[q].z / den, acc[q].w / den);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) store_out4(p.out, p.out_dtype, br * kRank + q * 128 + lane * 4, acc[q]);
-  if (p.out_lse != nullptr && lane == 0) p.out_lse[br] = (M == -INFINITY) ? -INFINITY : M + log2f(den);
+  for (int q = 0; q < kQuarters; ++q) store_out4(p.out, p.out_dtype, br * kRank + first_col + q * 128, acc[q]);
+  if (p.out_lse != nullptr && lane == 0 && warp % kRowWarps == 0) p.out_lse[br] = (M == -INFINITY) ? -INFINITY : M + log2f(den);
 }
 
 // sum_e w_e l_e of a row from its entries' second copies, over the warp
@@ -456,10 +471,9 @@ cudaError_t launch_merge_entries(const EntryMergeParams& p, cudaStream_t stream)
 
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
   const long long rows = static_cast<long long>(p.B) * p.rows;
-  const bool by_row = rows >= kMinRows;
-  const long long warps = by_row ? rows : rows * 4;
-  const int per_block = by_row ? kRowWarps : kWarps;
-  const long long blocks = (warps + per_block - 1) / per_block;
+  const int row_warps = rows >= kMinRowsOneWarp ? 1 : rows >= kMinRows ? 2 : 4;
+  const int per_block = row_warps == 1 ? RowMerge<1>::kThreads / 32 : row_warps == 2 ? RowMerge<2>::kThreads / 32 : kWarps;
+  const long long blocks = (rows * row_warps + per_block - 1) / per_block;
   if (blocks <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
@@ -471,7 +485,8 @@ cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, by_row ? mla_merge_rows_kernel : mla_merge_kernel, p);
+  return cudaLaunchKernelEx(&cfg, row_warps == 1   ? mla_merge_rows_kernel<1>
+                                  : row_warps == 2 ? mla_merge_rows_kernel<2> : mla_merge_kernel, p);
 }
 
 }  // namespace mla

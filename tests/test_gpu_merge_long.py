@@ -117,3 +117,62 @@ def test_a_request_of_many_parts_does_not_slow_its_batch():
     batch = Batch([64] + [1] * 7, tokens=128)
     seven, eight = microseconds(batch, 7), microseconds(batch, 8)
     assert eight <= 1.2 * seven, (seven, eight)
+
+
+def merge_microseconds(parts, rows=128, calls=20):
+    """Device time of a merge of partials over `rows` rows a request, calls back to back."""
+    n = sum(parts)
+    r = torch.Generator(device="cuda").manual_seed(3)
+    part, lse = torch.randn(n, 1, rows, 512, device="cuda", generator=r), torch.randn(n, 1, rows, device="cuda", generator=r)
+    ind = torch.tensor(np.concatenate([[0], np.cumsum(parts)]), dtype=torch.int32, device="cuda")
+    out, out_lse = torch.empty(len(parts), 1, rows, 512, device="cuda"), torch.empty(len(parts), 1, rows, device="cuda")
+
+    def go():
+        nb.mla_merge_states(part.data_ptr(), lse.data_ptr(), ind.data_ptr(), len(parts), 1, rows, out.data_ptr(), nb.MLA_F32,
+                            out_lse.data_ptr(), torch.cuda.current_stream().cuda_stream)
+
+    go()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(calls):
+            go()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    best = float("inf")
+    for _ in range(20):
+        graph.replay()
+        start.record()
+        graph.replay()
+        end.record()
+        torch.cuda.synchronize()
+        best = min(best, start.elapsed_time(end) / calls * 1e3)
+    return best
+
+
+def test_a_request_of_many_partials_does_not_slow_a_merge_of_many_rows():
+    """2048 rows are merged with fewer warps a row than 1920 are; a request of 76 partials among them must not wait
+    for that."""
+    few, many = merge_microseconds([76] + [2] * 14), merge_microseconds([76] + [2] * 15)
+    assert many <= 1.3 * few, (few, many)
+
+
+@pytest.mark.parametrize("parts", [[76] + [2] * 15, [1, 33, 0, 8, 9, 17, 40, 64, 65] + [3] * 11])
+def test_merges_of_many_rows_with_a_long_request_have_the_bits_of_few(parts):
+    B, rows, n = len(parts), 128, sum(parts)
+    r = torch.Generator(device="cuda").manual_seed(4)
+    part, lse = torch.randn(n, 1, rows, 512, device="cuda", generator=r), 4 * torch.randn(n, 1, rows, device="cuda", generator=r)
+    lse[::5, :, ::3] = -float("inf")
+    at = np.concatenate([[0], np.cumsum(parts)])
+
+    def merge(lo, hi):
+        out, out_lse = torch.empty(hi - lo, 1, rows, 512, device="cuda"), torch.empty(hi - lo, 1, rows, device="cuda")
+        ind = torch.tensor(at[lo:hi + 1], dtype=torch.int32, device="cuda")
+        nb.mla_merge_states(part.data_ptr(), lse.data_ptr(), ind.data_ptr(), hi - lo, 1, rows, out.data_ptr(), nb.MLA_F32,
+                            out_lse.data_ptr(), None)
+        torch.cuda.synchronize()
+        return out, out_lse
+
+    out, out_lse = merge(0, B)
+    for b in range(B):
+        one, one_lse = merge(b, b + 1)
+        assert torch.equal(out[b], one[0]) and torch.equal(out_lse[b], one_lse[0]), b
