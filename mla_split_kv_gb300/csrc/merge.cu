@@ -336,39 +336,37 @@ constexpr int kEntryRowWarps = 2, kEntryRowLoads = 4 / kEntryRowWarps;
 // their (row, 16 columns) out (one of 131,072 tokens, 40 entries, beside seven of 2000: 62.6 us, 67.1 by rows; eight
 // requests with 9 entries each, where the last blocks find nothing, 14.4 against 14.1 without them).
 constexpr long long kMinEntryRows = 128;
-constexpr int kMaxRowEntries = 12, kLongBlocks = 256;
+constexpr int kMaxRowEntries = 12, kLongBlocks = 256, kLongPortion = kEntryWarps * 32;
 
 __global__ void __launch_bounds__(kEntryWarps * 32, 4)
     mla_merge_entries_rows_kernel(const EntryMergeParams p, uint32_t row_blocks) {
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (blockIdx.x >= row_blocks) {  // long requests
-    __shared__ int found[kEntryWarps * 32];
+  if (blockIdx.x >= row_blocks) {
+    // long requests: of a portion of the batch, one request a thread, shared with the blocks of the same portion
+    __shared__ int found[kLongPortion];
     __shared__ uint32_t masks[kEntryWarps];
+    const int block = blockIdx.x - row_blocks, portions = (p.B + kLongPortion - 1) / kLongPortion;
+    const int b = block % portions * kLongPortion + tid;
     pdl_wait();
-    for (int base = 0; base < p.B; base += kEntryWarps * 32) {
-      const int b = base + tid;
-      const bool is_long = b < p.B && (__ldcg(p.o_indptr + b + 1) - __ldcg(p.o_indptr + b)) * p.epc > kMaxRowEntries;
-      const uint32_t mask = __ballot_sync(0xffffffffu, is_long);
-      if (lane == 0) masks[warp] = mask;
-      __syncthreads();
-      int at = __popc(mask & ((1u << lane) - 1)), count = 0;  // in request order: the same list in every block
+    const bool is_long = b < p.B && (__ldcg(p.o_indptr + b + 1) - __ldcg(p.o_indptr + b)) * p.epc > kMaxRowEntries;
+    const uint32_t mask = __ballot_sync(0xffffffffu, is_long);
+    if (lane == 0) masks[warp] = mask;
+    __syncthreads();
+    int at = __popc(mask & ((1u << lane) - 1)), count = 0;  // in request order: the same list in every block
 #pragma unroll
-      for (int w = 0; w < kEntryWarps; ++w) {
-        const int n = __popc(masks[w]);
-        at += w < warp ? n : 0;
-        count += n;
-      }
-      if (is_long) found[at] = b;
-      __syncthreads();
-      const long long units = static_cast<long long>(count) * p.rows * 32;
-      const long long step = static_cast<long long>(gridDim.x - row_blocks) * kEntryWarps;
-      for (long long u = static_cast<long long>(blockIdx.x - row_blocks) * kEntryWarps + warp; u < units; u += step) {
-        const int which = found[u / (p.rows * 32)], row = static_cast<int>(u / 32 % p.rows);
-        merge_entry_columns(p, static_cast<long long>(which) * p.rows + row, row, static_cast<int>(u % 32),
-                            __ldcg(p.o_indptr + which) * p.epc, __ldcg(p.o_indptr + which + 1) * p.epc, lane);
-      }
-      __syncthreads();
+    for (int w = 0; w < kEntryWarps; ++w) {
+      const int n = __popc(masks[w]);
+      at += w < warp ? n : 0;
+      count += n;
+    }
+    if (is_long) found[at] = b;
+    __syncthreads();
+    const int per_request = p.rows * 32, step = (gridDim.x - row_blocks) / portions * kEntryWarps;
+    for (int u = block / portions * kEntryWarps + warp; u < count * per_request; u += step) {
+      const int which = found[u / per_request], row = u % per_request / 32;
+      merge_entry_columns(p, static_cast<long long>(which) * p.rows + row, row, u % 32, __ldcg(p.o_indptr + which) * p.epc,
+                          __ldcg(p.o_indptr + which + 1) * p.epc, lane);
     }
     return;
   }
@@ -453,7 +451,8 @@ cudaError_t launch_merge_entries(const EntryMergeParams& p, cudaStream_t stream)
   const uint32_t row_blocks = static_cast<uint32_t>(blocks);
   if (by_row && !p.uniform) {  // as many blocks as the long requests that there may be can use
     const long long most = p.entries / (kMaxRowEntries + 1) * p.rows * (32 / kEntryWarps);
-    blocks += most < kLongBlocks ? most : kLongBlocks;
+    const long long wanted = most < kLongBlocks ? most : kLongBlocks, portions = (p.B + kLongPortion - 1) / kLongPortion;
+    blocks += (wanted + portions - 1) / portions * portions;  // each portion of the batch as many
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
