@@ -63,8 +63,6 @@
 // Warp roles: softmax, rescale and output (thread = token; 8 rows a thread: 8
 // warps for 16 rows, 16 for 32), one warp each that issues the score and the
 // value products, one that loads pages.
-#include <atomic>
-
 #include "q8_schedule.cuh"
 
 namespace mla {
@@ -957,17 +955,10 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) mla_merge_q8_part
 
 template <int NR, bool BF16>
 cudaError_t launch(cudaLaunchConfig_t cfg, const CUtensorMap& tm_ckv, const CUtensorMap& tm_kpe, const DecodeQ8Params& p) {
-  static std::atomic<uint64_t> ready{0};  // by device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static DeviceOnce once;
+  const cudaError_t e = set_attribute_once(once, reinterpret_cast<const void*>(&mla_decode_q8_kernel<NR, BF16>),
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR, BF16>::kSmem);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t{1} << (dev & 63);
-  if (dev > 63 || (ready.load(std::memory_order_relaxed) & bit) == 0) {
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_decode_q8_kernel<NR, BF16>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR, BF16>::kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev <= 63) ready.fetch_or(bit, std::memory_order_relaxed);
-  }
   cfg.gridDim = dim3(static_cast<unsigned>(p.groups), static_cast<unsigned>(p.gangs), 1);
   cfg.blockDim = dim3(Cfg<NR, BF16>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg<NR, BF16>::kSmem;

@@ -9,9 +9,17 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "device_once.h"
 #include "kernels.h"
 
 namespace mla {
+
+// A function attribute of a kernel on the current device, set there before its first launch.
+inline cudaError_t set_attribute_once(DeviceOnce& once, const void* fn, cudaFuncAttribute attribute, int value) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : once(dev, [&] { return cudaFuncSetAttribute(fn, attribute, value); });
+}
 
 // Device error word of this translation unit (each kernel file has its own),
 // read and cleared by mla_check_device_errors.

@@ -797,14 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool BF16, bool X16, bool FP8, bool kWin>
 cudaError_t launch_mh(const cudaLaunchConfig_t& cfg, const CUtensorMap& tm_pages, const CUtensorMap& tm_kpe_half,
                       const PartialParams& p) {
-  static bool done = false;
-  if (!done) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_partial_mh_kernel<BF16, X16, FP8, kWin>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    done = true;
-  }
+  static DeviceOnce once;
+  const cudaError_t e = set_attribute_once(once, reinterpret_cast<const void*>(&mla_partial_mh_kernel<BF16, X16, FP8, kWin>),
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, mla_partial_mh_kernel<BF16, X16, FP8, kWin>, tm_pages, tm_kpe_half, p);
 }
 template <bool X16, bool kWin>

@@ -569,13 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool BF16, bool kWin>
 cudaError_t launch_nx(const cudaLaunchConfig_t& cfg, const CUtensorMap& tm_pages, const CUtensorMap& tm_kpe_half,
                       const PartialParams& p) {
-  static bool done = false;
-  if (!done) {
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mla_partial_mh_nx_kernel<BF16, kWin>),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    done = true;
-  }
+  static DeviceOnce once;
+  const cudaError_t e = set_attribute_once(once, reinterpret_cast<const void*>(&mla_partial_mh_nx_kernel<BF16, kWin>),
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, mla_partial_mh_nx_kernel<BF16, kWin>, tm_pages, tm_kpe_half, p);
 }
 

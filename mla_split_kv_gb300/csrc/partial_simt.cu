@@ -258,19 +258,11 @@ cudaError_t launch_partial_simt(const CUtensorMap& tm_ckv, const CUtensorMap& tm
                                 int num_chunks, int cluster, bool bf16, cudaStream_t stream) {
   const void* fn = bf16 ? reinterpret_cast<const void*>(&mla_partial_simt_kernel<true>)
                         : reinterpret_cast<const void*>(&mla_partial_simt_kernel<false>);
-  static bool prepared[2] = {false, false};
-  static bool nonportable[2] = {false, false};
-  cudaError_t e = cudaSuccess;
-  if (!prepared[bf16]) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    prepared[bf16] = true;
-  }
-  if (cluster > 8 && !nonportable[bf16]) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    nonportable[bf16] = true;
-  }
+  static DeviceOnce smem_once[2], cluster_once[2];
+  cudaError_t e = set_attribute_once(smem_once[bf16], fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e == cudaSuccess && cluster > 8)
+    e = set_attribute_once(cluster_once[bf16], fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   const int rows = p.q_len * p.H;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster, num_chunks, (rows + kRows - 1) / kRows);

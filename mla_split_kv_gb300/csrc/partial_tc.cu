@@ -486,23 +486,13 @@ uint32_t tc_smem(int nr, bool bf16) {
 
 int variant_index(int nr, bool bf16) { return (bf16 ? 3 : 0) + (nr == 16 ? 0 : (nr == 32 ? 1 : 2)); }
 
-// Kernel attributes, set once per variant.
+// Kernel attributes, set once per variant and device.
 cudaError_t prepare(const void* fn, int nr, bool bf16, int cluster) {
-  static bool smem_set[6] = {false, false, false, false, false, false};
-  static bool np_set[6] = {false, false, false, false, false, false};
+  static DeviceOnce smem_once[6], cluster_once[6];
   const int v = variant_index(nr, bf16);
-  cudaError_t e = cudaSuccess;
-  if (!smem_set[v]) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem(nr, bf16));
-    if (e != cudaSuccess) return e;
-    smem_set[v] = true;
-  }
-  if (cluster > 8 && !np_set[v]) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    np_set[v] = true;
-  }
-  return e;
+  const cudaError_t e = set_attribute_once(smem_once[v], fn, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem(nr, bf16));
+  if (e != cudaSuccess || cluster <= 8) return e;
+  return set_attribute_once(cluster_once[v], fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 }  // namespace

@@ -1109,20 +1109,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool kFp8, bool kBf16, bool kWin>
 cudaError_t prepare(int cluster) {
-  static bool smem_set = false, np_set = false;
+  static DeviceOnce smem_once, cluster_once;
   const void* fn = reinterpret_cast<const void*>(&mla_partial_tc128_kernel<kFp8, kBf16, kWin>);
-  cudaError_t e = cudaSuccess;
-  if (!smem_set) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    smem_set = true;
-  }
-  if (cluster > 8 && !np_set) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    np_set = true;
-  }
-  return e;
+  const cudaError_t e = set_attribute_once(smem_once, fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess || cluster <= 8) return e;
+  return set_attribute_once(cluster_once, fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 template <bool kWin>

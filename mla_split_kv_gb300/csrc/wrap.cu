@@ -308,17 +308,14 @@ cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_merge_unembed(const UnembedParams& p, bool w_bf16, cudaStream_t stream) {
-  static bool smem_set[4] = {false, false, false, false};
+  static DeviceOnce smem_once[4];
   const int inst = (w_bf16 ? 1 : 0) + (p.entries ? 2 : 0);
   const void* fns[4] = {reinterpret_cast<const void*>(&mla_merge_unembed_kernel<false, false>),
                         reinterpret_cast<const void*>(&mla_merge_unembed_kernel<true, false>),
                         reinterpret_cast<const void*>(&mla_merge_unembed_kernel<false, true>),
                         reinterpret_cast<const void*>(&mla_merge_unembed_kernel<true, true>)};
-  if (!smem_set[inst]) {
-    const cudaError_t e = cudaFuncSetAttribute(fns[inst], cudaFuncAttributeMaxDynamicSharedMemorySize, kUnSmem);
-    if (e != cudaSuccess) return e;
-    smem_set[inst] = true;
-  }
+  const cudaError_t e = set_attribute_once(smem_once[inst], fns[inst], cudaFuncAttributeMaxDynamicSharedMemorySize, kUnSmem);
+  if (e != cudaSuccess) return e;
   const long long R = static_cast<long long>(p.B) * p.q_len;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.H), static_cast<unsigned>(p.v_head / kUnCols),
