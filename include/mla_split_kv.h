@@ -485,8 +485,16 @@ mla_status_t mla_decode(const void* q_absorbed, const void* q_pe, const void* ck
  * The CTA-pair kernels only: MLA_ERR_UNSUPPORTED for MLA_KERNEL_SIMT,
  * cluster_ctas 1, and clusters other than 2 (or 0 = auto) with more than 16
  * rows. Caches of any dtype that mla_decode takes. desc->prefix_ready speaks
- * of the same positions as there. Otherwise mla_decode's arguments and
- * results. The pages have no counterpart.
+ * of the same positions as there. desc->score_exchange: as there, but EXACT is
+ * NONE on 16-bit caches with any number of rows. Otherwise mla_decode's
+ * arguments and results. The pages have no counterpart.
+ *
+ * Precision: scores, maxima and sums are fp32. The probabilities of the value
+ * product are kept as in mla_decode: in fp16 beside fp16 and E4M3 caches
+ * (2^-11 of themselves), normalized by the sum of the rounded ones, and in two
+ * bf16 terms beside bf16 caches (2^-16). out_lse is that of the unrounded ones;
+ * only with MLA_DECODE_MERGE_TICKETS (16 rows) beside fp16 and E4M3 caches that
+ * of the rounded ones, up to 7.1e-4 off.
  */
 mla_status_t mla_decode_window(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
                                const int32_t* block_table, const int32_t* context_lens, float scale,
