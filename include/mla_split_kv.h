@@ -480,7 +480,9 @@ mla_status_t mla_decode(const void* q_absorbed, const void* q_pe, const void* ck
  * desc->chunks == NULL the run is split into num_partitions. A chunk past the
  * end of a run is empty, so a plan for the longest run a request can have
  * (a run's length repeats from page to page of its context) serves every
- * step, and a captured call may be replayed as the contexts grow.
+ * step, and a captured call may be replayed as the contexts grow. What a run
+ * has behind its last chunk is not seen: let that chunk end at 2^31 - 1 where
+ * a run may be longer than planned.
  *
  * The CTA-pair kernels only: MLA_ERR_UNSUPPORTED for MLA_KERNEL_SIMT,
  * cluster_ctas 1, and clusters other than 2 (or 0 = auto) with more than 16

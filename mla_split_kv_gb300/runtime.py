@@ -226,9 +226,9 @@ def plan_segments(seg, dev: nb.mla_device_info_t, max_partitions: int = 0, devic
 
 @dataclasses.dataclass
 class WindowPlan:
-    """A plan of mla_decode_window for one batch shape, with the buffers its calls use. It serves the lengths it
-    was made for and every request with a visible run no longer than planned. Calls that may overlap in time
-    (other streams) need a plan each."""
+    """A plan of mla_decode_window for one batch shape, with the buffers its calls use. It serves contexts of any
+    length, in the time planned for visible runs no longer than it was made for: each request's last partition takes
+    what its run has beyond that. Calls that may overlap in time (other streams) need a plan each."""
     num_requests: int
     num_heads: int
     q_len: int
@@ -293,12 +293,19 @@ def _window_partitions(runs: Sequence[int], num_heads: int, q_len: int, block_si
     return best
 
 
+def _open_ended(plan: nb.Plan) -> list:
+    """The plan's chunks, each request's last one up to the end of its run however long that is (the kernels clip)."""
+    last = set(plan.o_indptr[1:])
+    return [(b, t0, 2 ** 31 - 1 if slot + 1 in last else t1, slot) for b, t0, t1, slot in plan.chunks]
+
+
 def plan_window(context_lens: Sequence[int], num_heads: int, q_len: int, block_size: int, window: int, sinks: int = 0,
                 dtype: str = "f16", causal: bool = False, dev: Optional[nb.mla_device_info_t] = None,
                 max_partitions: int = 0, device="cuda", grow: int = 0) -> WindowPlan:
     """Partitions of the requests' visible runs: at most max_partitions each by mla_plan's thresholds, or (0) as many
     as fill the device. `grow`: tokens by which each context may grow while the plan is used (a run's length goes up
-    and down by a page with its context's place in the page, so a plan made for one length may miss the next)."""
+    and down by a page with its context's place in the page, so a plan made for one length may be a page short at the
+    next, which its last partition then has to take)."""
     if grow < 0:
         raise ValueError(f"grow: {grow}")
     runs = nb.mla_window_lens(context_lens, q_len, block_size, causal, window, sinks)
@@ -313,7 +320,7 @@ def plan_window(context_lens: Sequence[int], num_heads: int, q_len: int, block_s
         plan = _window_partitions(runs, num_heads, q_len, block_size, dtype, dev)
     part, lse = alloc_partials(plan.num_chunks, q_len, num_heads, device)
     return WindowPlan(len(runs), num_heads, q_len, block_size, dtype, causal, window, sinks, plan,
-                      chunks_to_device(plan.chunks, device),
+                      chunks_to_device(_open_ended(plan), device),
                       torch.tensor(plan.o_indptr, dtype=torch.int32, device=device), part, lse,
                       alloc_decode_workspace(len(runs), plan.num_chunks, plan.clusters_per_chunk, plan.cluster_ctas,
                                              q_len, num_heads, device))
