@@ -615,8 +615,9 @@ mla_status_t mla_decode_unembed(const void* q_absorbed, const void* q_pe, const 
  * tokens before the request's first new one lie in the block too, the larger
  * of that and the scale they have, and where the scale grows their bytes are
  * moved to it (e4m3(byte) * old / new, rounded once; exact but for values that
- * become subnormal). A value is stored as the E4M3 byte nearest to x / s, ties
- * to even, saturating at +-448. Whatever the block held behind its first new
+ * become subnormal; where `old` comes from elsewhere and is no power of two the
+ * product is formed in fp32 first). A value is stored as the E4M3 byte nearest
+ * to x / s, ties to even, saturating at +-448. Whatever the block held behind its first new
  * token counts for nothing, so positions may be written again after a
  * rejected draft. A block that gets a NaN, an infinity or a value above
  * 448 * 2^60 has its scale set to NaN and those new bytes to 0.

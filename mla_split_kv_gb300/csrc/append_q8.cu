@@ -44,6 +44,13 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t m, const uint4 v) {
   return __vmaxu2(__vmaxu2(m, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
 }
 
+// An fp32 result cut off towards zero, with its last bit set where something was cut off (`rest`): rounded to fewer
+// bits, this gives what the exact result does, while a result already rounded to nearest may lie on a tie that the
+// exact one does not. (Its 24 bits are many more than E4M3's 4 and two.)
+__device__ __forceinline__ float sticky(float cut, float rest) {
+  return rest != 0.f ? __uint_as_float(__float_as_uint(cut) | 1u) : cut;
+}
+
 // Eight values over the scale: by its inverse where it is a power of two (the same result, s and 1 / s are exact),
 // else (a scale from elsewhere that stays in force) by division.
 template <bool BF16>
@@ -60,12 +67,15 @@ __device__ __forceinline__ uint2 quantize8(const uint4 v, float s, float inv) {
     for (int j = 0; j < 8; ++j) x[j] *= inv;
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], s);
+    for (int j = 0; j < 8; ++j) {
+      const float q = __fdiv_rz(x[j], s);
+      x[j] = sticky(q, fmaf(-q, s, x[j]));
+    }
   }
   return make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
 }
 
-// a stored byte's value times ratio, four in a word
+// a stored byte's value times ratio in fp32 (exact where the old scale is a power of two), four in a word
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   uint32_t lo, hi;
   e4m3x4_to_f16x4(w, lo, hi);
