@@ -413,6 +413,8 @@ def _code_of(t: torch.Tensor, what: str) -> int:
 
 def alloc_q8_cache(num_blocks: int, block_size: int, scale_block: int, device="cuda") -> Q8Cache:
     """An empty pool (every byte 0, every scale 1)."""
+    if scale_block < 1 or block_size % scale_block:
+        raise ValueError(f"scale_block: {scale_block} does not divide pages of {block_size} tokens")
     return Q8Cache(torch.zeros((num_blocks, block_size, 512), dtype=torch.uint8, device=device),
                    torch.zeros((num_blocks, block_size, 64), dtype=torch.uint8, device=device),
                    torch.ones((num_blocks, block_size // scale_block), dtype=torch.float32, device=device))
