@@ -316,6 +316,11 @@ def plan_window(context_lens: Sequence[int], num_heads: int, q_len: int, block_s
     dev = dev if dev is not None else nb.mla_device_query(-1 if index is None else index)
     if max_partitions:
         plan = nb.mla_plan(runs, num_heads, q_len, block_size, dev, max_partitions=max_partitions, dtype=dtype)
+        while plan.cluster_ctas < 2 and max_partitions > 1:
+            # so many that a CTA pair's share of one would be under 128 tokens: planned for single CTAs, which a
+            # windowed call does not run on
+            max_partitions //= 2
+            plan = nb.mla_plan(runs, num_heads, q_len, block_size, dev, max_partitions=max_partitions, dtype=dtype)
     else:
         plan = _window_partitions(runs, num_heads, q_len, block_size, dtype, dev)
     part, lse = alloc_partials(plan.num_chunks, q_len, num_heads, device)
