@@ -231,7 +231,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     mine += n + (n > 0 ? int64_t{1} << kQ8CountShift : 0);
   }
   const int64_t prefix = block_prefix<kThreads>(mine, sm->scratch, &T);
-  const Q8Line line = q8_line(T & kQ8Tiles, static_cast<int32_t>(T >> kQ8CountShift), p.gangs);
+  const Q8Line line = q8_line<kQ8Gap<NR>>(T & kQ8Tiles, static_cast<int32_t>(T >> kQ8CountShift), p.gangs);
   const bool work = gang < line.gangs;
   const int64_t lo = work ? line.begin(gang) : 0, hi = work ? line.begin(gang + 1) : 0;
   {  // the thread whose requests the gang starts (ends) in finds the place: its request and tile, tiles before it

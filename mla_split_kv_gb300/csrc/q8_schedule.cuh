@@ -4,8 +4,8 @@
 // The batch's visible runs, cut into tiles request after request,
 // are one line, with a gap of a few cells between requests: what a gang spends on
 // going from one request to the next (its output, the next one's queries, the
-// first tiles' rescales: 8 us at 32 rows, 5 at 16, five to seven tiles) counts as
-// tiles. Gang j of J takes L / J cells of the line's L, the first L % J gangs one
+// first tiles' rescales: 8 us at 32 rows a CTA, 5 at 16, of tiles of 2600 cycles:
+// six, and four) counts as tiles. Gang j of J takes L / J cells of the line's L, the first L % J gangs one
 // more (one CTA of a gang per row group), so every gang works as long as the
 // others whatever the lengths (without the gaps, gangs with one request ended
 // after 55 us, those with two after 65 to 76; calls 4 to 7% slower). Lengths are
@@ -36,7 +36,12 @@ struct Q8Lens {
 // A pair of counts in one sum: tiles (at most 65535 * 2^25 < 2^44) and the requests that have any.
 constexpr int kQ8CountShift = 44;
 constexpr int64_t kQ8Tiles = (int64_t{1} << kQ8CountShift) - 1;
-constexpr int kQ8Gap = 6;
+// The gap. Measured with 4 / 5 / 6 / 7 tiles: 32 rows, 8 requests to 64K of 128 heads 141.4 / 140.6 / 139.7 / 138.9 us,
+// 48 windows of 4096 of 64 heads 67.0 / 65.6 / 65.7 / 65.6, 4 requests of 9 fp16 rows 141.9 / 140.9 / 140.3 / 140.3; 16
+// rows, 300 requests of 500 to 3000 tokens 69.0 / 69.1 / 70.2 / 71.5, 150 of 2K to 9K 90.2 / 90.4 / 91.5 / 92.7, 32 to 16K
+// 42.6 with each.
+template <int NR>
+constexpr int kQ8Gap = NR == 16 ? 4 : 6;
 
 // The line among the gangs that get any of it (all of them unless there are fewer tiles).
 struct Q8Line {
@@ -53,11 +58,12 @@ struct Q8Line {
     return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
   }
 };
+template <int kGap>
 __device__ __forceinline__ Q8Line q8_line(int64_t tiles, int32_t requests, int gangs) {
   Q8Line l;
   // a gap is at most a fifth of a gang's tiles, so every gang has some
   const int64_t share = Q8Line::div(tiles, gangs);
-  l.gap = share >= 5 * kQ8Gap ? kQ8Gap : static_cast<int32_t>(share) / 5;
+  l.gap = share >= 5 * kGap ? kGap : static_cast<int32_t>(share) / 5;
   l.length = tiles + (requests > 1 ? static_cast<int64_t>(l.gap) * (requests - 1) : 0);
   l.gangs = l.length < gangs ? static_cast<int32_t>(l.length) : gangs;
   l.base = l.gangs > 0 ? Q8Line::div(l.length, l.gangs) : 0;
