@@ -16,15 +16,15 @@
 // read twice, and 4.6 KB per warp are in flight), the warps of a block meet
 // once, and the maximum is taken over the 16-bit patterns themselves: without
 // its sign a pattern orders like its value, NaN above infinity. 65,536 tokens
-// in blocks of one: 24.6 us, 4.6 TB/s (one token at a time per warp, read
-// twice: 87 us); a single token: 3.8 us.
+// in blocks of one: 23.3 us, 4.9 TB/s (one token at a time per warp, read
+// twice: 87 us); a single token: 3.6 us.
 #include "device_common.cuh"
 
 namespace mla {
 
 namespace {
 
-constexpr int kWarps = 16, kFewWarps = 8;  // of a CTA; where a block needs no more, 8: shorter tails (24.6 us, 26.2 with 16)
+constexpr int kWarps = 16, kFewWarps = 8;  // of a CTA; where a block needs no more, 8: shorter tails (23.3 us, 25.3 with 16)
 constexpr int kHold = 4;  // tokens per warp: 16 warps hold a block of the longest page, 64 tokens
 constexpr int kMinExp = -60, kMaxExp = 60;
 

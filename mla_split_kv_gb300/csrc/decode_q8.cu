@@ -55,10 +55,10 @@
 //
 // Measured (us a call, captured back to back; scaling by HBM alone in brackets):
 // 131,072 tokens, 16 fp16 heads 25.5 (11.1); 32 requests up to 16K, 16 bf16 heads
-// 42.5 (25.8); 8 requests up to 64K, 128 bf16 heads 139 (26.2; the formula's
+// 42.7 (25.8); 8 requests up to 64K, 128 bf16 heads 139.7 (26.2; the formula's
 // products at the card's 16-bit matrix rate 44); 9 causal fp16 rows over 16 heads,
-// 4 requests up to 82K, 141 (19.9 and 38); 48 requests through a window of 4096,
-// 64 bf16 heads, 66.3 (17.3); 37 tokens 10.3.
+// 4 requests up to 82K, 140.5 (19.9 and 38); 48 requests through a window of 4096,
+// 64 bf16 heads, 66.4 (17.3); 37 tokens 10.1.
 //
 // Warp roles: softmax, rescale and output (thread = token; 8 rows a thread: 8
 // warps for 16 rows, 16 for 32), one warp each that issues the score and the
