@@ -322,7 +322,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     const int tok = lane << unit_shift;            // its first token in the tile
     // the table's entry for this lane's unit (looked at when it is used: its load has a tile's time)
     auto entry_of = [&](const Q8Walk& w, int tile) -> int {
-      const uint32_t at = tile * kT + tok;  // (past 2^31 at the end of the longest context)
+      const uint32_t at = run_position(tile, kT, tok);
       if (tok >= kT || at >= static_cast<uint32_t>(w.v.n)) return -1;
       const int u = static_cast<int>(at);
       const int pg = (u >> p.bs_shift) + (u >= w.v.sa ? w.v.skip >> p.bs_shift : 0);
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     int tile = w.ta;
     auto next_unit = [&]() -> Unit {
       if (!live) return Unit{-1, 0, 0};
-      const Unit r{entry_of(w, tile), (tile * kT + tok) & (p.bs - 1), (min(kT, w.v.n - tile * kT) + unit - 1) >> unit_shift};
+      const Unit r{entry_of(w, tile), static_cast<int>(run_position(tile, kT, tok)) & (p.bs - 1), (min(kT, w.v.n - tile * kT) + unit - 1) >> unit_shift};
       if (++tile == w.tb) {
         live = q8_next<kT>(p, lens, w, false);
         tile = w.ta;
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     // this thread's page of a tile, and its token's scale there: loads a tile ahead of their use each, so
     // neither looks at what it loaded
     auto page_at = [&](const Q8Walk& w, int tile) -> int {
-      const uint32_t at = tile * kT + tl;  // (past 2^31 at the end of the longest context)
+      const uint32_t at = run_position(tile, kT, tl);
       if (!has_tokens || at >= static_cast<uint32_t>(w.v.n)) return -1;
       const int u = static_cast<int>(at);
       const int pg = (u >> p.bs_shift) + (u >= w.v.sa ? w.v.skip >> p.bs_shift : 0);
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
     };
     auto scale_at = [&](int pid, int tile) -> float {  // 1 where there is no page
       if (pid < 0 || pid >= p.num_blocks) return 1.f;
-      const int row = (pid << p.bs_shift) + ((tile * kT + tl) & (p.bs - 1));  // (a pool has fewer than 2^31 tokens)
+      const int row = (pid << p.bs_shift) + (static_cast<int>(run_position(tile, kT, tl)) & (p.bs - 1));  // (a pool has fewer than 2^31 tokens)
       return __ldcg(p.scales + (row >> p.g_shift));
     };
     // The value product of tile t: it has left the slot. (The phase before on that barrier, tile t - kSlots,
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
       // rows' positions: the first and last row of this CTA, and what their windows leave out
       const int pos_first = p.causal ? w.v.n - p.q_len + (row0 >> p.h_shift) : w.v.n - 1;
       const int pos_last = p.causal ? w.v.n - p.q_len + ((row0 + nrows - 1) >> p.h_shift) : w.v.n - 1;
-      const int low_last = p.window > 0 ? max(-1, pos_last - p.window) : -1;
+      const int low_last = p.window > 0 ? window_floor(pos_last, p.window) : -1;
       // tiles of which every row sees every token (rows past the last, zeros, may see what they like: nothing of
       // theirs is written)
       const int plain_lo = low_last < 0 ? 0 : low_last / kT + 1, plain_hi = max(0, pos_first + 1) / kT;
@@ -543,10 +543,11 @@ __global__ void __launch_bounds__((Cfg<NR, BF16>::kThreads), 1)
             const int u0 = tile * kT, nvalid = min(kT, w.v.n - u0);
 #pragma unroll
             for (int k = 0; k < RH; ++k) {
-              const int r = row0 + RH * h + k, u = u0 + tl;
+              const int r = row0 + RH * h + k;
+              const uint32_t u = run_position(tile, kT, tl);
               const int pos = p.causal ? w.v.n - p.q_len + (r >> p.h_shift) : w.v.n - 1;
-              bool vis = tl < nvalid && u <= pos;
-              if (p.window > 0) vis = vis && (u > pos - p.window || u < p.sinks);
+              bool vis = tl < nvalid && static_cast<int>(u) <= pos;
+              if (p.window > 0) vis = vis && (static_cast<int>(u) > window_floor(pos, p.window) || static_cast<int>(u) < p.sinks);
               if (!vis) x[k] = -INFINITY;
             }
             // tokens that some row does not see: below the last row's window, behind the first row, and the

@@ -630,7 +630,7 @@ __device__ __forceinline__ int32_t table_page(const CtaWork& w, int32_t pg) {
 // The last position of the visible run that the window of the row at position `pos` leaves out (-1: none).
 template <bool kWin>
 __device__ __forceinline__ int32_t window_low(const PartialParams& p, int32_t pos) {
-  return kWin ? max(-1, pos - p.window) : -1;
+  return kWin ? window_floor(pos, p.window) : -1;
 }
 // Whether a window hides position u from the row at position `pos`, both in the visible run.
 template <bool kWin>

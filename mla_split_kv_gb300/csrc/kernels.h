@@ -151,6 +151,17 @@ MLA_HOST_DEVICE inline WindowView window_view(int32_t L, int32_t q_len, int32_t 
   return v;
 }
 
+// The last position that the window of the row at position `pos` leaves out (-1: none). A row before the request's
+// first token (pos < 0) sees nothing whatever this says.
+MLA_HOST_DEVICE inline int32_t window_floor(int32_t pos, int32_t window) {
+  const int32_t low = (pos > -1 ? pos : -1) - window;  // (no less than -2^31)
+  return low > -1 ? low : -1;
+}
+// Position of token t of a tile of a run, without a sign: a tile at the end of the longest run passes 2^31.
+MLA_HOST_DEVICE inline uint32_t run_position(int32_t tile, int32_t tile_tokens, int32_t t) {
+  return static_cast<uint32_t>(tile) * static_cast<uint32_t>(tile_tokens) + static_cast<uint32_t>(t);
+}
+
 // Block-scaled 8-bit caches: the value of a cached byte x of token row r is e4m3(x) * scales[r >> g_shift].
 struct AppendQ8Params {
   const uint16_t* ckv_new;     // [B, q_len, 512]
