@@ -14,6 +14,8 @@
 // its first read, so its launch latency hides behind the partial kernel's end.
 // The weights are computed lane-parallel (lane s holds partial s), the sum over
 // partials runs in fixed order, so the result is bitwise reproducible.
+#include <algorithm>
+
 #include "device_common.cuh"
 
 namespace mla {
@@ -333,38 +335,28 @@ constexpr int kEntryRowWarps = 2, kEntryRowLoads = 4 / kEntryRowWarps;
 // against 12.0 / 14.5, 8 with 4 / 9 entries 11.8 / 16.2 against 14.2 / 17.1, 32 with 2 entries 12.9 against 26.0,
 // 64 with one 13.2 against 41.5. So a request of more than 12 entries is merged as above, request by request (the host
 // knows no request's count, only their sum): the grid's last blocks look such requests up in the offsets and share
-// their (row, 16 columns) out (one of 131,072 tokens, 40 entries, beside seven of 2000: 62.6 us, 67.1 by rows; eight
-// requests with 9 entries each, where the last blocks find nothing, 14.4 against 14.1 without them).
+// their (row, 16 columns) out. One of 131,072 tokens, 40 entries, beside seven of 2000: 62.8 us, 67.1 by rows; 16
+// requests of 4096 tokens, where the last blocks find nothing, 25.2 (26.7 with a list of 528 bytes of shared memory,
+// for which an SM has no room beside the paired kernel).
 constexpr long long kMinEntryRows = 128;
-constexpr int kMaxRowEntries = 12, kLongBlocks = 256, kLongPortion = kEntryWarps * 32;
+constexpr int kMaxRowEntries = 12, kLongBlocks = 256;
 
 __global__ void __launch_bounds__(kEntryWarps * 32, 4)
     mla_merge_entries_rows_kernel(const EntryMergeParams p, uint32_t row_blocks) {
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x >= row_blocks) {
-    // long requests: of a portion of the batch, one request a thread, shared with the blocks of the same portion
-    __shared__ int found[kLongPortion];
-    __shared__ uint32_t masks[kEntryWarps];
-    const int block = blockIdx.x - row_blocks, portions = (p.B + kLongPortion - 1) / kLongPortion;
-    const int b = block % portions * kLongPortion + tid;
+    // long requests: of 32 in a row, one a lane, shared with the warps that look at the same ones (no shared memory,
+    // see above)
+    const int warps = (gridDim.x - row_blocks) * kEntryWarps, me = (blockIdx.x - row_blocks) * kEntryWarps + warp;
+    const int portions = (p.B + 31) / 32, portion = me % portions, b = portion * 32 + lane;
     pdl_wait();
-    const bool is_long = b < p.B && (__ldcg(p.o_indptr + b + 1) - __ldcg(p.o_indptr + b)) * p.epc > kMaxRowEntries;
-    const uint32_t mask = __ballot_sync(0xffffffffu, is_long);
-    if (lane == 0) masks[warp] = mask;
-    __syncthreads();
-    int at = __popc(mask & ((1u << lane) - 1)), count = 0;  // in request order: the same list in every block
-#pragma unroll
-    for (int w = 0; w < kEntryWarps; ++w) {
-      const int n = __popc(masks[w]);
-      at += w < warp ? n : 0;
-      count += n;
-    }
-    if (is_long) found[at] = b;
-    __syncthreads();
-    const int per_request = p.rows * 32, step = (gridDim.x - row_blocks) / portions * kEntryWarps;
-    for (int u = block / portions * kEntryWarps + warp; u < count * per_request; u += step) {
-      const int which = found[u / per_request], row = u % per_request / 32;
+    const uint32_t found = __ballot_sync(
+        0xffffffffu, b < p.B && (__ldcg(p.o_indptr + b + 1) - __ldcg(p.o_indptr + b)) * p.epc > kMaxRowEntries);
+    const int per_request = p.rows * 32, units = __popc(found) * per_request;
+    const int step = (warps - portion + portions - 1) / portions;
+    for (int u = me / portions; u < units; u += step) {
+      const int which = portion * 32 + static_cast<int>(__fns(found, 0, u / per_request + 1)), row = u % per_request / 32;
       merge_entry_columns(p, static_cast<long long>(which) * p.rows + row, row, u % 32, __ldcg(p.o_indptr + which) * p.epc,
                           __ldcg(p.o_indptr + which + 1) * p.epc, lane);
     }
@@ -451,8 +443,8 @@ cudaError_t launch_merge_entries(const EntryMergeParams& p, cudaStream_t stream)
   const uint32_t row_blocks = static_cast<uint32_t>(blocks);
   if (by_row && !p.uniform) {  // as many blocks as the long requests that there may be can use
     const long long most = p.entries / (kMaxRowEntries + 1) * p.rows * (32 / kEntryWarps);
-    const long long wanted = most < kLongBlocks ? most : kLongBlocks, portions = (p.B + kLongPortion - 1) / kLongPortion;
-    blocks += (wanted + portions - 1) / portions * portions;  // each portion of the batch as many
+    const long long portions = (p.B + 31) / 32, least = most > 0 ? (portions + kEntryWarps - 1) / kEntryWarps : 0;
+    blocks += std::max(least, std::min<long long>(most, kLongBlocks));
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
