@@ -1,5 +1,6 @@
 // C ABI entry points: argument checks (before any launch), TMA tensor-map
 // setup, kernel dispatch, launch counters and the device error word.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -499,6 +500,33 @@ mla_status_t launch_pair_entries(const void* q_absorbed, const void* q_pe, const
 
 namespace {
 
+// mla_merge_states; most_parts: the most partials that a request can have (0: not known)
+mla_status_t merge_states(const float* partials, const float* lse, const int32_t* o_indptr, int32_t B, int32_t q_len,
+                          int32_t num_heads, void* out, int32_t out_dtype, float* out_lse, int64_t most_parts,
+                          void* stream) {
+  if (partials == nullptr || lse == nullptr || o_indptr == nullptr || out == nullptr) return reject(MLA_ERR_INVALID_ARG);
+  if (B < 1 || B > (1 << 24)) return reject(MLA_ERR_INVALID_ARG);
+  if (!valid_heads(num_heads) || q_len < 1 || q_len > MLA_MAX_Q_LEN) return reject(MLA_ERR_UNSUPPORTED);
+  if (out_dtype != MLA_F16 && out_dtype != MLA_BF16 && out_dtype != MLA_F32) return reject(MLA_ERR_UNSUPPORTED);
+  if (!aligned(partials, 16) || !aligned(lse, 4) || !aligned(o_indptr, 4) || !aligned(out, 16) ||
+      (out_lse != nullptr && !aligned(out_lse, 4)))
+    return reject(MLA_ERR_INVALID_ARG);
+  mla::MergeParams p;
+  p.partials = partials;
+  p.lse = lse;
+  p.o_indptr = o_indptr;
+  p.out = out;
+  p.out_lse = out_lse;
+  p.B = B;
+  p.rows = q_len * num_heads;
+  p.out_dtype = out_dtype;
+  p.most_parts = most_parts;
+  const cudaError_t e = mla::launch_merge(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
+  g_counters[MLA_CTR_MERGE].fetch_add(1, std::memory_order_relaxed);
+  return MLA_OK;
+}
+
 // mla_decode, and mla_decode_window with its window
 mla_status_t decode_call(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
                          const int32_t* block_table, const int32_t* context_lens, float scale, int32_t num_partitions,
@@ -556,8 +584,10 @@ mla_status_t decode_call(const void* q_absorbed, const void* q_pe, const void* c
     mla_status_t st = launch_decode(q_absorbed, q_pe, ckv_cache, kpe_cache, block_table, context_lens, scale,
                                     num_partitions, partials, lse, d, N, d->workspace, FusedMerge{}, false, win);
     if (st != MLA_OK) return st;
-    return mla_merge_states(partials, lse, o_indptr, d->num_requests, d->q_len, d->num_heads, out, out_dtype, out_lse,
-                            d->stream);
+    // (with a table: one request has what the others, with one each, leave it)
+    const int64_t most_parts = d->chunks == nullptr ? num_partitions : std::max<int64_t>(1, N - (d->num_requests - 1));
+    return merge_states(partials, lse, o_indptr, d->num_requests, d->q_len, d->num_heads, out, out_dtype, out_lse,
+                        most_parts, d->stream);
   }
   const uint64_t need = mla_decode_workspace_bytes(d->num_requests, static_cast<int32_t>(N), d->clusters_per_chunk,
                                                    d->cluster_ctas, d->q_len, d->num_heads);
@@ -760,26 +790,7 @@ uint64_t mla_workspace_bytes(int32_t num_chunks, int32_t clusters_per_chunk, int
 mla_status_t mla_merge_states(const float* partials, const float* lse, const int32_t* o_indptr, int32_t B,
                               int32_t q_len, int32_t num_heads, void* out, int32_t out_dtype, float* out_lse,
                               void* stream) {
-  if (partials == nullptr || lse == nullptr || o_indptr == nullptr || out == nullptr) return reject(MLA_ERR_INVALID_ARG);
-  if (B < 1 || B > (1 << 24)) return reject(MLA_ERR_INVALID_ARG);
-  if (!valid_heads(num_heads) || q_len < 1 || q_len > MLA_MAX_Q_LEN) return reject(MLA_ERR_UNSUPPORTED);
-  if (out_dtype != MLA_F16 && out_dtype != MLA_BF16 && out_dtype != MLA_F32) return reject(MLA_ERR_UNSUPPORTED);
-  if (!aligned(partials, 16) || !aligned(lse, 4) || !aligned(o_indptr, 4) || !aligned(out, 16) ||
-      (out_lse != nullptr && !aligned(out_lse, 4)))
-    return reject(MLA_ERR_INVALID_ARG);
-  mla::MergeParams p;
-  p.partials = partials;
-  p.lse = lse;
-  p.o_indptr = o_indptr;
-  p.out = out;
-  p.out_lse = out_lse;
-  p.B = B;
-  p.rows = q_len * num_heads;
-  p.out_dtype = out_dtype;
-  const cudaError_t e = mla::launch_merge(p, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return MLA_ERR_CUDA;
-  g_counters[MLA_CTR_MERGE].fetch_add(1, std::memory_order_relaxed);
-  return MLA_OK;
+  return merge_states(partials, lse, o_indptr, B, q_len, num_heads, out, out_dtype, out_lse, 0, stream);
 }
 
 mla_status_t mla_cache_append(const void* ckv_new, const void* kpe_new, const int32_t* block_table,

@@ -92,6 +92,7 @@ struct MergeParams {
   float* out_lse;
   int32_t B, rows;  // rows = q_len * H
   int32_t out_dtype;
+  int64_t most_parts;  // the most partials that a request can have (0: not known)
 };
 
 // The cache write of a layer call: token i of request b's q_len new tokens goes to logical

@@ -112,13 +112,15 @@ __global__ void __launch_bounds__(kWarps * 32) mla_merge_kernel(const MergeParam
 // (request, row): one, or two, a lane owning 4 columns of each of its warp's quarters, so the weights' code runs once
 // (twice) a row instead of four times. A request of many partials goes through rounds of loads one behind the other
 // whatever its batch, so from 2048 rows on, where one such request sets the time, two warps with eight partials in
-// flight take a row, from 4096 on one warp with two. Measured, one warp / two / four: 2048 rows with 2 partials a row
-// 3.6 / 4.1 / 6.3 us, with 9 6.1 / 5.7 / 8.3, with 40 29 / 27.5 / 31, with 60 (76) in one request of 16 and 1 (2) in the
-// others 11.3 (14.1) / 6.8 (8.2) / 7.4 (8.3); 4096 rows with 60 in one request of 32 11.4 / 7.8 / 12.0, with 16 a row
-// 25.8 / 21.9 / 24.8, with 2 behind a partial kernel 1 us less with one than with two. Below 2048 rows four warps are
-// four chains of loads side by side: 1024 rows with 2 / 9 partials 2.6 / 4.0 us with one against 3.9 / 5.3, but 1 us
-// more behind a partial kernel (fewer of its larger blocks are resident early); 512 rows 2.4 / 3.6 against 2.4 / 3.2.
-constexpr long long kMinRows = 2048, kMinRowsOneWarp = 4096;
+// flight take a row, from 4096 on, or where no request can have many, one warp with two. Measured, one warp / two /
+// four: 2048 rows with 2 partials a row 3.6 / 4.1 / 6.3 us, with 9 6.1 / 5.7 / 8.3, with 40 29 / 27.5 / 31, with 20 (60,
+// 76) in one request of 16 and 1 (1, 2) in the others 5.6 (11.3, 14.1) / 4.2 (6.8, 8.2) / 6.5 (7.4, 8.3); 4096 rows with
+// 60 in one request of 32 11.4 / 7.8 / 12.0, with 16 a row 25.8 / 21.9 / 24.8; behind a partial kernel two warps take
+// longer than one, 2560 rows with 1 partial a row, whole calls 41.7 against 42.9 us, 3840 rows 25.3 against 26.8, 4096
+// rows with 2 108.0 against 109.1. Below 2048 rows four warps are four chains of loads side by side: 1024 rows with 2 /
+// 9 partials 2.6 / 4.0 us with one against 3.9 / 5.3, but 1 us more behind a partial kernel (fewer of its larger blocks
+// are resident early); 512 rows 2.4 / 3.6 against 2.4 / 3.2.
+constexpr long long kMinRows = 2048, kMinRowsOneWarp = 4096, kFewParts = 24;
 template <int kRowWarps>  // warps a row
 struct RowMerge {
   static constexpr int kQuarters = 4 / kRowWarps, kAhead = kRowWarps == 1 ? 2 : 8;
@@ -462,7 +464,8 @@ cudaError_t launch_merge_entries(const EntryMergeParams& p, cudaStream_t stream)
 
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
   const long long rows = static_cast<long long>(p.B) * p.rows;
-  const int row_warps = rows >= kMinRowsOneWarp ? 1 : rows >= kMinRows ? 2 : 4;
+  const bool few = p.most_parts > 0 && p.most_parts <= kFewParts;
+  const int row_warps = rows < kMinRows ? 4 : rows >= kMinRowsOneWarp || few ? 1 : 2;
   const int per_block = row_warps == 1 ? RowMerge<1>::kThreads / 32 : row_warps == 2 ? RowMerge<2>::kThreads / 32 : kWarps;
   const long long blocks = (rows * row_warps + per_block - 1) / per_block;
   if (blocks <= 0) return cudaSuccess;
