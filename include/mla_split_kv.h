@@ -702,6 +702,120 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
 uint64_t mla_decode_q8_workspace_bytes(const mla_device_info_t* dev, int32_t q_len, int32_t num_heads);
 
 /*
+ * A step of a serving loop: requests come, go on and go, and a step's new tokens
+ * are packed one request after the other, as many as each has.
+ */
+
+/* Shapes of mla_update_tables. */
+#define MLA_MAX_STEP_REQUESTS 8192
+typedef struct {
+  int32_t num_requests;       /* B, 1..MLA_MAX_STEP_REQUESTS                   */
+  int32_t block_size;         /* tokens per page: 16, 32 or 64                */
+  int32_t num_blocks;         /* pages in the cache pool                      */
+  int32_t max_blocks_per_req; /* row stride of block_table, in entries        */
+  int32_t capacity;           /* places in `slots`, >= 1                      */
+  void* stream;               /* cudaStream_t                                 */
+} mla_step_desc_t;
+
+/*
+ * mla_update_tables -- a step's block tables, slot map and offsets, on the
+ * device, from the requests' lengths and what each gets or gives back. One
+ * launch; may be captured and replayed.
+ *
+ * Request b has L_b = context_lens[b] tokens and changes by n_b = changes[b]
+ * (at least -L_b: what is below counts as that).
+ *  - Shrinking requests (n_b < 0: rejected drafts, finished requests) give the
+ *    pages that they no longer reach back to the stack of free pages,
+ *    free_pages[0 .. *free_count), request after request, each from its lowest
+ *    page up. A page must not be held elsewhere. Their rows of block_table stay
+ *    as they were.
+ *  - Then growing requests take the pages that they lack from the stack's top,
+ *    request after request, each into the next columns of its row, up to the
+ *    first that does not fit: fewer free pages than it lacks, a row too short
+ *    for it, or fewer than n_b places left in `slots`. That one and those
+ *    behind it do not grow. *served: the requests before it (B if all fit).
+ *
+ * context_lens_out: device [B], the lengths after the step
+ * free_count_out  : device [1], pages on the stack after it
+ * q_indptr        : device [B+1], the new tokens of the requests before b
+ * kv_indptr       : device [B+1], the sums of context_lens_out (with shared
+ *                   pages they may pass 2^31 - 1: that is then what is written,
+ *                   and MLA_ERR_DEVICE_CHECK raised)
+ * slots           : device [capacity], of new token q_indptr[b] + i its cache
+ *                   row page * block_size + t % block_size at t = L_b + i; -1
+ *                   behind the last one. A page id outside the pool gives -1
+ *                   and raises MLA_ERR_DEVICE_CHECK.
+ * served          : device [1]
+ * context_lens_out may be context_lens, and free_count_out free_count; no two
+ * other buffers may overlap. free_pages holds num_blocks entries. changes,
+ * context_lens: device [B]; block_table: device [B, max_blocks_per_req].
+ * A programmatic dependent launch, as mla_cache_append. No counterpart on the
+ * pages.
+ */
+mla_status_t mla_update_tables(const int32_t* changes, const int32_t* context_lens, int32_t* context_lens_out,
+                               int32_t* block_table, int32_t* free_pages, const int32_t* free_count,
+                               int32_t* free_count_out, int32_t* q_indptr, int32_t* kv_indptr, int64_t* slots,
+                               int32_t* served, const mla_step_desc_t* desc);
+
+/*
+ * mla_cache_append_slots -- mla_cache_append for packed tokens: token i goes to
+ * cache row slots[i], and nowhere if that is negative. A slot past the pool is
+ * not written and raises MLA_ERR_DEVICE_CHECK. No two tokens of a call may have
+ * the same slot.
+ *
+ * ckv_new : device, token i's 512 16-bit values at i * ckv_stride elements
+ * kpe_new : device, its 64 at i * kpe_stride; both 16-byte aligned, strides
+ *           multiples of 8 of at least 512 and 64 (576 for both: the two parts
+ *           of one projection's output)
+ * slots   : device [num_tokens]
+ * A programmatic dependent launch, as mla_cache_append.
+ */
+mla_status_t mla_cache_append_slots(const void* ckv_new, int64_t ckv_stride, const void* kpe_new, int64_t kpe_stride,
+                                    const int64_t* slots, int64_t num_tokens, int32_t block_size, int32_t num_blocks,
+                                    void* ckv_cache, void* kpe_cache, void* stream);
+
+/* Shapes of mla_expand_kv. */
+#define MLA_NOPE_DIM 128 /* key columns of a head without rotation */
+#define MLA_V_HEAD_DIM 128
+typedef struct {
+  int32_t num_requests;       /* B >= 1                                       */
+  int32_t num_heads;          /* H, 1..256                                    */
+  int32_t block_size;         /* tokens per page: 16, 32 or 64                */
+  int32_t num_blocks;         /* pages in the cache pool                      */
+  int32_t max_blocks_per_req; /* row stride of block_table, in entries        */
+  int32_t dtype;              /* MLA_F16 or MLA_BF16: caches, weights, outputs */
+  int32_t max_tokens;         /* rows that the outputs hold, >= 1             */
+  void* stream;               /* cudaStream_t                                 */
+} mla_expand_desc_t;
+
+/*
+ * mla_expand_kv -- keys and values of every head from the latents of cached
+ * tokens (the expanded form, what mla_prefill reads): request b's first
+ * kv_indptr[b+1] - kv_indptr[b] tokens go to the packed rows from kv_indptr[b]
+ * on. For the token t in row s, head h:
+ *   k_nope[s, h, :] = W_UK[h] . ckv[t, :],   v[s, h, :] = W_UV^T[h]^T . ckv[t, :]
+ * in fp32, rounded once to `dtype` (with fp16, values past 65504 become
+ * infinite), and k_pe[s, :] = kpe[t, :].
+ *
+ * w_uk    : device [H, 128, 512] of `dtype` (as it folds into q_absorbed =
+ *           q_nope . W_UK[h]), 16-byte aligned
+ * w_uv_t  : device [H, 512, 128] of `dtype` (as mla_decode_unembed's),
+ *           16-byte aligned
+ * kv_indptr: device [B+1] int32, non-decreasing from 0 on. Rows of the outputs
+ *           behind the last token stay as they were; tokens past max_tokens are
+ *           left out and raise MLA_ERR_DEVICE_CHECK.
+ * k_nope, v: device [max_tokens, H, 128] of `dtype`, 32-byte aligned (written)
+ * k_pe    : device [max_tokens, 64] of `dtype`, 16-byte aligned (written)
+ * Caches and block_table: as for mla_decode_partial, 16-bit caches only (a page
+ * outside the pool or the table row reads zeros and raises
+ * MLA_ERR_DEVICE_CHECK). A programmatic dependent launch. Counterpart of
+ * kv_b_proj in an expanded layer call; the pages describe the absorbed form only.
+ */
+mla_status_t mla_expand_kv(const void* ckv_cache, const void* kpe_cache, const int32_t* block_table,
+                           const int32_t* kv_indptr, const void* w_uk, const void* w_uv_t, void* k_nope, void* v,
+                           void* k_pe, const mla_expand_desc_t* desc);
+
+/*
  * mla_check_device_errors -- synchronize `stream`, read and clear the device
  * error word the kernels set (bit 0: a bounded wait timed out; bit 1: a page
  * id outside the pool; bit 2: a kernel found its launch unusable -- the
@@ -750,7 +864,9 @@ mla_status_t mla_selfcheck(float* max_abs_err);
 #define MLA_CTR_DECODE_FUSED 5 /* mla_decode calls that ran as one launch */
 #define MLA_CTR_WRAP 6 /* mla_cache_append(_q8), mla_merge_unembed and mla_decode_unembed unembed launches */
 #define MLA_CTR_DECODE_Q8 7 /* mla_decode_q8 calls */
-#define MLA_NUM_COUNTERS 8
+#define MLA_CTR_STEP 8 /* mla_update_tables and mla_cache_append_slots launches */
+#define MLA_CTR_PREFILL 9 /* mla_expand_kv and mla_prefill calls */
+#define MLA_NUM_COUNTERS 10
 /* mla_get_counters -- copy min(n, MLA_NUM_COUNTERS) counters to out (host). */
 void mla_get_counters(uint64_t* out, int32_t n);
 void mla_reset_counters(void);

@@ -31,8 +31,8 @@ MLA_MERGE_ENTRIES, MLA_MERGE_PARTIALS = 0, 1
 MLA_DECODE_MERGE_ENTRIES, MLA_DECODE_MERGE_TICKETS = 0, 1
 MLA_SCORE_EXCHANGE_EXACT, MLA_SCORE_EXCHANGE_F16, MLA_SCORE_EXCHANGE_NONE, MLA_SCORE_EXCHANGE_F32 = 0, 1, 2, 3
 
-CTR_PARTIAL_SIMT, CTR_PARTIAL_TC, CTR_MERGE, CTR_REJECTED, CTR_CTAS, CTR_DECODE_FUSED, CTR_WRAP, CTR_DECODE_Q8 = range(8)
-NUM_COUNTERS = 8
+CTR_PARTIAL_SIMT, CTR_PARTIAL_TC, CTR_MERGE, CTR_REJECTED, CTR_CTAS, CTR_DECODE_FUSED, CTR_WRAP, CTR_DECODE_Q8, CTR_STEP, CTR_PREFILL = range(10)
+NUM_COUNTERS = 10
 
 DTYPE_CODES = {"f16": MLA_F16, "bf16": MLA_BF16, "f32": MLA_F32, "e4m3": MLA_E4M3}
 
@@ -114,6 +114,30 @@ class mla_q8_desc_t(ctypes.Structure):
     ]
 
 
+class mla_step_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("num_requests", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("max_blocks_per_req", ctypes.c_int32),
+        ("capacity", ctypes.c_int32),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class mla_expand_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("num_requests", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("max_blocks_per_req", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("max_tokens", ctypes.c_int32),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -155,6 +179,13 @@ def load() -> ctypes.CDLL:
     lib.mla_decode_q8.restype = i32
     lib.mla_decode_q8_workspace_bytes.argtypes = [ctypes.POINTER(mla_device_info_t), i32, i32]
     lib.mla_decode_q8_workspace_bytes.restype = u64
+    lib.mla_update_tables.argtypes = [vp] * 11 + [ctypes.POINTER(mla_step_desc_t)]
+    lib.mla_update_tables.restype = i32
+    i64 = ctypes.c_int64
+    lib.mla_cache_append_slots.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, vp, vp, vp]
+    lib.mla_cache_append_slots.restype = i32
+    lib.mla_expand_kv.argtypes = [vp] * 9 + [ctypes.POINTER(mla_expand_desc_t)]
+    lib.mla_expand_kv.restype = i32
     lib.mla_merge_unembed.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp]
     lib.mla_merge_unembed.restype = i32
     lib.mla_decode_unembed.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, vp, vp, vp, vp, i32, i32, vp, i32,
@@ -343,6 +374,26 @@ def mla_decode_q8(q_absorbed: int, q_pe: int, ckv_cache: int, kpe_cache: int, sc
 
 def mla_decode_q8_workspace_bytes(dev: mla_device_info_t, q_len: int, num_heads: int) -> int:
     return int(load().mla_decode_q8_workspace_bytes(ctypes.byref(dev), q_len, num_heads))
+
+
+def mla_update_tables(changes: int, context_lens: int, context_lens_out: int, block_table: int, free_pages: int,
+                      free_count: int, free_count_out: int, q_indptr: int, kv_indptr: int, slots: int, served: int,
+                      desc: mla_step_desc_t) -> None:
+    _check(load().mla_update_tables(changes, context_lens, context_lens_out, block_table, free_pages, free_count,
+                                    free_count_out, q_indptr, kv_indptr, slots, served, desc), "mla_update_tables")
+
+
+def mla_cache_append_slots(ckv_new: int, ckv_stride: int, kpe_new: int, kpe_stride: int, slots: int, num_tokens: int,
+                           block_size: int, num_blocks: int, ckv_cache: int, kpe_cache: int,
+                           stream: Optional[int]) -> None:
+    _check(load().mla_cache_append_slots(ckv_new, ckv_stride, kpe_new, kpe_stride, slots, num_tokens, block_size,
+                                         num_blocks, ckv_cache, kpe_cache, stream or None), "mla_cache_append_slots")
+
+
+def mla_expand_kv(ckv_cache: int, kpe_cache: int, block_table: int, kv_indptr: int, w_uk: int, w_uv_t: int,
+                  k_nope: int, v: int, k_pe: int, desc: mla_expand_desc_t) -> None:
+    _check(load().mla_expand_kv(ckv_cache, kpe_cache, block_table, kv_indptr, w_uk, w_uv_t, k_nope, v, k_pe, desc),
+           "mla_expand_kv")
 
 
 def mla_merge_unembed(partials: int, lse: int, o_indptr: int, B: int, q_len: int, num_heads: int, w_uv_t: int,

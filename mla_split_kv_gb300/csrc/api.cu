@@ -196,6 +196,29 @@ int default_cluster(int64_t grid_yz) {
 
 }  // namespace
 
+namespace mla {
+void count_launch(int counter, uint64_t n) { g_counters[counter].fetch_add(n, std::memory_order_relaxed); }
+int32_t rejected(int32_t status) { return reject(static_cast<mla_status_t>(status)); }
+uint64_t wait_timeout_ns() { return g_timeout_ns.load(std::memory_order_relaxed); }
+bool is_aligned(const void* p, uintptr_t a) { return aligned(p, a); }
+bool encode_map16(CUtensorMap* out, const void* base, bool bf16, int rank, const uint64_t* dims,
+                  const uint64_t* strides, const uint32_t* box) {
+  const EncodeTiledFn enc = encoder();
+  if (enc == nullptr || rank < 2 || rank > 4) return false;
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i > 0) st[i - 1] = strides[i - 1];
+  }
+  std::memset(out, 0, sizeof(*out));
+  return enc(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+             const_cast<void*>(base), d, st, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace mla
+
 extern "C" {
 
 mla_status_t mla_device_query(int32_t device, mla_device_info_t* info) {
@@ -1003,13 +1026,14 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
 
 mla_status_t mla_check_device_errors(void* stream, uint32_t* code_out) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
-  uint32_t a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, h = 0, k = 0;
+  uint32_t a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, h = 0, k = 0, l = 0, m = 0;
   if (mla::simt_read_clear_error(&a) != cudaSuccess || mla::tc_read_clear_error(&b) != cudaSuccess ||
       mla::tc128_read_clear_error(&c) != cudaSuccess || mla::mh_read_clear_error(&e) != cudaSuccess ||
       mla::wrap_read_clear_error(&f) != cudaSuccess || mla::mh_nx_read_clear_error(&g) != cudaSuccess ||
-      mla::append_q8_read_clear_error(&h) != cudaSuccess || mla::decode_q8_read_clear_error(&k) != cudaSuccess)
+      mla::append_q8_read_clear_error(&h) != cudaSuccess || mla::decode_q8_read_clear_error(&k) != cudaSuccess ||
+      mla::step_tables_read_clear_error(&l) != cudaSuccess || mla::expand_read_clear_error(&m) != cudaSuccess)
     return MLA_ERR_CUDA;
-  const uint32_t code = a | b | c | e | f | g | h | k;
+  const uint32_t code = a | b | c | e | f | g | h | k | l | m;
   if (code_out != nullptr) *code_out = code;
   if (code != 0 && !clear_static_workspace()) return MLA_ERR_CUDA;
   if (code & mla::MLA_DEVERR_TIMEOUT) return MLA_ERR_TIMEOUT;

@@ -1,0 +1,150 @@
+// C ABI entry points of a serving step and its prompts: argument checks (before any launch) and dispatch.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "mla_split_kv.h"
+
+namespace {
+
+mla_status_t reject(mla_status_t s) { return static_cast<mla_status_t>(mla::rejected(s)); }
+
+bool valid_page(int32_t bs) { return bs == 16 || bs == 32 || bs == 64; }
+
+mla_status_t launched(cudaError_t e, int counter) {
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  mla::count_launch(counter);
+  return MLA_OK;
+}
+
+// A dense [rows, cols] matrix of 16-bit elements in boxes of 64 columns.
+bool rows_map(CUtensorMap* out, const void* base, bool bf16, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  const uint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
+  const uint32_t box[2] = {mla::kBoxCols, box_rows};
+  return mla::encode_map16(out, base, bf16, 2, dims, strides, box);
+}
+
+int current_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return sms;
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status_t mla_update_tables(const int32_t* changes, const int32_t* context_lens, int32_t* context_lens_out,
+                               int32_t* block_table, int32_t* free_pages, const int32_t* free_count,
+                               int32_t* free_count_out, int32_t* q_indptr, int32_t* kv_indptr, int64_t* slots,
+                               int32_t* served, const mla_step_desc_t* d) {
+  if (d == nullptr || changes == nullptr || context_lens == nullptr || context_lens_out == nullptr ||
+      block_table == nullptr || free_pages == nullptr || free_count == nullptr || free_count_out == nullptr ||
+      q_indptr == nullptr || kv_indptr == nullptr || slots == nullptr || served == nullptr)
+    return reject(MLA_ERR_INVALID_ARG);
+  if (d->num_requests < 1 || d->num_blocks < 1 || d->max_blocks_per_req < 1 || d->capacity < 1)
+    return reject(MLA_ERR_INVALID_ARG);
+  if (d->num_requests > MLA_MAX_STEP_REQUESTS || !valid_page(d->block_size)) return reject(MLA_ERR_UNSUPPORTED);
+  const int32_t* const words[] = {changes, context_lens, context_lens_out, block_table, free_pages, free_count,
+                                  free_count_out, q_indptr, kv_indptr, served};
+  for (const int32_t* w : words)
+    if (!mla::is_aligned(w, 4)) return reject(MLA_ERR_INVALID_ARG);
+  if (!mla::is_aligned(slots, 8)) return reject(MLA_ERR_INVALID_ARG);
+  mla::TablesParams p;
+  p.changes = changes;
+  p.lens = context_lens;
+  p.lens_out = context_lens_out;
+  p.block_table = block_table;
+  p.pages = free_pages;
+  p.free_count = free_count;
+  p.free_count_out = free_count_out;
+  p.q_indptr = q_indptr;
+  p.kv_indptr = kv_indptr;
+  p.slots = slots;
+  p.served = served;
+  p.B = d->num_requests;
+  p.bs = d->block_size;
+  p.bs_shift = d->block_size == 16 ? 4 : d->block_size == 32 ? 5 : 6;
+  p.num_blocks = d->num_blocks;
+  p.max_blocks = d->max_blocks_per_req;
+  p.capacity = d->capacity;
+  return launched(mla::launch_update_tables(p, static_cast<cudaStream_t>(d->stream)), MLA_CTR_STEP);
+}
+
+mla_status_t mla_cache_append_slots(const void* ckv_new, int64_t ckv_stride, const void* kpe_new, int64_t kpe_stride,
+                                    const int64_t* slots, int64_t num_tokens, int32_t block_size, int32_t num_blocks,
+                                    void* ckv_cache, void* kpe_cache, void* stream) {
+  if (ckv_new == nullptr || kpe_new == nullptr || slots == nullptr || ckv_cache == nullptr || kpe_cache == nullptr)
+    return reject(MLA_ERR_INVALID_ARG);
+  if (num_tokens < 1 || num_tokens > 0x7fffffffll || num_blocks < 1) return reject(MLA_ERR_INVALID_ARG);
+  if (!valid_page(block_size)) return reject(MLA_ERR_UNSUPPORTED);
+  if (ckv_stride < mla::kRank || kpe_stride < mla::kRope || ckv_stride % 8 != 0 || kpe_stride % 8 != 0)
+    return reject(MLA_ERR_INVALID_ARG);
+  if (!mla::is_aligned(ckv_new, 16) || !mla::is_aligned(kpe_new, 16) || !mla::is_aligned(ckv_cache, 16) ||
+      !mla::is_aligned(kpe_cache, 16) || !mla::is_aligned(slots, 8))
+    return reject(MLA_ERR_INVALID_ARG);
+  mla::AppendSlotsParams p;
+  p.ckv_new = static_cast<const uint16_t*>(ckv_new);
+  p.kpe_new = static_cast<const uint16_t*>(kpe_new);
+  p.slots = slots;
+  p.ckv = static_cast<uint16_t*>(ckv_cache);
+  p.kpe = static_cast<uint16_t*>(kpe_cache);
+  p.ckv_stride = ckv_stride;
+  p.kpe_stride = kpe_stride;
+  p.tokens = num_tokens;
+  p.rows = static_cast<int64_t>(num_blocks) * block_size;
+  return launched(mla::launch_append_slots(p, static_cast<cudaStream_t>(stream)), MLA_CTR_STEP);
+}
+
+mla_status_t mla_expand_kv(const void* ckv_cache, const void* kpe_cache, const int32_t* block_table,
+                           const int32_t* kv_indptr, const void* w_uk, const void* w_uv_t, void* k_nope, void* v,
+                           void* k_pe, const mla_expand_desc_t* d) {
+  if (d == nullptr || ckv_cache == nullptr || kpe_cache == nullptr || block_table == nullptr || kv_indptr == nullptr ||
+      w_uk == nullptr || w_uv_t == nullptr || k_nope == nullptr || v == nullptr || k_pe == nullptr)
+    return reject(MLA_ERR_INVALID_ARG);
+  if (d->num_requests < 1 || d->num_blocks < 1 || d->max_blocks_per_req < 1 || d->max_tokens < 1)
+    return reject(MLA_ERR_INVALID_ARG);
+  if (d->num_heads < 1 || d->num_heads > 256 || !valid_page(d->block_size)) return reject(MLA_ERR_UNSUPPORTED);
+  if (d->dtype != MLA_F16 && d->dtype != MLA_BF16) return reject(MLA_ERR_UNSUPPORTED);
+  if (!mla::is_aligned(ckv_cache, 16) || !mla::is_aligned(kpe_cache, 16) || !mla::is_aligned(w_uk, 16) ||
+      !mla::is_aligned(w_uv_t, 16) || !mla::is_aligned(k_nope, 32) || !mla::is_aligned(v, 32) ||
+      !mla::is_aligned(k_pe, 16) || !mla::is_aligned(block_table, 4) || !mla::is_aligned(kv_indptr, 4))
+    return reject(MLA_ERR_INVALID_ARG);
+  const uint64_t rows = static_cast<uint64_t>(d->num_blocks) * static_cast<uint64_t>(d->block_size);
+  if (rows > 0x7fffffffull) return reject(MLA_ERR_UNSUPPORTED);
+  const bool bf16 = d->dtype == MLA_BF16;
+  const int sms = current_sms();
+  CUtensorMap tm_ckv, tm_uk, tm_uv;
+  if (sms < 2 || !rows_map(&tm_ckv, ckv_cache, bf16, rows, mla::kRank, d->block_size) ||
+      !rows_map(&tm_uk, w_uk, bf16, static_cast<uint64_t>(d->num_heads) * MLA_NOPE_DIM, mla::kRank, mla::kBoxCols) ||
+      !rows_map(&tm_uv, w_uv_t, bf16, static_cast<uint64_t>(d->num_heads) * mla::kRank, MLA_V_HEAD_DIM, mla::kBoxCols))
+    return reject(MLA_ERR_CUDA);
+  mla::ExpandParams p;
+  p.kpe = static_cast<const uint16_t*>(kpe_cache);
+  p.block_table = block_table;
+  p.kv_indptr = kv_indptr;
+  p.k_nope = static_cast<uint16_t*>(k_nope);
+  p.v = static_cast<uint16_t*>(v);
+  p.k_pe = static_cast<uint16_t*>(k_pe);
+  p.B = d->num_requests;
+  p.H = d->num_heads;
+  p.bs = d->block_size;
+  p.max_blocks = d->max_blocks_per_req;
+  p.num_blocks = d->num_blocks;
+  p.max_tokens = d->max_tokens;
+  p.timeout_ns = mla::wait_timeout_ns();
+  return launched(mla::launch_expand_kv(tm_ckv, tm_uk, tm_uv, p, bf16, sms, static_cast<cudaStream_t>(d->stream)),
+                  MLA_CTR_PREFILL);
+}
+
+}  // extern "C"

@@ -207,6 +207,60 @@ cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kp
                              cudaStream_t stream);
 cudaError_t decode_q8_read_clear_error(uint32_t* out);
 
+// A step's tables from the requests' lengths (mla_update_tables).
+constexpr int kMaxStepRequests = 8192;  // MLA_MAX_STEP_REQUESTS
+struct TablesParams {
+  const int32_t* changes;      // [B]
+  const int32_t* lens;         // [B]
+  int32_t* lens_out;           // [B], may be lens
+  int32_t* block_table;        // [B, max_blocks]
+  int32_t* pages;              // [num_blocks], the stack of free ones
+  const int32_t* free_count;   // [1]
+  int32_t* free_count_out;     // [1], may be free_count
+  int32_t* q_indptr;           // [B+1]
+  int32_t* kv_indptr;          // [B+1]
+  int64_t* slots;              // [capacity]
+  int32_t* served;             // [1]
+  int32_t B, bs, bs_shift, num_blocks, max_blocks, capacity;
+};
+cudaError_t launch_update_tables(const TablesParams& p, cudaStream_t stream);
+struct AppendSlotsParams {
+  const uint16_t* ckv_new;
+  const uint16_t* kpe_new;
+  const int64_t* slots;        // [tokens]
+  uint16_t* ckv;               // [rows, 512]
+  uint16_t* kpe;               // [rows, 64]
+  int64_t ckv_stride, kpe_stride, tokens, rows;
+};
+cudaError_t launch_append_slots(const AppendSlotsParams& p, cudaStream_t stream);
+cudaError_t step_tables_read_clear_error(uint32_t* out);
+
+// Keys and values of every head from cached latents (mla_expand_kv): maps of boxes of 64 columns, a page high over the
+// [rows, 512] cache, 64 rows high over w_uk as [H * 128, 512] and w_uv_t as [H * 512, 128], 128-byte swizzle.
+struct ExpandParams {
+  const uint16_t* kpe;         // [num_blocks, bs, 64]
+  const int32_t* block_table;  // [B, max_blocks]
+  const int32_t* kv_indptr;    // [B+1]
+  uint16_t* k_nope;            // [max_tokens, H, 128]
+  uint16_t* v;                 // [max_tokens, H, 128]
+  uint16_t* k_pe;              // [max_tokens, 64]
+  int32_t B, H, bs, max_blocks, num_blocks, max_tokens;
+  uint64_t timeout_ns;
+};
+cudaError_t launch_expand_kv(const CUtensorMap& tm_ckv, const CUtensorMap& tm_uk, const CUtensorMap& tm_uv,
+                             const ExpandParams& p, bool bf16, int sms, cudaStream_t stream);
+cudaError_t expand_read_clear_error(uint32_t* out);
+
+// What the files of entry points share (api.cu).
+void count_launch(int counter, uint64_t n = 1);
+int32_t rejected(int32_t status);  // counts it and gives it back
+uint64_t wait_timeout_ns();
+bool is_aligned(const void* p, uintptr_t a);
+// A map over 16-bit elements: `rank` dimensions innermost first, strides in bytes of all but the innermost, 128-byte
+// swizzle, zeros outside. False where the driver refuses it.
+bool encode_map16(CUtensorMap* out, const void* base, bool bf16, int rank, const uint64_t* dims,
+                  const uint64_t* strides, const uint32_t* box);
+
 // Launchers return cudaSuccess or the launch error. grid.x = cluster of
 // `cluster` CTAs, grid.y = chunks, grid.z = row groups.
 cudaError_t launch_partial_simt(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kpe, const PartialParams& p,

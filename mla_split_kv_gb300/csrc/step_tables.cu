@@ -1,0 +1,331 @@
+// A step's block tables and slot map from the requests' lengths, and the cache write through the slot map, sm_103a.
+//
+// Request b has L_b tokens and gets (or, negative, gives back) n_b. With P(x) = ceil(x / bs) pages for x tokens:
+//  - back_b = P(L_b) - P(L_b + n_b) pages of each shrinking request go onto the stack of free pages, in the
+//    requests' order; top = count + sum back_b;
+//  - take_b = P(L_b + n_b) - P(L_b) pages of each growing request come from the stack's top, in the requests'
+//    order: with T_b = sum over growing requests before b of take, the j-th new page is stack[top - 1 - T_b - j];
+//  - new token i of request b is token t = L_b + i, slot page * bs + t % bs, at place Q_b + i, Q_b the new
+//    tokens of the requests before b.
+// Three exclusive prefix sums over the requests, then independent work per page given back and per new token (a new
+// page's first token is a new token, which writes the page's table entry). A page that another request has just
+// given back is looked up where that request's row still has it (the place on the stack tells which), so no thread
+// waits for another's write. What bounds it is latency: launch, one round of loads, the scans (two barriers each),
+// one search in shared memory, one or two dependent loads. A step of 256 single tokens: see the launch rule.
+//
+// A cluster of one CTA for small steps, of eight (each with scans of its own, cheaper than passing them on) where
+// the slots are many; the cluster's barrier keeps outputs that alias inputs from being written before all have read.
+//
+// mla_cache_append_slots: a copy of 1152 bytes a token, HBM-bound: a warp takes one token of a small step, four of a
+// large one, whose loads are all in flight together.
+#include "device_common.cuh"
+
+namespace mla {
+
+namespace {
+
+constexpr int kFewSlots = 8192;  // up to so many places in `slots`: one CTA
+constexpr int64_t kFewTokens = 8192;  // up to so many tokens: a warp each
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+
+// Exclusive prefix of v over the CTA's threads, and the total.
+__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  long long w = part[lane];  // (kWarps == 32)
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long y = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += y;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  __syncthreads();  // `part` may be written again
+  return x - v + (warp > 0 ? before : 0);
+}
+static_assert(kWarps == 32, "the second level of the scan is one warp");
+
+// The last b of [lo, hi] with at[b] <= i (at non-decreasing, at[lo] <= i).
+__device__ __forceinline__ int find_last(const int32_t* at, int lo, int hi, int32_t i) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (at[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+struct Request {
+  long long len;   // tokens before the step
+  long long base;  // tokens that stay: before the new ones, or after those given back
+  long long next;  // tokens that are asked for
+  long long held, want;  // pages before and after
+  long long back, take, grow;
+};
+
+__device__ __forceinline__ Request request_of(const TablesParams& p, int b) {
+  Request r;
+  const long long len = max(p.lens[b], 0), d = max(static_cast<long long>(p.changes[b]), -len);
+  r.len = len;
+  r.next = len + d;
+  r.base = min(len, r.next);
+  r.held = (len + p.bs - 1) >> p.bs_shift;
+  r.want = (r.next + p.bs - 1) >> p.bs_shift;
+  const long long width = p.max_blocks;
+  r.back = d < 0 ? max(min(r.held, width) - r.want, 0ll) : 0;  // (a row holds no more than its width)
+  r.take = d > 0 ? r.want - r.held : 0;
+  r.grow = d > 0 ? d : 0;
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) mla_update_tables_kernel(const TablesParams p) {
+  extern __shared__ int32_t sh[];
+  __shared__ long long part[kWarps];
+  __shared__ int first_misfit;
+  __shared__ long long misfit_q, misfit_take;
+  const int B = p.B, tid = threadIdx.x;
+  int32_t* const q_at = sh;                // [B + 1] new tokens of the requests before
+  int32_t* const take_at = q_at + B + 1;   // [B] pages taken by them
+  int32_t* const back_at = take_at + B;    // [B + 1] pages given back by them
+  int32_t* const base_of = back_at + B + 1;  // [B]
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid == 0) first_misfit = B;
+
+  const int per = (B + kThreads - 1) / kThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  long long back = 0, take = 0, grow = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = request_of(p, b);
+    back += r.back;
+    take += r.take;
+    grow += r.grow;
+  }
+  const long long count = min(max(*p.free_count, 0), p.num_blocks);
+  long long all_back, all_take, all_grow;
+  back = block_scan(back, part, &all_back);
+  take = block_scan(take, part, &all_take);
+  grow = block_scan(grow, part, &all_grow);
+  // (more than the pool has: a page given back twice)
+  if (tid == 0 && count + all_back > p.num_blocks) flag_error(MLA_DEVERR_BAD_PAGE);
+  const long long top = min(count + all_back, static_cast<long long>(p.num_blocks));
+
+  // the first growing request that does not fit; those from it on do not grow
+  {
+    long long t = take, q = grow;
+    for (int b = b0; b < b1; ++b) {
+      const Request r = request_of(p, b);
+      if (r.grow > 0 && (t + r.take > top || r.want > p.max_blocks || q + r.grow > p.capacity || r.next > 0x7fffffffll)) {
+        atomicMin(&first_misfit, b);
+        break;
+      }
+      t += r.take;
+      q += r.grow;
+    }
+  }
+  __syncthreads();
+  const int served = first_misfit;
+  long long lens = 0;
+  {
+    long long t = take, q = grow, k = back;
+    for (int b = b0; b < b1; ++b) {
+      const Request r = request_of(p, b);
+      if (b == served) {
+        misfit_q = q;
+        misfit_take = t;
+      }
+      if (b <= served) {  // (bounded by the capacity and the pool there)
+        q_at[b] = static_cast<int32_t>(q);
+        take_at[b] = static_cast<int32_t>(t);
+      }
+      back_at[b] = static_cast<int32_t>(min(k, 0x7fffffffll));
+      base_of[b] = static_cast<int32_t>(r.base);
+      lens += r.grow > 0 && b >= served ? r.len : r.next;
+      t += r.take;
+      q += r.grow;
+      k += r.back;
+    }
+  }
+  __syncthreads();
+  const int32_t tokens = static_cast<int32_t>(served < B ? misfit_q : all_grow);
+  const long long taken = served < B ? misfit_take : all_take;
+  for (int b = tid; b < B; b += kThreads)
+    if (b > served) q_at[b] = tokens;
+  if (tid == 0) {
+    q_at[B] = tokens;
+    back_at[B] = static_cast<int32_t>(min(all_back, 0x7fffffffll));
+  }
+  long long all_lens;
+  lens = block_scan(lens, part, &all_lens);  // (its barriers also publish what was written above)
+
+  // every CTA has read its inputs before outputs that may be the same memory are written
+  const int ctas = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+  int32_t keep_len[8];
+  const bool writes = rank == 0;
+  if (writes) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (b0 + j < b1) {
+        const Request r = request_of(p, b0 + j);
+        keep_len[j] = static_cast<int32_t>(r.grow > 0 && b0 + j >= served ? r.len : r.next);
+      }
+    }
+  }
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+  if (writes) {
+    long long s = lens;
+    bool over = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (b0 + j < b1) {
+        const int b = b0 + j;
+        over |= s > 0x7fffffffll;
+        p.lens_out[b] = keep_len[j];
+        p.q_indptr[b] = q_at[b];
+        p.kv_indptr[b] = static_cast<int32_t>(min(s, 0x7fffffffll));
+        s += keep_len[j];
+      }
+    }
+    if (tid == 0) {
+      over |= all_lens > 0x7fffffffll;
+      p.q_indptr[B] = tokens;
+      p.kv_indptr[B] = static_cast<int32_t>(min(all_lens, 0x7fffffffll));
+      *p.free_count_out = static_cast<int32_t>(top - taken);
+      *p.served = served;
+    }
+    if (over) flag_error(MLA_DEVERR_BAD_PAGE);
+  }
+
+  const int shift = p.bs_shift;
+  const int step = ctas * kThreads;
+  const int first = rank * kThreads + tid;
+  bool bad = false;
+  // pages given back: the k-th of the step goes to stack[count + k]
+  for (long long k = first; count + k < top; k += step) {
+    const int b = find_last(back_at, 0, B - 1, static_cast<int32_t>(k));
+    const int col = ((base_of[b] + p.bs - 1) >> shift) + static_cast<int>(k - back_at[b]);
+    p.pages[count + k] = p.block_table[static_cast<long long>(b) * p.max_blocks + col];
+  }
+  // new tokens
+  for (int i = first; i < tokens; i += step) {
+    const int b = find_last(q_at, 0, B - 1, i);
+    const int t = base_of[b] + (i - q_at[b]);
+    const int col = t >> shift, held = static_cast<int>((static_cast<long long>(base_of[b]) + p.bs - 1) >> shift);
+    int32_t* const entry = p.block_table + static_cast<long long>(b) * p.max_blocks + col;
+    int32_t page;
+    if (col < held) {
+      page = *entry;
+    } else {
+      const int at = static_cast<int>(top) - 1 - take_at[b] - (col - held);
+      if (at < count) {
+        page = p.pages[at];
+      } else {  // given back in this step
+        const int k = at - static_cast<int>(count);
+        const int from = find_last(back_at, 0, B - 1, k);
+        const int c = ((base_of[from] + p.bs - 1) >> shift) + (k - back_at[from]);
+        page = p.block_table[static_cast<long long>(from) * p.max_blocks + c];
+      }
+      if ((t & (p.bs - 1)) == 0) *entry = page;
+    }
+    const bool ok = page >= 0 && page < p.num_blocks;
+    bad |= !ok;
+    p.slots[i] = ok ? (static_cast<long long>(page) << shift) + (t & (p.bs - 1)) : -1ll;
+  }
+  for (long long i = static_cast<long long>(tokens) + first; i < p.capacity; i += step) p.slots[i] = -1;
+  if (bad) flag_error(MLA_DEVERR_BAD_PAGE);
+}
+
+constexpr int kCopyWarps = 8;
+
+// kHold tokens a warp. Lane l holds columns 8 l.. and 256 + 8 l.. of each token, and of its rope columns (l < 8).
+template <int kHold>
+__global__ void __launch_bounds__(kCopyWarps * 32) mla_cache_append_slots_kernel(const AppendSlotsParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long tok0 = (static_cast<long long>(blockIdx.x) * kCopyWarps + warp) * kHold;
+  if (tok0 >= p.tokens) return;
+  long long slot[kHold];
+  uint4 c0[kHold], c1[kHold], r[kHold];
+#pragma unroll
+  for (int j = 0; j < kHold; ++j) slot[j] = tok0 + j < p.tokens ? p.slots[tok0 + j] : -1ll;
+#pragma unroll
+  for (int j = 0; j < kHold; ++j) {
+    if (slot[j] < 0) continue;
+    const uint4* const c = reinterpret_cast<const uint4*>(p.ckv_new + (tok0 + j) * p.ckv_stride);
+    c0[j] = c[lane];
+    c1[j] = c[lane + 32];
+    if (lane < 8) r[j] = reinterpret_cast<const uint4*>(p.kpe_new + (tok0 + j) * p.kpe_stride)[lane];
+  }
+#pragma unroll
+  for (int j = 0; j < kHold; ++j) {
+    if (slot[j] < 0) continue;
+    if (slot[j] >= p.rows) {
+      if (lane == 0) flag_error(MLA_DEVERR_BAD_PAGE);
+      continue;
+    }
+    uint4* const c = reinterpret_cast<uint4*>(p.ckv + slot[j] * kRank);
+    c[lane] = c0[j];
+    c[lane + 32] = c1[j];
+    if (lane < 8) reinterpret_cast<uint4*>(p.kpe + slot[j] * kRope)[lane] = r[j];
+  }
+}
+
+template <class Params>
+cudaError_t launch_dependent(void (*kernel)(const Params), unsigned grid, unsigned block, unsigned cluster, size_t smem,
+                             const Params& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_update_tables(const TablesParams& p, cudaStream_t stream) {
+  static DeviceOnce once;
+  const size_t smem = (static_cast<size_t>(p.B) * 4 + 2) * sizeof(int32_t);
+  const cudaError_t e = set_attribute_once(once, reinterpret_cast<const void*>(&mla_update_tables_kernel),
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (kMaxStepRequests * 4 + 2) * static_cast<int>(sizeof(int32_t)));
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = p.capacity > kFewSlots ? 8 : 1;
+  return launch_dependent(mla_update_tables_kernel, ctas, kThreads, ctas, smem, p, stream);
+}
+
+cudaError_t launch_append_slots(const AppendSlotsParams& p, cudaStream_t stream) {
+  const long long warps_per_token = p.tokens > kFewTokens ? 4 : 1;
+  const long long units = (p.tokens + warps_per_token - 1) / warps_per_token;
+  const unsigned grid = static_cast<unsigned>((units + kCopyWarps - 1) / kCopyWarps);
+  return p.tokens > kFewTokens ? launch_dependent(mla_cache_append_slots_kernel<4>, grid, kCopyWarps * 32, 1, 0, p, stream)
+                               : launch_dependent(mla_cache_append_slots_kernel<1>, grid, kCopyWarps * 32, 1, 0, p, stream);
+}
+
+cudaError_t step_tables_read_clear_error(uint32_t* out) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
+}
+
+}  // namespace mla

@@ -492,3 +492,134 @@ def decode_q8(plan: Q8Plan, q_abs: torch.Tensor, q_pe: torch.Tensor, cache: Q8Ca
                      cache.scales.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), scale,
                      out.data_ptr(), out_lse.data_ptr() if out_lse is not None else None, d)
     return out
+
+
+# ---------------------------------------------------------------------------
+# a serving step: tables, slots, packed tokens
+# ---------------------------------------------------------------------------
+
+
+@dataclasses.dataclass
+class PagePool:
+    """The free pages of a cache pool, as a stack on the device: pages[0 .. count), the next one to go last."""
+    pages: torch.Tensor  # int32 [num_blocks]
+    count: torch.Tensor  # int32 [1]
+    block_size: int
+
+    def __post_init__(self):
+        self.num_blocks = int(self.pages.shape[0])
+        dev = self.pages.get_device()
+        _expect(self.pages, (self.num_blocks,), torch.int32, "pages", dev)
+        _expect(self.count, (1,), torch.int32, "count", dev)
+
+
+def alloc_pool(num_blocks: int, block_size: int, device="cuda") -> PagePool:
+    """A pool all of whose pages are free; page 0 goes first."""
+    return PagePool(torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=device),
+                    torch.full((1,), num_blocks, dtype=torch.int32, device=device), block_size)
+
+
+@dataclasses.dataclass
+class Step:
+    """What update_tables writes for one step (see mla_update_tables)."""
+    context_lens: torch.Tensor  # int32 [B], after the step
+    free_count: torch.Tensor    # int32 [1], after the step
+    q_indptr: torch.Tensor      # int32 [B + 1]
+    kv_indptr: torch.Tensor     # int32 [B + 1]
+    slots: torch.Tensor         # int64 [capacity]
+    served: torch.Tensor        # int32 [1]
+
+
+def alloc_step(num_requests: int, capacity: int, device="cuda") -> Step:
+    """Buffers of steps of num_requests requests and at most `capacity` new tokens."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return Step(torch.zeros(num_requests, **i32), torch.zeros(1, **i32), torch.zeros(num_requests + 1, **i32),
+                torch.zeros(num_requests + 1, **i32), torch.zeros(capacity, dtype=torch.int64, device=device),
+                torch.zeros(1, **i32))
+
+
+def update_tables(pool: PagePool, changes: torch.Tensor, context_lens: torch.Tensor, block_table: torch.Tensor,
+                  step: Step, stream: Optional[torch.cuda.Stream] = None) -> Step:
+    """One step's tables (mla_update_tables): block_table and pool.pages in place, the rest into `step`, whose
+    context_lens and free_count are the next step's (they may be the tensors of this one: context_lens itself,
+    pool.count)."""
+    dev = _device_of(pool.pages)
+    B, width, capacity = changes.shape[0], block_table.shape[-1], step.slots.shape[0]
+    _expect(changes, (B,), torch.int32, "changes", dev)
+    _expect(context_lens, (B,), torch.int32, "context_lens", dev)
+    _expect(block_table, (B, width), torch.int32, "block_table", dev)
+    _expect(step.context_lens, (B,), torch.int32, "step.context_lens", dev)
+    _expect(step.free_count, (1,), torch.int32, "step.free_count", dev)
+    _expect(step.q_indptr, (B + 1,), torch.int32, "step.q_indptr", dev)
+    _expect(step.kv_indptr, (B + 1,), torch.int32, "step.kv_indptr", dev)
+    _expect(step.slots, (capacity,), torch.int64, "step.slots", dev)
+    _expect(step.served, (1,), torch.int32, "step.served", dev)
+    raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
+    d = nb.mla_step_desc_t(B, pool.block_size, pool.num_blocks, width, capacity, raw_stream)
+    nb.mla_update_tables(changes.data_ptr(), context_lens.data_ptr(), step.context_lens.data_ptr(),
+                         block_table.data_ptr(), pool.pages.data_ptr(), pool.count.data_ptr(),
+                         step.free_count.data_ptr(), step.q_indptr.data_ptr(), step.kv_indptr.data_ptr(),
+                         step.slots.data_ptr(), step.served.data_ptr(), d)
+    return step
+
+
+def _expect_rows(t: torch.Tensor, shape, dtype, what: str, dev: int) -> None:
+    """Like _expect, with the last dimension dense and any stride between the rows."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what}: expected a {dtype} tensor of shape {shape} with dense rows beside the call's other "
+                         f"buffers, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def cache_append_slots(ckv: torch.Tensor, kpe: torch.Tensor, ckv_new: torch.Tensor, kpe_new: torch.Tensor,
+                       slots: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Write packed tokens [T, 512 / 64] (rows of any stride) into the cache rows that `slots` names
+    (mla_cache_append_slots); T may be less than what slots holds."""
+    dev = _device_of(ckv)
+    nblk, bs, T = ckv.shape[0], ckv.shape[1], ckv_new.shape[0]
+    if ckv.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"ckv: {ckv.dtype}")
+    _expect(ckv, (nblk, bs, 512), ckv.dtype, "ckv", dev)
+    _expect(kpe, (nblk, bs, 64), ckv.dtype, "kpe", dev)
+    _expect_rows(ckv_new, (T, 512), ckv.dtype, "ckv_new", dev)
+    _expect_rows(kpe_new, (T, 64), ckv.dtype, "kpe_new", dev)
+    if slots.dim() != 1 or slots.shape[0] < T:
+        raise ValueError(f"slots: {tuple(slots.shape)} for {T} tokens")
+    _expect(slots, (slots.shape[0],), torch.int64, "slots", dev)
+    raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
+    nb.mla_cache_append_slots(ckv_new.data_ptr(), _row_stride(ckv_new), kpe_new.data_ptr(), _row_stride(kpe_new),
+                              slots.data_ptr(), T, bs, nblk, ckv.data_ptr(), kpe.data_ptr(), raw_stream)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements from row to row (of a single row: its own length, whatever the tensor says)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+# ---------------------------------------------------------------------------
+# prompts: the expanded form
+# ---------------------------------------------------------------------------
+
+
+def expand_kv(ckv: torch.Tensor, kpe: torch.Tensor, block_table: torch.Tensor, kv_indptr: torch.Tensor,
+              w_uk: torch.Tensor, w_uv_t: torch.Tensor, k_nope: torch.Tensor, v: torch.Tensor, k_pe: torch.Tensor,
+              stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Every head's keys and values [S, H, 128] and the rotary keys [S, 64] of the requests' cached tokens, packed by
+    kv_indptr (mla_expand_kv); the outputs may hold more rows than there are tokens."""
+    dev = _device_of(ckv)
+    nblk, bs, width, B, H, S = ckv.shape[0], ckv.shape[1], block_table.shape[-1], kv_indptr.shape[0] - 1, w_uk.shape[0], v.shape[0]
+    dtype = ckv.dtype
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"ckv: {dtype}")
+    _expect(ckv, (nblk, bs, 512), dtype, "ckv", dev)
+    _expect(kpe, (nblk, bs, 64), dtype, "kpe", dev)
+    _expect(block_table, (B, width), torch.int32, "block_table", dev)
+    _expect(kv_indptr, (B + 1,), torch.int32, "kv_indptr", dev)
+    _expect(w_uk, (H, 128, 512), dtype, "w_uk", dev)
+    _expect(w_uv_t, (H, 512, 128), dtype, "w_uv_t", dev)
+    _expect(k_nope, (S, H, 128), dtype, "k_nope", dev)
+    _expect(v, (S, H, 128), dtype, "v", dev)
+    _expect(k_pe, (S, 64), dtype, "k_pe", dev)
+    raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
+    d = nb.mla_expand_desc_t(B, H, bs, nblk, width, CODE_OF[dtype], S, raw_stream)
+    nb.mla_expand_kv(ckv.data_ptr(), kpe.data_ptr(), block_table.data_ptr(), kv_indptr.data_ptr(), w_uk.data_ptr(),
+                     w_uv_t.data_ptr(), k_nope.data_ptr(), v.data_ptr(), k_pe.data_ptr(), d)
