@@ -815,6 +815,67 @@ mla_status_t mla_expand_kv(const void* ckv_cache, const void* kpe_cache, const i
                            const int32_t* kv_indptr, const void* w_uk, const void* w_uv_t, void* k_nope, void* v,
                            void* k_pe, const mla_expand_desc_t* desc);
 
+/* Shapes of mla_prefill. */
+typedef struct {
+  int32_t num_requests;       /* B, 1..MLA_MAX_STEP_REQUESTS                   */
+  int32_t num_heads;          /* H, 1..256                                    */
+  int32_t dtype;              /* MLA_F16 or MLA_BF16: queries, keys, values,
+                                 output                                       */
+  int32_t causal;             /* 1: row i of a request's n sees its tokens
+                                 t <= L - n + i; 0: all L of them             */
+  int32_t max_q_tokens;       /* T: rows that q_nope, q_pe, out hold          */
+  int32_t max_kv_tokens;      /* S: rows that k_nope, k_pe, v hold            */
+  int64_t q_nope_stride[2];   /* elements from row to row and from head to
+                                 head, multiples of 8 (dense: H * 128, 128;
+                                 of one [T, H, 192] tensor: H * 192, 192)     */
+  int64_t q_pe_stride[2];
+  void* workspace;            /* DEVICE, >= mla_prefill_workspace_bytes(...)
+                                 bytes, 256-byte aligned; need not be cleared.
+                                 Calls sharing it must not overlap in time.    */
+  uint64_t workspace_bytes;
+  void* stream;               /* cudaStream_t                                 */
+} mla_prefill_desc_t;
+
+/*
+ * mla_prefill -- attention of prompts over expanded keys and values (as
+ * mla_expand_kv writes them). Request b has n = q_indptr[b+1] - q_indptr[b] rows
+ * (its newest tokens) and L = kv_indptr[b+1] - kv_indptr[b] tokens, both packed
+ * request after request. For row i of a request and head h:
+ *   s_t  = scale * (q_nope[i,h,:] . k_nope[t,h,:] + q_pe[i,h,:] . k_pe[t,:])
+ *   out[i,h,:]   = sum_t softmax(s)_t v[t,h,:]     (rounded once)
+ *   out_lse[i,h] = log2 sum_t exp(s_t)
+ * over the tokens that the row sees. A row that sees none (n > L) gives 0 and
+ * -inf. Tokens that a row does not see do not reach it, NaN and infinities
+ * among them or not; nor does what the tensors hold behind the last request.
+ * Rows of out and out_lse behind the last request stay as they were.
+ *
+ * The work is shared out on the device from the offsets as they are when the
+ * call runs: no host plan, and a captured call may be replayed with others (the
+ * same T, S and B). The same bits on every call with the same offsets. Offsets
+ * that go back or pass T or S are cut off there and raise
+ * MLA_ERR_DEVICE_CHECK.
+ *
+ * Precision: scores, maxima, sums and out_lse are fp32, the weights of the value
+ * product are rounded once to `dtype` (half a step: 2^-12 of themselves in fp16,
+ * where the smallest count as at least 2^-33 of the row's greatest, 2^-9 in
+ * bf16) and the sum that normalizes takes them unrounded.
+ *
+ * q_nope : device, row i, head h at i * q_nope_stride[0] + h * q_nope_stride[1]
+ *          elements, 128 of them; q_pe alike, 64; both 16-byte aligned
+ * k_nope, v: device [S, H, 128], k_pe: device [S, 64], 16-byte aligned
+ * out    : device [T, H, 128], 32-byte aligned
+ * out_lse: device [T, H] fp32, or NULL
+ * Programmatic dependent launches.
+ */
+mla_status_t mla_prefill(const void* q_nope, const void* q_pe, const void* k_nope, const void* k_pe, const void* v,
+                         const int32_t* q_indptr, const int32_t* kv_indptr, float scale, void* out, float* out_lse,
+                         const mla_prefill_desc_t* desc);
+
+/* Workspace bytes of mla_prefill on `dev` (its num_sms) for calls of this shape.
+ * 0 for bad arguments. */
+uint64_t mla_prefill_workspace_bytes(const mla_device_info_t* dev, int32_t num_requests, int32_t num_heads,
+                                     int32_t max_q_tokens);
+
 /*
  * mla_check_device_errors -- synchronize `stream`, read and clear the device
  * error word the kernels set (bit 0: a bounded wait timed out; bit 1: a page

@@ -138,6 +138,22 @@ class mla_expand_desc_t(ctypes.Structure):
     ]
 
 
+class mla_prefill_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("num_requests", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("max_q_tokens", ctypes.c_int32),
+        ("max_kv_tokens", ctypes.c_int32),
+        ("q_nope_stride", ctypes.c_int64 * 2),
+        ("q_pe_stride", ctypes.c_int64 * 2),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_uint64),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -186,6 +202,10 @@ def load() -> ctypes.CDLL:
     lib.mla_cache_append_slots.restype = i32
     lib.mla_expand_kv.argtypes = [vp] * 9 + [ctypes.POINTER(mla_expand_desc_t)]
     lib.mla_expand_kv.restype = i32
+    lib.mla_prefill.argtypes = [vp] * 7 + [f32, vp, vp, ctypes.POINTER(mla_prefill_desc_t)]
+    lib.mla_prefill.restype = i32
+    lib.mla_prefill_workspace_bytes.argtypes = [ctypes.POINTER(mla_device_info_t), i32, i32, i32]
+    lib.mla_prefill_workspace_bytes.restype = u64
     lib.mla_merge_unembed.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp]
     lib.mla_merge_unembed.restype = i32
     lib.mla_decode_unembed.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, vp, vp, vp, vp, i32, i32, vp, i32,
@@ -394,6 +414,16 @@ def mla_expand_kv(ckv_cache: int, kpe_cache: int, block_table: int, kv_indptr: i
                   k_nope: int, v: int, k_pe: int, desc: mla_expand_desc_t) -> None:
     _check(load().mla_expand_kv(ckv_cache, kpe_cache, block_table, kv_indptr, w_uk, w_uv_t, k_nope, v, k_pe, desc),
            "mla_expand_kv")
+
+
+def mla_prefill(q_nope: int, q_pe: int, k_nope: int, k_pe: int, v: int, q_indptr: int, kv_indptr: int, scale: float,
+                out: int, out_lse: Optional[int], desc: mla_prefill_desc_t) -> None:
+    _check(load().mla_prefill(q_nope, q_pe, k_nope, k_pe, v, q_indptr, kv_indptr, scale, out, out_lse or None, desc),
+           "mla_prefill")
+
+
+def mla_prefill_workspace_bytes(dev: mla_device_info_t, num_requests: int, num_heads: int, max_q_tokens: int) -> int:
+    return int(load().mla_prefill_workspace_bytes(ctypes.byref(dev), num_requests, num_heads, max_q_tokens))
 
 
 def mla_merge_unembed(partials: int, lse: int, o_indptr: int, B: int, q_len: int, num_heads: int, w_uv_t: int,

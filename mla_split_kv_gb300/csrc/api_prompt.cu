@@ -30,6 +30,35 @@ bool rows_map(CUtensorMap* out, const void* base, bool bf16, uint64_t rows, uint
   return mla::encode_map16(out, base, bf16, 2, dims, strides, box);
 }
 
+// Boxes of 64 columns of one head, `box_rows` rows high, of a [rows, H, cols] tensor.
+bool heads_map(CUtensorMap* out, const void* base, bool bf16, uint64_t rows, uint64_t H, uint64_t cols,
+               int64_t row_stride, int64_t head_stride, uint32_t box_rows) {
+  const uint64_t dims[3] = {cols, H, rows};
+  const uint64_t strides[2] = {static_cast<uint64_t>(head_stride) * 2, static_cast<uint64_t>(row_stride) * 2};
+  const uint32_t box[3] = {mla::kBoxCols, 1, box_rows};
+  return mla::encode_map16(out, base, bf16, 3, dims, strides, box);
+}
+
+// mla_prefill's workspace: the plan's counts and lists, then the cut runs' pieces.
+struct PrefillSpace {
+  uint64_t items, merge, part_o, part_lse, bytes;
+  int max_items, max_slots, max_tiles;
+};
+PrefillSpace prefill_space(int32_t B, int32_t H, int32_t T, int sms) {
+  auto round256 = [](uint64_t x) { return (x + 255) / 256 * 256; };
+  PrefillSpace w;
+  w.max_slots = mla::prefill_max_slots(H, sms);
+  w.max_tiles = mla::prefill_max_tiles(B, T);
+  w.max_items = w.max_tiles + w.max_slots;
+  const uint64_t rows = static_cast<uint64_t>(w.max_slots) * 256 * H;
+  w.items = 256;
+  w.merge = w.items + round256(static_cast<uint64_t>(w.max_items) * 32);
+  w.part_o = w.merge + round256(static_cast<uint64_t>(w.max_slots) * 16);
+  w.part_lse = w.part_o + rows * MLA_V_HEAD_DIM * 4;
+  w.bytes = w.part_lse + rows * 4;
+  return w;
+}
+
 int current_sms() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -145,6 +174,88 @@ mla_status_t mla_expand_kv(const void* ckv_cache, const void* kpe_cache, const i
   p.timeout_ns = mla::wait_timeout_ns();
   return launched(mla::launch_expand_kv(tm_ckv, tm_uk, tm_uv, p, bf16, sms, static_cast<cudaStream_t>(d->stream)),
                   MLA_CTR_PREFILL);
+}
+
+uint64_t mla_prefill_workspace_bytes(const mla_device_info_t* dev, int32_t num_requests, int32_t num_heads,
+                                     int32_t max_q_tokens) {
+  if (dev == nullptr || dev->num_sms < 1 || num_requests < 1 || num_requests > MLA_MAX_STEP_REQUESTS || num_heads < 1 ||
+      num_heads > 256 || max_q_tokens < 1)
+    return 0;
+  return prefill_space(num_requests, num_heads, max_q_tokens, dev->num_sms).bytes;
+}
+
+mla_status_t mla_prefill(const void* q_nope, const void* q_pe, const void* k_nope, const void* k_pe, const void* v,
+                         const int32_t* q_indptr, const int32_t* kv_indptr, float scale, void* out, float* out_lse,
+                         const mla_prefill_desc_t* d) {
+  if (d == nullptr || q_nope == nullptr || q_pe == nullptr || k_nope == nullptr || k_pe == nullptr || v == nullptr ||
+      q_indptr == nullptr || kv_indptr == nullptr || out == nullptr)
+    return reject(MLA_ERR_INVALID_ARG);
+  if (d->num_requests < 1 || d->max_q_tokens < 1 || d->max_kv_tokens < 1 || (d->causal != 0 && d->causal != 1) ||
+      !std::isfinite(scale))
+    return reject(MLA_ERR_INVALID_ARG);
+  if (d->num_requests > MLA_MAX_STEP_REQUESTS || d->num_heads < 1 || d->num_heads > 256)
+    return reject(MLA_ERR_UNSUPPORTED);
+  if (d->dtype != MLA_F16 && d->dtype != MLA_BF16) return reject(MLA_ERR_UNSUPPORTED);
+  // work items are counted, and positions held, in 31 bits
+  if (d->max_kv_tokens > 0x7fffffff - 256 ||
+      (static_cast<int64_t>(mla::prefill_max_tiles(d->num_requests, d->max_q_tokens)) + 1024) * d->num_heads > 0x3fffffff)
+    return reject(MLA_ERR_UNSUPPORTED);
+  const int64_t* const strides[2] = {d->q_nope_stride, d->q_pe_stride};
+  const int64_t least[2] = {MLA_NOPE_DIM, mla::kRope};
+  for (int k = 0; k < 2; ++k)
+    for (int j = 0; j < 2; ++j)
+      if (strides[k][j] < least[k] || strides[k][j] % 8 != 0 || strides[k][j] >= (1ll << 38))
+        return reject(MLA_ERR_INVALID_ARG);
+  if (!mla::is_aligned(q_nope, 16) || !mla::is_aligned(q_pe, 16) || !mla::is_aligned(k_nope, 16) ||
+      !mla::is_aligned(k_pe, 16) || !mla::is_aligned(v, 16) || !mla::is_aligned(q_indptr, 4) ||
+      !mla::is_aligned(kv_indptr, 4) || !mla::is_aligned(out, 32) || (out_lse != nullptr && !mla::is_aligned(out_lse, 4)))
+    return reject(MLA_ERR_INVALID_ARG);
+  const int sms = current_sms();
+  if (sms < 1) return reject(MLA_ERR_CUDA);
+  const int B = d->num_requests, H = d->num_heads, T = d->max_q_tokens, S = d->max_kv_tokens;
+  const PrefillSpace space = prefill_space(B, H, T, sms);
+  if (d->workspace == nullptr || !mla::is_aligned(d->workspace, 256) || d->workspace_bytes < space.bytes)
+    return reject(MLA_ERR_INVALID_ARG);
+  const bool bf16 = d->dtype == MLA_BF16;
+  mla::PrefillMaps maps;
+  const uint64_t dims[2] = {static_cast<uint64_t>(mla::kRope), static_cast<uint64_t>(S)}, pitch[1] = {mla::kRope * 2};
+  const uint32_t box[2] = {mla::kBoxCols, 128};
+  const int64_t dense = static_cast<int64_t>(H) * MLA_V_HEAD_DIM;
+  if (!heads_map(&maps.q, q_nope, bf16, T, H, MLA_NOPE_DIM, d->q_nope_stride[0], d->q_nope_stride[1], 128) ||
+      !heads_map(&maps.qpe, q_pe, bf16, T, H, mla::kRope, d->q_pe_stride[0], d->q_pe_stride[1], 128) ||
+      !heads_map(&maps.k, k_nope, bf16, S, H, MLA_NOPE_DIM, dense, MLA_NOPE_DIM, 128) ||
+      !heads_map(&maps.v, v, bf16, S, H, MLA_V_HEAD_DIM, dense, MLA_V_HEAD_DIM, 64) ||
+      !mla::encode_map16(&maps.kpe, k_pe, bf16, 2, dims, pitch, box))
+    return reject(MLA_ERR_CUDA);
+  uint8_t* const ws = static_cast<uint8_t*>(d->workspace);
+  mla::PrefillPlanParams pl;
+  pl.num_items = reinterpret_cast<int32_t*>(ws);
+  pl.num_merges = pl.num_items + 1;
+  pl.items = reinterpret_cast<int32_t*>(ws + space.items);
+  pl.merge = reinterpret_cast<int4*>(ws + space.merge);
+  pl.max_items = space.max_items;
+  pl.max_slots = space.max_slots;
+  pl.max_tiles = space.max_tiles;
+  pl.sms = sms;
+  mla::PrefillParams p;
+  p.q_indptr = q_indptr;
+  p.kv_indptr = kv_indptr;
+  p.v = static_cast<const uint16_t*>(v);
+  p.out = out;
+  p.out_lse = out_lse;
+  p.items = mla::prefill_direct(B, T, S) ? nullptr : pl.items;
+  p.num_items = pl.num_items;
+  p.part_o = reinterpret_cast<float*>(ws + space.part_o);
+  p.part_lse = reinterpret_cast<float*>(ws + space.part_lse);
+  p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
+  p.negate = scale < 0 ? 1 : 0;
+  p.B = B;
+  p.H = H;
+  p.T = T;
+  p.S = S;
+  p.causal = d->causal;
+  p.timeout_ns = mla::wait_timeout_ns();
+  return launched(mla::launch_prefill(maps, p, pl, bf16, sms, static_cast<cudaStream_t>(d->stream)), MLA_CTR_PREFILL);
 }
 
 }  // extern "C"

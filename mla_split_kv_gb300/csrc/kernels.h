@@ -251,6 +251,40 @@ cudaError_t launch_expand_kv(const CUtensorMap& tm_ckv, const CUtensorMap& tm_uk
                              const ExpandParams& p, bool bf16, int sms, cudaStream_t stream);
 cudaError_t expand_read_clear_error(uint32_t* out);
 
+// Attention of prompts (mla_prefill). The maps, 128-byte swizzle, 64 columns a box: q and qpe [T, H, 128 / 64] and k [S,
+// H, 128] with boxes of 128 rows of one head, kpe [S, 64] of 128 rows, v [S, H, 128] of 64 rows of one head.
+struct PrefillMaps {
+  CUtensorMap q, qpe, k, kpe, v;
+};
+struct PrefillParams {
+  const int32_t* q_indptr;     // [B+1]
+  const int32_t* kv_indptr;    // [B+1]
+  const uint16_t* v;           // [S, H, 128]
+  void* out;                   // [T, H, 128]
+  float* out_lse;              // [T, H] or null
+  const int32_t* items;        // the plan's list, eight words an item, or null: planned in the kernel
+  const int32_t* num_items;
+  float* part_o;               // [slots, 256, H, 128]
+  float* part_lse;             // [slots, 256, H]
+  float scale_log2;            // |softmax scale| * log2(e)
+  int32_t negate;              // the scale is negative
+  int32_t B, H, T, S, causal;
+  uint64_t timeout_ns;
+};
+struct PrefillPlanParams {
+  int32_t* items;
+  int32_t* num_items;
+  int32_t* num_merges;
+  int4* merge;                 // {first row of out, rows, first slot, pieces}
+  int32_t max_items, max_slots, max_tiles, sms;
+};
+int prefill_max_slots(int H, int sms);
+int prefill_max_tiles(int B, int T);
+bool prefill_direct(int B, int T, int S);
+cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, const PrefillPlanParams& pl, bool bf16,
+                           int sms, cudaStream_t stream);
+cudaError_t prefill_read_clear_error(uint32_t* out);
+
 // What the files of entry points share (api.cu).
 void count_launch(int counter, uint64_t n = 1);
 int32_t rejected(int32_t status);  // counts it and gives it back

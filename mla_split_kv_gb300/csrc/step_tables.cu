@@ -18,6 +18,7 @@
 //
 // mla_cache_append_slots: a copy of 1152 bytes a token, HBM-bound: a warp takes one token of a small step, four of a
 // large one, whose loads are all in flight together.
+#include "block_scan.cuh"
 #include "device_common.cuh"
 
 namespace mla {
@@ -27,41 +28,7 @@ namespace {
 constexpr int kFewSlots = 8192;  // up to so many places in `slots`: one CTA
 constexpr int64_t kFewTokens = 8192;  // up to so many tokens: a warp each
 constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-
-// Exclusive prefix of v over the CTA's threads, and the total.
-__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  long long w = part[lane];  // (kWarps == 32)
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const long long y = __shfl_up_sync(0xffffffffu, w, d);
-    if (lane >= d) w += y;
-  }
-  *total = __shfl_sync(0xffffffffu, w, 31);
-  const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-  __syncthreads();  // `part` may be written again
-  return x - v + (warp > 0 ? before : 0);
-}
-static_assert(kWarps == 32, "the second level of the scan is one warp");
-
-// The last b of [lo, hi] with at[b] <= i (at non-decreasing, at[lo] <= i).
-__device__ __forceinline__ int find_last(const int32_t* at, int lo, int hi, int32_t i) {
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (at[mid] <= i) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
+static_assert(kThreads == 32 * kScanWarps, "block_scan's");
 
 struct Request {
   long long len;   // tokens before the step
@@ -88,7 +55,7 @@ __device__ __forceinline__ Request request_of(const TablesParams& p, int b) {
 
 __global__ void __launch_bounds__(kThreads, 1) mla_update_tables_kernel(const TablesParams p) {
   extern __shared__ int32_t sh[];
-  __shared__ long long part[kWarps];
+  __shared__ long long part[kScanWarps];
   __shared__ int first_misfit;
   __shared__ long long misfit_q, misfit_take;
   const int B = p.B, tid = threadIdx.x;

@@ -623,3 +623,63 @@ def expand_kv(ckv: torch.Tensor, kpe: torch.Tensor, block_table: torch.Tensor, k
     d = nb.mla_expand_desc_t(B, H, bs, nblk, width, CODE_OF[dtype], S, raw_stream)
     nb.mla_expand_kv(ckv.data_ptr(), kpe.data_ptr(), block_table.data_ptr(), kv_indptr.data_ptr(), w_uk.data_ptr(),
                      w_uv_t.data_ptr(), k_nope.data_ptr(), v.data_ptr(), k_pe.data_ptr(), d)
+
+
+@dataclasses.dataclass
+class PrefillPlan:
+    """What prefill calls of up to so many requests and packed rows keep between them. Calls that may overlap in time
+    (other streams) need a plan each."""
+    num_requests: int
+    num_heads: int
+    max_q_tokens: int
+    workspace: torch.Tensor
+
+
+def plan_prefill(num_requests: int, num_heads: int, max_q_tokens: int, device="cuda") -> PrefillPlan:
+    """The workspace of prefill calls of no more than num_requests requests and max_q_tokens rows. Offsets are not part
+    of it."""
+    index = torch.device(device).index
+    dev = nb.mla_device_query(-1 if index is None else index)
+    n = nb.mla_prefill_workspace_bytes(dev, num_requests, num_heads, max_q_tokens)
+    if n == 0:
+        raise nb.MlaError(nb.MLA_ERR_UNSUPPORTED, "mla_prefill_workspace_bytes")
+    return PrefillPlan(num_requests, num_heads, max_q_tokens, torch.empty(n, dtype=torch.uint8, device=device))
+
+
+def prefill(plan: PrefillPlan, q_nope: torch.Tensor, q_pe: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor,
+            v: torch.Tensor, q_indptr: torch.Tensor, kv_indptr: torch.Tensor, scale: float, out: torch.Tensor,
+            out_lse: Optional[torch.Tensor] = None, causal: bool = True,
+            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of packed prompts over expanded keys and values (mla_prefill), into out [T, H, 128]. q_nope [T, H,
+    128] and q_pe [T, H, 64] may be views of one [T, H, 192] tensor."""
+    dev = _device_of(plan.workspace)
+    T, H, S, B = q_nope.shape[0], plan.num_heads, v.shape[0], q_indptr.shape[0] - 1
+    if B > plan.num_requests or T > plan.max_q_tokens:
+        raise ValueError(f"{B} requests, {T} rows: the plan is for {plan.num_requests}, {plan.max_q_tokens}")
+    dtype = q_nope.dtype
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q_nope: {dtype}")
+    _expect_rows(q_nope, (T, H, 128), dtype, "q_nope", dev)
+    _expect_rows(q_pe, (T, H, 64), dtype, "q_pe", dev)
+    _expect(k_nope, (S, H, 128), dtype, "k_nope", dev)
+    _expect(k_pe, (S, 64), dtype, "k_pe", dev)
+    _expect(v, (S, H, 128), dtype, "v", dev)
+    _expect(q_indptr, (B + 1,), torch.int32, "q_indptr", dev)
+    _expect(kv_indptr, (B + 1,), torch.int32, "kv_indptr", dev)
+    _expect(out, (T, H, 128), dtype, "out", dev)
+    if out_lse is not None:
+        _expect(out_lse, (T, H), torch.float32, "out_lse", dev)
+    raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
+    d = nb.mla_prefill_desc_t(B, H, CODE_OF[dtype], 1 if causal else 0, T, S, _strides(q_nope), _strides(q_pe),
+                              plan.workspace.data_ptr(), plan.workspace.numel(), raw_stream)
+    nb.mla_prefill(q_nope.data_ptr(), q_pe.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(), v.data_ptr(),
+                   q_indptr.data_ptr(), kv_indptr.data_ptr(), scale, out.data_ptr(),
+                   out_lse.data_ptr() if out_lse is not None else None, d)
+    return out
+
+
+def _strides(t: torch.Tensor):
+    """From row to row and head to head of [T, H, n] (of a single one: what a dense tensor has)."""
+    T, H, n = t.shape
+    head = t.stride(1) if H > 1 else n
+    return (t.stride(0) if T > 1 else max(H * head, n), head)
