@@ -153,9 +153,12 @@ mla_status_t mla_expand_kv(const void* ckv_cache, const void* kpe_cache, const i
   if (rows > 0x7fffffffull) return reject(MLA_ERR_UNSUPPORTED);
   const bool bf16 = d->dtype == MLA_BF16;
   const int sms = current_sms();
-  CUtensorMap tm_ckv, tm_uk, tm_uv;
+  CUtensorMap tm_ckv, tm_uk, tm_uv, tm_k, tm_v;
+  const int64_t dense = static_cast<int64_t>(d->num_heads) * MLA_V_HEAD_DIM;
   if (sms < 2 || !rows_map(&tm_ckv, ckv_cache, bf16, rows, mla::kRank, d->block_size) ||
-      !rows_map(&tm_uk, w_uk, bf16, static_cast<uint64_t>(d->num_heads) * MLA_NOPE_DIM, mla::kRank, mla::kBoxCols) ||
+      !rows_map(&tm_uk, w_uk, bf16, static_cast<uint64_t>(d->num_heads) * MLA_NOPE_DIM, mla::kRank, 128) ||
+      !heads_map(&tm_k, k_nope, bf16, d->max_tokens, d->num_heads, MLA_NOPE_DIM, dense, MLA_NOPE_DIM, 32) ||
+      !heads_map(&tm_v, v, bf16, d->max_tokens, d->num_heads, MLA_V_HEAD_DIM, dense, MLA_V_HEAD_DIM, 32) ||
       !rows_map(&tm_uv, w_uv_t, bf16, static_cast<uint64_t>(d->num_heads) * mla::kRank, MLA_V_HEAD_DIM, mla::kBoxCols))
     return reject(MLA_ERR_CUDA);
   mla::ExpandParams p;
@@ -172,7 +175,7 @@ mla_status_t mla_expand_kv(const void* ckv_cache, const void* kpe_cache, const i
   p.num_blocks = d->num_blocks;
   p.max_tokens = d->max_tokens;
   p.timeout_ns = mla::wait_timeout_ns();
-  return launched(mla::launch_expand_kv(tm_ckv, tm_uk, tm_uv, p, bf16, sms, static_cast<cudaStream_t>(d->stream)),
+  return launched(mla::launch_expand_kv(tm_ckv, tm_uk, tm_uv, tm_k, tm_v, p, bf16, sms, static_cast<cudaStream_t>(d->stream)),
                   MLA_CTR_PREFILL);
 }
 

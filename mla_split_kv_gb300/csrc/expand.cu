@@ -10,15 +10,17 @@
 // outputs have to be drained as fast as four thousand cycles of products make them.
 //
 // A pair of CTAs (cta_group::2, M = 256) takes blocks of 256 tokens of one request, 128 rows a CTA, and walks over
-// the heads: the latents of a block stay in shared memory (128 KB a CTA, loaded page by page through the block
-// table, 128-byte swizzle) while the heads' weights stream through a ring of five 16 KB stages, each 64 latent
-// columns of W_UK (64 of the 128 key columns a CTA: the pair shares B) and of W_UV^T (64 value columns, the operand's
-// other dimension contiguous). One CTA per tile would read 256 KB of weights for the same products that a pair
-// reads 128 KB a CTA for, 64 bytes a cycle of L2 against 32. Accumulators of two heads alternate in tensor memory
-// (2 x 256 columns): eight warps drain one, 32 bytes a thread and store, while the next is computed. Every pair takes
-// an equal run of the (block, head) tiles, block after block.
+// the heads two at a time, their keys, then their values (N = 256): the latents of a block stay in shared memory (128
+// KB a CTA, loaded page by page through the block table, 128-byte swizzle) while the heads' weights stream through a
+// ring of four 16 KB stages, each 64 latent columns of one head a CTA (the pair shares B): W_UK as it lies, W_UV^T
+// with the operand's other dimension contiguous. Shared memory sets the tile: at 128 bytes a cycle, products of N =
+// 256 read 64 (N = 128, a head's keys beside its values: 96), the refills write 32 and the way out takes 32.
+// Accumulators of two tiles alternate in tensor memory (2 x 256 columns): eight warps drain one through 4 KB each of
+// shared memory and TMA stores of [32 tokens x 64 columns], while the next is computed. (32 bytes a thread, every
+// thread another token, straight to memory: 527 us against 352 without any stores, of 16,384 tokens and 128 heads.)
+// Every pair takes an equal run of the (block, two heads, keys or values) tiles (Walk).
 //
-// Warps: 0-7 epilogue (0-3 keys, 4-7 values), 8 loads, 9 products (of the pair's first CTA).
+// Warps: 0-7 epilogue (0-3 the first head, 4-7 the second), 8 loads, 9 products (of the pair's first CTA).
 #include "device_common.cuh"
 
 namespace mla {
@@ -28,17 +30,18 @@ namespace {
 constexpr int kBlock = 256;               // tokens a pair takes at a time
 constexpr int kRows = 128;                // of them a CTA
 constexpr int kHeadCols = 128;            // key (without rotation) and value columns of a head
-constexpr int kHalfCols = kHeadCols / 2;  // of each, a CTA's share of the B operand
 constexpr int kChunks = kRank / kBoxCols; // 8 column blocks of 64
 constexpr int kAChunk = kRows * 128;      // 16 KB: [128 tokens x 64 columns]
-constexpr int kBPart = kBoxCols * 128;    // 8 KB: [64 x 64]
-constexpr int kStage = 2 * kBPart;
-constexpr int kStages = 5;
+constexpr int kStage = kHeadCols * 128;   // 16 KB: [128 x 64] of W_UK, or two [64 x 64] of W_UV^T
+constexpr int kStages = 4;
+static_assert(kChunks % kStages == 0, "the products' addresses are known when they are compiled");
 constexpr int kEpiWarps = 8;
+constexpr int kOutBox = 32 * 128;         // 4 KB: [32 tokens x 64 columns] on the way out
 constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kThreads = (kEpiWarps + 2) * 32;
 constexpr uint32_t kOffRing = kChunks * kAChunk;
-constexpr uint32_t kOffSmall = kOffRing + kStages * kStage;
+constexpr uint32_t kOffOut = kOffRing + kStages * kStage;
+constexpr uint32_t kOffSmall = kOffOut + kEpiWarps * kOutBox;
 constexpr uint32_t kSmem = kOffSmall + 1024 + 1024;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 
@@ -46,7 +49,7 @@ struct Small {
   uint64_t full[kStages], empty[kStages], a_full, a_empty, t_full[2], t_empty[2];
   uint32_t tmem_base;
   int32_t abort_flag;
-  int32_t first_b, first_blk, blocks;
+  int32_t first_b, first_blk, last_b, last_blk;
   int32_t part[kThreads / 32];
 };
 static_assert(sizeof(Small) <= 1024, "small smem region");
@@ -69,12 +72,27 @@ __device__ __forceinline__ void umma2_commit(uint64_t* bar) {
       : "memory");
 }
 // A tile into this CTA's shared memory that completes on a barrier of the pair's first CTA.
-__device__ __forceinline__ void tma2_load_2d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+__device__ __forceinline__ void tma2_load_2d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar,
+                                             uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
+}
+// A box from shared memory out; the thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z, const void* src,
+                                             uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(
+                   map),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "l"(policy)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy_evict_last() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
 }
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -111,23 +129,39 @@ __device__ __forceinline__ int2 request_rows(const ExpandParams& p, int b) {
   const int k0 = p.kv_indptr[b], k1 = min(p.kv_indptr[b + 1], p.max_tokens);
   return k0 < 0 || k1 <= k0 ? make_int2(0, 0) : make_int2(k0, k1 - k0);
 }
+__host__ __device__ constexpr int tiles_per_block(int H) { return 2 * ((H + 1) / 2); }
 __device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlock - 1) / kBlock; }
 
-// The tiles of a pair, block after block, head after head.
+// The tiles of a pair: of a block, two heads' keys (h even), then their values (h odd). The run's last block comes
+// first, if the run ends inside it, then the others in order: all runs are equally long, so all pairs then go through
+// the heads at the same time, and the weights that one has brought into L2 serve the others before the outputs that
+// stream through it have pushed them out.
 struct Walk {
-  int b, blk, h;
+  int b, blk, h, per_block, left, jump;
   int2 rows;
   bool fresh;  // the first tile of a block
-  __device__ __forceinline__ void start(const ExpandParams& p, int b0, int blk0, int h0) {
+  __device__ __forceinline__ void at(const ExpandParams& p, int b0, int blk0, int h0) {
     b = b0;
     blk = blk0;
     h = h0;
     rows = request_rows(p, b);
     fresh = true;
   }
-  __device__ __forceinline__ void next(const ExpandParams& p) {
+  __device__ __forceinline__ void start(const ExpandParams& p, const Small* sm, int n, int h0) {
+    per_block = tiles_per_block(p.H);
+    left = n;
+    const int tail = (h0 + n) % per_block;  // tiles of the last block, if the run ends inside it
+    jump = h0 + n > per_block && tail > 0 ? n - tail : 0;  // that many are left behind them
+    if (jump > 0) at(p, sm->last_b, sm->last_blk, 0);
+    else at(p, sm->first_b, sm->first_blk, h0);
+  }
+  __device__ __forceinline__ void next(const ExpandParams& p, const Small* sm, int h0) {
     fresh = false;
-    if (++h < p.H) return;
+    if (--left == jump && jump > 0) {
+      at(p, sm->first_b, sm->first_blk, h0);
+      return;
+    }
+    if (++h < per_block) return;
     h = 0;
     fresh = true;
     if (++blk < blocks_of(rows.y)) return;
@@ -142,7 +176,8 @@ struct Walk {
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_expand_kv_kernel(const __grid_constant__ CUtensorMap tm_ckv, const __grid_constant__ CUtensorMap tm_uk,
-                         const __grid_constant__ CUtensorMap tm_uv, const ExpandParams p) {
+                         const __grid_constant__ CUtensorMap tm_uv, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const ExpandParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = align1024(smem_raw);
   Small* const sm = reinterpret_cast<Small*>(smem + kOffSmall);
@@ -162,7 +197,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm->t_empty[s], 2 * kEpiWarps);
     }
     sm->abort_flag = 0;
-    sm->first_b = p.B;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -199,18 +233,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     blocks += sm->part[w];
   }
   const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
-  const long long tiles = static_cast<long long>(blocks) * p.H;
+  const int per_block = tiles_per_block(p.H);
+  const long long tiles = static_cast<long long>(blocks) * per_block;
   const long long g0 = tiles * pair / pairs, g1 = tiles * (pair + 1) / pairs;
   const int n = static_cast<int>(g1 - g0);
-  const int first = static_cast<int>(g0 / p.H), h0 = static_cast<int>(g0 % p.H);
-  if (n > 0 && first >= before && first < before + mine) {
+  const int first = static_cast<int>(g0 / per_block), h0 = static_cast<int>(g0 % per_block);
+  const int last = static_cast<int>((g1 - 1) / per_block);
+  if (n > 0 && last >= before && first < before + mine) {  // this thread's requests have one of the two blocks
     int at = before;
     for (int b = b0; b < b1; ++b) {
       const int nb = blocks_of(request_rows(p, b).y);
-      if (first < at + nb) {
+      if (first >= at && first < at + nb) {
         sm->first_b = b;
         sm->first_blk = first - at;
-        break;
+      }
+      if (last >= at && last < at + nb) {
+        sm->last_b = b;
+        sm->last_blk = last - at;
       }
       at += nb;
     }
@@ -219,13 +258,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
   const uint64_t tmo = p.timeout_ns;
   Walk w;
-  if (n > 0) w.start(p, sm->first_b, sm->first_blk, h0);
+  if (n > 0) w.start(p, sm, n, h0);
 
   if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- loads
     uint32_t use = 0, block = 0;
     bool ok = true;
-    for (int i = 0; i < n && ok; ++i, w.next(p)) {
+    const uint64_t once = l2_policy_evict_first(), often = l2_policy_evict_last();  // latents; weights
+    for (int i = 0; i < n && ok; ++i, w.next(p, sm, h0)) {
       if (w.fresh) {
         if (block > 0) {
           if (lane == 0) ok = mbar_wait(&sm->a_empty, (block - 1) & 1, tmo) && !*abort_flag;
@@ -249,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pid = -1;  // (lies before the cache: zeros)
           }
           for (int c = 0; c < kChunks; ++c)
-            tma2_load_2d(smem + c * kAChunk + lane * p.bs * 128, &tm_ckv, c * kBoxCols, pid * p.bs, bar);
+            tma2_load_2d(smem + c * kAChunk + lane * p.bs * 128, &tm_ckv, c * kBoxCols, pid * p.bs, bar, once);
         }
         __syncwarp();
       }
@@ -263,8 +303,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* const at = smem + kOffRing + s * kStage;
           const uint32_t bar = dsmem_addr(&sm->full[s], 0);
           if (rank == 0) mbar_arrive_expect_tx(&sm->full[s], 2 * kStage);
-          tma2_load_2d(at, &tm_uk, c * kBoxCols, w.h * kHeadCols + rank * kHalfCols, bar);
-          tma2_load_2d(at + kBPart, &tm_uv, rank * kHalfCols, w.h * kRank + c * kBoxCols, bar);
+          const int head = (w.h & ~1) + rank;  // (past the last one: zeros)
+          if ((w.h & 1) == 0) {
+            tma2_load_2d(at, &tm_uk, c * kBoxCols, head * kHeadCols, bar, often);
+          } else {
+            tma2_load_2d(at, &tm_uv, 0, head * kRank + c * kBoxCols, bar, often);
+            tma2_load_2d(at + kStage / 2, &tm_uv, kBoxCols, head * kRank + c * kBoxCols, bar, often);
+          }
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -273,16 +318,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
     if (rank == 0 && lane == 0) {
-      const uint32_t idesc_k = idesc_f16_f32(kBlock, kHeadCols, BF16, false, false);
-      const uint32_t idesc_v = idesc_f16_f32(kBlock, kHeadCols, BF16, false, true);
+      const uint32_t idesc_k = idesc_f16_f32(kBlock, 2 * kHeadCols, BF16, false, false);
+      const uint32_t idesc_v = idesc_f16_f32(kBlock, 2 * kHeadCols, BF16, false, true);
       const Desc2 a0 = desc2(smem_desc_sw128(smem_u32(smem), 16, 1024));
       const Desc2 k0 = desc2(smem_desc_sw128(smem_u32(smem + kOffRing), 16, 1024));
-      const Desc2 v0 = desc2(smem_desc_sw128(smem_u32(smem + kOffRing + kBPart), 1024, 1024));
+      const Desc2 v0 = desc2(smem_desc_sw128(smem_u32(smem + kOffRing), kStage / 2, 1024));
+      // One thread feeds the tensor cores, whose queue holds but a few products: what it waits for next is looked at
+      // between products of this stage, not after them.
+      // (Not across blocks: the next one's weights are loaded behind its latents, which wait for this one's products.)
       uint32_t use = 0, block = 0;
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
         if (w.fresh) {
-          ok = mbar_wait_cluster(&sm->a_full, block & 1, tmo);
+          ok = mbar_wait(&sm->a_full, block & 1, tmo) && mbar_wait(&sm->full[use % kStages], (use / kStages) & 1, tmo);
           ++block;
         }
         const int buf = i & 1;
@@ -293,23 +341,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + buf * 2 * kHeadCols;
-        for (int c = 0; c < kChunks; ++c, ++use) {
-          const int s = use % kStages;
-          if (!mbar_wait_cluster(&sm->full[s], (use / kStages) & 1, tmo) || *abort_flag) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a16 = (c * kAChunk) >> 4, s16 = (s * kStage) >> 4;
+        const bool keys = (w.h & 1) == 0;
+        w.next(p, sm, h0);
+        const bool block_done = w.fresh;
+        auto stages = [&](const Desc2 b0, const uint32_t step, const uint32_t idesc) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            umma2_ss(d, a0, a16 + 2 * kk, k0, s16 + 2 * kk, idesc_k, c > 0 || kk > 0);
-            umma2_ss(d + kHeadCols, a0, a16 + 2 * kk, v0, s16 + 128 * kk, idesc_v, c > 0 || kk > 0);
+          for (int c = 0; c < kChunks; ++c, ++use) {
+            const int s = c % kStages;  // (a tile's chunks go round the ring a whole number of times)
+            constexpr int kA = kAChunk / 16, kS = kStage / 16;
+            umma2_ss(d, a0, c * kA, b0, s * kS, idesc, c > 0);
+            umma2_ss(d, a0, c * kA + 2, b0, s * kS + step, idesc, 1);
+            if (c + 1 < kChunks || (!block_done && i + 1 < n))
+              ok = ok && mbar_wait(&sm->full[(s + 1) % kStages], ((use + 1) / kStages) & 1, tmo);
+            umma2_ss(d, a0, c * kA + 4, b0, s * kS + 2 * step, idesc, 1);
+            umma2_ss(d, a0, c * kA + 6, b0, s * kS + 3 * step, idesc, 1);
+            umma2_commit(&sm->empty[s]);
           }
-          umma2_commit(&sm->empty[s]);
-        }
-        w.next(p);
-        if (w.fresh) umma2_commit(&sm->a_empty);
+        };
+        if (keys) stages(k0, 2, idesc_k);
+        else stages(v0, 128, idesc_v);
+        if (block_done) umma2_commit(&sm->a_empty);
         umma2_commit(&sm->t_full[buf]);
       }
       if (!ok) *abort_flag = 1;
@@ -317,11 +368,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int part = warp >> 2;  // 0: keys, 1: values
-    const int row = rank * kRows + 32 * (warp & 3) + lane;  // token of the block
-    uint16_t* const out = part == 0 ? p.k_nope : p.v;
+    const int part = warp >> 2;  // head of the two
+    const int row = rank * kRows + 32 * (warp & 3);  // the warp's first token of the block
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    for (int i = 0; i < n; ++i, w.next(p)) {
+    const uint64_t once = l2_policy_evict_first();  // the outputs pass through L2 and leave the weights there
+    uint8_t* const stage = smem + kOffOut + warp * kOutBox;
+    const uint32_t mine_at = smem_u32(stage) + lane * 128;
+    for (int i = 0; i < n; ++i, w.next(p, sm, h0)) {
       const int buf = i & 1;
       if (w.h == 0) {  // the block's rotary keys: eight lanes a token
         for (int r = tid >> 3; r < kRows; r += kEpiWarps * 4) {
@@ -343,25 +396,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      uint32_t x[kHeadCols / 2];
+      const int t = w.blk * kBlock + row, head = (w.h & ~1) + part;
+      const bool whole = t + 32 <= w.rows.y;  // else the rows behind the last token are someone else's
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t r[32];
-        tmem_ld32(tmem + lanes + (2 * buf + part) * kHeadCols + 32 * q, r);
-        tmem_wait_ld();
+      for (int half = 0; half < 2; ++half) {
+        uint32_t x[kBoxCols / 2];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[16 * q + j] = pack2<BF16>(r[2 * j], r[2 * j + 1]);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) remote_arrive(dsmem_addr(&sm->t_empty[buf], 0));
-      const int t = w.blk * kBlock + row;
-      if (t < w.rows.y) {
-        uint16_t* const at = out + (static_cast<long long>(w.rows.x + t) * p.H + w.h) * kHeadCols;
+        for (int q = 0; q < 2; ++q) {
+          uint32_t r[32];
+          tmem_ld32(tmem + lanes + (2 * buf + part) * kHeadCols + kBoxCols * half + 32 * q, r);
+          tmem_wait_ld();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) store32(at + 16 * q, x + 8 * q);
+          for (int j = 0; j < 16; ++j) x[16 * q + j] = pack2<BF16>(r[2 * j], r[2 * j + 1]);
+        }
+        if (half == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive(dsmem_addr(&sm->t_empty[buf], 0));
+        }
+        if (head >= p.H || t >= w.rows.y) continue;
+        if (whole) {
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the box before is read
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            sts128(mine_at + ((j ^ (lane & 7)) << 4), make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_3d((w.h & 1) == 0 ? &tm_k : &tm_v, kBoxCols * half, head, w.rows.x + t, stage, once);
+        } else if (t + lane < w.rows.y) {
+          uint16_t* const at = ((w.h & 1) == 0 ? p.k_nope : p.v) + (static_cast<long long>(w.rows.x + t + lane) * p.H + head) * kHeadCols + kBoxCols * half;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) store32(at + 16 * q, x + 8 * q);
+        }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   __syncthreads();
@@ -375,20 +445,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool BF16>
 cudaError_t launch(const cudaLaunchConfig_t& cfg, const CUtensorMap& tm_ckv, const CUtensorMap& tm_uk,
-                   const CUtensorMap& tm_uv, const ExpandParams& p) {
+                   const CUtensorMap& tm_uv, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const ExpandParams& p) {
   static DeviceOnce once;
   const cudaError_t e = set_attribute_once(once, reinterpret_cast<const void*>(&mla_expand_kv_kernel<BF16>),
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, mla_expand_kv_kernel<BF16>, tm_ckv, tm_uk, tm_uv, p);
+  return cudaLaunchKernelEx(&cfg, mla_expand_kv_kernel<BF16>, tm_ckv, tm_uk, tm_uv, tm_k, tm_v, p);
 }
 
 }  // namespace
 
 cudaError_t launch_expand_kv(const CUtensorMap& tm_ckv, const CUtensorMap& tm_uk, const CUtensorMap& tm_uv,
-                             const ExpandParams& p, bool bf16, int sms, cudaStream_t stream) {
+                             const CUtensorMap& tm_k, const CUtensorMap& tm_v, const ExpandParams& p, bool bf16,
+                             int sms, cudaStream_t stream) {
   // no more pairs than there can be tiles: every request may add a block that is not full
-  const int64_t tiles = (static_cast<int64_t>(p.max_tokens) / kBlock + p.B) * p.H;
+  const int64_t tiles = (static_cast<int64_t>(p.max_tokens) / kBlock + p.B) * tiles_per_block(p.H);
   const int64_t pairs = sms / 2 < tiles ? sms / 2 : tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs > 0 ? pairs : 1)), 1, 1);
@@ -404,7 +475,7 @@ cudaError_t launch_expand_kv(const CUtensorMap& tm_ckv, const CUtensorMap& tm_uk
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return bf16 ? launch<true>(cfg, tm_ckv, tm_uk, tm_uv, p) : launch<false>(cfg, tm_ckv, tm_uk, tm_uv, p);
+  return bf16 ? launch<true>(cfg, tm_ckv, tm_uk, tm_uv, tm_k, tm_v, p) : launch<false>(cfg, tm_ckv, tm_uk, tm_uv, tm_k, tm_v, p);
 }
 
 cudaError_t expand_read_clear_error(uint32_t* out) {

@@ -236,7 +236,8 @@ cudaError_t launch_append_slots(const AppendSlotsParams& p, cudaStream_t stream)
 cudaError_t step_tables_read_clear_error(uint32_t* out);
 
 // Keys and values of every head from cached latents (mla_expand_kv): maps of boxes of 64 columns, a page high over the
-// [rows, 512] cache, 64 rows high over w_uk as [H * 128, 512] and w_uv_t as [H * 512, 128], 128-byte swizzle.
+// [rows, 512] cache, 128 rows high over w_uk as [H * 128, 512], 64 over w_uv_t as [H * 512, 128], 32 rows of one head
+// high over the outputs, 128-byte swizzle.
 struct ExpandParams {
   const uint16_t* kpe;         // [num_blocks, bs, 64]
   const int32_t* block_table;  // [B, max_blocks]
@@ -248,7 +249,8 @@ struct ExpandParams {
   uint64_t timeout_ns;
 };
 cudaError_t launch_expand_kv(const CUtensorMap& tm_ckv, const CUtensorMap& tm_uk, const CUtensorMap& tm_uv,
-                             const ExpandParams& p, bool bf16, int sms, cudaStream_t stream);
+                             const CUtensorMap& tm_k, const CUtensorMap& tm_v, const ExpandParams& p, bool bf16,
+                             int sms, cudaStream_t stream);
 cudaError_t expand_read_clear_error(uint32_t* out);
 
 // Attention of prompts (mla_prefill). The maps, 128-byte swizzle, 64 columns a box: q and qpe [T, H, 128 / 64] and k [S,
