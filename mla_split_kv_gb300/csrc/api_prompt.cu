@@ -165,6 +165,8 @@ mla_status_t mla_expand_kv(const void* ckv_cache, const void* kpe_cache, const i
   p.kpe = static_cast<const uint16_t*>(kpe_cache);
   p.block_table = block_table;
   p.kv_indptr = kv_indptr;
+  p.w_uk = static_cast<const uint8_t*>(w_uk);
+  p.w_uv_t = static_cast<const uint8_t*>(w_uv_t);
   p.k_nope = static_cast<uint16_t*>(k_nope);
   p.v = static_cast<uint16_t*>(v);
   p.k_pe = static_cast<uint16_t*>(k_pe);

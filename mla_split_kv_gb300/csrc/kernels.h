@@ -242,6 +242,8 @@ struct ExpandParams {
   const uint16_t* kpe;         // [num_blocks, bs, 64]
   const int32_t* block_table;  // [B, max_blocks]
   const int32_t* kv_indptr;    // [B+1]
+  const uint8_t* w_uk;         // [H, 128, 512] 16-bit
+  const uint8_t* w_uv_t;       // [H, 512, 128] 16-bit
   uint16_t* k_nope;            // [max_tokens, H, 128]
   uint16_t* v;                 // [max_tokens, H, 128]
   uint16_t* k_pe;              // [max_tokens, 64]

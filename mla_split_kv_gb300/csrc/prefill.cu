@@ -49,9 +49,11 @@ constexpr int kChunk = 16384;
 constexpr int kRing = 8;
 constexpr int kTileChunks = 5;             // keys 0, 1, rotary, values 0, 1
 constexpr int kQBytes = 3 * kChunk;        // of a subtile
-constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kThreads = 10 * 32;
+constexpr int kThreads = 12 * 32;          // (the last two warps only make the third warpgroup whole)
+// Registers: launched with 168 a thread (64,512 in all); the softmax warps take 216, the third warpgroup keeps 64.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 64;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 168 * kThreads, "what the block was launched with");
 constexpr int kDirect = 64;                // items of a call that plans for itself
 constexpr float kTau = 8.0f;
 constexpr uint32_t kOffRing = 2 * kQBytes;
@@ -61,7 +63,7 @@ static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // + 128 * subtile
 
 struct Small {
-  uint64_t full[kRing], empty[kRing], q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], drain;
+  uint64_t k_full[2], v_full[2], empty[kRing], q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], drain;
   uint32_t tmem_base;
   int32_t abort_flag;
   int32_t items;
@@ -149,6 +151,10 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
 }
 
 // A request's rows and tokens in the packed tensors, within them.
@@ -277,11 +283,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(&sm->full[s], 1);
       mbar_init(&sm->empty[s], 1);
       sm->dirty[s] = 0;
     }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm->k_full[s], 3);  // one arrival a chunk
+      mbar_init(&sm->v_full[s], 2);
       mbar_init(&sm->q_full[s], 1);
       mbar_init(&sm->q_empty[s], 1);
       mbar_init(&sm->s_full[s], 1);
@@ -359,14 +366,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- loads
+    fewer_registers();
     if (lane == 0) {
-      uint32_t c = 0, used[2] = {0, 0};
+      uint32_t c = 0, tile = 0, used[2] = {0, 0};
       bool ok = true;
-      auto chunk = [&]() -> uint8_t* {  // the next chunk of the ring, free and armed
+      auto chunk = [&](uint64_t* bar) -> uint8_t* {  // the next chunk of the ring, free and armed
         const int s = c % kRing;
         if (c >= kRing && !mbar_wait(&sm->empty[s], (c / kRing - 1) & 1, tmo)) ok = false;
         if (!ok) return nullptr;
-        mbar_arrive_expect_tx(&sm->full[s], kChunk);
+        mbar_arrive_expect_tx(bar, kChunk);
         return smem + kOffRing + s * kChunk;
       };
       for (int k = 0; ok; ++k) {
@@ -391,13 +399,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(at + kChunk, &tm_q, 64, w.h, row, &sm->q_full[s]);
           tma_load_3d(at + 2 * kChunk, &tm_qpe, 0, w.h, row, &sm->q_full[s]);
         };
-        for (int i = 0; i < nt && ok; ++i) {
+        for (int i = 0; i < nt && ok; ++i, ++tile) {
           const int tok = w.kvrow + (w.j0 + i) * kTile;
           if (i == 0) queries(0);
           for (int x = 0; x < kTileChunks && ok; ++x, ++c) {
-            uint8_t* const at = chunk();
+            uint64_t* const bar = x < 3 ? &sm->k_full[tile & 1] : &sm->v_full[tile & 1];
+            uint8_t* const at = chunk(bar);
             if (at == nullptr) break;
-            uint64_t* const bar = &sm->full[c % kRing];
             if (x < 2) {
               tma_load_3d(at, &tm_k, 64 * x, w.h, tok, bar);
             } else if (x == 2) {
@@ -415,24 +423,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
+    fewer_registers();
     if (lane == 0) {
       const uint32_t idesc_s = idesc_f16_f32(kSub, kTile, BF16, false, false) | (p.negate ? 1u << 13 : 0u);
       const uint32_t idesc_o = idesc_f16_f32(kSub, kDim, BF16, false, true);
       const Desc2 q_desc = desc2(smem_desc_sw128(smem_u32(smem), 16, 1024));
       const Desc2 k_desc = desc2(smem_desc_sw128(smem_u32(smem + kOffRing), 16, 1024));
       const Desc2 v_desc = desc2(smem_desc_sw128(smem_u32(smem + kOffRing), kChunk / 2, 1024));
-      uint32_t c = 0;                      // first chunk of the unit
-      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // units and tiles so far
+      uint32_t tile0 = 0;                       // tiles before this unit
+      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // units and tiles of each subtile so far
       bool ok = true;
-      auto wait_chunk = [&](uint32_t x) { ok = ok && mbar_wait(&sm->full[x % kRing], (x / kRing) & 1, tmo); };
-      auto scores = [&](int s, int i) {  // S of tile i
-        const uint32_t x = c + kTileChunks * i;
-        const bool last = s == 1 || i >= w.tiles[1];
+      auto scores = [&](int s, int i) {  // S of tile i; the first of the subtiles waits for the keys
+        const uint32_t x = kTileChunks * (tile0 + i), t = tile0 + i;
+        const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
+        if (first) ok = ok && mbar_wait(&sm->k_full[t & 1], (t >> 1) & 1, tmo);
+        if (!ok) return;
+        tc_fence_after();
 #pragma unroll
         for (int y = 0; y < 3; ++y) {
-          wait_chunk(x + y);
-          if (!ok) return;
-          tc_fence_after();
           const uint32_t a16 = (s * kQBytes + y * kChunk) >> 4, b16 = (((x + y) % kRing) * kChunk) >> 4;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -444,12 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i + 1 == w.tiles[s]) umma_commit(&sm->q_empty[s]);
       };
       auto values = [&](int s, int i) {
-        const uint32_t x = c + kTileChunks * i + 3;
-        const bool last = s == 1 || i >= w.tiles[1];
+        const uint32_t x = kTileChunks * (tile0 + i) + 3, t = tile0 + i;
+        const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
+        if (first) ok = ok && mbar_wait(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           ok = ok && mbar_wait(&sm->p_full[s][y], pn[s] & 1, tmo);
-          wait_chunk(x + y);
           if (!ok) return;
           tc_fence_after();
           const uint32_t b16 = (((x + y) % kRing) * kChunk) >> 4;
@@ -487,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && i + 1 < w.tiles[s]) scores(s, i + 1);
           }
         }
-        c += kTileChunks * nt;
+        tile0 += nt;
       }
       if (!ok) *abort_flag = 1;
       // every product issued so far is done before tensor memory is freed
@@ -495,14 +503,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&sm->drain, 0, kDrainTimeoutNs);
     }
     __syncwarp();
-  } else {
+  } else if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- softmax, output: thread = row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int s = warp >> 2, r = tid & (kSub - 1);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + kTmemS + s * kTile, to = tmem + lanes + kTmemO + s * kDim;
     const float scale = p.scale_log2;
     uint32_t done = 0;   // tiles of this subtile so far
-    uint32_t chunks = 0; // chunks of all units so far
+    uint32_t tile0 = 0;  // tiles of all units before this one
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int u = unit_index(k);
@@ -533,10 +542,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < kTile; ++t) x[t] = t < nvis ? x[t] * scale : -INFINITY;
             f = 1.f;
           }
-          float mx = fmaxf(x[0], x[1]);
+          float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int t = 2; t < kTile; t += 2) mx = fmaxf(mx, fmaxf(x[t], x[t + 1]));
-          mx *= f;
+          for (int t = 4; t < kTile; t += 8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], t + 4 + j < kTile ? fmaxf(x[t + j], x[t + 4 + j]) : x[t + j]);
+          }
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
           const bool need = mx > m + kTau;
           if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
             const float m_new = need ? mx : m;
@@ -561,9 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = m_new;
           }
           if (masked) {
-            const uint32_t c = chunks + kTileChunks * i + 3;
-            ok = mbar_wait(&sm->full[c % kRing], (c / kRing) & 1, tmo) &&
-                 mbar_wait(&sm->full[(c + 1) % kRing], ((c + 1) / kRing) & 1, tmo);
+            const uint32_t t = tile0 + i, c = kTileChunks * t + 3;
+            ok = mbar_wait(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
             if (!ok) break;
             if (clean_values<BF16>(smem + kOffRing + (c % kRing) * kChunk, smem + kOffRing + ((c + 1) % kRing) * kChunk, tok0, w.L, r))
               *const_cast<volatile int32_t*>(&sm->dirty[k & 7]) = k + 1;
@@ -642,9 +653,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           else if (p.out_lse != nullptr) p.out_lse[row * p.H + w.h] = lse;
         }
       }
-      chunks += kTileChunks * max(w.tiles[0], w.tiles[1]);
+      tile0 += max(w.tiles[0], w.tiles[1]);
     }
     if (!ok) *abort_flag = 1;
+  } else {
+    fewer_registers();
   }
   __syncwarp();
   __syncthreads();
