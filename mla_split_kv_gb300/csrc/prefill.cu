@@ -36,6 +36,7 @@
 // Warps: 0-3 and 4-7 softmax and output of the two subtiles (thread = row), 8 products, 9 loads.
 #include "block_scan.cuh"
 #include "device_common.cuh"
+#include "umma_issue.cuh"
 
 namespace mla {
 
@@ -96,14 +97,6 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, Desc2 b, uint32_t b16, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %5, 0;\n mov.b64 db, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b.lo + b16), "r"(b.hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -423,85 +416,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
+    // The whole warp runs this; one lane's instructions count (umma_issue.cuh).
     fewer_registers();
-    if (lane == 0) {
-      const uint32_t idesc_s = idesc_f16_f32(kSub, kTile, BF16, false, false) | (p.negate ? 1u << 13 : 0u);
-      const uint32_t idesc_o = idesc_f16_f32(kSub, kDim, BF16, false, true);
-      const Desc2 q_desc = desc2(smem_desc_sw128(smem_u32(smem), 16, 1024));
-      const Desc2 k_desc = desc2(smem_desc_sw128(smem_u32(smem + kOffRing), 16, 1024));
-      const Desc2 v_desc = desc2(smem_desc_sw128(smem_u32(smem + kOffRing), kChunk / 2, 1024));
-      uint32_t tile0 = 0;                       // tiles before this unit
-      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // units and tiles of each subtile so far
-      bool ok = true;
-      auto scores = [&](int s, int i) {  // S of tile i; the first of the subtiles waits for the keys
-        const uint32_t x = kTileChunks * (tile0 + i), t = tile0 + i;
-        const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
-        if (first) ok = ok && mbar_wait(&sm->k_full[t & 1], (t >> 1) & 1, tmo);
+    const uint32_t leader = elect_one();
+    const uint32_t idesc_s = idesc_f16_f32(kSub, kTile, BF16, false, false) | (p.negate ? 1u << 13 : 0u);
+    const uint32_t idesc_o = idesc_f16_f32(kSub, kDim, BF16, false, true);
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + kOffRing), 16, 1024);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + kOffRing), kChunk / 2, 1024);
+    uint32_t tile0 = 0;                       // tiles before this unit
+    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // units and tiles of each subtile so far
+    bool ok = true;
+    auto scores = [&](int s, int i) {  // S of tile i; the first of the subtiles waits for the keys
+      const uint32_t x = kTileChunks * (tile0 + i), t = tile0 + i;
+      const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
+      if (first) ok = ok && mbar_wait(&sm->k_full[t & 1], (t >> 1) & 1, tmo);
+      if (!ok) return;
+      tc_fence_after();
+#pragma unroll
+      for (int y = 0; y < 3; ++y) {
+        const uint32_t slot = (x + y) % kRing;
+        const uint64_t a = q_desc + ((s * kQBytes + y * kChunk) >> 4), b = k_desc + ((slot * kChunk) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          issue_ss(leader, tmem + kTmemS + s * kTile, a + 2 * kk, b + 2 * kk, idesc_s, y > 0 || kk > 0);
+        if (last && y < 2) issue_commit(leader, &sm->empty[slot]);
+      }
+      issue_commit(leader, &sm->s_full[s]);
+      if (last) issue_commit(leader, &sm->empty[(x + 2) % kRing]);
+      if (i + 1 == w.tiles[s]) issue_commit(leader, &sm->q_empty[s]);
+    };
+    auto values = [&](int s, int i) {
+      const uint32_t x = kTileChunks * (tile0 + i) + 3, t = tile0 + i;
+      const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
+      if (first) ok = ok && mbar_wait(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        ok = ok && mbar_wait(&sm->p_full[s][y], pn[s] & 1, tmo);
         if (!ok) return;
         tc_fence_after();
+        const uint32_t slot = (x + y) % kRing;
+        const uint64_t b = v_desc + ((slot * kChunk) >> 4);
 #pragma unroll
-        for (int y = 0; y < 3; ++y) {
-          const uint32_t a16 = (s * kQBytes + y * kChunk) >> 4, b16 = (((x + y) % kRing) * kChunk) >> 4;
+        for (int kk = 0; kk < 4; ++kk)
+          issue_ts(leader, tmem + kTmemO + s * kDim, tmem + kTmemS + s * kTile + 32 * y + 8 * kk, b + 128 * kk, idesc_o,
+                   i > 0 || y > 0 || kk > 0);
+        if (last && y == 0) issue_commit(leader, &sm->empty[slot]);
+      }
+      issue_commit(leader, &sm->pv_done[s]);
+      if (last) issue_commit(leader, &sm->empty[(x + 1) % kRing]);
+      ++pn[s];
+    };
+    for (int k = 0; ok; ++k) {
+      const int u = unit_index(k);
+      if (u >= units) {
+        if (k * static_cast<int>(gridDim.x) >= units) break;
+        continue;
+      }
+      unit_of(p, sm, u, w);
+      const int nt = max(w.tiles[0], w.tiles[1]);
+      if (nt == 0) continue;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ss(tmem + kTmemS + s * kTile, q_desc, a16 + 2 * kk, k_desc, b16 + 2 * kk, idesc_s, y > 0 || kk > 0);
-          if (last && y < 2) umma_commit(&sm->empty[(x + y) % kRing]);
-        }
-        umma_commit(&sm->s_full[s]);
-        if (last) umma_commit(&sm->empty[(x + 2) % kRing]);
-        if (i + 1 == w.tiles[s]) umma_commit(&sm->q_empty[s]);
-      };
-      auto values = [&](int s, int i) {
-        const uint32_t x = kTileChunks * (tile0 + i) + 3, t = tile0 + i;
-        const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
-        if (first) ok = ok && mbar_wait(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          ok = ok && mbar_wait(&sm->p_full[s][y], pn[s] & 1, tmo);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t b16 = (((x + y) % kRing) * kChunk) >> 4;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ts(tmem + kTmemO + s * kDim, tmem + kTmemS + s * kTile + 32 * y + 8 * kk, v_desc, b16 + 128 * kk, idesc_o,
-                    i > 0 || y > 0 || kk > 0);
-          if (last && y == 0) umma_commit(&sm->empty[x % kRing]);
-        }
-        umma_commit(&sm->pv_done[s]);
-        if (last) umma_commit(&sm->empty[(x + 1) % kRing]);
-        ++pn[s];
-      };
-      for (int k = 0; ok; ++k) {
-        const int u = unit_index(k);
-        if (u >= units) {
-          if (k * static_cast<int>(gridDim.x) >= units) break;
-          continue;
-        }
-        unit_of(p, sm, u, w);
-        const int nt = max(w.tiles[0], w.tiles[1]);
-        if (nt == 0) continue;
+      for (int s = 0; s < 2; ++s) {
+        if (w.tiles[s] == 0 || !ok) continue;
+        ok = mbar_wait(&sm->q_full[s], qn[s] & 1, tmo);
+        ++qn[s];
+        if (ok) scores(s, 0);
+      }
+      for (int i = 0; i < nt && ok; ++i) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (w.tiles[s] == 0 || !ok) continue;
-          ok = mbar_wait(&sm->q_full[s], qn[s] & 1, tmo);
-          ++qn[s];
-          if (ok) scores(s, 0);
+          if (i >= w.tiles[s] || !ok) continue;
+          values(s, i);
+          if (ok && i + 1 < w.tiles[s]) scores(s, i + 1);
         }
-        for (int i = 0; i < nt && ok; ++i) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (i >= w.tiles[s] || !ok) continue;
-            values(s, i);
-            if (ok && i + 1 < w.tiles[s]) scores(s, i + 1);
-          }
-        }
-        tile0 += nt;
       }
-      if (!ok) *abort_flag = 1;
-      // every product issued so far is done before tensor memory is freed
-      umma_commit(&sm->drain);
-      mbar_wait(&sm->drain, 0, kDrainTimeoutNs);
+      tile0 += nt;
     }
+    if (!ok) *abort_flag = 1;
+    // every product issued so far is done before tensor memory is freed
+    __syncwarp();
+    issue_commit(leader, &sm->drain);
+    mbar_wait(&sm->drain, 0, kDrainTimeoutNs);
     __syncwarp();
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- softmax, output: thread = row
