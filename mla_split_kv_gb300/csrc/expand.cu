@@ -22,6 +22,7 @@
 //
 // Warps: 0-7 epilogue (0-3 the first head, 4-7 the second), 8 loads, 9 products (of the pair's first CTA).
 #include "device_common.cuh"
+#include "umma_issue.cuh"
 
 namespace mla {
 
@@ -54,23 +55,6 @@ struct Small {
 };
 static_assert(sizeof(Small) <= 1024, "small smem region");
 
-// D[tmem] (+)= A[smem] * B[smem] over a pair of CTAs: M = 256, half of it and of B's rows in each.
-__device__ __forceinline__ void umma2_ss(uint32_t d_tmem, Desc2 a, uint32_t a16, Desc2 b, uint32_t b16, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %6, 0;\n mov.b64 da, {%1, %2};\n"
-      " mov.b64 db, {%3, %4};\n tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d_tmem),
-      "r"(a.lo + a16), "r"(a.hi), "r"(b.lo + b16), "r"(b.hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on the barrier at this offset in both CTAs once every product issued so far has completed.
-__device__ __forceinline__ void umma2_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
 // A tile into this CTA's shared memory that completes on a barrier of the pair's first CTA.
 __device__ __forceinline__ void tma2_load_2d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar,
                                              uint64_t policy) {
@@ -325,20 +309,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) *abort_flag = 1;
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {  // the whole warp in step; one lane's instructions count
+      const uint32_t leader = elect_one();
       const uint32_t idesc_k = idesc_f16_f32(kBlock, 2 * kHeadCols, BF16, false, false);
       const uint32_t idesc_v = idesc_f16_f32(kBlock, 2 * kHeadCols, BF16, false, true);
-      const Desc2 a0 = desc2(smem_desc_sw128(smem_u32(smem), 16, 1024));
-      const Desc2 k0 = desc2(smem_desc_sw128(smem_u32(smem + kOffRing), 16, 1024));
-      const Desc2 v0 = desc2(smem_desc_sw128(smem_u32(smem + kOffRing), kStage / 2, 1024));
-      // One thread feeds the tensor cores, whose queue holds but a few products: what it waits for next is looked at
-      // between products of this stage, not after them.
-      // (Not across blocks: the next one's weights are loaded behind its latents, which wait for this one's products.)
+      const uint64_t a0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t k0 = smem_desc_sw128(smem_u32(smem + kOffRing), 16, 1024);
+      const uint64_t v0 = smem_desc_sw128(smem_u32(smem + kOffRing), kStage / 2, 1024);
       uint32_t use = 0, block = 0;
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
         if (w.fresh) {
-          ok = mbar_wait(&sm->a_full, block & 1, tmo) && mbar_wait(&sm->full[use % kStages], (use / kStages) & 1, tmo);
+          ok = mbar_wait(&sm->a_full, block & 1, tmo);
           ++block;
         }
         const int buf = i & 1;
@@ -352,24 +334,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool keys = (w.h & 1) == 0;
         w.next(p, sm, h0);
         const bool block_done = w.fresh;
-        auto stages = [&](const Desc2 b0, const uint32_t step, const uint32_t idesc) {
+        auto stages = [&](const uint64_t b0, const uint32_t step, const uint32_t idesc) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c, ++use) {
             const int s = c % kStages;  // (a tile's chunks go round the ring a whole number of times)
-            constexpr int kA = kAChunk / 16, kS = kStage / 16;
-            umma2_ss(d, a0, c * kA, b0, s * kS, idesc, c > 0);
-            umma2_ss(d, a0, c * kA + 2, b0, s * kS + step, idesc, 1);
-            if (c + 1 < kChunks || (!block_done && i + 1 < n))
-              ok = ok && mbar_wait(&sm->full[(s + 1) % kStages], ((use + 1) / kStages) & 1, tmo);
-            umma2_ss(d, a0, c * kA + 4, b0, s * kS + 2 * step, idesc, 1);
-            umma2_ss(d, a0, c * kA + 6, b0, s * kS + 3 * step, idesc, 1);
-            umma2_commit(&sm->empty[s]);
+            ok = ok && mbar_wait(&sm->full[s], (use / kStages) & 1, tmo);
+            const uint64_t a = a0 + c * (kAChunk / 16), b = b0 + s * (kStage / 16);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) issue2_ss(leader, d, a + 2 * kk, b + step * kk, idesc, c > 0 || kk > 0);
+            issue2_commit(leader, &sm->empty[s]);
           }
         };
         if (keys) stages(k0, 2, idesc_k);
         else stages(v0, 128, idesc_v);
-        if (block_done) umma2_commit(&sm->a_empty);
-        umma2_commit(&sm->t_full[buf]);
+        if (block_done) issue2_commit(leader, &sm->a_empty);
+        issue2_commit(leader, &sm->t_full[buf]);
       }
       if (!ok) *abort_flag = 1;
     }
