@@ -877,6 +877,106 @@ uint64_t mla_prefill_workspace_bytes(const mla_device_info_t* dev, int32_t num_r
                                      int32_t max_q_tokens);
 
 /*
+ * A batch whose contexts start with the same tokens (a system prompt, a document
+ * that many requests ask about).
+ */
+
+/* One piece of work of mla_decode_shared: a group of up to 128 consecutive rows
+ * of [B, q_len, H] over a run of tokens. */
+typedef struct {
+  int32_t row0, rows;         /* rows [row0, row0 + rows)                     */
+  int32_t request;            /* whose own tokens; -1: the common ones        */
+  int32_t t0, t1;             /* tokens (positions in the context)            */
+  int32_t slot;               /* its rows' partials go to slot `slot`         */
+  int32_t reserved[2];
+} mla_shared_item_t;
+
+typedef struct {
+  /* inputs */
+  int32_t shared_tokens;      /* P: the common tokens, a multiple of the page */
+  int32_t item_capacity;      /* entries of `items`                           */
+  mla_shared_item_t* items;   /* host, caller-owned                           */
+  int32_t* own_indptr;        /* host, caller-owned, >= B * ceil(q_len * H /
+                                 128) + 1 entries                             */
+  /* outputs */
+  int32_t num_items;
+  int32_t num_slots;
+  int32_t shared_parts;       /* pieces of the common tokens                  */
+} mla_shared_plan_t;
+
+/*
+ * mla_plan_shared -- lay out the work of mla_decode_shared for contexts of
+ * these lengths (the common tokens among them): the common tokens for the rows
+ * of the whole batch in groups of 128, each request's own ones for its own
+ * rows, each cut into pieces so that the device is evenly busy, the longest
+ * first. The plan serves contexts of any length (a request's last piece takes
+ * what it has grown by) of the same B, q_len, H, page size and P, in the time
+ * planned for these. own_indptr: of each request's group of 128 rows, its
+ * first slot (the slots before are the common tokens': of the group g of the
+ * batch's rows, shared_parts slots from g * shared_parts on). Host code; touches no GPU.
+ * MLA_ERR_CAPACITY (with num_items set) where items does not hold them.
+ */
+mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_t B, int32_t num_heads, int32_t q_len,
+                             int32_t block_size, const mla_device_info_t* dev, mla_shared_plan_t* plan);
+
+/* Shapes and buffers of mla_decode_shared. */
+typedef struct {
+  int32_t num_requests;       /* B                                            */
+  int32_t num_heads;          /* H in {16, 64, 128}                           */
+  int32_t q_len;              /* query rows per request, 1..32                */
+  int32_t block_size;         /* tokens per page: 16, 32 or 64                */
+  int32_t num_blocks;         /* pages in the cache pool                      */
+  int32_t max_blocks_per_req; /* row stride of block_table, in entries        */
+  int32_t dtype;              /* MLA_F16 or MLA_BF16: queries and caches      */
+  int32_t causal;             /* as mla_decode_desc_t.causal                  */
+  int32_t shared_tokens;      /* P, as planned                                */
+  int32_t out_dtype;          /* MLA_F16, MLA_BF16 or MLA_F32                 */
+  const mla_shared_item_t* items; /* DEVICE, as planned, 16-byte aligned      */
+  const int32_t* own_indptr;  /* DEVICE, as planned                           */
+  int32_t num_items, num_slots, shared_parts; /* as planned                   */
+  void* workspace;            /* DEVICE, >= mla_decode_shared_workspace_bytes
+                                 bytes, 16-byte aligned; need not be cleared.
+                                 Calls sharing it must not overlap in time.    */
+  uint64_t workspace_bytes;
+  void* stream;               /* cudaStream_t                                 */
+} mla_shared_desc_t;
+
+/*
+ * mla_decode_shared -- mla_decode (the whole layer call: scores, softmax,
+ * values, merge) of a batch whose requests have the same first P tokens, which
+ * are read and multiplied once for the batch: the pages of shared_table
+ * [P / block_size] hold them, and block_table a request's tokens from P on
+ * (columns from P / block_size on; those before are not read). Each row sees
+ * what mla_decode's sees: all of its request's context_lens tokens, or those up
+ * to its own position when causal. A request may be shorter than P: its rows
+ * then see its tokens of the common ones alone; of length 0, nothing: 0 and -inf.
+ *
+ * Tokens that a row does not see do not reach it, NaN among them or not. Pages:
+ * as for mla_decode_partial (one outside the pool or the table reads zeros and
+ * raises MLA_ERR_DEVICE_CHECK). The lengths are read on the device: a captured
+ * call may be replayed as contexts grow.
+ *
+ * Precision: scores, maxima, sums and out_lse are fp32; the weights of the value
+ * product are rounded once to `dtype` (half a step: 2^-12 of themselves in fp16,
+ * 2^-9 in bf16) and the sum that normalizes takes them unrounded. The partials
+ * are fp32; `out` is rounded once to out_dtype.
+ *
+ * q_absorbed, q_pe, caches: as for mla_decode_partial, 16-bit caches only
+ * shared_table: device [P / block_size] int32 (a row of block_table, for
+ *               requests whose tables start alike)
+ * out         : device [B, q_len, H, 512] of out_dtype, 16-byte aligned
+ * out_lse     : device [B, q_len, H] fp32, or NULL
+ * Programmatic dependent launches. No counterpart on the pages.
+ */
+mla_status_t mla_decode_shared(const void* q_absorbed, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                               const int32_t* shared_table, const int32_t* block_table, const int32_t* context_lens,
+                               float scale, void* out, float* out_lse, const mla_shared_desc_t* desc);
+
+/* Workspace bytes of mla_decode_shared: the slots' partials, [128, 512] fp32
+ * each, and their LSE. */
+uint64_t mla_decode_shared_workspace_bytes(int32_t num_slots);
+
+/*
  * mla_check_device_errors -- synchronize `stream`, read and clear the device
  * error word the kernels set (bit 0: a bounded wait timed out; bit 1: a page
  * id outside the pool; bit 2: a kernel found its launch unusable -- the
@@ -927,7 +1027,8 @@ mla_status_t mla_selfcheck(float* max_abs_err);
 #define MLA_CTR_DECODE_Q8 7 /* mla_decode_q8 calls */
 #define MLA_CTR_STEP 8 /* mla_update_tables and mla_cache_append_slots launches */
 #define MLA_CTR_PREFILL 9 /* mla_expand_kv and mla_prefill calls */
-#define MLA_NUM_COUNTERS 10
+#define MLA_CTR_DECODE_SHARED 10 /* mla_decode_shared calls */
+#define MLA_NUM_COUNTERS 11
 /* mla_get_counters -- copy min(n, MLA_NUM_COUNTERS) counters to out (host). */
 void mla_get_counters(uint64_t* out, int32_t n);
 void mla_reset_counters(void);

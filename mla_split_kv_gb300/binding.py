@@ -31,8 +31,8 @@ MLA_MERGE_ENTRIES, MLA_MERGE_PARTIALS = 0, 1
 MLA_DECODE_MERGE_ENTRIES, MLA_DECODE_MERGE_TICKETS = 0, 1
 MLA_SCORE_EXCHANGE_EXACT, MLA_SCORE_EXCHANGE_F16, MLA_SCORE_EXCHANGE_NONE, MLA_SCORE_EXCHANGE_F32 = 0, 1, 2, 3
 
-CTR_PARTIAL_SIMT, CTR_PARTIAL_TC, CTR_MERGE, CTR_REJECTED, CTR_CTAS, CTR_DECODE_FUSED, CTR_WRAP, CTR_DECODE_Q8, CTR_STEP, CTR_PREFILL = range(10)
-NUM_COUNTERS = 10
+CTR_PARTIAL_SIMT, CTR_PARTIAL_TC, CTR_MERGE, CTR_REJECTED, CTR_CTAS, CTR_DECODE_FUSED, CTR_WRAP, CTR_DECODE_Q8, CTR_STEP, CTR_PREFILL, CTR_DECODE_SHARED = range(11)
+NUM_COUNTERS = 11
 
 DTYPE_CODES = {"f16": MLA_F16, "bf16": MLA_BF16, "f32": MLA_F32, "e4m3": MLA_E4M3}
 
@@ -154,6 +154,45 @@ class mla_prefill_desc_t(ctypes.Structure):
     ]
 
 
+class mla_shared_item_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("row0", "rows", "request", "t0", "t1", "slot")] + [("reserved", ctypes.c_int32 * 2)]
+
+
+class mla_shared_plan_t(ctypes.Structure):
+    _fields_ = [
+        ("shared_tokens", ctypes.c_int32),
+        ("item_capacity", ctypes.c_int32),
+        ("items", ctypes.POINTER(mla_shared_item_t)),
+        ("own_indptr", ctypes.POINTER(ctypes.c_int32)),
+        ("num_items", ctypes.c_int32),
+        ("num_slots", ctypes.c_int32),
+        ("shared_parts", ctypes.c_int32),
+    ]
+
+
+class mla_shared_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("num_requests", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("q_len", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("max_blocks_per_req", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("shared_tokens", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("items", ctypes.c_void_p),
+        ("own_indptr", ctypes.c_void_p),
+        ("num_items", ctypes.c_int32),
+        ("num_slots", ctypes.c_int32),
+        ("shared_parts", ctypes.c_int32),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_uint64),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -206,6 +245,13 @@ def load() -> ctypes.CDLL:
     lib.mla_prefill.restype = i32
     lib.mla_prefill_workspace_bytes.argtypes = [ctypes.POINTER(mla_device_info_t), i32, i32, i32]
     lib.mla_prefill_workspace_bytes.restype = u64
+    lib.mla_plan_shared.argtypes = [ctypes.POINTER(i32), i32, i32, i32, i32, ctypes.POINTER(mla_device_info_t),
+                                    ctypes.POINTER(mla_shared_plan_t)]
+    lib.mla_plan_shared.restype = i32
+    lib.mla_decode_shared.argtypes = [vp] * 7 + [f32, vp, vp, ctypes.POINTER(mla_shared_desc_t)]
+    lib.mla_decode_shared.restype = i32
+    lib.mla_decode_shared_workspace_bytes.argtypes = [i32]
+    lib.mla_decode_shared_workspace_bytes.restype = u64
     lib.mla_merge_unembed.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp]
     lib.mla_merge_unembed.restype = i32
     lib.mla_decode_unembed.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, vp, vp, vp, vp, i32, i32, vp, i32,
@@ -424,6 +470,48 @@ def mla_prefill(q_nope: int, q_pe: int, k_nope: int, k_pe: int, v: int, q_indptr
 
 def mla_prefill_workspace_bytes(dev: mla_device_info_t, num_requests: int, num_heads: int, max_q_tokens: int) -> int:
     return int(load().mla_prefill_workspace_bytes(ctypes.byref(dev), num_requests, num_heads, max_q_tokens))
+
+
+class SharedPlan:
+    """Host result of :func:`mla_plan_shared`."""
+
+    def __init__(self, items, own_indptr, num_slots, shared_parts):
+        self.items = items  # list of (row0, rows, request, t0, t1, slot)
+        self.own_indptr = own_indptr  # first slot of each request's group of 128 rows
+        self.num_slots = num_slots
+        self.shared_parts = shared_parts
+
+
+def mla_plan_shared(context_lens: Sequence[int], shared_tokens: int, num_heads: int, q_len: int, block_size: int,
+                    dev: mla_device_info_t) -> SharedPlan:
+    lib = load()
+    B = len(context_lens)
+    lens = (ctypes.c_int32 * B)(*[int(x) for x in context_lens])
+    plan = mla_shared_plan_t()
+    plan.shared_tokens = shared_tokens
+    st = lib.mla_plan_shared(lens, B, num_heads, q_len, block_size, ctypes.byref(dev), ctypes.byref(plan))
+    if st not in (MLA_OK, MLA_ERR_CAPACITY):
+        raise MlaError(st, "mla_plan_shared")
+    items = (mla_shared_item_t * max(1, plan.num_items))()
+    indptr = (ctypes.c_int32 * (B * -(-q_len * num_heads // 128) + 1))()
+    plan.item_capacity = plan.num_items
+    plan.items = ctypes.cast(items, ctypes.POINTER(mla_shared_item_t))
+    plan.own_indptr = ctypes.cast(indptr, ctypes.POINTER(ctypes.c_int32))
+    _check(lib.mla_plan_shared(lens, B, num_heads, q_len, block_size, ctypes.byref(dev), ctypes.byref(plan)),
+           "mla_plan_shared")
+    out = [(x.row0, x.rows, x.request, x.t0, x.t1, x.slot) for x in items[: plan.num_items]]
+    return SharedPlan(out, list(indptr), plan.num_slots, plan.shared_parts)
+
+
+def mla_decode_shared(q_absorbed: int, q_pe: int, ckv_cache: int, kpe_cache: int, shared_table: int, block_table: int,
+                      context_lens: int, scale: float, out: int, out_lse: Optional[int],
+                      desc: mla_shared_desc_t) -> None:
+    _check(load().mla_decode_shared(q_absorbed, q_pe, ckv_cache, kpe_cache, shared_table, block_table, context_lens,
+                                    scale, out, out_lse or None, desc), "mla_decode_shared")
+
+
+def mla_decode_shared_workspace_bytes(num_slots: int) -> int:
+    return int(load().mla_decode_shared_workspace_bytes(num_slots))
 
 
 def mla_merge_unembed(partials: int, lse: int, o_indptr: int, B: int, q_len: int, num_heads: int, w_uv_t: int,

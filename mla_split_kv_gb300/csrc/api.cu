@@ -1026,15 +1026,15 @@ mla_status_t mla_decode_q8(const void* q_absorbed, const void* q_pe, const void*
 
 mla_status_t mla_check_device_errors(void* stream, uint32_t* code_out) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
-  uint32_t a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, h = 0, k = 0, l = 0, m = 0, n = 0;
+  uint32_t a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, h = 0, k = 0, l = 0, m = 0, n = 0, o = 0;
   if (mla::simt_read_clear_error(&a) != cudaSuccess || mla::tc_read_clear_error(&b) != cudaSuccess ||
       mla::tc128_read_clear_error(&c) != cudaSuccess || mla::mh_read_clear_error(&e) != cudaSuccess ||
       mla::wrap_read_clear_error(&f) != cudaSuccess || mla::mh_nx_read_clear_error(&g) != cudaSuccess ||
       mla::append_q8_read_clear_error(&h) != cudaSuccess || mla::decode_q8_read_clear_error(&k) != cudaSuccess ||
       mla::step_tables_read_clear_error(&l) != cudaSuccess || mla::expand_read_clear_error(&m) != cudaSuccess ||
-      mla::prefill_read_clear_error(&n) != cudaSuccess)
+      mla::prefill_read_clear_error(&n) != cudaSuccess || mla::decode_shared_read_clear_error(&o) != cudaSuccess)
     return MLA_ERR_CUDA;
-  const uint32_t code = a | b | c | e | f | g | h | k | l | m | n;
+  const uint32_t code = a | b | c | e | f | g | h | k | l | m | n | o;
   if (code_out != nullptr) *code_out = code;
   if (code != 0 && !clear_static_workspace()) return MLA_ERR_CUDA;
   if (code & mla::MLA_DEVERR_TIMEOUT) return MLA_ERR_TIMEOUT;

@@ -1,0 +1,602 @@
+// Decode attention of a batch whose contexts start with the same tokens, sm_103a.
+//
+// Absorbed latent attention (keys [ckv | kpe], values ckv) of B requests of q_len rows and H heads each, of whose tokens
+// the first P are common: those are read and multiplied once, for all rows of the batch in groups of 128, and each
+// request's own tokens once for its own rows:
+//   s_t = scale (q_abs . ckv_t + q_pe . kpe_t),  out = sum_t softmax(s)_t ckv_t,  lse = log2 sum_t exp(s_t)
+// over pieces of either, merged by their LSE. 2176 operations a (row, token): with the 1152 bytes of a token shared by
+// 128 rows or more, the common part is tensor-core bound, each CTA's own shared memory right behind.
+//
+// An item is a group of up to 128 rows and a run of tokens, as two units: one CTA computes the scores of the group and
+// one half of the value columns (O for all 512 would fill tensor memory), so that CTAs share nothing and wait for
+// none. Tiles of 64 tokens; a unit's tensor memory: O [128 x 256] fp32, S [128 x 64] fp32, and 384 of the 576 query
+// columns as the score product's A operand (the other 192 are in shared memory, 48 KB). The probabilities go through
+// 16 KB of shared memory, so S is free again once it has been read, and one buffer is enough: the products go
+//   S(i+1) PV(i) S(i+2) PV(i+1) ...
+// and S(i)'s softmax runs beside PV(i-1) and S(i+1). A tile is 72 KB: the half of its latents that only the score
+// product reads, with the rotary keys (two slots of 40 KB, free after S), and the half that is the values too (a ring
+// of five pieces of 128 columns, 16 KB, free after PV): what the next score product needs last has been on its way
+// longest.
+//
+// The running maximum moves only when a tile's passes it by more than 2^8; sums are of the unrounded weights, in fp32;
+// the weights are rounded once to the cache's type (2^-12 of themselves in fp16, 2^-9 in bf16: as the 16-bit output).
+// Tokens that some row of a group does not see (behind a shorter context or, in a window, behind the row) have weight 0
+// there, and values that are not finite are taken out of such tiles: for a row that does see one of them its score has
+// already made the weight so.
+//
+// Units are laid out by the host plan, longest first, and taken in turns. The merge is a kernel of its own.
+//
+// Warps: 0-3 softmax, queries and partial output (thread = row), 4 products, 5 loads.
+#include <type_traits>
+
+#include "device_common.cuh"
+#include "umma_issue.cuh"
+
+namespace mla {
+
+namespace {
+
+constexpr int kT = 64;                    // tokens a tile
+constexpr int kRows = 128;
+constexpr int kHalf = kRank / 2;          // value columns of a unit
+constexpr int kOther = kT * kHalf * 2;    // 32 KB: the other half of a tile's latents
+constexpr int kPe = kT * kRope * 2;       // 8 KB
+constexpr int kSlotA = kOther + kPe;
+constexpr int kPiece = kT * 128 * 2;      // 16 KB: 128 of the unit's own columns
+constexpr int kRingB = 5;
+constexpr int kQChunk = kRows * 128;      // 16 KB: [128 rows x 64 columns]
+constexpr int kQTmemBlocks = 6;           // blocks of 64 query columns in tensor memory; the last two and the rotary one are not
+constexpr int kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kThreads = 256;             // (two warps have nothing to do)
+constexpr float kTau = 8.0f;
+constexpr uint32_t kOffP = 3 * kQChunk;
+constexpr uint32_t kOffA = kOffP + kQChunk;
+constexpr uint32_t kOffB = kOffA + 2 * kSlotA;
+constexpr uint32_t kOffSmall = kOffB + kRingB * kPiece;
+constexpr uint32_t kSmem = kOffSmall + 1024 + 1024;
+static_assert(kSmem <= 232448, "shared memory per CTA");
+constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemQ = 320;
+
+struct Small {
+  uint64_t a_full[2], a_empty[2], b_full[kRingB], b_empty[kRingB], q_full, s_full, s_empty, p_full, pv_done, drain;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+static_assert(sizeof(Small) <= 1024, "small smem region");
+
+__device__ __forceinline__ void tma_load_pages(void* dst, const CUtensorMap* map, int32_t block, int32_t group, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(0), "r"(0), "r"(block), "r"(group), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, int32_t y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(0), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
+  tmem_ld16(taddr, v);
+  tmem_ld16(taddr + 16, v + 16);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+struct Unit {
+  int row0, rows, request, t0, t1, slot, half, tiles, least;  // least: tokens that every row of the group sees
+};
+
+// Tokens that flat row `row` ([B, q_len, H]) sees.
+__device__ __forceinline__ int visible(const SharedParams& p, int row) {
+  const int per = p.q_len * p.H, b = row / per;
+  const int L = max(p.context_lens[b], 0);
+  return p.causal ? max(0, L - p.q_len + (row % per) / p.H + 1) : L;
+}
+
+// The k-th unit of this CTA, by a whole warp: in turns, every second one backwards. False behind the last one.
+__device__ __forceinline__ bool unit_of(const SharedParams& p, int k, int lane, Unit& w, bool& skip) {
+  const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+  const int u = k * g + ((k & 1) ? g - 1 - c : c);
+  skip = u >= 2 * p.num_items;
+  if (skip) return k * g < 2 * p.num_items;
+  const int4* const at = reinterpret_cast<const int4*>(p.items) + 2 * (u >> 1);
+  const int4 x = __ldg(at), y = __ldg(at + 1);
+  w.row0 = x.x;
+  w.rows = max(0, min(min(x.y, kRows), p.rows - x.x));
+  w.request = x.z;
+  w.t0 = x.w;
+  w.slot = y.y;
+  w.half = u & 1;
+  int most = 0, least = 0x7fffffff;
+  for (int r = lane; r < w.rows; r += 32) {
+    const int v = visible(p, w.row0 + r);
+    most = max(most, v);
+    least = min(least, v);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  w.least = __reduce_min_sync(0xffffffffu, least);
+  w.t1 = max(w.t0, min(min(y.x, most), w.request < 0 ? p.shared_tokens : 0x7fffffff));
+  w.tiles = (w.t1 - w.t0 + kT - 1) / kT;
+  return true;
+}
+
+// Values that are not finite in the unit's pieces of a tile (two of [64 tokens x 128 columns]) become 0.
+template <bool BF16>
+__device__ __forceinline__ void clean_values(uint8_t* p0, uint8_t* p1, int r) {
+  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+#pragma unroll 4
+  for (int it = 0; it < 16; ++it) {
+    const int idx = it * kRows + r;  // 16-byte pieces, 1024 a piece
+    const uint32_t at = smem_u32((idx >= 1024 ? p1 : p0) + (idx & 1023) * 16);
+    const uint4 v = lds128(at);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & (kExp * 0x10001u));
+    if (__builtin_expect((m & 0xffffu) == kExp || (m >> 16) == kExp, 0)) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if ((w[j] & kExp) == kExp) w[j] &= 0xffff0000u;
+        if ((w[j] & (kExp << 16)) == (kExp << 16)) w[j] &= 0xffffu;
+      }
+      sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_decode_shared_kernel(const __grid_constant__ CUtensorMap tm_half, const __grid_constant__ CUtensorMap tm_piece,
+                             const __grid_constant__ CUtensorMap tm_kpe, const SharedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = align1024(smem_raw);
+  Small* const sm = reinterpret_cast<Small*>(smem + kOffSmall);
+  volatile int32_t* const abort_flag = &sm->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm->a_full[s], 1);
+      mbar_init(&sm->a_empty[s], 1);
+    }
+    for (int s = 0; s < kRingB; ++s) {
+      mbar_init(&sm->b_full[s], 1);
+      mbar_init(&sm->b_empty[s], 1);
+    }
+    mbar_init(&sm->q_full, 4);
+    mbar_init(&sm->s_full, 1);
+    mbar_init(&sm->s_empty, 4);
+    mbar_init(&sm->p_full, 4);
+    mbar_init(&sm->pv_done, 1);
+    mbar_init(&sm->drain, 1);
+    sm->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sm->tmem_base, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem_base;
+  const uint64_t tmo = p.timeout_ns;
+  Unit w;
+  bool skip;
+
+  if (warp == kLoadWarp) {
+    // ---------------------------------------------------------------- loads
+    uint32_t tile = 0, piece = 0;
+    bool ok = true;
+    for (int k = 0; ok && unit_of(p, k, lane, w, skip); ++k) {
+      if (skip) continue;
+      const int32_t* const table = w.request < 0 ? p.shared_table : p.block_table + static_cast<long long>(w.request) * p.max_blocks;
+      const int columns = w.request < 0 ? p.shared_tokens / p.bs : p.max_blocks;
+      for (int i = 0; i < w.tiles && ok; ++i, ++tile) {
+        const int tok = w.t0 + i * kT;
+        const int pages = (min(kT, w.t1 - tok) + p.bs - 1) / p.bs;  // (tok starts a page)
+        int pid = -1;
+        if (lane < pages) {
+          const int col = tok / p.bs + lane;
+          pid = col < columns ? __ldg(table + col) : -1;
+          if (pid < 0 || pid >= p.num_blocks) {
+            flag_error(MLA_DEVERR_BAD_PAGE);
+            pid = -1;  // (lies before the cache: zeros)
+          }
+        }
+        const int group = pid * (p.bs / 8);
+        const uint32_t s = tile & 1;
+        if (tile >= 2) ok = mbar_wait_warp(&sm->a_empty[s], ((tile >> 1) - 1) & 1, tmo);
+        if (!ok) break;
+        uint8_t* const a = smem + kOffA + s * kSlotA;
+        if (lane == 0) mbar_arrive_expect_tx(&sm->a_full[s], pages * p.bs * (kHalf + kRope) * 2);
+        __syncwarp();
+        if (lane < pages) {
+          tma_load_rows(a + kOther + lane * p.bs * 128, &tm_kpe, pid * p.bs, &sm->a_full[s]);
+          tma_load_pages(a + lane * p.bs * (kHalf * 2), &tm_half, 4 * (w.half ^ 1), group, &sm->a_full[s]);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x, ++piece) {
+          const uint32_t b = piece % kRingB;
+          if (piece >= kRingB) ok = ok && mbar_wait_warp(&sm->b_empty[b], (piece / kRingB - 1) & 1, tmo);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sm->b_full[b], pages * p.bs * 256);
+          __syncwarp();
+          if (lane < pages)
+            tma_load_pages(smem + kOffB + b * kPiece + lane * p.bs * 256, &tm_piece, 4 * w.half + 2 * x, group, &sm->b_full[b]);
+        }
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- products: the warp in step (umma_issue.cuh)
+    const uint32_t leader = elect_one();
+    const uint32_t idesc_s = idesc_f16_f32(kRows, kT, BF16, false, false);
+    const uint32_t idesc_o = idesc_f16_f32(kRows, 128, BF16, false, true);
+    const uint64_t q0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t p0 = smem_desc_sw128(smem_u32(smem + kOffP), 16, 1024);
+    const uint64_t a0 = smem_desc_sw128(smem_u32(smem + kOffA), 16, 4096);           // the other half, rows of tokens
+    const uint64_t pe0 = smem_desc_sw128(smem_u32(smem + kOffA + kOther), 16, 1024);
+    const uint64_t k0 = smem_desc_sw128(smem_u32(smem + kOffB), 16, 2048);           // a piece as keys
+    const uint64_t v0 = smem_desc_sw128(smem_u32(smem + kOffB), 1024, 2048);         // and as values
+    uint32_t tile0 = 0, unit = 0;
+    bool ok = true;
+    auto block = [&](int cb, uint64_t keys, uint32_t first) {  // a block of 64 latent columns
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (cb < kQTmemBlocks)
+          issue_ts(leader, tmem + kTmemS, tmem + kTmemQ + 32 * cb + 8 * kk, keys + 2 * kk, idesc_s, first == 0 || kk > 0);
+        else
+          issue_ss(leader, tmem + kTmemS, q0 + (cb - kQTmemBlocks) * (kQChunk / 16) + 2 * kk, keys + 2 * kk, idesc_s, 1);
+      }
+    };
+    auto scores = [&](int i, auto half_of) {
+      constexpr int half = decltype(half_of)::value;
+      const uint32_t t = tile0 + i, s = t & 1;
+      if (t > 0) ok = ok && mbar_wait_warp(&sm->s_empty, (t - 1) & 1, tmo);
+      ok = ok && mbar_wait_warp(&sm->a_full[s], (t >> 1) & 1, tmo);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t pe = pe0 + s * (kSlotA / 16), a = a0 + s * (kSlotA / 16);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) issue_ss(leader, tmem + kTmemS, q0 + 2 * (kQChunk / 16) + 2 * kk, pe + 2 * kk, idesc_s, kk > 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) block(4 * (half ^ 1) + j, a + j * 64, 0);
+      issue_commit(leader, &sm->a_empty[s]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t pc = 2 * t + x, b = pc % kRingB;
+        ok = ok && mbar_wait_warp(&sm->b_full[b], (pc / kRingB) & 1, tmo);
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) block(4 * half + 2 * x + j, k0 + b * (kPiece / 16) + j * 64, 0);
+      }
+      issue_commit(leader, &sm->s_full);
+    };
+    auto values = [&](int i) {
+      const uint32_t t = tile0 + i;
+      ok = ok && mbar_wait_warp(&sm->p_full, t & 1, tmo);
+      if (!ok) return;
+      tc_fence_after();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t pc = 2 * t + x, b = pc % kRingB;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          issue_ss(leader, tmem + kTmemO + 128 * x, p0 + 2 * kk, v0 + b * (kPiece / 16) + kk * 256, idesc_o, i > 0 || kk > 0);
+        if (x == 0) issue_commit(leader, &sm->b_empty[b]);
+      }
+      issue_commit(leader, &sm->pv_done);
+      issue_commit(leader, &sm->b_empty[(2 * t + 1) % kRingB]);
+    };
+    for (int k = 0; ok && unit_of(p, k, lane, w, skip); ++k) {
+      if (skip || w.tiles == 0) continue;
+      ok = mbar_wait_warp(&sm->q_full, unit & 1, tmo);
+      ++unit;
+      auto run = [&](auto half_of) {
+        if (ok) scores(0, half_of);
+        for (int i = 0; i < w.tiles && ok; ++i) {
+          if (i + 1 < w.tiles) scores(i + 1, half_of);
+          values(i);
+        }
+      };
+      if (w.half == 0) run(std::integral_constant<int, 0>{});
+      else run(std::integral_constant<int, 1>{});
+      tile0 += w.tiles;
+    }
+    if (!ok) *abort_flag = 1;
+    __syncwarp();
+    issue_commit(leader, &sm->drain);  // every product is done before tensor memory is freed
+    mbar_wait(&sm->drain, 0, kDrainTimeoutNs);
+    __syncwarp();
+  } else if (warp < kMmaWarp) {
+    // ---------------------------------------------------------------- softmax: thread = row
+    const int r = tid;
+    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    const float scale = p.scale_log2;
+    uint32_t tile0 = 0;
+    bool ok = true;
+    for (int k = 0; ok && unit_of(p, k, lane, w, skip); ++k) {
+      if (skip) continue;
+      const bool real = r < w.rows;
+      const long long row = w.row0 + (real ? r : 0);
+      const long long slot_row = static_cast<long long>(w.slot) * kRows + r;
+      if (w.tiles == 0) {
+        if (real && w.half == 0) p.part_lse[slot_row] = -INFINITY;  // (the merge does not read the values)
+        continue;
+      }
+      {  // the queries: the products of the unit before are done
+        const uint4* const src = reinterpret_cast<const uint4*>(p.q_abs + row * kRank);
+        const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int g = 0; g < kQTmemBlocks * 2; ++g) {  // 32 columns a step
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 x = real ? src[4 * g + j] : none;
+            v[4 * j] = __uint_as_float(x.x);
+            v[4 * j + 1] = __uint_as_float(x.y);
+            v[4 * j + 2] = __uint_as_float(x.z);
+            v[4 * j + 3] = __uint_as_float(x.w);
+          }
+          tmem_st16(tmem + lanes + kTmemQ + 16 * g, v);
+        }
+        const uint4* const pe = reinterpret_cast<const uint4*>(p.q_pe + row * kRope);
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4 x = !real ? none : c < 2 ? src[8 * (kQTmemBlocks + c) + j] : pe[j];
+            sts128(smem_u32(smem) + c * kQChunk + r * 128 + ((j ^ (r & 7)) << 4), x);
+          }
+        }
+        tmem_wait_st();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->q_full);
+      }
+      const int seen = real ? visible(p, static_cast<int>(row)) : 0x7fffffff;
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < w.tiles; ++i) {
+        const uint32_t t = tile0 + i;
+        const int tok = w.t0 + i * kT;
+        ok = mbar_wait_warp(&sm->s_full, t & 1, tmo);
+        if (!ok) break;
+        tc_fence_after();
+        float x[kT];
+        ld32(tmem + lanes + kTmemS, x);
+        ld32(tmem + lanes + kTmemS + 32, x + 32);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->s_empty);
+        const int limit = min(w.t1, w.least);  // tokens that every row sees
+        const bool masked = tok + kT > limit;
+        float f = scale;
+        if (masked) {
+          const int nvis = min(seen, w.t1) - tok;
+#pragma unroll
+          for (int j = 0; j < kT; ++j) x[j] = j < nvis ? x[j] * scale : -INFINITY;
+          f = 1.f;
+        }
+        float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int j = 4; j < kT; j += 4) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], x[j + q]);
+        }
+        // (a negative scale: the largest score is the smallest product's)
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
+        if (!masked && scale < 0.f) {
+          float lo = x[0];
+#pragma unroll
+          for (int j = 1; j < kT; ++j) lo = fminf(lo, x[j]);
+          mx = lo * f;
+        }
+        const bool need = mx > m + kTau;
+        if (i > 0) ok = mbar_wait_warp(&sm->pv_done, (t - 1) & 1, tmo);  // O and the weights' buffer are free
+        if (!ok) break;
+        if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
+          const float m_new = need ? mx : m;
+          const float alpha = need ? (m == -INFINITY ? 0.f : exp2f(m - m_new)) : 1.f;
+          if (i > 0) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < kHalf / 16; ++q) {
+              float o[16];
+              tmem_ld16(tmem + lanes + kTmemO + 16 * q, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] *= alpha;
+              tmem_st16(tmem + lanes + kTmemO + 16 * q, o);
+            }
+            tmem_wait_st();
+          }
+          l *= alpha;
+          m = m_new;
+        }
+        if (masked) {
+          const uint32_t b = 2 * t, c = b + 1;
+          ok = mbar_wait_warp(&sm->b_full[b % kRingB], (b / kRingB) & 1, tmo) && mbar_wait_warp(&sm->b_full[c % kRingB], (c / kRingB) & 1, tmo);
+          if (!ok) break;
+          clean_values<BF16>(smem + kOffB + (b % kRingB) * kPiece, smem + kOffB + (c % kRingB) * kPiece, r);
+        }
+        const float mm = m == -INFINITY ? 0.f : -m;
+        const float2 f2 = make_float2(f, f), m2 = make_float2(mm, mm);
+        float2 sum = make_float2(0.f, 0.f), sum_b = sum;
+        const uint32_t at = smem_u32(smem + kOffP) + r * 128;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t h[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float2 e = fma2(make_float2(x[8 * j + 2 * q], x[8 * j + 2 * q + 1]), f2, m2);
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            if (q & 1) sum_b = add2(sum_b, e);
+            else sum = add2(sum, e);
+            h[q] = pack2<BF16>(e.x, e.y);
+          }
+          sts128(at + ((j ^ (r & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+        }
+        sum = add2(sum, sum_b);
+        l += sum.x + sum.y;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->p_full);
+      }
+      if (!ok) break;
+      ok = mbar_wait_warp(&sm->pv_done, (tile0 + w.tiles - 1) & 1, tmo);
+      if (!ok) break;
+      tc_fence_after();
+      const bool any = m != -INFINITY;
+      const float inv = any ? 1.f / l : 0.f;
+      float* const out = p.part_o + slot_row * kRank + kHalf * w.half;
+#pragma unroll 1
+      for (int q = 0; q < kHalf / 16; ++q) {
+        float o[16];
+        tmem_ld16(tmem + lanes + kTmemO + 16 * q, o);
+        tmem_wait_ld();
+        if (real) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            reinterpret_cast<float4*>(out + 16 * q)[j] = make_float4(o[4 * j] * inv, o[4 * j + 1] * inv, o[4 * j + 2] * inv, o[4 * j + 3] * inv);
+        }
+      }
+      if (real && w.half == 0) p.part_lse[slot_row] = any ? m + log2f(l) : (l != l ? l : -INFINITY);
+      tc_fence_before();
+      tile0 += w.tiles;
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  __syncwarp();
+  __syncthreads();
+  if (*abort_flag) settle_in_flight(3000000ull);  // copies in flight land before shared memory goes
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// A warp a row: its parts in order (the common tokens' pieces, then its own tokens'), M = max lse, weights 2^(lse - M).
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) mla_decode_shared_merge_kernel(const SharedParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  const int per = p.q_len * p.H, b = row / per, r = row % per;
+  const int own = b * ((per + kRows - 1) / kRows) + r / kRows;
+  const int s0 = p.own_indptr[own], n_own = p.own_indptr[own + 1] - s0;
+  const int n = p.shared_parts + n_own;
+  // the row of part j in the slots
+  auto at = [&](int j) -> long long {
+    return j < p.shared_parts ? (static_cast<long long>(row / kRows) * p.shared_parts + j) * kRows + row % kRows
+                              : static_cast<long long>(s0 + j - p.shared_parts) * kRows + r % kRows;
+  };
+  float M = -INFINITY;
+  for (int j = lane; j < n; j += 32) M = max_nan(M, p.part_lse[at(j)]);
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float4 acc[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
+  if (M != -INFINITY) {
+    for (int j0 = 0; j0 < n; j0 += 4) {
+      float wj[4];
+      float4 v[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const long long a = at(min(j0 + j, n - 1));
+        const float lj = j0 + j < n ? p.part_lse[a] : -INFINITY;
+        wj[j] = lj == -INFINITY ? 0.f : exp2f(lj - M);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          v[j][c] = lj != -INFINITY ? reinterpret_cast<const float4*>(p.part_o + a * kRank)[lane + 32 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        den += wj[j];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[c].x = fmaf(wj[j], v[j][c].x, acc[c].x);
+          acc[c].y = fmaf(wj[j], v[j][c].y, acc[c].y);
+          acc[c].z = fmaf(wj[j], v[j][c].z, acc[c].z);
+          acc[c].w = fmaf(wj[j], v[j][c].w, acc[c].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(acc[c].x / den, acc[c].y / den, acc[c].z / den, acc[c].w / den);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) store_out4(p.out, p.out_dtype, static_cast<long long>(row) * kRank + 4 * (lane + 32 * c), acc[c]);
+  if (lane == 0 && p.out_lse != nullptr) p.out_lse[row] = merged_lse(M, den);
+}
+
+cudaError_t launch_dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, unsigned grid, unsigned block, size_t smem,
+                             cudaStream_t stream) {
+  cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& tm_piece, const CUtensorMap& tm_kpe,
+                                 const SharedParams& p, bool bf16, int sms, cudaStream_t stream) {
+  static DeviceOnce once_f16, once_bf16;
+  const void* const fn = bf16 ? reinterpret_cast<const void*>(&mla_decode_shared_kernel<true>)
+                              : reinterpret_cast<const void*>(&mla_decode_shared_kernel<false>);
+  cudaError_t e = set_attribute_once(bf16 ? once_bf16 : once_f16, fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  const int units = 2 * p.num_items;
+  launch_dependent(cfg, attr, units < sms ? units : sms, kThreads, kSmem, stream);
+  e = bf16 ? cudaLaunchKernelEx(&cfg, mla_decode_shared_kernel<true>, tm_half, tm_piece, tm_kpe, p)
+           : cudaLaunchKernelEx(&cfg, mla_decode_shared_kernel<false>, tm_half, tm_piece, tm_kpe, p);
+  if (e != cudaSuccess) return e;
+  launch_dependent(cfg, attr, (p.rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32), kMergeThreads, 0, stream);
+  return cudaLaunchKernelEx(&cfg, mla_decode_shared_merge_kernel, p);
+}
+
+cudaError_t decode_shared_read_clear_error(uint32_t* out) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
+}
+
+}  // namespace mla

@@ -320,12 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
         if (w.fresh) {
-          ok = mbar_wait(&sm->a_full, block & 1, tmo);
+          ok = mbar_wait_warp(&sm->a_full, block & 1, tmo);
           ++block;
         }
         const int buf = i & 1;
-        if (i >= 2) ok = ok && mbar_wait_cluster(&sm->t_empty[buf], ((i >> 1) - 1) & 1, tmo);
-        if (!ok || *abort_flag) {
+        if (i >= 2) ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&sm->t_empty[buf], ((i >> 1) - 1) & 1, tmo));
+        if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
           ok = false;
           break;
         }
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kChunks; ++c, ++use) {
             const int s = c % kStages;  // (a tile's chunks go round the ring a whole number of times)
-            ok = ok && mbar_wait(&sm->full[s], (use / kStages) & 1, tmo);
+            ok = ok && mbar_wait_warp(&sm->full[s], (use / kStages) & 1, tmo);
             const uint64_t a = a0 + c * (kAChunk / 16), b = b0 + s * (kStage / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) issue2_ss(leader, d, a + 2 * kk, b + step * kk, idesc, c > 0 || kk > 0);

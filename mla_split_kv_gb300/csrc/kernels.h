@@ -289,6 +289,29 @@ cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, cons
                            int sms, cudaStream_t stream);
 cudaError_t prefill_read_clear_error(uint32_t* out);
 
+// A batch whose contexts start with the same tokens (mla_decode_shared). Maps over the [rows, 512] cache as (64 columns,
+// 8 rows, 8 column blocks, row groups), a page high, four (tm_half) and two (tm_piece) column blocks a box, and over
+// the [rows, 64] one, 128-byte swizzle.
+struct SharedParams {
+  const uint16_t* q_abs;       // [rows, 512]
+  const uint16_t* q_pe;        // [rows, 64]
+  const int32_t* shared_table; // [shared_tokens / bs]
+  const int32_t* block_table;  // [B, max_blocks]
+  const int32_t* context_lens; // [B]
+  const int32_t* items;        // eight words an item (mla_shared_item_t)
+  const int32_t* own_indptr;   // [B * groups of a request + 1]
+  void* out;                   // [rows, 512] of out_dtype
+  float* out_lse;              // [rows] or null
+  float* part_o;               // [slots, 128, 512]
+  float* part_lse;             // [slots, 128]
+  float scale_log2;
+  int32_t B, H, q_len, rows, bs, max_blocks, num_blocks, causal, shared_tokens, shared_parts, num_items, out_dtype;
+  uint64_t timeout_ns;
+};
+cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& tm_piece, const CUtensorMap& tm_kpe,
+                                 const SharedParams& p, bool bf16, int sms, cudaStream_t stream);
+cudaError_t decode_shared_read_clear_error(uint32_t* out);
+
 // What the files of entry points share (api.cu).
 void count_launch(int counter, uint64_t n = 1);
 int32_t rejected(int32_t status);  // counts it and gives it back

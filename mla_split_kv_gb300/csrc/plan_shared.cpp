@@ -1,0 +1,135 @@
+// Work of a batch whose contexts start with the same tokens (host only, no GPU access).
+//
+// The common tokens are cut into pieces for every group of 128 of the batch's rows, each request's own tokens for its
+// own groups, all pieces about equally long: a piece is two units of work (one half of the value columns each), the
+// units go to the SMs longest first, and the length is the one among some tried whose busiest SM and merge are done
+// first.
+#include <algorithm>
+#include <cstdint>
+#include <functional>
+#include <queue>
+#include <vector>
+
+#include "kernels.h"
+#include "mla_split_kv.h"
+
+namespace {
+
+constexpr int64_t kTile = 64;   // tokens
+constexpr int64_t kGroup = 128; // rows
+// A unit's time in tiles of about 1.1 us: its tiles, and the start and the end (queries, the first loads, the partial
+// output). A row's part costs the merge about 2 KB of L2, of which the device reads 5 MB in the time of a tile.
+constexpr int64_t kUnitTiles = 5;
+constexpr int64_t kMergeParts = 2500;
+
+struct Piece {
+  int64_t row0, rows;
+  int32_t request;
+  int64_t t0, t1, tiles, slot;
+};
+
+int64_t tiles_of(int64_t tokens) { return (tokens + kTile - 1) / kTile; }
+// Pieces of about `length` tiles, none longer.
+int64_t pieces_of(int64_t tiles, int64_t length) { return std::max<int64_t>(1, (tiles + length - 1) / length); }
+
+}  // namespace
+
+extern "C" mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_t B, int32_t num_heads, int32_t q_len,
+                                        int32_t block_size, const mla_device_info_t* dev, mla_shared_plan_t* plan) try {
+  if (context_lens_host == nullptr || dev == nullptr || plan == nullptr) return MLA_ERR_INVALID_ARG;
+  if (B < 1 || dev->num_sms < 1 || plan->item_capacity < 0) return MLA_ERR_INVALID_ARG;
+  if (num_heads != 16 && num_heads != 64 && num_heads != 128) return MLA_ERR_UNSUPPORTED;
+  if (q_len < 1 || q_len > MLA_MAX_Q_LEN) return MLA_ERR_UNSUPPORTED;
+  if (block_size != 16 && block_size != 32 && block_size != 64) return MLA_ERR_UNSUPPORTED;
+  const int64_t P = plan->shared_tokens;
+  if (P < block_size || P % block_size != 0) return MLA_ERR_INVALID_ARG;
+  const int64_t per = static_cast<int64_t>(q_len) * num_heads, rows = per * B;
+  if (rows > (1ll << 28)) return MLA_ERR_UNSUPPORTED;
+  int64_t longest = 0;
+  for (int32_t b = 0; b < B; ++b) {
+    if (context_lens_host[b] < 0) return MLA_ERR_INVALID_ARG;
+    longest = std::max<int64_t>(longest, context_lens_host[b]);
+  }
+  const int64_t groups = (rows + kGroup - 1) / kGroup, own_groups = (per + kGroup - 1) / kGroup;
+  const int64_t common = tiles_of(P);
+  std::vector<int64_t> own(B);
+  int64_t all = groups * common, most = common;
+  for (int32_t b = 0; b < B; ++b) {
+    own[b] = tiles_of(std::max<int64_t>(0, context_lens_host[b] - P));
+    all += own_groups * own[b];
+    most = std::max(most, own[b]);
+  }
+
+  // tile counts a piece may have, around an even share of one SM's two units at a time
+  const int64_t share = std::max<int64_t>(1, 2 * all / dev->num_sms);
+  int64_t best = most, best_cost = -1;
+  for (int64_t eighths : {2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 16}) {
+    const int64_t length = std::min(most, std::max<int64_t>(2, (share * eighths + 7) / 8));
+    // lengths of the units, counted: the pieces of one run are equally long but for the last
+    std::vector<std::pair<int64_t, int64_t>> units;  // tiles, how many
+    int64_t parts = 0;
+    auto add = [&](int64_t tiles, int64_t times, int64_t rows_of) {
+      const int64_t n = pieces_of(tiles, length), each = (tiles + n - 1) / n;
+      units.emplace_back(each, 2 * times * n);
+      parts += n * rows_of;
+    };
+    add(common, groups, rows);
+    for (int32_t b = 0; b < B; ++b) add(own[b], own_groups, per);
+    std::sort(units.begin(), units.end(), std::greater<>());
+    int64_t busiest = 0;
+    std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
+    for (int32_t i = 0; i < dev->num_sms; ++i) ends.push(0);
+    for (const auto& u : units) {
+      for (int64_t i = 0; i < u.second; ++i) {
+        const int64_t end = ends.top() + u.first + kUnitTiles;
+        ends.pop();
+        ends.push(end);
+        busiest = std::max(busiest, end);
+      }
+    }
+    const int64_t cost = busiest + parts / kMergeParts;
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = length;
+    }
+  }
+
+  std::vector<Piece> pieces;
+  int64_t slot = 0;
+  auto cut = [&](int64_t row0, int64_t n_rows, int32_t request, int64_t t0, int64_t tokens, bool open) {
+    const int64_t tiles = tiles_of(tokens), n = pieces_of(tiles, best), each = std::max<int64_t>(1, (tiles + n - 1) / n);
+    for (int64_t j = 0; j < n; ++j) {
+      const int64_t a = std::min(tokens, j * each * kTile), e = std::min(tokens, (j + 1) * each * kTile);
+      const bool last = j + 1 == n;
+      pieces.push_back(Piece{row0, n_rows, request, t0 + a, last && open ? 0x7fffffffll : t0 + e, tiles_of(e - a), slot++});
+    }
+    return n;
+  };
+  int64_t parts = 0;
+  for (int64_t g = 0; g < groups; ++g)
+    parts = cut(g * kGroup, std::min(kGroup, rows - g * kGroup), -1, 0, P, false);
+  std::vector<int64_t> first;
+  for (int32_t b = 0; b < B; ++b) {
+    for (int64_t g = 0; g < own_groups; ++g) {
+      first.push_back(slot);
+      cut(b * per + g * kGroup, std::min(kGroup, per - g * kGroup), b, P, std::max<int64_t>(0, context_lens_host[b] - P), true);
+    }
+  }
+  first.push_back(slot);
+  if (slot > (1ll << 28)) return MLA_ERR_UNSUPPORTED;
+  plan->num_items = static_cast<int32_t>(pieces.size());
+  plan->num_slots = static_cast<int32_t>(slot);
+  plan->shared_parts = static_cast<int32_t>(parts);
+  if (plan->num_items > plan->item_capacity) return MLA_ERR_CAPACITY;
+  if (plan->items == nullptr || plan->own_indptr == nullptr) return MLA_ERR_INVALID_ARG;
+  std::stable_sort(pieces.begin(), pieces.end(), [](const Piece& a, const Piece& b) { return a.tiles > b.tiles; });
+  for (size_t i = 0; i < pieces.size(); ++i) {
+    const Piece& x = pieces[i];
+    plan->items[i] = mla_shared_item_t{static_cast<int32_t>(x.row0), static_cast<int32_t>(x.rows), x.request, static_cast<int32_t>(x.t0),
+                                       static_cast<int32_t>(x.t1), static_cast<int32_t>(x.slot), {0, 0}};
+  }
+  for (size_t i = 0; i < first.size(); ++i) plan->own_indptr[i] = static_cast<int32_t>(first[i]);
+  return MLA_OK;
+} catch (...) {  // out of memory
+  return MLA_ERR_CAPACITY;
+}

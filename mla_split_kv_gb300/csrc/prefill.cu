@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto scores = [&](int s, int i) {  // S of tile i; the first of the subtiles waits for the keys
       const uint32_t x = kTileChunks * (tile0 + i), t = tile0 + i;
       const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
-      if (first) ok = ok && mbar_wait(&sm->k_full[t & 1], (t >> 1) & 1, tmo);
+      if (first) ok = ok && mbar_wait_warp(&sm->k_full[t & 1], (t >> 1) & 1, tmo);
       if (!ok) return;
       tc_fence_after();
 #pragma unroll
@@ -449,10 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto values = [&](int s, int i) {
       const uint32_t x = kTileChunks * (tile0 + i) + 3, t = tile0 + i;
       const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
-      if (first) ok = ok && mbar_wait(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
+      if (first) ok = ok && mbar_wait_warp(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        ok = ok && mbar_wait(&sm->p_full[s][y], pn[s] & 1, tmo);
+        ok = ok && mbar_wait_warp(&sm->p_full[s][y], pn[s] & 1, tmo);
         if (!ok) return;
         tc_fence_after();
         const uint32_t slot = (x + y) % kRing;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (w.tiles[s] == 0 || !ok) continue;
-        ok = mbar_wait(&sm->q_full[s], qn[s] & 1, tmo);
+        ok = mbar_wait_warp(&sm->q_full[s], qn[s] & 1, tmo);
         ++qn[s];
         if (ok) scores(s, 0);
       }
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < nt; ++i, ++done) {
           const int tok0 = (w.j0 + i) * kTile;
-          ok = mbar_wait(&sm->s_full[s], done & 1, tmo);
+          ok = mbar_wait_warp(&sm->s_full[s], done & 1, tmo);
           if (!ok) break;
           tc_fence_after();
           float x[kTile];
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float m_new = need ? mx : m;
             const float alpha = need ? (m == -INFINITY ? 0.f : exp2f(m - m_new)) : 1.f;
             if (i > 0) {
-              ok = mbar_wait(&sm->pv_done[s], (done - 1) & 1, tmo);
+              ok = mbar_wait_warp(&sm->pv_done[s], (done - 1) & 1, tmo);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (masked) {
             const uint32_t t = tile0 + i, c = kTileChunks * t + 3;
-            ok = mbar_wait(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
+            ok = mbar_wait_warp(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
             if (!ok) break;
             if (clean_values<BF16>(smem + kOffRing + (c % kRing) * kChunk, smem + kOffRing + ((c + 1) % kRing) * kChunk, tok0, w.L, r))
               *const_cast<volatile int32_t*>(&sm->dirty[k & 7]) = k + 1;
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         if (nt > 0) {
-          ok = mbar_wait(&sm->pv_done[s], (done - 1) & 1, tmo);
+          ok = mbar_wait_warp(&sm->pv_done[s], (done - 1) & 1, tmo);
           if (!ok) break;
           tc_fence_after();
         }

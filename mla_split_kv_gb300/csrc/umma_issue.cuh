@@ -16,6 +16,10 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n .reg .pred p;\n .reg .b32 r;\n elect.sync r|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(one));
   return one;
 }
+// A bounded wait (mbar_wait) of a whole warp, with one answer for all its lanes: they stay together after a timeout.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, timeout_ns));
+}
 // D[tmem] (+)= A[smem] * B[smem]
 __device__ __forceinline__ void issue_ss(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {

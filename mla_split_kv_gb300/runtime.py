@@ -683,3 +683,77 @@ def _strides(t: torch.Tensor):
     T, H, n = t.shape
     head = t.stride(1) if H > 1 else n
     return (t.stride(0) if T > 1 else max(H * head, n), head)
+
+
+# ---------------------------------------------------------------------------
+# a batch whose contexts start with the same tokens
+# ---------------------------------------------------------------------------
+
+
+@dataclasses.dataclass
+class SharedPlan:
+    """A plan of mla_decode_shared for one batch shape, with the buffers its calls use. It serves contexts of any
+    length, in the time planned for the ones it was made for. Calls that may overlap in time (other streams) need a
+    plan each."""
+    num_requests: int
+    num_heads: int
+    q_len: int
+    block_size: int
+    dtype: str
+    causal: bool
+    shared_tokens: int
+    plan: nb.SharedPlan
+    items: torch.Tensor
+    own_indptr: torch.Tensor
+    workspace: torch.Tensor
+
+
+def plan_shared(context_lens: Sequence[int], shared_tokens: int, num_heads: int, q_len: int, block_size: int,
+                dtype: str = "f16", causal: bool = False, dev: Optional[nb.mla_device_info_t] = None,
+                device="cuda") -> SharedPlan:
+    """Lay out decode_shared calls of a batch of these lengths, the first shared_tokens (a multiple of the page) of
+    them common to all requests."""
+    if dtype not in TORCH_DTYPE:
+        raise ValueError(f"dtype: {dtype}")
+    index = torch.device(device).index
+    dev = dev if dev is not None else nb.mla_device_query(-1 if index is None else index)
+    plan = nb.mla_plan_shared(context_lens, shared_tokens, num_heads, q_len, block_size, dev)
+    items = np.zeros((len(plan.items), 8), np.int32)
+    items[:, :6] = plan.items
+    return SharedPlan(len(context_lens), num_heads, q_len, block_size, dtype, causal, shared_tokens, plan,
+                      torch.from_numpy(items).to(device), torch.tensor(plan.own_indptr, dtype=torch.int32, device=device),
+                      torch.empty(nb.mla_decode_shared_workspace_bytes(plan.num_slots), dtype=torch.uint8, device=device))
+
+
+def decode_shared(plan: SharedPlan, q_abs: torch.Tensor, q_pe: torch.Tensor, ckv: torch.Tensor, kpe: torch.Tensor,
+                  block_table: torch.Tensor, context_lens: torch.Tensor, scale: float, out: torch.Tensor,
+                  out_lse: Optional[torch.Tensor] = None, shared_table: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One decode layer call of a batch with a common prefix (mla_decode_shared), into out [B, q_len, H, 512].
+    shared_table: the prefix's pages; without one, the first request's row of block_table has them."""
+    B, q_len, H, bs = plan.num_requests, plan.q_len, plan.num_heads, plan.block_size
+    dtype, dev = TORCH_DTYPE[plan.dtype], _device_of(plan.workspace)
+    nblk, width, columns = ckv.shape[0], block_table.shape[-1], plan.shared_tokens // bs
+    _expect(q_abs, (B, q_len, H, 512), dtype, "q_abs", dev)
+    _expect(q_pe, (B, q_len, H, 64), dtype, "q_pe", dev)
+    _expect(ckv, (nblk, bs, 512), dtype, "ckv", dev)
+    _expect(kpe, (nblk, bs, 64), dtype, "kpe", dev)
+    _expect(out, (B, q_len, H, 512), out.dtype, "out", dev)
+    if out_lse is not None:
+        _expect(out_lse, (B, q_len, H), torch.float32, "out_lse", dev)
+    _expect(context_lens, (B,), torch.int32, "context_lens", dev)
+    _expect(block_table, (B, width), torch.int32, "block_table", dev)
+    if shared_table is not None:
+        _expect(shared_table, (columns,), torch.int32, "shared_table", dev)
+    elif width < columns:
+        raise ValueError(f"block_table: rows of {width} pages do not hold the {columns} of the common prefix")
+    raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
+    p = plan.plan
+    d = nb.mla_shared_desc_t(B, H, q_len, bs, nblk, width, CODE_OF[dtype], 1 if plan.causal else 0, plan.shared_tokens,
+                             _code_of(out, "out"), plan.items.data_ptr(), plan.own_indptr.data_ptr(), len(p.items),
+                             p.num_slots, p.shared_parts, plan.workspace.data_ptr(), plan.workspace.numel(), raw_stream)
+    nb.mla_decode_shared(q_abs.data_ptr(), q_pe.data_ptr(), ckv.data_ptr(), kpe.data_ptr(),
+                         (shared_table if shared_table is not None else block_table).data_ptr(), block_table.data_ptr(),
+                         context_lens.data_ptr(), scale, out.data_ptr(),
+                         out_lse.data_ptr() if out_lse is not None else None, d)
+    return out
