@@ -898,18 +898,22 @@ typedef struct {
   mla_shared_item_t* items;   /* host, caller-owned                           */
   int32_t* own_indptr;        /* host, caller-owned, >= B * ceil(q_len * H /
                                  128) + 1 entries                             */
+  int32_t* units;             /* host, caller-owned, >= 2 * item_capacity     */
+  int32_t* cta_indptr;        /* host, caller-owned, >= dev->num_sms + 1      */
   /* outputs */
   int32_t num_items;
   int32_t num_slots;
   int32_t shared_parts;       /* pieces of the common tokens                  */
+  int32_t num_ctas;
 } mla_shared_plan_t;
 
 /*
  * mla_plan_shared -- lay out the work of mla_decode_shared for contexts of
  * these lengths (the common tokens among them): the common tokens for the rows
  * of the whole batch in groups of 128, each request's own ones for its own
- * rows, each cut into pieces so that the device is evenly busy, the longest
- * first. The plan serves contexts of any length (a request's last piece takes
+ * rows, each cut into pieces so that the device is evenly busy. An item is two
+ * units of work, 2 * item + half of the value columns; CTA c does
+ * units[cta_indptr[c] .. cta_indptr[c + 1]). The plan serves contexts of any length (a request's last piece takes
  * what it has grown by) of the same B, q_len, H, page size and P, in the time
  * planned for these. own_indptr: of each request's group of 128 rows, its
  * first slot (the slots before are the common tokens': of the group g of the
@@ -933,7 +937,9 @@ typedef struct {
   int32_t out_dtype;          /* MLA_F16, MLA_BF16 or MLA_F32                 */
   const mla_shared_item_t* items; /* DEVICE, as planned, 16-byte aligned      */
   const int32_t* own_indptr;  /* DEVICE, as planned                           */
-  int32_t num_items, num_slots, shared_parts; /* as planned                   */
+  const int32_t* units;       /* DEVICE, as planned                           */
+  const int32_t* cta_indptr;  /* DEVICE, as planned                           */
+  int32_t num_items, num_slots, shared_parts, num_ctas; /* as planned         */
   void* workspace;            /* DEVICE, >= mla_decode_shared_workspace_bytes
                                  bytes, 16-byte aligned; need not be cleared.
                                  Calls sharing it must not overlap in time.    */

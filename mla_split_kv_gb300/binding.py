@@ -164,9 +164,12 @@ class mla_shared_plan_t(ctypes.Structure):
         ("item_capacity", ctypes.c_int32),
         ("items", ctypes.POINTER(mla_shared_item_t)),
         ("own_indptr", ctypes.POINTER(ctypes.c_int32)),
+        ("units", ctypes.POINTER(ctypes.c_int32)),
+        ("cta_indptr", ctypes.POINTER(ctypes.c_int32)),
         ("num_items", ctypes.c_int32),
         ("num_slots", ctypes.c_int32),
         ("shared_parts", ctypes.c_int32),
+        ("num_ctas", ctypes.c_int32),
     ]
 
 
@@ -184,9 +187,12 @@ class mla_shared_desc_t(ctypes.Structure):
         ("out_dtype", ctypes.c_int32),
         ("items", ctypes.c_void_p),
         ("own_indptr", ctypes.c_void_p),
+        ("units", ctypes.c_void_p),
+        ("cta_indptr", ctypes.c_void_p),
         ("num_items", ctypes.c_int32),
         ("num_slots", ctypes.c_int32),
         ("shared_parts", ctypes.c_int32),
+        ("num_ctas", ctypes.c_int32),
         ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_uint64),
         ("stream", ctypes.c_void_p),
@@ -475,9 +481,11 @@ def mla_prefill_workspace_bytes(dev: mla_device_info_t, num_requests: int, num_h
 class SharedPlan:
     """Host result of :func:`mla_plan_shared`."""
 
-    def __init__(self, items, own_indptr, num_slots, shared_parts):
+    def __init__(self, items, own_indptr, units, cta_indptr, num_slots, shared_parts):
         self.items = items  # list of (row0, rows, request, t0, t1, slot)
         self.own_indptr = own_indptr  # first slot of each request's group of 128 rows
+        self.units = units  # 2 * item + half, CTA after CTA
+        self.cta_indptr = cta_indptr
         self.num_slots = num_slots
         self.shared_parts = shared_parts
 
@@ -497,10 +505,15 @@ def mla_plan_shared(context_lens: Sequence[int], shared_tokens: int, num_heads: 
     plan.item_capacity = plan.num_items
     plan.items = ctypes.cast(items, ctypes.POINTER(mla_shared_item_t))
     plan.own_indptr = ctypes.cast(indptr, ctypes.POINTER(ctypes.c_int32))
+    units = (ctypes.c_int32 * (2 * max(1, plan.num_items)))()
+    ctas = (ctypes.c_int32 * (dev.num_sms + 1))()
+    plan.units = ctypes.cast(units, ctypes.POINTER(ctypes.c_int32))
+    plan.cta_indptr = ctypes.cast(ctas, ctypes.POINTER(ctypes.c_int32))
     _check(lib.mla_plan_shared(lens, B, num_heads, q_len, block_size, ctypes.byref(dev), ctypes.byref(plan)),
            "mla_plan_shared")
     out = [(x.row0, x.rows, x.request, x.t0, x.t1, x.slot) for x in items[: plan.num_items]]
-    return SharedPlan(out, list(indptr), plan.num_slots, plan.shared_parts)
+    return SharedPlan(out, list(indptr), list(units)[: 2 * plan.num_items], list(ctas)[: plan.num_ctas + 1], plan.num_slots,
+                      plan.shared_parts)
 
 
 def mla_decode_shared(q_absorbed: int, q_pe: int, ckv_cache: int, kpe_cache: int, shared_table: int, block_table: int,

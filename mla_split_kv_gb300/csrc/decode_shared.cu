@@ -24,7 +24,7 @@
 // there, and values that are not finite are taken out of such tiles: for a row that does see one of them its score has
 // already made the weight so.
 //
-// Units are laid out by the host plan, longest first, and taken in turns. The merge is a kernel of its own.
+// Units are shared out by the host plan (plan_shared.cpp). The merge is a kernel of its own.
 //
 // Warps: 0-3 softmax, queries and partial output (thread = row), 4 products, 5 loads.
 #include <type_traits>
@@ -58,7 +58,7 @@ static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemQ = 320;
 
 struct Small {
-  uint64_t a_full[2], a_empty[2], b_full[kRingB], b_empty[kRingB], q_full, s_full, s_empty, p_full, pv_done, drain;
+  uint64_t a_full[2], a_empty[2], b_full[2], b_empty[kRingB], q_full, s_full, s_empty, p_full, pv_done, drain;
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -112,14 +112,13 @@ __device__ __forceinline__ int visible(const SharedParams& p, int row) {
   return p.causal ? max(0, L - p.q_len + (row % per) / p.H + 1) : L;
 }
 
-// The k-th unit of this CTA, by a whole warp: in turns, every second one backwards. False behind the last one.
-__device__ __forceinline__ bool unit_of(const SharedParams& p, int k, int lane, Unit& w, bool& skip) {
-  const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-  const int u = k * g + ((k & 1) ? g - 1 - c : c);
-  skip = u >= 2 * p.num_items;
-  if (skip) return k * g < 2 * p.num_items;
-  const int4* const at = reinterpret_cast<const int4*>(p.items) + 2 * (u >> 1);
-  const int4 x = __ldg(at), y = __ldg(at + 1);
+// The k-th unit of this CTA, by a whole warp. False behind the last one.
+__device__ __forceinline__ bool unit_of(const SharedParams& p, int k, int lane, Unit& w) {
+  const int at = __ldg(p.cta_indptr + blockIdx.x) + k;
+  if (at >= __ldg(p.cta_indptr + blockIdx.x + 1)) return false;
+  const int u = __ldg(p.units + at);
+  const int4* const item = reinterpret_cast<const int4*>(p.items) + 2 * (u >> 1);
+  const int4 x = __ldg(item), y = __ldg(item + 1);
   w.row0 = x.x;
   w.rows = max(0, min(min(x.y, kRows), p.rows - x.x));
   w.request = x.z;
@@ -177,11 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm->a_full[s], 1);
       mbar_init(&sm->a_empty[s], 1);
+      mbar_init(&sm->b_full[s], 2);  // one arrival a piece
     }
-    for (int s = 0; s < kRingB; ++s) {
-      mbar_init(&sm->b_full[s], 1);
-      mbar_init(&sm->b_empty[s], 1);
-    }
+    for (int s = 0; s < kRingB; ++s) mbar_init(&sm->b_empty[s], 1);
     mbar_init(&sm->q_full, 4);
     mbar_init(&sm->s_full, 1);
     mbar_init(&sm->s_empty, 4);
@@ -203,14 +200,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
   const uint64_t tmo = p.timeout_ns;
   Unit w;
-  bool skip;
 
   if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- loads
     uint32_t tile = 0, piece = 0;
     bool ok = true;
-    for (int k = 0; ok && unit_of(p, k, lane, w, skip); ++k) {
-      if (skip) continue;
+    for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
       const int32_t* const table = w.request < 0 ? p.shared_table : p.block_table + static_cast<long long>(w.request) * p.max_blocks;
       const int columns = w.request < 0 ? p.shared_tokens / p.bs : p.max_blocks;
       for (int i = 0; i < w.tiles && ok; ++i, ++tile) {
@@ -241,10 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t b = piece % kRingB;
           if (piece >= kRingB) ok = ok && mbar_wait_warp(&sm->b_empty[b], (piece / kRingB - 1) & 1, tmo);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sm->b_full[b], pages * p.bs * 256);
+          if (lane == 0) mbar_arrive_expect_tx(&sm->b_full[s], pages * p.bs * 256);
           __syncwarp();
           if (lane < pages)
-            tma_load_pages(smem + kOffB + b * kPiece + lane * p.bs * 256, &tm_piece, 4 * w.half + 2 * x, group, &sm->b_full[b]);
+            tma_load_pages(smem + kOffB + b * kPiece + lane * p.bs * 256, &tm_piece, 4 * w.half + 2 * x, group, &sm->b_full[s]);
         }
       }
     }
@@ -262,36 +257,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t v0 = smem_desc_sw128(smem_u32(smem + kOffB), 1024, 2048);         // and as values
     uint32_t tile0 = 0, unit = 0;
     bool ok = true;
-    auto block = [&](int cb, uint64_t keys, uint32_t first) {  // a block of 64 latent columns
+    auto block = [&](int cb, uint64_t keys) {  // a block of 64 latent columns
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         if (cb < kQTmemBlocks)
-          issue_ts(leader, tmem + kTmemS, tmem + kTmemQ + 32 * cb + 8 * kk, keys + 2 * kk, idesc_s, first == 0 || kk > 0);
+          issue_ts(leader, tmem + kTmemS, tmem + kTmemQ + 32 * cb + 8 * kk, keys + 2 * kk, idesc_s, 1);
         else
           issue_ss(leader, tmem + kTmemS, q0 + (cb - kQTmemBlocks) * (kQChunk / 16) + 2 * kk, keys + 2 * kk, idesc_s, 1);
       }
     };
-    auto scores = [&](int i, auto half_of) {
+    // Each wait stands behind products that are still in the queue, as far as the order allows.
+    auto loaded = [&](int i) { ok = ok && mbar_wait_warp(&sm->a_full[(tile0 + i) & 1], ((tile0 + i) >> 1) & 1, tmo); };
+    auto scores = [&](int i, auto half_of) {  // (behind loaded(i))
       constexpr int half = decltype(half_of)::value;
       const uint32_t t = tile0 + i, s = t & 1;
       if (t > 0) ok = ok && mbar_wait_warp(&sm->s_empty, (t - 1) & 1, tmo);
-      ok = ok && mbar_wait_warp(&sm->a_full[s], (t >> 1) & 1, tmo);
       if (!ok) return;
       tc_fence_after();
       const uint64_t pe = pe0 + s * (kSlotA / 16), a = a0 + s * (kSlotA / 16);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) issue_ss(leader, tmem + kTmemS, q0 + 2 * (kQChunk / 16) + 2 * kk, pe + 2 * kk, idesc_s, kk > 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) block(4 * (half ^ 1) + j, a + j * 64, 0);
+      for (int j = 0; j < 4; ++j) block(4 * (half ^ 1) + j, a + j * 64);
       issue_commit(leader, &sm->a_empty[s]);
+      ok = ok && mbar_wait_warp(&sm->b_full[s], (t >> 1) & 1, tmo);
+      if (!ok) return;
+      tc_fence_after();
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint32_t pc = 2 * t + x, b = pc % kRingB;
-        ok = ok && mbar_wait_warp(&sm->b_full[b], (pc / kRingB) & 1, tmo);
-        if (!ok) return;
-        tc_fence_after();
+        const uint32_t b = (2 * t + x) % kRingB;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) block(4 * half + 2 * x + j, k0 + b * (kPiece / 16) + j * 64, 0);
+        for (int j = 0; j < 2; ++j) block(4 * half + 2 * x + j, k0 + b * (kPiece / 16) + j * 64);
       }
       issue_commit(leader, &sm->s_full);
     };
@@ -302,21 +298,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint32_t pc = 2 * t + x, b = pc % kRingB;
+        const uint32_t b = (2 * t + x) % kRingB;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           issue_ss(leader, tmem + kTmemO + 128 * x, p0 + 2 * kk, v0 + b * (kPiece / 16) + kk * 256, idesc_o, i > 0 || kk > 0);
-        if (x == 0) issue_commit(leader, &sm->b_empty[b]);
+        if (x == 0) {
+          issue_commit(leader, &sm->b_empty[b]);
+          if (i + 2 < w.tiles) loaded(i + 2);
+        }
       }
       issue_commit(leader, &sm->pv_done);
       issue_commit(leader, &sm->b_empty[(2 * t + 1) % kRingB]);
     };
-    for (int k = 0; ok && unit_of(p, k, lane, w, skip); ++k) {
-      if (skip || w.tiles == 0) continue;
+    for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
+      if (w.tiles == 0) continue;
       ok = mbar_wait_warp(&sm->q_full, unit & 1, tmo);
       ++unit;
       auto run = [&](auto half_of) {
+        loaded(0);
         if (ok) scores(0, half_of);
+        if (w.tiles > 1) loaded(1);
         for (int i = 0; i < w.tiles && ok; ++i) {
           if (i + 1 < w.tiles) scores(i + 1, half_of);
           values(i);
@@ -338,8 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale = p.scale_log2;
     uint32_t tile0 = 0;
     bool ok = true;
-    for (int k = 0; ok && unit_of(p, k, lane, w, skip); ++k) {
-      if (skip) continue;
+    for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
       const bool real = r < w.rows;
       const long long row = w.row0 + (real ? r : 0);
       const long long slot_row = static_cast<long long>(w.slot) * kRows + r;
@@ -417,10 +417,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx = lo * f;
         }
         const bool need = mx > m + kTau;
-        if (i > 0) ok = mbar_wait_warp(&sm->pv_done, (t - 1) & 1, tmo);  // O and the weights' buffer are free
-        if (!ok) break;
+        const float m_new = need ? mx : m;
+        const float mm = m_new == -INFINITY ? 0.f : -m_new;
+        const float2 f2 = make_float2(f, f), m2 = make_float2(mm, mm);
+        float2 sum = make_float2(0.f, 0.f), sum_b = sum;
+        uint32_t h[kT / 2];
+#pragma unroll
+        for (int j = 0; j < kT / 2; ++j) {
+          float2 e = fma2(make_float2(x[2 * j], x[2 * j + 1]), f2, m2);
+          e.x = fast_exp2(e.x);
+          e.y = fast_exp2(e.y);
+          if (j & 1) sum_b = add2(sum_b, e);
+          else sum = add2(sum, e);
+          h[j] = pack2<BF16>(e.x, e.y);
+        }
+        sum = add2(sum, sum_b);
+        if (i > 0) {  // O and the weights' buffer are free
+          ok = mbar_wait_warp(&sm->pv_done, (t - 1) & 1, tmo);
+          if (!ok) break;
+        }
         if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
-          const float m_new = need ? mx : m;
           const float alpha = need ? (m == -INFINITY ? 0.f : exp2f(m - m_new)) : 1.f;
           if (i > 0) {
             tc_fence_after();
@@ -438,32 +454,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= alpha;
           m = m_new;
         }
-        if (masked) {
+        l += sum.x + sum.y;
+        if (masked) {  // (b_full is complete: so are the scores)
           const uint32_t b = 2 * t, c = b + 1;
-          ok = mbar_wait_warp(&sm->b_full[b % kRingB], (b / kRingB) & 1, tmo) && mbar_wait_warp(&sm->b_full[c % kRingB], (c / kRingB) & 1, tmo);
+          ok = mbar_wait_warp(&sm->b_full[t & 1], (t >> 1) & 1, tmo);
           if (!ok) break;
           clean_values<BF16>(smem + kOffB + (b % kRingB) * kPiece, smem + kOffB + (c % kRingB) * kPiece, r);
         }
-        const float mm = m == -INFINITY ? 0.f : -m;
-        const float2 f2 = make_float2(f, f), m2 = make_float2(mm, mm);
-        float2 sum = make_float2(0.f, 0.f), sum_b = sum;
         const uint32_t at = smem_u32(smem + kOffP) + r * 128;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t h[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float2 e = fma2(make_float2(x[8 * j + 2 * q], x[8 * j + 2 * q + 1]), f2, m2);
-            e.x = fast_exp2(e.x);
-            e.y = fast_exp2(e.y);
-            if (q & 1) sum_b = add2(sum_b, e);
-            else sum = add2(sum, e);
-            h[q] = pack2<BF16>(e.x, e.y);
-          }
-          sts128(at + ((j ^ (r & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
-        }
-        sum = add2(sum, sum_b);
-        l += sum.x + sum.y;
+        for (int j = 0; j < 8; ++j) sts128(at + ((j ^ (r & 7)) << 4), make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]));
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -575,7 +575,7 @@ cudaError_t launch_dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr,
 }  // namespace
 
 cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& tm_piece, const CUtensorMap& tm_kpe,
-                                 const SharedParams& p, bool bf16, int sms, cudaStream_t stream) {
+                                 const SharedParams& p, bool bf16, cudaStream_t stream) {
   static DeviceOnce once_f16, once_bf16;
   const void* const fn = bf16 ? reinterpret_cast<const void*>(&mla_decode_shared_kernel<true>)
                               : reinterpret_cast<const void*>(&mla_decode_shared_kernel<false>);
@@ -583,8 +583,7 @@ cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  const int units = 2 * p.num_items;
-  launch_dependent(cfg, attr, units < sms ? units : sms, kThreads, kSmem, stream);
+  launch_dependent(cfg, attr, p.num_ctas, kThreads, kSmem, stream);
   e = bf16 ? cudaLaunchKernelEx(&cfg, mla_decode_shared_kernel<true>, tm_half, tm_piece, tm_kpe, p)
            : cudaLaunchKernelEx(&cfg, mla_decode_shared_kernel<false>, tm_half, tm_piece, tm_kpe, p);
   if (e != cudaSuccess) return e;

@@ -2,8 +2,8 @@
 //
 // The common tokens are cut into pieces for every group of 128 of the batch's rows, each request's own tokens for its
 // own groups, all pieces about equally long: a piece is two units of work (one half of the value columns each), the
-// units go to the SMs longest first, and the length is the one among some tried whose busiest SM and merge are done
-// first.
+// units go longest first to the CTA (one an SM) that is free first, and the length is the one among some tried whose
+// busiest CTA and merge are done first.
 #include <algorithm>
 #include <cstdint>
 #include <functional>
@@ -121,13 +121,31 @@ extern "C" mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_
   plan->num_slots = static_cast<int32_t>(slot);
   plan->shared_parts = static_cast<int32_t>(parts);
   if (plan->num_items > plan->item_capacity) return MLA_ERR_CAPACITY;
-  if (plan->items == nullptr || plan->own_indptr == nullptr) return MLA_ERR_INVALID_ARG;
+  if (plan->items == nullptr || plan->own_indptr == nullptr || plan->units == nullptr || plan->cta_indptr == nullptr)
+    return MLA_ERR_INVALID_ARG;
   std::stable_sort(pieces.begin(), pieces.end(), [](const Piece& a, const Piece& b) { return a.tiles > b.tiles; });
   for (size_t i = 0; i < pieces.size(); ++i) {
     const Piece& x = pieces[i];
     plan->items[i] = mla_shared_item_t{static_cast<int32_t>(x.row0), static_cast<int32_t>(x.rows), x.request, static_cast<int32_t>(x.t0),
                                        static_cast<int32_t>(x.t1), static_cast<int32_t>(x.slot), {0, 0}};
   }
+  const int32_t ctas = static_cast<int32_t>(std::min<int64_t>(dev->num_sms, 2 * static_cast<int64_t>(pieces.size())));
+  std::vector<std::vector<int32_t>> lists(ctas);
+  std::priority_queue<std::pair<int64_t, int32_t>, std::vector<std::pair<int64_t, int32_t>>, std::greater<>> free_at;
+  for (int32_t c = 0; c < ctas; ++c) free_at.emplace(0, c);
+  for (size_t u = 0; u < 2 * pieces.size(); ++u) {
+    const auto next = free_at.top();
+    free_at.pop();
+    lists[next.second].push_back(static_cast<int32_t>(u));
+    free_at.emplace(next.first + pieces[u >> 1].tiles + kUnitTiles, next.second);
+  }
+  int32_t at = 0;
+  for (int32_t c = 0; c < ctas; ++c) {
+    plan->cta_indptr[c] = at;
+    for (const int32_t u : lists[c]) plan->units[at++] = u;
+  }
+  plan->cta_indptr[ctas] = at;
+  plan->num_ctas = ctas;
   for (size_t i = 0; i < first.size(); ++i) plan->own_indptr[i] = static_cast<int32_t>(first[i]);
   return MLA_OK;
 } catch (...) {  // out of memory

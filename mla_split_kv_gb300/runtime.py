@@ -705,6 +705,8 @@ class SharedPlan:
     plan: nb.SharedPlan
     items: torch.Tensor
     own_indptr: torch.Tensor
+    units: torch.Tensor
+    cta_indptr: torch.Tensor
     workspace: torch.Tensor
 
 
@@ -721,7 +723,8 @@ def plan_shared(context_lens: Sequence[int], shared_tokens: int, num_heads: int,
     items = np.zeros((len(plan.items), 8), np.int32)
     items[:, :6] = plan.items
     return SharedPlan(len(context_lens), num_heads, q_len, block_size, dtype, causal, shared_tokens, plan,
-                      torch.from_numpy(items).to(device), torch.tensor(plan.own_indptr, dtype=torch.int32, device=device),
+                      torch.from_numpy(items).to(device),
+                      *(torch.tensor(x, dtype=torch.int32, device=device) for x in (plan.own_indptr, plan.units, plan.cta_indptr)),
                       torch.empty(nb.mla_decode_shared_workspace_bytes(plan.num_slots), dtype=torch.uint8, device=device))
 
 
@@ -750,8 +753,9 @@ def decode_shared(plan: SharedPlan, q_abs: torch.Tensor, q_pe: torch.Tensor, ckv
     raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
     p = plan.plan
     d = nb.mla_shared_desc_t(B, H, q_len, bs, nblk, width, CODE_OF[dtype], 1 if plan.causal else 0, plan.shared_tokens,
-                             _code_of(out, "out"), plan.items.data_ptr(), plan.own_indptr.data_ptr(), len(p.items),
-                             p.num_slots, p.shared_parts, plan.workspace.data_ptr(), plan.workspace.numel(), raw_stream)
+                             _code_of(out, "out"), plan.items.data_ptr(), plan.own_indptr.data_ptr(),
+                             plan.units.data_ptr(), plan.cta_indptr.data_ptr(), len(p.items), p.num_slots,
+                             p.shared_parts, len(p.cta_indptr) - 1, plan.workspace.data_ptr(), plan.workspace.numel(), raw_stream)
     nb.mla_decode_shared(q_abs.data_ptr(), q_pe.data_ptr(), ckv.data_ptr(), kpe.data_ptr(),
                          (shared_table if shared_table is not None else block_table).data_ptr(), block_table.data_ptr(),
                          context_lens.data_ptr(), scale, out.data_ptr(),
