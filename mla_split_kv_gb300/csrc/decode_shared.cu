@@ -13,7 +13,7 @@
 // columns as the score product's A operand (the other 192 are in shared memory, 48 KB). The probabilities go through
 // 16 KB of shared memory, so S is free again once it has been read, and one buffer is enough: the products go
 //   S(i+1) PV(i) S(i+2) PV(i+1) ...
-// and S(i)'s softmax runs beside PV(i-1) and S(i+1). A tile is 72 KB: the half of its latents that only the score
+// (issued by two warps) and S(i)'s softmax runs beside PV(i-1) and S(i+1). A tile is 72 KB: the half of its latents that only the score
 // product reads, with the rotary keys (two slots of 40 KB, free after S), and the half that is the values too (a ring
 // of five pieces of 128 columns, 16 KB, free after PV): what the next score product needs last has been on its way
 // longest.
@@ -26,7 +26,7 @@
 //
 // Units are shared out by the host plan (plan_shared.cpp). The merge is a kernel of its own.
 //
-// Warps: 0-3 softmax, queries and partial output (thread = row), 4 products, 5 loads.
+// Warps: 0-3 softmax, queries and partial output (thread = row), 4 score products, 5 loads, 6 value products.
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -46,8 +46,8 @@ constexpr int kPiece = kT * 128 * 2;      // 16 KB: 128 of the unit's own column
 constexpr int kRingB = 5;
 constexpr int kQChunk = kRows * 128;      // 16 KB: [128 rows x 64 columns]
 constexpr int kQTmemBlocks = 6;           // blocks of 64 query columns in tensor memory; the last two and the rotary one are not
-constexpr int kMmaWarp = 4, kLoadWarp = 5;
-constexpr int kThreads = 256;             // (two warps have nothing to do)
+constexpr int kScoreWarp = 4, kLoadWarp = 5, kValueWarp = 6;
+constexpr int kThreads = 256;             // (the last warp has nothing to do)
 constexpr float kTau = 8.0f;
 constexpr uint32_t kOffP = 3 * kQChunk;
 constexpr uint32_t kOffA = kOffP + kQChunk;
@@ -58,7 +58,7 @@ static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemQ = 320;
 
 struct Small {
-  uint64_t a_full[2], a_empty[2], b_full[2], b_empty[kRingB], q_full, s_full, s_empty, p_full, pv_done, drain;
+  uint64_t a_full[2], a_empty[2], b_full[4], b_empty[kRingB], q_full, s_full, s_empty, p_full, pv_done, drain[2];
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -176,19 +176,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm->a_full[s], 1);
       mbar_init(&sm->a_empty[s], 1);
-      mbar_init(&sm->b_full[s], 2);  // one arrival a piece
     }
+    // one arrival a piece; of four tiles, since pieces of the tile after next may be on their way while the score product
+    // still waits for the second one of this
+    for (int s = 0; s < 4; ++s) mbar_init(&sm->b_full[s], 2);
     for (int s = 0; s < kRingB; ++s) mbar_init(&sm->b_empty[s], 1);
     mbar_init(&sm->q_full, 4);
     mbar_init(&sm->s_full, 1);
     mbar_init(&sm->s_empty, 4);
     mbar_init(&sm->p_full, 4);
     mbar_init(&sm->pv_done, 1);
-    mbar_init(&sm->drain, 1);
+    mbar_init(&sm->drain[0], 1);
+    mbar_init(&sm->drain[1], 1);
     sm->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tmem_alloc(&sm->tmem_base, 512);
     tmem_relinquish();
   }
@@ -236,53 +239,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t b = piece % kRingB;
           if (piece >= kRingB) ok = ok && mbar_wait_warp(&sm->b_empty[b], (piece / kRingB - 1) & 1, tmo);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sm->b_full[s], pages * p.bs * 256);
+          if (lane == 0) mbar_arrive_expect_tx(&sm->b_full[tile & 3], pages * p.bs * 256);
           __syncwarp();
           if (lane < pages)
-            tma_load_pages(smem + kOffB + b * kPiece + lane * p.bs * 256, &tm_piece, 4 * w.half + 2 * x, group, &sm->b_full[s]);
+            tma_load_pages(smem + kOffB + b * kPiece + lane * p.bs * 256, &tm_piece, 4 * w.half + 2 * x, group, &sm->b_full[tile & 3]);
         }
       }
     }
     if (!ok) *abort_flag = 1;
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- products: the warp in step (umma_issue.cuh)
+  } else if (warp == kScoreWarp) {
+    // ---------------------------------------------------------------- score products: the warp in step (umma_issue.cuh)
     const uint32_t leader = elect_one();
-    const uint32_t idesc_s = idesc_f16_f32(kRows, kT, BF16, false, false);
-    const uint32_t idesc_o = idesc_f16_f32(kRows, 128, BF16, false, true);
+    const uint32_t idesc = idesc_f16_f32(kRows, kT, BF16, false, false);
     const uint64_t q0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t p0 = smem_desc_sw128(smem_u32(smem + kOffP), 16, 1024);
-    const uint64_t a0 = smem_desc_sw128(smem_u32(smem + kOffA), 16, 4096);           // the other half, rows of tokens
+    const uint64_t a0 = smem_desc_sw128(smem_u32(smem + kOffA), 16, 4096);  // the other half, rows of tokens
     const uint64_t pe0 = smem_desc_sw128(smem_u32(smem + kOffA + kOther), 16, 1024);
-    const uint64_t k0 = smem_desc_sw128(smem_u32(smem + kOffB), 16, 2048);           // a piece as keys
-    const uint64_t v0 = smem_desc_sw128(smem_u32(smem + kOffB), 1024, 2048);         // and as values
+    const uint64_t k0 = smem_desc_sw128(smem_u32(smem + kOffB), 16, 2048);  // a piece as keys
     uint32_t tile0 = 0, unit = 0;
     bool ok = true;
     auto block = [&](int cb, uint64_t keys) {  // a block of 64 latent columns
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         if (cb < kQTmemBlocks)
-          issue_ts(leader, tmem + kTmemS, tmem + kTmemQ + 32 * cb + 8 * kk, keys + 2 * kk, idesc_s, 1);
+          issue_ts(leader, tmem + kTmemS, tmem + kTmemQ + 32 * cb + 8 * kk, keys + 2 * kk, idesc, 1);
         else
-          issue_ss(leader, tmem + kTmemS, q0 + (cb - kQTmemBlocks) * (kQChunk / 16) + 2 * kk, keys + 2 * kk, idesc_s, 1);
+          issue_ss(leader, tmem + kTmemS, q0 + (cb - kQTmemBlocks) * (kQChunk / 16) + 2 * kk, keys + 2 * kk, idesc, 1);
       }
     };
-    // Each wait stands behind products that are still in the queue, as far as the order allows.
-    auto loaded = [&](int i) { ok = ok && mbar_wait_warp(&sm->a_full[(tile0 + i) & 1], ((tile0 + i) >> 1) & 1, tmo); };
-    auto scores = [&](int i, auto half_of) {  // (behind loaded(i))
+    auto scores = [&](int i, auto half_of) {
       constexpr int half = decltype(half_of)::value;
       const uint32_t t = tile0 + i, s = t & 1;
+      ok = ok && mbar_wait_warp(&sm->a_full[s], (t >> 1) & 1, tmo);
       if (t > 0) ok = ok && mbar_wait_warp(&sm->s_empty, (t - 1) & 1, tmo);
       if (!ok) return;
       tc_fence_after();
       const uint64_t pe = pe0 + s * (kSlotA / 16), a = a0 + s * (kSlotA / 16);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) issue_ss(leader, tmem + kTmemS, q0 + 2 * (kQChunk / 16) + 2 * kk, pe + 2 * kk, idesc_s, kk > 0);
+      for (int kk = 0; kk < 4; ++kk) issue_ss(leader, tmem + kTmemS, q0 + 2 * (kQChunk / 16) + 2 * kk, pe + 2 * kk, idesc, kk > 0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) block(4 * (half ^ 1) + j, a + j * 64);
       issue_commit(leader, &sm->a_empty[s]);
-      ok = ok && mbar_wait_warp(&sm->b_full[s], (t >> 1) & 1, tmo);
+      ok = ok && mbar_wait_warp(&sm->b_full[t & 3], (t >> 2) & 1, tmo);
       if (!ok) return;
-      tc_fence_after();
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const uint32_t b = (2 * t + x) % kRingB;
@@ -291,48 +289,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       issue_commit(leader, &sm->s_full);
     };
-    auto values = [&](int i) {
-      const uint32_t t = tile0 + i;
-      ok = ok && mbar_wait_warp(&sm->p_full, t & 1, tmo);
-      if (!ok) return;
-      tc_fence_after();
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t b = (2 * t + x) % kRingB;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          issue_ss(leader, tmem + kTmemO + 128 * x, p0 + 2 * kk, v0 + b * (kPiece / 16) + kk * 256, idesc_o, i > 0 || kk > 0);
-        if (x == 0) {
-          issue_commit(leader, &sm->b_empty[b]);
-          if (i + 2 < w.tiles) loaded(i + 2);
-        }
-      }
-      issue_commit(leader, &sm->pv_done);
-      issue_commit(leader, &sm->b_empty[(2 * t + 1) % kRingB]);
-    };
     for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
       if (w.tiles == 0) continue;
       ok = mbar_wait_warp(&sm->q_full, unit & 1, tmo);
       ++unit;
-      auto run = [&](auto half_of) {
-        loaded(0);
-        if (ok) scores(0, half_of);
-        if (w.tiles > 1) loaded(1);
-        for (int i = 0; i < w.tiles && ok; ++i) {
-          if (i + 1 < w.tiles) scores(i + 1, half_of);
-          values(i);
-        }
-      };
-      if (w.half == 0) run(std::integral_constant<int, 0>{});
-      else run(std::integral_constant<int, 1>{});
+      if (w.half == 0) {
+        for (int i = 0; i < w.tiles && ok; ++i) scores(i, std::integral_constant<int, 0>{});
+      } else {
+        for (int i = 0; i < w.tiles && ok; ++i) scores(i, std::integral_constant<int, 1>{});
+      }
       tile0 += w.tiles;
     }
     if (!ok) *abort_flag = 1;
     __syncwarp();
-    issue_commit(leader, &sm->drain);  // every product is done before tensor memory is freed
-    mbar_wait(&sm->drain, 0, kDrainTimeoutNs);
+    issue_commit(leader, &sm->drain[0]);  // every product is done before tensor memory is freed
+    mbar_wait(&sm->drain[0], 0, kDrainTimeoutNs);
     __syncwarp();
-  } else if (warp < kMmaWarp) {
+  } else if (warp == kValueWarp) {
+    // ---------------------------------------------------------------- value products: a warp of their own, so that what one
+    // of the two waits for is hidden behind the other's products
+    const uint32_t leader = elect_one();
+    const uint32_t idesc = idesc_f16_f32(kRows, 128, BF16, false, true);
+    const uint64_t p0 = smem_desc_sw128(smem_u32(smem + kOffP), 16, 1024);
+    const uint64_t v0 = smem_desc_sw128(smem_u32(smem + kOffB), 1024, 2048);  // a piece as values
+    uint32_t t = 0;
+    bool ok = true;
+    for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
+      for (int i = 0; i < w.tiles; ++i, ++t) {
+        ok = mbar_wait_warp(&sm->p_full, t & 1, tmo);  // (its scores are done: the tile is there)
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t b = (2 * t + x) % kRingB;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            issue_ss(leader, tmem + kTmemO + 128 * x, p0 + 2 * kk, v0 + b * (kPiece / 16) + kk * 256, idesc, i > 0 || kk > 0);
+          if (x == 0) issue_commit(leader, &sm->b_empty[b]);
+        }
+        issue_commit(leader, &sm->pv_done);
+        issue_commit(leader, &sm->b_empty[(2 * t + 1) % kRingB]);
+      }
+    }
+    if (!ok) *abort_flag = 1;
+    __syncwarp();
+    issue_commit(leader, &sm->drain[1]);
+    mbar_wait(&sm->drain[1], 0, kDrainTimeoutNs);
+    __syncwarp();
+  } else if (warp < kScoreWarp) {
     // ---------------------------------------------------------------- softmax: thread = row
     const int r = tid;
     const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += sum.x + sum.y;
         if (masked) {  // (b_full is complete: so are the scores)
           const uint32_t b = 2 * t, c = b + 1;
-          ok = mbar_wait_warp(&sm->b_full[t & 1], (t >> 1) & 1, tmo);
+          ok = mbar_wait_warp(&sm->b_full[t & 3], (t >> 2) & 1, tmo);
           if (!ok) break;
           clean_values<BF16>(smem + kOffB + (b % kRingB) * kPiece, smem + kOffB + (c % kRingB) * kPiece, r);
         }
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort_flag) settle_in_flight(3000000ull);  // copies in flight land before shared memory goes
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kScoreWarp) tmem_dealloc(tmem, 512);
 }
 
 // A warp a row: its parts in order (the common tokens' pieces, then its own tokens'), M = max lse, weights 2^(lse - M).
