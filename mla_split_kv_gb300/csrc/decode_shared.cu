@@ -18,15 +18,17 @@
 // of five pieces of 128 columns, 16 KB, free after PV): what the next score product needs last has been on its way
 // longest.
 //
-// The running maximum moves only when a tile's passes it by more than 2^8; sums are of the unrounded weights, in fp32;
-// the weights are rounded once to the cache's type (2^-12 of themselves in fp16, 2^-9 in bf16: as the 16-bit output).
+// The running maximum moves only when a tile's passes it by more than the weights' type has room for (2^15 in fp16, 2^60
+// in bf16, whose sums and O stay far below fp32's end too): with a slack of 2^8 some row of a warp moved it every few
+// tiles, and with it all of O, 590 cycles a tile of the serving batch. Sums are of the unrounded weights, in fp32; the weights are rounded once to the cache's type (2^-12 of themselves in fp16, 2^-9 in bf16: as the 16-bit output).
 // Tokens that some row of a group does not see (behind a shorter context or, in a window, behind the row) have weight 0
 // there, and values that are not finite are taken out of such tiles: for a row that does see one of them its score has
 // already made the weight so.
 //
 // Units are shared out by the host plan (plan_shared.cpp). The merge is a kernel of its own.
 //
-// Warps: 0-3 softmax, queries and partial output (thread = row), 4 score products, 5 loads, 6 value products.
+// Warps: 0-3 softmax, queries and partial output (thread = row), 4 score products, 6 value products, 5 and 7 loads (of the
+// two parts of a tile, each as soon as there is room).
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -46,9 +48,8 @@ constexpr int kPiece = kT * 128 * 2;      // 16 KB: 128 of the unit's own column
 constexpr int kRingB = 5;
 constexpr int kQChunk = kRows * 128;      // 16 KB: [128 rows x 64 columns]
 constexpr int kQTmemBlocks = 6;           // blocks of 64 query columns in tensor memory; the last two and the rotary one are not
-constexpr int kScoreWarp = 4, kLoadWarp = 5, kValueWarp = 6;
-constexpr int kThreads = 256;             // (the last warp has nothing to do)
-constexpr float kTau = 8.0f;
+constexpr int kScoreWarp = 4, kLoadWarpA = 5, kValueWarp = 6, kLoadWarpB = 7;
+constexpr int kThreads = 256;
 constexpr uint32_t kOffP = 3 * kQChunk;
 constexpr uint32_t kOffA = kOffP + kQChunk;
 constexpr uint32_t kOffB = kOffA + 2 * kSlotA;
@@ -204,9 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t tmo = p.timeout_ns;
   Unit w;
 
-  if (warp == kLoadWarp) {
+  if (warp == kLoadWarpA || warp == kLoadWarpB) {
     // ---------------------------------------------------------------- loads
-    uint32_t tile = 0, piece = 0;
+    const bool first = warp == kLoadWarpA;  // the half that is only keys, and the rotary keys; else the values' half
+    uint32_t tile = 0;
     bool ok = true;
     for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
       const int32_t* const table = w.request < 0 ? p.shared_table : p.block_table + static_cast<long long>(w.request) * p.max_blocks;
@@ -224,19 +226,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int group = pid * (p.bs / 8);
-        const uint32_t s = tile & 1;
-        if (tile >= 2) ok = mbar_wait_warp(&sm->a_empty[s], ((tile >> 1) - 1) & 1, tmo);
-        if (!ok) break;
-        uint8_t* const a = smem + kOffA + s * kSlotA;
-        if (lane == 0) mbar_arrive_expect_tx(&sm->a_full[s], pages * p.bs * (kHalf + kRope) * 2);
-        __syncwarp();
-        if (lane < pages) {
-          tma_load_rows(a + kOther + lane * p.bs * 128, &tm_kpe, pid * p.bs, &sm->a_full[s]);
-          tma_load_pages(a + lane * p.bs * (kHalf * 2), &tm_half, 4 * (w.half ^ 1), group, &sm->a_full[s]);
+        if (first) {
+          const uint32_t s = tile & 1;
+          if (tile >= 2) ok = mbar_wait_warp(&sm->a_empty[s], ((tile >> 1) - 1) & 1, tmo);
+          if (!ok) break;
+          uint8_t* const a = smem + kOffA + s * kSlotA;
+          if (lane == 0) mbar_arrive_expect_tx(&sm->a_full[s], pages * p.bs * (kHalf + kRope) * 2);
+          __syncwarp();
+          if (lane < pages) {
+            tma_load_rows(a + kOther + lane * p.bs * 128, &tm_kpe, pid * p.bs, &sm->a_full[s]);
+            tma_load_pages(a + lane * p.bs * (kHalf * 2), &tm_half, 4 * (w.half ^ 1), group, &sm->a_full[s]);
+          }
+          continue;
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x, ++piece) {
-          const uint32_t b = piece % kRingB;
+        for (uint32_t x = 0; x < 2; ++x) {
+          const uint32_t piece = 2 * tile + x, b = piece % kRingB;
           if (piece >= kRingB) ok = ok && mbar_wait_warp(&sm->b_empty[b], (piece / kRingB - 1) & 1, tmo);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&sm->b_full[tile & 3], pages * p.bs * 256);
@@ -341,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = tid;
     const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
     const float scale = p.scale_log2;
+    constexpr float kSlack = BF16 ? 60.f : 15.f;
     uint32_t tile0 = 0;
     bool ok = true;
     for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
@@ -353,27 +359,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       {  // the queries: the products of the unit before are done
         const uint4* const src = reinterpret_cast<const uint4*>(p.q_abs + row * kRank);
-        const uint4 none = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-        for (int g = 0; g < kQTmemBlocks * 2; ++g) {  // 32 columns a step
-          float v[16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 x = real ? src[4 * g + j] : none;
-            v[4 * j] = __uint_as_float(x.x);
-            v[4 * j + 1] = __uint_as_float(x.y);
-            v[4 * j + 2] = __uint_as_float(x.z);
-            v[4 * j + 3] = __uint_as_float(x.w);
-          }
-          tmem_st16(tmem + lanes + kTmemQ + 16 * g, v);
-        }
         const uint4* const pe = reinterpret_cast<const uint4*>(p.q_pe + row * kRope);
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        constexpr int kPieces = 24;  // 16 bytes each, in flight together: 192 columns
+        static_assert(kQTmemBlocks * 8 == 2 * kPieces && 3 * 8 == kPieces, "three rounds of loads");
 #pragma unroll
-        for (int c = 0; c < 3; ++c) {
+        for (int round = 0; round < 3; ++round) {
+          uint4 x[kPieces];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 x = !real ? none : c < 2 ? src[8 * (kQTmemBlocks + c) + j] : pe[j];
-            sts128(smem_u32(smem) + c * kQChunk + r * 128 + ((j ^ (r & 7)) << 4), x);
+          for (int j = 0; j < kPieces; ++j) {
+            const int at = round * kPieces + j;
+            x[j] = !real ? none : at < kRank / 8 ? src[at] : pe[at - kRank / 8];
+          }
+          if (round < 2) {
+#pragma unroll
+            for (int g = 0; g < kPieces / 4; ++g) {
+              float v[16];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                v[4 * j] = __uint_as_float(x[4 * g + j].x);
+                v[4 * j + 1] = __uint_as_float(x[4 * g + j].y);
+                v[4 * j + 2] = __uint_as_float(x[4 * g + j].z);
+                v[4 * j + 3] = __uint_as_float(x[4 * g + j].w);
+              }
+              tmem_st16(tmem + lanes + kTmemQ + 16 * (round * (kPieces / 4) + g), v);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) sts128(smem_u32(smem) + (j >> 3) * kQChunk + r * 128 + (((j & 7) ^ (r & 7)) << 4), x[j]);
           }
         }
         tmem_wait_st();
@@ -420,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 1; j < kT; ++j) lo = fminf(lo, x[j]);
           mx = lo * f;
         }
-        const bool need = mx > m + kTau;
+        const bool need = mx > m + kSlack;
         const float m_new = need ? mx : m;
         const float mm = m_new == -INFINITY ? 0.f : -m_new;
         const float2 f2 = make_float2(f, f), m2 = make_float2(mm, mm);
@@ -479,18 +492,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool any = m != -INFINITY;
       const float inv = any ? 1.f / l : 0.f;
-      float* const out = p.part_o + slot_row * kRank + kHalf * w.half;
+      // the partial output, 32 columns at a time through the warp's quarter of the weights' buffer: rows of 128 bytes out,
+      // four to an instruction (a thread a row, 16 bytes each, takes the memory pipeline eight times as long)
+      float* const out = p.part_o + (static_cast<long long>(w.slot) * kRows + 32 * warp) * kRank + kHalf * w.half;
+      const uint32_t stage = smem_u32(smem + kOffP) + 4096 * warp;
 #pragma unroll 1
-      for (int q = 0; q < kHalf / 16; ++q) {
-        float o[16];
-        tmem_ld16(tmem + lanes + kTmemO + 16 * q, o);
+      for (int q = 0; q < kHalf / 32; ++q) {
+        float o[32];
+        ld32(tmem + lanes + kTmemO + 32 * q, o);
         tmem_wait_ld();
-        if (real) {
+        __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            reinterpret_cast<float4*>(out + 16 * q)[j] = make_float4(o[4 * j] * inv, o[4 * j + 1] * inv, o[4 * j + 2] * inv, o[4 * j + 3] * inv);
+        for (int j = 0; j < 8; ++j)
+          sts128(stage + lane * 128 + ((j ^ (lane & 7)) << 4),
+                 make_uint4(__float_as_uint(o[4 * j] * inv), __float_as_uint(o[4 * j + 1] * inv), __float_as_uint(o[4 * j + 2] * inv), __float_as_uint(o[4 * j + 3] * inv)));
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int at = 4 * j + (lane >> 3), c = lane & 7;  // row, 16-byte piece
+          const uint4 v = lds128(stage + at * 128 + ((c ^ (at & 7)) << 4));
+          if (32 * warp + at < w.rows) *reinterpret_cast<uint4*>(out + static_cast<long long>(at) * kRank + 32 * q + 4 * c) = v;
         }
       }
+      __syncwarp();
       if (real && w.half == 0) p.part_lse[slot_row] = any ? m + log2f(l) : (l != l ? l : -INFINITY);
       tc_fence_before();
       tile0 += w.tiles;
