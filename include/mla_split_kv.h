@@ -881,27 +881,27 @@ uint64_t mla_prefill_workspace_bytes(const mla_device_info_t* dev, int32_t num_r
  * that many requests ask about).
  */
 
-/* One piece of work of mla_decode_shared: a group of up to 128 consecutive rows
- * of [B, q_len, H] over a run of tokens. */
+/* One unit of work of mla_decode_shared: a group of up to 128 consecutive rows
+ * of [B, q_len, H] over a run of tokens, for one half of the value columns. */
 typedef struct {
   int32_t row0, rows;         /* rows [row0, row0 + rows)                     */
   int32_t request;            /* whose own tokens; -1: the common ones        */
   int32_t t0, t1;             /* tokens (positions in the context)            */
   int32_t slot;               /* its rows' partials go to slot `slot`         */
-  int32_t reserved[2];
-} mla_shared_item_t;
+  int32_t half;               /* columns [256 half, 256 half + 256)           */
+  int32_t reserved;
+} mla_shared_unit_t;
 
 typedef struct {
   /* inputs */
   int32_t shared_tokens;      /* P: the common tokens, a multiple of the page */
-  int32_t item_capacity;      /* entries of `items`                           */
-  mla_shared_item_t* items;   /* host, caller-owned                           */
+  int32_t unit_capacity;      /* entries of `units`                           */
+  mla_shared_unit_t* units;   /* host, caller-owned                           */
   int32_t* own_indptr;        /* host, caller-owned, >= B * ceil(q_len * H /
                                  128) + 1 entries                             */
-  int32_t* units;             /* host, caller-owned, >= 2 * item_capacity     */
   int32_t* cta_indptr;        /* host, caller-owned, >= dev->num_sms + 1      */
   /* outputs */
-  int32_t num_items;
+  int32_t num_units;
   int32_t num_slots;
   int32_t shared_parts;       /* pieces of the common tokens                  */
   int32_t num_ctas;
@@ -911,14 +911,14 @@ typedef struct {
  * mla_plan_shared -- lay out the work of mla_decode_shared for contexts of
  * these lengths (the common tokens among them): the common tokens for the rows
  * of the whole batch in groups of 128, each request's own ones for its own
- * rows, each cut into pieces so that the device is evenly busy. An item is two
- * units of work, 2 * item + half of the value columns; CTA c does
+ * rows, each cut into pieces so that the device is evenly busy. A piece is two
+ * units, one for each half of the value columns; CTA c does
  * units[cta_indptr[c] .. cta_indptr[c + 1]). The plan serves contexts of any length (a request's last piece takes
  * what it has grown by) of the same B, q_len, H, page size and P, in the time
  * planned for these. own_indptr: of each request's group of 128 rows, its
  * first slot (the slots before are the common tokens': of the group g of the
  * batch's rows, shared_parts slots from g * shared_parts on). Host code; touches no GPU.
- * MLA_ERR_CAPACITY (with num_items set) where items does not hold them.
+ * MLA_ERR_CAPACITY (with num_units set) where units does not hold them.
  */
 mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_t B, int32_t num_heads, int32_t q_len,
                              int32_t block_size, const mla_device_info_t* dev, mla_shared_plan_t* plan);
@@ -935,11 +935,10 @@ typedef struct {
   int32_t causal;             /* as mla_decode_desc_t.causal                  */
   int32_t shared_tokens;      /* P, as planned                                */
   int32_t out_dtype;          /* MLA_F16, MLA_BF16 or MLA_F32                 */
-  const mla_shared_item_t* items; /* DEVICE, as planned, 16-byte aligned      */
+  const mla_shared_unit_t* units; /* DEVICE, as planned, 16-byte aligned      */
   const int32_t* own_indptr;  /* DEVICE, as planned                           */
-  const int32_t* units;       /* DEVICE, as planned                           */
   const int32_t* cta_indptr;  /* DEVICE, as planned                           */
-  int32_t num_items, num_slots, shared_parts, num_ctas; /* as planned         */
+  int32_t num_units, num_slots, shared_parts, num_ctas; /* as planned         */
   void* workspace;            /* DEVICE, >= mla_decode_shared_workspace_bytes
                                  bytes, 16-byte aligned; need not be cleared.
                                  Calls sharing it must not overlap in time.    */

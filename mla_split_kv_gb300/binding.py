@@ -154,19 +154,18 @@ class mla_prefill_desc_t(ctypes.Structure):
     ]
 
 
-class mla_shared_item_t(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("row0", "rows", "request", "t0", "t1", "slot")] + [("reserved", ctypes.c_int32 * 2)]
+class mla_shared_unit_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("row0", "rows", "request", "t0", "t1", "slot", "half", "reserved")]
 
 
 class mla_shared_plan_t(ctypes.Structure):
     _fields_ = [
         ("shared_tokens", ctypes.c_int32),
-        ("item_capacity", ctypes.c_int32),
-        ("items", ctypes.POINTER(mla_shared_item_t)),
+        ("unit_capacity", ctypes.c_int32),
+        ("units", ctypes.POINTER(mla_shared_unit_t)),
         ("own_indptr", ctypes.POINTER(ctypes.c_int32)),
-        ("units", ctypes.POINTER(ctypes.c_int32)),
         ("cta_indptr", ctypes.POINTER(ctypes.c_int32)),
-        ("num_items", ctypes.c_int32),
+        ("num_units", ctypes.c_int32),
         ("num_slots", ctypes.c_int32),
         ("shared_parts", ctypes.c_int32),
         ("num_ctas", ctypes.c_int32),
@@ -185,11 +184,10 @@ class mla_shared_desc_t(ctypes.Structure):
         ("causal", ctypes.c_int32),
         ("shared_tokens", ctypes.c_int32),
         ("out_dtype", ctypes.c_int32),
-        ("items", ctypes.c_void_p),
-        ("own_indptr", ctypes.c_void_p),
         ("units", ctypes.c_void_p),
+        ("own_indptr", ctypes.c_void_p),
         ("cta_indptr", ctypes.c_void_p),
-        ("num_items", ctypes.c_int32),
+        ("num_units", ctypes.c_int32),
         ("num_slots", ctypes.c_int32),
         ("shared_parts", ctypes.c_int32),
         ("num_ctas", ctypes.c_int32),
@@ -481,10 +479,9 @@ def mla_prefill_workspace_bytes(dev: mla_device_info_t, num_requests: int, num_h
 class SharedPlan:
     """Host result of :func:`mla_plan_shared`."""
 
-    def __init__(self, items, own_indptr, units, cta_indptr, num_slots, shared_parts):
-        self.items = items  # list of (row0, rows, request, t0, t1, slot)
+    def __init__(self, units, own_indptr, cta_indptr, num_slots, shared_parts):
+        self.units = units  # list of (row0, rows, request, t0, t1, slot, half), CTA after CTA
         self.own_indptr = own_indptr  # first slot of each request's group of 128 rows
-        self.units = units  # 2 * item + half, CTA after CTA
         self.cta_indptr = cta_indptr
         self.num_slots = num_slots
         self.shared_parts = shared_parts
@@ -500,20 +497,17 @@ def mla_plan_shared(context_lens: Sequence[int], shared_tokens: int, num_heads: 
     st = lib.mla_plan_shared(lens, B, num_heads, q_len, block_size, ctypes.byref(dev), ctypes.byref(plan))
     if st not in (MLA_OK, MLA_ERR_CAPACITY):
         raise MlaError(st, "mla_plan_shared")
-    items = (mla_shared_item_t * max(1, plan.num_items))()
+    units = (mla_shared_unit_t * max(1, plan.num_units))()
     indptr = (ctypes.c_int32 * (B * -(-q_len * num_heads // 128) + 1))()
-    plan.item_capacity = plan.num_items
-    plan.items = ctypes.cast(items, ctypes.POINTER(mla_shared_item_t))
-    plan.own_indptr = ctypes.cast(indptr, ctypes.POINTER(ctypes.c_int32))
-    units = (ctypes.c_int32 * (2 * max(1, plan.num_items)))()
     ctas = (ctypes.c_int32 * (dev.num_sms + 1))()
-    plan.units = ctypes.cast(units, ctypes.POINTER(ctypes.c_int32))
+    plan.unit_capacity = plan.num_units
+    plan.units = ctypes.cast(units, ctypes.POINTER(mla_shared_unit_t))
+    plan.own_indptr = ctypes.cast(indptr, ctypes.POINTER(ctypes.c_int32))
     plan.cta_indptr = ctypes.cast(ctas, ctypes.POINTER(ctypes.c_int32))
     _check(lib.mla_plan_shared(lens, B, num_heads, q_len, block_size, ctypes.byref(dev), ctypes.byref(plan)),
            "mla_plan_shared")
-    out = [(x.row0, x.rows, x.request, x.t0, x.t1, x.slot) for x in items[: plan.num_items]]
-    return SharedPlan(out, list(indptr), list(units)[: 2 * plan.num_items], list(ctas)[: plan.num_ctas + 1], plan.num_slots,
-                      plan.shared_parts)
+    out = [(x.row0, x.rows, x.request, x.t0, x.t1, x.slot, x.half) for x in units[: plan.num_units]]
+    return SharedPlan(out, list(indptr), list(ctas)[: plan.num_ctas + 1], plan.num_slots, plan.shared_parts)
 
 
 def mla_decode_shared(q_absorbed: int, q_pe: int, ckv_cache: int, kpe_cache: int, shared_table: int, block_table: int,

@@ -273,10 +273,10 @@ mla_status_t mla_decode_shared(const void* q_absorbed, const void* q_pe, const v
                                float scale, void* out, float* out_lse, const mla_shared_desc_t* d) {
   if (d == nullptr || q_absorbed == nullptr || q_pe == nullptr || ckv_cache == nullptr || kpe_cache == nullptr ||
       shared_table == nullptr || block_table == nullptr || context_lens == nullptr || out == nullptr ||
-      d->items == nullptr || d->own_indptr == nullptr || d->units == nullptr || d->cta_indptr == nullptr)
+      d->units == nullptr || d->own_indptr == nullptr || d->cta_indptr == nullptr)
     return reject(MLA_ERR_INVALID_ARG);
   if (d->num_requests < 1 || d->num_blocks < 1 || d->max_blocks_per_req < 1 || (d->causal != 0 && d->causal != 1) ||
-      !std::isfinite(scale) || d->num_items < 1 || d->num_slots < 1 || d->shared_parts < 1 || d->num_ctas < 1)
+      !std::isfinite(scale) || d->num_units < 1 || d->num_slots < 1 || d->shared_parts < 1 || d->num_ctas < 1)
     return reject(MLA_ERR_INVALID_ARG);
   if ((d->num_heads != 16 && d->num_heads != 64 && d->num_heads != 128) || d->q_len < 1 || d->q_len > MLA_MAX_Q_LEN ||
       !valid_page(d->block_size))
@@ -286,11 +286,11 @@ mla_status_t mla_decode_shared(const void* q_absorbed, const void* q_pe, const v
   if (d->shared_tokens < d->block_size || d->shared_tokens % d->block_size != 0) return reject(MLA_ERR_INVALID_ARG);
   const int64_t rows = static_cast<int64_t>(d->num_requests) * d->q_len * d->num_heads;
   const uint64_t cached = static_cast<uint64_t>(d->num_blocks) * static_cast<uint64_t>(d->block_size);
-  if (rows > (1ll << 28) || cached > 0x7fffffffull || d->num_items > (1 << 28) || d->num_ctas > 65535) return reject(MLA_ERR_UNSUPPORTED);
+  if (rows > (1ll << 28) || cached > 0x7fffffffull || d->num_units > (1 << 28) || d->num_ctas > 65535) return reject(MLA_ERR_UNSUPPORTED);
   if (!mla::is_aligned(q_absorbed, 16) || !mla::is_aligned(q_pe, 16) || !mla::is_aligned(ckv_cache, 16) ||
       !mla::is_aligned(kpe_cache, 16) || !mla::is_aligned(out, 16) || !mla::is_aligned(shared_table, 4) ||
-      !mla::is_aligned(block_table, 4) || !mla::is_aligned(context_lens, 4) || !mla::is_aligned(d->items, 16) ||
-      !mla::is_aligned(d->own_indptr, 4) || !mla::is_aligned(d->units, 4) || !mla::is_aligned(d->cta_indptr, 4) || (out_lse != nullptr && !mla::is_aligned(out_lse, 4)))
+      !mla::is_aligned(block_table, 4) || !mla::is_aligned(context_lens, 4) || !mla::is_aligned(d->units, 16) ||
+      !mla::is_aligned(d->own_indptr, 4) || !mla::is_aligned(d->cta_indptr, 4) || (out_lse != nullptr && !mla::is_aligned(out_lse, 4)))
     return reject(MLA_ERR_INVALID_ARG);
   if (d->workspace == nullptr || !mla::is_aligned(d->workspace, 16) ||
       d->workspace_bytes < mla_decode_shared_workspace_bytes(d->num_slots))
@@ -312,9 +312,8 @@ mla_status_t mla_decode_shared(const void* q_absorbed, const void* q_pe, const v
   p.shared_table = shared_table;
   p.block_table = block_table;
   p.context_lens = context_lens;
-  p.items = reinterpret_cast<const int32_t*>(d->items);
+  p.units = reinterpret_cast<const int32_t*>(d->units);
   p.own_indptr = d->own_indptr;
-  p.units = d->units;
   p.cta_indptr = d->cta_indptr;
   p.out = out;
   p.out_lse = out_lse;
@@ -331,7 +330,6 @@ mla_status_t mla_decode_shared(const void* q_absorbed, const void* q_pe, const v
   p.causal = d->causal;
   p.shared_tokens = d->shared_tokens;
   p.shared_parts = d->shared_parts;
-  p.num_items = d->num_items;
   p.num_ctas = d->num_ctas;
   p.out_dtype = d->out_dtype == MLA_F32 ? 2 : d->out_dtype == MLA_BF16 ? 1 : 0;
   p.timeout_ns = mla::wait_timeout_ns();

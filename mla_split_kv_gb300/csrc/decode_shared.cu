@@ -117,15 +117,14 @@ __device__ __forceinline__ int visible(const SharedParams& p, int row) {
 __device__ __forceinline__ bool unit_of(const SharedParams& p, int k, int lane, Unit& w) {
   const int at = __ldg(p.cta_indptr + blockIdx.x) + k;
   if (at >= __ldg(p.cta_indptr + blockIdx.x + 1)) return false;
-  const int u = __ldg(p.units + at);
-  const int4* const item = reinterpret_cast<const int4*>(p.items) + 2 * (u >> 1);
-  const int4 x = __ldg(item), y = __ldg(item + 1);
+  const int4* const unit = reinterpret_cast<const int4*>(p.units) + 2 * at;
+  const int4 x = __ldg(unit), y = __ldg(unit + 1);
   w.row0 = x.x;
   w.rows = max(0, min(min(x.y, kRows), p.rows - x.x));
   w.request = x.z;
   w.t0 = x.w;
   w.slot = y.y;
-  w.half = u & 1;
+  w.half = y.z & 1;
   int most = 0, least = 0x7fffffff;
   for (int r = lane; r < w.rows; r += 32) {
     const int v = visible(p, w.row0 + r);
@@ -359,36 +358,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       {  // the queries: the products of the unit before are done
         const uint4* const src = reinterpret_cast<const uint4*>(p.q_abs + row * kRank);
-        const uint4* const pe = reinterpret_cast<const uint4*>(p.q_pe + row * kRope);
         const uint4 none = make_uint4(0, 0, 0, 0);
-        constexpr int kPieces = 24;  // 16 bytes each, in flight together: 192 columns
-        static_assert(kQTmemBlocks * 8 == 2 * kPieces && 3 * 8 == kPieces, "three rounds of loads");
+        // the blocks of shared memory, eight lanes a row's 128 bytes, all in flight; those of tensor memory beside them, a
+        // thread a row, in two rounds of 24 16-byte pieces
+        for (int at = tid; at < 3 * kRows * 8; at += kRows) {
+          const int c = at / (kRows * 8), rr = at / 8 % kRows, j = at % 8;
+          const bool in = rr < w.rows;
+          const long long from = w.row0 + (in ? rr : 0);
+          const uint16_t* const piece = c < 2 ? p.q_abs + from * kRank + (kQTmemBlocks + c) * kBoxCols + 8 * j : p.q_pe + from * kRope + 8 * j;
+          cp_async16(smem + c * kQChunk + rr * 128 + ((j ^ (rr & 7)) << 4), piece, in ? 16u : 0u);
+        }
+        constexpr int kPieces = 24;
+        static_assert(kQTmemBlocks * 8 == 2 * kPieces, "two rounds of loads");
 #pragma unroll
-        for (int round = 0; round < 3; ++round) {
+        for (int round = 0; round < 2; ++round) {
           uint4 x[kPieces];
 #pragma unroll
-          for (int j = 0; j < kPieces; ++j) {
-            const int at = round * kPieces + j;
-            x[j] = !real ? none : at < kRank / 8 ? src[at] : pe[at - kRank / 8];
-          }
-          if (round < 2) {
+          for (int j = 0; j < kPieces; ++j) x[j] = real ? src[round * kPieces + j] : none;
 #pragma unroll
-            for (int g = 0; g < kPieces / 4; ++g) {
-              float v[16];
+          for (int g = 0; g < kPieces / 4; ++g) {
+            float v[16];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                v[4 * j] = __uint_as_float(x[4 * g + j].x);
-                v[4 * j + 1] = __uint_as_float(x[4 * g + j].y);
-                v[4 * j + 2] = __uint_as_float(x[4 * g + j].z);
-                v[4 * j + 3] = __uint_as_float(x[4 * g + j].w);
-              }
-              tmem_st16(tmem + lanes + kTmemQ + 16 * (round * (kPieces / 4) + g), v);
+            for (int j = 0; j < 4; ++j) {
+              v[4 * j] = __uint_as_float(x[4 * g + j].x);
+              v[4 * j + 1] = __uint_as_float(x[4 * g + j].y);
+              v[4 * j + 2] = __uint_as_float(x[4 * g + j].z);
+              v[4 * j + 3] = __uint_as_float(x[4 * g + j].w);
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j) sts128(smem_u32(smem) + (j >> 3) * kQChunk + r * 128 + (((j & 7) ^ (r & 7)) << 4), x[j]);
+            tmem_st16(tmem + lanes + kTmemQ + 16 * (round * (kPieces / 4) + g), v);
           }
         }
+        cp_async_wait_all();
         tmem_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();

@@ -298,16 +298,15 @@ struct SharedParams {
   const int32_t* shared_table; // [shared_tokens / bs]
   const int32_t* block_table;  // [B, max_blocks]
   const int32_t* context_lens; // [B]
-  const int32_t* items;        // eight words an item (mla_shared_item_t)
+  const int32_t* units;        // eight words a unit (mla_shared_unit_t)
   const int32_t* own_indptr;   // [B * groups of a request + 1]
-  const int32_t* units;        // 2 * item + half
   const int32_t* cta_indptr;   // [num_ctas + 1]
   void* out;                   // [rows, 512] of out_dtype
   float* out_lse;              // [rows] or null
   float* part_o;               // [slots, 128, 512]
   float* part_lse;             // [slots, 128]
   float scale_log2;
-  int32_t B, H, q_len, rows, bs, max_blocks, num_blocks, causal, shared_tokens, shared_parts, num_items, num_ctas, out_dtype;
+  int32_t B, H, q_len, rows, bs, max_blocks, num_blocks, causal, shared_tokens, shared_parts, num_ctas, out_dtype;
   uint64_t timeout_ns;
 };
 cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& tm_piece, const CUtensorMap& tm_kpe,

@@ -37,7 +37,7 @@ int64_t pieces_of(int64_t tiles, int64_t length) { return std::max<int64_t>(1, (
 extern "C" mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_t B, int32_t num_heads, int32_t q_len,
                                         int32_t block_size, const mla_device_info_t* dev, mla_shared_plan_t* plan) try {
   if (context_lens_host == nullptr || dev == nullptr || plan == nullptr) return MLA_ERR_INVALID_ARG;
-  if (B < 1 || dev->num_sms < 1 || plan->item_capacity < 0) return MLA_ERR_INVALID_ARG;
+  if (B < 1 || dev->num_sms < 1 || plan->unit_capacity < 0) return MLA_ERR_INVALID_ARG;
   if (num_heads != 16 && num_heads != 64 && num_heads != 128) return MLA_ERR_UNSUPPORTED;
   if (q_len < 1 || q_len > MLA_MAX_Q_LEN) return MLA_ERR_UNSUPPORTED;
   if (block_size != 16 && block_size != 32 && block_size != 64) return MLA_ERR_UNSUPPORTED;
@@ -116,36 +116,33 @@ extern "C" mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_
     }
   }
   first.push_back(slot);
-  if (slot > (1ll << 28)) return MLA_ERR_UNSUPPORTED;
-  plan->num_items = static_cast<int32_t>(pieces.size());
+  if (slot > (1ll << 27)) return MLA_ERR_UNSUPPORTED;
+  plan->num_units = 2 * static_cast<int32_t>(pieces.size());
   plan->num_slots = static_cast<int32_t>(slot);
   plan->shared_parts = static_cast<int32_t>(parts);
-  if (plan->num_items > plan->item_capacity) return MLA_ERR_CAPACITY;
-  if (plan->items == nullptr || plan->own_indptr == nullptr || plan->units == nullptr || plan->cta_indptr == nullptr)
-    return MLA_ERR_INVALID_ARG;
+  plan->num_ctas = std::min(dev->num_sms, plan->num_units);
+  if (plan->num_units > plan->unit_capacity) return MLA_ERR_CAPACITY;
+  if (plan->units == nullptr || plan->own_indptr == nullptr || plan->cta_indptr == nullptr) return MLA_ERR_INVALID_ARG;
   std::stable_sort(pieces.begin(), pieces.end(), [](const Piece& a, const Piece& b) { return a.tiles > b.tiles; });
-  for (size_t i = 0; i < pieces.size(); ++i) {
-    const Piece& x = pieces[i];
-    plan->items[i] = mla_shared_item_t{static_cast<int32_t>(x.row0), static_cast<int32_t>(x.rows), x.request, static_cast<int32_t>(x.t0),
-                                       static_cast<int32_t>(x.t1), static_cast<int32_t>(x.slot), {0, 0}};
-  }
-  const int32_t ctas = static_cast<int32_t>(std::min<int64_t>(dev->num_sms, 2 * static_cast<int64_t>(pieces.size())));
-  std::vector<std::vector<int32_t>> lists(ctas);
+  std::vector<std::vector<int32_t>> lists(plan->num_ctas);
   std::priority_queue<std::pair<int64_t, int32_t>, std::vector<std::pair<int64_t, int32_t>>, std::greater<>> free_at;
-  for (int32_t c = 0; c < ctas; ++c) free_at.emplace(0, c);
-  for (size_t u = 0; u < 2 * pieces.size(); ++u) {
+  for (int32_t c = 0; c < plan->num_ctas; ++c) free_at.emplace(0, c);
+  for (int32_t u = 0; u < plan->num_units; ++u) {
     const auto next = free_at.top();
     free_at.pop();
-    lists[next.second].push_back(static_cast<int32_t>(u));
+    lists[next.second].push_back(u);
     free_at.emplace(next.first + pieces[u >> 1].tiles + kUnitTiles, next.second);
   }
   int32_t at = 0;
-  for (int32_t c = 0; c < ctas; ++c) {
+  for (int32_t c = 0; c < plan->num_ctas; ++c) {
     plan->cta_indptr[c] = at;
-    for (const int32_t u : lists[c]) plan->units[at++] = u;
+    for (const int32_t u : lists[c]) {
+      const Piece& x = pieces[u >> 1];
+      plan->units[at++] = mla_shared_unit_t{static_cast<int32_t>(x.row0), static_cast<int32_t>(x.rows), x.request,
+                                            static_cast<int32_t>(x.t0), static_cast<int32_t>(x.t1), static_cast<int32_t>(x.slot), u & 1, 0};
+    }
   }
-  plan->cta_indptr[ctas] = at;
-  plan->num_ctas = ctas;
+  plan->cta_indptr[plan->num_ctas] = at;
   for (size_t i = 0; i < first.size(); ++i) plan->own_indptr[i] = static_cast<int32_t>(first[i]);
   return MLA_OK;
 } catch (...) {  // out of memory

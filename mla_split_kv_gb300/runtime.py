@@ -703,9 +703,8 @@ class SharedPlan:
     causal: bool
     shared_tokens: int
     plan: nb.SharedPlan
-    items: torch.Tensor
-    own_indptr: torch.Tensor
     units: torch.Tensor
+    own_indptr: torch.Tensor
     cta_indptr: torch.Tensor
     workspace: torch.Tensor
 
@@ -720,11 +719,11 @@ def plan_shared(context_lens: Sequence[int], shared_tokens: int, num_heads: int,
     index = torch.device(device).index
     dev = dev if dev is not None else nb.mla_device_query(-1 if index is None else index)
     plan = nb.mla_plan_shared(context_lens, shared_tokens, num_heads, q_len, block_size, dev)
-    items = np.zeros((len(plan.items), 8), np.int32)
-    items[:, :6] = plan.items
+    units = np.zeros((len(plan.units), 8), np.int32)
+    units[:, :7] = plan.units
     return SharedPlan(len(context_lens), num_heads, q_len, block_size, dtype, causal, shared_tokens, plan,
-                      torch.from_numpy(items).to(device),
-                      *(torch.tensor(x, dtype=torch.int32, device=device) for x in (plan.own_indptr, plan.units, plan.cta_indptr)),
+                      torch.from_numpy(units).to(device),
+                      *(torch.tensor(x, dtype=torch.int32, device=device) for x in (plan.own_indptr, plan.cta_indptr)),
                       torch.empty(nb.mla_decode_shared_workspace_bytes(plan.num_slots), dtype=torch.uint8, device=device))
 
 
@@ -753,8 +752,8 @@ def decode_shared(plan: SharedPlan, q_abs: torch.Tensor, q_pe: torch.Tensor, ckv
     raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
     p = plan.plan
     d = nb.mla_shared_desc_t(B, H, q_len, bs, nblk, width, CODE_OF[dtype], 1 if plan.causal else 0, plan.shared_tokens,
-                             _code_of(out, "out"), plan.items.data_ptr(), plan.own_indptr.data_ptr(),
-                             plan.units.data_ptr(), plan.cta_indptr.data_ptr(), len(p.items), p.num_slots,
+                             _code_of(out, "out"), plan.units.data_ptr(), plan.own_indptr.data_ptr(),
+                             plan.cta_indptr.data_ptr(), len(p.units), p.num_slots,
                              p.shared_parts, len(p.cta_indptr) - 1, plan.workspace.data_ptr(), plan.workspace.numel(), raw_stream)
     nb.mla_decode_shared(q_abs.data_ptr(), q_pe.data_ptr(), ckv.data_ptr(), kpe.data_ptr(),
                          (shared_table if shared_table is not None else block_table).data_ptr(), block_table.data_ptr(),
