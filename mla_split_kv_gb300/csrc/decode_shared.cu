@@ -162,8 +162,9 @@ __device__ __forceinline__ void clean_values(uint8_t* p0, uint8_t* p1, int r) {
   }
 }
 
+// 168 registers a thread: the merge's CTAs then fit on an SM beside this kernel's one and wait there for its end.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __maxnreg__(168)
     mla_decode_shared_kernel(const __grid_constant__ CUtensorMap tm_half, const __grid_constant__ CUtensorMap tm_piece,
                              const __grid_constant__ CUtensorMap tm_kpe, const SharedParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -529,16 +530,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // A warp a row: its parts in order (the common tokens' pieces, then its own tokens'), M = max lse, weights 2^(lse - M).
-constexpr int kMergeThreads = 256;
-__global__ void __launch_bounds__(kMergeThreads) mla_decode_shared_merge_kernel(const SharedParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
+// Latency: the offsets (the plan's) are read before the decode kernel ends, the first parts' values beside their LSE.
+constexpr int kMergeThreads = 128;
+constexpr int kMergeDepth = 2;  // parts in flight
+__global__ void __launch_bounds__(kMergeThreads, 6) mla_decode_shared_merge_kernel(const SharedParams p) {
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
   const int per = p.q_len * p.H, b = row / per, r = row % per;
   const int own = b * ((per + kRows - 1) / kRows) + r / kRows;
-  const int s0 = p.own_indptr[own], n_own = p.own_indptr[own + 1] - s0;
+  const bool in = row < p.rows;
+  const int s0 = in ? p.own_indptr[own] : 0, n_own = in ? p.own_indptr[own + 1] - s0 : 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!in) return;
   const int n = p.shared_parts + n_own;
   // the row of part j in the slots
   auto at = [&](int j) -> long long {
@@ -547,34 +551,38 @@ __global__ void __launch_bounds__(kMergeThreads) mla_decode_shared_merge_kernel(
   };
   float M = -INFINITY;
   for (int j = lane; j < n; j += 32) M = max_nan(M, p.part_lse[at(j)]);
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, d));
   float4 acc[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
+  float l[kMergeDepth];
+  float4 v[kMergeDepth][4];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int j = 0; j < kMergeDepth; ++j) {
+      const long long a = at(min(j0 + j, n - 1));
+      l[j] = j0 + j < n ? p.part_lse[a] : -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[j][c] = reinterpret_cast<const float4*>(p.part_o + a * kRank)[lane + 32 * c];
+    }
+  };
+  load(0);
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, d));
   if (M != -INFINITY) {
-    for (int j0 = 0; j0 < n; j0 += 4) {
-      float wj[4];
-      float4 v[4][4];
+    for (int j0 = 0; j0 < n; j0 += kMergeDepth) {
+      if (j0 > 0) load(j0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long long a = at(min(j0 + j, n - 1));
-        const float lj = j0 + j < n ? p.part_lse[a] : -INFINITY;
-        wj[j] = lj == -INFINITY ? 0.f : exp2f(lj - M);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          v[j][c] = lj != -INFINITY ? reinterpret_cast<const float4*>(p.part_o + a * kRank)[lane + 32 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        den += wj[j];
+      for (int j = 0; j < kMergeDepth; ++j) {
+        if (l[j] == -INFINITY) continue;  // (nothing was written there)
+        const float wj = exp2f(l[j] - M);
+        den += wj;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          acc[c].x = fmaf(wj[j], v[j][c].x, acc[c].x);
-          acc[c].y = fmaf(wj[j], v[j][c].y, acc[c].y);
-          acc[c].z = fmaf(wj[j], v[j][c].z, acc[c].z);
-          acc[c].w = fmaf(wj[j], v[j][c].w, acc[c].w);
+          acc[c].x = fmaf(wj, v[j][c].x, acc[c].x);
+          acc[c].y = fmaf(wj, v[j][c].y, acc[c].y);
+          acc[c].z = fmaf(wj, v[j][c].z, acc[c].z);
+          acc[c].w = fmaf(wj, v[j][c].w, acc[c].w);
         }
       }
     }

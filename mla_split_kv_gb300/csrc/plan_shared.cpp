@@ -19,7 +19,7 @@ constexpr int64_t kTile = 64;   // tokens
 constexpr int64_t kGroup = 128; // rows
 // A unit's time in tiles of about 1.1 us: its tiles, and the start and the end (queries, the first loads, the partial
 // output). A row's part costs the merge about 2 KB of L2, of which the device reads 5 MB in the time of a tile.
-constexpr int64_t kUnitTiles = 5;
+constexpr int64_t kUnitTiles = 6;
 constexpr int64_t kMergeParts = 2500;
 
 struct Piece {
@@ -62,9 +62,11 @@ extern "C" mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_
 
   // tile counts a piece may have, around an even share of one SM's two units at a time
   const int64_t share = std::max<int64_t>(1, 2 * all / dev->num_sms);
-  int64_t best = most, best_cost = -1;
-  for (int64_t eighths : {2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 16}) {
-    const int64_t length = std::min(most, std::max<int64_t>(2, (share * eighths + 7) / 8));
+  int64_t best = most, best_cost = -1, tried = 0;
+  for (int64_t part = 8; part <= 64; ++part) {  // 32nds of the share
+    const int64_t length = std::min(most, std::max<int64_t>(2, (share * part + 31) / 32));
+    if (length == tried) continue;
+    tried = length;
     // lengths of the units, counted: the pieces of one run are equally long but for the last
     std::vector<std::pair<int64_t, int64_t>> units;  // tiles, how many
     int64_t parts = 0;
