@@ -1,9 +1,9 @@
 // Work of a batch whose contexts start with the same tokens (host only, no GPU access).
 //
 // The common tokens are cut into pieces for every group of 128 of the batch's rows, each request's own tokens for its
-// own groups, all pieces about equally long: a piece is two units of work (one half of the value columns each), the
-// units go longest first to the CTA (one an SM) that is free first, and the length is the one among some tried whose
-// busiest CTA and merge are done first.
+// own groups: into equally long ones, or into ones of a length and what is left. A piece is two units of work (one half
+// of the value columns each), the units go longest first to the CTA (one an SM) that is free first, and the way and
+// length are those among some tried whose busiest CTA and merge are done first.
 #include <algorithm>
 #include <cstdint>
 #include <functional>
@@ -29,8 +29,16 @@ struct Piece {
 };
 
 int64_t tiles_of(int64_t tokens) { return (tokens + kTile - 1) / kTile; }
-// Pieces of about `length` tiles, none longer.
-int64_t pieces_of(int64_t tiles, int64_t length) { return std::max<int64_t>(1, (tiles + length - 1) / length); }
+// How runs are cut: no piece longer than `length` tiles, all but the last as long as `of` says.
+struct Cut {
+  int64_t length;
+  bool even;
+  int64_t pieces(int64_t tiles) const { return std::max<int64_t>(1, (tiles + length - 1) / length); }
+  int64_t of(int64_t tiles) const {
+    const int64_t n = pieces(tiles);
+    return even ? std::max<int64_t>(1, (tiles + n - 1) / n) : length;
+  }
+};
 
 }  // namespace
 
@@ -62,44 +70,50 @@ extern "C" mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_
 
   // tile counts a piece may have, around an even share of one SM's two units at a time
   const int64_t share = std::max<int64_t>(1, 2 * all / dev->num_sms);
-  int64_t best = most, best_cost = -1, tried = 0;
-  for (int64_t part = 8; part <= 64; ++part) {  // 32nds of the share
+  Cut best{most, true};
+  int64_t best_cost = -1, tried = 0;
+  // (many requests even out by themselves: fewer lengths are tried)
+  const int64_t step = groups + static_cast<int64_t>(B) * own_groups > 500 ? 8 : 1;
+  for (int64_t part = 8; part <= 64; part += step) {  // 32nds of the share
     const int64_t length = std::min(most, std::max<int64_t>(2, (share * part + 31) / 32));
     if (length == tried) continue;
     tried = length;
-    // lengths of the units, counted: the pieces of one run are equally long but for the last
-    std::vector<std::pair<int64_t, int64_t>> units;  // tiles, how many
-    int64_t parts = 0;
-    auto add = [&](int64_t tiles, int64_t times, int64_t rows_of) {
-      const int64_t n = pieces_of(tiles, length), each = (tiles + n - 1) / n;
-      units.emplace_back(each, 2 * times * n);
-      parts += n * rows_of;
-    };
-    add(common, groups, rows);
-    for (int32_t b = 0; b < B; ++b) add(own[b], own_groups, per);
-    std::sort(units.begin(), units.end(), std::greater<>());
-    int64_t busiest = 0;
-    std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
-    for (int32_t i = 0; i < dev->num_sms; ++i) ends.push(0);
-    for (const auto& u : units) {
-      for (int64_t i = 0; i < u.second; ++i) {
-        const int64_t end = ends.top() + u.first + kUnitTiles;
-        ends.pop();
-        ends.push(end);
-        busiest = std::max(busiest, end);
+    for (const bool even : {true, false}) {
+      const Cut cut{length, even};
+      std::vector<std::pair<int64_t, int64_t>> units;  // tiles, how many
+      int64_t parts = 0;
+      auto add = [&](int64_t tiles, int64_t times, int64_t rows_of) {
+        const int64_t n = cut.pieces(tiles), each = cut.of(tiles);
+        if (n > 1) units.emplace_back(each, 2 * times * (n - 1));
+        units.emplace_back(tiles - (n - 1) * each, 2 * times);
+        parts += n * rows_of;
+      };
+      add(common, groups, rows);
+      for (int32_t b = 0; b < B; ++b) add(own[b], own_groups, per);
+      std::sort(units.begin(), units.end(), std::greater<>());
+      int64_t busiest = 0;
+      std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
+      for (int32_t i = 0; i < dev->num_sms; ++i) ends.push(0);
+      for (const auto& u : units) {
+        for (int64_t i = 0; i < u.second; ++i) {
+          const int64_t end = ends.top() + u.first + kUnitTiles;
+          ends.pop();
+          ends.push(end);
+          busiest = std::max(busiest, end);
+        }
       }
-    }
-    const int64_t cost = busiest + parts / kMergeParts;
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = length;
+      const int64_t cost = busiest + parts / kMergeParts;
+      if (best_cost < 0 || cost < best_cost) {
+        best_cost = cost;
+        best = cut;
+      }
     }
   }
 
   std::vector<Piece> pieces;
   int64_t slot = 0;
   auto cut = [&](int64_t row0, int64_t n_rows, int32_t request, int64_t t0, int64_t tokens, bool open) {
-    const int64_t tiles = tiles_of(tokens), n = pieces_of(tiles, best), each = std::max<int64_t>(1, (tiles + n - 1) / n);
+    const int64_t tiles = tiles_of(tokens), n = best.pieces(tiles), each = best.of(tiles);
     for (int64_t j = 0; j < n; ++j) {
       const int64_t a = std::min(tokens, j * each * kTile), e = std::min(tokens, (j + 1) * each * kTile);
       const bool last = j + 1 == n;
