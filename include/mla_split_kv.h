@@ -857,8 +857,8 @@ typedef struct {
  *
  * Precision: scores, maxima, sums and out_lse are fp32, the weights of the value
  * product are rounded once to `dtype` (half a step: 2^-12 of themselves in fp16,
- * where the smallest count as at least 2^-33 of the row's greatest, 2^-9 in
- * bf16) and the sum that normalizes takes them unrounded.
+ * or 2^-25 of the row's greatest where that is more, 2^-9 of themselves in bf16)
+ * and the sum that normalizes takes them unrounded.
  *
  * q_nope : device, row i, head h at i * q_nope_stride[0] + h * q_nope_stride[1]
  *          elements, 128 of them; q_pe alike, 64; both 16-byte aligned
@@ -963,7 +963,8 @@ typedef struct {
  *
  * Precision: scores, maxima, sums and out_lse are fp32; the weights of the value
  * product are rounded once to `dtype` (half a step: 2^-12 of themselves in fp16,
- * 2^-9 in bf16) and the sum that normalizes takes them unrounded. The partials
+ * or 2^-25 of the row's greatest where that is more, 2^-9 of themselves in bf16)
+ * and the sum that normalizes takes them unrounded. The partials
  * are fp32; `out` is rounded once to out_dtype.
  *
  * q_absorbed, q_pe, caches: as for mla_decode_partial, 16-bit caches only

@@ -19,14 +19,15 @@
 // each with barriers of its own, so that a chunk is refilled as soon as its last product is done. A tile's keys and
 // values together are 80 KB: two whole ones would not fit beside the queries, eight chunks are 1.6.
 //
-// The running maximum is moved only when a tile's maximum passes it by more than 2^8 (the weights stay below 256, in
-// fp16 too), so O is seldom rescaled; the sums are those of the unrounded weights in fp32. P is rounded once to 16 bits
+// The running maximum is moved only when a tile's maximum passes it by more than the weights' type has room for (2^15 in
+// fp16; 2^60 in bf16, whose sums and O stay far below fp32's end, too), so O is hardly ever rescaled; the sums are those of
+// the unrounded weights in fp32. P is rounded once to 16 bits
 // (2^-9 of itself in bf16, 2^-12 in fp16, as the output is).
 //
 // What lies in a tile behind a row's last visible token counts for nothing, infinities and NaN included: its weight is
 // an exact 0, and where a tile has tokens that some row of the subtile does not see, its values are searched for
 // numbers that are not finite, which are set to 0 in shared memory; if one of them belongs to a token that other rows
-// do see, those rows take it from the values themselves at the end (poison()).
+// do see, those rows take it from the values themselves at the end.
 //
 // Units (256 rows, head, run of tiles) go to the CTAs longest first, in turns. Where there are too few of them for the
 // GPU, long runs are cut into pieces whose normalized outputs and LSE are merged by a kernel of their own
@@ -52,11 +53,10 @@ constexpr int kTileChunks = 5;             // keys 0, 1, rotary, values 0, 1
 constexpr int kQBytes = 3 * kChunk;        // of a subtile
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kThreads = 12 * 32;          // (the last two warps only make the third warpgroup whole)
-// Registers: launched with 168 a thread (64,512 in all); the softmax warps take 216, the third warpgroup keeps 64.
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 64;
+// Registers: launched with 168 a thread (64,512 in all); the softmax warps take 224, the third warpgroup keeps 56.
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 168 * kThreads, "what the block was launched with");
 constexpr int kDirect = 64;                // items of a call that plans for itself
-constexpr float kTau = 8.0f;
 constexpr uint32_t kOffRing = 2 * kQBytes;
 constexpr uint32_t kOffSmall = kOffRing + kRing * kChunk;
 constexpr uint32_t kSmem = kOffSmall + 2048 + 1024;
@@ -130,6 +130,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+// the largest of three (NaN passed over)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (BF16) {
@@ -179,7 +185,9 @@ __device__ __forceinline__ int item_tiles(const PrefillParams& p, const Request&
   return tiles_of(p, r.n, r.L, q0, min(r.n - q0, kUnitRows));
 }
 
-__device__ __forceinline__ void unit_of(const PrefillParams& p, const Small* sm, int u, Unit& w) {
+// (A Unit stays in registers: nothing takes its address or indexes it by a variable. Local memory is behind L2 here.)
+__device__ __forceinline__ Unit unit_of(const PrefillParams& p, const Small* sm, int u) {
+  Unit w;
   Item it;
   const int at = u / p.H;
   if (p.items != nullptr) {
@@ -199,7 +207,9 @@ __device__ __forceinline__ void unit_of(const PrefillParams& p, const Small* sm,
   }
   w.h = u % p.H;
   w.rows[0] = w.rows[1] = w.tiles[0] = w.tiles[1] = 0;
-  if (it.b < 0) return;
+  w.q0 = w.j0 = w.n = w.L = w.qrow = w.kvrow = 0;
+  w.slot = -1;
+  if (it.b < 0) return w;
   const Request r = request_of(p, it.b);
   w.q0 = it.q0;
   w.j0 = it.j0;
@@ -213,6 +223,7 @@ __device__ __forceinline__ void unit_of(const PrefillParams& p, const Small* sm,
     w.rows[s] = max(0, min(kSub, r.n - it.q0 - s * kSub));
     w.tiles[s] = max(0, min(it.j1, tiles_of(p, r.n, r.L, it.q0 + s * kSub, w.rows[s])) - it.j0);
   }
+  return w;
 }
 // The k-th unit of this CTA: in turns, every second one backwards, so that what is left over evens out.
 __device__ __forceinline__ int unit_index(int k) {
@@ -221,11 +232,10 @@ __device__ __forceinline__ int unit_index(int k) {
 }
 
 // Values that are not finite in the tile at chunks c0, c1 (two of 64 tokens x 128 columns, each as two swizzled
-// [64 x 64] boxes) become 0; true if one of them belonged to a token before `seen`.
+// [64 x 64] boxes) become 0; *dirty = mark first, where one of them belongs to a token before `seen`.
 template <bool BF16>
-__device__ __forceinline__ bool clean_values(uint8_t* c0, uint8_t* c1, int tok0, int seen, int r) {
+__device__ __forceinline__ void clean_values(uint8_t* c0, uint8_t* c1, int tok0, int seen, int r, volatile int32_t* dirty, int mark) {
   constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
-  bool found = false;
 #pragma unroll 4
   for (int it = 0; it < 16; ++it) {
     const int idx = it * kSub + r;  // 16-byte pieces, 1024 a chunk
@@ -241,24 +251,12 @@ __device__ __forceinline__ bool clean_values(uint8_t* c0, uint8_t* c1, int tok0,
         if ((w[j] & kExp) == kExp) w[j] &= 0xffff0000u;
         if ((w[j] & (kExp << 16)) == (kExp << 16)) w[j] &= 0xffffu;
       }
-      sts128(smem_u32(at), make_uint4(w[0], w[1], w[2], w[3]));
       const int tok = tok0 + ((idx >= 1024) ? 64 : 0) + ((idx & 511) >> 3);
-      found |= tok < seen;
-    }
-  }
-  return found;
-}
-
-// What the values that clean_values took out of a unit's tiles from token t0 on add to a row that sees the tokens
-// before `seen`: per 32 columns, NaN or an infinity (weights are positive).
-template <bool BF16>
-__device__ __noinline__ void poison(const PrefillParams& p, const Unit& w, int t0, int seen, int col, float* o) {
-  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
-  for (int t = t0; t < seen; ++t) {
-    const uint16_t* const v = p.v + (static_cast<long long>(w.kvrow + t) * p.H + w.h) * kDim + col;
-    for (int j = 0; j < 32; ++j) {
-      const uint16_t x = v[j];
-      if ((x & kExp) == kExp) o[j] += h2f<BF16>(x);  // inf - inf and NaN give NaN, as in the sum
+      if (tok < seen) {
+        *dirty = mark;
+        __threadfence_block();
+      }
+      sts128(smem_u32(at), make_uint4(w[0], w[1], w[2], w[3]));
     }
   }
 }
@@ -355,7 +353,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
   const uint64_t tmo = p.timeout_ns;
   const int units = (p.items != nullptr ? *p.num_items : sm->items) * p.H;
-  Unit w;
 
   if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- loads
@@ -376,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k * static_cast<int>(gridDim.x) >= units) break;
           continue;
         }
-        unit_of(p, sm, u, w);
+        const Unit w = unit_of(p, sm, u);
         const int nt = max(w.tiles[0], w.tiles[1]);
         auto queries = [&](int s) {
           if (w.tiles[s] == 0 || !ok) return;
@@ -427,9 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t tile0 = 0;                       // tiles before this unit
     uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // units and tiles of each subtile so far
     bool ok = true;
+    int tiles0 = 0, tiles1 = 0;  // of the unit
     auto scores = [&](int s, int i) {  // S of tile i; the first of the subtiles waits for the keys
       const uint32_t x = kTileChunks * (tile0 + i), t = tile0 + i;
-      const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
+      const bool last = s == 1 || i >= tiles1, first = s == 0 || i >= tiles0;
       if (first) ok = ok && mbar_wait_warp(&sm->k_full[t & 1], (t >> 1) & 1, tmo);
       if (!ok) return;
       tc_fence_after();
@@ -444,11 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       issue_commit(leader, &sm->s_full[s]);
       if (last) issue_commit(leader, &sm->empty[(x + 2) % kRing]);
-      if (i + 1 == w.tiles[s]) issue_commit(leader, &sm->q_empty[s]);
+      if (i + 1 == (s == 0 ? tiles0 : tiles1)) issue_commit(leader, &sm->q_empty[s]);
     };
     auto values = [&](int s, int i) {
       const uint32_t x = kTileChunks * (tile0 + i) + 3, t = tile0 + i;
-      const bool last = s == 1 || i >= w.tiles[1], first = s == 0 || i >= w.tiles[0];
+      const bool last = s == 1 || i >= tiles1, first = s == 0 || i >= tiles0;
       if (first) ok = ok && mbar_wait_warp(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -473,12 +471,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k * static_cast<int>(gridDim.x) >= units) break;
         continue;
       }
-      unit_of(p, sm, u, w);
-      const int nt = max(w.tiles[0], w.tiles[1]);
+      const Unit w = unit_of(p, sm, u);
+      tiles0 = w.tiles[0];
+      tiles1 = w.tiles[1];
+      const int nt = max(tiles0, tiles1);
       if (nt == 0) continue;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        if (w.tiles[s] == 0 || !ok) continue;
+        if ((s == 0 ? tiles0 : tiles1) == 0 || !ok) continue;
         ok = mbar_wait_warp(&sm->q_full[s], qn[s] & 1, tmo);
         ++qn[s];
         if (ok) scores(s, 0);
@@ -486,9 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < nt && ok; ++i) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (i >= w.tiles[s] || !ok) continue;
+          if (i >= (s == 0 ? tiles0 : tiles1) || !ok) continue;
           values(s, i);
-          if (ok && i + 1 < w.tiles[s]) scores(s, i + 1);
+          if (ok && i + 1 < (s == 0 ? tiles0 : tiles1)) scores(s, i + 1);
         }
       }
       tile0 += nt;
@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + kTmemS + s * kTile, to = tmem + lanes + kTmemO + s * kDim;
     const float scale = p.scale_log2;
+    constexpr float kSlack = BF16 ? 60.f : 15.f;
     uint32_t done = 0;   // tiles of this subtile so far
     uint32_t tile0 = 0;  // tiles of all units before this one
     bool ok = true;
@@ -515,8 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k * static_cast<int>(gridDim.x) >= units) break;
         continue;
       }
-      unit_of(p, sm, u, w);
-      const int nt = w.tiles[s], rows = w.rows[s], q0 = w.q0 + s * kSub;
+      const Unit w = unit_of(p, sm, u);
+      const int nt = s == 0 ? w.tiles[0] : w.tiles[1], rows = s == 0 ? w.rows[0] : w.rows[1], q0 = w.q0 + s * kSub;
       if (rows > 0) {
         const int seen = visible(p, w.n, w.L, q0 + min(r, rows - 1));  // tokens that this row sees
         const int all = visible(p, w.n, w.L, q0);                      // that every row of the subtile sees
@@ -540,12 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int t = 4; t < kTile; t += 8) {
+          for (int t = 4; t < kTile - 4; t += 8) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], t + 4 + j < kTile ? fmaxf(x[t + j], x[t + 4 + j]) : x[t + j]);
+            for (int j = 0; j < 4; ++j) m4[j] = max3(m4[j], x[t + j], x[t + 4 + j]);
           }
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
-          const bool need = mx > m + kTau;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], x[kTile - 4 + j]);
+          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * f;
+          const bool need = mx > m + kSlack;
           if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
             const float m_new = need ? mx : m;
             const float alpha = need ? (m == -INFINITY ? 0.f : exp2f(m - m_new)) : 1.f;
@@ -572,8 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t t = tile0 + i, c = kTileChunks * t + 3;
             ok = mbar_wait_warp(&sm->v_full[t & 1], (t >> 1) & 1, tmo);
             if (!ok) break;
-            if (clean_values<BF16>(smem + kOffRing + (c % kRing) * kChunk, smem + kOffRing + ((c + 1) % kRing) * kChunk, tok0, w.L, r))
-              *const_cast<volatile int32_t*>(&sm->dirty[k & 7]) = k + 1;
+            clean_values<BF16>(smem + kOffRing + (c % kRing) * kChunk, smem + kOffRing + ((c + 1) % kRing) * kChunk, tok0, w.L, r,
+                               &sm->dirty[k & 7], k + 1);
             fence_proxy_async_smem();  // (the product waits for all four warps' weights, so for all of the search)
           }
           const float mm = m == -INFINITY ? 0.f : -m;
@@ -624,7 +627,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = any ? o[j] * inv : (l != l ? l : 0.f);
-          if (__builtin_expect(dirty, 0)) poison<BF16>(p, w, first, last, 32 * q, o);
+          if (__builtin_expect(dirty, 0)) {
+            // values that are not finite were taken out of the searched tiles: those that this row sees belong to its sum
+            // (weights are positive; infinities of both signs, or a NaN, give NaN)
+            constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+#pragma unroll 1
+            for (int t = first; t < last; ++t) {
+              const uint16_t* const v = p.v + (static_cast<long long>(w.kvrow + t) * p.H + w.h) * kDim + 32 * q;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if ((v[j] & kExp) == kExp) o[j] += h2f<BF16>(v[j]);
+            }
+          }
           if (r < rows) {
             if (w.slot < 0) {
               uint32_t b[16];
