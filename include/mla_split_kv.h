@@ -728,7 +728,9 @@ typedef struct {
  *    pages that they no longer reach back to the stack of free pages,
  *    free_pages[0 .. *free_count), request after request, each from its lowest
  *    page up. A page must not be held elsewhere. Their rows of block_table stay
- *    as they were.
+ *    as they were. (A request whose first pages are another's, as in
+ *    mla_decode_shared, starts with its length set to theirs; it ends by
+ *    shrinking to that, and then its length is set to 0.)
  *  - Then growing requests take the pages that they lack from the stack's top,
  *    request after request, each into the next columns of its row, up to the
  *    first that does not fit: fewer free pages than it lacks, a row too short
@@ -913,12 +915,13 @@ typedef struct {
  * of the whole batch in groups of 128, each request's own ones for its own
  * rows, each cut into pieces so that the device is evenly busy. A piece is two
  * units, one for each half of the value columns; CTA c does
- * units[cta_indptr[c] .. cta_indptr[c + 1]). The plan serves contexts of any length (a request's last piece takes
- * what it has grown by) of the same B, q_len, H, page size and P, in the time
- * planned for these. own_indptr: of each request's group of 128 rows, its
- * first slot (the slots before are the common tokens': of the group g of the
- * batch's rows, shared_parts slots from g * shared_parts on). Host code; touches no GPU.
- * MLA_ERR_CAPACITY (with num_units set) where units does not hold them.
+ * units[cta_indptr[c] .. cta_indptr[c + 1]). The plan serves contexts of any
+ * length (a request's last piece takes what it has grown by) of the same B,
+ * q_len, H, page size and P, in the time planned for these. own_indptr: of each
+ * request's group of 128 rows, its first slot (the slots before are the common
+ * tokens': of the group g of the batch's rows, shared_parts slots from
+ * g * shared_parts on). Host code; touches no GPU. MLA_ERR_CAPACITY (with
+ * num_units set) where units does not hold them.
  */
 mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_t B, int32_t num_heads, int32_t q_len,
                              int32_t block_size, const mla_device_info_t* dev, mla_shared_plan_t* plan);
@@ -964,8 +967,8 @@ typedef struct {
  * Precision: scores, maxima, sums and out_lse are fp32; the weights of the value
  * product are rounded once to `dtype` (half a step: 2^-12 of themselves in fp16,
  * or 2^-25 of the row's greatest where that is more, 2^-9 of themselves in bf16)
- * and the sum that normalizes takes them unrounded. The partials
- * are fp32; `out` is rounded once to out_dtype.
+ * and the sum that normalizes takes them unrounded. The partials are fp32; `out`
+ * is rounded once to out_dtype.
  *
  * q_absorbed, q_pe, caches: as for mla_decode_partial, 16-bit caches only
  * shared_table: device [P / block_size] int32 (a row of block_table, for
