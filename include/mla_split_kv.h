@@ -720,7 +720,8 @@ typedef struct {
 /*
  * mla_update_tables -- a step's block tables, slot map and offsets, on the
  * device, from the requests' lengths and what each gets or gives back. One
- * launch; may be captured and replayed.
+ * launch, two where `slots` has more than 8192 places; may be captured and
+ * replayed.
  *
  * Request b has L_b = context_lens[b] tokens and changes by n_b = changes[b]
  * (at least -L_b: what is below counts as that).
@@ -751,7 +752,7 @@ typedef struct {
  * context_lens_out may be context_lens, and free_count_out free_count; no two
  * other buffers may overlap. free_pages holds num_blocks entries. changes,
  * context_lens: device [B]; block_table: device [B, max_blocks_per_req].
- * A programmatic dependent launch, as mla_cache_append. No counterpart on the
+ * Programmatic dependent launches, as mla_cache_append. No counterpart on the
  * pages.
  */
 mla_status_t mla_update_tables(const int32_t* changes, const int32_t* context_lens, int32_t* context_lens_out,

@@ -11,10 +11,13 @@
 // page's first token is a new token, which writes the page's table entry). A page that another request has just
 // given back is looked up where that request's row still has it (the place on the stack tells which), so no thread
 // waits for another's write. What bounds it is latency: launch, one round of loads, the scans (two barriers each),
-// one search in shared memory, one or two dependent loads. A step of 256 single tokens: see the launch rule.
+// one search in shared memory, one or two dependent loads. A step of 256 single tokens takes 5.5 us a call in a
+// replayed graph.
 //
-// A cluster of one CTA for small steps, of eight (each with scans of its own, cheaper than passing them on) where
-// the slots are many; the cluster's barrier keeps outputs that alias inputs from being written before all have read.
+// One CTA does all of a small step (as many slots as it has threads, eight times over). Where there are more places in
+// `slots`, it leaves them to a second kernel over the whole device, which reads offsets, lengths and tables back:
+// 512 requests, 30% of which give pages back, and 100,147 new tokens in all: 13.7 us a call; 23.1 us with a cluster of
+// eight CTAs that scanned the requests each and wrote the slots, too.
 //
 // mla_cache_append_slots: a copy of 1152 bytes a token, HBM-bound: a warp takes one token of a small step, four of a
 // large one, whose loads are all in flight together.
@@ -29,6 +32,7 @@ constexpr int kFewSlots = 8192;  // up to so many places in `slots`: one CTA
 constexpr int64_t kFewTokens = 8192;  // up to so many tokens: a warp each
 constexpr int kThreads = 1024;
 static_assert(kThreads == 32 * kScanWarps, "block_scan's");
+constexpr int kEach = 4;  // pages that a thread looks up before it stores any
 
 struct Request {
   long long len;   // tokens before the step
@@ -53,6 +57,15 @@ __device__ __forceinline__ Request request_of(const TablesParams& p, int b) {
   return r;
 }
 
+// The cache row of token t in its page; -1 for a page outside the pool.
+__device__ __forceinline__ long long slot_of(const TablesParams& p, int32_t page, int t, bool* bad) {
+  const bool ok = page >= 0 && page < p.num_blocks;
+  *bad |= !ok;
+  return ok ? (static_cast<long long>(page) << p.bs_shift) + (t & (p.bs - 1)) : -1ll;
+}
+
+// kSlots: the slots, too; else the next kernel writes them.
+template <bool kSlots>
 __global__ void __launch_bounds__(kThreads, 1) mla_update_tables_kernel(const TablesParams p) {
   extern __shared__ int32_t sh[];
   __shared__ long long part[kScanWarps];
@@ -133,81 +146,123 @@ __global__ void __launch_bounds__(kThreads, 1) mla_update_tables_kernel(const Ta
   long long all_lens;
   lens = block_scan(lens, part, &all_lens);  // (its barriers also publish what was written above)
 
-  // every CTA has read its inputs before outputs that may be the same memory are written
-  const int ctas = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+  // the inputs are read before outputs that may be the same memory are written
   int32_t keep_len[8];
-  const bool writes = rank == 0;
-  if (writes) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (b0 + j < b1) {
-        const Request r = request_of(p, b0 + j);
-        keep_len[j] = static_cast<int32_t>(r.grow > 0 && b0 + j >= served ? r.len : r.next);
-      }
+  for (int j = 0; j < 8; ++j) {
+    if (b0 + j < b1) {
+      const Request r = request_of(p, b0 + j);
+      keep_len[j] = static_cast<int32_t>(r.grow > 0 && b0 + j >= served ? r.len : r.next);
     }
   }
-  if (ctas > 1) cluster_sync();
-  else __syncthreads();
-  if (writes) {
-    long long s = lens;
-    bool over = false;
+  __syncthreads();
+  long long s = lens;
+  bool over = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (b0 + j < b1) {
-        const int b = b0 + j;
-        over |= s > 0x7fffffffll;
-        p.lens_out[b] = keep_len[j];
-        p.q_indptr[b] = q_at[b];
-        p.kv_indptr[b] = static_cast<int32_t>(min(s, 0x7fffffffll));
-        s += keep_len[j];
-      }
+  for (int j = 0; j < 8; ++j) {
+    if (b0 + j < b1) {
+      const int b = b0 + j;
+      over |= s > 0x7fffffffll;
+      p.lens_out[b] = keep_len[j];
+      p.q_indptr[b] = q_at[b];
+      p.kv_indptr[b] = static_cast<int32_t>(min(s, 0x7fffffffll));
+      s += keep_len[j];
     }
-    if (tid == 0) {
-      over |= all_lens > 0x7fffffffll;
-      p.q_indptr[B] = tokens;
-      p.kv_indptr[B] = static_cast<int32_t>(min(all_lens, 0x7fffffffll));
-      *p.free_count_out = static_cast<int32_t>(top - taken);
-      *p.served = served;
-    }
-    if (over) flag_error(MLA_DEVERR_BAD_PAGE);
   }
-
+  if (tid == 0) {
+    over |= all_lens > 0x7fffffffll;
+    p.q_indptr[B] = tokens;
+    p.kv_indptr[B] = static_cast<int32_t>(min(all_lens, 0x7fffffffll));
+    *p.free_count_out = static_cast<int32_t>(top - taken);
+    *p.served = served;
+  }
+  if (over) flag_error(MLA_DEVERR_BAD_PAGE);
   const int shift = p.bs_shift;
-  const int step = ctas * kThreads;
-  const int first = rank * kThreads + tid;
-  bool bad = false;
   // pages given back: the k-th of the step goes to stack[count + k]
-  for (long long k = first; count + k < top; k += step) {
-    const int b = find_last(back_at, 0, B - 1, static_cast<int32_t>(k));
-    const int col = ((base_of[b] + p.bs - 1) >> shift) + static_cast<int>(k - back_at[b]);
-    p.pages[count + k] = p.block_table[static_cast<long long>(b) * p.max_blocks + col];
+  auto given_back = [&](int k) {
+    const int b = find_last(back_at, 0, B - 1, k);
+    const int col = ((base_of[b] + p.bs - 1) >> shift) + (k - back_at[b]);
+    return p.block_table[static_cast<long long>(b) * p.max_blocks + col];
+  };
+  for (int k0 = tid; count + k0 < top; k0 += kEach * kThreads) {
+    int32_t page[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (count + k0 + j * kThreads < top) page[j] = given_back(k0 + j * kThreads);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (count + k0 + j * kThreads < top) p.pages[count + k0 + j * kThreads] = page[j];
   }
-  // new tokens
-  for (int i = first; i < tokens; i += step) {
-    const int b = find_last(q_at, 0, B - 1, i);
-    const int t = base_of[b] + (i - q_at[b]);
-    const int col = t >> shift, held = static_cast<int>((static_cast<long long>(base_of[b]) + p.bs - 1) >> shift);
-    int32_t* const entry = p.block_table + static_cast<long long>(b) * p.max_blocks + col;
-    int32_t page;
-    if (col < held) {
-      page = *entry;
-    } else {
-      const int at = static_cast<int>(top) - 1 - take_at[b] - (col - held);
-      if (at < count) {
-        page = p.pages[at];
-      } else {  // given back in this step
-        const int k = at - static_cast<int>(count);
-        const int from = find_last(back_at, 0, B - 1, k);
-        const int c = ((base_of[from] + p.bs - 1) >> shift) + (k - back_at[from]);
-        page = p.block_table[static_cast<long long>(from) * p.max_blocks + c];
+  // the j-th page that request b takes
+  auto page_taken = [&](int b, int j) {
+    const int at = static_cast<int>(top) - 1 - take_at[b] - j;
+    return at < count ? p.pages[at] : given_back(at - static_cast<int>(count));
+  };
+  if constexpr (!kSlots) {
+    for (int i0 = tid; i0 < taken; i0 += kEach * kThreads) {
+      int32_t page[kEach];
+      int32_t* entry[kEach];
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const int i = i0 + k * kThreads;
+        if (i >= taken) continue;
+        // (as many requests as were served: those behind have no places in take_at)
+        const int b = find_last(take_at, 0, min(served, B - 1), i), j = i - take_at[b];
+        entry[k] = p.block_table + static_cast<long long>(b) * p.max_blocks + ((base_of[b] + p.bs - 1) >> shift) + j;
+        page[k] = page_taken(b, j);
       }
-      if ((t & (p.bs - 1)) == 0) *entry = page;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (i0 + k * kThreads < taken) *entry[k] = page[k];
     }
-    const bool ok = page >= 0 && page < p.num_blocks;
-    bad |= !ok;
-    p.slots[i] = ok ? (static_cast<long long>(page) << shift) + (t & (p.bs - 1)) : -1ll;
+  } else {
+    bool bad = false;
+    for (int i = tid; i < tokens; i += kThreads) {
+      const int b = find_last(q_at, 0, B - 1, i);
+      const int t = base_of[b] + (i - q_at[b]);
+      const int col = t >> shift, held = static_cast<int>((static_cast<long long>(base_of[b]) + p.bs - 1) >> shift);
+      int32_t* const entry = p.block_table + static_cast<long long>(b) * p.max_blocks + col;
+      int32_t page;
+      if (col < held) {
+        page = *entry;
+      } else {
+        page = page_taken(b, col - held);
+        if ((t & (p.bs - 1)) == 0) *entry = page;
+      }
+      p.slots[i] = slot_of(p, page, t, &bad);
+    }
+    for (long long i = static_cast<long long>(tokens) + tid; i < p.capacity; i += kThreads) p.slots[i] = -1;
+    if (bad) flag_error(MLA_DEVERR_BAD_PAGE);
   }
-  for (long long i = static_cast<long long>(tokens) + first; i < p.capacity; i += step) p.slots[i] = -1;
+}
+
+// The slots of a step with many places, from the tables that the kernel above has written.
+constexpr int kSlotThreads = 256, kSlotsEach = 4;
+
+__global__ void __launch_bounds__(kSlotThreads) mla_step_slots_kernel(const TablesParams p) {
+  extern __shared__ int32_t q_at[];  // [B + 1]
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int b = threadIdx.x; b <= p.B; b += kSlotThreads) q_at[b] = p.q_indptr[b];
+  __syncthreads();
+  const int tokens = q_at[p.B];
+  bool bad = false;
+  const long long step = static_cast<long long>(gridDim.x) * kSlotThreads * kSlotsEach;
+  for (long long i0 = static_cast<long long>(blockIdx.x) * kSlotThreads * kSlotsEach + threadIdx.x; i0 < p.capacity; i0 += step) {
+    long long slot[kSlotsEach];
+#pragma unroll
+    for (int k = 0; k < kSlotsEach; ++k) {
+      const long long i = i0 + k * kSlotThreads;
+      slot[k] = -1;
+      if (i >= tokens) continue;
+      const int b = find_last(q_at, 0, p.B - 1, static_cast<int32_t>(i));
+      const int t = p.lens_out[b] - (q_at[b + 1] - static_cast<int>(i));  // (its new tokens are its last)
+      slot[k] = slot_of(p, p.block_table[static_cast<long long>(b) * p.max_blocks + (t >> p.bs_shift)], t, &bad);
+    }
+#pragma unroll
+    for (int k = 0; k < kSlotsEach; ++k)
+      if (i0 + k * kSlotThreads < p.capacity) p.slots[i0 + k * kSlotThreads] = slot[k];
+  }
   if (bad) flag_error(MLA_DEVERR_BAD_PAGE);
 }
 
@@ -248,44 +303,46 @@ __global__ void __launch_bounds__(kCopyWarps * 32) mla_cache_append_slots_kernel
 }
 
 template <class Params>
-cudaError_t launch_dependent(void (*kernel)(const Params), unsigned grid, unsigned block, unsigned cluster, size_t smem,
-                             const Params& p, cudaStream_t stream) {
+cudaError_t launch_dependent(void (*kernel)(const Params), unsigned grid, unsigned block, size_t smem, const Params& p,
+                             cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(block, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
 
 cudaError_t launch_update_tables(const TablesParams& p, cudaStream_t stream) {
-  static DeviceOnce once;
+  static DeviceOnce once, once_slots;
+  const bool few = p.capacity <= kFewSlots;
+  const auto kernel = few ? &mla_update_tables_kernel<true> : &mla_update_tables_kernel<false>;
   const size_t smem = (static_cast<size_t>(p.B) * 4 + 2) * sizeof(int32_t);
-  const cudaError_t e = set_attribute_once(once, reinterpret_cast<const void*>(&mla_update_tables_kernel),
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (kMaxStepRequests * 4 + 2) * static_cast<int>(sizeof(int32_t)));
+  cudaError_t e = set_attribute_once(few ? once_slots : once, reinterpret_cast<const void*>(kernel),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (kMaxStepRequests * 4 + 2) * static_cast<int>(sizeof(int32_t)));
   if (e != cudaSuccess) return e;
-  const unsigned ctas = p.capacity > kFewSlots ? 8 : 1;
-  return launch_dependent(mla_update_tables_kernel, ctas, kThreads, ctas, smem, p, stream);
+  e = launch_dependent(kernel, 1, kThreads, smem, p, stream);
+  if (e != cudaSuccess || few) return e;
+  constexpr int kMostCtas = 1024;
+  const long long ctas = (static_cast<long long>(p.capacity) + kSlotThreads * kSlotsEach - 1) / (kSlotThreads * kSlotsEach);
+  return launch_dependent(mla_step_slots_kernel, static_cast<unsigned>(ctas < kMostCtas ? ctas : kMostCtas), kSlotThreads,
+                          (static_cast<size_t>(p.B) + 1) * sizeof(int32_t), p, stream);
 }
 
 cudaError_t launch_append_slots(const AppendSlotsParams& p, cudaStream_t stream) {
   const long long warps_per_token = p.tokens > kFewTokens ? 4 : 1;
   const long long units = (p.tokens + warps_per_token - 1) / warps_per_token;
   const unsigned grid = static_cast<unsigned>((units + kCopyWarps - 1) / kCopyWarps);
-  return p.tokens > kFewTokens ? launch_dependent(mla_cache_append_slots_kernel<4>, grid, kCopyWarps * 32, 1, 0, p, stream)
-                               : launch_dependent(mla_cache_append_slots_kernel<1>, grid, kCopyWarps * 32, 1, 0, p, stream);
+  return p.tokens > kFewTokens ? launch_dependent(mla_cache_append_slots_kernel<4>, grid, kCopyWarps * 32, 0, p, stream)
+                               : launch_dependent(mla_cache_append_slots_kernel<1>, grid, kCopyWarps * 32, 0, p, stream);
 }
 
 cudaError_t step_tables_read_clear_error(uint32_t* out) {

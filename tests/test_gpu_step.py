@@ -128,6 +128,21 @@ def test_requests_behind_one_that_does_not_fit_stay(why):
     assert want["served"] == [{"pages": 4, "width": 4, "slots": 4}[why]] and want["q_indptr"][4:] == [90, 90, 90]
 
 
+@pytest.mark.parametrize("why", ["pages", "width"])
+def test_many_places_and_requests_that_do_not_fit(why):
+    """More places than one CTA fills: the slots come from a kernel of their own, which must not see what did not fit."""
+    rng = np.random.default_rng(6)
+    lens, bs, capacity = [30, 0, 6400, 17, 1000, 3, 5000, 0], 16, 30000
+    nblk, width = {"pages": (1200, 3000), "width": (6000, 700)}[why]
+    host = HostStep(lens, bs, nblk, width, rng)
+    dev = DeviceStep(host, nblk, capacity, True)
+    for changes in ([9000, 1, -6000, 4000, 0, 900, -1, 0], [1, 0, 1, 1, 1, 1, 1, 5000], [-9030, 3, 3000, 16, -1000, 1, 2, 15000]):
+        want = host.step(changes, capacity)
+        dev.step(changes)
+        torch.cuda.synchronize()
+        dev.check(host, want)
+
+
 def test_pages_given_back_are_taken_in_the_same_step():
     rng = np.random.default_rng(6)
     host = HostStep([160, 0, 160, 5], 16, 21, 30, rng)
