@@ -529,56 +529,62 @@ __global__ void __maxnreg__(168)
   if (warp == kScoreWarp) tmem_dealloc(tmem, 512);
 }
 
-// A warp a row: its parts in order (the common tokens' pieces, then its own tokens'), M = max lse, weights 2^(lse - M).
-// Latency: the offsets (the plan's) are read before the decode kernel ends, the first parts' values beside their LSE.
+// kSplit warps a row, each a share of its columns: the parts in order (the common tokens' pieces, then its own tokens'),
+// M = max lse, weights 2^(lse - M). Latency: the offsets (the plan's) are read before the decode kernel ends, the first
+// parts' values beside their LSE, and 4 KB a warp are in flight. Four warps a row up to 2048 rows, one with more (64 rows
+// of 17 parts: 13.9 us a call with four, 16.5 with one; 1024 rows: 105.9, 109.2; 6144: 148.5, 145.2).
 constexpr int kMergeThreads = 128;
-constexpr int kMergeDepth = 2;  // parts in flight
+constexpr int kMergeFewRows = 2048;
+template <int kSplit>
 __global__ void __launch_bounds__(kMergeThreads, 6) mla_decode_shared_merge_kernel(const SharedParams p) {
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  constexpr int kCols = 4 / kSplit;       // times 4 columns a lane
+  constexpr int kMergeDepth = 2 * kSplit;  // parts in flight
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * (4 / kSplit) + warp / kSplit, col = kRank / kSplit * (warp % kSplit) + 4 * lane;
   const int per = p.q_len * p.H, b = row / per, r = row % per;
   const int own = b * ((per + kRows - 1) / kRows) + r / kRows;
   const bool in = row < p.rows;
-  const int s0 = in ? p.own_indptr[own] : 0, n_own = in ? p.own_indptr[own + 1] - s0 : 0;
+  const int s0 = in ? p.own_indptr[own] : 0, n = in ? p.shared_parts + p.own_indptr[own + 1] - s0 : 0;
   pdl_wait();
   pdl_launch_dependents();
   if (!in) return;
-  const int n = p.shared_parts + n_own;
   // the row of part j in the slots
   auto at = [&](int j) -> long long {
     return j < p.shared_parts ? (static_cast<long long>(row / kRows) * p.shared_parts + j) * kRows + row % kRows
                               : static_cast<long long>(s0 + j - p.shared_parts) * kRows + r % kRows;
   };
-  float M = -INFINITY;
-  for (int j = lane; j < n; j += 32) M = max_nan(M, p.part_lse[at(j)]);
-  float4 acc[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f;
-  float l[kMergeDepth];
-  float4 v[kMergeDepth][4];
+  // a group of parts' values and, in as many lanes, their LSE
+  float lse;
+  float4 v[kMergeDepth][kCols];
   auto load = [&](int j0) {
+    lse = lane < kMergeDepth && j0 + lane < n ? p.part_lse[at(j0 + lane)] : -INFINITY;
 #pragma unroll
     for (int j = 0; j < kMergeDepth; ++j) {
-      const long long a = at(min(j0 + j, n - 1));
-      l[j] = j0 + j < n ? p.part_lse[a] : -INFINITY;
+      const float* const from = p.part_o + at(min(j0 + j, n - 1)) * kRank + col;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[j][c] = reinterpret_cast<const float4*>(p.part_o + a * kRank)[lane + 32 * c];
+      for (int c = 0; c < kCols; ++c) v[j][c] = *reinterpret_cast<const float4*>(from + 128 * c);
     }
   };
   load(0);
+  float M = lse;
+  for (int j = kMergeDepth + lane; j < n; j += 32) M = max_nan(M, p.part_lse[at(j)]);
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float4 acc[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
   if (M != -INFINITY) {
     for (int j0 = 0; j0 < n; j0 += kMergeDepth) {
       if (j0 > 0) load(j0);
+      const float w = lse == -INFINITY ? -1.f : exp2f(lse - M);
 #pragma unroll
       for (int j = 0; j < kMergeDepth; ++j) {
-        if (l[j] == -INFINITY) continue;  // (nothing was written there)
-        const float wj = exp2f(l[j] - M);
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        if (wj == -1.f) continue;  // (nothing was written there)
         den += wj;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kCols; ++c) {
           acc[c].x = fmaf(wj, v[j][c].x, acc[c].x);
           acc[c].y = fmaf(wj, v[j][c].y, acc[c].y);
           acc[c].z = fmaf(wj, v[j][c].z, acc[c].z);
@@ -587,11 +593,11 @@ __global__ void __launch_bounds__(kMergeThreads, 6) mla_decode_shared_merge_kern
       }
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = make_float4(acc[c].x / den, acc[c].y / den, acc[c].z / den, acc[c].w / den);
+    for (int c = 0; c < kCols; ++c) acc[c] = make_float4(acc[c].x / den, acc[c].y / den, acc[c].z / den, acc[c].w / den);
   }
 #pragma unroll
-  for (int c = 0; c < 4; ++c) store_out4(p.out, p.out_dtype, static_cast<long long>(row) * kRank + 4 * (lane + 32 * c), acc[c]);
-  if (lane == 0 && p.out_lse != nullptr) p.out_lse[row] = merged_lse(M, den);
+  for (int c = 0; c < kCols; ++c) store_out4(p.out, p.out_dtype, static_cast<long long>(row) * kRank + col + 128 * c, acc[c]);
+  if (lane == 0 && warp % kSplit == 0 && p.out_lse != nullptr) p.out_lse[row] = merged_lse(M, den);
 }
 
 cudaError_t launch_dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, unsigned grid, unsigned block, size_t smem,
@@ -623,8 +629,12 @@ cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& 
   e = bf16 ? cudaLaunchKernelEx(&cfg, mla_decode_shared_kernel<true>, tm_half, tm_piece, tm_kpe, p)
            : cudaLaunchKernelEx(&cfg, mla_decode_shared_kernel<false>, tm_half, tm_piece, tm_kpe, p);
   if (e != cudaSuccess) return e;
-  launch_dependent(cfg, attr, (p.rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32), kMergeThreads, 0, stream);
-  return cudaLaunchKernelEx(&cfg, mla_decode_shared_merge_kernel, p);
+  if (p.rows <= kMergeFewRows) {
+    launch_dependent(cfg, attr, p.rows, kMergeThreads, 0, stream);
+    return cudaLaunchKernelEx(&cfg, mla_decode_shared_merge_kernel<4>, p);
+  }
+  launch_dependent(cfg, attr, (p.rows + 3) / 4, kMergeThreads, 0, stream);
+  return cudaLaunchKernelEx(&cfg, mla_decode_shared_merge_kernel<1>, p);
 }
 
 cudaError_t decode_shared_read_clear_error(uint32_t* out) {

@@ -793,7 +793,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mla_prefill_plan_kernel(const
 
 // Cut runs: a warp a (row, head), the pieces in order, M = max lse, weights 2^(lse - M).
 constexpr int kMergeThreads = 256;
-__global__ void __launch_bounds__(kMergeThreads) mla_prefill_merge_kernel(const PrefillParams p, const PrefillPlanParams pl, int bf16) {
+constexpr int kMergeDepth = 8;  // pieces in flight
+__global__ void __launch_bounds__(kMergeThreads, 3) mla_prefill_merge_kernel(const PrefillParams p, const PrefillPlanParams pl, int bf16) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -804,25 +805,29 @@ __global__ void __launch_bounds__(kMergeThreads) mla_prefill_merge_kernel(const 
     const int4 e = __ldg(pl.merge + i / p.H / kUnitRows);
     if (r >= e.y) continue;
     const long long first = (static_cast<long long>(e.z) * kUnitRows + r) * p.H + h, stride = static_cast<long long>(kUnitRows) * p.H;
-    float M = -INFINITY;
-    for (int j = lane; j < e.w; j += 32) M = max_nan(M, p.part_lse[first + j * stride]);
+    // a group of pieces' values and, in as many lanes, their LSE; the first on its way while the maximum is found
+    float lse;
+    float4 v[kMergeDepth];
+    auto load = [&](int j0) {
+      lse = lane < kMergeDepth && j0 + lane < e.w ? p.part_lse[first + (j0 + lane) * stride] : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kMergeDepth; ++j)
+        v[j] = j0 + j < e.w ? reinterpret_cast<const float4*>(p.part_o + (first + (j0 + j) * stride) * kDim)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    float M = lse;
+    for (int j = kMergeDepth + lane; j < e.w; j += 32) M = max_nan(M, p.part_lse[first + j * stride]);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, d));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f;
     if (M != -INFINITY) {
-      for (int j0 = 0; j0 < e.w; j0 += 4) {
-        float l[4];
-        float4 v[4];
+      for (int j0 = 0; j0 < e.w; j0 += kMergeDepth) {
+        if (j0 > 0) load(j0);
+        const float w = lse == -INFINITY ? 0.f : exp2f(lse - M);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool in = j0 + j < e.w;
-          l[j] = in ? p.part_lse[first + (j0 + j) * stride] : -INFINITY;
-          v[j] = in ? reinterpret_cast<const float4*>(p.part_o + (first + (j0 + j) * stride) * kDim)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float wj = l[j] == -INFINITY ? 0.f : exp2f(l[j] - M);
+        for (int j = 0; j < kMergeDepth; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, w, j);
           den += wj;
           acc.x = fmaf(wj, v[j].x, acc.x);
           acc.y = fmaf(wj, v[j].y, acc.y);
