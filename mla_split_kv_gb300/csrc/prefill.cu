@@ -680,12 +680,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kPlanThreads = 1024;
 constexpr int kSteps = 256;
 constexpr int kLeastPiece = 12;  // half tiles (of 128 rows): a piece's start and its share of the merge cost about two
+constexpr int kFewRuns = 2048;
+
+// Tiles a piece of a run of so many tiles: even ones, of no more than the target's cost as far as tiles are whole.
+__device__ __forceinline__ int piece_length(int cost, int tiles, int target) {
+  const int pieces = (cost + target - 1) / target;
+  return max(1, (tiles + pieces - 1) / pieces);
+}
 
 __global__ void __launch_bounds__(kPlanThreads, 1) mla_prefill_plan_kernel(const PrefillParams p, const PrefillPlanParams pl) {
   extern __shared__ int32_t tile_at[];  // [B + 1]
   __shared__ long long part[32];
   __shared__ unsigned long long sum_cost;
-  __shared__ int longest, slots, merges, hist[kSteps], cursor[kSteps];
+  __shared__ int longest, slots, merges, hist[kSteps], cursor[kSteps], aims[32];
+  __shared__ int2 runs[kFewRuns];  // cost, tiles
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_launch_dependents();
@@ -724,17 +732,69 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mla_prefill_plan_kernel(const
   int most = 0;
   for (int i = tid; i < n; i += kPlanThreads) {
     const int c = cost_of(i, &b, &q0, &tiles);
+    if (n <= kFewRuns) runs[i] = make_int2(c, tiles);
     cost += c;
     most = max(most, c);
   }
   atomicAdd(&sum_cost, cost);
   atomicMax(&longest, most);
   __syncthreads();
-  // four units a CTA, if that takes cutting
-  const long long fair = static_cast<long long>((sum_cost * p.H + 4 * pl.sms - 1) / (4 * pl.sms));
-  const int target = static_cast<int>(max(static_cast<long long>(kLeastPiece), min(fair, 0x3fffffffll)));
+  // How runs are cut: each into as many pieces as its cost holds targets. With few enough runs a warp a candidate: the
+  // longest into 1 to 16 pieces, or all into as many as fill 1 to 16 rounds of the GPU's CTAs. Units in turns take at most
+  // their rounds times the longest, or the average and the longest; merging a piece costs about a twelfth of a half tile.
+  // (1000 and 670 rows behind 29,192 and 31,316 tokens, 16 heads: 112 units as long as 492 half tiles into 448, three rounds
+  // of 152, 396 us; into pieces of a quarter of a CTA's share, 672 of them, 442 us.)
+  if (n <= kFewRuns) {
+    const int k = tid >> 5, lane = tid & 31;
+    const long long r = static_cast<long long>(k - 15) * pl.sms / max(1ll, static_cast<long long>(n) * p.H);
+    const int wanted = static_cast<int>(k < 16 ? k + 1 : max(1ll, min(r, 1ll << 20)));
+    const int aim = max(1, (longest + wanted - 1) / wanted);
+    int units = 0, parts = 0, most_of = 0;
+    long long sum = 0;
+    for (int i = lane; i < n; i += 32) {
+      const int2 run = runs[i];
+      const int len = piece_length(run.x, run.y, aim), count = max(1, (run.y + len - 1) / len);
+      units += count;
+      parts += count > 1 ? count : 0;
+      sum += run.x + 2 * (count - 1);
+      most_of = max(most_of, (run.x - 2) / max(1, run.y) * min(len, run.y) + 2);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    units = __reduce_add_sync(0xffffffffu, units);
+    parts = __reduce_add_sync(0xffffffffu, parts);
+    most_of = __reduce_max_sync(0xffffffffu, most_of);
+    const long long rounds = (static_cast<long long>(units) * p.H + pl.sms - 1) / pl.sms;
+    const long long time = min(rounds * most_of, sum * p.H / pl.sms + most_of) + static_cast<long long>(parts) * p.H / 12;
+    const bool fits = k == 0 || (aim >= kLeastPiece && parts <= pl.max_slots);
+    if (lane == 0) {
+      part[k] = fits ? time : 0x7fffffffffffffffll;
+      aims[k] = aim;
+    }
+    __syncthreads();
+  }
+  int target;
+  bool slack = false;
+  if (n <= kFewRuns) {
+    long long time = part[tid & 31];
+    int best = tid & 31;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+      const long long time_of = __shfl_xor_sync(0xffffffffu, time, d);
+      const int other = __shfl_xor_sync(0xffffffffu, best, d);
+      if (time_of < time || (time_of == time && other < best)) {
+        time = time_of;
+        best = other;
+      }
+    }
+    target = aims[best];
+  } else {  // four units a CTA, if that takes cutting
+    const long long fair = static_cast<long long>((sum_cost * p.H + 4 * pl.sms - 1) / (4 * pl.sms));
+    target = static_cast<int>(max(static_cast<long long>(kLeastPiece), min(fair, 0x3fffffffll)));
+    slack = true;
+  }
   auto pieces_of = [&](int c, int tiles) {  // tiles a piece
-    return 2ll * c > 3ll * target ? max(1, (tiles + (c + target - 1) / target - 1) / ((c + target - 1) / target)) : max(1, tiles);
+    return slack && 2ll * c <= 3ll * target ? max(1, tiles) : piece_length(c, tiles, target);
   };
   const int top = longest;
   auto step_of = [&](int c, int tiles, int len) {
@@ -861,8 +921,9 @@ cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned bl
 
 }  // namespace
 
-// The pieces of all cut runs together, at most: a run is cut where it costs more than 3/2 of the target, into no more
-// than cost / target + 1 <= 5/3 cost / target pieces, and the costs of all runs, H times, are at most 4 sms targets.
+// The pieces of all cut runs together, at most. With many runs: a run is cut where it costs more than 3/2 of the target,
+// into no more than cost / target + 1 <= 5/3 cost / target pieces, and the costs of all runs, H times, are at most 4 sms
+// targets. With few, ways of cutting that would take more are not taken.
 int prefill_max_slots(int H, int sms) { return (4 * sms * 5 / 3) / H + 2; }
 int prefill_max_tiles(int B, int T) { return T / kUnitRows + B; }
 bool prefill_direct(int B, int T, int S) {

@@ -128,6 +128,18 @@ def test_planned_and_cut_calls(new, ctx, H, dtype, causal):
     case.check(out, lse, heads=[0, H - 1], rows=rows, requests=range(min(4, len(new))))
 
 
+@pytest.mark.parametrize("new,ctx,H,dtype", [
+    ([1024], [5000], 24, "bf16"), ([1], [30000], 1, "f16"), ([600, 520, 1], [3000, 2500, 9000], 40, "f16"), ([512] * 6, [512, 900, 4000, 513, 2048, 6000], 16, "bf16"),
+    ([1] * 2100 + [300], [20] * 2100 + [9000], 2, "f16"), ([1] * 2050 + [130], [3] * 2050 + [40000], 1, "bf16")])
+def test_ways_of_cutting(new, ctx, H, dtype):
+    """Equal runs, one run alone, unequal ones, and a long one behind more than the planner weighs ways for."""
+    case = Case(len(new) + H, new, ctx, H, dtype, joint=True)
+    out, lse = case.run()
+    torch.cuda.synchronize()
+    B = len(new)
+    case.check(out, lse, heads=sorted({0, H // 2, H - 1}), rows=[0, 127, 128, 255, 256, 511, 519, 599, 1023], requests=sorted({0, 1, 7, B // 2, B - 2, B - 1} & set(range(B))))
+
+
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 2.0])
 def test_any_scale(scale):
     case = Case(21, [150], [200], 2, "bf16", scale=scale)
