@@ -9,26 +9,33 @@
 //
 // An item is a group of up to 128 rows and a run of tokens, as two units: one CTA computes the scores of the group and
 // one half of the value columns (O for all 512 would fill tensor memory), so that CTAs share nothing and wait for
-// none. Tiles of 64 tokens; a unit's tensor memory: O [128 x 256] fp32, S [128 x 64] fp32, and 384 of the 576 query
-// columns as the score product's A operand (the other 192 are in shared memory, 48 KB). The probabilities go through
-// 16 KB of shared memory, so S is free again once it has been read, and one buffer is enough: the products go
+// none. Tiles of 64 tokens; a unit's tensor memory: O [128 x 256] fp32, S [128 x 64] fp32, the weights [128 x 64] in 16
+// bits as the value product's A operand, and 320 of the 576 query columns as the score product's (the other 256 are in
+// shared memory, 64 KB: a product that reads A there takes 49 cycles in place of 33). The products go
 //   S(i+1) PV(i) S(i+2) PV(i+1) ...
-// (issued by two warps) and S(i)'s softmax runs beside PV(i-1) and S(i+1). A tile is 72 KB: the half of its latents that only the score
-// product reads, with the rotary keys (two slots of 40 KB, free after S), and the half that is the values too (a ring
-// of five pieces of 128 columns, 16 KB, free after PV): what the next score product needs last has been on its way
-// longest.
+// each issued by a warp of its own, PV(i) only behind S(i+1): S(i+1) is read out of its one buffer beside PV(i), and
+// S(i)'s softmax runs beside PV(i-1) and S(i+1). (With PV(i) as soon as its weights are there it ran in the middle of
+// S(i+1), and the tensor cores idled behind that: 2340 cycles a tile, 2100 in turns, of which the products take 1960.)
+// A tile is 72 KB: the half of its latents that only the score product reads, with the rotary keys (two slots of 40 KB,
+// free after S), and the half that is the values too (a ring of five pieces of 128 columns, 16 KB, free after PV): what
+// the next score product needs last has been on its way longest.
+//
+// Four warps of their own read the next unit's queries while the last tiles of a unit are in the works, write them as
+// soon as its last score product is done, and take its output out of tensor memory beside the next unit's first scores.
+// 65,536 common tokens, 2432 rows: 296 us, 1.79 PFLOP/s of products as they run (the scores once in each of two CTAs).
 //
 // The running maximum moves only when a tile's passes it by more than the weights' type has room for (2^15 in fp16, 2^60
 // in bf16, whose sums and O stay far below fp32's end too): with a slack of 2^8 some row of a warp moved it every few
-// tiles, and with it all of O, 590 cycles a tile of the serving batch. Sums are of the unrounded weights, in fp32; the weights are rounded once to the cache's type (2^-12 of themselves in fp16, 2^-9 in bf16: as the 16-bit output).
+// tiles, and with it all of O, 590 cycles a tile of the serving batch. Sums are of the unrounded weights, in fp32; the
+// weights are rounded once to the cache's type (2^-12 of themselves in fp16, 2^-9 in bf16: as the 16-bit output).
 // Tokens that some row of a group does not see (behind a shorter context or, in a window, behind the row) have weight 0
 // there, and values that are not finite are taken out of such tiles: for a row that does see one of them its score has
 // already made the weight so.
 //
 // Units are shared out by the host plan (plan_shared.cpp). The merge is a kernel of its own.
 //
-// Warps: 0-3 softmax, queries and partial output (thread = row), 4 score products, 6 value products, 5 and 7 loads (of the
-// two parts of a tile, each as soon as there is room).
+// Warps: 0-3 softmax (thread = row), 4 score products, 6 value products, 5 and 7 loads (of the two parts of a tile, each as
+// soon as there is room), 8-11 queries and partial output (thread = row).
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -47,23 +54,29 @@ constexpr int kSlotA = kOther + kPe;
 constexpr int kPiece = kT * 128 * 2;      // 16 KB: 128 of the unit's own columns
 constexpr int kRingB = 5;
 constexpr int kQChunk = kRows * 128;      // 16 KB: [128 rows x 64 columns]
-constexpr int kQTmemBlocks = 6;           // blocks of 64 query columns in tensor memory; the last two and the rotary one are not
+constexpr int kQTmemBlocks = 5;           // blocks of 64 query columns in tensor memory; the last three and the rotary one are not
+constexpr int kQSmemChunks = kRank / kBoxCols - kQTmemBlocks + 1;
 constexpr int kScoreWarp = 4, kLoadWarpA = 5, kValueWarp = 6, kLoadWarpB = 7;
-constexpr int kThreads = 256;
-constexpr uint32_t kOffP = 3 * kQChunk;
-constexpr uint32_t kOffA = kOffP + kQChunk;
+constexpr int kThreads = 384;
+// Registers: launched with 120 a thread.
+constexpr int kSoftmaxRegs = 168, kIssueRegs = 64, kAuxRegs = 128;
+static_assert(kSoftmaxRegs + kIssueRegs + kAuxRegs <= 3 * 120, "what the block was launched with");
+constexpr uint32_t kOffA = kQSmemChunks * kQChunk;
 constexpr uint32_t kOffB = kOffA + 2 * kSlotA;
 constexpr uint32_t kOffSmall = kOffB + kRingB * kPiece;
-constexpr uint32_t kSmem = kOffSmall + 1024 + 1024;
+constexpr uint32_t kSmallBytes = 2048;
+constexpr uint32_t kSmem = kOffSmall + kSmallBytes + 1024;
 static_assert(kSmem <= 232448, "shared memory per CTA");
-constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemQ = 320;
+constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemP = 320, kTmemQ = 352;
+static_assert(kTmemQ + 32 * kQTmemBlocks == 512, "tensor memory's columns");
 
 struct Small {
-  uint64_t a_full[2], a_empty[2], b_full[4], b_empty[kRingB], q_full, s_full, s_empty, p_full, pv_done, drain[2];
+  uint64_t a_full[2], a_empty[2], b_full[4], b_empty[kRingB], q_full, q_empty, s_full, s_empty, s_issued[2], p_full, pv_done, stat_full[2], o_empty, drain[2];
+  float inv[2][kRows];  // 1 / sum, of the units in turn
   uint32_t tmem_base;
   int32_t abort_flag;
 };
-static_assert(sizeof(Small) <= 1024, "small smem region");
+static_assert(sizeof(Small) <= kSmallBytes, "small smem region");
 
 __device__ __forceinline__ void tma_load_pages(void* dst, const CUtensorMap* map, int32_t block, int32_t group, uint64_t* bar) {
   asm volatile(
@@ -100,6 +113,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+
+__device__ __forceinline__ void store32(float* dst, const float* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void issue_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
 }
 
 struct Unit {
@@ -162,9 +184,9 @@ __device__ __forceinline__ void clean_values(uint8_t* p0, uint8_t* p1, int r) {
   }
 }
 
-// 168 registers a thread: the merge's CTAs then fit on an SM beside this kernel's one and wait there for its end.
+// 120 registers a thread at launch: a CTA of the merge then fits on an SM beside this kernel's one and waits there.
 template <bool BF16>
-__global__ void __maxnreg__(168)
+__global__ void __maxnreg__(120)
     mla_decode_shared_kernel(const __grid_constant__ CUtensorMap tm_half, const __grid_constant__ CUtensorMap tm_piece,
                              const __grid_constant__ CUtensorMap tm_kpe, const SharedParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -183,7 +205,13 @@ __global__ void __maxnreg__(168)
     for (int s = 0; s < 4; ++s) mbar_init(&sm->b_full[s], 2);
     for (int s = 0; s < kRingB; ++s) mbar_init(&sm->b_empty[s], 1);
     mbar_init(&sm->q_full, 4);
+    mbar_init(&sm->q_empty, 1);
+    mbar_init(&sm->stat_full[0], 4);
+    mbar_init(&sm->stat_full[1], 4);
+    mbar_init(&sm->o_empty, 4);
     mbar_init(&sm->s_full, 1);
+    mbar_init(&sm->s_issued[0], 1);
+    mbar_init(&sm->s_issued[1], 1);
     mbar_init(&sm->s_empty, 4);
     mbar_init(&sm->p_full, 4);
     mbar_init(&sm->pv_done, 1);
@@ -207,6 +235,7 @@ __global__ void __maxnreg__(168)
 
   if (warp == kLoadWarpA || warp == kLoadWarpB) {
     // ---------------------------------------------------------------- loads
+    issue_registers();
     const bool first = warp == kLoadWarpA;  // the half that is only keys, and the rotary keys; else the values' half
     uint32_t tile = 0;
     bool ok = true;
@@ -254,6 +283,7 @@ __global__ void __maxnreg__(168)
     if (!ok) *abort_flag = 1;
   } else if (warp == kScoreWarp) {
     // ---------------------------------------------------------------- score products: the warp in step (umma_issue.cuh)
+    issue_registers();
     const uint32_t leader = elect_one();
     const uint32_t idesc = idesc_f16_f32(kRows, kT, BF16, false, false);
     const uint64_t q0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
@@ -280,7 +310,7 @@ __global__ void __maxnreg__(168)
       tc_fence_after();
       const uint64_t pe = pe0 + s * (kSlotA / 16), a = a0 + s * (kSlotA / 16);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) issue_ss(leader, tmem + kTmemS, q0 + 2 * (kQChunk / 16) + 2 * kk, pe + 2 * kk, idesc, kk > 0);
+      for (int kk = 0; kk < 4; ++kk) issue_ss(leader, tmem + kTmemS, q0 + (kQSmemChunks - 1) * (kQChunk / 16) + 2 * kk, pe + 2 * kk, idesc, kk > 0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) block(4 * (half ^ 1) + j, a + j * 64);
       issue_commit(leader, &sm->a_empty[s]);
@@ -290,9 +320,14 @@ __global__ void __maxnreg__(168)
       for (int x = 0; x < 2; ++x) {
         const uint32_t b = (2 * t + x) % kRingB;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) block(4 * half + 2 * x + j, k0 + b * (kPiece / 16) + j * 64);
+        for (int j = 0; j < 2; ++j) {
+          if (x == 1 && j == 1 && lane == 0) mbar_arrive(&sm->s_issued[t & 1]);
+          __syncwarp();
+          block(4 * half + 2 * x + j, k0 + b * (kPiece / 16) + j * 64);
+        }
       }
       issue_commit(leader, &sm->s_full);
+      if (i + 1 == w.tiles) issue_commit(leader, &sm->q_empty);
     };
     for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
       if (w.tiles == 0) continue;
@@ -313,15 +348,20 @@ __global__ void __maxnreg__(168)
   } else if (warp == kValueWarp) {
     // ---------------------------------------------------------------- value products: a warp of their own, so that what one
     // of the two waits for is hidden behind the other's products
+    issue_registers();
     const uint32_t leader = elect_one();
     const uint32_t idesc = idesc_f16_f32(kRows, 128, BF16, false, true);
-    const uint64_t p0 = smem_desc_sw128(smem_u32(smem + kOffP), 16, 1024);
     const uint64_t v0 = smem_desc_sw128(smem_u32(smem + kOffB), 1024, 2048);  // a piece as values
-    uint32_t t = 0;
+    uint32_t t = 0, unit = 0;
     bool ok = true;
     for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
-      for (int i = 0; i < w.tiles; ++i, ++t) {
+      if (w.tiles == 0) continue;
+      if (unit > 0) ok = mbar_wait_warp(&sm->o_empty, (unit - 1) & 1, tmo);
+      ++unit;
+      for (int i = 0; i < w.tiles && ok; ++i, ++t) {
         ok = mbar_wait_warp(&sm->p_full, t & 1, tmo);  // (its scores are done: the tile is there)
+        // behind the next tile's scores, whose softmax then runs beside this product
+        if (i + 1 < w.tiles) ok = ok && mbar_wait_warp(&sm->s_issued[(t + 1) & 1], ((t + 1) >> 1) & 1, tmo);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -329,7 +369,7 @@ __global__ void __maxnreg__(168)
           const uint32_t b = (2 * t + x) % kRingB;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            issue_ss(leader, tmem + kTmemO + 128 * x, p0 + 2 * kk, v0 + b * (kPiece / 16) + kk * 256, idesc, i > 0 || kk > 0);
+            issue_ts(leader, tmem + kTmemO + 128 * x, tmem + kTmemP + 8 * kk, v0 + b * (kPiece / 16) + kk * 256, idesc, i > 0 || kk > 0);
           if (x == 0) issue_commit(leader, &sm->b_empty[b]);
         }
         issue_commit(leader, &sm->pv_done);
@@ -343,11 +383,12 @@ __global__ void __maxnreg__(168)
     __syncwarp();
   } else if (warp < kScoreWarp) {
     // ---------------------------------------------------------------- softmax: thread = row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int r = tid;
     const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
     const float scale = p.scale_log2;
     constexpr float kSlack = BF16 ? 60.f : 15.f;
-    uint32_t tile0 = 0;
+    uint32_t tile0 = 0, unit = 0;
     bool ok = true;
     for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
       const bool real = r < w.rows;
@@ -356,45 +397,6 @@ __global__ void __maxnreg__(168)
       if (w.tiles == 0) {
         if (real && w.half == 0) p.part_lse[slot_row] = -INFINITY;  // (the merge does not read the values)
         continue;
-      }
-      {  // the queries: the products of the unit before are done
-        const uint4* const src = reinterpret_cast<const uint4*>(p.q_abs + row * kRank);
-        const uint4 none = make_uint4(0, 0, 0, 0);
-        // the blocks of shared memory, eight lanes a row's 128 bytes, all in flight; those of tensor memory beside them, a
-        // thread a row, in two rounds of 24 16-byte pieces
-        for (int at = tid; at < 3 * kRows * 8; at += kRows) {
-          const int c = at / (kRows * 8), rr = at / 8 % kRows, j = at % 8;
-          const bool in = rr < w.rows;
-          const long long from = w.row0 + (in ? rr : 0);
-          const uint16_t* const piece = c < 2 ? p.q_abs + from * kRank + (kQTmemBlocks + c) * kBoxCols + 8 * j : p.q_pe + from * kRope + 8 * j;
-          cp_async16(smem + c * kQChunk + rr * 128 + ((j ^ (rr & 7)) << 4), piece, in ? 16u : 0u);
-        }
-        constexpr int kPieces = 24;
-        static_assert(kQTmemBlocks * 8 == 2 * kPieces, "two rounds of loads");
-#pragma unroll
-        for (int round = 0; round < 2; ++round) {
-          uint4 x[kPieces];
-#pragma unroll
-          for (int j = 0; j < kPieces; ++j) x[j] = real ? src[round * kPieces + j] : none;
-#pragma unroll
-          for (int g = 0; g < kPieces / 4; ++g) {
-            float v[16];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[4 * j] = __uint_as_float(x[4 * g + j].x);
-              v[4 * j + 1] = __uint_as_float(x[4 * g + j].y);
-              v[4 * j + 2] = __uint_as_float(x[4 * g + j].z);
-              v[4 * j + 3] = __uint_as_float(x[4 * g + j].w);
-            }
-            tmem_st16(tmem + lanes + kTmemQ + 16 * (round * (kPieces / 4) + g), v);
-          }
-        }
-        cp_async_wait_all();
-        tmem_wait_st();
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->q_full);
       }
       const int seen = real ? visible(p, static_cast<int>(row)) : 0x7fffffff;
       float m = -INFINITY, l = 0.f;
@@ -450,9 +452,10 @@ __global__ void __maxnreg__(168)
           h[j] = pack2<BF16>(e.x, e.y);
         }
         sum = add2(sum, sum_b);
-        if (i > 0) {  // O and the weights' buffer are free
+        if (t > 0) {  // the weights' buffer, and (but for a unit's first tile) O, are free
           ok = mbar_wait_warp(&sm->pv_done, (t - 1) & 1, tmo);
           if (!ok) break;
+          tc_fence_after();
         }
         if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
           const float alpha = need ? (m == -INFINITY ? 0.f : exp2f(m - m_new)) : 1.f;
@@ -478,48 +481,145 @@ __global__ void __maxnreg__(168)
           ok = mbar_wait_warp(&sm->b_full[t & 3], (t >> 2) & 1, tmo);
           if (!ok) break;
           clean_values<BF16>(smem + kOffB + (b % kRingB) * kPiece, smem + kOffB + (c % kRingB) * kPiece, r);
+          fence_proxy_async_smem();
         }
-        const uint32_t at = smem_u32(smem + kOffP) + r * 128;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sts128(at + ((j ^ (r & 7)) << 4), make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]));
-        fence_proxy_async_smem();
+        for (int j = 0; j < 2; ++j) {
+          float v[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(h[16 * j + c]);
+          tmem_st16(tmem + lanes + kTmemP + 16 * j, v);
+        }
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->p_full);
       }
       if (!ok) break;
-      ok = mbar_wait_warp(&sm->pv_done, (tile0 + w.tiles - 1) & 1, tmo);
-      if (!ok) break;
-      tc_fence_after();
       const bool any = m != -INFINITY;
-      const float inv = any ? 1.f / l : 0.f;
-      // the partial output, 32 columns at a time through the warp's quarter of the weights' buffer: rows of 128 bytes out,
-      // four to an instruction (a thread a row, 16 bytes each, takes the memory pipeline eight times as long)
-      float* const out = p.part_o + (static_cast<long long>(w.slot) * kRows + 32 * warp) * kRank + kHalf * w.half;
-      const uint32_t stage = smem_u32(smem + kOffP) + 4096 * warp;
+      sm->inv[unit & 1][r] = any ? 1.f / l : 0.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->stat_full[unit & 1]);
+      if (real && w.half == 0) p.part_lse[slot_row] = any ? m + log2f(l) : (l != l ? l : -INFINITY);
+      ++unit;
+      tile0 += w.tiles;
+    }
+    if (!ok) *abort_flag = 1;
+  } else {
+    // ---------------------------------------------------------------- queries and partial output: thread = row
+    // While a unit's last tiles are still in the works, the next one's queries are read, and written as soon as its last
+    // score product is done; its first scores and their softmax run beside the output of the unit before.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
+    const int r = tid & (kRows - 1);
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    uint32_t unit = 0, tile0 = 0;
+    int slot = 0, rows = 0, half = 0;  // of the unit before
+    bool ok = true;
+    auto output = [&](auto last_of) {  // of unit - 1, whose last tile is tile0 - 1
+      constexpr bool last = decltype(last_of)::value;
+      // (a barrier a unit in turns: the unit after may be through its softmax, the one behind that waits for this output)
+      ok = mbar_wait_warp(&sm->stat_full[(unit - 1) & 1], ((unit - 1) >> 1) & 1, tmo);
+      ok = ok && mbar_wait_warp(&sm->pv_done, (tile0 - 1) & 1, tmo);
+      if (!ok) return;
+      tc_fence_after();
+      const float inv = sm->inv[(unit - 1) & 1][r];
+      float* const out = p.part_o + (static_cast<long long>(slot) * kRows + r) * kRank + kHalf * half;
+      const uint32_t stage = smem_u32(smem + kOffA) + 4096 * (warp & 3);
 #pragma unroll 1
       for (int q = 0; q < kHalf / 32; ++q) {
         float o[32];
         ld32(tmem + lanes + kTmemO + 32 * q, o);
         tmem_wait_ld();
-        __syncwarp();
+        if constexpr (last) {
+          // nothing else runs any more: through 4 KB a warp of the tiles' place, rows of 128 bytes out, four to an
+          // instruction (a thread a row, 32 bytes each, takes the memory pipeline longer)
+          __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          sts128(stage + lane * 128 + ((j ^ (lane & 7)) << 4),
-                 make_uint4(__float_as_uint(o[4 * j] * inv), __float_as_uint(o[4 * j + 1] * inv), __float_as_uint(o[4 * j + 2] * inv), __float_as_uint(o[4 * j + 3] * inv)));
-        __syncwarp();
+          for (int j = 0; j < 8; ++j)
+            sts128(stage + lane * 128 + ((j ^ (lane & 7)) << 4),
+                   make_uint4(__float_as_uint(o[4 * j] * inv), __float_as_uint(o[4 * j + 1] * inv), __float_as_uint(o[4 * j + 2] * inv), __float_as_uint(o[4 * j + 3] * inv)));
+          __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int at = 4 * j + (lane >> 3), c = lane & 7;  // row, 16-byte piece
-          const uint4 v = lds128(stage + at * 128 + ((c ^ (at & 7)) << 4));
-          if (32 * warp + at < w.rows) *reinterpret_cast<uint4*>(out + static_cast<long long>(at) * kRank + 32 * q + 4 * c) = v;
+          for (int j = 0; j < 8; ++j) {
+            const int at = 4 * j + (lane >> 3), c = lane & 7;  // row, 16-byte piece
+            const uint4 v = lds128(stage + at * 128 + ((c ^ (at & 7)) << 4));
+            if (32 * (warp & 3) + at < rows) *reinterpret_cast<uint4*>(out + static_cast<long long>(at - lane) * kRank + 32 * q + 4 * c) = v;
+          }
+          continue;
+        }
+        if (q == kHalf / 32 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->o_empty);
+        }
+        if (r < rows) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = o[8 * j + i] * inv;
+            store32(out + 32 * q + 8 * j, v);
+          }
         }
       }
-      __syncwarp();
-      if (real && w.half == 0) p.part_lse[slot_row] = any ? m + log2f(l) : (l != l ? l : -INFINITY);
+    };
+    for (int k = 0; ok && unit_of(p, k, lane, w); ++k) {
+      const bool real = r < w.rows;
+      const long long row = w.row0 + (real ? r : 0);
+      if (w.tiles == 0) continue;
+      const uint4* const src = reinterpret_cast<const uint4*>(p.q_abs + row * kRank);
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      constexpr int kPieces = 4 * kQTmemBlocks;
+      static_assert(kQTmemBlocks * 8 == 2 * kPieces, "two rounds of loads");
+      uint4 x[kPieces];
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) x[j] = real ? src[j] : none;
+      if (unit > 0) ok = mbar_wait_warp(&sm->q_empty, (unit - 1) & 1, tmo);
+      if (!ok) break;
+      tc_fence_after();
+      // the blocks of shared memory, eight lanes a row's 128 bytes, all in flight; those of tensor memory beside them, a
+      // thread a row, in two rounds of 16-byte pieces
+      for (int at = r; at < kQSmemChunks * kRows * 8; at += kRows) {
+        const int c = at / (kRows * 8), rr = at / 8 % kRows, j = at % 8;
+        const bool in = rr < w.rows;
+        const long long from = w.row0 + (in ? rr : 0);
+        const uint16_t* const piece = c < kQSmemChunks - 1 ? p.q_abs + from * kRank + (kQTmemBlocks + c) * kBoxCols + 8 * j : p.q_pe + from * kRope + 8 * j;
+        cp_async16(smem + c * kQChunk + rr * 128 + ((j ^ (rr & 7)) << 4), piece, in ? 16u : 0u);
+      }
+#pragma unroll
+      for (int round = 0; round < 2; ++round) {
+#pragma unroll
+        for (int g = 0; g < kPieces / 4; ++g) {
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[4 * j] = __uint_as_float(x[4 * g + j].x);
+            v[4 * j + 1] = __uint_as_float(x[4 * g + j].y);
+            v[4 * j + 2] = __uint_as_float(x[4 * g + j].z);
+            v[4 * j + 3] = __uint_as_float(x[4 * g + j].w);
+          }
+          tmem_st16(tmem + lanes + kTmemQ + 16 * (round * (kPieces / 4) + g), v);
+        }
+        if (round == 0) {
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) x[j] = real ? src[kPieces + j] : none;
+        }
+      }
+      cp_async_wait_all();
+      tmem_wait_st();
+      fence_proxy_async_smem();
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->q_full);
+      if (unit > 0) output(std::false_type{});
+      slot = w.slot;
+      rows = w.rows;
+      half = w.half;
       tile0 += w.tiles;
+      ++unit;
     }
+    if (ok && unit > 0) output(std::true_type{});
+    tc_fence_before();
     if (!ok) *abort_flag = 1;
   }
   __syncwarp();
