@@ -861,7 +861,8 @@ typedef struct {
  * Precision: scores, maxima, sums and out_lse are fp32, the weights of the value
  * product are rounded once to `dtype` (half a step: 2^-12 of themselves in fp16,
  * or 2^-25 of the row's greatest where that is more, 2^-9 of themselves in bf16)
- * and the sum that normalizes takes them unrounded.
+ * and the sum that normalizes takes them unrounded. A weight may reach 2^15 before
+ * the sums are moved to a new maximum: bf16 values times tokens stay below 2^112.
  *
  * q_nope : device, row i, head h at i * q_nope_stride[0] + h * q_nope_stride[1]
  *          elements, 128 of them; q_pe alike, 64; both 16-byte aligned
@@ -968,8 +969,10 @@ typedef struct {
  * Precision: scores, maxima, sums and out_lse are fp32; the weights of the value
  * product are rounded once to `dtype` (half a step: 2^-12 of themselves in fp16,
  * or 2^-25 of the row's greatest where that is more, 2^-9 of themselves in bf16)
- * and the sum that normalizes takes them unrounded. The partials are fp32; `out`
- * is rounded once to out_dtype.
+ * and the sum that normalizes takes them unrounded. A weight may reach 2^15 (fp16)
+ * or 2^30 (bf16) before the sums are moved to a new maximum: bf16 values times
+ * tokens stay below 2^97. The partials are fp32; `out` is rounded once to
+ * out_dtype.
  *
  * q_absorbed, q_pe, caches: as for mla_decode_partial, 16-bit caches only
  * shared_table: device [P / block_size] int32 (a row of block_table, for

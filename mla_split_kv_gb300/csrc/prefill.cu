@@ -19,10 +19,9 @@
 // each with barriers of its own, so that a chunk is refilled as soon as its last product is done. A tile's keys and
 // values together are 80 KB: two whole ones would not fit beside the queries, eight chunks are 1.6.
 //
-// The running maximum is moved only when a tile's maximum passes it by more than the weights' type has room for (2^15 in
-// fp16; 2^60 in bf16, whose sums and O stay far below fp32's end, too), so O is hardly ever rescaled; the sums are those of
-// the unrounded weights in fp32. P is rounded once to 16 bits
-// (2^-9 of itself in bf16, 2^-12 in fp16, as the output is).
+// The running maximum is moved only when a tile's maximum passes it by more than 2^15, the room that fp16 has for weights
+// above 1 (more, in bf16, is no faster), so O is hardly ever rescaled; the sums are those of the unrounded weights in fp32.
+// P is rounded once to 16 bits (2^-9 of itself in bf16, 2^-12 in fp16, as the output is).
 //
 // What lies in a tile behind a row's last visible token counts for nothing, infinities and NaN included: its weight is
 // an exact 0, and where a tile has tokens that some row of the subtile does not see, its values are searched for
@@ -506,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + kTmemS + s * kTile, to = tmem + lanes + kTmemO + s * kDim;
     const float scale = p.scale_log2;
-    constexpr float kSlack = BF16 ? 60.f : 15.f;
+    constexpr float kSlack = 15.f;
     uint32_t done = 0;   // tiles of this subtile so far
     uint32_t tile0 = 0;  // tiles of all units before this one
     bool ok = true;

@@ -154,6 +154,16 @@ def test_scores_that_rise_and_peak(dtype):
     case.check(*case.run())
 
 
+def test_large_values():
+    """Values of 2^98 in bf16 under scores that rise: sums of weights that lag behind the maximum stay finite."""
+    case = Case(23, [700], [700], 2, "bf16")
+    case.k.mul_((torch.arange(700, device="cuda") / 200)[:, None, None].to(case.dtype))
+    case.v.mul_(2.0 ** 98)
+    out, lse = case.run()
+    assert torch.isfinite(out).all()
+    case.check(out, lse)
+
+
 @pytest.mark.parametrize("new,ctx", [([300], [300]), ([300], [1500]), ([130, 600], [130, 2600])])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("what", ["nan", "inf"])

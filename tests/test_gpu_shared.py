@@ -168,6 +168,25 @@ def test_scores_that_rise(dtype):
     case.check(*case.run())
 
 
+def test_large_values():
+    """Latents of 2^80 (queries as much smaller) whose scores rise: sums of weights that lag behind the maximum stay finite."""
+    case = Case(14, [900, 800], 640, 16, 1, 32, "bf16")
+    case.ckv.mul_(2.0 ** 80)
+    case.q_abs.mul_(2.0 ** -80)
+    for b, n in enumerate(case.lens):
+        row = case.rows_of(b, n)[case.shared if b else 0:]
+        case.ckv.view(-1, 512)[row] *= (torch.arange(len(row), device="cuda") / 300)[:, None].to(case.dtype)
+    out, lse = case.run()
+    assert torch.isfinite(out).all()
+    case.check(out, lse, heads=[0, 7, 15])
+
+
+@pytest.mark.parametrize("lens,shared,H,q_len", [([700 + 9 * i for i in range(18)], 512, 128, 1), ([16500], 16384, 16, 1), ([30000, 29000], 28672, 16, 1)])
+def test_merges_of_many_rows_and_of_many_parts(lens, shared, H, q_len):
+    case = Case(15, lens, shared, H, q_len, 64, "f16")
+    case.check(*case.run(), requests=sorted({0, len(lens) - 1}), heads=sorted({0, 5, H - 1}))
+
+
 def test_hidden_tokens_that_are_not_finite():
     """In a causal window, a token that only the last rows see: the rows before it do not."""
     case = Case(7, [300, 290], 256, 16, 4, 16, "f16", True)
