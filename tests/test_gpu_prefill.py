@@ -154,6 +154,30 @@ def test_scores_that_rise_and_peak(dtype):
     case.check(*case.run())
 
 
+@pytest.mark.parametrize("new,ctx,H", [([300, 5], [300, 700], 3), ([700], [4000], 6), ([1, 1], [40, 1], 2)])
+def test_queries_in_other_orders(new, ctx, H):
+    """Queries that lie head by head, that are every second row of a tensor, and parts of wider ones."""
+    case = Case(24, new, ctx, H, "bf16")
+    want = case.run()
+    q = torch.cat((case.q_nope, case.q_pe), 2)
+    by_head = torch.empty(H, case.T, 192, dtype=q.dtype, device="cuda")
+    by_head.copy_(q.transpose(0, 1))
+    apart = torch.full((2 * case.T, H, 200), float("nan"), dtype=q.dtype, device="cuda")
+    apart[::2, :, :192] = q
+    for x in (by_head.transpose(0, 1), apart[::2]):
+        case.q_nope, case.q_pe = x[..., :128], x[..., 128:192]
+        got = case.run()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    case.check(*got)
+
+
+@pytest.mark.parametrize("H", [1, 256])
+def test_fewest_and_most_heads(H):
+    case = Case(25, [130, 2], [200, 2], H, "f16", joint=True)
+    case.check(*case.run(), heads=sorted({0, H // 2, H - 1}))
+
+
 def test_large_values():
     """Values of 2^98 in bf16 under scores that rise: sums of weights that lag behind the maximum stay finite."""
     case = Case(23, [700], [700], 2, "bf16")
