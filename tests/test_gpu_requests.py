@@ -205,8 +205,11 @@ def test_waits_that_run_out_are_reported(call):
     nb.mla_check_device_errors(None)
     nb.mla_set_wait_timeout_ns(1)
     try:
-        case.run()
-        st, code = nb.mla_check_device_errors(None)
+        for _ in range(50):  # (a wait is found too long when the device's timer has moved on and it still lasts)
+            case.run()
+            st, code = nb.mla_check_device_errors(None)
+            if st != nb.MLA_OK:
+                break
     finally:
         nb.mla_set_wait_timeout_ns(2_000_000_000)
     assert st == nb.MLA_ERR_TIMEOUT and code & 1, (st, code)
