@@ -494,18 +494,17 @@ def mla_plan_shared(context_lens: Sequence[int], shared_tokens: int, num_heads: 
     lens = (ctypes.c_int32 * B)(*[int(x) for x in context_lens])
     plan = mla_shared_plan_t()
     plan.shared_tokens = shared_tokens
-    st = lib.mla_plan_shared(lens, B, num_heads, q_len, block_size, ctypes.byref(dev), ctypes.byref(plan))
-    if st not in (MLA_OK, MLA_ERR_CAPACITY):
-        raise MlaError(st, "mla_plan_shared")
-    units = (mla_shared_unit_t * max(1, plan.num_units))()
-    indptr = (ctypes.c_int32 * (B * -(-q_len * num_heads // 128) + 1))()
-    ctas = (ctypes.c_int32 * (dev.num_sms + 1))()
-    plan.unit_capacity = plan.num_units
-    plan.units = ctypes.cast(units, ctypes.POINTER(mla_shared_unit_t))
+    indptr = (ctypes.c_int32 * (B * -(-max(q_len, 0) * max(num_heads, 0) // 128) + 1))()
+    ctas = (ctypes.c_int32 * (max(dev.num_sms, 0) + 1))()
     plan.own_indptr = ctypes.cast(indptr, ctypes.POINTER(ctypes.c_int32))
     plan.cta_indptr = ctypes.cast(ctas, ctypes.POINTER(ctypes.c_int32))
-    _check(lib.mla_plan_shared(lens, B, num_heads, q_len, block_size, ctypes.byref(dev), ctypes.byref(plan)),
-           "mla_plan_shared")
+    st, plan.num_units = MLA_ERR_CAPACITY, 4096
+    while st == MLA_ERR_CAPACITY and plan.num_units > plan.unit_capacity:  # (a second time where those are not enough)
+        plan.unit_capacity = plan.num_units
+        units = (mla_shared_unit_t * plan.unit_capacity)()
+        plan.units = ctypes.cast(units, ctypes.POINTER(mla_shared_unit_t))
+        st = lib.mla_plan_shared(lens, B, num_heads, q_len, block_size, ctypes.byref(dev), ctypes.byref(plan))
+    _check(st, "mla_plan_shared")
     out = [(x.row0, x.rows, x.request, x.t0, x.t1, x.slot, x.half) for x in units[: plan.num_units]]
     return SharedPlan(out, list(indptr), list(ctas)[: plan.num_ctas + 1], plan.num_slots, plan.shared_parts)
 

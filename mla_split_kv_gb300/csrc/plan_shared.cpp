@@ -81,32 +81,35 @@ extern "C" mla_status_t mla_plan_shared(const int32_t* context_lens_host, int32_
     for (const bool even : {true, false}) {
       const Cut cut{length, even};
       std::vector<std::pair<int64_t, int64_t>> units;  // tiles, how many
-      int64_t parts = 0;
+      int64_t parts = 0, sum = 0;
       auto add = [&](int64_t tiles, int64_t times, int64_t rows_of) {
         const int64_t n = cut.pieces(tiles), each = cut.of(tiles);
         if (n > 1) units.emplace_back(each, 2 * times * (n - 1));
         units.emplace_back(tiles - (n - 1) * each, 2 * times);
         parts += n * rows_of;
+        sum += 2 * times * (tiles + n * kUnitTiles);
       };
       add(common, groups, rows);
       for (int32_t b = 0; b < B; ++b) add(own[b], own_groups, per);
+      // (no better than the average, and none that is already as long as the best is gone on with)
+      const int64_t merge = parts / kMergeParts;
+      int64_t busiest = (sum + dev->num_sms - 1) / dev->num_sms;
+      auto lost = [&] { return best_cost >= 0 && busiest + merge >= best_cost; };
+      if (lost()) continue;
       std::sort(units.begin(), units.end(), std::greater<>());
-      int64_t busiest = 0;
       std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
       for (int32_t i = 0; i < dev->num_sms; ++i) ends.push(0);
       for (const auto& u : units) {
-        for (int64_t i = 0; i < u.second; ++i) {
+        for (int64_t i = 0; i < u.second && !lost(); ++i) {
           const int64_t end = ends.top() + u.first + kUnitTiles;
           ends.pop();
           ends.push(end);
           busiest = std::max(busiest, end);
         }
       }
-      const int64_t cost = busiest + parts / kMergeParts;
-      if (best_cost < 0 || cost < best_cost) {
-        best_cost = cost;
-        best = cut;
-      }
+      if (lost()) continue;
+      best_cost = busiest + merge;
+      best = cut;
     }
   }
 
