@@ -18,7 +18,8 @@ namespace {
 constexpr int64_t kTile = 64;   // tokens
 constexpr int64_t kGroup = 128; // rows
 // A unit's time in tiles of about 1.1 us: its tiles, and the start and the end (queries, the first loads, the partial
-// output; plans made with 4 or 8 are within 1%). A row's part costs the merge about 2 KB of L2, of which the device reads 5 MB in the time of a tile.
+// output; plans made with 4 or 8 are within 1%). A row's part costs the merge about 2 KB of L2, of which the device
+// reads 5 MB in the time of a tile.
 constexpr int64_t kUnitTiles = 6;
 constexpr int64_t kMergeParts = 2500;
 

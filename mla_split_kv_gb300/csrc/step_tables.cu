@@ -20,7 +20,8 @@
 // eight CTAs that scanned the requests each and wrote the slots, too.
 //
 // mla_cache_append_slots: a copy of 1152 bytes a token, HBM-bound: a warp takes one token of a small step, four of a
-// large one, whose loads are all in flight together.
+// large one, whose loads are all in flight together. 65,536 tokens: 22.6 us, 6.7 TB/s, the rate of a plain copy; 24 tokens:
+// 1 us in a replayed graph.
 #include "block_scan.cuh"
 #include "device_common.cuh"
 
