@@ -720,7 +720,7 @@ typedef struct {
 /*
  * mla_update_tables -- a step's block tables, slot map and offsets, on the
  * device, from the requests' lengths and what each gets or gives back. One
- * launch, two where `slots` has more than 8192 places; may be captured and
+ * launch, two where `slots` has more than 4096 places; may be captured and
  * replayed.
  *
  * Request b has L_b = context_lens[b] tokens and changes by n_b = changes[b]

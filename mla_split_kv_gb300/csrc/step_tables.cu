@@ -14,14 +14,15 @@
 // one search in shared memory, one or two dependent loads. A step of 256 single tokens takes 5.5 us a call in a
 // replayed graph.
 //
-// One CTA does all of a small step (as many slots as it has threads, eight times over). Where there are more places in
-// `slots`, it leaves them to a second kernel over the whole device, which reads offsets, lengths and tables back:
+// One CTA does all of a small step. Where there are more than 4096 places in `slots`, it leaves them to a second kernel
+// over the whole device, which reads offsets, lengths and tables back (256 requests: 4096 places 7.8 us a call with one
+// kernel, 8.6 with two; 8192: 11.6, 9.9; 16,384: 18.3, 10.2):
 // 512 requests, 30% of which give pages back, and 100,147 new tokens in all: 13.7 us a call; 23.1 us with a cluster of
 // eight CTAs that scanned the requests each and wrote the slots, too.
 //
-// mla_cache_append_slots: a copy of 1152 bytes a token, HBM-bound: a warp takes one token of a small step, four of a
-// large one, whose loads are all in flight together. 65,536 tokens: 22.6 us, 6.7 TB/s, the rate of a plain copy; 24 tokens:
-// 1 us in a replayed graph.
+// mla_cache_append_slots: a copy of 1152 bytes a token, HBM-bound: a warp a token (four tokens a warp, all their loads in
+// flight together, took as long from 16,384 tokens on and longer below). 65,536 tokens: 22.6 us, 6.7 TB/s, the rate of a
+// plain copy; 24 tokens: 1 us in a replayed graph.
 #include "block_scan.cuh"
 #include "device_common.cuh"
 
@@ -29,8 +30,7 @@ namespace mla {
 
 namespace {
 
-constexpr int kFewSlots = 8192;  // up to so many places in `slots`: one CTA
-constexpr int64_t kFewTokens = 8192;  // up to so many tokens: a warp each
+constexpr int kFewSlots = 4096;  // up to so many places in `slots`: one CTA
 constexpr int kThreads = 1024;
 static_assert(kThreads == 32 * kScanWarps, "block_scan's");
 constexpr int kEach = 4;  // pages that a thread looks up before it stores any
@@ -269,38 +269,27 @@ __global__ void __launch_bounds__(kSlotThreads) mla_step_slots_kernel(const Tabl
 
 constexpr int kCopyWarps = 8;
 
-// kHold tokens a warp. Lane l holds columns 8 l.. and 256 + 8 l.. of each token, and of its rope columns (l < 8).
-template <int kHold>
+// A warp a token. Lane l holds its columns 8 l.. and 256 + 8 l.., and of the rope columns 8 l.. (l < 8).
 __global__ void __launch_bounds__(kCopyWarps * 32) mla_cache_append_slots_kernel(const AppendSlotsParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long tok0 = (static_cast<long long>(blockIdx.x) * kCopyWarps + warp) * kHold;
-  if (tok0 >= p.tokens) return;
-  long long slot[kHold];
-  uint4 c0[kHold], c1[kHold], r[kHold];
-#pragma unroll
-  for (int j = 0; j < kHold; ++j) slot[j] = tok0 + j < p.tokens ? p.slots[tok0 + j] : -1ll;
-#pragma unroll
-  for (int j = 0; j < kHold; ++j) {
-    if (slot[j] < 0) continue;
-    const uint4* const c = reinterpret_cast<const uint4*>(p.ckv_new + (tok0 + j) * p.ckv_stride);
-    c0[j] = c[lane];
-    c1[j] = c[lane + 32];
-    if (lane < 8) r[j] = reinterpret_cast<const uint4*>(p.kpe_new + (tok0 + j) * p.kpe_stride)[lane];
+  const long long tok = static_cast<long long>(blockIdx.x) * kCopyWarps + warp;
+  if (tok >= p.tokens) return;
+  const long long slot = p.slots[tok];
+  if (slot < 0) return;
+  if (slot >= p.rows) {
+    if (lane == 0) flag_error(MLA_DEVERR_BAD_PAGE);
+    return;
   }
-#pragma unroll
-  for (int j = 0; j < kHold; ++j) {
-    if (slot[j] < 0) continue;
-    if (slot[j] >= p.rows) {
-      if (lane == 0) flag_error(MLA_DEVERR_BAD_PAGE);
-      continue;
-    }
-    uint4* const c = reinterpret_cast<uint4*>(p.ckv + slot[j] * kRank);
-    c[lane] = c0[j];
-    c[lane + 32] = c1[j];
-    if (lane < 8) reinterpret_cast<uint4*>(p.kpe + slot[j] * kRope)[lane] = r[j];
-  }
+  const uint4* const from = reinterpret_cast<const uint4*>(p.ckv_new + tok * p.ckv_stride);
+  const uint4 c0 = from[lane], c1 = from[lane + 32];
+  uint4 r;
+  if (lane < 8) r = reinterpret_cast<const uint4*>(p.kpe_new + tok * p.kpe_stride)[lane];
+  uint4* const to = reinterpret_cast<uint4*>(p.ckv + slot * kRank);
+  to[lane] = c0;
+  to[lane + 32] = c1;
+  if (lane < 8) reinterpret_cast<uint4*>(p.kpe + slot * kRope)[lane] = r;
 }
 
 template <class Params>
@@ -339,11 +328,8 @@ cudaError_t launch_update_tables(const TablesParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_append_slots(const AppendSlotsParams& p, cudaStream_t stream) {
-  const long long warps_per_token = p.tokens > kFewTokens ? 4 : 1;
-  const long long units = (p.tokens + warps_per_token - 1) / warps_per_token;
-  const unsigned grid = static_cast<unsigned>((units + kCopyWarps - 1) / kCopyWarps);
-  return p.tokens > kFewTokens ? launch_dependent(mla_cache_append_slots_kernel<4>, grid, kCopyWarps * 32, 0, p, stream)
-                               : launch_dependent(mla_cache_append_slots_kernel<1>, grid, kCopyWarps * 32, 0, p, stream);
+  const unsigned grid = static_cast<unsigned>((p.tokens + kCopyWarps - 1) / kCopyWarps);
+  return launch_dependent(mla_cache_append_slots_kernel, grid, kCopyWarps * 32, 0, p, stream);
 }
 
 cudaError_t step_tables_read_clear_error(uint32_t* out) {
