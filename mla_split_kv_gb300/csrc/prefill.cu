@@ -61,6 +61,7 @@ constexpr int kThreads = 12 * 32;          // (the last two warps only make the 
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 168 * kThreads, "what the block was launched with");
 constexpr int kDirect = 64;                // items of a call that plans for itself
+constexpr int kDirectCost = 36;            // half tiles of its longest
 constexpr uint32_t kOffRing = 2 * kQBytes;
 constexpr uint32_t kOffSmall = kOffRing + kRing * kChunk;
 constexpr uint32_t kSmem = kOffSmall + 2048 + 1024;
@@ -744,8 +745,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mla_prefill_plan_kernel(const
   atomicMax(&longest, most);
   __syncthreads();
   // How runs are cut: each into as many pieces as its cost holds targets. With few enough runs a warp a candidate: the
-  // longest into 1 to 16 pieces, or all into as many as fill 1 to 16 rounds of the GPU's CTAs. Units in turns take at most
-  // their rounds times the longest, or the average and the longest; merging a piece costs about a twelfth of a half tile.
+  // longest into 1 to 16 pieces, or all into as many as fill 1 to 16 rounds of the GPU's CTAs. A CTA's time is the average,
+  // or more where the units at least as long as x take whole rounds of x; merging a piece costs about a twelfth of a half
+  // tile, and the first one six. (With the average and the longest unit for the time, 4000 causal rows of 16 heads were cut
+  // in two and took 116 us; whole, 77.)
   // (1000 and 670 rows behind 29,192 and 31,316 tokens, 16 heads: 112 units as long as 492 half tiles into 448, three rounds
   // of 152, 396 us; into pieces of a quarter of a CTA's share, 672 of them, 442 us.)
   if (n <= kFewRuns) {
@@ -753,23 +756,39 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mla_prefill_plan_kernel(const
     const long long r = static_cast<long long>(k - 15) * pl.sms / max(1ll, static_cast<long long>(n) * p.H);
     const int wanted = static_cast<int>(k < 16 ? k + 1 : max(1ll, min(r, 1ll << 20)));
     const int aim = max(1, (longest + wanted - 1) / wanted);
-    int units = 0, parts = 0, most_of = 0;
+    int parts = 0, most_of = 0;
     long long sum = 0;
     for (int i = lane; i < n; i += 32) {
       const int2 run = runs[i];
       const int len = piece_length(run.x, run.y, aim), count = max(1, (run.y + len - 1) / len);
-      units += count;
       parts += count > 1 ? count : 0;
       sum += run.x + 2 * (count - 1);
       most_of = max(most_of, (run.x - 2) / max(1, run.y) * min(len, run.y) + 2);
     }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    units = __reduce_add_sync(0xffffffffu, units);
     parts = __reduce_add_sync(0xffffffffu, parts);
     most_of = __reduce_max_sync(0xffffffffu, most_of);
-    const long long rounds = (static_cast<long long>(units) * p.H + pl.sms - 1) / pl.sms;
-    const long long time = min(rounds * most_of, sum * p.H / pl.sms + most_of) + static_cast<long long>(parts) * p.H / 12;
+    int at_least[8] = {};  // units of no less than an eighth, two, ... of the longest
+    for (int i = lane; i < n; i += 32) {
+      const int2 run = runs[i];
+      const int len = piece_length(run.x, run.y, aim), count = max(1, (run.y + len - 1) / len), each = (run.x - 2) / max(1, run.y);
+      const int full = each * len + 2, rest = each * (run.y - (count - 1) * len) + 2;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        at_least[j] += (8 * full >= (j + 1) * most_of ? count - 1 : 0) + (8 * rest >= (j + 1) * most_of ? 1 : 0);
+    }
+    int units = 0;  // lane j: of the j-th kind
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int all = __reduce_add_sync(0xffffffffu, at_least[j]);
+      if (lane == j) units = all;
+    }
+    // (a way that is weighed has at most 16 pieces a run, or 16 rounds of them: 31 bits hold units times heads)
+    const unsigned rounds = (static_cast<unsigned>(units) * p.H + pl.sms - 1) / static_cast<unsigned>(pl.sms);
+    const long long whole = static_cast<long long>(rounds) * (static_cast<long long>(lane + 1) * most_of / 8);
+    long long time = max(sum * p.H / pl.sms, static_cast<long long>(__reduce_max_sync(0xffffffffu, static_cast<int>(min(whole, 0x7fffffffll)))));
+    if (parts > 0) time += static_cast<long long>(parts) * p.H / 12 + 6;
     const bool fits = k == 0 || (aim >= kLeastPiece && parts <= pl.max_slots);
     if (lane == 0) {
       part[k] = fits ? time : 0x7fffffffffffffffll;
@@ -931,9 +950,10 @@ cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned bl
 int prefill_max_slots(int H, int sms) { return (4 * sms * 5 / 3) / H + 2; }
 int prefill_max_tiles(int B, int T) { return T / kUnitRows + B; }
 bool prefill_direct(int B, int T, int S) {
-  // planned in the kernel itself: few runs, and none that could be cut (300 rows, 16 heads: 13.0 us a call; with the
-  // planning kernel and a merge with nothing to do 23.8; 1000 rows: 23.5, 34.1)
-  return prefill_max_tiles(B, T) <= kDirect && 2 * ((S + kTile - 1) / kTile) + 2 <= kLeastPiece * 3 / 2;
+  // planned in the kernel itself: few runs, and none so long that cutting it would save the ten microseconds of the planning
+  // kernel and the merge (16 heads, planned here and there: 300 rows 13.0 and 23.8 us, 2000 rows 37.1 and 47.6, 16 rows
+  // behind 2100 tokens 31.8 and 41.4, 512 rows 40.5 and 37.6; behind 4000 tokens 53 to 66 and 34 to 43)
+  return prefill_max_tiles(B, T) <= kDirect && 2 * ((S + kTile - 1) / kTile) + 2 <= kDirectCost;
 }
 
 cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, const PrefillPlanParams& pl, bool bf16,
