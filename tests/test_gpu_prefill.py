@@ -129,6 +129,15 @@ def test_planned_and_cut_calls(new, ctx, H, dtype, causal):
 
 
 @pytest.mark.parametrize("new,ctx,H,dtype", [
+    ([4], [2176], 3, "f16"), ([900, 700], [900, 1276], 5, "bf16"), ([2176], [2176], 2, "bf16"), ([2177], [2177], 2, "f16"), ([1] * 50 + [200], [2] * 50 + [2000], 2, "bf16")])
+def test_longest_calls_that_plan_for_themselves(new, ctx, H, dtype):
+    case = Case(len(new) + sum(ctx), new, ctx, H, dtype, joint=True)
+    out, lse = case.run()
+    torch.cuda.synchronize()
+    case.check(out, lse, heads=[0, H - 1], rows=[0, 3, 127, 128, 199, 255, 256, 699, 899, 2047, 2048, 2175, 2176], requests=sorted({0, len(new) // 2, len(new) - 1}))
+
+
+@pytest.mark.parametrize("new,ctx,H,dtype", [
     ([1024], [5000], 24, "bf16"), ([1], [30000], 1, "f16"), ([600, 520, 1], [3000, 2500, 9000], 40, "f16"), ([512] * 6, [512, 900, 4000, 513, 2048, 6000], 16, "bf16"),
     ([1] * 2100 + [300], [20] * 2100 + [9000], 2, "f16"), ([1] * 2050 + [130], [3] * 2050 + [40000], 1, "bf16")])
 def test_ways_of_cutting(new, ctx, H, dtype):
