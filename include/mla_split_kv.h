@@ -945,7 +945,7 @@ typedef struct {
   const int32_t* cta_indptr;  /* DEVICE, as planned                           */
   int32_t num_units, num_slots, shared_parts, num_ctas; /* as planned         */
   void* workspace;            /* DEVICE, >= mla_decode_shared_workspace_bytes
-                                 bytes, 16-byte aligned; need not be cleared.
+                                 bytes, 32-byte aligned; need not be cleared.
                                  Calls sharing it must not overlap in time.    */
   uint64_t workspace_bytes;
   void* stream;               /* cudaStream_t                                 */

@@ -292,7 +292,8 @@ mla_status_t mla_decode_shared(const void* q_absorbed, const void* q_pe, const v
       !mla::is_aligned(block_table, 4) || !mla::is_aligned(context_lens, 4) || !mla::is_aligned(d->units, 16) ||
       !mla::is_aligned(d->own_indptr, 4) || !mla::is_aligned(d->cta_indptr, 4) || (out_lse != nullptr && !mla::is_aligned(out_lse, 4)))
     return reject(MLA_ERR_INVALID_ARG);
-  if (d->workspace == nullptr || !mla::is_aligned(d->workspace, 16) ||
+  // (partial outputs are stored 32 bytes at a time, at multiples of 32 from its start)
+  if (d->workspace == nullptr || !mla::is_aligned(d->workspace, 32) ||
       d->workspace_bytes < mla_decode_shared_workspace_bytes(d->num_slots))
     return reject(MLA_ERR_INVALID_ARG);
   const bool bf16 = d->dtype == MLA_BF16;
