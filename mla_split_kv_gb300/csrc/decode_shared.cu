@@ -249,7 +249,7 @@ __global__ void __maxnreg__(120)
         int pid = -1;
         if (lane < pages) {
           const int col = tok / p.bs + lane;
-          pid = col < columns ? __ldg(table + col) : -1;
+          pid = col < columns ? table[col] : -1;  // (no __ldg: the kernel before this one may write tables while this one waits)
           if (pid < 0 || pid >= p.num_blocks) {
             flag_error(MLA_DEVERR_BAD_PAGE);
             pid = -1;  // (lies before the cache: zeros)

@@ -640,8 +640,9 @@ __device__ __forceinline__ bool window_hides(const PartialParams& p, int32_t u, 
 
 // Page id of logical page `pg` of request b, with a range check: an entry
 // outside [0, num_blocks) is flagged and mapped to -1 (TMA then reads zeros).
+// (No __ldg: the kernel before a dependent launch may write tables while that one is resident and waits.)
 __device__ __forceinline__ int32_t checked_page(const PartialParams& p, int32_t b, int32_t pg) {
-  int32_t pid = __ldg(p.block_table + static_cast<long long>(b) * p.max_blocks + pg);
+  int32_t pid = p.block_table[static_cast<long long>(b) * p.max_blocks + pg];
   if (pid < 0 || pid >= p.num_blocks) {
     flag_error(MLA_DEVERR_BAD_PAGE);
     pid = -1;

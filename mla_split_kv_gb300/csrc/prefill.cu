@@ -196,12 +196,12 @@ __device__ __forceinline__ Unit unit_of(const PrefillParams& p, const Small* sm,
   Item it;
   const int at = u / p.H;
   if (p.items != nullptr) {
-    const int4 x = __ldg(reinterpret_cast<const int4*>(p.items) + 2 * at);
+    const int4 x = reinterpret_cast<const int4*>(p.items)[2 * at];  // (no __ldg: the list may be written while this kernel waits)
     it.b = x.x;
     it.q0 = x.y;
     it.j0 = x.z;
     it.j1 = x.w;
-    it.slot = __ldg(reinterpret_cast<const int*>(p.items) + 8 * at + 4);
+    it.slot = p.items[8 * at + 4];
   } else {
     const int4 x = sm->list[at];
     it.b = x.x;
@@ -885,7 +885,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) mla_prefill_merge_kernel(con
   const long long warps = static_cast<long long>(gridDim.x) * (kMergeThreads / 32);
   for (long long i = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5); i < total; i += warps) {
     const int h = static_cast<int>(i % p.H), r = static_cast<int>(i / p.H % kUnitRows);
-    const int4 e = __ldg(pl.merge + i / p.H / kUnitRows);
+    const int4 e = pl.merge[i / p.H / kUnitRows];
     if (r >= e.y) continue;
     const long long first = (static_cast<long long>(e.z) * kUnitRows + r) * p.H + h, stride = static_cast<long long>(kUnitRows) * p.H;
     // a group of pieces' values and, in as many lanes, their LSE; the first on its way while the maximum is found
