@@ -961,9 +961,11 @@ typedef struct {
  * to its own position when causal. A request may be shorter than P: its rows
  * then see its tokens of the common ones alone; of length 0, nothing: 0 and -inf.
  *
- * Tokens that a row does not see do not reach it, NaN among them or not. Pages:
- * as for mla_decode_partial (one outside the pool or the table reads zeros and
- * raises MLA_ERR_DEVICE_CHECK). The lengths are read on the device: a captured
+ * Tokens that a row does not see do not reach it, NaN among them or not. Those
+ * that it sees do as the formula says: an infinite latent whose score is -inf has
+ * weight 0, and makes its column NaN. (Where no score of a row is above -inf, the
+ * row gives 0 and -inf.) Pages: as for mla_decode_partial (one outside the pool or
+ * the table reads zeros and raises MLA_ERR_DEVICE_CHECK). The lengths are read on the device: a captured
  * call may be replayed as contexts grow.
  *
  * Precision: scores, maxima, sums and out_lse are fp32; the weights of the value

@@ -310,6 +310,7 @@ mla_status_t mla_decode_shared(const void* q_absorbed, const void* q_pe, const v
   mla::SharedParams p;
   p.q_abs = static_cast<const uint16_t*>(q_absorbed);
   p.q_pe = static_cast<const uint16_t*>(q_pe);
+  p.ckv = static_cast<const uint16_t*>(ckv_cache);
   p.shared_table = shared_table;
   p.block_table = block_table;
   p.context_lens = context_lens;

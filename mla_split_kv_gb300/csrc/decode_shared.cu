@@ -30,8 +30,9 @@
 // below fp32's end. Sums are of the unrounded weights, in fp32; the
 // weights are rounded once to the cache's type (2^-12 of themselves in fp16, 2^-9 in bf16: as the 16-bit output).
 // Tokens that some row of a group does not see (behind a shorter context or, in a window, behind the row) have weight 0
-// there, and values that are not finite are taken out of such tiles: for a row that does see one of them its score has
-// already made the weight so.
+// there, and values that are not finite are taken out of such tiles. For a row that does see one of them its score is not
+// finite either: a weight that is NaN, which makes all of the row so, or, with a score of -inf, one of 0, which times the
+// value is NaN in that column: there the CTA writes NaN at its end (Small::dirty), as the product does in other tiles.
 //
 // Units are shared out by the host plan (plan_shared.cpp). The merge is a kernel of its own.
 //
@@ -71,9 +72,12 @@ static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemP = 320, kTmemQ = 352;
 static_assert(kTmemQ + 32 * kQTmemBlocks == 512, "tensor memory's columns");
 
+constexpr float kLowest = -3.402823466e38f;  // LSE of a part that has no score above -inf
+
 struct Small {
   uint64_t a_full[2], a_empty[2], b_full[4], b_empty[kRingB], q_full, q_empty, s_full, s_empty, s_issued[2], p_full, pv_done, stat_full[2], o_empty, drain[2];
   float inv[2][kRows];  // 1 / sum, of the units in turn
+  int32_t dirty;        // a value that some row sees was taken out of a tile
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -161,9 +165,10 @@ __device__ __forceinline__ bool unit_of(const SharedParams& p, int k, int lane, 
   return true;
 }
 
-// Values that are not finite in the unit's pieces of a tile (two of [64 tokens x 128 columns]) become 0.
+// Values that are not finite in the unit's pieces of a tile (two of [64 tokens x 128 columns], eight tokens' rows of 64
+// columns beside the same tokens' next 64) become 0; *dirty is set where one of them belongs to a token before `seen`.
 template <bool BF16>
-__device__ __forceinline__ void clean_values(uint8_t* p0, uint8_t* p1, int r) {
+__device__ __forceinline__ void clean_values(uint8_t* p0, uint8_t* p1, int r, int tok0, int seen, volatile int32_t* dirty) {
   constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
 #pragma unroll 4
   for (int it = 0; it < 16; ++it) {
@@ -180,7 +185,38 @@ __device__ __forceinline__ void clean_values(uint8_t* p0, uint8_t* p1, int r) {
         if ((w[j] & kExp) == kExp) w[j] &= 0xffff0000u;
         if ((w[j] & (kExp << 16)) == (kExp << 16)) w[j] &= 0xffffu;
       }
+      if (tok0 + ((idx & 1023) >> 7) * 8 + ((idx & 63) >> 3) < seen) *dirty = 1;
       sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+  }
+}
+
+// Of a unit whose partial output this warp has written (rows from row0 on), the columns in which a row sees a value that was
+// taken out of a masked tile become NaN: a token a round, eight columns a lane.
+template <bool BF16>
+__device__ __forceinline__ void spoil_output(const SharedParams& p, const Unit& w, int lane, int row0) {
+  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+  const int32_t* const table = w.request < 0 ? p.shared_table : p.block_table + static_cast<long long>(w.request) * p.max_blocks;
+  const int columns = w.request < 0 ? p.shared_tokens / p.bs : p.max_blocks;
+  const int sees = row0 + lane < w.rows ? min(visible(p, w.row0 + row0 + lane), w.t1) : 0;
+  const int most = __reduce_max_sync(0xffffffffu, sees);
+  float* const out = p.part_o + (static_cast<long long>(w.slot) * kRows + row0) * kRank + kHalf * w.half + 8 * lane;
+  __syncwarp();  // behind the rows' stores by other lanes
+  for (int t = w.t0 + max(0, w.least - w.t0) / kT * kT; t < most; ++t) {
+    const int col = t / p.bs, pid = col < columns ? table[col] : -1;
+    if (pid < 0 || pid >= p.num_blocks) continue;  // (zeros)
+    const uint16_t* const from = p.ckv + (static_cast<long long>(pid) * p.bs + t % p.bs) * kRank + kHalf * w.half + 8 * lane;
+    const uint4 v = *reinterpret_cast<const uint4*>(from);
+    const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+    uint32_t bad = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bad |= ((word[j / 2] >> (16 * (j & 1)) & kExp) == kExp ? 1u : 0u) << j;
+    if (!__any_sync(0xffffffffu, bad != 0)) continue;
+    for (int r = 0; r < 32; ++r) {
+      if (__shfl_sync(0xffffffffu, sees, r) <= t) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (bad >> j & 1) out[static_cast<long long>(r) * kRank + j] = __int_as_float(0x7fffffff);
     }
   }
 }
@@ -189,7 +225,7 @@ __device__ __forceinline__ void clean_values(uint8_t* p0, uint8_t* p1, int r) {
 template <bool BF16>
 __global__ void __maxnreg__(120)
     mla_decode_shared_kernel(const __grid_constant__ CUtensorMap tm_half, const __grid_constant__ CUtensorMap tm_piece,
-                             const __grid_constant__ CUtensorMap tm_kpe, const SharedParams p) {
+                             const __grid_constant__ CUtensorMap tm_kpe, const __grid_constant__ SharedParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = align1024(smem_raw);
   Small* const sm = reinterpret_cast<Small*>(smem + kOffSmall);
@@ -219,6 +255,7 @@ __global__ void __maxnreg__(120)
     mbar_init(&sm->drain[0], 1);
     mbar_init(&sm->drain[1], 1);
     sm->abort_flag = 0;
+    sm->dirty = 0;
     fence_mbar_init();
   }
   if (warp == kScoreWarp) {
@@ -481,7 +518,7 @@ __global__ void __maxnreg__(120)
           const uint32_t b = 2 * t, c = b + 1;
           ok = mbar_wait_warp(&sm->b_full[t & 3], (t >> 2) & 1, tmo);
           if (!ok) break;
-          clean_values<BF16>(smem + kOffB + (b % kRingB) * kPiece, smem + kOffB + (c % kRingB) * kPiece, r);
+          clean_values<BF16>(smem + kOffB + (b % kRingB) * kPiece, smem + kOffB + (c % kRingB) * kPiece, r, tok, w.t1, &sm->dirty);
           fence_proxy_async_smem();
         }
 #pragma unroll
@@ -501,7 +538,8 @@ __global__ void __maxnreg__(120)
       sm->inv[unit & 1][r] = any ? 1.f / l : 0.f;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->stat_full[unit & 1]);
-      if (real && w.half == 0) p.part_lse[slot_row] = any ? m + log2f(l) : (l != l ? l : -INFINITY);
+      // (-inf is for what was not written: a part whose scores are all -inf counts with weight 0, its NaN among its values)
+      if (real && w.half == 0) p.part_lse[slot_row] = any ? m + log2f(l) : (l != l ? l : kLowest);
       ++unit;
       tile0 += w.tiles;
     }
@@ -620,6 +658,10 @@ __global__ void __maxnreg__(120)
       ++unit;
     }
     if (ok && unit > 0) output(std::true_type{});
+    if (__builtin_expect(ok && *const_cast<volatile int32_t*>(&sm->dirty) != 0, 0)) {
+      for (int k = 0; unit_of(p, k, lane, w); ++k)
+        if (w.tiles > 0) spoil_output<BF16>(p, w, lane, 32 * (warp & 3));
+    }
     tc_fence_before();
     if (!ok) *abort_flag = 1;
   }
@@ -675,7 +717,8 @@ __global__ void __launch_bounds__(kMergeThreads, 6) mla_decode_shared_merge_kern
 #pragma unroll
   for (int c = 0; c < kCols; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
-  if (M != -INFINITY) {
+  const bool none = M <= kLowest;  // no score above -inf
+  if (!none) {
     for (int j0 = 0; j0 < n; j0 += kMergeDepth) {
       if (j0 > 0) load(j0);
       const float w = lse == -INFINITY ? -1.f : exp2f(lse - M);
@@ -698,7 +741,7 @@ __global__ void __launch_bounds__(kMergeThreads, 6) mla_decode_shared_merge_kern
   }
 #pragma unroll
   for (int c = 0; c < kCols; ++c) store_out4(p.out, p.out_dtype, static_cast<long long>(row) * kRank + col + 128 * c, acc[c]);
-  if (lane == 0 && warp % kSplit == 0 && p.out_lse != nullptr) p.out_lse[row] = merged_lse(M, den);
+  if (lane == 0 && warp % kSplit == 0 && p.out_lse != nullptr) p.out_lse[row] = none ? -INFINITY : merged_lse(M, den);
 }
 
 cudaError_t launch_dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, unsigned grid, unsigned block, size_t smem,

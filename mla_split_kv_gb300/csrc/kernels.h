@@ -295,6 +295,7 @@ cudaError_t prefill_read_clear_error(uint32_t* out);
 struct SharedParams {
   const uint16_t* q_abs;       // [rows, 512]
   const uint16_t* q_pe;        // [rows, 64]
+  const uint16_t* ckv;         // [num_blocks, bs, 512]
   const int32_t* shared_table; // [shared_tokens / bs]
   const int32_t* block_table;  // [B, max_blocks]
   const int32_t* context_lens; // [B]
