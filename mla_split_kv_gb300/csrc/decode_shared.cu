@@ -11,7 +11,7 @@
 // one half of the value columns (O for all 512 would fill tensor memory), so that CTAs share nothing and wait for
 // none. Tiles of 64 tokens; a unit's tensor memory: O [128 x 256] fp32, S [128 x 64] fp32, the weights [128 x 64] in 16
 // bits as the value product's A operand, and 320 of the 576 query columns as the score product's (the other 256 are in
-// shared memory, 64 KB: a product that reads A there takes 49 cycles in place of 33). The products go
+// shared memory, 64 KB; with two terms 256 and 320: a product that reads A there takes 49 cycles in place of 33). The products go
 //   S(i+1) PV(i) S(i+2) PV(i+1) ...
 // each issued by a warp of its own, PV(i) only behind S(i+1): S(i+1) is read out of its one buffer beside PV(i), and
 // S(i)'s softmax runs beside PV(i-1) and S(i+1). (With PV(i) as soon as its weights are there it ran in the middle of
@@ -27,8 +27,11 @@
 // The running maximum moves only when a tile's passes it by more than 2^15 (fp16, the room its weights have above 1) or
 // 2^30 (bf16), since with it all of O moves, for some row of a warp every few tiles. 64 requests, 32,768 common tokens,
 // bf16, random latents: 116 us with 2^15, 109 with 2^20, 98 with 2^30 and with 2^60, which would leave values less room
-// below fp32's end. Sums are of the unrounded weights, in fp32; the
-// weights are rounded once to the cache's type (2^-12 of themselves in fp16, 2^-9 in bf16: as the 16-bit output).
+// below fp32's end. Sums are of the unrounded weights, in fp32; the weights are rounded once to the cache's type (by half a
+// step: 2^-11 of themselves in fp16, 2^-8 in bf16), as a 16-bit output is. Beside fp32 outputs a bf16 weight is two terms,
+// 2^-16 of itself (kTwo): rounded once, it leaves 0.7e-3 to 1.5e-3 of an output, where fp32 results are to keep 1e-3. The
+// second term is a second value product over the same tile (captured: 64 requests as above 130 us, 98 with 16-bit outputs; 24
+// requests of 2 x 128 rows, 8192 common tokens 179 and 132), with 16 KB less of the ring and 64 fewer query columns in tensor memory.
 // Tokens that some row of a group does not see (behind a shorter context or, in a window, behind the row) have weight 0
 // there, and values that are not finite are taken out of such tiles. For a row that does see one of them its score is not
 // finite either: a weight that is NaN, which makes all of the row so, or, with a score of -inf, one of 0, which times the
@@ -54,28 +57,34 @@ constexpr int kOther = kT * kHalf * 2;    // 32 KB: the other half of a tile's l
 constexpr int kPe = kT * kRope * 2;       // 8 KB
 constexpr int kSlotA = kOther + kPe;
 constexpr int kPiece = kT * 128 * 2;      // 16 KB: 128 of the unit's own columns
-constexpr int kRingB = 5;
 constexpr int kQChunk = kRows * 128;      // 16 KB: [128 rows x 64 columns]
-constexpr int kQTmemBlocks = 5;           // blocks of 64 query columns in tensor memory; the last three and the rotary one are not
-constexpr int kQSmemChunks = kRank / kBoxCols - kQTmemBlocks + 1;
 constexpr int kScoreWarp = 4, kLoadWarpA = 5, kValueWarp = 6, kLoadWarpB = 7;
 constexpr int kThreads = 384;
 // Registers: launched with 120 a thread.
 constexpr int kSoftmaxRegs = 168, kIssueRegs = 64, kAuxRegs = 128;
 static_assert(kSoftmaxRegs + kIssueRegs + kAuxRegs <= 3 * 120, "what the block was launched with");
-constexpr uint32_t kOffA = kQSmemChunks * kQChunk;
-constexpr uint32_t kOffB = kOffA + 2 * kSlotA;
-constexpr uint32_t kOffSmall = kOffB + kRingB * kPiece;
 constexpr uint32_t kSmallBytes = 2048;
-constexpr uint32_t kSmem = kOffSmall + kSmallBytes + 1024;
-static_assert(kSmem <= 232448, "shared memory per CTA");
-constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemP = 320, kTmemQ = 352;
-static_assert(kTmemQ + 32 * kQTmemBlocks == 512, "tensor memory's columns");
+// Where things lie. With the weights as two terms (kTwo) their second 32 columns of tensor memory come from the queries', whose
+// place in shared memory comes from the ring.
+template <bool kTwo>
+struct Shape {
+  static constexpr int kRingB = kTwo ? 4 : 5;
+  static constexpr int kQTmemBlocks = kTwo ? 4 : 5;  // blocks of 64 query columns in tensor memory; the others and the rotary one are not
+  static constexpr int kQSmemChunks = kRank / kBoxCols - kQTmemBlocks + 1;
+  static constexpr uint32_t kOffA = kQSmemChunks * kQChunk;
+  static constexpr uint32_t kOffB = kOffA + 2 * kSlotA;
+  static constexpr uint32_t kOffSmall = kOffB + kRingB * kPiece;
+  static constexpr uint32_t kSmem = kOffSmall + kSmallBytes + 1024;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+  static constexpr uint32_t kTmemQ = kTwo ? 384 : 352;
+  static_assert(kTmemQ + 32 * kQTmemBlocks == 512, "tensor memory's columns");
+};
+constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemP = 320, kTmemLow = 352;
 
 constexpr float kLowest = -3.402823466e38f;  // LSE of a part that has no score above -inf
 
 struct Small {
-  uint64_t a_full[2], a_empty[2], b_full[4], b_empty[kRingB], q_full, q_empty, s_full, s_empty, s_issued[2], p_full, pv_done, stat_full[2], o_empty, drain[2];
+  uint64_t a_full[2], a_empty[2], b_full[4], b_empty[5], q_full, q_empty, s_full, s_empty, s_issued[2], p_full, pv_done, stat_full[2], o_empty, drain[2];
   float inv[2][kRows];  // 1 / sum, of the units in turn
   int32_t dirty;        // a value that some row sees was taken out of a tile
   uint32_t tmem_base;
@@ -222,13 +231,17 @@ __device__ __forceinline__ void spoil_output(const SharedParams& p, const Unit& 
 }
 
 // 120 registers a thread at launch: a CTA of the merge then fits on an SM beside this kernel's one and waits there.
-template <bool BF16>
+// kTwo (bf16): the weights as two terms.
+template <bool BF16, bool kTwo>
 __global__ void __maxnreg__(120)
     mla_decode_shared_kernel(const __grid_constant__ CUtensorMap tm_half, const __grid_constant__ CUtensorMap tm_piece,
                              const __grid_constant__ CUtensorMap tm_kpe, const __grid_constant__ SharedParams p) {
+  using Place = Shape<kTwo>;
+  constexpr int kRingB = Place::kRingB, kQTmemBlocks = Place::kQTmemBlocks, kQSmemChunks = Place::kQSmemChunks;
+  constexpr uint32_t kOffA = Place::kOffA, kOffB = Place::kOffB, kTmemQ = Place::kTmemQ;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = align1024(smem_raw);
-  Small* const sm = reinterpret_cast<Small*>(smem + kOffSmall);
+  Small* const sm = reinterpret_cast<Small*>(smem + Place::kOffSmall);
   volatile int32_t* const abort_flag = &sm->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -408,6 +421,11 @@ __global__ void __maxnreg__(120)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             issue_ts(leader, tmem + kTmemO + 128 * x, tmem + kTmemP + 8 * kk, v0 + b * (kPiece / 16) + kk * 256, idesc, i > 0 || kk > 0);
+          if constexpr (kTwo) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              issue_ts(leader, tmem + kTmemO + 128 * x, tmem + kTmemLow + 8 * kk, v0 + b * (kPiece / 16) + kk * 256, idesc, 1);
+          }
           if (x == 0) issue_commit(leader, &sm->b_empty[b]);
         }
         issue_commit(leader, &sm->pv_done);
@@ -479,7 +497,7 @@ __global__ void __maxnreg__(120)
         const float mm = m_new == -INFINITY ? 0.f : -m_new;
         const float2 f2 = make_float2(f, f), m2 = make_float2(mm, mm);
         float2 sum = make_float2(0.f, 0.f), sum_b = sum;
-        uint32_t h[kT / 2];
+        uint32_t h[kT / 2], low[kTwo ? kT / 2 : 1];
 #pragma unroll
         for (int j = 0; j < kT / 2; ++j) {
           float2 e = fma2(make_float2(x[2 * j], x[2 * j + 1]), f2, m2);
@@ -488,6 +506,7 @@ __global__ void __maxnreg__(120)
           if (j & 1) sum_b = add2(sum_b, e);
           else sum = add2(sum, e);
           h[j] = pack2<BF16>(e.x, e.y);
+          if constexpr (kTwo) low[j] = pack2<BF16>(e.x - __uint_as_float(h[j] << 16), e.y - __uint_as_float(h[j] & 0xffff0000u));
         }
         sum = add2(sum, sum_b);
         if (t > 0) {  // the weights' buffer, and (but for a unit's first tile) O, are free
@@ -527,6 +546,11 @@ __global__ void __maxnreg__(120)
 #pragma unroll
           for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(h[16 * j + c]);
           tmem_st16(tmem + lanes + kTmemP + 16 * j, v);
+          if constexpr (kTwo) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(low[16 * j + c]);
+            tmem_st16(tmem + lanes + kTmemLow + 16 * j, v);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -758,21 +782,31 @@ cudaError_t launch_dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr,
   return cudaSuccess;
 }
 
-}  // namespace
-
-cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& tm_piece, const CUtensorMap& tm_kpe,
-                                 const SharedParams& p, bool bf16, cudaStream_t stream) {
-  static DeviceOnce once_f16, once_bf16;
-  const void* const fn = bf16 ? reinterpret_cast<const void*>(&mla_decode_shared_kernel<true>)
-                              : reinterpret_cast<const void*>(&mla_decode_shared_kernel<false>);
-  cudaError_t e = set_attribute_once(bf16 ? once_bf16 : once_f16, fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+template <bool BF16, bool kTwo>
+cudaError_t launch_units(const CUtensorMap& tm_half, const CUtensorMap& tm_piece, const CUtensorMap& tm_kpe, const SharedParams& p,
+                         cudaStream_t stream) {
+  static DeviceOnce once;
+  constexpr uint32_t kSmem = Shape<kTwo>::kSmem;
+  const cudaError_t e = set_attribute_once(once, reinterpret_cast<const void*>(&mla_decode_shared_kernel<BF16, kTwo>),
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   launch_dependent(cfg, attr, p.num_ctas, kThreads, kSmem, stream);
-  e = bf16 ? cudaLaunchKernelEx(&cfg, mla_decode_shared_kernel<true>, tm_half, tm_piece, tm_kpe, p)
-           : cudaLaunchKernelEx(&cfg, mla_decode_shared_kernel<false>, tm_half, tm_piece, tm_kpe, p);
+  return cudaLaunchKernelEx(&cfg, mla_decode_shared_kernel<BF16, kTwo>, tm_half, tm_piece, tm_kpe, p);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& tm_piece, const CUtensorMap& tm_kpe,
+                                 const SharedParams& p, bool bf16, cudaStream_t stream) {
+  // (fp32 outputs of bf16 caches: the weights as two terms)
+  const cudaError_t e = !bf16                ? launch_units<false, false>(tm_half, tm_piece, tm_kpe, p, stream)
+                        : p.out_dtype == 2 ? launch_units<true, true>(tm_half, tm_piece, tm_kpe, p, stream)
+                                           : launch_units<true, false>(tm_half, tm_piece, tm_kpe, p, stream);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
   if (p.rows <= kMergeFewRows) {
     launch_dependent(cfg, attr, p.rows, kMergeThreads, 0, stream);
     return cudaLaunchKernelEx(&cfg, mla_decode_shared_merge_kernel<4>, p);
