@@ -847,10 +847,10 @@ typedef struct {
  *   s_t  = scale * (q_nope[i,h,:] . k_nope[t,h,:] + q_pe[i,h,:] . k_pe[t,:])
  *   out[i,h,:]   = sum_t softmax(s)_t v[t,h,:]     (rounded once)
  *   out_lse[i,h] = log2 sum_t exp(s_t)
- * over the tokens that the row sees. A row that sees none (n > L) gives 0 and
- * -inf. Tokens that a row does not see do not reach it, NaN and infinities
- * among them or not; nor does what the tensors hold behind the last request.
- * Rows of out and out_lse behind the last request stay as they were.
+ * over the tokens that the row sees. A row that sees none (n > L), or whose every
+ * score is -inf, gives 0 and -inf. Tokens that a row does not see do not reach it,
+ * NaN and infinities among them or not; nor does what the tensors hold behind the
+ * last request. Rows of out and out_lse behind it stay as they were.
  *
  * The work is shared out on the device from the offsets as they are when the
  * call runs: no host plan, and a captured call may be replayed with others (the

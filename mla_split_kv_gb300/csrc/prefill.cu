@@ -618,7 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool any = nt > 0 && m != -INFINITY;
         const float inv = any ? 1.f / l : 0.f;
         const float lse = any ? m + log2f(l) : (l != l ? l : -INFINITY);  // (every score NaN: no maximum)
-        const bool dirty = nt > 0 && *const_cast<volatile int32_t*>(&sm->dirty[k & 7]) == k + 1;
+        // (a piece without a score above -inf counts with weight 0 in the merge, and its infinite values are NaN there)
+        const bool counts = any || (nt > 0 && w.slot >= 0);
+        const bool dirty = counts && *const_cast<volatile int32_t*>(&sm->dirty[k & 7]) == k + 1;
         // the tiles that were searched, of either subtile, as far as this row sees
         const int first = max(w.j0 * kTile, visible(p, w.n, w.L, w.q0) / kTile * kTile);
         const int last = min(seen, (w.j0 + nt) * kTile);
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = any ? o[j] * inv : (l != l ? l : 0.f);
+          for (int j = 0; j < 32; ++j) o[j] = counts ? o[j] * inv : (l != l ? l : 0.f);
           if (__builtin_expect(dirty, 0)) {
             // values that are not finite were taken out of the searched tiles: those that this row sees belong to its sum
             // (weights are positive; infinities of both signs, or a NaN, give NaN)
