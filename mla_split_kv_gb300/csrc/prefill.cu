@@ -620,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lse = any ? m + log2f(l) : (l != l ? l : -INFINITY);  // (every score NaN: no maximum)
         // (a piece without a score above -inf counts with weight 0 in the merge, and its infinite values are NaN there)
         const bool counts = any || (nt > 0 && w.slot >= 0);
-        const bool dirty = counts && *const_cast<volatile int32_t*>(&sm->dirty[k & 7]) == k + 1;
+        // (a later unit's mark, from a subtile that is eight units ahead, may lie over this one's: looked for in vain at worst)
+        const bool dirty = counts && *const_cast<volatile int32_t*>(&sm->dirty[k & 7]) > k;
         // the tiles that were searched, of either subtile, as far as this row sees
         const int first = max(w.j0 * kTile, visible(p, w.n, w.L, w.q0) / kTile * kTile);
         const int last = min(seen, (w.j0 + nt) * kTile);
