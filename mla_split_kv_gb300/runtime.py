@@ -530,19 +530,23 @@ class Step:
     served: torch.Tensor        # int32 [1]
 
 
-def alloc_step(num_requests: int, capacity: int, device="cuda") -> Step:
-    """Buffers of steps of num_requests requests and at most `capacity` new tokens."""
+def alloc_step(num_requests: int, capacity: int, device="cuda", pool: Optional[PagePool] = None) -> Step:
+    """Buffers of steps of num_requests requests, all without tokens, and at most `capacity` new tokens. With a pool,
+    steps count its free pages in place, as a loop of them has to: update_tables reads pool.count. Without one, a
+    step's free_count is a tensor of its own, which the caller copies to pool.count before the next step."""
+    if pool is not None:
+        device = pool.count.device
     i32 = dict(dtype=torch.int32, device=device)
-    return Step(torch.zeros(num_requests, **i32), torch.zeros(1, **i32), torch.zeros(num_requests + 1, **i32),
+    return Step(torch.zeros(num_requests, **i32), pool.count if pool is not None else torch.zeros(1, **i32), torch.zeros(num_requests + 1, **i32),
                 torch.zeros(num_requests + 1, **i32), torch.zeros(capacity, dtype=torch.int64, device=device),
                 torch.zeros(1, **i32))
 
 
 def update_tables(pool: PagePool, changes: torch.Tensor, context_lens: torch.Tensor, block_table: torch.Tensor,
                   step: Step, stream: Optional[torch.cuda.Stream] = None) -> Step:
-    """One step's tables (mla_update_tables): block_table and pool.pages in place, the rest into `step`, whose
-    context_lens and free_count are the next step's (they may be the tensors of this one: context_lens itself,
-    pool.count)."""
+    """One step's tables (mla_update_tables): block_table and pool.pages in place, the rest into `step`. Its
+    context_lens and free_count are what the next step starts from, as context_lens and pool.count: give it
+    step.context_lens as context_lens and a step that alloc_step has made with the pool, or copy both."""
     dev = _device_of(pool.pages)
     B, width, capacity = changes.shape[0], block_table.shape[-1], step.slots.shape[0]
     _expect(changes, (B,), torch.int32, "changes", dev)
