@@ -770,7 +770,8 @@ mla_status_t mla_update_tables(const int32_t* changes, const int32_t* context_le
  * kpe_new : device, its 64 at i * kpe_stride; both 16-byte aligned, strides
  *           multiples of 8 of at least 512 and 64 (576 for both: the two parts
  *           of one projection's output)
- * slots   : device [num_tokens]
+ * slots   : device [num_tokens]; num_tokens >= 1 (a step without new tokens needs
+ *           no call)
  * A programmatic dependent launch, as mla_cache_append.
  */
 mla_status_t mla_cache_append_slots(const void* ckv_new, int64_t ckv_stride, const void* kpe_new, int64_t kpe_stride,
@@ -826,8 +827,8 @@ typedef struct {
                                  output                                       */
   int32_t causal;             /* 1: row i of a request's n sees its tokens
                                  t <= L - n + i; 0: all L of them             */
-  int32_t max_q_tokens;       /* T: rows that q_nope, q_pe, out hold          */
-  int32_t max_kv_tokens;      /* S: rows that k_nope, k_pe, v hold            */
+  int32_t max_q_tokens;       /* T: rows that q_nope, q_pe, out hold, >= 1     */
+  int32_t max_kv_tokens;      /* S: rows that k_nope, k_pe, v hold, >= 1       */
   int64_t q_nope_stride[2];   /* elements from row to row and from head to
                                  head, multiples of 8 (dense: H * 128, 128;
                                  of one [T, H, 192] tensor: H * 192, 192)     */

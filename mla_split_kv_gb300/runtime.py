@@ -577,7 +577,7 @@ def _expect_rows(t: torch.Tensor, shape, dtype, what: str, dev: int) -> None:
 def cache_append_slots(ckv: torch.Tensor, kpe: torch.Tensor, ckv_new: torch.Tensor, kpe_new: torch.Tensor,
                        slots: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Write packed tokens [T, 512 / 64] (rows of any stride) into the cache rows that `slots` names
-    (mla_cache_append_slots); T may be less than what slots holds."""
+    (mla_cache_append_slots); T may be less than what slots holds, and 0: a step without new tokens launches nothing."""
     dev = _device_of(ckv)
     nblk, bs, T = ckv.shape[0], ckv.shape[1], ckv_new.shape[0]
     if ckv.dtype not in (torch.float16, torch.bfloat16):
@@ -589,6 +589,8 @@ def cache_append_slots(ckv: torch.Tensor, kpe: torch.Tensor, ckv_new: torch.Tens
     if slots.dim() != 1 or slots.shape[0] < T:
         raise ValueError(f"slots: {tuple(slots.shape)} for {T} tokens")
     _expect(slots, (slots.shape[0],), torch.int64, "slots", dev)
+    if T == 0:
+        return
     raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
     nb.mla_cache_append_slots(ckv_new.data_ptr(), _row_stride(ckv_new), kpe_new.data_ptr(), _row_stride(kpe_new),
                               slots.data_ptr(), T, bs, nblk, ckv.data_ptr(), kpe.data_ptr(), raw_stream)
@@ -608,7 +610,8 @@ def expand_kv(ckv: torch.Tensor, kpe: torch.Tensor, block_table: torch.Tensor, k
               w_uk: torch.Tensor, w_uv_t: torch.Tensor, k_nope: torch.Tensor, v: torch.Tensor, k_pe: torch.Tensor,
               stream: Optional[torch.cuda.Stream] = None) -> None:
     """Every head's keys and values [S, H, 128] and the rotary keys [S, 64] of the requests' cached tokens, packed by
-    kv_indptr (mla_expand_kv); the outputs may hold more rows than there are tokens."""
+    kv_indptr (mla_expand_kv); the outputs may hold more rows than there are tokens. Outputs of no rows: nothing is
+    launched."""
     dev = _device_of(ckv)
     nblk, bs, width, B, H, S = ckv.shape[0], ckv.shape[1], block_table.shape[-1], kv_indptr.shape[0] - 1, w_uk.shape[0], v.shape[0]
     dtype = ckv.dtype
@@ -623,6 +626,8 @@ def expand_kv(ckv: torch.Tensor, kpe: torch.Tensor, block_table: torch.Tensor, k
     _expect(k_nope, (S, H, 128), dtype, "k_nope", dev)
     _expect(v, (S, H, 128), dtype, "v", dev)
     _expect(k_pe, (S, 64), dtype, "k_pe", dev)
+    if S == 0:
+        return
     raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
     d = nb.mla_expand_desc_t(B, H, bs, nblk, width, CODE_OF[dtype], S, raw_stream)
     nb.mla_expand_kv(ckv.data_ptr(), kpe.data_ptr(), block_table.data_ptr(), kv_indptr.data_ptr(), w_uk.data_ptr(),
@@ -655,7 +660,7 @@ def prefill(plan: PrefillPlan, q_nope: torch.Tensor, q_pe: torch.Tensor, k_nope:
             out_lse: Optional[torch.Tensor] = None, causal: bool = True,
             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Attention of packed prompts over expanded keys and values (mla_prefill), into out [T, H, 128]. q_nope [T, H,
-    128] and q_pe [T, H, 64] may be views of one [T, H, 192] tensor."""
+    128] and q_pe [T, H, 64] may be views of one [T, H, 192] tensor. T = 0, a step without prompts: nothing is launched."""
     dev = _device_of(plan.workspace)
     T, H, S, B = q_nope.shape[0], plan.num_heads, v.shape[0], q_indptr.shape[0] - 1
     if B > plan.num_requests or T > plan.max_q_tokens:
@@ -673,6 +678,8 @@ def prefill(plan: PrefillPlan, q_nope: torch.Tensor, q_pe: torch.Tensor, k_nope:
     _expect(out, (T, H, 128), dtype, "out", dev)
     if out_lse is not None:
         _expect(out_lse, (T, H), torch.float32, "out_lse", dev)
+    if T == 0:
+        return out
     raw_stream = stream.cuda_stream if stream is not None else _current_stream(dev)
     d = nb.mla_prefill_desc_t(B, H, CODE_OF[dtype], 1 if causal else 0, T, S, _strides(q_nope), _strides(q_pe),
                               plan.workspace.data_ptr(), plan.workspace.numel(), raw_stream)
