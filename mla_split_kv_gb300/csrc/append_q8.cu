@@ -223,11 +223,6 @@ cudaError_t launch_append_q8(const AppendQ8Params& p, bool bf16, cudaStream_t st
               : cudaLaunchKernelEx(&cfg, mla_append_q8_kernel<false>, p, per_request, subs);
 }
 
-cudaError_t append_q8_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t append_q8_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

@@ -1000,11 +1000,6 @@ cudaError_t launch_decode_q8(const CUtensorMap& tm_ckv, const CUtensorMap& tm_kp
   return cudaLaunchKernelEx(&cfg, p.cuts_by_request ? mla_merge_q8_parts_kernel : mla_merge_q8_rows_kernel, p);
 }
 
-cudaError_t decode_q8_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t decode_q8_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

@@ -815,11 +815,6 @@ cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& 
   return cudaLaunchKernelEx(&cfg, mla_decode_shared_merge_kernel<1>, p);
 }
 
-cudaError_t decode_shared_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t decode_shared_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

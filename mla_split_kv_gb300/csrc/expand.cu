@@ -465,11 +465,6 @@ cudaError_t launch_expand_kv(const CUtensorMap& tm_ckv, const CUtensorMap& tm_uk
   return bf16 ? launch<true>(cfg, tm_ckv, tm_uk, tm_uv, tm_k, tm_v, p) : launch<false>(cfg, tm_ckv, tm_uk, tm_uv, tm_k, tm_v, p);
 }
 
-cudaError_t expand_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t expand_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

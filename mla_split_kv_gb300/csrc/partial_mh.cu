@@ -842,11 +842,6 @@ cudaError_t launch_partial_mh(const CUtensorMap& tm_pages, const CUtensorMap& tm
              : launch_mh_dtype<false, false>(cfg, tm_pages, tm_kpe_half, p, bf16);
 }
 
-cudaError_t mh_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t mh_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

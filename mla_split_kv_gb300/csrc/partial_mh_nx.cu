@@ -600,11 +600,6 @@ cudaError_t launch_partial_mh_nx(const CUtensorMap& tm_pages, const CUtensorMap&
   return bf16 ? launch_nx<true, false>(cfg, tm_pages, tm_kpe_half, p) : launch_nx<false, false>(cfg, tm_pages, tm_kpe_half, p);
 }
 
-cudaError_t mh_nx_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t mh_nx_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

@@ -280,11 +280,6 @@ cudaError_t launch_partial_simt(const CUtensorMap& tm_ckv, const CUtensorMap& tm
   return cudaLaunchKernelEx(&cfg, mla_partial_simt_kernel<false>, tm_ckv, tm_kpe, p);
 }
 
-cudaError_t simt_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t simt_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

@@ -1180,11 +1180,6 @@ int tc128_max_active_clusters(int cluster) {
   return n;
 }
 
-cudaError_t tc128_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t tc128_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

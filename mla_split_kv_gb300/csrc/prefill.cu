@@ -981,11 +981,6 @@ cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, cons
   return launch_dependent(mla_prefill_merge_kernel, static_cast<unsigned>(4 * sms), kMergeThreads, 0, stream, p, pl, bf16 ? 1 : 0);
 }
 
-cudaError_t prefill_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t prefill_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

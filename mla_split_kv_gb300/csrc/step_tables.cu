@@ -332,11 +332,6 @@ cudaError_t launch_append_slots(const AppendSlotsParams& p, cudaStream_t stream)
   return launch_dependent(mla_cache_append_slots_kernel, grid, kCopyWarps * 32, 0, p, stream);
 }
 
-cudaError_t step_tables_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t step_tables_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla

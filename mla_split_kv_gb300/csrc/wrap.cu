@@ -336,11 +336,6 @@ cudaError_t launch_merge_unembed(const UnembedParams& p, bool w_bf16, cudaStream
   }
 }
 
-cudaError_t wrap_read_clear_error(uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_device_error, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(uint32_t));
-}
+cudaError_t wrap_read_clear_error(uint32_t* out) { return read_clear_device_error(out); }
 
 }  // namespace mla
