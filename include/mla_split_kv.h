@@ -972,9 +972,9 @@ typedef struct {
  * Precision: scores, maxima, sums and out_lse are fp32. The weights of the value
  * product are rounded to `dtype` by half a step, once (2^-11 of themselves in fp16,
  * or 2^-25 of the row's greatest where that is more; 2^-8 of themselves in bf16,
- * which is as much as a bf16 output is rounded by), but with bf16 and out_dtype
- * MLA_F32 they are kept as two bf16 terms, 2^-16 of themselves, as mla_decode's
- * are, for a third more time. The sum that normalizes takes them unrounded. A weight may reach 2^15 (fp16)
+ * which is as much as a bf16 output is rounded by), but with bf16 caches and an
+ * out_dtype of MLA_F32 or MLA_F16 they are kept as two bf16 terms, 2^-16 of
+ * themselves, as mla_decode's are, for a third more time. The sum that normalizes takes them unrounded. A weight may reach 2^15 (fp16)
  * or 2^30 (bf16) before the sums are moved to a new maximum: bf16 values times
  * tokens stay below 2^97. The partials are fp32; `out` is rounded once to
  * out_dtype.

@@ -28,10 +28,11 @@
 // 2^30 (bf16), since with it all of O moves, for some row of a warp every few tiles. 64 requests, 32,768 common tokens,
 // bf16, random latents: 116 us with 2^15, 109 with 2^20, 98 with 2^30 and with 2^60, which would leave values less room
 // below fp32's end. Sums are of the unrounded weights, in fp32; the weights are rounded once to the cache's type (by half a
-// step: 2^-11 of themselves in fp16, 2^-8 in bf16), as a 16-bit output is. Beside fp32 outputs a bf16 weight is two terms,
-// 2^-16 of itself (kTwo): rounded once, it leaves 0.7e-3 to 1.5e-3 of an output, where fp32 results are to keep 1e-3. The
-// second term is a second value product over the same tile (captured: 64 requests as above 130 us, 98 with 16-bit outputs; 24
-// requests of 2 x 128 rows, 8192 common tokens 179 and 132), with 16 KB less of the ring and 64 fewer query columns in tensor memory.
+// step: 2^-11 of themselves in fp16, 2^-8 in bf16), as an output of that type is. Beside fp32 and fp16 outputs a bf16 weight is
+// two terms, 2^-16 of itself (kTwo): rounded once, it leaves 0.7e-3 to 1.5e-3 of an output, where fp32 results are to keep
+// 1e-3. The second term is a second value product over the same tile (captured: 64 requests as above 130 us, 98 with bf16
+// outputs; 24 requests of 2 x 128 rows, 8192 common tokens 179 and 132), with 16 KB less of the ring and 64 fewer query columns
+// in tensor memory.
 // Tokens that some row of a group does not see (behind a shorter context or, in a window, behind the row) have weight 0
 // there, and values that are not finite are taken out of such tiles. For a row that does see one of them its score is not
 // finite either: a weight that is NaN, which makes all of the row so, or, with a score of -inf, one of 0, which times the
@@ -800,9 +801,9 @@ cudaError_t launch_units(const CUtensorMap& tm_half, const CUtensorMap& tm_piece
 
 cudaError_t launch_decode_shared(const CUtensorMap& tm_half, const CUtensorMap& tm_piece, const CUtensorMap& tm_kpe,
                                  const SharedParams& p, bool bf16, cudaStream_t stream) {
-  // (fp32 outputs of bf16 caches: the weights as two terms)
-  const cudaError_t e = !bf16                ? launch_units<false, false>(tm_half, tm_piece, tm_kpe, p, stream)
-                        : p.out_dtype == 2 ? launch_units<true, true>(tm_half, tm_piece, tm_kpe, p, stream)
+  // (bf16 caches, and outputs that hold more than bf16 does: the weights as two terms)
+  const cudaError_t e = !bf16              ? launch_units<false, false>(tm_half, tm_piece, tm_kpe, p, stream)
+                        : p.out_dtype != 1 ? launch_units<true, true>(tm_half, tm_piece, tm_kpe, p, stream)
                                            : launch_units<true, false>(tm_half, tm_piece, tm_kpe, p, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;

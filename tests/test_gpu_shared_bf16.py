@@ -76,6 +76,16 @@ def test_16_bit_outputs(lens, shared, H, q_len, bs, causal, size, dtype):
     case.check(*case.run(out_dtype=dtype), requests=range(min(5, len(lens))), heads=sorted({0, H // 2, H - 1}))
 
 
+@pytest.mark.parametrize("lens,shared,H,q_len,bs,causal,size", CASES)
+def test_fp16_outputs_are_the_fp32_ones_rounded_once(lens, shared, H, q_len, bs, causal, size):
+    """They hold more than bf16 weights rounded once would leave them."""
+    case = Case(56 + H, lens, shared, H, q_len, bs, "bf16", causal, size=size)
+    plan = case.plan()
+    out, lse = case.run(plan)
+    half, half_lse = case.run(plan, "f16")
+    assert torch.equal(half, out.half()) and torch.equal(half_lse, lse)
+
+
 @pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
 def test_scores_that_rise(out_dtype):
     """Keys that grow along the tokens: the running maximum moves all the time, and weights reach far above 1."""
