@@ -752,8 +752,10 @@ typedef struct {
  * context_lens_out may be context_lens, and free_count_out free_count; no two
  * other buffers may overlap. free_pages holds num_blocks entries. changes,
  * context_lens: device [B]; block_table: device [B, max_blocks_per_req].
- * Programmatic dependent launches, as mla_cache_append. No counterpart on the
- * pages.
+ * Programmatic dependent launches, as mla_cache_append: a decode call behind it
+ * has tables_ready = 0, also with mla_cache_append_slots in between, which may
+ * start, and let the decode start, while the tables are still being written. No
+ * counterpart on the pages.
  */
 mla_status_t mla_update_tables(const int32_t* changes, const int32_t* context_lens, int32_t* context_lens_out,
                                int32_t* block_table, int32_t* free_pages, const int32_t* free_count,
@@ -860,8 +862,8 @@ typedef struct {
  * MLA_ERR_DEVICE_CHECK.
  *
  * Precision: scores, maxima, sums and out_lse are fp32, the weights of the value
- * product are rounded once to `dtype` (half a step: 2^-12 of themselves in fp16,
- * or 2^-25 of the row's greatest where that is more, 2^-9 of themselves in bf16)
+ * product are rounded once to `dtype` (half a step: 2^-11 of themselves in fp16,
+ * or 2^-25 of the row's greatest where that is more, 2^-8 of themselves in bf16)
  * and the sum that normalizes takes them unrounded. A weight may reach 2^15 before
  * the sums are moved to a new maximum: bf16 values times tokens stay below 2^112.
  *

@@ -18,7 +18,8 @@
 // Accumulators of two tiles alternate in tensor memory (2 x 256 columns): eight warps drain one through 4 KB each of
 // shared memory and TMA stores of [32 tokens x 64 columns], while the next is computed. (32 bytes a thread, every
 // thread another token, straight to memory: 527 us against 352 without any stores, of 16,384 tokens and 128 heads.)
-// Every pair takes an equal run of the (block, two heads, keys or values) tiles (Walk).
+// Every pair takes an equal run of the (block, two heads, keys or values) tiles (Walk). A block's tile costs the same 2.3 us
+// however few of its 256 rows are tokens: 32 requests of 18 tokens under 128 heads take 132 us, as one request 25.
 //
 // Warps: 0-7 epilogue (0-3 the first head, 4-7 the second), 8 loads, 9 products (of the pair's first CTA).
 #include "device_common.cuh"

@@ -1,4 +1,4 @@
-"""The steps that README.md shows, run as they stand there, step after step."""
+"""The steps that the documentation shows, run as they stand there, step after step."""
 import os
 import re
 
