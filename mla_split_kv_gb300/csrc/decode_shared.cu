@@ -212,7 +212,7 @@ __device__ __forceinline__ void spoil_output(const SharedParams& p, const Unit& 
   const int most = __reduce_max_sync(0xffffffffu, sees);
   float* const out = p.part_o + (static_cast<long long>(w.slot) * kRows + row0) * kRank + kHalf * w.half + 8 * lane;
   __syncwarp();  // behind the rows' stores by other lanes
-  for (int t = w.t0 + max(0, w.least - w.t0) / kT * kT; t < most; ++t) {
+  for (int t = w.t0 + max(0, min(w.least, w.t1) - w.t0) / kT * kT; t < most; ++t) {
     const int col = t / p.bs, pid = col < columns ? table[col] : -1;
     if (pid < 0 || pid >= p.num_blocks) continue;  // (zeros)
     const uint16_t* const from = p.ckv + (static_cast<long long>(pid) * p.bs + t % p.bs) * kRank + kHalf * w.half + 8 * lane;

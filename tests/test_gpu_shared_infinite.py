@@ -101,6 +101,16 @@ def test_a_causal_window(H, q_len):
     check(case, *case.run())
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shared", [16, 48, 528, 1632])
+def test_a_prefix_that_ends_inside_a_tile(shared, dtype):
+    """Its last tile is masked although every row sees all of its tokens."""
+    case = Case(35, [shared + 90, shared + 200, shared + 64], shared, 64, 2, 16, dtype, True)
+    for t, column in zip((shared - 1, shared - 16, shared // 64 * 64 if shared % 64 else shared - 64), COLUMNS):
+        poison(case, 0, t, column)
+    check(case, *case.run())
+
+
 def test_pieces_and_units_in_turns():
     """Many units a CTA, some with such a token and some without, in tiles that are masked."""
     case = Case(34, [2048 + 37 * i for i in range(40)], 2048, 16, 1, 16, "bf16")
